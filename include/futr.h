@@ -47,6 +47,7 @@ typedef int32_t futr_status;
 #define FUTR_ERR_NOT_PD        7  /* GPTQ: a dampened Hessian is not positive definite */
 #define FUTR_ERR_CORRUPT       8  /* device: guard words after a region overwritten    */
 #define FUTR_ERR_BOUNDS        9  /* device, debug build: an index failed its check    */
+#define FUTR_ERR_NOT_FINITE   10  /* device: infinity or NaN appended to a paged cache */
 
 /* Shape of one decoder block. */
 typedef struct futr_shape {
@@ -351,6 +352,177 @@ futr_status futr_decode_step(const int32_t* tokens, const uint16_t* embedding, i
  * nonzero device error word of the workspace `ws` and of the cache `kv` (either
  * may be NULL), or FUTR_ERR_CUDA if a CUDA error is pending. */
 futr_status futr_check(const futr_ws* ws, const futr_kv* kv, void* stream);
+
+/* ------------------------------------------------------ paged 8-bit cache --
+ *
+ * A key/value cache in pages, for sequences that grow, share and free memory,
+ * with any number of new tokens per call (single tokens, drafts, prompts).  A
+ * page holds `page` consecutive positions of one sequence.  Memory, in order
+ * (each region followed by 256 guard bytes):
+ *   codes  [n_layers][n_pages][Hkv][2: keys, values][page][d]  e4m3, one byte each
+ *   scales [n_layers][n_pages][Hkv][2]                          fp32
+ *   the RoPE cos/sin table [max_pos][d/2] and the error word.
+ * A value is code * scale.  Scales written here are powers of two.  Which page
+ * holds positions page*i .. page*i + page - 1 of sequence b is entry [b][i] of
+ * the caller's page table (device int32 [batch][table_ld]); entries past a
+ * sequence's last page are not read.  Several sequences may read one page; in
+ * one append, a page may belong to one sequence only.
+ *
+ * Ragged rows: rows start[b] .. start[b+1]-1 of a call's row tensors are the
+ * new tokens of sequence b, at positions pos[b], pos[b]+1, ...  start is device
+ * int32 [batch+1], non-decreasing, with start[batch] <= n_rows (rows behind it
+ * are ignored, and left as they were in an output); NULL means one row per
+ * sequence (n_rows == batch).  pos (device int32 [batch]) is the number of
+ * tokens cached before the call.  A sequence whose rows do not fit n_rows, the
+ * table (table_ld * page positions) or max_pos, and a page id outside
+ * [0, n_pages), set FUTR_ERR_OUT_OF_RANGE (see futr_paged_check); that
+ * sequence is skipped, or that page counts as not visible.
+ *
+ * Row tensors are 16-bit (FUTR_DTYPE_*), heads and dims contiguous, tokens ld_*
+ * elements apart (a multiple of 8, so a slice of a fused QKV row will do),
+ * 16-byte aligned.  Only the shape's head counts, head_dim and rope_theta are
+ * used.  The calls launch one kernel with programmatic dependent launch, read
+ * pos, start and table on the device, and can be captured in a CUDA graph; a
+ * captured call follows lengths that change. */
+#define FUTR_DTYPE_BF16 0
+#define FUTR_DTYPE_F16  1
+
+typedef struct futr_paged {
+  futr_shape shape;
+  int32_t n_layers, n_pages, page, max_pos;
+  int32_t rope;            /* keys are rotated on append and queries in attention */
+  void* base;
+  uint64_t bytes;
+  uint64_t scale_offset, rope_offset, err_offset;
+  uint64_t magic;
+} futr_paged;
+
+/* Workspace of futr_paged_attention: arrival counters and split records. */
+typedef struct futr_paged_ws {
+  int32_t head_dim, ctas;
+  void* base;
+  uint64_t bytes;
+  uint64_t rec_offset;
+  uint64_t magic;
+} futr_paged_ws;
+
+/* Bytes of a cache: page 16, 32, 64 or 128; max_pos up to 2^20 positions. */
+futr_status futr_paged_size(const futr_shape* shape, int32_t n_layers, int32_t n_pages, int32_t page,
+                            int32_t max_pos, size_t* bytes);
+
+/* Zero `mem` (256-byte aligned), write the RoPE table (float64 rounded to fp32)
+ * and the guards, fill the host descriptor.  rope 0: the rows of both calls
+ * carry their positions already.  Asynchronous on `stream`. */
+futr_status futr_paged_init(const futr_shape* shape, int32_t n_layers, int32_t n_pages, int32_t page,
+                            int32_t max_pos, int32_t rope, void* mem, size_t mem_bytes, futr_paged* cache,
+                            void* stream);
+
+/*
+ * Append k, v rows [n_rows][Hkv][d].  Keys are rotated in fp32 (dims i and
+ * i + d/2, rotate-half).  For each touched page, kv-head, and keys and values
+ * apart: s = max(s_old, 2^e) with 2^e the smallest power of two such that the
+ * new rows' largest magnitude is at most 448 * 2^e, and e >= -60; codes are
+ * e4m3(x / s), rounded to nearest even.  When s > s_old the page's other codes
+ * c become e4m3(c * s_old / s).  A call that writes slot 0 of a page starts the
+ * page over (s_old = 0): what its other slots held is void.  An infinity or NaN
+ * (after the rotation) is stored as 0 and sets FUTR_ERR_NOT_FINITE.
+ */
+futr_status futr_paged_append(const futr_paged* cache, int32_t layer, int32_t batch, const int32_t* pos,
+                              const int32_t* start, int32_t n_rows, const int32_t* table, int32_t table_ld,
+                              const void* k, int64_t ld_k, const void* v, int64_t ld_v, int32_t dtype,
+                              void* stream);
+
+/* Bytes of the workspace of futr_paged_attention on the current device (it
+ * depends on head_dim and the device only), and its set-up (counters to zero,
+ * guards).  Calls that overlap on the GPU (other streams, graphs replayed side
+ * by side) need a workspace each. */
+futr_status futr_paged_workspace_size(const futr_shape* shape, size_t* bytes);
+futr_status futr_paged_workspace_init(const futr_shape* shape, void* mem, size_t mem_bytes, futr_paged_ws* ws,
+                                      void* stream);
+
+/*
+ * Causal attention of the new rows over the cache, after futr_paged_append has
+ * stored them: q [n_rows][Hq][d] (rotated here when the cache rotates), out
+ * [n_rows][Hq][d].  The row at position p sees positions max(0, p - window + 1)
+ * .. p (window 0: 0 .. p); query head h reads kv-head h / (Hq/Hkv).
+ *   out = sum_j softmax_j(scale * q'.k_j) v_j      (scale 0: 1/sqrt(d))
+ * The rotated query and the softmax weights enter the products as fp16 (the
+ * query divided by a power of two near its largest element), sums and softmax
+ * statistics are fp32.  A row that sees no position (missing pages) gets zeros.
+ * out may not be q.
+ */
+futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t batch, const int32_t* pos,
+                                 const int32_t* start, int32_t n_rows, const int32_t* table, int32_t table_ld,
+                                 const void* q, int64_t ld_q, void* out, int64_t ld_out, int32_t dtype,
+                                 float scale, int32_t window, const futr_paged_ws* ws, void* stream);
+
+/* Compare the guards of `cache` and `ws` (may be NULL), synchronize `stream` and
+ * return (and clear) the cache's first device error. */
+futr_status futr_paged_check(const futr_paged* cache, const futr_paged_ws* ws, void* stream);
+
+/* ------------------------------------------------------ mixture of experts -- */
+typedef struct futr_moe_shape {
+  int32_t hidden;      /* model width H, a multiple of 128                      */
+  int32_t inter;       /* width I of one expert, a multiple of 128              */
+  int32_t n_experts;   /* E, 1..256                                             */
+  int32_t top_k;       /* experts of a token K, 1..min(E, 16)                   */
+  int32_t group;       /* INT4 scale group along the input dim (128)            */
+  int32_t renorm;      /* 1: the K weights of a token are divided by their sum  */
+  float rms_eps;       /* RMSNorm epsilon; 0: the input is taken as it is       */
+} futr_moe_shape;
+
+typedef struct futr_moe_ws {
+  futr_moe_shape shape;
+  int32_t max_batch, ctas, _pad;
+  void* base;
+  uint64_t bytes;
+  uint64_t off_cnt, off_route, off_logits, off_act, off_rec;
+  uint64_t magic;
+} futr_moe_ws;
+
+/* Bytes of the packed experts of one layer. */
+futr_status futr_moe_weights_size(const futr_moe_shape* shape, size_t* bytes);
+
+/* Pack one expert (fp32 wgate, wup [I, H], wdown [H, I], nn.Linear layout) into
+ * the layer's blob (256-byte aligned): the codes, scales and unit layout of
+ * futr_pack_weights.  gain: the RMSNorm gain [H] folded into gate and up, or
+ * NULL.  Experts may be packed in any order; all of them before the first use. */
+futr_status futr_moe_pack(const futr_moe_shape* shape, int32_t expert, const float* wgate, const float* wup,
+                          const float* wdown, const float* gain, void* blob, size_t blob_bytes, void* stream);
+
+/* Canonical view of one packed projection of an expert (FUTR_PROJ_GATE, _UP or
+ * _DOWN): codes int8 [rows, cols], fp16 scales [rows, cols/128]. */
+futr_status futr_moe_unpack(const futr_moe_shape* shape, const void* blob, int32_t expert, int32_t which,
+                            int8_t* codes, uint16_t* scales, void* stream);
+
+/* Workspace of futr_moe_layer for batches up to max_batch (1..32).  Calls that
+ * overlap on the GPU need a workspace each. */
+futr_status futr_moe_workspace_size(const futr_moe_shape* shape, int32_t max_batch, size_t* bytes);
+futr_status futr_moe_workspace_init(const futr_moe_shape* shape, int32_t max_batch, void* mem, size_t mem_bytes,
+                                    futr_moe_ws* ws, void* stream);
+
+/*
+ * One mixture-of-experts layer for `batch` tokens:
+ *   r = 1/sqrt(mean(x^2) + eps)  (1 when rms_eps is 0)
+ *   logits = r * router (x * gain)           (router bf16 [E][H]; gain fp32 [H] or NULL)
+ *   the K largest logits of each token, equal ones by the lowest expert; their
+ *   softmax probabilities w over all E experts, divided by their sum if renorm
+ *   y = bf16(resid + sum_j w_j Wdown_j (silu(r W'gate_j x) * (r W'up_j x)))
+ * x, y, resid: bf16 [batch][H], 16-byte aligned (y may be x or resid; resid may
+ * be NULL).  The products w * silu * up are rounded to bf16 before the down
+ * projection, everything else is fp32.  ids (int32) and weights (fp32)
+ * [batch][K], either may be NULL: the choice of each token, largest first.  A
+ * token whose logits hold a NaN gets NaN weights.  A blob of another shape sets
+ * FUTR_ERR_BAD_BLOB (see futr_moe_check).  Three kernels with programmatic
+ * dependent launch; capturable in a CUDA graph.
+ */
+futr_status futr_moe_layer(const uint16_t* x, const float* gain, const uint16_t* router, const void* blob,
+                           int32_t batch, const uint16_t* resid, uint16_t* y, int32_t* ids, float* weights,
+                           const futr_moe_ws* ws, void* stream);
+
+/* Compare the guards of `ws`, synchronize `stream` and return (and clear) its
+ * first device error. */
+futr_status futr_moe_check(const futr_moe_ws* ws, void* stream);
 
 #ifdef __cplusplus
 }

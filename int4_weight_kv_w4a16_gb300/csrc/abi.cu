@@ -489,6 +489,7 @@ const char* futr_status_string(futr_status s) {
     case FUTR_ERR_NOT_PD: return "dampened Hessian not positive definite";
     case FUTR_ERR_CORRUPT: return "guard words after a workspace or cache region overwritten";
     case FUTR_ERR_BOUNDS: return "device bounds check failed (debug build)";
+    case FUTR_ERR_NOT_FINITE: return "infinity or NaN in a row appended to the paged cache";
     default: return "unknown status";
   }
 }
@@ -826,6 +827,23 @@ void describe_workspace(const futr_shape& s, int max_batch, int capacity, int n_
 }
 
 int sm_count() { return current_sm_count(); }
+
+bool shape_valid(const futr_shape* s) { return shape_ok(s); }
+
+uint64_t region_after(uint64_t off, uint64_t size) { return after(off, size); }
+
+// A region that starts at `start` is preceded by its predecessor's guard.
+cudaError_t fill_guards_before(void* base, const uint64_t* starts, int n, cudaStream_t st) {
+  uint64_t g[kMaxGuards];
+  for (int i = 0; i < n; ++i) g[i] = starts[i] - kGuardBytes;
+  return fill_guards(base, g, n, st);
+}
+
+cudaError_t check_guards_before(void* base, const uint64_t* starts, int n, int* err, cudaStream_t st) {
+  uint64_t g[kMaxGuards];
+  for (int i = 0; i < n; ++i) g[i] = starts[i] - kGuardBytes;
+  return check_guards(base, g, n, err, st);
+}
 
 bool kv_valid(const futr_kv* kv) { return kv_ok(kv) && shape_ok(&kv->shape) && kv->capacity > 0; }
 

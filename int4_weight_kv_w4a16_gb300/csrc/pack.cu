@@ -157,6 +157,45 @@ cudaError_t launch_pack(const futr_shape& s, const float* wq, const float* wk, c
   return cudaGetLastError();
 }
 
+// One expert's gate/up and down sections.
+cudaError_t launch_pack_expert(int hidden, int inter, const float* wg, const float* wu, const float* wd,
+                               const float* gain, uint8_t* gu, uint8_t* down, cudaStream_t st) {
+  const size_t smem = (size_t)kRowsPerBlock * kTileLd * 4 + kRowsPerBlock * kCodeLd;
+  cudaError_t e = cudaFuncSetAttribute(pack_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  for (int i = 0; i < 2; ++i) {
+    PackArgs a{};
+    a.kind = i == 0 ? 2 : 1;
+    a.src[0] = i == 0 ? wg : wd;
+    a.src[1] = wu;
+    a.gain = i == 0 ? gain : nullptr;
+    a.K = i == 0 ? hidden : inter;
+    a.n_groups = a.K / kGroup;
+    a.out = i == 0 ? gu : down;
+    const int units = (i == 0 ? 2 * inter : hidden) / kRowsPerBlock * a.n_groups;
+    pack_kernel<<<units, kPackThreads, smem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_unpack_expert(int hidden, int inter, const uint8_t* gu, const uint8_t* down, int which,
+                                 int8_t* codes, uint16_t* scales, cudaStream_t st) {
+  UnpackArgs a{};
+  const bool is_down = which == FUTR_PROJ_DOWN;
+  a.map = which == FUTR_PROJ_GATE ? 1 : which == FUTR_PROJ_UP ? 2 : 0;
+  a.rows = is_down ? hidden : inter;
+  a.cols = is_down ? inter : hidden;
+  a.sec = is_down ? down : gu;
+  a.n_groups = a.cols / kGroup;
+  a.codes = codes;
+  a.scales = scales;
+  const size_t n = (size_t)a.rows * a.cols;
+  unpack_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_unpack(const futr_shape& s, const uint8_t* blob, int which, int8_t* codes,
                           uint16_t* scales, cudaStream_t st) {
   const BlobSections sec = blob_sections(s);

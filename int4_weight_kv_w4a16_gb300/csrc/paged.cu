@@ -1,0 +1,247 @@
+// Append to the paged 8-bit cache: RoPE, page scale, e4m3 codes, in one pass
+// over the new rows.
+//
+//   k'_i = k_i cos a - k_{i+d/2} sin a,  k'_{i+d/2} = k_{i+d/2} cos a + k_i sin a,
+//   a = p theta^(-2i/d)   (fp32 products, each rounded, from the fp32 table)
+//   s = max(s_old, 2^e),  2^e the smallest power of two with amax <= 448 2^e
+//   code = e4m3(x / s);   where s > s_old, an old code c becomes e4m3(c s_old / s)
+//
+// One CTA per (touched page, kv-head, K or V): it alone writes that page's
+// codes and scale, so there are no atomics and the result does not depend on
+// any order.  A group of d/8 lanes takes one row, 8 elements a lane (one 16-byte
+// load, one 8-byte store; the rotation partner is d/16 lanes away).
+//
+// Bound by memory for prompts (2 bytes read and 1 written per element) and by
+// latency for single tokens, whose chain is: row bounds -> table entry -> old
+// scale, and beside it row -> rotation -> maximum.
+#include <cuda_fp8.h>
+
+#include "paged.cuh"
+
+namespace futr {
+
+namespace {
+
+constexpr int kAppThreads = 128;
+
+// e4m3 of x in [-448, 448] (saturating), as bits; and back.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// Exponent of the page scale for a largest magnitude amax: 448 = 1.75 * 2^8.
+__device__ __forceinline__ int scale_exp(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int x = (int)(u >> 23) - 127;
+  const int e = x - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return e < kPagedMinExp ? kPagedMinExp : e;
+}
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+template <bool kHalf>
+__device__ __forceinline__ void widen8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kHalf) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    } else {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+struct AppendArgs {
+  PagedView c;
+  PagedRows r;
+  const uint16_t* src[2];   // K, V rows
+  long long ld[2];
+  int* err;
+};
+
+// One row's 8 elements of this lane, rotated (keys) and with non-finite values
+// replaced by 0 (bad set).
+template <int D, bool kHalf>
+__device__ __forceinline__ void load_row(const AppendArgs& a, const uint16_t* row, int p, int lg, bool rotate,
+                                         float (&x)[8], bool& bad) {
+  constexpr int L = D / 8;   // lanes of a row
+  widen8<kHalf>(*reinterpret_cast<const uint4*>(row + 8 * lg), x);
+  if (rotate) {
+    const bool upper = lg >= L / 2;
+    const float4* t = reinterpret_cast<const float4*>(a.c.rope + (size_t)p * (D / 2) + 8 * (upper ? lg - L / 2 : lg));
+    float4 cs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = t[i];
+    const float* f = reinterpret_cast<const float*>(cs);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float o = __shfl_xor_sync(0xffffffffu, x[i], L / 2);
+      const float xc = __fmul_rn(x[i], f[2 * i]), os = __fmul_rn(o, f[2 * i + 1]);
+      x[i] = upper ? __fadd_rn(xc, os) : __fsub_rn(xc, os);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (!(fabsf(x[i]) <= 3.4028234e38f)) {
+      x[i] = 0.f;
+      bad = true;
+    }
+}
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendArgs a) {
+  constexpr int L = D / 8, kRows = kAppThreads / L;   // lanes of a row, rows at a time
+  __shared__ float s_max[kAppThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, lg = tid % L, rg = tid / L;
+  const int kvh = blockIdx.y, which = blockIdx.z;
+  pdl_trigger();
+  pdl_wait();
+  // one warp of the grid looks every sequence over (the search below stops early)
+  if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0 && tid >= kAppThreads - 32)
+    for (int s = lane; s < a.r.batch; s += 32) {
+      int r0, nn, pp;
+      if (!paged_seq(a.r, a.c, s, r0, nn, pp)) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
+    }
+  // the touched page of this CTA: sequences in order, each with the pages that
+  // its new rows meet
+  int item = blockIdx.x, row0 = 0, n = 0, p0 = 0, b = -1;
+  for (int b0 = 0; b0 < a.r.batch; b0 += 32) {
+    int rr = 0, nn = 0, pp = 0, pages = 0;
+    if (b0 + lane < a.r.batch) {
+      paged_seq(a.r, a.c, b0 + lane, rr, nn, pp);
+      if (nn > 0) pages = ((pp + nn - 1) >> a.c.page_log2) - (pp >> a.c.page_log2) + 1;
+    }
+    int incl = pages;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > item);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      b = b0 + src;
+      row0 = __shfl_sync(0xffffffffu, rr, src);
+      n = __shfl_sync(0xffffffffu, nn, src);
+      p0 = __shfl_sync(0xffffffffu, pp, src);
+      item -= __shfl_sync(0xffffffffu, incl - pages, src);
+      break;
+    }
+    item -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (b < 0) return;   // the grid is an upper bound
+  const int page = a.c.page, pi = (p0 >> a.c.page_log2) + item;
+  const int id = a.r.table[(size_t)b * a.r.table_ld + pi];
+  if (id < 0 || id >= a.c.n_pages) {
+    if (tid == 0) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
+    return;
+  }
+  const int base = pi << a.c.page_log2;
+  const int lo = max(base, p0) - base, hi = min(base + page, p0 + n) - base;   // slots [lo, hi) are new
+  const size_t blk = ((size_t)id * a.c.n_kv + kvh) * 2 + which;
+  uint8_t* codes = a.c.codes + blk * page * D;
+  float* scale = a.c.scales + blk;
+  const uint16_t* src = a.src[which] + (size_t)kvh * D;
+  const bool rotate = which == 0 && a.c.rope != nullptr;
+  // a page whose slot 0 is written starts over
+  const float s_old = lo == 0 ? 0.f : *scale;
+
+  // largest magnitude; the first row of each lane group stays in registers
+  float x[8], first[8], m = 0.f;
+  bool bad = false;
+  const int rounds = (hi - lo + kRows - 1) / kRows;
+  for (int i = 0; i < rounds; ++i) {
+    const int slot = lo + i * kRows + rg;
+    const int use = slot < hi ? slot : lo;   // idle groups repeat a row: every lane takes part in the shuffles
+    load_row<D, kHalf>(a, src + (size_t)(row0 + base + use - p0) * a.ld[which], base + use, lg, rotate, x, bad);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m = fmaxf(m, fabsf(x[j]));
+      if (i == 0) first[j] = x[j];
+    }
+  }
+  if (bad) set_err(a.err, FUTR_ERR_NOT_FINITE);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) s_max[tid >> 5] = m;
+  __syncthreads();   // every thread has read the old scale by now, too
+#pragma unroll
+  for (int w = 0; w < kAppThreads / 32; ++w) m = fmaxf(m, s_max[w]);
+  const float s_new = fmaxf(s_old, pow2(scale_exp(m)));
+  if (tid == 0 && s_new != s_old) *scale = s_new;
+  if (s_old > 0.f && s_new > s_old) {
+    // the page's other slots at the new scale, 8 codes a thread
+    const float ratio = __fdiv_rn(s_old, s_new);
+    for (int i = tid; i < page * L; i += kAppThreads) {
+      const int slot = i / L;
+      if (slot >= lo && slot < hi) continue;
+      uint2* at = reinterpret_cast<uint2*>(codes) + i;
+      uint2 u = *at;
+      uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 f0 = e4m3x2_to_f32(w[j] & 0xFFFFu), f1 = e4m3x2_to_f32(w[j] >> 16);
+        w[j] = e4m3x2(f0.x * ratio, f0.y * ratio) | (e4m3x2(f1.x * ratio, f1.y * ratio) << 16);
+      }
+      *at = make_uint2(w[0], w[1]);
+    }
+  }
+  const float inv = __fdiv_rn(1.0f, s_new);   // exact: a power of two
+  for (int i = 0; i < rounds; ++i) {
+    const int slot = lo + i * kRows + rg;
+    const int use = slot < hi ? slot : lo;
+    if (i == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = first[j];
+    } else {
+      load_row<D, kHalf>(a, src + (size_t)(row0 + base + use - p0) * a.ld[which], base + use, lg, rotate, x, bad);
+    }
+    if (slot < hi) {
+      uint32_t w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        w[j] = e4m3x2(x[4 * j] * inv, x[4 * j + 1] * inv) | (e4m3x2(x[4 * j + 2] * inv, x[4 * j + 3] * inv) << 16);
+      *(reinterpret_cast<uint2*>(codes) + (size_t)slot * L + lg) = make_uint2(w[0], w[1]);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedView& c, const PagedRows& r, int d, int dtype, const void* k, long long ld_k,
+                                const void* v, long long ld_v, int* err, cudaStream_t st) {
+  AppendArgs a{c, r, {static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v)}, {ld_k, ld_v}, err};
+  // touched pages: a sequence of n rows meets at most (n - 1) / page + 2, one row exactly 1
+  const long long rows = r.n_rows, per = r.start ? 2 : 1;
+  const long long bound = r.start ? rows / c.page + per * (rows < r.batch ? rows : r.batch) : r.batch;
+  const long long items = bound < rows ? bound : rows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)items, (unsigned)c.n_kv, 2);
+  cfg.blockDim = dim3(kAppThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool half = dtype == FUTR_DTYPE_F16;
+  if (d == 128)
+    return half ? cudaLaunchKernelEx(&cfg, paged_append_kernel<128, true>, a)
+                : cudaLaunchKernelEx(&cfg, paged_append_kernel<128, false>, a);
+  return half ? cudaLaunchKernelEx(&cfg, paged_append_kernel<64, true>, a)
+              : cudaLaunchKernelEx(&cfg, paged_append_kernel<64, false>, a);
+}
+
+}  // namespace futr

@@ -26,6 +26,9 @@ FUTR_ERR_BAD_BLOB = 6
 FUTR_ERR_NOT_PD = 7
 FUTR_ERR_CORRUPT = 8
 FUTR_ERR_BOUNDS = 9
+FUTR_ERR_NOT_FINITE = 10
+
+FUTR_DTYPE_BF16, FUTR_DTYPE_F16 = range(2)
 
 FUTR_PROJ_QKV, FUTR_PROJ_O, FUTR_PROJ_GATE, FUTR_PROJ_UP, FUTR_PROJ_DOWN = range(5)
 
@@ -51,6 +54,29 @@ class futr_ws(C.Structure):
                 ("off_yout", C.c_uint64), ("off_pos", C.c_uint64), ("off_part", C.c_uint64),
                 ("part_bytes", C.c_uint64), ("off_apart", C.c_uint64), ("apart_bytes", C.c_uint64),
                 ("off_cnt", C.c_uint64), ("cnt_words", C.c_uint64), ("magic", C.c_uint64)]
+
+
+class futr_paged(C.Structure):
+    _fields_ = [("shape", futr_shape), ("n_layers", C.c_int32), ("n_pages", C.c_int32), ("page", C.c_int32),
+                ("max_pos", C.c_int32), ("rope", C.c_int32), ("base", C.c_void_p), ("bytes", C.c_uint64),
+                ("scale_offset", C.c_uint64), ("rope_offset", C.c_uint64), ("err_offset", C.c_uint64),
+                ("magic", C.c_uint64)]
+
+
+class futr_paged_ws(C.Structure):
+    _fields_ = [("head_dim", C.c_int32), ("ctas", C.c_int32), ("base", C.c_void_p), ("bytes", C.c_uint64),
+                ("rec_offset", C.c_uint64), ("magic", C.c_uint64)]
+
+
+class futr_moe_shape(C.Structure):
+    _fields_ = [("hidden", C.c_int32), ("inter", C.c_int32), ("n_experts", C.c_int32), ("top_k", C.c_int32),
+                ("group", C.c_int32), ("renorm", C.c_int32), ("rms_eps", C.c_float)]
+
+
+class futr_moe_ws(C.Structure):
+    _fields_ = [("shape", futr_moe_shape), ("max_batch", C.c_int32), ("ctas", C.c_int32), ("_pad", C.c_int32),
+                ("base", C.c_void_p), ("bytes", C.c_uint64), ("off_cnt", C.c_uint64), ("off_route", C.c_uint64),
+                ("off_logits", C.c_uint64), ("off_act", C.c_uint64), ("off_rec", C.c_uint64), ("magic", C.c_uint64)]
 
 
 class FutrError(RuntimeError):
@@ -83,6 +109,22 @@ _SIGS = {
     "futr_decode_block_host": (I32, [P, P, C.POINTER(futr_kv), I32, I32, P, P, C.POINTER(futr_ws), P]),
     "futr_check": (I32, [C.POINTER(futr_ws), C.POINTER(futr_kv), P]),
     "futr_decode_block_noalloc": (I32, [P, P, C.POINTER(futr_kv), I32, I32, P, P, P]),
+    "futr_paged_size": (I32, [C.POINTER(futr_shape), I32, I32, I32, I32, C.POINTER(C.c_size_t)]),
+    "futr_paged_init": (I32, [C.POINTER(futr_shape), I32, I32, I32, I32, I32, P, C.c_size_t,
+                              C.POINTER(futr_paged), P]),
+    "futr_paged_append": (I32, [P, I32, I32, P, P, I32, P, I32, P, C.c_int64, P, C.c_int64, I32, P]),
+    "futr_paged_workspace_size": (I32, [C.POINTER(futr_shape), C.POINTER(C.c_size_t)]),
+    "futr_paged_workspace_init": (I32, [C.POINTER(futr_shape), P, C.c_size_t, C.POINTER(futr_paged_ws), P]),
+    "futr_paged_attention": (I32, [P, I32, I32, P, P, I32, P, I32, P, C.c_int64, P, C.c_int64, I32, C.c_float, I32,
+                                   P, P]),
+    "futr_paged_check": (I32, [P, P, P]),
+    "futr_moe_weights_size": (I32, [C.POINTER(futr_moe_shape), C.POINTER(C.c_size_t)]),
+    "futr_moe_pack": (I32, [C.POINTER(futr_moe_shape), I32, P, P, P, P, P, C.c_size_t, P]),
+    "futr_moe_unpack": (I32, [C.POINTER(futr_moe_shape), P, I32, I32, P, P, P]),
+    "futr_moe_workspace_size": (I32, [C.POINTER(futr_moe_shape), I32, C.POINTER(C.c_size_t)]),
+    "futr_moe_workspace_init": (I32, [C.POINTER(futr_moe_shape), I32, P, C.c_size_t, C.POINTER(futr_moe_ws), P]),
+    "futr_moe_layer": (I32, [P, P, P, P, I32, P, P, P, P, P, P]),
+    "futr_moe_check": (I32, [P, P]),
     "futr_decode_step": (I32, [P, P, I32, C.POINTER(C.c_void_p), I32, C.POINTER(futr_kv), I32, P, P, P, P,
                                C.POINTER(futr_ws), P]),
 }
@@ -256,6 +298,203 @@ def futr_check(ws=None, kv=None, stream=None) -> int:
     """Synchronize and return the device status (0 = ok); does not raise."""
     return lib().futr_check(C.byref(ws) if ws is not None else None, C.byref(kv) if kv is not None else None,
                             _stream(stream))
+
+
+# ----------------------------------------------------------------------------
+# paged 8-bit cache.  Row tensors, positions and tables are torch CUDA tensors;
+# their types, shapes and strides are checked here, the C side cannot see them.
+# ----------------------------------------------------------------------------
+
+def _dtype16(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return FUTR_DTYPE_BF16
+    if t.dtype == torch.float16:
+        return FUTR_DTYPE_F16
+    raise TypeError(f"rows are bfloat16 or float16, not {t.dtype}")
+
+
+def _ints(t, name: str, device: int, size: int) -> int:
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != size:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {size} elements")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on CUDA device {device}, the current one")
+    return t.data_ptr()
+
+
+def _rows(t, name: str, device: int, shape) -> int:
+    """Checks a row tensor [n_rows, heads, head_dim] with contiguous heads; returns its row stride."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on CUDA device {device}, the current one")
+    st = t.stride()
+    if st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return st[0] if shape[0] > 1 else max(shape[1] * shape[2], 8 * (st[0] // 8))
+
+
+def _current(stream):
+    import torch
+    device = torch.cuda.current_device()
+    return device, (torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream))
+
+
+def _paged_rows(cache, batch, pos, start, table, n_rows, device):
+    if table.dim() != 2 or table.shape[0] != batch:
+        raise ValueError(f"table must have the shape ({batch}, pages)")
+    width = table.shape[1]
+    return (_ints(pos, "pos", device, batch), None if start is None else _ints(start, "start", device, batch + 1),
+            n_rows, _ints(table, "table", device, batch * width), width)
+
+
+def futr_paged_size(shape, n_layers, n_pages, page, max_pos) -> int:
+    n = C.c_size_t()
+    _ok(lib().futr_paged_size(C.byref(shape), n_layers, n_pages, page, max_pos, C.byref(n)), "futr_paged_size")
+    return n.value
+
+
+def futr_paged_init(shape, n_layers, n_pages, page, max_pos, rope, mem, stream=None) -> futr_paged:
+    cache = futr_paged()
+    _ok(lib().futr_paged_init(C.byref(shape), n_layers, n_pages, page, max_pos, int(rope), _ptr(mem),
+                              mem.numel() * mem.element_size(), C.byref(cache), _stream(stream)), "futr_paged_init")
+    cache._mem = mem
+    return cache
+
+
+def paged_views(cache):
+    """The cache's codes (float8_e4m3fn [layers, pages, kv-heads, 2, page, head_dim])
+    and scales (float32 [layers, pages, kv-heads, 2]) as tensors on its memory:
+    index 0 keys, 1 values; a value is code * scale."""
+    import torch
+    s = cache.shape
+    lead = (cache.n_layers, cache.n_pages, s.n_kv_heads, 2)
+    n = cache.n_layers * cache.n_pages * s.n_kv_heads * 2
+    codes = cache._mem[:n * cache.page * s.head_dim].view(torch.float8_e4m3fn)
+    scales = cache._mem[cache.scale_offset:cache.scale_offset + 4 * n].view(torch.float32)
+    return codes.view(*lead, cache.page, s.head_dim), scales.view(*lead)
+
+
+def futr_paged_append(cache, layer, batch, pos, start, table, k, v, stream=None):
+    """Append the rows k, v [n_rows, kv-heads, head_dim]; start None: one row per sequence."""
+    device, st = _current(stream)
+    shape = (k.shape[0], cache.shape.n_kv_heads, cache.shape.head_dim)
+    if v.dtype != k.dtype:
+        raise TypeError("k and v must have the same type")
+    ld_k, ld_v = _rows(k, "k", device, shape), _rows(v, "v", device, shape)
+    r = _paged_rows(cache, batch, pos, start, table, shape[0], device)
+    _ok(lib().futr_paged_append(C.addressof(cache), layer, batch, *r, k.data_ptr(), ld_k, v.data_ptr(), ld_v,
+                                _dtype16(k), st), "futr_paged_append")
+
+
+def futr_paged_workspace_size(shape) -> int:
+    n = C.c_size_t()
+    _ok(lib().futr_paged_workspace_size(C.byref(shape), C.byref(n)), "futr_paged_workspace_size")
+    return n.value
+
+
+def futr_paged_workspace_init(shape, mem, stream=None) -> futr_paged_ws:
+    ws = futr_paged_ws()
+    _ok(lib().futr_paged_workspace_init(C.byref(shape), _ptr(mem), mem.numel() * mem.element_size(), C.byref(ws),
+                                        _stream(stream)), "futr_paged_workspace_init")
+    ws._mem = mem
+    return ws
+
+
+def futr_paged_attention(cache, layer, batch, pos, start, table, q, out, ws, scale=0.0, window=0, stream=None):
+    """Attention of the rows q [n_rows, heads, head_dim] over the cache into out
+    (same shape and type); scale 0 is 1/sqrt(head_dim), window 0 is none."""
+    device, st = _current(stream)
+    shape = (q.shape[0], cache.shape.n_q_heads, cache.shape.head_dim)
+    if out.dtype != q.dtype:
+        raise TypeError("q and out must have the same type")
+    ld_q, ld_out = _rows(q, "q", device, shape), _rows(out, "out", device, shape)
+    r = _paged_rows(cache, batch, pos, start, table, shape[0], device)
+    _ok(lib().futr_paged_attention(C.addressof(cache), layer, batch, *r, q.data_ptr(), ld_q, out.data_ptr(), ld_out,
+                                   _dtype16(q), scale, window, C.addressof(ws), st), "futr_paged_attention")
+
+
+def futr_paged_check(cache, ws=None, stream=None) -> int:
+    """Synchronize and return the device status (0 = ok); does not raise."""
+    return lib().futr_paged_check(C.byref(cache), C.byref(ws) if ws is not None else None, _stream(stream))
+
+
+# ----------------------------------------------------------------------------
+# mixture of experts
+# ----------------------------------------------------------------------------
+
+def make_moe_shape(hidden, inter, n_experts, top_k, renorm=True, rms_eps=1e-5, group=128) -> futr_moe_shape:
+    return futr_moe_shape(hidden, inter, n_experts, top_k, group, int(renorm), rms_eps)
+
+
+def futr_moe_weights_size(shape) -> int:
+    n = C.c_size_t()
+    _ok(lib().futr_moe_weights_size(C.byref(shape), C.byref(n)), "futr_moe_weights_size")
+    return n.value
+
+
+def _dense(t, name: str, dtype, shape, device: int) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of the shape {shape}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on CUDA device {device}, the current one")
+    return t.data_ptr()
+
+
+def futr_moe_pack(shape, expert, wgate, wup, wdown, gain, blob, stream=None):
+    import torch
+    device, st = _current(stream)
+    H, I, f32 = shape.hidden, shape.inter, torch.float32
+    _ok(lib().futr_moe_pack(C.byref(shape), expert, _dense(wgate, "wgate", f32, (I, H), device),
+                            _dense(wup, "wup", f32, (I, H), device), _dense(wdown, "wdown", f32, (H, I), device),
+                            _dense(gain, "gain", f32, (H,), device), _ptr(blob), blob.numel() * blob.element_size(),
+                            st), "futr_moe_pack")
+
+
+def futr_moe_unpack(shape, blob, expert, which, codes, scales, stream=None):
+    _ok(lib().futr_moe_unpack(C.byref(shape), _ptr(blob), expert, which, _ptr(codes), _ptr(scales), _stream(stream)),
+        "futr_moe_unpack")
+
+
+def futr_moe_workspace_size(shape, max_batch) -> int:
+    n = C.c_size_t()
+    _ok(lib().futr_moe_workspace_size(C.byref(shape), max_batch, C.byref(n)), "futr_moe_workspace_size")
+    return n.value
+
+
+def futr_moe_workspace_init(shape, max_batch, mem, stream=None) -> futr_moe_ws:
+    ws = futr_moe_ws()
+    _ok(lib().futr_moe_workspace_init(C.byref(shape), max_batch, _ptr(mem), mem.numel() * mem.element_size(),
+                                      C.byref(ws), _stream(stream)), "futr_moe_workspace_init")
+    ws._mem = mem
+    return ws
+
+
+def futr_moe_layer(x, gain, router, blob, resid, y, ws, ids=None, weights=None, stream=None):
+    """The layer of x [batch, hidden] (bf16) into y; resid, gain, ids and weights may be None."""
+    import torch
+    device, st = _current(stream)
+    s = ws.shape
+    H, E, bf = s.hidden, s.n_experts, torch.bfloat16
+    rows, picks = (x.shape[0], H), (x.shape[0], s.top_k)
+    if blob.numel() * blob.element_size() < futr_moe_weights_size(s):
+        raise ValueError("blob is smaller than the layer's packed experts")
+    if blob.get_device() != device:
+        raise ValueError(f"blob must be on CUDA device {device}, the current one")
+    _ok(lib().futr_moe_layer(_dense(x, "x", bf, rows, device), _dense(gain, "gain", torch.float32, (H,), device),
+                             _dense(router, "router", bf, (E, H), device), blob.data_ptr(), rows[0],
+                             _dense(resid, "resid", bf, rows, device), _dense(y, "y", bf, rows, device),
+                             _dense(ids, "ids", torch.int32, picks, device),
+                             _dense(weights, "weights", torch.float32, picks, device), C.addressof(ws), st),
+        "futr_moe_layer")
+
+
+def futr_moe_check(ws, stream=None) -> int:
+    """Synchronize and return the device status (0 = ok); does not raise."""
+    return lib().futr_moe_check(C.byref(ws), _stream(stream))
 
 
 # ----------------------------------------------------------------------------

@@ -1,0 +1,362 @@
+"""Paged 8-bit cache: append and attention against plain 64-bit forms."""
+import math
+
+import pytest
+import torch
+
+from int4_weight_kv_w4a16_gb300 import futr
+from tests._gpu_helpers import ensure_lib
+from tests._paged_ref import F64, Paged, ints, page_scale, rotate, starts
+
+pytestmark = pytest.mark.gpu
+
+HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_lib()
+
+
+def rows(n, heads, d, dtype, seed, fused=False, gain=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((n, heads + (3 if fused else 0), d), generator=g, device="cuda") * gain
+    return x.to(dtype)[:, 1:1 + heads] if fused else x.to(dtype)
+
+
+# ----------------------------------------------------------------- append --
+
+def check_append(c, before, k, v, pos, counts, layer=0):
+    """Codes and scales of the touched pages against the definition in 64 bits.
+
+    A code is e4m3's rounding of x / s: off by half a step, 2^-4 |x| + 2^-10 s, and x
+    itself by the rotation's three fp32 roundings, 3 * 2^-24 (|x1| + |x2|)."""
+    codes0, scales0 = before
+    x = torch.stack([k.to(F64), v.to(F64)], 2)                                       # [rows, kv-heads, 2, d]
+    at = torch.tensor([pos[b] + i for b, n in enumerate(counts) for i in range(n)], device="cuda")
+    seq = [b for b, n in enumerate(counts) for _ in range(n)]
+    slack = torch.zeros_like(x)
+    if c.rope:
+        x[:, :, 0] = rotate(x[:, :, 0], at, c.shape.rope_theta)
+        d = c.d
+        mag = k.to(F64).abs()
+        slack[:, :, 0] = 3 * 2.0 ** -24 * torch.cat([mag[..., :d // 2] + mag[..., d // 2:]] * 2, -1)
+    touched = {}
+    for i, (b, p) in enumerate(zip(seq, at.tolist())):
+        touched.setdefault(int(c.table[b, p // c.page]), []).append((i, p % c.page))
+    for page in range(c.n_pages):
+        new, old = c.codes[layer, page].to(F64), codes0[page].to(F64)
+        if page not in touched:
+            assert torch.equal(new, old) and torch.equal(c.scales[layer, page], scales0[page]), page
+            continue
+        idx, slots = [t[0] for t in touched[page]], [t[1] for t in touched[page]]
+        amax = x[idx].abs().amax((0, 3))
+        for h in range(c.kv_heads):
+            for w in range(2):
+                s_old = 0.0 if 0 in slots else float(scales0[page, h, w])
+                s = max(s_old, page_scale(float(amax[h, w])))
+                assert float(c.scales[layer, page, h, w]) == s, (page, h, w)
+                err = (new[h, w, slots] * s - x[idx, h, w]).abs()
+                tol = 2.0 ** -4 * x[idx, h, w].abs() + 2.0 ** -10 * s + slack[idx, h, w]
+                assert bool((err <= tol).all()), (page, h, w, float((err - tol).max()))
+                keep = [j for j in range(c.page) if j not in slots]
+                want = old[h, w, keep]
+                if s_old > 0 and s > s_old:
+                    want = (want * (s_old / s)).float().to(torch.float8_e4m3fn).to(F64)
+                assert torch.equal(new[h, w, keep], want), (page, h, w)
+
+
+APPEND = [
+    # page, d, kv-heads, rope, dtype, fused, positions, rows of each sequence
+    (16, 128, 8, True, torch.bfloat16, False, [0], [1]),
+    (16, 64, 2, True, torch.float16, False, [15, 16, 17], [1, 1, 1]),
+    (32, 128, 2, True, torch.bfloat16, True, [5, 0, 63], [3, 0, 66]),
+    (64, 64, 4, True, torch.float16, True, [0, 1], [257, 63]),
+    (64, 128, 1, False, torch.bfloat16, False, [60, 7], [9, 1]),
+    (128, 128, 4, True, torch.float16, False, [127, 255, 3], [2, 1, 300]),
+    (16, 128, 2, True, torch.bfloat16, False, list(range(3, 40)), [1 + i % 3 for i in range(37)]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(APPEND)))
+@pytest.mark.parametrize("gain", [1.0, 37.0], ids=["same", "grown"])
+def test_append(case, gain):
+    page, d, hkv, rope, dtype, fused, pos, counts = APPEND[case]
+    width = -(-max(p + n for p, n in zip(pos, counts)) // page) + 1
+    c = Paged(2 * hkv, hkv, d, page, len(pos), width, layers=2, rope=rope)
+    c.fill(1, layer=1)
+    other = c.codes[0].clone()
+    before = c.codes[1].clone(), c.scales[1].clone()
+    n = sum(counts)
+    k, v = rows(n, hkv, d, dtype, 2, fused, gain), rows(n, hkv, d, dtype, 3, fused, gain)
+    futr.futr_paged_append(c.cache, 1, len(pos), ints(pos), starts(counts), c.table, k, v)
+    assert futr.futr_paged_check(c.cache) == futr.FUTR_OK
+    check_append(c, before, k, v, pos, counts, layer=1)
+    assert torch.equal(c.codes[0].view(torch.uint8), other.view(torch.uint8))
+    # the same rows again change nothing
+    once = c.codes[1].clone(), c.scales[1].clone()
+    futr.futr_paged_append(c.cache, 1, len(pos), ints(pos), starts(counts), c.table, k, v)
+    assert torch.equal(c.codes[1].view(torch.uint8), once[0].view(torch.uint8)) and torch.equal(c.scales[1], once[1])
+
+
+def test_append_grows_a_page_token_by_token():
+    """A page whose every token is twice the last: each growth halves the old codes, and
+    a value keeps its first rounding until it reaches e4m3's subnormals."""
+    c = Paged(2, 1, 128, 16, 1, 1, rope=False)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((16, 1, 128), generator=g, device="cuda") * 2.0 ** torch.arange(16, device="cuda")[:, None, None]
+    x = x.to(torch.bfloat16)
+    for i in range(16):
+        futr.futr_paged_append(c.cache, 0, 1, ints([i]), None, c.table, x[i:i + 1], x[i:i + 1])
+    assert futr.futr_paged_check(c.cache) == futr.FUTR_OK
+    k, v = c.values(0, 16)
+    s = page_scale(float(x.abs().max()))
+    assert float(c.scales[0, int(c.table[0, 0]), 0, 0]) == s
+    for t in (k, v):
+        err = (t[0] - x[:, 0].to(F64)).abs()
+        # half a step at first; each of the 15 growths may cost a subnormal half its step, at scales
+        # that double: in all less than 2 * 2^-10 s
+        assert bool((err <= 2.0 ** -4 * x[:, 0].to(F64).abs() + 2 * 2.0 ** -10 * s).all())
+
+
+def test_append_values_of_every_size():
+    """Zeros, subnormals, the largest bf16 values and ties."""
+    c = Paged(2, 1, 64, 16, 6, 1, rope=False)
+    x = torch.zeros((6, 1, 64), dtype=torch.bfloat16, device="cuda")
+    x[1] = 1e-40
+    x[2] = 3.38e38
+    x[3, 0, :32], x[3, 0, 32:] = 448.0, 0.0009765625   # 2^-10: half of e4m3's smallest, a tie to zero
+    x[4, 0] = 1.0625                                     # between 1 and 1.125: a tie to 1
+    x[4, 0, 0] = 448.0
+    x[5, 0] = -449.0                                     # bf16 rounds it to 448 or 450: the scale follows
+    futr.futr_paged_append(c.cache, 0, 6, ints([0] * 6), None, c.table, x, x)
+    assert futr.futr_paged_check(c.cache) == futr.FUTR_OK
+    for b in range(6):
+        k, v = c.values(b, 1)
+        s = page_scale(float(x[b].abs().max()))
+        assert float(c.scales[0, int(c.table[b, 0]), 0, 0]) == s
+        want = (x[b, 0].to(F64) / s).float().to(torch.float8_e4m3fn).to(F64) * s
+        assert torch.equal(k[0, 0], want) and torch.equal(v[0, 0], want), b
+
+
+def test_append_reports_what_is_not_finite():
+    c = Paged(2, 1, 64, 16, 2, 1)
+    x = rows(2, 1, 64, torch.bfloat16, 3)
+    y = x.clone()
+    y[0, 0, 5], y[1, 0, 9] = math.inf, math.nan
+    futr.futr_paged_append(c.cache, 0, 2, ints([0, 3]), None, c.table, x, y)
+    assert futr.futr_paged_check(c.cache) == futr.FUTR_ERR_NOT_FINITE
+    assert futr.futr_paged_check(c.cache) == futr.FUTR_OK
+    z = x.clone()
+    z[0, 0, 5], z[1, 0, 9] = 0.0, 0.0
+    assert bool(torch.isfinite(c.codes.to(torch.float32)).all())
+    for b, p in ((0, 0), (1, 3)):
+        v = c.values(b, p + 1)[1][0, p]
+        s = page_scale(float(z[b].abs().max()))
+        assert torch.equal(v, (z[b, 0].to(F64) / s).float().to(torch.float8_e4m3fn).to(F64) * s)
+
+
+# -------------------------------------------------------------- attention --
+
+ATTN = [
+    # heads, kv-heads, d, page, dtype, fused, window, positions, rows of each sequence
+    (32, 8, 128, 16, torch.bfloat16, False, 0, [0], [1]),
+    (32, 8, 128, 16, torch.bfloat16, False, 0, [1023], [1]),
+    (32, 8, 128, 64, torch.bfloat16, True, 0, [3, 64, 1000, 127, 15], [1, 1, 1, 1, 1]),
+    (8, 1, 128, 128, torch.float16, False, 0, [5000, 40], [1, 1]),
+    (10, 2, 64, 32, torch.float16, True, 0, [77, 200], [1, 1]),
+    (28, 4, 128, 32, torch.bfloat16, False, 100, [90, 99, 100, 101, 700], [1, 1, 1, 1, 1]),
+    (32, 2, 64, 16, torch.bfloat16, False, 0, [333, 12], [1, 1]),
+    (16, 1, 128, 64, torch.float16, False, 0, [2000], [1]),
+    (32, 8, 128, 64, torch.bfloat16, True, 0, [0, 5, 300], [37, 0, 4]),
+    (16, 4, 64, 16, torch.float16, False, 33, [0, 250], [70, 5]),
+    (4, 4, 128, 128, torch.bfloat16, False, 0, [100, 0, 1], [130, 1, 0]),
+    (64, 8, 128, 64, torch.bfloat16, False, 1, [70, 0], [3, 2]),
+    (16, 16, 64, 64, torch.bfloat16, True, 0, [i * 37 % 400 for i in range(45)], [1 + (i % 5 == 0) for i in range(45)]),
+]
+
+
+def run_attention(c, q, pos, counts, window=0, start=True, scale=0.0, layer=0):
+    out = torch.full((q.shape[0] + 2, c.heads, c.d), 7.0, dtype=q.dtype, device="cuda")
+    futr.futr_paged_attention(c.cache, layer, len(pos), ints(pos), starts(counts) if start else None, c.table, q,
+                              out[1:-1], c.ws, scale=scale, window=window)
+    assert futr.futr_paged_check(c.cache, c.ws) == futr.FUTR_OK
+    assert bool((out[0] == 7).all()) and bool((out[-1] == 7).all())
+    return out[1:-1]
+
+
+def check_attention(c, q, got, pos, counts, window=0, scale=None, layer=0):
+    """The output's rounding, half a step, and what the operands' fp16 roundings
+    can move it by: 2^-11 of each weight, and of the query, whose score error
+    moves a weight by as much relatively."""
+    want, bound = c.attention(q, pos, counts, window, scale, layer)
+    err = (got.to(F64) - want).abs()
+    tol = HALF_STEP[q.dtype] * want.abs() + bound + 2.0 ** -24
+    assert bool((err <= tol).all()), float((err / tol).max())
+    assert float(err.norm() / want.norm()) <= 2 * HALF_STEP[q.dtype] + 2.0 ** -9
+
+
+@pytest.mark.parametrize("case", range(len(ATTN)))
+def test_attention(case):
+    heads, hkv, d, page, dtype, fused, window, pos, counts = ATTN[case]
+    width = -(-max(p + n for p, n in zip(pos, counts)) // page) + 1
+    c = Paged(heads, hkv, d, page, len(pos), width, layers=2)
+    c.fill(case, layer=1)
+    q = rows(sum(counts), heads, d, dtype, case + 50, fused)
+    got = run_attention(c, q, pos, counts, window, layer=1)
+    check_attention(c, q, got, pos, counts, window, layer=1)
+    again = run_attention(c, q, pos, counts, window, layer=1)
+    assert torch.equal(again, got)   # no sum depends on timing
+    if all(n == 1 for n in counts):
+        assert torch.equal(run_attention(c, q, pos, counts, window, start=False, layer=1), got)
+
+
+def test_attention_scale_and_large_scores():
+    """A scale of its own, and scores so far apart that one key takes the whole weight."""
+    c = Paged(8, 2, 128, 32, 2, 20)
+    c.fill(3)
+    q = rows(2, 8, 128, torch.float16, 4)
+    check_attention(c, q, run_attention(c, q, [600, 31], [1, 1], scale=0.01), [600, 31], [1, 1], scale=0.01)
+    q = (q * 300).to(torch.float16)
+    got = run_attention(c, q, [600, 31], [1, 1]).to(F64)
+    want, _ = c.attention(q, [600, 31], [1, 1])
+    assert bool(torch.isfinite(got).all())
+    # a score can move by more than 1 here: the output is still a mean of the values
+    assert float(got.abs().max()) <= float(c.values(0, 601)[1].abs().max()) * (1 + 2.0 ** -10)
+    assert float((got - want).norm() / want.norm()) < 0.2
+
+
+def test_attention_pages_of_very_different_value_scales():
+    """Value scales 2^40 apart: the page that holds the weight decides, large or small."""
+    c = Paged(4, 1, 128, 16, 1, 8, rope=False)
+    c.fill(2, gain=1.0)
+    ids = c.table[0].long()
+    c.scales[0, ids[1], 0, 1] *= 2.0 ** 40
+    c.scales[0, ids[3], 0, 1] *= 2.0 ** -40
+    c.codes[0, ids[5], 0, 1] = torch.zeros((16, 128), device="cuda").to(torch.float8_e4m3fn)
+    c.scales[0, ids[5], 0, 1] = 2.0 ** -60
+    q = rows(1, 4, 128, torch.bfloat16, 9)
+    check_attention(c, q, run_attention(c, q, [127], [1]), [127], [1])
+    # all weight on one page: its keys along the query, the others against it
+    for hot in (3, 5, 0):
+        c.fill(2, gain=1.0)
+        c.scales[0, ids[1], 0, 1] *= 2.0 ** 40
+        c.scales[0, ids[3], 0, 1] *= 2.0 ** -40
+        c.scales[0, ids[5], 0, 1] *= 2.0 ** -20
+        line = torch.sign(q[0, 0].float())
+        for j in range(8):
+            sign = 1.0 if j == hot else -1.0
+            c.codes[0, ids[j], 0, 0] = (sign * 448 * line).expand(16, -1).to(torch.float8_e4m3fn)
+            c.scales[0, ids[j], 0, 0] = 2.0 ** -6
+        one = q[:, :1].expand(-1, 4, -1).contiguous()
+        check_attention(c, one, run_attention(c, one, [127], [1]), [127], [1])
+
+
+def test_attention_ignores_what_unwritten_slots_hold():
+    """NaN codes and any scale behind the last token, and in pages of no one, change nothing."""
+    c = Paged(8, 2, 64, 32, 2, 4)
+    c.fill(1)
+    pos, counts = [40, 3], [2, 1]
+    q = rows(3, 8, 64, torch.bfloat16, 2)
+    got = run_attention(c, q, pos, counts)
+    bits = c.codes.view(torch.uint8)
+    used = {int(c.table[0, 0]): 32, int(c.table[0, 1]): 10, int(c.table[1, 0]): 4}
+    for p in range(c.n_pages):
+        bits[0, p, :, :, used.get(p, 0):] = 0x7F
+        if p not in used:
+            c.scales[0, p] = math.nan
+    c.table[0, 2:] = -5
+    c.table[1, 1:] = 1 << 30
+    assert torch.equal(run_attention(c, q, pos, counts), got)
+
+
+def test_bad_rows_and_pages_are_reported_and_skipped():
+    c = Paged(8, 2, 64, 16, 3, 4)
+    c.fill(1)
+    q, k = rows(3, 8, 64, torch.bfloat16, 2), rows(3, 2, 64, torch.bfloat16, 3)
+    good = run_attention(c, q, [20, 30, 40], [1, 1, 1])
+    for pos in ([20, 64, 40], [20, -1, 40], [20, 2 ** 31 - 1, 40]):
+        out = torch.zeros_like(good)
+        futr.futr_paged_attention(c.cache, 0, 3, ints(pos), None, c.table, q, out, c.ws)
+        assert futr.futr_paged_check(c.cache, c.ws) == futr.FUTR_ERR_OUT_OF_RANGE
+        assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2]) and bool((out[1] == 0).all())
+        before = c.codes.clone().view(torch.uint8)
+        futr.futr_paged_append(c.cache, 0, 3, ints(pos), None, c.table, k, k)
+        assert futr.futr_paged_check(c.cache) == futr.FUTR_ERR_OUT_OF_RANGE
+        changed = (c.codes.view(torch.uint8) != before).flatten(2).any(-1)[0].nonzero().flatten().tolist()
+        assert sorted(changed) == sorted([int(c.table[0, 1]), int(c.table[2, 2])])
+        c.fill(1)
+    # rows that are not in order, and rows past the end
+    for start in ([0, 2, 1, 3], [0, 1, 2, 4], [-1, 0, 1, 3]):
+        out = torch.zeros_like(good)
+        futr.futr_paged_attention(c.cache, 0, 3, ints([20, 30, 40]), ints(start), c.table, q, out, c.ws)
+        assert futr.futr_paged_check(c.cache, c.ws) == futr.FUTR_ERR_OUT_OF_RANGE
+        futr.futr_paged_append(c.cache, 0, 3, ints([20, 30, 40]), ints(start), c.table, k, k)
+        assert futr.futr_paged_check(c.cache) == futr.FUTR_ERR_OUT_OF_RANGE
+    # page ids outside the pool: not visible, not written
+    c.fill(1)
+    tab = c.table.clone()
+    tab[1, 0], tab[1, 1] = -1, c.n_pages
+    out = torch.full_like(good, 7.0)
+    futr.futr_paged_attention(c.cache, 0, 3, ints([20, 30, 40]), None, tab, q, out, c.ws)
+    assert futr.futr_paged_check(c.cache, c.ws) == futr.FUTR_ERR_OUT_OF_RANGE
+    assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2]) and bool((out[1] == 0).all())
+    before = c.codes.clone().view(torch.uint8)
+    futr.futr_paged_append(c.cache, 0, 3, ints([20, 30, 40]), None, tab, k, k)
+    assert futr.futr_paged_check(c.cache) == futr.FUTR_ERR_OUT_OF_RANGE
+    assert int((c.codes.view(torch.uint8) != before).flatten(2).any(-1).sum()) == 2
+
+
+def test_append_then_attention_in_a_graph_and_on_another_stream():
+    """One captured append + attention follows tables, positions and rows that change between replays."""
+    c = Paged(32, 8, 128, 16, 3, 40)
+    c.fill(4)
+    pos, counts = ints([5, 100, 31]), [1, 1, 1]
+    q, k, v = (rows(3, h, 128, torch.bfloat16, 20 + h) for h in (32, 8, 8))
+    out = torch.empty_like(q)
+
+    def step():
+        futr.futr_paged_append(c.cache, 0, 3, pos, None, c.table, k, v)
+        futr.futr_paged_attention(c.cache, 0, 3, pos, None, c.table, q, out, c.ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        lens = [5 + 150 * i, 100 + i, 31 + i]
+        pos.copy_(ints(lens))
+        for t, s in ((q, 1), (k, 2), (v, 3)):
+            t.copy_(rows(3, t.shape[1], 128, torch.bfloat16, 100 * i + s))
+        before = c.codes[0].clone(), c.scales[0].clone()
+        graph.replay()
+        assert futr.futr_paged_check(c.cache, c.ws) == futr.FUTR_OK
+        check_append(c, before, k, v, lens, counts)
+        check_attention(c, q, out, lens, counts)
+
+
+def test_shared_pages_and_prompts_in_pieces():
+    """Two sequences that read the same first pages; a prompt in one call and in pieces gives
+    the same output where the pages' scales are the same (values of one size)."""
+    c = Paged(8, 2, 128, 32, 2, 8)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = 200
+    k = torch.where(torch.rand((n, 2, 128), generator=g, device="cuda") < 0.5, -1.0, 1.0).to(torch.bfloat16)
+    q = rows(n, 8, 128, torch.bfloat16, 6)
+    futr.futr_paged_append(c.cache, 0, 1, ints([0]), ints([0, n]), c.table[:1], k, k)
+    whole = torch.empty_like(q)
+    futr.futr_paged_attention(c.cache, 0, 1, ints([0]), ints([0, n]), c.table[:1], q, whole, c.ws)
+    check_attention(c, q, whole, [0], [n])
+    table = c.table.clone()
+    table[1, :3] = table[0, :3]          # 96 positions shared
+    m = n - 96
+    futr.futr_paged_append(c.cache, 0, 1, ints([96]), ints([0, m]), table[1:].contiguous(), k[96:], k[96:])
+    part = torch.empty_like(q[96:])
+    futr.futr_paged_attention(c.cache, 0, 1, ints([96]), ints([0, m]), table[1:].contiguous(), q[96:], part, c.ws)
+    c.table = table[1:].contiguous()
+    check_attention(c, q[96:], part, [96], [m])
+    assert futr.futr_paged_check(c.cache, c.ws) == futr.FUTR_OK
