@@ -5,7 +5,7 @@
 //   o   = sum_j 2^(x_j log2 e) v_j / sum_j 2^(x_j log2 e)
 //
 // A row tile is up to R = 8 NT rows of one sequence that share a kv-head (row =
-// new token x query head of the group).  Its work is a run of 64-position
+// new token x query head of the group).  Its work is a run of 128-position
 // tiles; all runs of the call, one after the other, are cut into equal
 // contiguous shares, one per CTA of a grid that fills the GPU once.  The cut is
 // made on the device from the sequences' lengths, so ragged batches balance
@@ -13,9 +13,9 @@
 // CTAs leaves one record (m, l, O) per CTA; the CTA that arrives last adds them
 // in CTA order: no result depends on timing.
 //
-// In a CTA warp 4 streams tiles (2- or 3-D tensor copies, one per page up to 64
-// positions, swizzled so that the fragment reads below meet no bank conflicts)
-// through a ring, warps 0..3 take 16 positions of each tile:
+// In a CTA warp 4 streams tiles (tensor copies, one per page, swizzled so that
+// the fragment reads below meet no bank conflicts) through a ring, warps 0..3
+// take 32 positions of each tile:
 //   S^T = K q'^T: mma.m16n8k16 f16, A = 16 positions of key codes converted in
 //     registers (exact: e4m3 is a subset of f16), B = the rows as columns;
 //   w = 2^(x + log2(value scale) - M), M the running maximum of that exponent:
@@ -37,23 +37,24 @@ namespace {
 
 constexpr int kPaCW = 4;                        // consumer warps
 constexpr int kPaThreads = (kPaCW + 1) * 32;
-constexpr int kPaTile = 64;                     // positions of a tile
-constexpr int kPaRing = 4;
+constexpr int kPaTile = 128;                    // positions of a tile: 32 a warp
+constexpr int kPaSub = kPaTile / 16;            // 16-position sub-tiles: what one page is a multiple of
 constexpr unsigned long long kPaWaitNs = 1000000000ull;
 
 template <int D, int NT>
 struct PaLayout {
   static constexpr int R = 8 * NT;
+  static constexpr int kRing = D == 128 ? 2 : 4;                // 64 KB: three CTAs share an SM's memory
   static constexpr int kStage = 2 * kPaTile * D;                // K and V codes
-  static constexpr int kScale = kPaRing * kStage;               // [ring][4 sub-tiles] float4 (ks, lv, 1/vs, -)
-  static constexpr int kQ = kScale + kPaRing * 4 * 16;          // query fragments [D/16][NT][32] uint2
+  static constexpr int kScale = kRing * kStage;                 // [ring][sub-tiles] float4 (ks, lv, 1/vs, -)
+  static constexpr int kQ = kScale + kRing * kPaSub * 16;       // query fragments [D/16][NT][32] uint2
   static constexpr int kQs = kQ + (D / 16) * NT * 32 * 8;       // [R] score factors
   static constexpr int kOLd = D + 4;
   static constexpr int kO = kQs + R * 4;                        // [R][kOLd] fp32
   static constexpr int kM = kO + R * kOLd * 4;                  // [4 warps][R]
   static constexpr int kL = kM + kPaCW * R * 4;                 // [4 warps][R]
   static constexpr int kBar = kL + kPaCW * R * 4;
-  static constexpr int kBytes = kBar + 2 * kPaRing * 8 + 32;
+  static constexpr int kBytes = kBar + 2 * kRing * 8 + 32;
 };
 
 __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, const int* err) {
@@ -88,7 +89,7 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
 // ------------------------------------------------------------------ shares --
 
 // Row tile rt of a sequence (n rows from position p0, G query heads a kv-head,
-// R rows a tile): its 64-position tiles [t0, t1).
+// R rows a tile): its tiles [t0, t1).
 struct TileRange {
   int t0, t1;
 };
@@ -110,7 +111,7 @@ __device__ __forceinline__ long long seq_tiles(int n, int p0, int G, int R, int 
 }
 
 // The position of a CTA in the call's work: sequence b, kv-head, row tile and
-// the next 64-position tile.  Every warp keeps its own copy and steps it the
+// the next tile.  Every warp keeps its own copy and steps it the
 // same way.
 struct Walk {
   int b, kvh, rt, row0, n, p0;
@@ -157,17 +158,26 @@ struct Walk {
 __device__ __forceinline__ int find_share(const PagedAttnArgs& a, int R, int cta, int ctas, Walk& w, long long& total,
                                           bool report) {
   const int lane = threadIdx.x & 31;
+  int row0 = 0, n = 0, p0 = 0;   // of sequence b0 + lane
+  long long per = 0, incl = 0;   // its tiles per kv-head; all tiles of this round's sequences up to it
+  auto look = [&](int b0) {
+    n = 0;
+    per = 0;
+    if (b0 + lane < a.r.batch) {
+      if (!paged_seq(a.r, a.c, b0 + lane, row0, n, p0) && report) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
+      per = seq_tiles(n, p0, a.G, R, a.window);
+    }
+    incl = per * a.Hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+  };
   total = 0;
   for (int b0 = 0; b0 < a.r.batch; b0 += 32) {
-    long long units = 0;
-    if (b0 + lane < a.r.batch) {
-      int row0, n, p0;
-      if (!paged_seq(a.r, a.c, b0 + lane, row0, n, p0) && report) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
-      units = seq_tiles(n, p0, a.G, R, a.window) * a.Hkv;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
-    total += units;
+    look(b0);
+    total += __shfl_sync(0xffffffffu, incl, 31);
   }
   const int use = (int)(total < ctas ? total : ctas);
   if (cta >= use) return use;
@@ -175,18 +185,7 @@ __device__ __forceinline__ int find_share(const PagedAttnArgs& a, int R, int cta
   w.u1 = total * (cta + 1) / use;
   long long before = 0;
   for (int b0 = 0; b0 < a.r.batch; b0 += 32) {
-    int row0 = 0, n = 0, p0 = 0;
-    long long per = 0;
-    if (b0 + lane < a.r.batch) {
-      paged_seq(a.r, a.c, b0 + lane, row0, n, p0);
-      per = seq_tiles(n, p0, a.G, R, a.window);
-    }
-    long long incl = per * a.Hkv;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
+    if (a.r.batch > 32) look(b0);   // up to 32 sequences: still at hand
     const unsigned hit = __ballot_sync(0xffffffffu, before + incl > w.u);
     if (hit) {
       const int src = __ffs(hit) - 1;
@@ -206,12 +205,22 @@ __device__ __forceinline__ int find_share(const PagedAttnArgs& a, int R, int cta
 
 // ---------------------------------------------------------------- consumer --
 
+// The consumers' current item, in shared memory: its bounds are read where they
+// are needed instead of being held in registers through the tile loop.
+struct PaItem {
+  Walk w;
+  int first, count, valid;       // tiles of this CTA's part, rows of the tile
+  int written;                   // positions below it exist
+  int hi_min, lo_max;            // positions [lo_max, hi_min] are visible to every row
+  int hi_max, lo_min;            // positions that some row sees
+  int back;                      // a row at p sees positions >= p - back
+  int hi[16];                    // each row's position
+};
+
 template <int D, int NT>
 struct PaWarp {
   float m[NT][2], l[NT][2], o[D / 16][NT][4];
   float qs[NT][2];
-  int hi[NT][2], lo[NT][2];   // visible positions of this lane's columns
-  int hi_min, lo_max;         // positions [lo_max, hi_min] are visible to every row
 
   __device__ __forceinline__ void init() {
 #pragma unroll
@@ -229,53 +238,77 @@ struct PaWarp {
         for (int e = 0; e < 4; ++e) o[j][nt][e] = 0.f;
   }
 
-  // 16 positions from pos0: key codes at ks_, value codes at vs_ (16 rows of D
-  // bytes each, swizzled by the copy), sc = (key scale, log2 and inverse of the
-  // value scale); qf: the query fragments.  `written`: positions below it exist.
-  __device__ __forceinline__ void sub_tile(const uint8_t* ks_, const uint8_t* vs_, float4 sc, const uint2* qf, int pos0,
-                                           int written) {
+  // 32 positions from pos0, in two halves of 16: key codes at ks[h], value codes
+  // at vs[h] (16 rows of D bytes each, swizzled by the copy), sc[h] = (key scale,
+  // log2 and inverse of the value scale); qf: the query fragments; positions
+  // below it.written exist.  Two halves at a time: their products are
+  // independent chains, and they share one maximum.
+  __device__ __forceinline__ void tile32(const uint8_t* const (&ks)[2], const uint8_t* const (&vs)[2],
+                                         const float4 (&sc)[2], const uint2* qf, const PaItem& it, int pos0) {
     constexpr int CH = D / 64;   // 16-byte chunks of a lane's key dims
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int swz = D == 128 ? g : (g >> 1) & 3;   // rows g and g + 8 share it
-    float s[NT][4];
+    float s[2][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[h][nt][e] = 0.f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int ch = (CH * t + j) ^ swz;
-      const uint4 k0 = *reinterpret_cast<const uint4*>(ks_ + g * D + ch * 16);
-      const uint4 k1 = *reinterpret_cast<const uint4*>(ks_ + (g + 8) * D + ch * 16);
-      const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+      uint32_t w[2][2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint4 k = *reinterpret_cast<const uint4*>(ks[h] + (g + 8 * r) * D + ch * 16);
+          w[h][r][0] = k.x; w[h][r][1] = k.y; w[h][r][2] = k.z; w[h][r][3] = k.w;
+        }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t af[4];
-        cvt4(w0[i], af[0], af[2]);
-        cvt4(w1[i], af[1], af[3]);
+        uint32_t af[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          cvt4(w[h][0][i], af[h][0], af[h][2]);
+          cvt4(w[h][1][i], af[h][1], af[h][3]);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint2 q = qf[((4 * j + i) * NT + nt) * 32 + lane];
-          mma_f16_16816(s[nt], af, q.x, q.y);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) mma_f16_16816(s[h][nt], af[h], q.x, q.y);
         }
       }
     }
-    const int pa = pos0 + g, pb = pa + 8;
-    const bool all = pos0 >= lo_max && pos0 + 15 <= hi_min;
-    uint32_t bt[NT], bb[NT];
+    // positions below end[h] of a half exist (a missing page: none of them)
+    int end[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) end[h] = sc[h].y == -INFINITY ? 0 : it.written;
+    const bool all = pos0 >= it.lo_max && pos0 + 31 <= it.hi_min && end[0] > 0 && end[1] > 0;
+    uint32_t bt[2][NT], bb[2][NT];
     bool moved = false;
     float corr[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float f = sc.x * qs[nt][e];
-        float xa = fmaf(s[nt][e], f, sc.y), xb = fmaf(s[nt][2 + e], f, sc.y);
-        if (!all) {
-          if (pa > hi[nt][e] || pa < lo[nt][e]) xa = -INFINITY;
-          if (pb > hi[nt][e] || pb < lo[nt][e]) xb = -INFINITY;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float f = sc[h].x * qs[nt][e];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float x = fmaf(s[h][nt][2 * r + e], f, sc[h].y);
+            if (!all) {
+              const int p = pos0 + 16 * h + 8 * r + g, top = it.hi[8 * nt + 2 * t + e];
+              if (p > top || p < top - it.back || p >= end[h]) x = -INFINITY;
+            }
+            s[h][nt][2 * r + e] = x;
+            mx = fmaxf(mx, x);
+          }
         }
-        float mx = fmaxf(xa, xb);
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
         const float mn = fmaxf(m[nt][e], mx);
@@ -283,12 +316,21 @@ struct PaWarp {
         corr[nt][e] = pa_ex2(m[nt][e] - ref);
         moved |= m[nt][e] != mn;
         m[nt][e] = mn;
-        s[nt][e] = pa_ex2(xa - ref);
-        s[nt][2 + e] = pa_ex2(xb - ref);
-        l[nt][e] = fmaf(s[nt][e] + s[nt][2 + e], sc.z, l[nt][e] * corr[nt][e]);
+        float sum = l[nt][e] * corr[nt][e];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float wa = pa_ex2(s[h][nt][e] - ref), wb = pa_ex2(s[h][nt][2 + e] - ref);
+          s[h][nt][e] = wa;
+          s[h][nt][2 + e] = wb;
+          sum = fmaf(wa + wb, sc[h].z, sum);
+        }
+        l[nt][e] = sum;
       }
-      bt[nt] = movmatrix_trans(pack_half2(s[nt][0], s[nt][1]));
-      bb[nt] = movmatrix_trans(pack_half2(s[nt][2], s[nt][3]));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bt[h][nt] = movmatrix_trans(pack_half2(s[h][nt][0], s[h][nt][1]));
+        bb[h][nt] = movmatrix_trans(pack_half2(s[h][nt][2], s[h][nt][3]));
+      }
     }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -301,32 +343,43 @@ struct PaWarp {
           o[j][nt][3] *= corr[nt][1];
         }
     }
-    // slots that no row has been written to may hold anything, NaN codes
-    // included: their codes are cleared (a weight of 0 alone would not do)
-    uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-    if (pos0 + 16 > written) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) keep[i] = pos0 + 2 * t + (i & 1) + 8 * (i >> 1) < written ? ~0u : 0u;
-    }
+    for (int h = 0; h < 2; ++h) {
+      // slots that no row has been written to may hold anything, NaN codes
+      // included: their codes are cleared (a weight of 0 alone would not do)
+      const int p1 = pos0 + 16 * h;
+      uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+      if (p1 + 16 > end[h]) {
 #pragma unroll
-    for (int jj = 0; jj < D / 32; ++jj) {
-      uint32_t v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-        const int ch = (2 * jj + (g >> 2)) ^ (D == 128 ? row & 7 : (row >> 1) & 3);
-        v[i] = *reinterpret_cast<const uint32_t*>(vs_ + row * D + ch * 16 + (g & 3) * 4) & keep[i];
+        for (int i = 0; i < 4; ++i) keep[i] = p1 + 2 * t + (i & 1) + 8 * (i >> 1) < end[h] ? ~0u : 0u;
       }
-      uint32_t p0a, p0b, p1a, p1b, p2a, p2b, p3a, p3b;   // dims 0..3 of this lane, position pairs a, b
-      cvt4(__byte_perm(v[0], v[1], 0x5140), p0a, p1a);
-      cvt4(__byte_perm(v[0], v[1], 0x7362), p2a, p3a);
-      cvt4(__byte_perm(v[2], v[3], 0x5140), p0b, p1b);
-      cvt4(__byte_perm(v[2], v[3], 0x7362), p2b, p3b);
-      const uint32_t a0[4] = {p0a, p1a, p0b, p1b}, a1[4] = {p2a, p3a, p2b, p3b};
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mma_f16_16816(o[2 * jj][nt], a0, bt[nt], bb[nt]);
-        mma_f16_16816(o[2 * jj + 1][nt], a1, bt[nt], bb[nt]);
+      for (int jj = 0; jj < D / 64; ++jj) {
+        // dims 64 jj + 8 g .. + 7 of positions 2t, 2t + 1, 2t + 8, 2t + 9
+        uint2 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+          const int ch = (4 * jj + (g >> 1)) ^ (D == 128 ? row & 7 : (row >> 1) & 3);
+          v[i] = *reinterpret_cast<const uint2*>(vs[h] + row * D + ch * 16 + (g & 1) * 8);
+          v[i].x &= keep[i];
+          v[i].y &= keep[i];
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t v0 = q ? v[0].y : v[0].x, v1 = q ? v[1].y : v[1].x, v2 = q ? v[2].y : v[2].x,
+                         v3 = q ? v[3].y : v[3].x;
+          uint32_t a0[4], a1[4];   // rows g, g + 8: dims 4q, 4q + 1 (a0) and 4q + 2, 4q + 3 (a1)
+          cvt4(__byte_perm(v0, v1, 0x5140), a0[0], a0[1]);
+          cvt4(__byte_perm(v2, v3, 0x5140), a0[2], a0[3]);
+          cvt4(__byte_perm(v0, v1, 0x7362), a1[0], a1[1]);
+          cvt4(__byte_perm(v2, v3, 0x7362), a1[2], a1[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16_16816(o[4 * jj + 2 * q][nt], a0, bt[h][nt], bb[h][nt]);
+            mma_f16_16816(o[4 * jj + 2 * q + 1][nt], a1, bt[h][nt], bb[h][nt]);
+          }
+        }
       }
     }
   }
@@ -344,57 +397,72 @@ __device__ __forceinline__ uint32_t narrow2(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Row r of the tile (one warp): rotated, divided by a power of two and stored
-// as f16 into its place in the B fragments; its score factor to qs[r].
+// Rows warp, warp + 4, ... of the tile: rotated, divided by a power of two and
+// stored as f16 into their places in the B fragments; their score factors to
+// qs.  The loads of all of a warp's rows are in flight together.
 template <int D, int NT, bool kHalf>
-__device__ __forceinline__ void load_query(const PagedAttnArgs& a, const Walk& w, int r, int valid, __half* qf,
-                                           float* qs) {
-  constexpr int J = D / 32, CH = D / 64;
-  const int lane = threadIdx.x & 31;
-  float x[J];
+__device__ __forceinline__ void load_queries(const PagedAttnArgs& a, const Walk& w, int valid, __half* qf, float* qs) {
+  constexpr int J = D / 32, CH = D / 64, RW = 8 * NT / kPaCW;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint16_t u[RW][J];
+  float2 cs[RW][J / 2];
 #pragma unroll
-  for (int j = 0; j < J; ++j) x[j] = 0.f;
-  float factor = 0.f;
-  if (r < valid) {
-    const int row = w.rt * 8 * NT + r, i = row / a.G, head = w.kvh * a.G + row - i * a.G;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (size_t)(w.row0 + i) * a.ld_q + (size_t)head * D;
+  for (int k = 0; k < RW; ++k) {
+    const int r = warp + kPaCW * k;
+    if (r < valid) {
+      const int row = w.rt * 8 * NT + r, i = row / a.G, head = w.kvh * a.G + row - i * a.G;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) + (size_t)(w.row0 + i) * a.ld_q + (size_t)head * D;
 #pragma unroll
-    for (int j = 0; j < J; ++j) x[j] = widen<kHalf>(q[lane + 32 * j]);
-    if (a.c.rope) {
-      const float2* cs = a.c.rope + (size_t)(w.p0 + i) * (D / 2);
+      for (int j = 0; j < J; ++j) u[k][j] = q[lane + 32 * j];
+      if (a.c.rope) {
 #pragma unroll
-      for (int j = 0; j < J / 2; ++j) {
-        const float2 f = cs[lane + 32 * j];
-        const float x1 = x[j], x2 = x[j + J / 2];
-        x[j] = x1 * f.x - x2 * f.y;
-        x[j + J / 2] = x2 * f.x + x1 * f.y;
+        for (int j = 0; j < J / 2; ++j) cs[k][j] = a.c.rope[(size_t)(w.p0 + i) * (D / 2) + lane + 32 * j];
       }
     }
-    float mx = 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) mx = fmaxf(mx, fabsf(x[j]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // exponent of the largest element, kept where 2^e and 2^-e are normal
-    const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-    for (int j = 0; j < J; ++j) x[j] *= inv;
-    factor = __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
   }
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int i = lane + 32 * j, t = i / (16 * CH), rem = i % (16 * CH), ks = (rem / 16) * 4 + (rem % 16) / 4;
-    qf[((ks * NT + (r >> 3)) * 32 + (r & 7) * 4 + t) * 4 + (i & 3)] = __float2half_rn(x[j]);
+  for (int k = 0; k < RW; ++k) {
+    const int r = warp + kPaCW * k;
+    float x[J], factor = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) x[j] = 0.f;
+    if (r < valid) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) x[j] = widen<kHalf>(u[k][j]);
+      if (a.c.rope) {
+#pragma unroll
+        for (int j = 0; j < J / 2; ++j) {
+          const float x1 = x[j], x2 = x[j + J / 2];
+          x[j] = x1 * cs[k][j].x - x2 * cs[k][j].y;
+          x[j + J / 2] = x2 * cs[k][j].x + x1 * cs[k][j].y;
+        }
+      }
+      float mx = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) mx = fmaxf(mx, fabsf(x[j]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // exponent of the largest element, kept where 2^e and 2^-e are normal
+      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int j = 0; j < J; ++j) x[j] *= inv;
+      factor = __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int i = lane + 32 * j, t = i / (16 * CH), rem = i % (16 * CH), ks = (rem / 16) * 4 + (rem % 16) / 4;
+      qf[((ks * NT + (r >> 3)) * 32 + (r & 7) * 4 + t) * 4 + (i & 3)] = __float2half_rn(x[j]);
+    }
+    if (lane == 0) qs[r] = factor;
   }
-  if (lane == 0) qs[r] = factor;
 }
 
 template <int D, int NT, bool kHalf>
-__global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
+__global__ void __launch_bounds__(kPaThreads, NT == 1 ? 3 : 2)
     paged_attn_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap map) {
   using Lay = PaLayout<D, NT>;
-  constexpr int R = Lay::R;
+  constexpr int R = Lay::R, kPaRing = Lay::kRing;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float4* s_scale = reinterpret_cast<float4*>(smem + Lay::kScale);
@@ -409,6 +477,7 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
   volatile int* s_issued = s_dead + 1;
   volatile int* s_last = s_dead + 2;
   volatile int* s_snap = s_dead + 3;                                          // s_dead as the consumers saw it together
+  __shared__ PaItem s_item;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kPaRing; ++i) {
@@ -431,9 +500,9 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
 
   if (warp == kPaCW) {
     // ---------------------------------------------------------- producer --
-    // copies of a tile: whole (page, kv-head) blocks, keys then values, for
-    // pages up to 64 positions; else 64 rows of keys and 64 of values
-    const int ppt = page >= kPaTile ? 1 : kPaTile / page;   // pages of a tile
+    // copies of a tile: whole (page, kv-head) blocks, keys then values
+    const int ppt = kPaTile >> plog;   // pages of a tile
+    const uint32_t bytes = (uint32_t)(2 * page * D);
     int slot = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -459,7 +528,7 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
       if (base + 32 <= pg1) fetch(base + 32 + lane, id_next, sc_next);
       for (int i = 0; i < count && ok; ++i) {
         const int pos = (first + i) * kPaTile, pg = pos >> plog;
-        if (pg >= base + 32) {   // 32 is a multiple of the pages of a tile and base of their number: no tile straddles
+        if (pg >= base + 32) {   // 32 and pg0 are multiples of the pages of a tile: no tile straddles
           base += 32;
           id = id_next;
           sc = sc_next;
@@ -470,11 +539,17 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
           break;
         }
         uint8_t* st = smem + slot * Lay::kStage;
-        // the 4 sub-tiles' scales
-        const int mine = lane < 4 ? ((pos + 16 * lane) >> plog) - base : 0;
-        const float kscale = __shfl_sync(0xffffffffu, sc.x, mine & 31), vscale = __shfl_sync(0xffffffffu, sc.y, mine & 31);
-        const int myid = __shfl_sync(0xffffffffu, id, mine & 31);
-        if (lane < 4) {
+        // the copies need the page ids only: they are under way while the
+        // scales, loaded with the ids, arrive
+        const int zid = __shfl_sync(0xffffffffu, id, (pg - base + lane) & 31);
+        const bool have = lane < ppt && pg + lane <= pg1 && zid >= 0;
+        const unsigned mask = __ballot_sync(0xffffffffu, have);
+        if (have)
+          tma_3d(smem_u32(st + lane * bytes), &map, 0, (int)(a.block0 + (long long)zid * a.Hkv + w.kvh), &full[slot]);
+        const int from = (((pos + 16 * (lane & (kPaSub - 1))) >> plog) - base) & 31;   // the page of sub-tile `lane`
+        const float kscale = __shfl_sync(0xffffffffu, sc.x, from), vscale = __shfl_sync(0xffffffffu, sc.y, from);
+        const int myid = __shfl_sync(0xffffffffu, id, from);
+        if (lane < kPaSub) {
           // log2 of the value scale, its power of two apart (a scale of 0, a
           // page never written, counts as the smallest; a missing page as
           // not visible)
@@ -485,30 +560,10 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
             inv = __fdiv_rn(1.0f, vscale);
           }
           if (myid < 0) lv = -INFINITY;
-          s_scale[slot * 4 + lane] = make_float4(kscale, lv, inv, 0.f);
+          s_scale[slot * kPaSub + lane] = make_float4(kscale, lv, inv, 0.f);
         }
         __syncwarp();
-        if (page <= kPaTile) {
-          const int last = min(ppt, ((end - 1 - pos) >> plog) + 1);   // pages of this tile
-          const uint32_t bytes = (uint32_t)(2 * page * D);
-          const int zid = __shfl_sync(0xffffffffu, id, (pg - base + lane) & 31);
-          const bool have = lane < last && zid >= 0;
-          const unsigned mask = __ballot_sync(0xffffffffu, have);
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes * __popc(mask));
-          __syncwarp();
-          if (have)
-            tma_3d(smem_u32(st + lane * bytes), &map, 0, (int)(a.block0 + (long long)zid * a.Hkv + w.kvh), &full[slot]);
-        } else {
-          const int zid = __shfl_sync(0xffffffffu, id, (pg - base) & 31);
-          if (lane == 0) {
-            const int z = (int)(a.block0 + (long long)zid * a.Hkv + w.kvh), y = pos & (page - 1);
-            mbar_arrive_expect_tx(&full[slot], zid >= 0 ? Lay::kStage : 0u);
-            if (zid >= 0) {
-              tma_3d(smem_u32(st), &map, y, z, &full[slot]);
-              tma_3d(smem_u32(st + kPaTile * D), &map, page + y, z, &full[slot]);
-            }
-          }
-        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes * __popc(mask));
         ++issued;
         if (++slot == kPaRing) {
           slot = 0;
@@ -527,45 +582,57 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
     // ---------------------------------------------------------- consumers --
     const int g = lane >> 2, t = lane & 3;
     // where a sub-tile's codes lie in a stage
-    const int pin = 16 * warp;                               // first position in the tile
-    const int koff = page <= kPaTile ? (pin >> plog) * (2 * page * D) + (pin & (page - 1)) * D : pin * D;
-    const int voff = koff + (page <= kPaTile ? page * D : kPaTile * D);
+    int koff[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int p = 32 * warp + 16 * h;   // first position in the tile
+      koff[h] = (p >> plog) * (2 * page * D) + (p & (page - 1)) * D;
+    }
+    const int voff = page * D;
     PaWarp<D, NT> aw;
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
-    while (w.u < w.u1) {
-      const int first = w.t.t0 + (int)(w.u - w.item0);
-      const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);
-      const int valid = min(R, w.n * a.G - w.rt * R);
-      for (int r = warp; r < R; r += kPaCW) load_query<D, NT, kHalf>(a, w, r, valid, reinterpret_cast<__half*>(qf), s_qs);
+    if (tid == 0) s_item.w = w;
+    for (bool more = true; more;) {
+      PaItem& it = s_item;
+      if (tid == 0) {
+        const Walk& c = it.w;
+        it.first = c.t.t0 + (int)(c.u - c.item0);
+        it.count = (int)(min(c.u1, c.item0 + (c.t.t1 - c.t.t0)) - c.u);
+        it.valid = min(R, c.n * a.G - c.rt * R);
+        it.written = c.p0 + c.n;
+        it.hi_min = c.p0 + (c.rt * R) / a.G;
+        it.hi_max = c.p0 + (c.rt * R + it.valid - 1) / a.G;
+        it.back = a.window > 0 ? a.window - 1 : 0x3fffffff;
+        it.lo_min = it.hi_min - it.back;
+        it.lo_max = it.hi_max - it.back;
+      }
+      pa_sync();
+      const int valid = it.valid, count = it.count;
+      if (tid < R) it.hi[tid] = it.w.p0 + (it.w.rt * R + min(tid, valid - 1)) / a.G;
+      load_queries<D, NT, kHalf>(a, it.w, valid, reinterpret_cast<__half*>(qf), s_qs);
       pa_sync();
       aw.init();
-      aw.hi_min = 0x7fffffff;
-      aw.lo_max = 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 8 * nt + 2 * t + e;
-          aw.qs[nt][e] = s_qs[r];
-          const int p = w.p0 + (w.rt * R + min(r, valid - 1)) / a.G;
-          aw.hi[nt][e] = p;
-          aw.lo[nt][e] = a.window > 0 ? p - a.window + 1 : 0;
-        }
-      aw.hi_min = w.p0 + (w.rt * R) / a.G;
-      aw.lo_max = a.window > 0 ? w.p0 + (w.rt * R + valid - 1) / a.G - a.window + 1 : 0;
-      const int written = w.p0 + w.n;
+        for (int e = 0; e < 2; ++e) aw.qs[nt][e] = s_qs[8 * nt + 2 * t + e];
+      int pos0 = it.first * kPaTile + 32 * warp;
       for (int i = 0; i < count; ++i) {
         if (ok && !pa_wait(&full[slot], phase, a.err)) {
           ok = false;
           record_timeout(a.err);
           *s_dead = 1;
         }
-        const int pos0 = (first + i) * kPaTile + pin;
-        if (ok && pos0 < written && s_scale[slot * 4 + warp].y != -INFINITY)
-          aw.sub_tile(smem + slot * Lay::kStage + koff, smem + slot * Lay::kStage + voff, s_scale[slot * 4 + warp], qf,
-                      pos0, written);
+        if (ok && pos0 <= it.hi_max && pos0 + 31 >= it.lo_min) {
+          const uint8_t* st = smem + slot * Lay::kStage;
+          const uint8_t* ks[2] = {st + koff[0], st + koff[1]};
+          const uint8_t* vs[2] = {ks[0] + voff, ks[1] + voff};
+          const float4 sc[2] = {s_scale[slot * kPaSub + 2 * warp], s_scale[slot * kPaSub + 2 * warp + 1]};
+          aw.tile32(ks, vs, sc, qf, it, pos0);
+        }
+        pos0 += kPaTile;
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
         if (++slot == kPaRing) {
@@ -573,8 +640,7 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
           phase ^= 1u;
         }
       }
-      // ---- the four warps' (m, l, O): common maximum, then O added in shared
-      // memory, each warp on its own quarter of the dims per round
+      // ---- the four warps' (m, l, O): common maximum, then O added in shared memory
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -598,41 +664,36 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
           const float M = fmaxf(fmaxf(s_m[r], s_m[R + r]), fmaxf(s_m[2 * R + r], s_m[3 * R + r]));
           f[nt][e] = M == -INFINITY ? 0.f : pa_ex2(aw.m[nt][e] - M);
         }
+      for (int k = 0; k < kPaCW; ++k) {   // warp by warp: a fixed order
+        if (warp == k) {
 #pragma unroll
-      for (int k = 0; k < kPaCW; ++k) {
-        // round k: quarter (warp + k) mod 4 of the D / 16 row tiles
+          for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int qd = 0; qd < kPaCW; ++qd)
-          if (qd == ((warp + k) & 3)) {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int jq = 0; jq < D / 64; ++jq) {
-              const int j = qd * (D / 64) + jq;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float2* p = reinterpret_cast<float2*>(s_o + (8 * nt + 2 * t + e) * Lay::kOLd + 32 * (j >> 1) + 4 * g +
-                                                        2 * (j & 1));
-                  float2 v = make_float2(aw.o[j][nt][e] * f[nt][e], aw.o[j][nt][2 + e] * f[nt][e]);
-                  if (k > 0) {
-                    const float2 c = *p;
-                    v.x += c.x;
-                    v.y += c.y;
-                  }
-                  *p = v;
+              for (int e = 0; e < 2; ++e) {
+                float2* p = reinterpret_cast<float2*>(s_o + (8 * nt + 2 * t + e) * Lay::kOLd + 64 * (j >> 2) + 8 * g +
+                                                      2 * (j & 3));
+                float2 v = make_float2(aw.o[j][nt][e] * f[nt][e], aw.o[j][nt][2 + e] * f[nt][e]);
+                if (k > 0) {
+                  const float2 c = *p;
+                  v.x += c.x;
+                  v.y += c.y;
                 }
-            }
-          }
+                *p = v;
+              }
+        }
         pa_sync();
       }
       // ---- a whole item: the rows; a part of one: a record, and the CTA that
       // arrives last adds the records in CTA order
-      const long long item1 = w.item0 + (w.t.t1 - w.t.t0);
-      const bool whole = w.u == w.item0 && w.u + count == item1;
+      const Walk& c = it.w;
+      const long long item1 = c.item0 + (c.t.t1 - c.t.t0);
+      const bool whole = c.u == c.item0 && c.u + count == item1;
       const int dead = *s_snap;
       bool write = whole && !dead;
       if (!whole && !dead) {
-        float* rec = a.rec + ((size_t)cta * 2 + (w.item0 < w.u ? 0 : 1)) * (R * (D + 2));
+        float* rec = a.rec + ((size_t)cta * 2 + (c.item0 < c.u ? 0 : 1)) * (R * (D + 2));
         for (int r = tid; r < valid; r += kPaCW * 32) {
           const float M = fmaxf(fmaxf(s_m[r], s_m[R + r]), fmaxf(s_m[2 * R + r], s_m[3 * R + r]));
           float L = 0.f;
@@ -643,12 +704,12 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
           rec[R + r] = L;
         }
         for (int e = tid; e < valid * (D / 4); e += kPaCW * 32) {
-          const int r = e / (D / 4), c = e - r * (D / 4);
-          reinterpret_cast<float4*>(rec + 2 * R)[e] = *reinterpret_cast<const float4*>(s_o + r * Lay::kOLd + 4 * c);
+          const int r = e / (D / 4), q = e - r * (D / 4);
+          reinterpret_cast<float4*>(rec + 2 * R)[e] = *reinterpret_cast<const float4*>(s_o + r * Lay::kOLd + 4 * q);
         }
         pa_sync();
         // the CTAs of this item: those whose shares hold its first and last unit
-        const int c0 = (int)(((w.item0 + 1) * ctas - 1) / total), c1 = (int)((item1 * ctas - 1) / total);
+        const int c0 = (int)(((c.item0 + 1) * ctas - 1) / total), c1 = (int)((item1 * ctas - 1) / total);
         if (tid == 0) {
           const unsigned arrived = atom_add_acq_rel_gpu(&a.cnt[c0], 1u);
           *s_last = arrived == (unsigned)(c1 - c0) ? 1 : 0;
@@ -657,55 +718,48 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
         pa_sync();
         if (*s_last) {
           write = true;
-          // maximum and normalizer of each row into s_m, s_l of warp 0
+          // one pass over the records with a running maximum: thread = 4 dims of a row
           const size_t step = (size_t)2 * R * (D + 2);
           const float* r0 = a.rec + ((size_t)c0 * 2 + 1) * (R * (D + 2));   // CTA c0's second slot
           const float* rn = a.rec + (size_t)(c0 + 1) * step;                 // the others' first
           const int nc = c1 - c0;                                            // others
-          for (int r = warp; r < valid; r += kPaCW) {
-            float M = lane == 0 ? __ldcg(r0 + r) : -INFINITY;
-            for (int k = lane; k < nc; k += 32) M = fmaxf(M, __ldcg(rn + k * step + r));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            float L = 0.f;
-            if (M != -INFINITY) {
-              if (lane == 0) L = __ldcg(r0 + R + r) * pa_ex2(__ldcg(r0 + r) - M);
-              for (int k = lane; k < nc; k += 32) L += __ldcg(rn + k * step + R + r) * pa_ex2(__ldcg(rn + k * step + r) - M);
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            }
-            if (lane == 0) {
-              s_m[r] = M;
-              s_l[r] = L;
-            }
-          }
-          pa_sync();
           for (int e = tid; e < valid * (D / 4); e += kPaCW * 32) {
-            const int r = e / (D / 4), c = e - r * (D / 4);
-            const float M = s_m[r] == -INFINITY ? 0.f : s_m[r];
+            const int r = e / (D / 4), q = e - r * (D / 4);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int kU = 8;   // records in flight
+            float M = -INFINITY, L = 0.f;
+            constexpr int kU = 4;   // records in flight
             for (int k = -1; k < nc; k += kU) {
               float4 v[kU];
-              float mm[kU];
+              float mm[kU], ll[kU], mx = M;
 #pragma unroll
-              for (int i = 0; i < kU; ++i)
+              for (int i = 0; i < kU; ++i) {
+                mm[i] = -INFINITY;
                 if (k + i < nc) {
                   const float* src = k + i < 0 ? r0 : rn + (size_t)(k + i) * step;
                   mm[i] = __ldcg(src + r);
+                  ll[i] = __ldcg(src + R + r);
                   v[i] = __ldcg(reinterpret_cast<const float4*>(src + 2 * R) + e);
                 }
+              }
+#pragma unroll
+              for (int i = 0; i < kU; ++i) mx = fmaxf(mx, mm[i]);
+              const float ref = mx == -INFINITY ? 0.f : mx, f = pa_ex2(M - ref);
+              acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+              L *= f;
+              M = mx;
 #pragma unroll
               for (int i = 0; i < kU; ++i)
                 if (k + i < nc) {
-                  const float wt = pa_ex2(mm[i] - M);
+                  const float wt = pa_ex2(mm[i] - ref);
                   acc.x = fmaf(v[i].x, wt, acc.x);
                   acc.y = fmaf(v[i].y, wt, acc.y);
                   acc.z = fmaf(v[i].z, wt, acc.z);
                   acc.w = fmaf(v[i].w, wt, acc.w);
+                  L = fmaf(ll[i], wt, L);
                 }
             }
-            *reinterpret_cast<float4*>(s_o + r * Lay::kOLd + 4 * c) = acc;
+            *reinterpret_cast<float4*>(s_o + r * Lay::kOLd + 4 * q) = acc;
+            if (q == 0) s_l[r] = L;
           }
           pa_sync();
         }
@@ -722,24 +776,27 @@ __global__ void __launch_bounds__(kPaThreads, NT <= 2 ? 3 : 2)
       }
       if (write) {
         for (int e = tid; e < valid * (D / 8); e += kPaCW * 32) {
-          const int r = e / (D / 8), c = e - r * (D / 8);
-          const int row = w.rt * R + r, i = row / a.G, head = w.kvh * a.G + row - i * a.G;
+          const int r = e / (D / 8), q = e - r * (D / 8);
+          const int row = c.rt * R + r, i = row / a.G, head = c.kvh * a.G + row - i * a.G;
           const float L = s_l[r], inv = L != 0.f ? __fdiv_rn(1.0f, L) : 0.f;   // a row that sees nothing: zeros
-          const float4* p = reinterpret_cast<const float4*>(s_o + r * Lay::kOLd + 8 * c);
+          const float4* p = reinterpret_cast<const float4*>(s_o + r * Lay::kOLd + 8 * q);
           const float4 v0 = p[0], v1 = p[1];
           uint4 u;
           u.x = narrow2<kHalf>(v0.x * inv, v0.y * inv);
           u.y = narrow2<kHalf>(v0.z * inv, v0.w * inv);
           u.z = narrow2<kHalf>(v1.x * inv, v1.y * inv);
           u.w = narrow2<kHalf>(v1.z * inv, v1.w * inv);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (size_t)(w.row0 + i) * a.ld_out + (size_t)head * D +
-                                    8 * c) = u;
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (size_t)(c.row0 + i) * a.ld_out + (size_t)head * D +
+                                    8 * q) = u;
         }
       }
-      w.u += count;
-      if (w.u < w.u1) {
-        w.next_item(a, R);
-        pa_sync();   // s_o, s_m, s_l and the query fragments are free again
+      more = c.u + count < c.u1;
+      if (more) {
+        pa_sync();   // s_o, s_m, s_l, the query fragments and the item are free again
+        if (tid == 0) {
+          it.w.u += count;
+          it.w.next_item(a, R);
+        }
       }
     }
   }
@@ -812,17 +869,15 @@ cudaError_t pa_launch(const PagedAttnArgs& a, const CUtensorMap& map, cudaStream
 
 template <int D, bool kHalf>
 cudaError_t pa_launch_nt(const PagedAttnArgs& a, const CUtensorMap& map, cudaStream_t st) {
-  // rows of a tile: one new token's group where every sequence has one row,
-  // else 32 rows (several tokens of a group, or a chunk's tiles)
-  const int rows = a.r.start == nullptr || a.r.n_rows <= a.r.batch ? a.G : 32;
+  // rows of a tile: those that a sequence has on average (the counts are on the device)
+  const int rows = (a.r.n_rows + a.r.batch - 1) / a.r.batch * a.G;
   if (rows <= 8) return pa_launch<D, 1, kHalf>(a, map, st);
-  if (rows <= 16) return pa_launch<D, 2, kHalf>(a, map, st);
-  return pa_launch<D, 4, kHalf>(a, map, st);
+  return pa_launch<D, 2, kHalf>(a, map, st);
 }
 
 }  // namespace
 
-constexpr int kPaMaxRows = 32;
+constexpr int kPaMaxRows = 16;
 
 size_t paged_rec_floats(int d) { return (size_t)2 * kPaMaxRows * (d + 2); }
 
@@ -839,9 +894,8 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, const CUtensorMap& ma
   return half ? pa_launch_nt<64, true>(a, map, st) : pa_launch_nt<64, false>(a, map, st);
 }
 
-// Codes as [blocks][2 page][d] bytes, a block per (page, kv-head); boxes of
-// a whole block up to pages of 64, else of 64 rows; rows of 128 (64) bytes
-// with the 128-byte (64-byte) swizzle.
+// Codes as [blocks][2 page][d] bytes, a block per (page, kv-head), copied whole;
+// rows of 128 (64) bytes with the 128-byte (64-byte) swizzle.
 bool make_paged_map(CUtensorMap* m, const void* codes, int d, int page, uint64_t blocks) {
   static std::atomic<void*> entry{nullptr};
   void* p = entry.load(std::memory_order_acquire);
@@ -857,7 +911,7 @@ bool make_paged_map(CUtensorMap* m, const void* codes, int d, int page, uint64_t
                           CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)(2 * page), blocks};
   const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)(2 * page) * d};
-  const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)(page <= kPaTile ? 2 * page : kPaTile), 1};
+  const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)(2 * page), 1};
   const cuuint32_t elem[3] = {1, 1, 1};
   return reinterpret_cast<Fn>(p)(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box,
                                  elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
