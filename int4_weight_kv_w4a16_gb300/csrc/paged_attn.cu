@@ -44,14 +44,14 @@ constexpr unsigned long long kPaWaitNs = 1000000000ull;
 template <int D, int NT>
 struct PaLayout {
   static constexpr int R = 8 * NT;
-  static constexpr int kRing = D == 128 ? 2 : 4;                // 64 KB: three CTAs share an SM's memory
+  static constexpr int kRing = D == 128 ? 2 : 4;                // 64 KB of tiles: two CTAs share an SM's memory
   static constexpr int kStage = 2 * kPaTile * D;                // K and V codes
   static constexpr int kScale = kRing * kStage;                 // [ring][sub-tiles] float4 (ks, lv, 1/vs, -)
   static constexpr int kQ = kScale + kRing * kPaSub * 16;       // query fragments [D/16][NT][32] uint2
   static constexpr int kQs = kQ + (D / 16) * NT * 32 * 8;       // [R] score factors
   static constexpr int kOLd = D + 4;
-  static constexpr int kO = kQs + R * 4;                        // [R][kOLd] fp32
-  static constexpr int kM = kO + R * kOLd * 4;                  // [4 warps][R]
+  static constexpr int kO = kQs + R * 4;                        // [4 warps][R][kOLd] fp32
+  static constexpr int kM = kO + kPaCW * R * kOLd * 4;          // [4 warps][R]
   static constexpr int kL = kM + kPaCW * R * 4;                 // [4 warps][R]
   static constexpr int kBar = kL + kPaCW * R * 4;
   static constexpr int kBytes = kBar + 2 * kRing * 8 + 32;
@@ -94,8 +94,12 @@ struct TileRange {
   int t0, t1;
 };
 __device__ __forceinline__ TileRange row_tile(int n, int p0, int G, int R, int window, int rt) {
-  const int rows = n * G, r0 = rt * R, r1 = min(rows, r0 + R) - 1;
-  const int first = p0 + r0 / G, last = p0 + r1 / G;
+  int first = p0, last = p0;
+  if (n > 1) {
+    const int r0 = rt * R, r1 = min(n * G, r0 + R) - 1;
+    first = p0 + r0 / G;
+    last = p0 + r1 / G;
+  }
   const int lo = window > 0 ? max(0, first - window + 1) : 0;
   return {lo / kPaTile, last / kPaTile + 1};
 }
@@ -103,6 +107,7 @@ __device__ __forceinline__ TileRange row_tile(int n, int p0, int G, int R, int w
 __device__ __forceinline__ long long seq_tiles(int n, int p0, int G, int R, int window) {
   long long w = 0;
   const int nrt = (n * G + R - 1) / R;
+#pragma unroll 1
   for (int rt = 0; rt < nrt; ++rt) {
     const TileRange t = row_tile(n, p0, G, R, window, rt);
     w += t.t1 - t.t0;
@@ -110,9 +115,37 @@ __device__ __forceinline__ long long seq_tiles(int n, int p0, int G, int R, int 
   return w;
 }
 
+// a / b for a >= 0, b > 0, on the path to the first copy: unit counts are small
+// numbers in all but the longest calls, and there one fp32 division, off by one
+// at most, with its remainder checked costs a fraction of an integer division.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  if (((a | b) >> 21) != 0) return a / b;
+  int q = (int)__fdividef((float)(int)a, (float)(int)b);
+  const int r = (int)a - q * (int)b;
+  if (r < 0) --q;
+  if (r >= (int)b) ++q;
+  return q;
+}
+
+// `total` units cut into `use` shares: the first `rem` of per + 1, the others of per.
+struct Cut {
+  long long total, per;
+  int use, rem;
+  __device__ __forceinline__ void set(long long units, int ctas) {
+    total = units;
+    use = (int)(units < ctas ? units : ctas);
+    per = units <= ctas ? 1 : quot(units, ctas);
+    rem = (int)(units - per * use);
+  }
+  __device__ __forceinline__ long long begin(int cta) const { return per * cta + min(cta, rem); }
+  __device__ __forceinline__ int owner(long long u) const {
+    const long long big = (per + 1) * rem;
+    return (int)(u < big ? quot(u, per + 1) : rem + (per == 1 ? u - big : quot(u - big, per)));
+  }
+};
+
 // The position of a CTA in the call's work: sequence b, kv-head, row tile and
-// the next tile.  Every warp keeps its own copy and steps it the
-// same way.
+// the next tile.  The producer warp keeps one copy, the consumers another.
 struct Walk {
   int b, kvh, rt, row0, n, p0;
   long long per_head;      // tiles of one kv-head of sequence b
@@ -122,10 +155,11 @@ struct Walk {
 
   // Enter sequence b (rows known); the item that holds unit `at` of its units.
   __device__ __forceinline__ void enter(const PagedAttnArgs& a, int R, long long at, long long base) {
-    kvh = (int)(at / per_head);
+    kvh = (int)quot(at, per_head);
     long long rem = at - (long long)kvh * per_head;
     rt = 0;
     t = row_tile(n, p0, a.G, R, a.window, 0);
+#pragma unroll 1
     while (rem >= t.t1 - t.t0) {
       rem -= t.t1 - t.t0;
       ++rt;
@@ -153,10 +187,10 @@ struct Walk {
   }
 };
 
-// Units of the whole call and the share of CTA `cta` of `ctas` (a full warp).
-// Returns the number of CTAs that get a share.
-__device__ __forceinline__ int find_share(const PagedAttnArgs& a, int R, int cta, int ctas, Walk& w, long long& total,
-                                          bool report) {
+// The call's units, their cut, and the share of CTA `cta` (a full warp).  False:
+// it has none.
+__device__ __forceinline__ bool find_share(const PagedAttnArgs& a, int R, int cta, int ctas, Walk& w, Cut& cut,
+                                           bool report) {
   const int lane = threadIdx.x & 31;
   int row0 = 0, n = 0, p0 = 0;   // of sequence b0 + lane
   long long per = 0, incl = 0;   // its tiles per kv-head; all tiles of this round's sequences up to it
@@ -168,25 +202,28 @@ __device__ __forceinline__ int find_share(const PagedAttnArgs& a, int R, int cta
       per = seq_tiles(n, p0, a.G, R, a.window);
     }
     incl = per * a.Hkv;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll 1
+    for (int o = 1; o < 32 && o < a.r.batch; o <<= 1) {
       const long long t = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += t;
     }
   };
-  total = 0;
+  const int top = min(31, a.r.batch - 1);   // a lane whose prefix sum is complete
+  long long total = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.r.batch; b0 += 32) {
     look(b0);
-    total += __shfl_sync(0xffffffffu, incl, 31);
+    total += __shfl_sync(0xffffffffu, incl, top);
   }
-  const int use = (int)(total < ctas ? total : ctas);
-  if (cta >= use) return use;
-  w.u = total * cta / use;
-  w.u1 = total * (cta + 1) / use;
+  cut.set(total, ctas);
+  if (cta >= cut.use) return false;
+  w.u = cut.begin(cta);
+  w.u1 = cut.begin(cta + 1);
   long long before = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.r.batch; b0 += 32) {
     if (a.r.batch > 32) look(b0);   // up to 32 sequences: still at hand
-    const unsigned hit = __ballot_sync(0xffffffffu, before + incl > w.u);
+    const unsigned hit = __ballot_sync(0xffffffffu, lane <= top && before + incl > w.u);
     if (hit) {
       const int src = __ffs(hit) - 1;
       w.b = b0 + src;
@@ -196,11 +233,11 @@ __device__ __forceinline__ int find_share(const PagedAttnArgs& a, int R, int cta
       w.per_head = __shfl_sync(0xffffffffu, per, src);
       const long long base = before + __shfl_sync(0xffffffffu, incl - per * a.Hkv, src);
       w.enter(a, R, w.u - base, base);
-      return use;
+      return true;
     }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+    before += __shfl_sync(0xffffffffu, incl, top);
   }
-  return 0;   // not reached: u < total
+  return false;   // not reached: u < total
 }
 
 // ---------------------------------------------------------------- consumer --
@@ -209,6 +246,8 @@ __device__ __forceinline__ int find_share(const PagedAttnArgs& a, int R, int cta
 // are needed instead of being held in registers through the tile loop.
 struct PaItem {
   Walk w;
+  Cut cut;
+  int active;                    // this CTA has a share
   int first, count, valid;       // tiles of this CTA's part, rows of the tile
   int written;                   // positions below it exist
   int hi_min, lo_max;            // positions [lo_max, hi_min] are visible to every row
@@ -458,8 +497,56 @@ __device__ __forceinline__ void load_queries(const PagedAttnArgs& a, const Walk&
   }
 }
 
+// The records r0 and rn[0 .. nc - 1] (m [R], l [R], O [R][D] each) added into
+// s_o and s_l in this order, in one pass with a running maximum: a thread takes
+// 4 dims of a row, eight records in flight.
+template <int D, int R>
+__device__ __forceinline__ void sum_records(const float* r0, const float* rn, int nc, int valid, float* s_o, int ld,
+                                         float* s_l) {
+  constexpr size_t step = (size_t)2 * R * (D + 2);
+  for (int e = threadIdx.x; e < valid * (D / 4); e += kPaCW * 32) {
+    const int r = e / (D / 4), q = e - r * (D / 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, L = 0.f;
+    constexpr int kU = 8;
+#pragma unroll 1
+    for (int k = -1; k < nc; k += kU) {
+      float4 v[kU];
+      float mm[kU], ll[kU], mx = M;
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        mm[i] = -INFINITY;
+        if (k + i < nc) {
+          const float* src = k + i < 0 ? r0 : rn + (size_t)(k + i) * step;
+          mm[i] = __ldcg(src + r);
+          ll[i] = __ldcg(src + R + r);
+          v[i] = __ldcg(reinterpret_cast<const float4*>(src + 2 * R) + e);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kU; ++i) mx = fmaxf(mx, mm[i]);
+      const float ref = mx == -INFINITY ? 0.f : mx, f = pa_ex2(M - ref);
+      acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+      L *= f;
+      M = mx;
+#pragma unroll
+      for (int i = 0; i < kU; ++i)
+        if (k + i < nc) {
+          const float wt = pa_ex2(mm[i] - ref);
+          acc.x = fmaf(v[i].x, wt, acc.x);
+          acc.y = fmaf(v[i].y, wt, acc.y);
+          acc.z = fmaf(v[i].z, wt, acc.z);
+          acc.w = fmaf(v[i].w, wt, acc.w);
+          L = fmaf(ll[i], wt, L);
+        }
+    }
+    *reinterpret_cast<float4*>(s_o + r * ld + 4 * q) = acc;
+    if (q == 0) s_l[r] = L;
+  }
+}
+
 template <int D, int NT, bool kHalf>
-__global__ void __launch_bounds__(kPaThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kPaThreads, 2)
     paged_attn_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap map) {
   using Lay = PaLayout<D, NT>;
   constexpr int R = Lay::R, kPaRing = Lay::kRing;
@@ -478,6 +565,7 @@ __global__ void __launch_bounds__(kPaThreads, NT == 1 ? 3 : 2)
   volatile int* s_last = s_dead + 2;
   volatile int* s_snap = s_dead + 3;                                          // s_dead as the consumers saw it together
   __shared__ PaItem s_item;
+  __shared__ float s_tot[2 * R];   // a part's (or the whole item's) maxima and normalizers
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kPaRing; ++i) {
@@ -491,15 +579,14 @@ __global__ void __launch_bounds__(kPaThreads, NT == 1 ? 3 : 2)
   __syncthreads();
   pdl_trigger();
   pdl_wait();
-  Walk w;
-  long long total;
   const int cta = blockIdx.x;
-  const int ctas = find_share(a, R, cta, gridDim.x, w, total, cta == 0 && warp == 0);
-  if (cta >= ctas) return;
   const int page = a.c.page, plog = a.c.page_log2;
 
   if (warp == kPaCW) {
     // ---------------------------------------------------------- producer --
+    Walk w;
+    Cut cut;
+    if (!find_share(a, R, cta, gridDim.x, w, cut, false)) return;
     // copies of a tile: whole (page, kv-head) blocks, keys then values
     const int ppt = kPaTile >> plog;   // pages of a tile
     const uint32_t bytes = (uint32_t)(2 * page * D);
@@ -593,9 +680,20 @@ __global__ void __launch_bounds__(kPaThreads, NT == 1 ? 3 : 2)
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
-    if (tid == 0) s_item.w = w;
+    PaItem& it = s_item;
+    if (warp == 0) {
+      Walk w;
+      Cut cut;
+      const bool active = find_share(a, R, cta, gridDim.x, w, cut, cta == 0);
+      if (lane == 0) {
+        it.w = w;
+        it.cut = cut;
+        it.active = active;
+      }
+    }
+    pa_sync();
+    if (!it.active) return;
     for (bool more = true; more;) {
-      PaItem& it = s_item;
       if (tid == 0) {
         const Walk& c = it.w;
         it.first = c.t.t0 + (int)(c.u - c.item0);
@@ -640,7 +738,7 @@ __global__ void __launch_bounds__(kPaThreads, NT == 1 ? 3 : 2)
           phase ^= 1u;
         }
       }
-      // ---- the four warps' (m, l, O): common maximum, then O added in shared memory
+      // ---- the four warps' (m, l, O) to shared memory, each at its own maximum
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -648,43 +746,45 @@ __global__ void __launch_bounds__(kPaThreads, NT == 1 ? 3 : 2)
           float v = aw.l[nt][e];
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) v += __shfl_xor_sync(0xffffffffu, v, sh);
+          const int r = 8 * nt + 2 * t + e;
           if (g == 0) {
-            s_m[warp * R + 8 * nt + 2 * t + e] = aw.m[nt][e];
-            s_l[warp * R + 8 * nt + 2 * t + e] = v;
+            s_m[warp * R + r] = aw.m[nt][e];
+            s_l[warp * R + r] = v;
+          }
+          if (r < valid) {
+            float2* p = reinterpret_cast<float2*>(s_o + (warp * R + r) * Lay::kOLd + 8 * g);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+              p[32 * (j >> 2) + (j & 3)] = make_float2(aw.o[j][nt][e], aw.o[j][nt][2 + e]);
           }
         }
       if (tid == 0) *s_snap = *s_dead;   // one value for every branch below
       pa_sync();
-      float f[NT][2];
+      // the sums over the four warps, in warp order: a thread takes 4 dims of a
+      // row; they stay where warp 0's were
+      for (int e = tid; e < valid * (D / 4); e += kPaCW * 32) {
+        const int r = e / (D / 4), q = e - r * (D / 4);
+        const float M = fmaxf(fmaxf(s_m[r], s_m[R + r]), fmaxf(s_m[2 * R + r], s_m[3 * R + r]));
+        const float ref = M == -INFINITY ? 0.f : M;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 8 * nt + 2 * t + e;
-          const float M = fmaxf(fmaxf(s_m[r], s_m[R + r]), fmaxf(s_m[2 * R + r], s_m[3 * R + r]));
-          f[nt][e] = M == -INFINITY ? 0.f : pa_ex2(aw.m[nt][e] - M);
+        for (int k = 0; k < kPaCW; ++k) {
+          const float f = pa_ex2(s_m[k * R + r] - ref);
+          const float4 v = *reinterpret_cast<const float4*>(s_o + (k * R + r) * Lay::kOLd + 4 * q);
+          L = fmaf(s_l[k * R + r], f, L);
+          acc.x = fmaf(v.x, f, acc.x);
+          acc.y = fmaf(v.y, f, acc.y);
+          acc.z = fmaf(v.z, f, acc.z);
+          acc.w = fmaf(v.w, f, acc.w);
         }
-      for (int k = 0; k < kPaCW; ++k) {   // warp by warp: a fixed order
-        if (warp == k) {
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float2* p = reinterpret_cast<float2*>(s_o + (8 * nt + 2 * t + e) * Lay::kOLd + 64 * (j >> 2) + 8 * g +
-                                                      2 * (j & 3));
-                float2 v = make_float2(aw.o[j][nt][e] * f[nt][e], aw.o[j][nt][2 + e] * f[nt][e]);
-                if (k > 0) {
-                  const float2 c = *p;
-                  v.x += c.x;
-                  v.y += c.y;
-                }
-                *p = v;
-              }
+        *reinterpret_cast<float4*>(s_o + r * Lay::kOLd + 4 * q) = acc;
+        if (q == 0) {
+          s_tot[r] = M;
+          s_tot[R + r] = L;
         }
-        pa_sync();
       }
+      pa_sync();
       // ---- a whole item: the rows; a part of one: a record, and the CTA that
       // arrives last adds the records in CTA order
       const Walk& c = it.w;
@@ -694,22 +794,14 @@ __global__ void __launch_bounds__(kPaThreads, NT == 1 ? 3 : 2)
       bool write = whole && !dead;
       if (!whole && !dead) {
         float* rec = a.rec + ((size_t)cta * 2 + (c.item0 < c.u ? 0 : 1)) * (R * (D + 2));
-        for (int r = tid; r < valid; r += kPaCW * 32) {
-          const float M = fmaxf(fmaxf(s_m[r], s_m[R + r]), fmaxf(s_m[2 * R + r], s_m[3 * R + r]));
-          float L = 0.f;
-#pragma unroll
-          for (int k = 0; k < kPaCW; ++k)
-            L += s_m[k * R + r] == -INFINITY ? 0.f : s_l[k * R + r] * pa_ex2(s_m[k * R + r] - M);
-          rec[r] = M;
-          rec[R + r] = L;
-        }
+        for (int r = tid; r < 2 * R; r += kPaCW * 32) rec[r] = s_tot[r];
         for (int e = tid; e < valid * (D / 4); e += kPaCW * 32) {
           const int r = e / (D / 4), q = e - r * (D / 4);
           reinterpret_cast<float4*>(rec + 2 * R)[e] = *reinterpret_cast<const float4*>(s_o + r * Lay::kOLd + 4 * q);
         }
         pa_sync();
         // the CTAs of this item: those whose shares hold its first and last unit
-        const int c0 = (int)(((c.item0 + 1) * ctas - 1) / total), c1 = (int)((item1 * ctas - 1) / total);
+        const int c0 = it.cut.owner(c.item0), c1 = it.cut.owner(item1 - 1);
         if (tid == 0) {
           const unsigned arrived = atom_add_acq_rel_gpu(&a.cnt[c0], 1u);
           *s_last = arrived == (unsigned)(c1 - c0) ? 1 : 0;
@@ -718,67 +810,17 @@ __global__ void __launch_bounds__(kPaThreads, NT == 1 ? 3 : 2)
         pa_sync();
         if (*s_last) {
           write = true;
-          // one pass over the records with a running maximum: thread = 4 dims of a row
-          const size_t step = (size_t)2 * R * (D + 2);
-          const float* r0 = a.rec + ((size_t)c0 * 2 + 1) * (R * (D + 2));   // CTA c0's second slot
-          const float* rn = a.rec + (size_t)(c0 + 1) * step;                 // the others' first
-          const int nc = c1 - c0;                                            // others
-          for (int e = tid; e < valid * (D / 4); e += kPaCW * 32) {
-            const int r = e / (D / 4), q = e - r * (D / 4);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float M = -INFINITY, L = 0.f;
-            constexpr int kU = 4;   // records in flight
-            for (int k = -1; k < nc; k += kU) {
-              float4 v[kU];
-              float mm[kU], ll[kU], mx = M;
-#pragma unroll
-              for (int i = 0; i < kU; ++i) {
-                mm[i] = -INFINITY;
-                if (k + i < nc) {
-                  const float* src = k + i < 0 ? r0 : rn + (size_t)(k + i) * step;
-                  mm[i] = __ldcg(src + r);
-                  ll[i] = __ldcg(src + R + r);
-                  v[i] = __ldcg(reinterpret_cast<const float4*>(src + 2 * R) + e);
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < kU; ++i) mx = fmaxf(mx, mm[i]);
-              const float ref = mx == -INFINITY ? 0.f : mx, f = pa_ex2(M - ref);
-              acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-              L *= f;
-              M = mx;
-#pragma unroll
-              for (int i = 0; i < kU; ++i)
-                if (k + i < nc) {
-                  const float wt = pa_ex2(mm[i] - ref);
-                  acc.x = fmaf(v[i].x, wt, acc.x);
-                  acc.y = fmaf(v[i].y, wt, acc.y);
-                  acc.z = fmaf(v[i].z, wt, acc.z);
-                  acc.w = fmaf(v[i].w, wt, acc.w);
-                  L = fmaf(ll[i], wt, L);
-                }
-            }
-            *reinterpret_cast<float4*>(s_o + r * Lay::kOLd + 4 * q) = acc;
-            if (q == 0) s_l[r] = L;
-          }
+          // CTA c0's second slot, then the others' first
+          sum_records<D, R>(a.rec + ((size_t)c0 * 2 + 1) * (R * (D + 2)), a.rec + (size_t)(c0 + 1) * 2 * (R * (D + 2)),
+                            c1 - c0, valid, s_o, Lay::kOLd, s_tot + R);
           pa_sync();
         }
-      } else if (write) {
-        for (int r = tid; r < valid; r += kPaCW * 32) {
-          const float M = fmaxf(fmaxf(s_m[r], s_m[R + r]), fmaxf(s_m[2 * R + r], s_m[3 * R + r]));
-          float L = 0.f;
-#pragma unroll
-          for (int k = 0; k < kPaCW; ++k)
-            L += s_m[k * R + r] == -INFINITY ? 0.f : s_l[k * R + r] * pa_ex2(s_m[k * R + r] - M);
-          s_l[r] = L;   // this thread alone reads and writes row r of warp 0's sums
-        }
-        pa_sync();
       }
       if (write) {
         for (int e = tid; e < valid * (D / 8); e += kPaCW * 32) {
           const int r = e / (D / 8), q = e - r * (D / 8);
           const int row = c.rt * R + r, i = row / a.G, head = c.kvh * a.G + row - i * a.G;
-          const float L = s_l[r], inv = L != 0.f ? __fdiv_rn(1.0f, L) : 0.f;   // a row that sees nothing: zeros
+          const float L = s_tot[R + r], inv = L != 0.f ? __fdiv_rn(1.0f, L) : 0.f;   // a row that sees nothing: zeros
           const float4* p = reinterpret_cast<const float4*>(s_o + r * Lay::kOLd + 8 * q);
           const float4 v0 = p[0], v1 = p[1];
           uint4 u;
@@ -792,7 +834,7 @@ __global__ void __launch_bounds__(kPaThreads, NT == 1 ? 3 : 2)
       }
       more = c.u + count < c.u1;
       if (more) {
-        pa_sync();   // s_o, s_m, s_l, the query fragments and the item are free again
+        pa_sync();   // the sums, the query fragments and the item are free again
         if (tid == 0) {
           it.w.u += count;
           it.w.next_item(a, R);
@@ -823,7 +865,7 @@ cudaError_t pa_configure(int dev) {
   return cudaSuccess;
 }
 
-constexpr int kPaMaxPerSm = 3;   // CTAs an SM that any variant is launched with at most
+constexpr int kPaMaxPerSm = 2;   // CTAs an SM that any variant is launched with at most
 
 template <int D, int NT, bool kHalf>
 int pa_per_sm(int dev) {
