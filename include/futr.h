@@ -394,6 +394,7 @@ typedef struct futr_paged {
   void* base;
   uint64_t bytes;
   uint64_t scale_offset, rope_offset, err_offset;
+  uint64_t copy_map[16];   /* how the copies find a page (filled by futr_paged_init) */
   uint64_t magic;
 } futr_paged;
 
@@ -477,6 +478,7 @@ typedef struct futr_moe_ws {
   void* base;
   uint64_t bytes;
   uint64_t off_cnt, off_route, off_logits, off_act, off_rec;
+  uint64_t blob_bytes;     /* size of the layer's packed experts */
   uint64_t magic;
 } futr_moe_ws;
 

@@ -66,6 +66,7 @@ void ws_layout(const futr_moe_shape& s, int max_batch, int ctas, futr_moe_ws* w)
   off = host::region_after(off, (uint64_t)max_batch * s.top_k * s.inter * 2);
   w->off_rec = off;
   w->bytes = host::region_after(off, (uint64_t)ctas * 2 * kMoeRecFloats * 4);
+  w->blob_bytes = kHeaderBytes + expert_bytes(s) * s.n_experts;
   w->magic = kMoeWsMagic;
 }
 

@@ -1,6 +1,7 @@
 // Entry points of the paged 8-bit cache (declared in include/futr.h): argument
 // checks, memory layouts, launches.
 #include <cmath>
+#include <cstring>
 
 #include "paged.cuh"
 
@@ -134,6 +135,10 @@ futr_status futr_paged_init(const futr_shape* shape, int32_t n_layers, int32_t n
     d.rope_offset = L.rope;
     d.err_offset = L.err;
     d.magic = kPagedMagic;
+    CUtensorMap map;
+    static_assert(sizeof(map) == sizeof(d.copy_map), "a tensor map fills the descriptor's field");
+    if (!make_paged_map(&map, mem, shape->head_dim, page, L.blocks)) return FUTR_ERR_CUDA;
+    std::memcpy(d.copy_map, &map, sizeof(map));
     uint64_t g[4];
     cache_guards(d, g);
     if (host::fill_guards_before(mem, g, 4, s) != cudaSuccess) return FUTR_ERR_CUDA;
@@ -227,9 +232,7 @@ futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t
     a.cnt = at<unsigned>(ws->base, 0);
     a.err = at<int>(cache->base, cache->err_offset);
     CUtensorMap map;
-    if (!make_paged_map(&map, cache->base, s.head_dim, cache->page,
-                        (uint64_t)cache->n_layers * cache->n_pages * s.n_kv_heads))
-      return FUTR_ERR_CUDA;
+    std::memcpy(&map, cache->copy_map, sizeof(map));
     return launch_paged_attention(a, map, s.head_dim, dtype, as_stream(stream)) == cudaSuccess ? FUTR_OK
                                                                                                : FUTR_ERR_CUDA;
   });

@@ -60,7 +60,7 @@ class futr_paged(C.Structure):
     _fields_ = [("shape", futr_shape), ("n_layers", C.c_int32), ("n_pages", C.c_int32), ("page", C.c_int32),
                 ("max_pos", C.c_int32), ("rope", C.c_int32), ("base", C.c_void_p), ("bytes", C.c_uint64),
                 ("scale_offset", C.c_uint64), ("rope_offset", C.c_uint64), ("err_offset", C.c_uint64),
-                ("magic", C.c_uint64)]
+                ("copy_map", C.c_uint64 * 16), ("magic", C.c_uint64)]
 
 
 class futr_paged_ws(C.Structure):
@@ -76,7 +76,8 @@ class futr_moe_shape(C.Structure):
 class futr_moe_ws(C.Structure):
     _fields_ = [("shape", futr_moe_shape), ("max_batch", C.c_int32), ("ctas", C.c_int32), ("_pad", C.c_int32),
                 ("base", C.c_void_p), ("bytes", C.c_uint64), ("off_cnt", C.c_uint64), ("off_route", C.c_uint64),
-                ("off_logits", C.c_uint64), ("off_act", C.c_uint64), ("off_rec", C.c_uint64), ("magic", C.c_uint64)]
+                ("off_logits", C.c_uint64), ("off_act", C.c_uint64), ("off_rec", C.c_uint64), ("blob_bytes", C.c_uint64),
+                ("magic", C.c_uint64)]
 
 
 class FutrError(RuntimeError):
@@ -305,48 +306,63 @@ def futr_check(ws=None, kv=None, stream=None) -> int:
 # their types, shapes and strides are checked here, the C side cannot see them.
 # ----------------------------------------------------------------------------
 
-def _dtype16(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return FUTR_DTYPE_BF16
-    if t.dtype == torch.float16:
-        return FUTR_DTYPE_F16
-    raise TypeError(f"rows are bfloat16 or float16, not {t.dtype}")
+# Decoding calls these once per layer and token, so the checks cost as few
+# Python steps as they can: types and devices are bound once.
+_T = None
 
 
-def _ints(t, name: str, device: int, size: int) -> int:
-    import torch
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != size:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of {size} elements")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on CUDA device {device}, the current one")
-    return t.data_ptr()
+class _Torch:
+    """What the checks need of torch (imported on first use)."""
+
+    def __init__(self):
+        import torch
+        self.int32, self.float32, self.bfloat16 = torch.int32, torch.float32, torch.bfloat16
+        self.rows = {torch.bfloat16: FUTR_DTYPE_BF16, torch.float16: FUTR_DTYPE_F16}
+        self.device = torch.cuda.current_device
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _rows(t, name: str, device: int, shape) -> int:
-    """Checks a row tensor [n_rows, heads, head_dim] with contiguous heads; returns its row stride."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on CUDA device {device}, the current one")
-    st = t.stride()
-    if st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return st[0] if shape[0] > 1 else max(shape[1] * shape[2], 8 * (st[0] // 8))
+def _torch() -> _Torch:
+    global _T
+    if _T is None:
+        _T = _Torch()
+    return _T
 
 
-def _current(stream):
-    import torch
-    device = torch.cuda.current_device()
-    return device, (torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream))
+def _bad_tensor(t, name, want, device):
+    where = "" if t.get_device() == device else f" on CUDA device {device}, the current one"
+    raise ValueError(f"{name} must be {want}{where}, not {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _paged_rows(cache, batch, pos, start, table, n_rows, device):
-    if table.dim() != 2 or table.shape[0] != batch:
-        raise ValueError(f"table must have the shape ({batch}, pages)")
-    width = table.shape[1]
-    return (_ints(pos, "pos", device, batch), None if start is None else _ints(start, "start", device, batch + 1),
-            n_rows, _ints(table, "table", device, batch * width), width)
+def _row_dtype(T, a, b, names) -> int:
+    dtype = a.dtype
+    if b.dtype is not dtype or dtype not in T.rows:
+        raise TypeError(f"{names} must both be bfloat16 or both float16, not {dtype} and {b.dtype}")
+    return T.rows[dtype]
+
+
+def _row_stride(t, name, device, n, heads, d) -> int:
+    """Elements from one row to the next of a row tensor [n, heads, d]."""
+    ld, sh, sd = t.stride()
+    if t.shape != (n, heads, d) or sd != 1 or (sh != d and heads != 1) or t.get_device() != device:
+        _bad_tensor(t, name, f"rows ({n}, {heads}, {d}), the heads of a row contiguous,", device)
+    return ld if n > 1 else -(-heads * d // 8) * 8
+
+
+def _paged_rows(T, batch, pos, start, table, n_rows, device):
+    """The arguments pos, start, n_rows, table, table_ld of a paged call."""
+    int32 = T.int32
+    if pos.dtype is not int32 or pos.shape != (batch,) or not pos.is_contiguous() or pos.get_device() != device:
+        _bad_tensor(pos, "pos", f"a contiguous int32 tensor ({batch},)", device)
+    if start is not None and (start.dtype is not int32 or start.shape != (batch + 1,) or not start.is_contiguous() or
+                              start.get_device() != device):
+        _bad_tensor(start, "start", f"a contiguous int32 tensor ({batch + 1},)", device)
+    shape = table.shape
+    if (table.dtype is not int32 or len(shape) != 2 or shape[0] != batch or not table.is_contiguous() or
+            table.get_device() != device):
+        _bad_tensor(table, "table", f"a contiguous int32 tensor ({batch}, pages)", device)
+    return pos.data_ptr(), None if start is None else start.data_ptr(), n_rows, table.data_ptr(), shape[1]
 
 
 def futr_paged_size(shape, n_layers, n_pages, page, max_pos) -> int:
@@ -378,14 +394,16 @@ def paged_views(cache):
 
 def futr_paged_append(cache, layer, batch, pos, start, table, k, v, stream=None):
     """Append the rows k, v [n_rows, kv-heads, head_dim]; start None: one row per sequence."""
-    device, st = _current(stream)
-    shape = (k.shape[0], cache.shape.n_kv_heads, cache.shape.head_dim)
-    if v.dtype != k.dtype:
-        raise TypeError("k and v must have the same type")
-    ld_k, ld_v = _rows(k, "k", device, shape), _rows(v, "v", device, shape)
-    r = _paged_rows(cache, batch, pos, start, table, shape[0], device)
-    _ok(lib().futr_paged_append(C.addressof(cache), layer, batch, *r, k.data_ptr(), ld_k, v.data_ptr(), ld_v,
-                                _dtype16(k), st), "futr_paged_append")
+    T = _T or _torch()
+    device = T.device()
+    shape = cache.shape
+    n, heads, d = k.shape[0], shape.n_kv_heads, shape.head_dim
+    dtype = _row_dtype(T, k, v, "k and v")
+    ld_k, ld_v = _row_stride(k, "k", device, n, heads, d), _row_stride(v, "v", device, n, heads, d)
+    p, s, n, t, ld = _paged_rows(T, batch, pos, start, table, n, device)
+    _ok(lib().futr_paged_append(C.addressof(cache), layer, batch, p, s, n, t, ld, k.data_ptr(), ld_k, v.data_ptr(),
+                                ld_v, dtype, T.stream(device) if stream is None else _stream(stream)),
+        "futr_paged_append")
 
 
 def futr_paged_workspace_size(shape) -> int:
@@ -405,14 +423,16 @@ def futr_paged_workspace_init(shape, mem, stream=None) -> futr_paged_ws:
 def futr_paged_attention(cache, layer, batch, pos, start, table, q, out, ws, scale=0.0, window=0, stream=None):
     """Attention of the rows q [n_rows, heads, head_dim] over the cache into out
     (same shape and type); scale 0 is 1/sqrt(head_dim), window 0 is none."""
-    device, st = _current(stream)
-    shape = (q.shape[0], cache.shape.n_q_heads, cache.shape.head_dim)
-    if out.dtype != q.dtype:
-        raise TypeError("q and out must have the same type")
-    ld_q, ld_out = _rows(q, "q", device, shape), _rows(out, "out", device, shape)
-    r = _paged_rows(cache, batch, pos, start, table, shape[0], device)
-    _ok(lib().futr_paged_attention(C.addressof(cache), layer, batch, *r, q.data_ptr(), ld_q, out.data_ptr(), ld_out,
-                                   _dtype16(q), scale, window, C.addressof(ws), st), "futr_paged_attention")
+    T = _T or _torch()
+    device = T.device()
+    shape = cache.shape
+    n, heads, d = q.shape[0], shape.n_q_heads, shape.head_dim
+    dtype = _row_dtype(T, q, out, "q and out")
+    ld_q, ld_out = _row_stride(q, "q", device, n, heads, d), _row_stride(out, "out", device, n, heads, d)
+    p, s, n, t, ld = _paged_rows(T, batch, pos, start, table, n, device)
+    _ok(lib().futr_paged_attention(C.addressof(cache), layer, batch, p, s, n, t, ld, q.data_ptr(), ld_q,
+                                   out.data_ptr(), ld_out, dtype, scale, window, C.addressof(ws),
+                                   T.stream(device) if stream is None else _stream(stream)), "futr_paged_attention")
 
 
 def futr_paged_check(cache, ws=None, stream=None) -> int:
@@ -437,21 +457,19 @@ def futr_moe_weights_size(shape) -> int:
 def _dense(t, name: str, dtype, shape, device: int) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of the shape {shape}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on CUDA device {device}, the current one")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        _bad_tensor(t, name, f"a contiguous {dtype} tensor {shape}", device)
     return t.data_ptr()
 
 
 def futr_moe_pack(shape, expert, wgate, wup, wdown, gain, blob, stream=None):
-    import torch
-    device, st = _current(stream)
-    H, I, f32 = shape.hidden, shape.inter, torch.float32
+    T = _T or _torch()
+    device = T.device()
+    H, I, f32 = shape.hidden, shape.inter, T.float32
     _ok(lib().futr_moe_pack(C.byref(shape), expert, _dense(wgate, "wgate", f32, (I, H), device),
                             _dense(wup, "wup", f32, (I, H), device), _dense(wdown, "wdown", f32, (H, I), device),
                             _dense(gain, "gain", f32, (H,), device), _ptr(blob), blob.numel() * blob.element_size(),
-                            st), "futr_moe_pack")
+                            _stream(stream)), "futr_moe_pack")
 
 
 def futr_moe_unpack(shape, blob, expert, which, codes, scales, stream=None):
@@ -475,21 +493,20 @@ def futr_moe_workspace_init(shape, max_batch, mem, stream=None) -> futr_moe_ws:
 
 def futr_moe_layer(x, gain, router, blob, resid, y, ws, ids=None, weights=None, stream=None):
     """The layer of x [batch, hidden] (bf16) into y; resid, gain, ids and weights may be None."""
-    import torch
-    device, st = _current(stream)
+    T = _T or _torch()
+    device = T.device()
     s = ws.shape
-    H, E, bf = s.hidden, s.n_experts, torch.bfloat16
-    rows, picks = (x.shape[0], H), (x.shape[0], s.top_k)
-    if blob.numel() * blob.element_size() < futr_moe_weights_size(s):
-        raise ValueError("blob is smaller than the layer's packed experts")
-    if blob.get_device() != device:
-        raise ValueError(f"blob must be on CUDA device {device}, the current one")
-    _ok(lib().futr_moe_layer(_dense(x, "x", bf, rows, device), _dense(gain, "gain", torch.float32, (H,), device),
-                             _dense(router, "router", bf, (E, H), device), blob.data_ptr(), rows[0],
+    H, K, bf, n = s.hidden, s.top_k, T.bfloat16, x.shape[0]
+    rows = (n, H)
+    if blob.nbytes < ws.blob_bytes or not blob.is_contiguous() or blob.get_device() != device:
+        raise ValueError(f"blob must hold the layer's packed experts, {ws.blob_bytes} contiguous bytes on CUDA device "
+                         f"{device}, the current one")
+    _ok(lib().futr_moe_layer(_dense(x, "x", bf, rows, device), _dense(gain, "gain", T.float32, (H,), device),
+                             _dense(router, "router", bf, (s.n_experts, H), device), blob.data_ptr(), n,
                              _dense(resid, "resid", bf, rows, device), _dense(y, "y", bf, rows, device),
-                             _dense(ids, "ids", torch.int32, picks, device),
-                             _dense(weights, "weights", torch.float32, picks, device), C.addressof(ws), st),
-        "futr_moe_layer")
+                             _dense(ids, "ids", T.int32, (n, K), device),
+                             _dense(weights, "weights", T.float32, (n, K), device), C.addressof(ws),
+                             T.stream(device) if stream is None else _stream(stream)), "futr_moe_layer")
 
 
 def futr_moe_check(ws, stream=None) -> int:
