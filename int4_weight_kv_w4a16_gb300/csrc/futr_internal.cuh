@@ -520,8 +520,6 @@ cudaError_t launch_unpack(const futr_shape& s, const uint8_t* blob, int which, i
 // One expert of a mixture-of-experts blob: its gate/up and down sections.
 cudaError_t launch_pack_expert(int hidden, int inter, const float* wg, const float* wu, const float* wd,
                                const float* gain, uint8_t* gu, uint8_t* down, cudaStream_t st);
-cudaError_t launch_unpack_expert(int hidden, int inter, const uint8_t* gu, const uint8_t* down, int which,
-                                 int8_t* codes, uint16_t* scales, cudaStream_t st);
 size_t gptq_scratch_bytes(const futr_shape& s);
 // Synchronizes st; *bad_host = 1 when a dampened Hessian was not positive definite.
 cudaError_t launch_pack_gptq(const futr_shape& s, const float* wq, const float* wk, const float* wv,

@@ -6,25 +6,37 @@
 //   y_t = resid_t + sum_j w_tj Wd_e (silu(r_t W'g_e x_t) * (r_t W'u_e x_t)),  e = e_tj
 //
 // Three kernels with programmatic dependent launch:
-//   router   a warp per expert and four tokens; the CTA that arrives last picks
-//            the experts of every token and sorts the (token, expert) pairs by expert;
+//   router   a CTA per four experts and eight tokens, which also leaves its part
+//            of the tokens as f16; the CTA that arrives last picks the experts of
+//            every token and sorts the (token, expert) pairs by expert;
 //   gate/up  streams the chosen experts' gate/up units once;
 //   down     streams their down units once, beginning before gate/up has ended.
 // The expert kernels are bound by the weight stream.  All units of the chosen
 // experts form one run, cut into equal contiguous shares, one per CTA of a
 // grid that fills the GPU; the cut is made on the device from the routing.  A
-// unit (128 rows x 128 inputs) comes by one bulk copy, the 128 inputs of each
-// of the expert's tokens by one 256-byte copy each; four warps unpack the
-// nibbles straight into bf16 A fragments (as the block's projections do) and
-// the tokens are the N side, so an expert costs its own tokens' columns only.
-// A row block that spans CTAs leaves one record per CTA, added in CTA order by
-// the one that arrives last.  Down runs over (row block, expert, group) with
-// the expert inside: the experts of a row block meet in one fp32 tile per
-// token in shared memory, so y needs no second pass.
+// unit (128 rows x 128 inputs) comes by one bulk copy, the record of each of the
+// expert's tokens (128 inputs and their sum) by one more; four warps unpack the
+// nibbles straight into f16 A fragments and the tokens are the N side, so an
+// expert costs its own tokens' columns only.  A row block that spans CTAs leaves
+// one record per CTA, added in CTA order by the one that arrives last.  Down
+// runs over (row block, expert, group) with the expert inside: the experts of a
+// row block meet in one fp32 tile per token in shared memory, so y needs no
+// second pass.
 //
-// Rounding: the activation w * silu * up is rounded to bf16 between the two
-// expert kernels (it is the B operand of the down product), the routing weight
-// inside, so the weighted sum over experts is an fp32 sum.  Everything else is
+// The products.  A nibble u = code + 8 enters as v = 1 + u/16 (rows g of an MMA
+// tile) or 1 + u/256 (rows g + 8), so
+//   sum code x = 16 (sum v x - 1.5 sum x)   or   256 (sum v x - 1.03125 sum x):
+// the accumulators start at -1.5 (-1.03125) times the inputs' sum, and 16 (256)
+// is multiplied in once at the end.  That takes 5 operations a word instead of the
+// 9 of an exact conversion, which is what the kernels were short of.  It costs
+// accuracy where sums cancel: the fp32 accumulator holds up to 1.03 |sum x| next
+// to terms u x / 256, so a group's product is good to about 2^-24 * 264 |sum x|
+// against |code| |x|, some 2^-14 of it for 128 inputs of random sign, far below
+// the bf16 output's 2^-9.
+//
+// Rounding: inputs are f16 (x divided by a power of two near its RMS, so bf16
+// values keep all their bits down to 2^-14 of it; w * silu * up, the routing
+// weight inside, by one at the largest of each 64: 11 bits).  Everything else is
 // fp32 until y.
 #include "moe.cuh"
 
@@ -35,8 +47,10 @@ namespace {
 constexpr int kMoeCW = 4;
 constexpr int kMoeThreads = (kMoeCW + 1) * 32;
 constexpr int kMoeMaxPerSm = 3;
-constexpr int kRouterThreads = 256;
-constexpr int kRouterTokens = 4;   // tokens of a router warp
+constexpr int kRouterThreads = 1024;
+constexpr int kRouterE = 4;        // experts of a router CTA
+constexpr int kRouterT = 8;        // its tokens
+constexpr int kRouterSlices = kRouterThreads / 32 / kRouterE;   // parts of the inputs: a warp's share
 constexpr unsigned long long kMoeWaitNs = 1000000000ull;
 
 __device__ __forceinline__ bool moe_wait(uint64_t* bar, uint32_t parity, const int* err) {
@@ -53,91 +67,156 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// 2^e at the leading bit of v >= 0 (1 for 0, and bounded so that 2^-e is normal).
+__device__ __forceinline__ float pow2_at(float v) {
+  const int e = min(max((int)(__float_as_uint(v) >> 23) - 127, -120), 120);
+  return v > 0.f ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.f;
+}
+__device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+
 // ------------------------------------------------------------------ router --
 
+// Floats in ascending order as unsigned integers in ascending order (NaN: below -inf).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 0u;
+  const uint32_t u = __float_as_uint(v + 0.f);   // -0 counts as 0
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
 __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArgs a) {
+  __shared__ float s_dot[kRouterE][kRouterSlices][kRouterT], s_sq[kRouterSlices][kRouterT];
+  __shared__ float s_factor[kRouterT];
   __shared__ int s_last;
   __shared__ int s_id[kMoeMaxPairs];
   __shared__ float s_w[kMoeMaxPairs];
   __shared__ unsigned s_mask[kMoeMaxExperts];   // tokens of each expert
   __shared__ int s_off[kMoeMaxExperts];
-  __shared__ int s_sum[2][kRouterThreads / 32];
+  __shared__ int s_sum[2][kMoeMaxExperts / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();
-  const int task = blockIdx.x * (kRouterThreads / 32) + warp;
-  const int e = task % a.E, t0 = task / a.E * kRouterTokens;
-  if (task == 0 && lane == 0) {
+  const int et = blockIdx.x, t0 = blockIdx.y * kRouterT, nt = min(kRouterT, a.T - t0);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
     const MoeHeader* h = reinterpret_cast<const MoeHeader*>(a.blob);
     if (h->magic != kMoeMagic || h->hidden != a.H || h->inter != a.I || h->n_experts != a.E)
       set_err(a.err, FUTR_ERR_BAD_BLOB);
   }
-  if (t0 < a.T) {
-    const int nt = min(kRouterTokens, a.T - t0);
-    float acc[kRouterTokens] = {}, ss[kRouterTokens] = {};
-    const __nv_bfloat16* wr = a.router + (size_t)e * a.H;
-#pragma unroll 4
-    for (int j = 8 * lane; j < a.H; j += 256) {
-      float w[8], g[8];
-      const uint4 wv = *reinterpret_cast<const uint4*>(wr + j);
-      const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
+  // warp = (expert, slice): every kRouterSlices-th chunk of 256 inputs
+  {
+    const int el = warp / kRouterSlices, sl = warp % kRouterSlices, e = et * kRouterE + el;
+    float acc[kRouterT], ss[kRouterT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[2 * i] = __uint_as_float(wu[i] << 16);
-        w[2 * i + 1] = __uint_as_float(wu[i] & 0xffff0000u);
-        g[2 * i] = g[2 * i + 1] = 1.f;
-      }
-      if (a.gain) {
-        const float4 g0 = *reinterpret_cast<const float4*>(a.gain + j), g1 = *reinterpret_cast<const float4*>(a.gain + j + 4);
-        g[0] = g0.x; g[1] = g0.y; g[2] = g0.z; g[3] = g0.w;
-        g[4] = g1.x; g[5] = g1.y; g[6] = g1.z; g[7] = g1.w;
-      }
+    for (int t = 0; t < kRouterT; ++t) acc[t] = ss[t] = 0.f;
+    if (e < a.E || el == 0) {
+      const __nv_bfloat16* wr = a.router + (size_t)min(e, a.E - 1) * a.H;
+      for (int j = 256 * sl + 8 * lane; j < a.H; j += 256 * kRouterSlices) {
+        float w[8];
+        const uint4 wv = *reinterpret_cast<const uint4*>(wr + j);
+        uint4 xv[kRouterT];
 #pragma unroll
-      for (int t = 0; t < kRouterTokens; ++t)
-        if (t < nt) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(a.x + (size_t)(t0 + t) * a.H + j);
-          const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
-          float s = 0.f, q = 0.f;   // sums of 8 first: a short chain of additions
+        for (int t = 0; t < kRouterT; ++t)
+          if (t < nt) xv[t] = *reinterpret_cast<const uint4*>(a.x + (size_t)(t0 + t) * a.H + j);
+        float g[8];
+        if (a.gain) {
+          const float4 g0 = *reinterpret_cast<const float4*>(a.gain + j), g1 = *reinterpret_cast<const float4*>(a.gain + j + 4);
+          g[0] = g0.x; g[1] = g0.y; g[2] = g0.z; g[3] = g0.w;
+          g[4] = g1.x; g[5] = g1.y; g[6] = g1.z; g[7] = g1.w;
+        } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float lo = __uint_as_float(xu[i] << 16), hi = __uint_as_float(xu[i] & 0xffff0000u);
-            s = fmaf(__fmul_rn(lo, g[2 * i]), w[2 * i], s);
-            s = fmaf(__fmul_rn(hi, g[2 * i + 1]), w[2 * i + 1], s);
-            q = fmaf(lo, lo, fmaf(hi, hi, q));
-          }
-          acc[t] += s;
-          ss[t] += q;
+          for (int i = 0; i < 8; ++i) g[i] = 1.f;
         }
+        const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[2 * i] = __uint_as_float(wu[i] << 16);
+          w[2 * i + 1] = __uint_as_float(wu[i] & 0xffff0000u);
+        }
+#pragma unroll
+        for (int t = 0; t < kRouterT; ++t)
+          if (t < nt) {
+            const uint32_t xu[4] = {xv[t].x, xv[t].y, xv[t].z, xv[t].w};
+            float s = 0.f, q = 0.f;   // sums of 8 first: a short chain of additions
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float lo = __uint_as_float(xu[i] << 16), hi = __uint_as_float(xu[i] & 0xffff0000u);
+              s = fmaf(__fmul_rn(lo, g[2 * i]), w[2 * i], s);
+              s = fmaf(__fmul_rn(hi, g[2 * i + 1]), w[2 * i + 1], s);
+              q = fmaf(lo, lo, fmaf(hi, hi, q));
+            }
+            acc[t] += s;
+            ss[t] += q;
+          }
+      }
     }
 #pragma unroll
-    for (int t = 0; t < kRouterTokens; ++t)
+    for (int t = 0; t < kRouterT; ++t)
       if (t < nt) {
-        const float s = warp_sum(acc[t]), q = warp_sum(ss[t]);
-        const float r = a.eps > 0.f ? __fdiv_rn(1.0f, sqrtf(__fdiv_rn(q, (float)a.H) + a.eps)) : 1.f;
-        if (lane == 0) {
-          a.logits[(size_t)(t0 + t) * a.E + e] = r * s;
-          if (e == 0) a.route->rms[t0 + t] = r;
+        const float s = warp_sum(acc[t]);
+        if (lane == 0) s_dot[el][sl][t] = s;
+        if (el == 0) {
+          const float q = warp_sum(ss[t]);
+          if (lane == 0) s_sq[sl][t] = q;
         }
       }
   }
   __syncthreads();
+  if (tid < kRouterE * kRouterT) {
+    const int el = tid / kRouterT, t = tid % kRouterT, e = et * kRouterE + el;
+    if (t < nt) {
+      float s = 0.f, q = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRouterSlices; ++i) {
+        s += s_dot[el][i][t];
+        q += s_sq[i][t];
+      }
+      const float mean = __fdiv_rn(q, (float)a.H);
+      const float r = a.eps > 0.f ? __fdiv_rn(1.0f, sqrtf(mean + a.eps)) : 1.f;
+      if (e < a.E) a.logits[(size_t)(t0 + t) * a.E + e] = r * s;
+      if (el == 0) {
+        const float f = pow2_at(sqrtf(mean));
+        s_factor[t] = pow2_inverse(f);
+        if (et == 0) a.route->rms[t0 + t] = r * f;
+      }
+    }
+  }
+  __syncthreads();
+  // this CTA's part of its tokens as f16 records: a warp per record of 128 inputs
+  const int ng = a.H / kGroup;
+  for (int i = warp; ; i += kRouterThreads / 32) {
+    const int t = i % kRouterT, g = et + i / kRouterT * (int)gridDim.x;
+    if (g >= ng) break;
+    if (t >= nt) continue;
+    const uint2 v = *reinterpret_cast<const uint2*>(a.x + (size_t)(t0 + t) * a.H + g * kGroup + 4 * lane);
+    const float f = s_factor[t];
+    const __half2 h0 = __floats2half2_rn(__uint_as_float(v.x << 16) * f, __uint_as_float(v.x & 0xffff0000u) * f);
+    const __half2 h1 = __floats2half2_rn(__uint_as_float(v.y << 16) * f, __uint_as_float(v.y & 0xffff0000u) * f);
+    const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+    const float sum = warp_sum((f0.x + f0.y) + (f1.x + f1.y));
+    __half* rec = a.xh + ((size_t)(t0 + t) * ng + g) * kRecHalves;
+    reinterpret_cast<uint2*>(rec)[lane] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+    if (lane == 0) *reinterpret_cast<float4*>(rec + kGroup) = make_float4(sum, 0.f, 1.f, 1.f);
+  }
+  __syncthreads();
   if (tid == 0) {
-    s_last = atom_add_acq_rel_gpu(a.cnt + a.n_cnt, 1u) == gridDim.x - 1 ? 1 : 0;
+    s_last = atom_add_acq_rel_gpu(a.cnt + a.n_cnt, 1u) == gridDim.x * gridDim.y - 1 ? 1 : 0;
     if (s_last) a.cnt[a.n_cnt] = 0u;
   }
+  if (tid < kMoeMaxExperts) s_mask[tid] = 0u;
   __syncthreads();
   if (!s_last) return;
 
   // the choice of experts: a warp per token, expert lane + 32 i in v[i]
-  for (int i = tid; i < kMoeMaxExperts; i += kRouterThreads) s_mask[i] = 0u;
-  __syncthreads();
   constexpr int kV = kMoeMaxExperts / 32;
-  for (int t = warp; t < a.T; t += kRouterThreads / 32) {
+  if (warp < a.T) {
+    const int t = warp;
     float v[kV], mx = -INFINITY, sum = 0.f;
+    uint32_t key[kV];
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       v[i] = lane + 32 * i < a.E ? __ldcg(a.logits + (size_t)t * a.E + lane + 32 * i) : -INFINITY;
+      key[i] = order_key(v[i]);
       mx = fmaxf(mx, v[i]);
       nan |= v[i] != v[i];
     }
@@ -145,39 +224,34 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     nan = __any_sync(0xffffffffu, nan);
 #pragma unroll
-    for (int i = 0; i < kV; ++i) sum += lane + 32 * i < a.E ? expf(v[i] - mx) : 0.f;
+    for (int i = 0; i < kV; ++i)
+      if (32 * i < a.E) sum += lane + 32 * i < a.E ? expf(v[i] - mx) : 0.f;
     sum = warp_sum(sum);
-    unsigned taken = 0u;   // this lane's chosen experts
+    unsigned taken = 0u;               // this lane's chosen experts
     float chosen = 0.f, total = 0.f;   // lane j: weight of the j-th choice
     int chosen_id = 0;
+#pragma unroll 1
     for (int j = 0; j < a.K; ++j) {
-      // largest value, then lowest index; NaN ranks with -inf
-      float bv = -INFINITY;
+      // largest key, then lowest index, among the experts not taken
+      uint32_t bk = 0u;
       int bi = 0x7fffffff;
+      float bv = 0.f;
 #pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const int id = lane + 32 * i;
-        const float c = v[i] != v[i] ? -INFINITY : v[i];
-        if (id < a.E && !((taken >> i) & 1u) && (bi == 0x7fffffff || c > bv)) {
-          bv = c;
-          bi = id;
+      for (int i = 0; i < kV; ++i)
+        if (lane + 32 * i < a.E && !((taken >> i) & 1u) && (bi == 0x7fffffff || key[i] > bk)) {
+          bk = key[i];
+          bi = lane + 32 * i;
+          bv = v[i];
         }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-        const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-        if (oi != 0x7fffffff && (bi == 0x7fffffff || ov > bv || (ov == bv && oi < bi))) {
-          bv = ov;
-          bi = oi;
-        }
-      }
-      if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
-      const float w = nan ? __int_as_float(0x7fc00000) : __fdiv_rn(expf(bv - mx), sum);
+      const uint32_t best = __reduce_max_sync(0xffffffffu, bi == 0x7fffffff ? 0u : bk);
+      const int id = __reduce_min_sync(0xffffffffu, bk == best ? bi : 0x7fffffff);
+      const float val = __shfl_sync(0xffffffffu, bv, id & 31);
+      if ((id & 31) == lane) taken |= 1u << (id >> 5);
+      const float w = nan ? __int_as_float(0x7fc00000) : __fdiv_rn(expf(val - mx), sum);
       total += w;
       if (lane == j) {
         chosen = w;
-        chosen_id = bi;
+        chosen_id = id;
       }
     }
     if (a.renorm) chosen = __fdiv_rn(chosen, total);
@@ -192,10 +266,12 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
   }
   __syncthreads();
   // experts in use and the first pair of each: prefix sums over the experts
-  {
-    const unsigned mask = tid < a.E ? s_mask[tid] : 0u;
-    const int n = __popc(mask), used = n > 0;
-    int pn = n, pu = used;
+  int n = 0, used = 0, pn = 0, pu = 0;
+  if (tid < kMoeMaxExperts) {
+    n = __popc(s_mask[tid]);
+    used = n > 0;
+    pn = n;
+    pu = used;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, pn, o), y = __shfl_up_sync(0xffffffffu, pu, o);
@@ -208,7 +284,9 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
       s_sum[0][warp] = pn;
       s_sum[1][warp] = pu;
     }
-    __syncthreads();
+  }
+  __syncthreads();
+  if (tid < kMoeMaxExperts) {
     int bn = 0, bu = 0;
     for (int w = 0; w < warp; ++w) {
       bn += s_sum[0][w];
@@ -219,7 +297,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
       a.route->expert[bu + pu - 1] = tid;
       a.route->off[bu + pu - 1] = bn + pn - n;
     }
-    if (tid == kRouterThreads - 1) {
+    if (tid == kMoeMaxExperts - 1) {
       a.route->n_active = bu + pu;
       a.route->off[bu + pu] = bn + pn;
     }
@@ -237,19 +315,33 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
 
 template <int NT>
 struct MoeLayout {
-  static constexpr int kRing = NT == 4 ? 5 : 6;                      // two CTAs an SM at the least
-  static constexpr int kStage = kUnitBytes + 8 * NT * kTileLd * 2;   // unit, then [8 NT][136] bf16
-  static constexpr int kRed = kRing * kStage;                        // [8 NT][kRedLd] fp32
+  static constexpr int kRing = NT == 4 ? 5 : 6;                  // two CTAs an SM at the least
+  static constexpr int kStage = kUnitBytes + 8 * NT * kRecBytes;  // unit, then [8 NT] records
+  static constexpr int kRed = kRing * kStage;                    // [8 NT][kRedLd] fp32
   static constexpr int kBar = kRed + 8 * NT * kRedLd * 4;
   static constexpr int kBytes = kBar + 2 * kRing * 8 + 16;
 };
 
-// One unit times n_nt tiles of 8 columns for this warp's 32 rows: the group's
-// product in fp32, then times the rows' scales into acc.
-template <int NT>
-__device__ __forceinline__ void moe_unit(const uint8_t* st, const int (&xrow)[NT], int n_nt, float (&acc)[2][NT][4]) {
+// The four f16x2 registers of a word (see moe.cuh): rows g 1 + u/16, rows g + 8
+// 1 + u/256.
+__device__ __forceinline__ void place4(uint32_t w, uint32_t (&r)[4]) {
+  const uint32_t s = __byte_perm(w, w, 0x2301);
+  r[0] = (w & 0x03C003C0u) | 0x3C003C00u;
+  r[1] = (w & 0x003C003Cu) | 0x3C003C00u;
+  r[2] = (s & 0x03C003C0u) | 0x3C003C00u;
+  r[3] = (s & 0x003C003Cu) | 0x3C003C00u;
+}
+constexpr float kBiasA = -1.5f, kBiasB = -1.03125f;   // -(16 + 8) / 16, -(256 + 8) / 256
+constexpr float kUnitA = 16.f, kUnitB = 256.f;
+
+// One unit times NT tiles of 8 columns for this warp's 32 rows, the group's
+// product times the rows' scales into acc.  Down: the two halves of the inputs
+// have factors of their own.
+template <int NT, bool kDown>
+__device__ __forceinline__ void moe_unit(const uint8_t* st, const int (&xrow)[NT], const int (&col)[NT],
+                                         float (&acc)[2][NT][4]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2;
-  const __nv_bfloat16* tile = reinterpret_cast<const __nv_bfloat16*>(st + kUnitBytes);
+  const __half* tile = reinterpret_cast<const __half*>(st + kUnitBytes);
   const uint4* wt = reinterpret_cast<const uint4*>(st + 2 * warp * 1024);
   const __half* sc = reinterpret_cast<const __half*>(st + kUnitCodeBytes);
   uint32_t words[2][8];
@@ -263,39 +355,61 @@ __device__ __forceinline__ void moe_unit(const uint8_t* st, const int (&xrow)[NT
     s_lo[m] = __half2float(sc[r0]);
     s_hi[m] = __half2float(sc[r0 + 8]);
   }
-  float d[2][NT][4];
+  // sums (and factors) of this lane's two columns of each tile
+  MoeTail tail[NT][2];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[m][nt][i] = 0.f;
+    for (int i = 0; i < 2; ++i) {
+      const float* p = reinterpret_cast<const float*>(tile + (col[nt] + i) * kRecHalves + kGroup);
+      if (kDown) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        tail[nt][i] = MoeTail{{v.x, v.y}, {v.z, v.w}};
+      } else {
+        tail[nt][i].sum[0] = *p;
+      }
+    }
+  float d[2][NT][4], part[2][NT][4];
 #pragma unroll
   for (int kp = 0; kp < 4; ++kp) {
+    if (kp == 0 || (kDown && kp == 2)) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (kp == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[m][nt][i] = d[m][nt][i] * tail[nt][i & 1].factor[0];
+          }
+          const float s0 = tail[nt][0].sum[kp >> 1], s1 = tail[nt][1].sum[kp >> 1];
+          d[m][nt][0] = kBiasA * s0;
+          d[m][nt][1] = kBiasA * s1;
+          d[m][nt][2] = kBiasB * s0;
+          d[m][nt][3] = kBiasB * s1;
+        }
+    }
     uint32_t b[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      if (nt < n_nt) ldmatrix_x4(b[nt], tile + xrow[nt] + 32 * kp);
+    for (int nt = 0; nt < NT; ++nt) ldmatrix_x4(b[nt], tile + xrow[nt] + 32 * kp);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         uint32_t af[4];
-        nib4_bf16x2(words[m][2 * kp + h], af);
+        place4(words[m][2 * kp + h], af);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          if (nt < n_nt) mma_bf16_16816(d[m][nt], af, b[nt][2 * h], b[nt][2 * h + 1]);
+        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(d[m][nt], af, b[nt][2 * h], b[nt][2 * h + 1]);
       }
   }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      acc[m][nt][0] = fmaf(s_lo[m], d[m][nt][0], acc[m][nt][0]);
-      acc[m][nt][1] = fmaf(s_lo[m], d[m][nt][1], acc[m][nt][1]);
-      acc[m][nt][2] = fmaf(s_hi[m], d[m][nt][2], acc[m][nt][2]);
-      acc[m][nt][3] = fmaf(s_hi[m], d[m][nt][3], acc[m][nt][3]);
-    }
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = kDown ? fmaf(d[m][nt][i], tail[nt][i & 1].factor[1], part[m][nt][i]) : d[m][nt][i];
+        acc[m][nt][i] = fmaf(i < 2 ? s_lo[m] : s_hi[m], v, acc[m][nt][i]);
+      }
 }
 
 // The run of units of a kernel.  Gate/up: item = (expert, row block), its
@@ -327,6 +441,70 @@ struct MoeRun {
     end = u - g + ng;
   }
 };
+
+// A CTA's place in its ring of stages.
+struct MoeRing {
+  int slot;
+  uint32_t phase;
+  bool ok;
+};
+
+// The units u .. end - 1 of one (row block, expert) with n <= 8 NT columns, and
+// their sums into this warp's 32 rows of the tile red[column][row].  Down:
+// column = token, added expert by expert (a token has one column per expert, and
+// only this warp touches these rows).
+template <int NT, int NTL, bool kDown>
+__device__ __forceinline__ void run_units(const MoeArgs& a, uint8_t* smem, float* red, uint64_t* full, uint64_t* empty,
+                                          volatile int* s_dead, const int* token, int n, int units, MoeRing& ring) {
+  using Lay = MoeLayout<NTL>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t4 = lane & 3;
+  // columns past n read column 0: they only feed MMA columns that are not stored
+  int xrow[NT], col[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int c = 8 * nt + (lane & 7);
+    xrow[nt] = (c < n ? c : 0) * kRecHalves + 8 * (lane >> 3);
+    col[nt] = 8 * nt + 2 * t4 + 1 < 8 * NTL ? 8 * nt + 2 * t4 : 0;
+  }
+  float acc[2][NT][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][nt][i] = 0.f;
+#pragma unroll 1
+  for (int u = 0; u < units; ++u) {
+    if (ring.ok && !moe_wait(&full[ring.slot], ring.phase, a.err)) {
+      ring.ok = false;
+      record_timeout(a.err);
+      *s_dead = 1;
+    }
+    if (ring.ok) moe_unit<NT, kDown>(smem + ring.slot * Lay::kStage, xrow, col, acc);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[ring.slot]);
+    if (++ring.slot == Lay::kRing) {
+      ring.slot = 0;
+      ring.phase ^= 1u;
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = 8 * nt + 2 * t4 + i;
+      if (c < n) {
+        float* p = red + (kDown ? token[c] : c) * kRedLd + 32 * warp + gr;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float lo = kUnitA * acc[m][nt][i], hi = kUnitB * acc[m][nt][2 + i];
+          p[16 * m] = kDown ? p[16 * m] + lo : lo;
+          p[16 * m + 8] = kDown ? p[16 * m + 8] + hi : hi;
+        }
+      }
+    }
+  __syncwarp();
+}
 
 template <int NT, bool kDown>
 __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kernel(const MoeArgs a) {
@@ -366,7 +544,6 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
   const int cta = blockIdx.x, ctas = min(total, (int)gridDim.x);
   if (cta >= ctas) return;
   const int u0 = (int)((long long)total * cta / ctas), u1 = (int)((long long)total * (cta + 1) / ctas);
-  const int K = kDown ? a.I : a.H;   // inputs of the product
 
   if (warp == kMoeCW) {
     // ---------------------------------------------------------- producer --
@@ -375,7 +552,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
     bool ok = true;
     bool waited = !kDown;
     int rows_due = 0;   // down: stages whose activations wait for gate/up
-    const __nv_bfloat16* due[kMoeRing];
+    const __half* due[kMoeRing];
     int due_n[kMoeRing];
     for (int u = u0; u < u1 && ok;) {
       int rb, ai, g, end;
@@ -384,10 +561,9 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
       const int e = rt->expert[ai], off = rt->off[ai], n = rt->off[ai + 1] - off;
       const uint8_t* w = a.blob + kHeaderBytes + (size_t)e * a.expert_bytes + (kDown ? a.gu_bytes : 0) +
                          ((size_t)rb * run.ng + g) * kUnitBytes;
-      // this lane's token row (columns n..31 have none)
-      const __nv_bfloat16* row = nullptr;
-      if (lane < n) row = kDown ? a.act + (size_t)(off + lane) * K : a.x + (size_t)rt->token[off + lane] * K;
-      row += (size_t)g * kGroup;
+      // this lane's token's records (columns n..31 have none)
+      const __half* row = kDown ? a.act : a.xh;
+      if (lane < n) row += ((size_t)(kDown ? off + lane : rt->token[off + lane]) * run.ng + g) * kRecHalves;
       for (; u < end; ++u) {
         if (issued >= kMoeRing) {
           if (!moe_wait(&empty[slot], phase ^ 1u, a.err)) {
@@ -397,11 +573,11 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
         }
         uint8_t* st = smem + slot * Lay::kStage;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&full[slot], kUnitBytes + n * kGroup * 2);
+          mbar_arrive_expect_tx(&full[slot], kUnitBytes + n * kRecBytes);
           bulk_g2s(st, w, kUnitBytes, &full[slot]);
         }
         if (waited) {
-          if (lane < n) bulk_g2s(st + kUnitBytes + lane * kTileLd * 2, row, kGroup * 2, &full[slot]);
+          if (lane < n) bulk_g2s(st + kUnitBytes + lane * kRecBytes, row, kRecBytes, &full[slot]);
         } else {
           // the ring's first stages: weights now, activations after the wait
 #pragma unroll
@@ -417,11 +593,11 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
 #pragma unroll
             for (int i = 0; i < kMoeRing; ++i)
               if (i < rows_due && lane < due_n[i])
-                bulk_g2s(smem + i * Lay::kStage + kUnitBytes + lane * kTileLd * 2, due[i], kGroup * 2, &full[i]);
+                bulk_g2s(smem + i * Lay::kStage + kUnitBytes + lane * kRecBytes, due[i], kRecBytes, &full[i]);
           }
         }
         w += kUnitBytes;
-        row += kGroup;
+        row += kRecHalves;
         ++issued;
         if (++slot == kMoeRing) {
           slot = 0;
@@ -437,10 +613,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
   } else {
     // ---------------------------------------------------------- consumers --
     if (kDown) pdl_wait();   // records and counters are gate/up's until it has ended
-    const int gr = lane >> 2, t4 = lane & 3;
-    int slot = 0;
-    uint32_t phase = 0;
-    bool ok = true;
+    MoeRing ring{0, 0u, true};
     for (int u = u0; u < u1;) {
       // one item's part in this share
       const int item = u / run.item_len, i0 = item * run.item_len, i1 = i0 + run.item_len;
@@ -455,52 +628,14 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
         end = min(end, seg1);
         off = rt->off[ai];
         n = rt->off[ai + 1] - off;
-        const int n_nt = (n + 7) >> 3;
-        int xrow[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int c = 8 * nt + (lane & 7);
-          xrow[nt] = (c < n ? c : 0) * kTileLd + 8 * (lane >> 3);
-        }
-        float acc[2][NT][4];
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][nt][i] = 0.f;
-        for (; u < end; ++u) {
-          if (ok && !moe_wait(&full[slot], phase, a.err)) {
-            ok = false;
-            record_timeout(a.err);
-            *s_dead = 1;
-          }
-          if (ok) moe_unit<NT>(smem + slot * Lay::kStage, xrow, n_nt, acc);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[slot]);
-          if (++slot == kMoeRing) {
-            slot = 0;
-            phase ^= 1u;
-          }
-        }
-        // this warp's 32 rows of the tile red[column][row]; down: column = token,
-        // added expert by expert (a token has one column per expert, and only
-        // this warp touches these rows)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int c = 8 * nt + 2 * t4 + i;
-            if (c < n) {
-              float* p = red + (kDown ? rt->token[off + c] : c) * kRedLd + 32 * warp + gr;
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                p[16 * m] = kDown ? p[16 * m] + acc[m][nt][i] : acc[m][nt][i];
-                p[16 * m + 8] = kDown ? p[16 * m + 8] + acc[m][nt][2 + i] : acc[m][nt][2 + i];
-              }
-            }
-          }
-        __syncwarp();
+        const int* token = rt->token + off;
+        if (NT == 1 || n <= 8)
+          run_units<1, NT, kDown>(a, smem, red, full, empty, s_dead, token, n, end - u, ring);
+        else if (NT == 2 || n <= 16)
+          run_units<2, NT, kDown>(a, smem, red, full, empty, s_dead, token, n, end - u, ring);
+        else
+          run_units<4, NT, kDown>(a, smem, red, full, empty, s_dead, token, n, end - u, ring);
+        u = end;
       }
       const int cols = kDown ? a.T : n;
       if (tid == 0) *s_snap = *s_dead;
@@ -563,12 +698,29 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
                 make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
           }
         } else {
-          for (int i = tid; i < cols * 64; i += kMoeCW * 32) {
-            const int c = i >> 6, j = i & 63;
-            const float r = rt->rms[rt->token[off + c]];
-            const float gt = r * red[c * kRedLd + j], up = r * red[c * kRedLd + 64 + j];
-            const float s = __fdiv_rn(gt, 1.0f + expf(-gt)) * up;
-            a.act[(size_t)(off + c) * a.I + (size_t)rb * 64 + j] = __float2bfloat16_rn(rt->weight[off + c] * s);
+          // a warp per column: outputs 64 rb .. 64 rb + 63 of pair off + c, half a record
+          for (int c = warp; c < cols; c += kMoeCW) {
+            const float r = rt->rms[rt->token[off + c]], wt = rt->weight[off + c];
+            float v[2], mx = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float gt = r * red[c * kRedLd + 2 * lane + h], up = r * red[c * kRedLd + 64 + 2 * lane + h];
+              v[h] = wt * (__fdiv_rn(gt, 1.0f + expf(-gt)) * up);
+              mx = fmaxf(mx, fabsf(v[h]));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float f = pow2_at(mx), inv = pow2_inverse(f);
+            const __half2 hv = __floats2half2_rn(v[0] * inv, v[1] * inv);
+            const float2 hf = __half22float2(hv);
+            const float sum = warp_sum(hf.x + hf.y);
+            __half* rec = a.act + ((size_t)(off + c) * (a.I / kGroup) + (rb >> 1)) * kRecHalves;
+            reinterpret_cast<__half2*>(rec + 64 * (rb & 1))[lane] = hv;
+            if (lane == 0) {
+              MoeTail* tail = reinterpret_cast<MoeTail*>(rec + kGroup);
+              tail->sum[rb & 1] = sum;
+              tail->factor[rb & 1] = f;
+            }
           }
         }
       }
@@ -616,9 +768,9 @@ int moe_sms(int dev) {
 }
 
 template <class Kernel>
-cudaError_t moe_go(Kernel k, int grid, int threads, size_t smem, cudaStream_t st, const MoeArgs& a) {
+cudaError_t moe_go(Kernel k, dim3 grid, int threads, size_t smem, cudaStream_t st, const MoeArgs& a) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -636,9 +788,62 @@ cudaError_t launch_experts(const MoeArgs& a, int dev, cudaStream_t st) {
   if (e == cudaSuccess) e = moe_configure<NT, true>(dev);
   if (e != cudaSuccess) return e;
   const int sms = moe_sms(dev);
-  e = moe_go(moe_expert_kernel<NT, false>, sms * moe_per_sm<NT, false>(dev), kMoeThreads, MoeLayout<NT>::kBytes, st, a);
+  e = moe_go(moe_expert_kernel<NT, false>, dim3((unsigned)(sms * moe_per_sm<NT, false>(dev))), kMoeThreads,
+             MoeLayout<NT>::kBytes, st, a);
   if (e != cudaSuccess) return e;
-  return moe_go(moe_expert_kernel<NT, true>, sms * moe_per_sm<NT, true>(dev), kMoeThreads, MoeLayout<NT>::kBytes, st, a);
+  return moe_go(moe_expert_kernel<NT, true>, dim3((unsigned)(sms * moe_per_sm<NT, true>(dev))), kMoeThreads,
+                MoeLayout<NT>::kBytes, st, a);
+}
+
+// ----------------------------------------------------------------- packing --
+
+__host__ __device__ inline uint32_t place_word(uint32_t w) {
+  uint32_t r = 0;
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t u0 = (w >> (16 * h)) & 15u, u1 = (w >> (16 * h + 4)) & 15u, u2 = (w >> (16 * h + 8)) & 15u,
+                   u3 = (w >> (16 * h + 12)) & 15u;
+    r |= ((u0 << 6) | (u1 << 2) | (u3 << 10) | ((u2 & 3u) << 14) | (u2 >> 2)) << (16 * h);
+  }
+  return r;
+}
+
+__host__ __device__ inline uint32_t plain_word(uint32_t w) {
+  uint32_t r = 0;
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t v = (w >> (16 * h)) & 0xFFFFu;
+    const uint32_t u0 = (v >> 6) & 15u, u1 = (v >> 2) & 15u, u2 = ((v >> 14) & 3u) | ((v & 3u) << 2), u3 = (v >> 10) & 15u;
+    r |= (u0 | (u1 << 4) | (u2 << 8) | (u3 << 12)) << (16 * h);
+  }
+  return r;
+}
+
+// One CTA per unit.
+__global__ void __launch_bounds__(256) moe_place_kernel(uint8_t* units) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(units + (size_t)blockIdx.x * kUnitBytes);
+  for (int i = threadIdx.x; i < kUnitCodeBytes / 4; i += 256) w[i] = place_word(w[i]);
+}
+
+struct MoeUnpackArgs {
+  const uint8_t* sec;
+  int rows, cols, n_groups;
+  int map;  // 0 identity, 1 gate rows, 2 up rows
+  int8_t* codes;
+  uint16_t* scales;
+};
+
+__global__ void __launch_bounds__(256) moe_unpack_kernel(const MoeUnpackArgs a) {
+  const size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (e >= (size_t)a.rows * a.cols) return;
+  const int R = (int)(e / a.cols), C = (int)(e % a.cols);
+  const int SR = a.map == 0 ? R : 128 * (R / 64) + 64 * (a.map - 1) + (R % 64);
+  const int rb = SR >> 7, lr = SR & 127, rt = lr >> 4, rr = lr & 15;
+  const int grp = C >> 7, cc = C & 127, ks = cc >> 4, kk = cc & 15;
+  const int slot = (rr >> 3) + 2 * (kk >> 3) + 4 * (kk & 1);
+  const int lane = 4 * (rr & 7) + ((kk & 7) >> 1);
+  const uint8_t* unit = a.sec + ((size_t)rb * a.n_groups + grp) * kUnitBytes;
+  const uint32_t word = plain_word(reinterpret_cast<const uint32_t*>(unit)[rt * 256 + (ks >> 2) * 128 + lane * 4 + (ks & 3)]);
+  a.codes[e] = (int8_t)((int)((word >> (4 * slot)) & 0xF) - 8);
+  if (cc == 0) a.scales[(size_t)R * a.n_groups + grp] = reinterpret_cast<const uint16_t*>(unit + kUnitCodeBytes)[lr];
 }
 
 }  // namespace
@@ -653,13 +858,34 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const int tasks = a.E * ((a.T + kRouterTokens - 1) / kRouterTokens), warps = kRouterThreads / 32;
-  e = moe_go(moe_router_kernel, (tasks + warps - 1) / warps, kRouterThreads, 0, st, a);
+  e = moe_go(moe_router_kernel, dim3((unsigned)((a.E + kRouterE - 1) / kRouterE), (unsigned)((a.T + kRouterT - 1) / kRouterT)),
+             kRouterThreads, 0, st, a);
   if (e != cudaSuccess) return e;
   // an expert has at most T tokens
   if (a.T <= 8) return launch_experts<1>(a, dev, st);
   if (a.T <= 16) return launch_experts<2>(a, dev, st);
   return launch_experts<4>(a, dev, st);
+}
+
+cudaError_t launch_moe_place(uint8_t* units, size_t n_units, cudaStream_t st) {
+  moe_place_kernel<<<(unsigned)n_units, 256, 0, st>>>(units);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_moe_unpack(int hidden, int inter, const uint8_t* gu, const uint8_t* down, int which, int8_t* codes,
+                              uint16_t* scales, cudaStream_t st) {
+  const bool is_down = which == FUTR_PROJ_DOWN;
+  MoeUnpackArgs a{};
+  a.map = which == FUTR_PROJ_GATE ? 1 : which == FUTR_PROJ_UP ? 2 : 0;
+  a.rows = is_down ? hidden : inter;
+  a.cols = is_down ? inter : hidden;
+  a.sec = is_down ? down : gu;
+  a.n_groups = a.cols / kGroup;
+  a.codes = codes;
+  a.scales = scales;
+  const size_t n = (size_t)a.rows * a.cols;
+  moe_unpack_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace futr

@@ -3,7 +3,21 @@
 //
 // Blob: a 256-byte header, then for each expert its gate/up section (row blocks
 // of 64 gate and 64 up rows) and its down section, in the same 8448-byte units
-// of 128 rows x 128 inputs as a block's blob.
+// of 128 rows x 128 inputs as a block's blob, the eight nibbles u = code + 8 of a
+// word placed for f16 operands.  Each 16-bit half of a word holds
+//   bits 6-9: u of slot 0    bits 2-5: slot 1    bits 10-13: slot 3
+//   bits 14, 15, 0, 1: slot 2, low bit first
+// (slots as in the block's units: half 0 holds slots 0..3, half 1 slots 4..7, a
+// register pairs slots i and i + 4).  Masked, and with the bytes of each half
+// swapped masked again, all of them land in an f16's mantissa without a shift:
+// a word takes one byte permutation and four logic operations.  Or-ed with 1.0,
+// slots 0 and 2 (rows g of the A fragment) read 1 + u / 16 and slots 1 and 3
+// (rows g + 8) 1 + u / 256.
+//
+// Activations are f16 rows, cut into records of 128 inputs (a unit's) and 16
+// bytes: what a product with 1 + u/16 and 1 + u/256 owes to the constant part
+// is a multiple of the inputs' sum, so each record carries that sum (of the
+// rounded values, fp32).
 #pragma once
 
 #include "futr_internal.cuh"
@@ -11,11 +25,21 @@
 
 namespace futr {
 
-constexpr uint64_t kMoeMagic = 0x3145304d52545546ull;
+constexpr uint64_t kMoeMagic = 0x3245304d52545546ull;
 constexpr uint64_t kMoeWsMagic = 0x5745304d52545546ull;
 constexpr int kMoeMaxExperts = 256;
 constexpr int kMoeMaxTopK = 16;
 constexpr int kMoeMaxPairs = kMaxBatch * kMoeMaxTopK;
+
+// One record of an activation row: 128 f16 values; then two sums and two factors
+// (inputs 0..63 and 64..127).  Gate/up inputs: sum[0] is the sum of all 128, the
+// factor is the token's (MoeRoute::rms).  Down inputs: each half is divided by
+// the power of two at its largest value, factor[h], and has its own sum.
+constexpr int kRecHalves = 136;
+constexpr int kRecBytes = 2 * kRecHalves;
+struct MoeTail {
+  float sum[2], factor[2];
+};
 
 struct MoeHeader {
   uint64_t magic;
@@ -30,7 +54,7 @@ struct MoeRoute {
   int off[kMoeMaxExperts + 1];         // first pair of each
   int token[kMoeMaxPairs];             // token of each pair
   float weight[kMoeMaxPairs];          // its weight
-  float rms[kMaxBatch];                // RMSNorm factor of each token
+  float rms[kMaxBatch];                // RMSNorm factor of each token, times its inputs' factor
 };
 
 inline uint64_t moe_gu_bytes(const futr_moe_shape& s) {
@@ -55,7 +79,8 @@ struct MoeArgs {
   int* err;
   float* logits;                       // [T][E]
   MoeRoute* route;
-  __nv_bfloat16* act;                  // [pairs][I]
+  __half* xh;                          // [T][H / 128][136]: the tokens as f16 records
+  __half* act;                         // [pairs][I / 128][136]: the down product's inputs
   float* rec;                          // split records, two per CTA
   unsigned* cnt;                       // one counter per CTA, then the router's
   int n_cnt;
@@ -65,5 +90,9 @@ constexpr int kMoeRecFloats = kMaxBatch * kRowsPerBlock;   // one record: up to 
 
 int moe_ctas();   // most CTAs any launch uses on the current device
 cudaError_t launch_moe(const MoeArgs& a, cudaStream_t st);
+// Between a block's nibble order and this one, in place.
+cudaError_t launch_moe_place(uint8_t* units, size_t n_units, cudaStream_t st);
+cudaError_t launch_moe_unpack(int hidden, int inter, const uint8_t* gu, const uint8_t* down, int which, int8_t* codes,
+                              uint16_t* scales, cudaStream_t st);
 
 }  // namespace futr

@@ -62,8 +62,10 @@ void ws_layout(const futr_moe_shape& s, int max_batch, int ctas, futr_moe_ws* w)
   off = host::region_after(off, sizeof(MoeRoute));
   w->off_logits = off;
   off = host::region_after(off, (uint64_t)max_batch * s.n_experts * 4);
+  w->off_x = off;
+  off = host::region_after(off, (uint64_t)max_batch * (s.hidden / kGroup) * kRecBytes);
   w->off_act = off;
-  off = host::region_after(off, (uint64_t)max_batch * s.top_k * s.inter * 2);
+  off = host::region_after(off, (uint64_t)max_batch * s.top_k * (s.inter / kGroup) * kRecBytes);
   w->off_rec = off;
   w->bytes = host::region_after(off, (uint64_t)ctas * 2 * kMoeRecFloats * 4);
   w->blob_bytes = kHeaderBytes + expert_bytes(s) * s.n_experts;
@@ -71,9 +73,9 @@ void ws_layout(const futr_moe_shape& s, int max_batch, int ctas, futr_moe_ws* w)
 }
 
 int ws_guards(const futr_moe_ws& w, uint64_t* g) {
-  const uint64_t starts[] = {w.off_cnt, w.off_route, w.off_logits, w.off_act, w.off_rec, w.bytes};
+  const uint64_t starts[] = {w.off_cnt, w.off_route, w.off_logits, w.off_x, w.off_act, w.off_rec, w.bytes};
   std::memcpy(g, starts, sizeof(starts));
-  return 6;
+  return 7;
 }
 
 __global__ void moe_header_kernel(MoeHeader* dst, const MoeHeader h) { *dst = h; }
@@ -100,7 +102,8 @@ futr_status futr_moe_pack(const futr_moe_shape* shape, int32_t expert, const flo
     const cudaStream_t s = as_stream(stream);
     uint8_t* gu = at<uint8_t>(blob, kHeaderBytes + expert_bytes(*shape) * expert);
     if (launch_pack_expert(shape->hidden, shape->inter, wgate, wup, wdown, gain, gu, gu + moe_gu_bytes(*shape), s) !=
-        cudaSuccess)
+            cudaSuccess ||
+        launch_moe_place(gu, expert_bytes(*shape) / kUnitBytes, s) != cudaSuccess)
       return FUTR_ERR_CUDA;
     const MoeHeader h{kMoeMagic, 1, shape->hidden, shape->inter, shape->n_experts};
     moe_header_kernel<<<1, 1, 0, s>>>(at<MoeHeader>(blob, 0), h);
@@ -115,7 +118,7 @@ futr_status futr_moe_unpack(const futr_moe_shape* shape, const void* blob, int32
     if (!blob || !codes || !scales || expert < 0 || expert >= shape->n_experts) return FUTR_ERR_INVALID_ARG;
     if (which != FUTR_PROJ_GATE && which != FUTR_PROJ_UP && which != FUTR_PROJ_DOWN) return FUTR_ERR_INVALID_ARG;
     const uint8_t* gu = reinterpret_cast<const uint8_t*>(blob) + kHeaderBytes + expert_bytes(*shape) * expert;
-    return launch_unpack_expert(shape->hidden, shape->inter, gu, gu + moe_gu_bytes(*shape), which, codes, scales,
+    return launch_moe_unpack(shape->hidden, shape->inter, gu, gu + moe_gu_bytes(*shape), which, codes, scales,
                                 as_stream(stream)) == cudaSuccess
                ? FUTR_OK
                : FUTR_ERR_CUDA;
@@ -150,7 +153,7 @@ futr_status futr_moe_workspace_init(const futr_moe_shape* shape, int32_t max_bat
     const cudaStream_t s = as_stream(stream);
     // error words, counters and routing start at zero
     if (cudaMemsetAsync(mem, 0, w.off_logits, s) != cudaSuccess) return FUTR_ERR_CUDA;
-    uint64_t g[6];
+    uint64_t g[7];
     const int n = ws_guards(w, g);
     if (host::fill_guards_before(mem, g, n, s) != cudaSuccess) return FUTR_ERR_CUDA;
     *ws = w;
@@ -193,7 +196,8 @@ futr_status futr_moe_layer(const uint16_t* x, const float* gain, const uint16_t*
     a.n_cnt = ws->ctas;
     a.route = at<MoeRoute>(ws->base, ws->off_route);
     a.logits = at<float>(ws->base, ws->off_logits);
-    a.act = at<__nv_bfloat16>(ws->base, ws->off_act);
+    a.xh = at<__half>(ws->base, ws->off_x);
+    a.act = at<__half>(ws->base, ws->off_act);
     a.rec = at<float>(ws->base, ws->off_rec);
     return launch_moe(a, as_stream(stream)) == cudaSuccess ? FUTR_OK : FUTR_ERR_CUDA;
   });
@@ -204,7 +208,7 @@ futr_status futr_moe_check(const futr_moe_ws* ws, void* stream) {
     if (!ws_ok(ws)) return FUTR_ERR_INVALID_ARG;
     const cudaStream_t s = as_stream(stream);
     int* err = at<int>(ws->base, 0);
-    uint64_t g[6];
+    uint64_t g[7];
     const int n = ws_guards(*ws, g);
     if (host::check_guards_before(ws->base, g, n, err, s) != cudaSuccess) return FUTR_ERR_CUDA;
     int v[2] = {0, 0};

@@ -180,22 +180,6 @@ cudaError_t launch_pack_expert(int hidden, int inter, const float* wg, const flo
   return cudaSuccess;
 }
 
-cudaError_t launch_unpack_expert(int hidden, int inter, const uint8_t* gu, const uint8_t* down, int which,
-                                 int8_t* codes, uint16_t* scales, cudaStream_t st) {
-  UnpackArgs a{};
-  const bool is_down = which == FUTR_PROJ_DOWN;
-  a.map = which == FUTR_PROJ_GATE ? 1 : which == FUTR_PROJ_UP ? 2 : 0;
-  a.rows = is_down ? hidden : inter;
-  a.cols = is_down ? inter : hidden;
-  a.sec = is_down ? down : gu;
-  a.n_groups = a.cols / kGroup;
-  a.codes = codes;
-  a.scales = scales;
-  const size_t n = (size_t)a.rows * a.cols;
-  unpack_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
-  return cudaGetLastError();
-}
-
 cudaError_t launch_unpack(const futr_shape& s, const uint8_t* blob, int which, int8_t* codes,
                           uint16_t* scales, cudaStream_t st) {
   const BlobSections sec = blob_sections(s);
