@@ -477,7 +477,7 @@ typedef struct futr_moe_ws {
   int32_t max_batch, ctas, _pad;
   void* base;
   uint64_t bytes;
-  uint64_t off_cnt, off_route, off_logits, off_x, off_act, off_rec;
+  uint64_t off_cnt, off_rms, off_logits, off_x, off_act, off_rec;
   uint64_t blob_bytes;     /* size of the layer's packed experts */
   uint64_t magic;
 } futr_moe_ws;
@@ -511,8 +511,9 @@ futr_status futr_moe_workspace_init(const futr_moe_shape* shape, int32_t max_bat
  *   softmax probabilities w over all E experts, divided by their sum if renorm
  *   y = bf16(resid + sum_j w_j Wdown_j (silu(r W'gate_j x) * (r W'up_j x)))
  * x, y, resid: bf16 [batch][H], 16-byte aligned (y may be x or resid; resid may
- * be NULL).  The inputs of both products are fp16 (x divided by a power of two
- * near its RMS; w * silu * up by one near the largest of each 64), sums are fp32.  ids (int32) and weights (fp32)
+ * be NULL).  The inputs of both products are sums of e4m3 terms times a power of
+ * two for each 128 (gate/up: x to 8 bits, its own; w * silu * up for each 64, 12
+ * bits); all sums are fp32. ids (int32) and weights (fp32)
  * [batch][K], either may be NULL: the choice of each token, largest first.  A
  * token whose logits hold a NaN gets NaN weights.  A blob of another shape sets
  * FUTR_ERR_BAD_BLOB (see futr_moe_check).  Three kernels with programmatic

@@ -6,11 +6,13 @@
 //   y_t = resid_t + sum_j w_tj Wd_e (silu(r_t W'g_e x_t) * (r_t W'u_e x_t)),  e = e_tj
 //
 // Three kernels with programmatic dependent launch:
-//   router   a CTA per four experts and eight tokens, which also leaves its part
-//            of the tokens as f16; the CTA that arrives last picks the experts of
-//            every token and sorts the (token, expert) pairs by expert;
+//   router   the logits, a CTA per two experts and eight tokens, which also leaves
+//            its part of the tokens as f16;
 //   gate/up  streams the chosen experts' gate/up units once;
 //   down     streams their down units once, beginning before gate/up has ended.
+// Every CTA of the expert kernels picks the experts of all tokens from the logits
+// itself and sorts the (token, expert) pairs by expert: some 1.5 us on every SM
+// at once, less than one CTA takes to do it for the others and hand it over.
 // The expert kernels are bound by the weight stream.  All units of the chosen
 // experts form one run, cut into equal contiguous shares, one per CTA of a
 // grid that fills the GPU; the cut is made on the device from the routing.  A
@@ -47,8 +49,8 @@ namespace {
 constexpr int kMoeCW = 4;
 constexpr int kMoeThreads = (kMoeCW + 1) * 32;
 constexpr int kMoeMaxPerSm = 3;
-constexpr int kRouterThreads = 1024;
-constexpr int kRouterE = 4;        // experts of a router CTA
+constexpr int kRouterThreads = 512;
+constexpr int kRouterE = 2;        // experts of a router CTA
 constexpr int kRouterT = 8;        // its tokens
 constexpr int kRouterSlices = kRouterThreads / 32 / kRouterE;   // parts of the inputs: a warp's share
 constexpr unsigned long long kMoeWaitNs = 1000000000ull;
@@ -86,12 +88,6 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArgs a) {
   __shared__ float s_dot[kRouterE][kRouterSlices][kRouterT], s_sq[kRouterSlices][kRouterT];
   __shared__ float s_factor[kRouterT];
-  __shared__ int s_last;
-  __shared__ int s_id[kMoeMaxPairs];
-  __shared__ float s_w[kMoeMaxPairs];
-  __shared__ unsigned s_mask[kMoeMaxExperts];   // tokens of each expert
-  __shared__ int s_off[kMoeMaxExperts];
-  __shared__ int s_sum[2][kMoeMaxExperts / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();
@@ -175,7 +171,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
       if (el == 0) {
         const float f = pow2_at(sqrtf(mean));
         s_factor[t] = pow2_inverse(f);
-        if (et == 0) a.route->rms[t0 + t] = r * f;
+        if (et == 0) a.rms[t0 + t] = r * f;
       }
     }
   }
@@ -197,36 +193,51 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
         make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
     if (lane == 0) *reinterpret_cast<float4*>(rec + kGroup) = make_float4(sum, 0.f, 1.f, 1.f);
   }
-  __syncthreads();
-  if (tid == 0) {
-    s_last = atom_add_acq_rel_gpu(a.cnt + a.n_cnt, 1u) == gridDim.x * gridDim.y - 1 ? 1 : 0;
-    if (s_last) a.cnt[a.n_cnt] = 0u;
-  }
-  if (tid < kMoeMaxExperts) s_mask[tid] = 0u;
-  __syncthreads();
-  if (!s_last) return;
+}
 
-  // the choice of experts: a warp per token, expert lane + 32 i in v[i]
+// The routing, in shared memory.  A pair is one (token, chosen expert); pairs
+// are ordered by expert, then token.
+struct MoeRoute {
+  float weight[kMoeMaxPairs];                // of each pair
+  unsigned mask[kMoeMaxExperts];             // tokens of each expert
+  int n_active;                              // experts that some token chose
+  uint16_t off[kMoeMaxExperts + 1];          // first pair of each of them
+  uint16_t first[kMoeMaxExperts];            // first pair of each expert
+  uint8_t expert[kMoeMaxExperts];            // their ids, ascending
+  uint8_t token[kMoeMaxPairs];               // of each pair
+  uint8_t id[kMoeMaxPairs];                  // choices in the tokens' order
+};
+
+// From the logits, by all threads of the CTA.  Gate/up
+// also wants the weights, and one of its CTAs stores the choices.
+template <bool kWeights>
+__device__ __forceinline__ void make_route(const MoeArgs& a, MoeRoute& rt, bool store) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kV = kMoeMaxExperts / 32;
-  if (warp < a.T) {
-    const int t = warp;
+  for (int i = tid; i < kMoeMaxExperts; i += kMoeThreads) rt.mask[i] = 0u;
+  __syncthreads();
+  // a warp per token, expert lane + 32 i in v[i]
+  for (int t = warp; t < a.T; t += kMoeThreads / 32) {
     float v[kV], mx = -INFINITY, sum = 0.f;
     uint32_t key[kV];
     bool nan = false;
 #pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = lane + 32 * i < a.E ? __ldcg(a.logits + (size_t)t * a.E + lane + 32 * i) : -INFINITY;
+#pragma unroll
     for (int i = 0; i < kV; ++i) {
-      v[i] = lane + 32 * i < a.E ? __ldcg(a.logits + (size_t)t * a.E + lane + 32 * i) : -INFINITY;
       key[i] = order_key(v[i]);
       mx = fmaxf(mx, v[i]);
       nan |= v[i] != v[i];
     }
+    if (kWeights) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    nan = __any_sync(0xffffffffu, nan);
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      nan = __any_sync(0xffffffffu, nan);
 #pragma unroll
-    for (int i = 0; i < kV; ++i)
-      if (32 * i < a.E) sum += lane + 32 * i < a.E ? expf(v[i] - mx) : 0.f;
-    sum = warp_sum(sum);
+      for (int i = 0; i < kV; ++i)
+        if (32 * i < a.E) sum += lane + 32 * i < a.E ? expf(v[i] - mx) : 0.f;
+      sum = warp_sum(sum);
+    }
     unsigned taken = 0u;               // this lane's chosen experts
     float chosen = 0.f, total = 0.f;   // lane j: weight of the j-th choice
     int chosen_id = 0;
@@ -245,33 +256,46 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
         }
       const uint32_t best = __reduce_max_sync(0xffffffffu, bi == 0x7fffffff ? 0u : bk);
       const int id = __reduce_min_sync(0xffffffffu, bk == best ? bi : 0x7fffffff);
-      const float val = __shfl_sync(0xffffffffu, bv, id & 31);
       if ((id & 31) == lane) taken |= 1u << (id >> 5);
-      const float w = nan ? __int_as_float(0x7fc00000) : __fdiv_rn(expf(val - mx), sum);
-      total += w;
-      if (lane == j) {
-        chosen = w;
-        chosen_id = id;
+      if (kWeights) {
+        const float val = __shfl_sync(0xffffffffu, bv, id & 31);
+        const float w = nan ? __int_as_float(0x7fc00000) : __fdiv_rn(expf(val - mx), sum);
+        total += w;
+        if (lane == j) chosen = w;
       }
+      if (lane == j) chosen_id = id;
     }
-    if (a.renorm) chosen = __fdiv_rn(chosen, total);
+    if (kWeights && a.renorm) chosen = __fdiv_rn(chosen, total);
     if (lane < a.K) {
       const int p = t * a.K + lane;
-      s_id[p] = chosen_id;
-      s_w[p] = chosen;
-      atomicOr(&s_mask[chosen_id], 1u << t);
-      if (a.ids) a.ids[p] = chosen_id;
-      if (a.weights) a.weights[p] = chosen;
+      rt.id[p] = (uint8_t)chosen_id;
+      atomicOr(&rt.mask[chosen_id], 1u << t);
+      if (kWeights) {
+        rt.weight[p] = chosen;   // in the tokens' order so far
+        if (store && a.ids) a.ids[p] = chosen_id;
+        if (store && a.weights) a.weights[p] = chosen;
+      }
     }
   }
   __syncthreads();
-  // experts in use and the first pair of each: prefix sums over the experts
-  int n = 0, used = 0, pn = 0, pu = 0;
-  if (tid < kMoeMaxExperts) {
-    n = __popc(s_mask[tid]);
-    used = n > 0;
-    pn = n;
-    pu = used;
+  // (the pairs' weights change their order: read them before they are overwritten)
+  constexpr int kP = (kMoeMaxPairs + kMoeThreads - 1) / kMoeThreads;
+  float pw[kP];
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int p = tid + i * kMoeThreads;
+    pw[i] = kWeights && p < a.T * a.K ? rt.weight[p] : 0.f;
+  }
+  // experts in use and the first pair of each: prefix sums, eight experts a lane
+  if (warp == 0) {
+    int n = 0, used = 0;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const unsigned m = rt.mask[kV * lane + i];
+      n += __popc(m);
+      used += m != 0u;
+    }
+    int pn = n, pu = used;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, pn, o), y = __shfl_up_sync(0xffffffffu, pu, o);
@@ -281,34 +305,35 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
       }
     }
     if (lane == 31) {
-      s_sum[0][warp] = pn;
-      s_sum[1][warp] = pu;
+      rt.n_active = pu;
+      rt.off[pu] = (uint16_t)pn;
+    }
+    pn -= n;
+    pu -= used;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const unsigned m = rt.mask[kV * lane + i];
+      rt.first[kV * lane + i] = (uint16_t)pn;
+      if (m != 0u) {
+        rt.expert[pu] = (uint8_t)(kV * lane + i);
+        rt.off[pu] = (uint16_t)pn;
+        ++pu;
+      }
+      pn += __popc(m);
     }
   }
   __syncthreads();
-  if (tid < kMoeMaxExperts) {
-    int bn = 0, bu = 0;
-    for (int w = 0; w < warp; ++w) {
-      bn += s_sum[0][w];
-      bu += s_sum[1][w];
-    }
-    s_off[tid] = bn + pn - n;
-    if (used) {
-      a.route->expert[bu + pu - 1] = tid;
-      a.route->off[bu + pu - 1] = bn + pn - n;
-    }
-    if (tid == kMoeMaxExperts - 1) {
-      a.route->n_active = bu + pu;
-      a.route->off[bu + pu] = bn + pn;
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int p = tid + i * kMoeThreads;
+    if (p < a.T * a.K) {
+      const int t = p / a.K, id = rt.id[p];
+      const int at = rt.first[id] + __popc(rt.mask[id] & ((1u << t) - 1u));
+      rt.token[at] = (uint8_t)t;
+      if (kWeights) rt.weight[at] = pw[i];
     }
   }
   __syncthreads();
-  for (int p = tid; p < a.T * a.K; p += kRouterThreads) {
-    const int t = p / a.K, id = s_id[p];
-    const int at = s_off[id] + __popc(s_mask[id] & ((1u << t) - 1u));
-    a.route->token[at] = t;
-    a.route->weight[at] = s_w[p];
-  }
 }
 
 // ---------------------------------------------------------- expert kernels --
@@ -325,11 +350,16 @@ struct MoeLayout {
 // The four f16x2 registers of a word (see moe.cuh): rows g 1 + u/16, rows g + 8
 // 1 + u/256.
 __device__ __forceinline__ void place4(uint32_t w, uint32_t (&r)[4]) {
-  const uint32_t s = __byte_perm(w, w, 0x2301);
-  r[0] = (w & 0x03C003C0u) | 0x3C003C00u;
-  r[1] = (w & 0x003C003Cu) | 0x3C003C00u;
-  r[2] = (s & 0x03C003C0u) | 0x3C003C00u;
-  r[3] = (s & 0x003C003Cu) | 0x3C003C00u;
+  // "(a & b) | c" in one operation each; written out, because the compiler's own
+  // lowering of the expression takes two
+  asm("{\n\t.reg .b32 s;\n\t"
+      "prmt.b32 s, %4, %4, 0x2301;\n\t"
+      "lop3.b32 %0, %4, 0x03C003C0, %5, 0xEA;\n\t"
+      "lop3.b32 %1, %4, 0x003C003C, %5, 0xEA;\n\t"
+      "lop3.b32 %2, s, 0x03C003C0, %5, 0xEA;\n\t"
+      "lop3.b32 %3, s, 0x003C003C, %5, 0xEA;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w), "r"(0x3C003C00u));
 }
 constexpr float kBiasA = -1.5f, kBiasB = -1.03125f;   // -(16 + 8) / 16, -(256 + 8) / 256
 constexpr float kUnitA = 16.f, kUnitB = 256.f;
@@ -455,7 +485,7 @@ struct MoeRing {
 // only this warp touches these rows).
 template <int NT, int NTL, bool kDown>
 __device__ __forceinline__ void run_units(const MoeArgs& a, uint8_t* smem, float* red, uint64_t* full, uint64_t* empty,
-                                          volatile int* s_dead, const int* token, int n, int units, MoeRing& ring) {
+                                          volatile int* s_dead, const uint8_t* token, int n, int units, MoeRing& ring) {
   using Lay = MoeLayout<NTL>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t4 = lane & 3;
   // columns past n read column 0: they only feed MMA columns that are not stored
@@ -530,7 +560,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
   }
   __syncthreads();
   // Gate/up waits for the router, then lets down start.  Down starts once
-  // every gate/up CTA has passed its wait, so the routing is complete; its
+  // every gate/up CTA has passed its wait, so the logits are complete; its
   // weights do not depend on gate/up, only the activations do.
   if (!kDown) {
     pdl_wait();
@@ -538,7 +568,9 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
   } else {
     pdl_trigger();
   }
-  const MoeRoute* rt = a.route;
+  __shared__ MoeRoute s_route;
+  make_route<!kDown>(a, s_route, blockIdx.x == 0);
+  const MoeRoute* rt = &s_route;
   const MoeRun<kDown> run(a, rt->n_active);
   const int total = run.total();
   const int cta = blockIdx.x, ctas = min(total, (int)gridDim.x);
@@ -628,7 +660,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
         end = min(end, seg1);
         off = rt->off[ai];
         n = rt->off[ai + 1] - off;
-        const int* token = rt->token + off;
+        const uint8_t* token = rt->token + off;
         if (NT == 1 || n <= 8)
           run_units<1, NT, kDown>(a, smem, red, full, empty, s_dead, token, n, end - u, ring);
         else if (NT == 2 || n <= 16)
@@ -700,7 +732,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
         } else {
           // a warp per column: outputs 64 rb .. 64 rb + 63 of pair off + c, half a record
           for (int c = warp; c < cols; c += kMoeCW) {
-            const float r = rt->rms[rt->token[off + c]], wt = rt->weight[off + c];
+            const float r = a.rms[rt->token[off + c]], wt = rt->weight[off + c];
             float v[2], mx = 0.f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {

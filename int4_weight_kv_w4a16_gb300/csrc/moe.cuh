@@ -33,7 +33,7 @@ constexpr int kMoeMaxPairs = kMaxBatch * kMoeMaxTopK;
 
 // One record of an activation row: 128 f16 values; then two sums and two factors
 // (inputs 0..63 and 64..127).  Gate/up inputs: sum[0] is the sum of all 128, the
-// factor is the token's (MoeRoute::rms).  Down inputs: each half is divided by
+// factor is the token's (MoeArgs::rms).  Down inputs: each half is divided by
 // the power of two at its largest value, factor[h], and has its own sum.
 constexpr int kRecHalves = 136;
 constexpr int kRecBytes = 2 * kRecHalves;
@@ -44,17 +44,6 @@ struct MoeTail {
 struct MoeHeader {
   uint64_t magic;
   int32_t version, hidden, inter, n_experts;
-};
-
-// What the router leaves for the expert kernels.  A pair is one (token, chosen
-// expert); pairs are ordered by expert, then token.
-struct MoeRoute {
-  int n_active;                        // experts that some token chose
-  int expert[kMoeMaxExperts];          // their ids, ascending
-  int off[kMoeMaxExperts + 1];         // first pair of each
-  int token[kMoeMaxPairs];             // token of each pair
-  float weight[kMoeMaxPairs];          // its weight
-  float rms[kMaxBatch];                // RMSNorm factor of each token, times its inputs' factor
 };
 
 inline uint64_t moe_gu_bytes(const futr_moe_shape& s) {
@@ -78,12 +67,11 @@ struct MoeArgs {
   float* weights;                      // [T][K] or nullptr
   int* err;
   float* logits;                       // [T][E]
-  MoeRoute* route;
+  float* rms;                          // [T] RMSNorm factor times the factor of the token's f16 records
   __half* xh;                          // [T][H / 128][136]: the tokens as f16 records
   __half* act;                         // [pairs][I / 128][136]: the down product's inputs
   float* rec;                          // split records, two per CTA
-  unsigned* cnt;                       // one counter per CTA, then the router's
-  int n_cnt;
+  unsigned* cnt;                       // arrival counters, one per CTA
 };
 
 constexpr int kMoeRecFloats = kMaxBatch * kRowsPerBlock;   // one record: up to 32 columns of 128 rows

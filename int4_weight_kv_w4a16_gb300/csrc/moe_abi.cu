@@ -57,9 +57,9 @@ void ws_layout(const futr_moe_shape& s, int max_batch, int ctas, futr_moe_ws* w)
   w->ctas = ctas;
   uint64_t off = host::region_after(0, 16);   // error words
   w->off_cnt = off;
-  off = host::region_after(off, (uint64_t)(ctas + 1) * 4);
-  w->off_route = off;
-  off = host::region_after(off, sizeof(MoeRoute));
+  off = host::region_after(off, (uint64_t)ctas * 4);
+  w->off_rms = off;
+  off = host::region_after(off, (uint64_t)max_batch * 4);
   w->off_logits = off;
   off = host::region_after(off, (uint64_t)max_batch * s.n_experts * 4);
   w->off_x = off;
@@ -73,7 +73,7 @@ void ws_layout(const futr_moe_shape& s, int max_batch, int ctas, futr_moe_ws* w)
 }
 
 int ws_guards(const futr_moe_ws& w, uint64_t* g) {
-  const uint64_t starts[] = {w.off_cnt, w.off_route, w.off_logits, w.off_x, w.off_act, w.off_rec, w.bytes};
+  const uint64_t starts[] = {w.off_cnt, w.off_rms, w.off_logits, w.off_x, w.off_act, w.off_rec, w.bytes};
   std::memcpy(g, starts, sizeof(starts));
   return 7;
 }
@@ -151,8 +151,8 @@ futr_status futr_moe_workspace_init(const futr_moe_shape* shape, int32_t max_bat
     ws_layout(*shape, max_batch, moe_ctas(), &w);
     w.base = mem;
     const cudaStream_t s = as_stream(stream);
-    // error words, counters and routing start at zero
-    if (cudaMemsetAsync(mem, 0, w.off_logits, s) != cudaSuccess) return FUTR_ERR_CUDA;
+    // error words and counters start at zero
+    if (cudaMemsetAsync(mem, 0, w.off_rms, s) != cudaSuccess) return FUTR_ERR_CUDA;
     uint64_t g[7];
     const int n = ws_guards(w, g);
     if (host::fill_guards_before(mem, g, n, s) != cudaSuccess) return FUTR_ERR_CUDA;
@@ -193,8 +193,7 @@ futr_status futr_moe_layer(const uint16_t* x, const float* gain, const uint16_t*
     a.weights = weights;
     a.err = at<int>(ws->base, 0);
     a.cnt = at<unsigned>(ws->base, ws->off_cnt);
-    a.n_cnt = ws->ctas;
-    a.route = at<MoeRoute>(ws->base, ws->off_route);
+    a.rms = at<float>(ws->base, ws->off_rms);
     a.logits = at<float>(ws->base, ws->off_logits);
     a.xh = at<__half>(ws->base, ws->off_x);
     a.act = at<__half>(ws->base, ws->off_act);
@@ -217,7 +216,7 @@ futr_status futr_moe_check(const futr_moe_ws* ws, void* stream) {
     if (v[0] == 0 && v[1] == 0) return FUTR_OK;
     if (cudaMemsetAsync(err, 0, 16, s) != cudaSuccess) return FUTR_ERR_CUDA;
     // a launch that gave up left its arrival counters mid-count
-    if (v[1] != 0 && cudaMemsetAsync(at<uint8_t>(ws->base, ws->off_cnt), 0, (size_t)(ws->ctas + 1) * 4, s) != cudaSuccess)
+    if (v[1] != 0 && cudaMemsetAsync(at<uint8_t>(ws->base, ws->off_cnt), 0, (size_t)ws->ctas * 4, s) != cudaSuccess)
       return FUTR_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return FUTR_ERR_CUDA;
     return v[0] != 0 ? v[0] : FUTR_ERR_TIMEOUT;

@@ -75,7 +75,7 @@ class futr_moe_shape(C.Structure):
 
 class futr_moe_ws(C.Structure):
     _fields_ = [("shape", futr_moe_shape), ("max_batch", C.c_int32), ("ctas", C.c_int32), ("_pad", C.c_int32),
-                ("base", C.c_void_p), ("bytes", C.c_uint64), ("off_cnt", C.c_uint64), ("off_route", C.c_uint64),
+                ("base", C.c_void_p), ("bytes", C.c_uint64), ("off_cnt", C.c_uint64), ("off_rms", C.c_uint64),
                 ("off_logits", C.c_uint64), ("off_x", C.c_uint64), ("off_act", C.c_uint64), ("off_rec", C.c_uint64), ("blob_bytes", C.c_uint64),
                 ("magic", C.c_uint64)]
 
