@@ -7,12 +7,13 @@
 //
 // Three kernels with programmatic dependent launch:
 //   router   the logits, a CTA per two experts and eight tokens, which also leaves
-//            its part of the tokens as f16;
+//            its part of the tokens as f16; the CTA that arrives last for its eight
+//            tokens picks their experts, a warp per token;
 //   gate/up  streams the chosen experts' gate/up units once;
 //   down     streams their down units once, beginning before gate/up has ended.
-// Every CTA of the expert kernels picks the experts of all tokens from the logits
-// itself and sorts the (token, expert) pairs by expert: some 1.5 us on every SM
-// at once, less than one CTA takes to do it for the others and hand it over.
+// Every CTA of the expert kernels sorts the (token, expert) pairs by expert itself,
+// on every SM at once: less time than one CTA takes to do it for the others and
+// hand it over.
 // The expert kernels are bound by the weight stream.  All units of the chosen
 // experts form one run, cut into equal contiguous shares, one per CTA of a
 // grid that fills the GPU; the cut is made on the device from the routing.  A
@@ -51,7 +52,6 @@ constexpr int kMoeThreads = (kMoeCW + 1) * 32;
 constexpr int kMoeMaxPerSm = 3;
 constexpr int kRouterThreads = 512;
 constexpr int kRouterE = 2;        // experts of a router CTA
-constexpr int kRouterT = 8;        // its tokens
 constexpr int kRouterSlices = kRouterThreads / 32 / kRouterE;   // parts of the inputs: a warp's share
 constexpr unsigned long long kMoeWaitNs = 1000000000ull;
 
@@ -78,16 +78,78 @@ __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float(
 
 // ------------------------------------------------------------------ router --
 
-// Floats in ascending order as unsigned integers in ascending order (NaN: below -inf).
+// Floats in ascending order as unsigned integers in ascending order above 0 (NaN: below -inf).
 __device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0u;
+  if (v != v) return 1u;
   const uint32_t u = __float_as_uint(v + 0.f);   // -0 counts as 0
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// The experts of token t (a warp): the K largest logits, equal ones by the lowest
+// index, and their weights.  Expert lane + 32 i in v[i].
+__device__ __forceinline__ void pick_experts(const MoeArgs& a, int t) {
+  constexpr int kV = kMoeMaxExperts / 32;
+  const int lane = threadIdx.x & 31;
+  float v[kV];
+  uint32_t key[kV];   // the order of v; 0: taken, absent
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) v[i] = lane + 32 * i < a.E ? __ldcg(a.logits + (size_t)t * a.E + lane + 32 * i) : 0.f;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    key[i] = lane + 32 * i < a.E ? order_key(v[i]) : 0u;
+    nan |= v[i] != v[i];
+  }
+  nan = __any_sync(0xffffffffu, nan);
+  float mine = 0.f, top = 0.f;   // lane j: the j-th choice
+  int mine_id = 0;
+#pragma unroll 1
+  for (int j = 0; j < a.K; ++j) {
+    uint32_t bk = key[0];
+    float bv = v[0];
+    int bi = 0;
+#pragma unroll
+    for (int i = 1; i < kV; ++i)
+      if (32 * i < a.E && key[i] > bk) {
+        bk = key[i];
+        bv = v[i];
+        bi = i;
+      }
+    const uint32_t best = __reduce_max_sync(0xffffffffu, bk);
+    const int id = __reduce_min_sync(0xffffffffu, bk == best ? lane + 32 * bi : 0x7fffffff);
+    const float val = __shfl_sync(0xffffffffu, bv, id & 31);
+    if ((id & 31) == lane) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+        if (i == id >> 5) key[i] = 0u;
+    }
+    if (j == 0) top = val;
+    if (lane == j) {
+      mine = val;
+      mine_id = id;
+    }
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kV; ++i)
+    if (32 * i < a.E) sum += lane + 32 * i < a.E ? expf(v[i] - top) : 0.f;
+  sum = warp_sum(sum);
+  float w = lane < a.K ? __fdiv_rn(expf(mine - top), sum) : 0.f;
+  if (a.renorm) w = __fdiv_rn(w, warp_sum(w));
+  if (nan) w = __int_as_float(0x7fc00000);
+  if (lane < a.K) {
+    const int p = t * a.K + lane;
+    a.choice[p] = mine_id;
+    a.share[p] = w;
+    if (a.ids) a.ids[p] = mine_id;
+    if (a.weights) a.weights[p] = w;
+  }
 }
 
 __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArgs a) {
   __shared__ float s_dot[kRouterE][kRouterSlices][kRouterT], s_sq[kRouterSlices][kRouterT];
   __shared__ float s_factor[kRouterT];
+  __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();
@@ -193,146 +255,85 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
         make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
     if (lane == 0) *reinterpret_cast<float4*>(rec + kGroup) = make_float4(sum, 0.f, 1.f, 1.f);
   }
+  // the last CTA of these tokens picks their experts
+  __syncthreads();
+  if (tid == 0) {
+    s_last = atom_add_acq_rel_gpu(a.cnt + blockIdx.y, 1u) == gridDim.x - 1 ? 1 : 0;
+    if (s_last) a.cnt[blockIdx.y] = 0u;
+  }
+  __syncthreads();
+  if (s_last && warp < nt) pick_experts(a, t0 + warp);
 }
 
 // The routing, in shared memory.  A pair is one (token, chosen expert); pairs
 // are ordered by expert, then token.
 struct MoeRoute {
-  float weight[kMoeMaxPairs];                // of each pair
   unsigned mask[kMoeMaxExperts];             // tokens of each expert
   int n_active;                              // experts that some token chose
   uint16_t off[kMoeMaxExperts + 1];          // first pair of each of them
   uint16_t first[kMoeMaxExperts];            // first pair of each expert
-  uint8_t expert[kMoeMaxExperts];            // their ids, ascending
+  uint16_t pick[kMoeMaxPairs];               // of each pair: its place in the choices
+  uint8_t expert[kMoeMaxExperts];            // experts in use, ascending
   uint8_t token[kMoeMaxPairs];               // of each pair
-  uint8_t id[kMoeMaxPairs];                  // choices in the tokens' order
 };
 
-// From the logits, by all threads of the CTA.  Gate/up
-// also wants the weights, and one of its CTAs stores the choices.
-template <bool kWeights>
-__device__ __forceinline__ void make_route(const MoeArgs& a, MoeRoute& rt, bool store) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kV = kMoeMaxExperts / 32;
-  for (int i = tid; i < kMoeMaxExperts; i += kMoeThreads) rt.mask[i] = 0u;
-  __syncthreads();
-  // a warp per token, expert lane + 32 i in v[i]
-  for (int t = warp; t < a.T; t += kMoeThreads / 32) {
-    float v[kV], mx = -INFINITY, sum = 0.f;
-    uint32_t key[kV];
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) v[i] = lane + 32 * i < a.E ? __ldcg(a.logits + (size_t)t * a.E + lane + 32 * i) : -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      key[i] = order_key(v[i]);
-      mx = fmaxf(mx, v[i]);
-      nan |= v[i] != v[i];
-    }
-    if (kWeights) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      nan = __any_sync(0xffffffffu, nan);
-#pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if (32 * i < a.E) sum += lane + 32 * i < a.E ? expf(v[i] - mx) : 0.f;
-      sum = warp_sum(sum);
-    }
-    unsigned taken = 0u;               // this lane's chosen experts
-    float chosen = 0.f, total = 0.f;   // lane j: weight of the j-th choice
-    int chosen_id = 0;
-#pragma unroll 1
-    for (int j = 0; j < a.K; ++j) {
-      // largest key, then lowest index, among the experts not taken
-      uint32_t bk = 0u;
-      int bi = 0x7fffffff;
-      float bv = 0.f;
-#pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if (lane + 32 * i < a.E && !((taken >> i) & 1u) && (bi == 0x7fffffff || key[i] > bk)) {
-          bk = key[i];
-          bi = lane + 32 * i;
-          bv = v[i];
-        }
-      const uint32_t best = __reduce_max_sync(0xffffffffu, bi == 0x7fffffff ? 0u : bk);
-      const int id = __reduce_min_sync(0xffffffffu, bk == best ? bi : 0x7fffffff);
-      if ((id & 31) == lane) taken |= 1u << (id >> 5);
-      if (kWeights) {
-        const float val = __shfl_sync(0xffffffffu, bv, id & 31);
-        const float w = nan ? __int_as_float(0x7fc00000) : __fdiv_rn(expf(val - mx), sum);
-        total += w;
-        if (lane == j) chosen = w;
-      }
-      if (lane == j) chosen_id = id;
-    }
-    if (kWeights && a.renorm) chosen = __fdiv_rn(chosen, total);
-    if (lane < a.K) {
-      const int p = t * a.K + lane;
-      rt.id[p] = (uint8_t)chosen_id;
-      atomicOr(&rt.mask[chosen_id], 1u << t);
-      if (kWeights) {
-        rt.weight[p] = chosen;   // in the tokens' order so far
-        if (store && a.ids) a.ids[p] = chosen_id;
-        if (store && a.weights) a.weights[p] = chosen;
-      }
-    }
-  }
-  __syncthreads();
-  // (the pairs' weights change their order: read them before they are overwritten)
-  constexpr int kP = (kMoeMaxPairs + kMoeThreads - 1) / kMoeThreads;
-  float pw[kP];
+// From the choices, by all threads of the CTA.
+__device__ __forceinline__ void make_route(const MoeArgs& a, MoeRoute& rt) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pairs = a.T * a.K;
+  constexpr int kP = (kMoeMaxPairs + kMoeThreads - 1) / kMoeThreads, kV = kMoeMaxExperts / 32;
+  int id[kP], t[kP];
 #pragma unroll
   for (int i = 0; i < kP; ++i) {
     const int p = tid + i * kMoeThreads;
-    pw[i] = kWeights && p < a.T * a.K ? rt.weight[p] : 0.f;
+    id[i] = p < pairs ? __ldcg(a.choice + p) : 0;
+    t[i] = p / a.K;
   }
+  for (int i = tid; i < kMoeMaxExperts; i += kMoeThreads) rt.mask[i] = 0u;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kP; ++i)
+    if (tid + i * kMoeThreads < pairs) atomicOr(&rt.mask[id[i]], 1u << t[i]);
+  __syncthreads();
   // experts in use and the first pair of each: prefix sums, eight experts a lane
   if (warp == 0) {
+    unsigned m[kV];
     int n = 0, used = 0;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-      const unsigned m = rt.mask[kV * lane + i];
-      n += __popc(m);
-      used += m != 0u;
+      m[i] = rt.mask[kV * lane + i];
+      n += __popc(m[i]);
+      used += m[i] != 0u;
     }
-    int pn = n, pu = used;
+    int both = n | (used << 16);   // at most 512 and 256
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, pn, o), y = __shfl_up_sync(0xffffffffu, pu, o);
-      if (lane >= o) {
-        pn += x;
-        pu += y;
-      }
+      const int x = __shfl_up_sync(0xffffffffu, both, o);
+      if (lane >= o) both += x;
     }
     if (lane == 31) {
-      rt.n_active = pu;
-      rt.off[pu] = (uint16_t)pn;
+      rt.n_active = both >> 16;
+      rt.off[both >> 16] = (uint16_t)(both & 0xffff);
     }
-    pn -= n;
-    pu -= used;
+    int pn = (both & 0xffff) - n, pu = (both >> 16) - used;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-      const unsigned m = rt.mask[kV * lane + i];
       rt.first[kV * lane + i] = (uint16_t)pn;
-      if (m != 0u) {
+      if (m[i] != 0u) {
         rt.expert[pu] = (uint8_t)(kV * lane + i);
         rt.off[pu] = (uint16_t)pn;
         ++pu;
       }
-      pn += __popc(m);
+      pn += __popc(m[i]);
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kP; ++i) {
-    const int p = tid + i * kMoeThreads;
-    if (p < a.T * a.K) {
-      const int t = p / a.K, id = rt.id[p];
-      const int at = rt.first[id] + __popc(rt.mask[id] & ((1u << t) - 1u));
-      rt.token[at] = (uint8_t)t;
-      if (kWeights) rt.weight[at] = pw[i];
+  for (int i = 0; i < kP; ++i)
+    if (tid + i * kMoeThreads < pairs) {
+      const int at = rt.first[id[i]] + __popc(rt.mask[id[i]] & ((1u << t[i]) - 1u));
+      rt.token[at] = (uint8_t)t[i];
+      rt.pick[at] = (uint16_t)(tid + i * kMoeThreads);
     }
-  }
   __syncthreads();
 }
 
@@ -472,6 +473,27 @@ struct MoeRun {
   }
 };
 
+// The run cut into shares, one per CTA: the first `rem` of per + 1 units, the
+// others of per.  Whole items where that costs at most a few units more than equal
+// shares: an item that two CTAs share costs both a record and an arrival, about
+// the time of eight units (8.4 KB each at a CTA's part of the memory bandwidth).
+struct MoeCut {
+  int use, per, rem, len;   // len: units that a share is a multiple of
+  __device__ __forceinline__ MoeCut(int total, int item_len, int ctas) {
+    const int items = total / item_len, most = (items + ctas - 1) / ctas;
+    len = (long long)most * item_len * ctas <= total + 8LL * ctas ? item_len : 1;
+    const int n = total / len;
+    use = min(n, ctas);
+    per = n / use;
+    rem = n - per * use;
+  }
+  __device__ __forceinline__ int begin(int cta) const { return (per * cta + min(cta, rem)) * len; }
+  __device__ __forceinline__ int owner(int u) const {
+    const int n = u / len, big = (per + 1) * rem;
+    return n < big ? n / (per + 1) : rem + (n - big) / per;
+  }
+};
+
 // A CTA's place in its ring of stages.
 struct MoeRing {
   int slot;
@@ -560,7 +582,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
   }
   __syncthreads();
   // Gate/up waits for the router, then lets down start.  Down starts once
-  // every gate/up CTA has passed its wait, so the logits are complete; its
+  // every gate/up CTA has passed its wait, so the choices are complete; its
   // weights do not depend on gate/up, only the activations do.
   if (!kDown) {
     pdl_wait();
@@ -569,13 +591,14 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
     pdl_trigger();
   }
   __shared__ MoeRoute s_route;
-  make_route<!kDown>(a, s_route, blockIdx.x == 0);
+  make_route(a, s_route);
   const MoeRoute* rt = &s_route;
   const MoeRun<kDown> run(a, rt->n_active);
   const int total = run.total();
-  const int cta = blockIdx.x, ctas = min(total, (int)gridDim.x);
-  if (cta >= ctas) return;
-  const int u0 = (int)((long long)total * cta / ctas), u1 = (int)((long long)total * (cta + 1) / ctas);
+  const MoeCut cut(total, run.item_len, (int)gridDim.x);
+  const int cta = blockIdx.x;
+  if (cta >= cut.use) return;
+  const int u0 = cut.begin(cta), u1 = cut.begin(cta + 1);
 
   if (warp == kMoeCW) {
     // ---------------------------------------------------------- producer --
@@ -681,10 +704,10 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
           reinterpret_cast<float4*>(rec)[i] = *reinterpret_cast<const float4*>(red + c * kRedLd + 4 * q);
         }
         moe_sync();
-        const int c0 = (int)(((long long)(i0 + 1) * ctas - 1) / total), c1 = (int)(((long long)i1 * ctas - 1) / total);
+        const int c0 = cut.owner(i0), c1 = cut.owner(i1 - 1);
         if (tid == 0) {
-          *s_last = atom_add_acq_rel_gpu(&a.cnt[c0], 1u) == (unsigned)(c1 - c0) ? 1 : 0;
-          if (*s_last) a.cnt[c0] = 0u;
+          *s_last = atom_add_acq_rel_gpu(&a.cnt[kRouterTiles + c0], 1u) == (unsigned)(c1 - c0) ? 1 : 0;
+          if (*s_last) a.cnt[kRouterTiles + c0] = 0u;
         }
         moe_sync();
         write = *s_last != 0;
@@ -732,7 +755,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
         } else {
           // a warp per column: outputs 64 rb .. 64 rb + 63 of pair off + c, half a record
           for (int c = warp; c < cols; c += kMoeCW) {
-            const float r = a.rms[rt->token[off + c]], wt = rt->weight[off + c];
+            const float r = a.rms[rt->token[off + c]], wt = a.share[rt->pick[off + c]];
             float v[2], mx = 0.f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {

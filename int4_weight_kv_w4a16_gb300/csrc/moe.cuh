@@ -71,9 +71,13 @@ struct MoeArgs {
   __half* xh;                          // [T][H / 128][136]: the tokens as f16 records
   __half* act;                         // [pairs][I / 128][136]: the down product's inputs
   float* rec;                          // split records, two per CTA
-  unsigned* cnt;                       // arrival counters, one per CTA
+  int* choice;                         // [T][K] the router's choices
+  float* share;                        // [T][K] and their weights
+  unsigned* cnt;                       // arrival counters: kRouterTiles of the router, then one per CTA
 };
 
+constexpr int kRouterT = 8;                                 // tokens of a router CTA
+constexpr int kRouterTiles = kMaxBatch / kRouterT;
 constexpr int kMoeRecFloats = kMaxBatch * kRowsPerBlock;   // one record: up to 32 columns of 128 rows
 
 int moe_ctas();   // most CTAs any launch uses on the current device

@@ -57,9 +57,9 @@ void ws_layout(const futr_moe_shape& s, int max_batch, int ctas, futr_moe_ws* w)
   w->ctas = ctas;
   uint64_t off = host::region_after(0, 16);   // error words
   w->off_cnt = off;
-  off = host::region_after(off, (uint64_t)ctas * 4);
+  off = host::region_after(off, (uint64_t)(ctas + kRouterTiles) * 4);
   w->off_rms = off;
-  off = host::region_after(off, (uint64_t)max_batch * 4);
+  off = host::region_after(off, (uint64_t)max_batch * (1 + 2 * s.top_k) * 4);   // factors, choices, weights
   w->off_logits = off;
   off = host::region_after(off, (uint64_t)max_batch * s.n_experts * 4);
   w->off_x = off;
@@ -194,6 +194,8 @@ futr_status futr_moe_layer(const uint16_t* x, const float* gain, const uint16_t*
     a.err = at<int>(ws->base, 0);
     a.cnt = at<unsigned>(ws->base, ws->off_cnt);
     a.rms = at<float>(ws->base, ws->off_rms);
+    a.share = a.rms + ws->max_batch;
+    a.choice = reinterpret_cast<int*>(a.share + (size_t)ws->max_batch * s.top_k);
     a.logits = at<float>(ws->base, ws->off_logits);
     a.xh = at<__half>(ws->base, ws->off_x);
     a.act = at<__half>(ws->base, ws->off_act);
@@ -216,7 +218,7 @@ futr_status futr_moe_check(const futr_moe_ws* ws, void* stream) {
     if (v[0] == 0 && v[1] == 0) return FUTR_OK;
     if (cudaMemsetAsync(err, 0, 16, s) != cudaSuccess) return FUTR_ERR_CUDA;
     // a launch that gave up left its arrival counters mid-count
-    if (v[1] != 0 && cudaMemsetAsync(at<uint8_t>(ws->base, ws->off_cnt), 0, (size_t)ws->ctas * 4, s) != cudaSuccess)
+    if (v[1] != 0 && cudaMemsetAsync(at<uint8_t>(ws->base, ws->off_cnt), 0, (size_t)(ws->ctas + kRouterTiles) * 4, s) != cudaSuccess)
       return FUTR_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return FUTR_ERR_CUDA;
     return v[0] != 0 ? v[0] : FUTR_ERR_TIMEOUT;
