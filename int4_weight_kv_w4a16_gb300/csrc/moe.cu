@@ -269,15 +269,18 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
 // are ordered by expert, then token.
 struct MoeRoute {
   unsigned mask[kMoeMaxExperts];             // tokens of each expert
-  int n_active;                              // experts that some token chose
-  uint16_t off[kMoeMaxExperts + 1];          // first pair of each of them
+  // the runs of at most C pairs of one expert: an expert of more pairs has several
+  int n_active;
+  uint16_t off[kMoeMaxPairs + 1];            // first pair of each
   uint16_t first[kMoeMaxExperts];            // first pair of each expert
   uint16_t pick[kMoeMaxPairs];               // of each pair: its place in the choices
-  uint8_t expert[kMoeMaxExperts];            // experts in use, ascending
+  uint8_t expert[kMoeMaxPairs];              // its expert, ascending
   uint8_t token[kMoeMaxPairs];               // of each pair
 };
 
-// From the choices, by all threads of the CTA.
+// From the choices, by all threads of the CTA.  C: columns that one pass over an
+// expert's units takes.
+template <int C>
 __device__ __forceinline__ void make_route(const MoeArgs& a, MoeRoute& rt) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pairs = a.T * a.K;
   constexpr int kP = (kMoeMaxPairs + kMoeThreads - 1) / kMoeThreads, kV = kMoeMaxExperts / 32;
@@ -302,9 +305,9 @@ __device__ __forceinline__ void make_route(const MoeArgs& a, MoeRoute& rt) {
     for (int i = 0; i < kV; ++i) {
       m[i] = rt.mask[kV * lane + i];
       n += __popc(m[i]);
-      used += m[i] != 0u;
+      used += (__popc(m[i]) + C - 1) / C;
     }
-    int both = n | (used << 16);   // at most 512 and 256
+    int both = n | (used << 16);   // at most 512 each
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, both, o);
@@ -318,12 +321,13 @@ __device__ __forceinline__ void make_route(const MoeArgs& a, MoeRoute& rt) {
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       rt.first[kV * lane + i] = (uint16_t)pn;
-      if (m[i] != 0u) {
+      const int cnt = __popc(m[i]);
+      for (int c = 0; c < cnt; c += C) {
         rt.expert[pu] = (uint8_t)(kV * lane + i);
-        rt.off[pu] = (uint16_t)pn;
+        rt.off[pu] = (uint16_t)(pn + c);
         ++pu;
       }
-      pn += __popc(m[i]);
+      pn += cnt;
     }
   }
   __syncthreads();
@@ -341,10 +345,11 @@ __device__ __forceinline__ void make_route(const MoeArgs& a, MoeRoute& rt) {
 
 template <int NT>
 struct MoeLayout {
-  static constexpr int kRing = NT == 4 ? 5 : 6;                  // two CTAs an SM at the least
+  // three CTAs an SM; with 32 columns two
+  static constexpr int kRing = NT == 1 ? 6 : NT == 2 ? 4 : 5;
   static constexpr int kStage = kUnitBytes + 8 * NT * kRecBytes;  // unit, then [8 NT] records
-  static constexpr int kRed = kRing * kStage;                    // [8 NT][kRedLd] fp32
-  static constexpr int kBar = kRed + 8 * NT * kRedLd * 4;
+  static constexpr int kRed = kRing * kStage;                    // [columns, down: tokens][kRedLd] fp32
+  static constexpr int kBar = kRed + (NT == 1 ? 8 : kMaxBatch) * kRedLd * 4;
   static constexpr int kBytes = kBar + 2 * kRing * 8 + 16;
 };
 
@@ -559,7 +564,7 @@ __device__ __forceinline__ void run_units(const MoeArgs& a, uint8_t* smem, float
 }
 
 template <int NT, bool kDown>
-__global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kernel(const MoeArgs a) {
+__global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kernel(const MoeArgs a) {
   using Lay = MoeLayout<NT>;
   constexpr int kMoeRing = Lay::kRing;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -591,7 +596,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 1 ? 3 : 2) moe_expert_kerne
     pdl_trigger();
   }
   __shared__ MoeRoute s_route;
-  make_route(a, s_route);
+  make_route<8 * NT>(a, s_route);
   const MoeRoute* rt = &s_route;
   const MoeRun<kDown> run(a, rt->n_active);
   const int total = run.total();
@@ -916,9 +921,12 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t st) {
   e = moe_go(moe_router_kernel, dim3((unsigned)((a.E + kRouterE - 1) / kRouterE), (unsigned)((a.T + kRouterT - 1) / kRouterT)),
              kRouterThreads, 0, st, a);
   if (e != cudaSuccess) return e;
-  // an expert has at most T tokens
+  // Columns of a pass: an expert has at most T tokens.  Above 16, passes of 16 (three
+  // CTAs an SM) unless experts have more than 8 tokens on average, where many would
+  // have to be streamed twice: 32 tokens through 2 of 8 experts take
+  // 194 us in passes of 16 and 229 us in passes of 32.
   if (a.T <= 8) return launch_experts<1>(a, dev, st);
-  if (a.T <= 16) return launch_experts<2>(a, dev, st);
+  if (a.T <= 16 || a.T * a.K <= 8 * a.E) return launch_experts<2>(a, dev, st);
   return launch_experts<4>(a, dev, st);
 }
 
