@@ -14,7 +14,7 @@
 // Every CTA of the expert kernels sorts the (token, expert) pairs by expert itself,
 // on every SM at once: less time than one CTA takes to do it for the others and
 // hand it over.
-// The expert kernels are bound by the weight stream.  All units of the chosen
+// Above 8 tokens a fourth adds down's parts.  The expert kernels are bound by the weight stream.  All units of the chosen
 // experts form one run, cut into equal contiguous shares, one per CTA of a
 // grid that fills the GPU; the cut is made on the device from the routing.  A
 // unit (128 rows x 128 inputs) comes by one bulk copy, the record of each of the
@@ -499,6 +499,11 @@ struct MoeCut {
   }
 };
 
+// More than 8 tokens: the records of a down row block (14 of 16 KB at 32 tokens on
+// 152 SMs) are added by a kernel of their own, by 8 tokens; the one CTA that arrives
+// last would read them alone, for longer than a launch takes.
+__host__ __device__ inline bool sums_apart(int T) { return T > 8; }
+
 // A CTA's place in its ring of stages.
 struct MoeRing {
   int slot;
@@ -561,6 +566,38 @@ __device__ __forceinline__ void run_units(const MoeArgs& a, uint8_t* smem, float
       }
     }
   __syncwarp();
+}
+
+__device__ __forceinline__ uint2 out4(const MoeArgs& a, size_t o, float4 v) {
+  if (a.resid) {
+    const uint2 ru = *reinterpret_cast<const uint2*>(a.resid + o);
+    v.x += __uint_as_float(ru.x << 16);
+    v.y += __uint_as_float(ru.x & 0xffff0000u);
+    v.z += __uint_as_float(ru.y << 16);
+    v.w += __uint_as_float(ru.y & 0xffff0000u);
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// Records r0 and rn[0 .. nc - 1], float4 i of each, added in this order.
+__device__ __forceinline__ float4 sum_parts(const float4* r0, const float4* rn, int nc, int i) {
+  constexpr size_t step = (size_t)2 * kMoeRecFloats / 4;
+  constexpr int kU = 8;   // records in flight
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int k = -1; k < nc; k += kU) {
+    float4 v[kU];
+#pragma unroll
+    for (int j = 0; j < kU; ++j)
+      if (k + j < nc) v[j] = __ldcg(k + j < 0 ? r0 + i : rn + (size_t)(k + j) * step + i);
+#pragma unroll
+    for (int j = 0; j < kU; ++j)
+      if (k + j < nc) {
+        s.x += v[j].x; s.y += v[j].y; s.z += v[j].z; s.w += v[j].w;
+      }
+  }
+  return s;
 }
 
 template <int NT, bool kDown>
@@ -701,7 +738,8 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
       if (tid == 0) *s_snap = *s_dead;
       moe_sync();
       bool write = !*s_snap;
-      if (write && (seg0 != i0 || seg1 != i1)) {
+      const bool apart = kDown && sums_apart(a.T);
+      if (write && (apart || seg0 != i0 || seg1 != i1)) {
         // a part: this CTA's record, then the last arrival adds them in CTA order
         float* rec = a.rec + ((size_t)cta * 2 + (i0 < seg0 ? 0 : 1)) * kMoeRecFloats;
         for (int i = tid; i < cols * 32; i += kMoeCW * 32) {
@@ -710,33 +748,19 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
         }
         moe_sync();
         const int c0 = cut.owner(i0), c1 = cut.owner(i1 - 1);
-        if (tid == 0) {
+        if (apart) {
+          if (cta == 0 && tid == 0) *a.active = rt->n_active;
+        } else if (tid == 0) {
           *s_last = atom_add_acq_rel_gpu(&a.cnt[kRouterTiles + c0], 1u) == (unsigned)(c1 - c0) ? 1 : 0;
           if (*s_last) a.cnt[kRouterTiles + c0] = 0u;
         }
         moe_sync();
-        write = *s_last != 0;
+        write = !apart && *s_last != 0;
         if (write) {
           const float4* r0 = reinterpret_cast<const float4*>(a.rec + ((size_t)c0 * 2 + 1) * kMoeRecFloats);
           const float4* rn = reinterpret_cast<const float4*>(a.rec + (size_t)(c0 + 1) * 2 * kMoeRecFloats);
-          constexpr size_t step = (size_t)2 * kMoeRecFloats / 4;
-          const int nc = c1 - c0;
-          for (int i = tid; i < cols * 32; i += kMoeCW * 32) {
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int kU = 8;   // records in flight
-            for (int k = -1; k < nc; k += kU) {
-              float4 v[kU];
-#pragma unroll
-              for (int j = 0; j < kU; ++j)
-                if (k + j < nc) v[j] = __ldcg(k + j < 0 ? r0 + i : rn + (size_t)(k + j) * step + i);
-#pragma unroll
-              for (int j = 0; j < kU; ++j)
-                if (k + j < nc) {
-                  s.x += v[j].x; s.y += v[j].y; s.z += v[j].z; s.w += v[j].w;
-                }
-            }
-            *reinterpret_cast<float4*>(red + (i >> 5) * kRedLd + 4 * (i & 31)) = s;
-          }
+          for (int i = tid; i < cols * 32; i += kMoeCW * 32)
+            *reinterpret_cast<float4*>(red + (i >> 5) * kRedLd + 4 * (i & 31)) = sum_parts(r0, rn, c1 - c0, i);
           moe_sync();
         }
       }
@@ -745,17 +769,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
           for (int i = tid; i < cols * 32; i += kMoeCW * 32) {
             const int c = i >> 5, q = i & 31;
             const size_t o = (size_t)c * a.H + (size_t)rb * kRowsPerBlock + 4 * q;
-            float4 v = *reinterpret_cast<const float4*>(red + c * kRedLd + 4 * q);
-            if (a.resid) {
-              const uint2 ru = *reinterpret_cast<const uint2*>(a.resid + o);
-              v.x += __uint_as_float(ru.x << 16);
-              v.y += __uint_as_float(ru.x & 0xffff0000u);
-              v.z += __uint_as_float(ru.y << 16);
-              v.w += __uint_as_float(ru.y & 0xffff0000u);
-            }
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-            *reinterpret_cast<uint2*>(a.y + o) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            *reinterpret_cast<uint2*>(a.y + o) = out4(a, o, *reinterpret_cast<const float4*>(red + c * kRedLd + 4 * q));
           }
         } else {
           // a warp per column: outputs 64 rb .. 64 rb + 63 of pair off + c, half a record
@@ -789,6 +803,22 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
   }
   __syncthreads();
   if (*s_dead && tid == 0) drain_ring(full, kMoeRing, *s_issued);
+}
+
+// y from the records of down: a CTA per row block and eight tokens, a thread per
+// four outputs.
+__global__ void __launch_bounds__(256) moe_sum_kernel(const MoeArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const MoeRun<true> run(a, *a.active);
+  const MoeCut cut(run.total(), run.item_len, a.down_ctas);
+  const int rb = blockIdx.x, t = 8 * blockIdx.y + (threadIdx.x >> 5), q = threadIdx.x & 31;
+  if (t >= a.T) return;
+  const int i0 = rb * run.item_len, c0 = cut.owner(i0), c1 = cut.owner(i0 + run.item_len - 1);
+  const float4* r0 = reinterpret_cast<const float4*>(a.rec + ((size_t)c0 * 2 + 1) * kMoeRecFloats);
+  const float4* rn = reinterpret_cast<const float4*>(a.rec + (size_t)(c0 + 1) * 2 * kMoeRecFloats);
+  const size_t o = (size_t)t * a.H + (size_t)rb * kRowsPerBlock + 4 * q;
+  *reinterpret_cast<uint2*>(a.y + o) = out4(a, o, sum_parts(r0, rn, c1 - c0, 32 * t + q));
 }
 
 template <int NT, bool kDown>
@@ -843,7 +873,7 @@ cudaError_t moe_go(Kernel k, dim3 grid, int threads, size_t smem, cudaStream_t s
 }
 
 template <int NT>
-cudaError_t launch_experts(const MoeArgs& a, int dev, cudaStream_t st) {
+cudaError_t launch_experts(MoeArgs a, int dev, cudaStream_t st) {
   cudaError_t e = moe_configure<NT, false>(dev);
   if (e == cudaSuccess) e = moe_configure<NT, true>(dev);
   if (e != cudaSuccess) return e;
@@ -851,8 +881,10 @@ cudaError_t launch_experts(const MoeArgs& a, int dev, cudaStream_t st) {
   e = moe_go(moe_expert_kernel<NT, false>, dim3((unsigned)(sms * moe_per_sm<NT, false>(dev))), kMoeThreads,
              MoeLayout<NT>::kBytes, st, a);
   if (e != cudaSuccess) return e;
-  return moe_go(moe_expert_kernel<NT, true>, dim3((unsigned)(sms * moe_per_sm<NT, true>(dev))), kMoeThreads,
-                MoeLayout<NT>::kBytes, st, a);
+  a.down_ctas = sms * moe_per_sm<NT, true>(dev);
+  e = moe_go(moe_expert_kernel<NT, true>, dim3((unsigned)a.down_ctas), kMoeThreads, MoeLayout<NT>::kBytes, st, a);
+  if (e != cudaSuccess || !sums_apart(a.T)) return e;
+  return moe_go(moe_sum_kernel, dim3((unsigned)(a.H / kRowsPerBlock), (unsigned)((a.T + 7) / 8)), 256, 0, st, a);
 }
 
 // ----------------------------------------------------------------- packing --

@@ -73,6 +73,8 @@ struct MoeArgs {
   float* rec;                          // split records, two per CTA
   int* choice;                         // [T][K] the router's choices
   float* share;                        // [T][K] and their weights
+  int* active;                         // runs of pairs that down streamed (for the sums)
+  int down_ctas;                       // the grid of down
   unsigned* cnt;                       // arrival counters: kRouterTiles of the router, then one per CTA
 };
 

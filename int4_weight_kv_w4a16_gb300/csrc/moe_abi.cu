@@ -59,7 +59,7 @@ void ws_layout(const futr_moe_shape& s, int max_batch, int ctas, futr_moe_ws* w)
   w->off_cnt = off;
   off = host::region_after(off, (uint64_t)(ctas + kRouterTiles) * 4);
   w->off_rms = off;
-  off = host::region_after(off, (uint64_t)max_batch * (1 + 2 * s.top_k) * 4);   // factors, choices, weights
+  off = host::region_after(off, (uint64_t)max_batch * (1 + 2 * s.top_k) * 4 + 4);   // factors, weights, choices, a count
   w->off_logits = off;
   off = host::region_after(off, (uint64_t)max_batch * s.n_experts * 4);
   w->off_x = off;
@@ -196,6 +196,7 @@ futr_status futr_moe_layer(const uint16_t* x, const float* gain, const uint16_t*
     a.rms = at<float>(ws->base, ws->off_rms);
     a.share = a.rms + ws->max_batch;
     a.choice = reinterpret_cast<int*>(a.share + (size_t)ws->max_batch * s.top_k);
+    a.active = a.choice + (size_t)ws->max_batch * s.top_k;
     a.logits = at<float>(ws->base, ws->off_logits);
     a.xh = at<__half>(ws->base, ws->off_x);
     a.act = at<__half>(ws->base, ws->off_act);
