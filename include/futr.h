@@ -365,7 +365,8 @@ futr_status futr_check(const futr_ws* ws, const futr_kv* kv, void* stream);
  * A value is code * scale.  Scales written here are powers of two.  Which page
  * holds positions page*i .. page*i + page - 1 of sequence b is entry [b][i] of
  * the caller's page table (device int32 [batch][table_ld]); entries past a
- * sequence's last page are not read.  Several sequences may read one page; in
+ * sequence's last page, and those of pages before every row's window, are not
+ * read.  Several sequences may read one page; in
  * one append, a page may belong to one sequence only.
  *
  * Ragged rows: rows start[b] .. start[b+1]-1 of a call's row tensors are the

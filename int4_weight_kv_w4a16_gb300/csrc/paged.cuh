@@ -67,8 +67,12 @@ struct PagedAttnArgs {
   int* err;
 };
 
-size_t paged_rec_floats(int d);     // floats of one CTA's records
-int paged_attn_ctas(int d);         // most CTAs any launch for head size d uses on the current device
+int paged_attn_sms();                        // of the current device
+int paged_attn_ctas(int sms);                // most CTAs any launch uses
+size_t paged_rec_floats(int d, int sms);     // floats of all their records
+size_t paged_tc_rec_floats(int d);           // of one CTA of the many-row kernel
+cudaError_t launch_paged_attention_tc(const PagedAttnArgs& a, const CUtensorMap& map, int d, int dtype, int ctas,
+                                      cudaStream_t st);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, const CUtensorMap& map, int d, int dtype, cudaStream_t st);
 bool make_paged_map(CUtensorMap* m, const void* codes, int d, int page, uint64_t blocks);
 

@@ -168,10 +168,10 @@ futr_status futr_paged_workspace_size(const futr_shape* shape, size_t* bytes) {
   return guarded([&]() -> futr_status {
     if (!bytes) return FUTR_ERR_INVALID_ARG;
     if (!host::shape_valid(shape)) return FUTR_ERR_UNSUPPORTED;
-    const int ctas = paged_attn_ctas(shape->head_dim);
-    if (ctas <= 0) return FUTR_ERR_CUDA;
-    const uint64_t rec = host::region_after(0, (uint64_t)ctas * 4);
-    *bytes = (size_t)host::region_after(rec, (uint64_t)ctas * paged_rec_floats(shape->head_dim) * 4);
+    const int sms = paged_attn_sms();
+    if (sms <= 0) return FUTR_ERR_CUDA;
+    const uint64_t rec = host::region_after(0, (uint64_t)paged_attn_ctas(sms) * 4);
+    *bytes = (size_t)host::region_after(rec, (uint64_t)paged_rec_floats(shape->head_dim, sms) * 4);
     return FUTR_OK;
   });
 }
@@ -186,7 +186,7 @@ futr_status futr_paged_workspace_init(const futr_shape* shape, void* mem, size_t
     if (!aligned(mem, 256) || mem_bytes < need) return FUTR_ERR_INVALID_ARG;
     futr_paged_ws w{};
     w.head_dim = shape->head_dim;
-    w.ctas = paged_attn_ctas(shape->head_dim);
+    w.ctas = paged_attn_ctas(paged_attn_sms());
     w.base = mem;
     w.bytes = need;
     w.rec_offset = host::region_after(0, (uint64_t)w.ctas * 4);
@@ -214,7 +214,7 @@ futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t
     const int width = s.n_q_heads * s.head_dim;
     if (!rows_ok(q, ld_q, width) || !rows_ok(out, ld_out, width) || q == out) return FUTR_ERR_INVALID_ARG;
     // the workspace has to fit the grid on the current device
-    if (paged_attn_ctas(s.head_dim) > ws->ctas) return FUTR_ERR_INVALID_ARG;
+    if (paged_attn_ctas(paged_attn_sms()) > ws->ctas) return FUTR_ERR_INVALID_ARG;
     PagedAttnArgs a{};
     a.c = view(*cache, layer);
     a.r = PagedRows{pos, start, table, batch, n_rows, table_ld};

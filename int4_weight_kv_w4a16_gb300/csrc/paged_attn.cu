@@ -29,7 +29,7 @@
 //
 // Bound by memory while R <= 16 (the codes are read once, 2 d bytes a position
 // and kv-head), by the tensor pipe for long row runs.
-#include "paged.cuh"
+#include "paged_dev.cuh"
 
 namespace futr {
 
@@ -37,10 +37,6 @@ namespace {
 
 constexpr int kPaCW = 4;                        // consumer warps
 constexpr int kPaThreads = (kPaCW + 1) * 32;
-constexpr int kPaTile = 128;                    // positions of a tile: 32 a warp
-constexpr int kPaSub = kPaTile / 16;            // 16-position sub-tiles: what one page is a multiple of
-constexpr unsigned long long kPaWaitNs = 1000000000ull;
-
 template <int D, int NT>
 struct PaLayout {
   static constexpr int R = 8 * NT;
@@ -57,188 +53,7 @@ struct PaLayout {
   static constexpr int kBytes = kBar + 2 * kRing * 8 + 32;
 };
 
-__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, const int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long dl = global_ns() + kPaWaitNs;
-  return mbar_wait_until(bar, parity, dl, err);
-}
-
 __device__ __forceinline__ void pa_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kPaCW * 32) : "memory"); }
-
-__device__ __forceinline__ float pa_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ void cvt4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// ------------------------------------------------------------------ shares --
-
-// Row tile rt of a sequence (n rows from position p0, G query heads a kv-head,
-// R rows a tile): its tiles [t0, t1).
-struct TileRange {
-  int t0, t1;
-};
-__device__ __forceinline__ TileRange row_tile(int n, int p0, int G, int R, int window, int rt) {
-  int first = p0, last = p0;
-  if (n > 1) {
-    const int r0 = rt * R, r1 = min(n * G, r0 + R) - 1;
-    first = p0 + r0 / G;
-    last = p0 + r1 / G;
-  }
-  const int lo = window > 0 ? max(0, first - window + 1) : 0;
-  return {lo / kPaTile, last / kPaTile + 1};
-}
-
-__device__ __forceinline__ long long seq_tiles(int n, int p0, int G, int R, int window) {
-  long long w = 0;
-  const int nrt = (n * G + R - 1) / R;
-#pragma unroll 1
-  for (int rt = 0; rt < nrt; ++rt) {
-    const TileRange t = row_tile(n, p0, G, R, window, rt);
-    w += t.t1 - t.t0;
-  }
-  return w;
-}
-
-// a / b for a >= 0, b > 0, on the path to the first copy: unit counts are small
-// numbers in all but the longest calls, and there one fp32 division, off by one
-// at most, with its remainder checked costs a fraction of an integer division.
-__device__ __forceinline__ long long quot(long long a, long long b) {
-  if (((a | b) >> 21) != 0) return a / b;
-  int q = (int)__fdividef((float)(int)a, (float)(int)b);
-  const int r = (int)a - q * (int)b;
-  if (r < 0) --q;
-  if (r >= (int)b) ++q;
-  return q;
-}
-
-// `total` units cut into `use` shares: the first `rem` of per + 1, the others of per.
-struct Cut {
-  long long total, per;
-  int use, rem;
-  __device__ __forceinline__ void set(long long units, int ctas) {
-    total = units;
-    use = (int)(units < ctas ? units : ctas);
-    per = units <= ctas ? 1 : quot(units, ctas);
-    rem = (int)(units - per * use);
-  }
-  __device__ __forceinline__ long long begin(int cta) const { return per * cta + min(cta, rem); }
-  __device__ __forceinline__ int owner(long long u) const {
-    const long long big = (per + 1) * rem;
-    return (int)(u < big ? quot(u, per + 1) : rem + (per == 1 ? u - big : quot(u - big, per)));
-  }
-};
-
-// The position of a CTA in the call's work: sequence b, kv-head, row tile and
-// the next tile.  The producer warp keeps one copy, the consumers another.
-struct Walk {
-  int b, kvh, rt, row0, n, p0;
-  long long per_head;      // tiles of one kv-head of sequence b
-  long long u, u1;         // this CTA's share [u, u1), u advancing
-  long long item0;         // unit index of the current item's first tile
-  TileRange t;
-
-  // Enter sequence b (rows known); the item that holds unit `at` of its units.
-  __device__ __forceinline__ void enter(const PagedAttnArgs& a, int R, long long at, long long base) {
-    kvh = (int)quot(at, per_head);
-    long long rem = at - (long long)kvh * per_head;
-    rt = 0;
-    t = row_tile(n, p0, a.G, R, a.window, 0);
-#pragma unroll 1
-    while (rem >= t.t1 - t.t0) {
-      rem -= t.t1 - t.t0;
-      ++rt;
-      t = row_tile(n, p0, a.G, R, a.window, rt);
-    }
-    item0 = base + at - rem;
-  }
-
-  // Step to the item after the current one (its units start at item0 + tiles).
-  __device__ __forceinline__ void next_item(const PagedAttnArgs& a, int R) {
-    item0 += t.t1 - t.t0;
-    ++rt;
-    if (rt * R >= n * a.G) {
-      rt = 0;
-      if (++kvh == a.Hkv) {
-        kvh = 0;
-        do {
-          ++b;
-          paged_seq(a.r, a.c, b, row0, n, p0);
-        } while (n == 0);   // u < u1: a later sequence has rows
-        per_head = seq_tiles(n, p0, a.G, R, a.window);
-      }
-    }
-    t = row_tile(n, p0, a.G, R, a.window, rt);
-  }
-};
-
-// The call's units, their cut, and the share of CTA `cta` (a full warp).  False:
-// it has none.
-__device__ __forceinline__ bool find_share(const PagedAttnArgs& a, int R, int cta, int ctas, Walk& w, Cut& cut,
-                                           bool report) {
-  const int lane = threadIdx.x & 31;
-  int row0 = 0, n = 0, p0 = 0;   // of sequence b0 + lane
-  long long per = 0, incl = 0;   // its tiles per kv-head; all tiles of this round's sequences up to it
-  auto look = [&](int b0) {
-    n = 0;
-    per = 0;
-    if (b0 + lane < a.r.batch) {
-      if (!paged_seq(a.r, a.c, b0 + lane, row0, n, p0) && report) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
-      per = seq_tiles(n, p0, a.G, R, a.window);
-    }
-    incl = per * a.Hkv;
-#pragma unroll 1
-    for (int o = 1; o < 32 && o < a.r.batch; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-  };
-  const int top = min(31, a.r.batch - 1);   // a lane whose prefix sum is complete
-  long long total = 0;
-#pragma unroll 1
-  for (int b0 = 0; b0 < a.r.batch; b0 += 32) {
-    look(b0);
-    total += __shfl_sync(0xffffffffu, incl, top);
-  }
-  cut.set(total, ctas);
-  if (cta >= cut.use) return false;
-  w.u = cut.begin(cta);
-  w.u1 = cut.begin(cta + 1);
-  long long before = 0;
-#pragma unroll 1
-  for (int b0 = 0; b0 < a.r.batch; b0 += 32) {
-    if (a.r.batch > 32) look(b0);   // up to 32 sequences: still at hand
-    const unsigned hit = __ballot_sync(0xffffffffu, lane <= top && before + incl > w.u);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      w.b = b0 + src;
-      w.row0 = __shfl_sync(0xffffffffu, row0, src);
-      w.n = __shfl_sync(0xffffffffu, n, src);
-      w.p0 = __shfl_sync(0xffffffffu, p0, src);
-      w.per_head = __shfl_sync(0xffffffffu, per, src);
-      const long long base = before + __shfl_sync(0xffffffffu, incl - per * a.Hkv, src);
-      w.enter(a, R, w.u - base, base);
-      return true;
-    }
-    before += __shfl_sync(0xffffffffu, incl, top);
-  }
-  return false;   // not reached: u < total
-}
 
 // ---------------------------------------------------------------- consumer --
 
@@ -424,18 +239,6 @@ struct PaWarp {
   }
 };
 
-template <bool kHalf>
-__device__ __forceinline__ float widen(uint16_t u) {
-  return kHalf ? __half2float(__ushort_as_half(u)) : __uint_as_float((uint32_t)u << 16);
-}
-
-template <bool kHalf>
-__device__ __forceinline__ uint32_t narrow2(float a, float b) {
-  if (kHalf) return pack_half2(a, b);
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
 // Rows warp, warp + 4, ... of the tile: rotated, divided by a power of two and
 // stored as f16 into their places in the B fragments; their score factors to
 // qs.  The loads of all of a warp's rows are in flight together.
@@ -587,79 +390,8 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     Walk w;
     Cut cut;
     if (!find_share(a, R, cta, gridDim.x, w, cut, false)) return;
-    // copies of a tile: whole (page, kv-head) blocks, keys then values
-    const int ppt = kPaTile >> plog;   // pages of a tile
-    const uint32_t bytes = (uint32_t)(2 * page * D);
-    int slot = 0, issued = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    while (w.u < w.u1 && ok) {
-      const int first = w.t.t0 + (int)(w.u - w.item0);
-      const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);
-      const int end = min(w.p0 + w.n, (first + count) * kPaTile);   // positions needed
-      // page ids and scales, 32 pages a round (one per lane), one round ahead
-      const int pg0 = (first * kPaTile) >> plog, pg1 = (end - 1) >> plog;
-      const int* tab = a.r.table + (size_t)w.b * a.r.table_ld;
-      auto fetch = [&](int pg, int& id, float2& s) {
-        id = pg <= pg1 ? tab[pg] : 0;
-        if (id < 0 || id >= a.c.n_pages) {
-          set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
-          id = -1;
-        }
-        s = make_float2(0.f, 0.f);
-        if (id >= 0) s = reinterpret_cast<const float2*>(a.c.scales)[(size_t)id * a.Hkv + w.kvh];
-      };
-      int id, id_next = 0, base = pg0;
-      float2 sc, sc_next = make_float2(0.f, 0.f);
-      fetch(base + lane, id, sc);
-      if (base + 32 <= pg1) fetch(base + 32 + lane, id_next, sc_next);
-      for (int i = 0; i < count && ok; ++i) {
-        const int pos = (first + i) * kPaTile, pg = pos >> plog;
-        if (pg >= base + 32) {   // 32 and pg0 are multiples of the pages of a tile: no tile straddles
-          base += 32;
-          id = id_next;
-          sc = sc_next;
-          if (base + 32 <= pg1) fetch(base + 32 + lane, id_next, sc_next);
-        }
-        if (issued >= kPaRing && !pa_wait(&empty[slot], phase ^ 1u, a.err)) {
-          ok = false;
-          break;
-        }
-        uint8_t* st = smem + slot * Lay::kStage;
-        // the copies need the page ids only: they are under way while the
-        // scales, loaded with the ids, arrive
-        const int zid = __shfl_sync(0xffffffffu, id, (pg - base + lane) & 31);
-        const bool have = lane < ppt && pg + lane <= pg1 && zid >= 0;
-        const unsigned mask = __ballot_sync(0xffffffffu, have);
-        if (have)
-          tma_3d(smem_u32(st + lane * bytes), &map, 0, (int)(a.block0 + (long long)zid * a.Hkv + w.kvh), &full[slot]);
-        const int from = (((pos + 16 * (lane & (kPaSub - 1))) >> plog) - base) & 31;   // the page of sub-tile `lane`
-        const float kscale = __shfl_sync(0xffffffffu, sc.x, from), vscale = __shfl_sync(0xffffffffu, sc.y, from);
-        const int myid = __shfl_sync(0xffffffffu, id, from);
-        if (lane < kPaSub) {
-          // log2 of the value scale, its power of two apart (a scale of 0, a
-          // page never written, counts as the smallest; a missing page as
-          // not visible)
-          float lv = (float)kPagedMinExp, inv = __uint_as_float((uint32_t)(127 - kPagedMinExp) << 23);
-          if (vscale > 0.f) {
-            const uint32_t u = __float_as_uint(vscale);
-            lv = (float)((int)(u >> 23) - 127) + log2f(__uint_as_float((u & 0x7FFFFFu) | 0x3F800000u));
-            inv = __fdiv_rn(1.0f, vscale);
-          }
-          if (myid < 0) lv = -INFINITY;
-          s_scale[slot * kPaSub + lane] = make_float4(kscale, lv, inv, 0.f);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes * __popc(mask));
-        ++issued;
-        if (++slot == kPaRing) {
-          slot = 0;
-          phase ^= 1u;
-        }
-      }
-      w.u += count;
-      if (w.u < w.u1) w.next_item(a, R);
-    }
+    int issued = 0;
+    const bool ok = produce_tiles<D>(a, &map, R, w, smem, s_scale, full, empty, kPaRing, issued);
     if (!ok) {
       record_timeout(a.err);
       *s_dead = 1;
@@ -909,6 +641,8 @@ cudaError_t pa_launch(const PagedAttnArgs& a, const CUtensorMap& map, cudaStream
   return cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, NT, kHalf>, a, map);
 }
 
+constexpr int kTcMinRows = 64;   // rows (tokens x query heads of a kv-head) a sequence, on average
+
 template <int D, bool kHalf>
 cudaError_t pa_launch_nt(const PagedAttnArgs& a, const CUtensorMap& map, cudaStream_t st) {
   // rows of a tile: those that a sequence has on average (the counts are on the device)
@@ -921,16 +655,25 @@ cudaError_t pa_launch_nt(const PagedAttnArgs& a, const CUtensorMap& map, cudaStr
 
 constexpr int kPaMaxRows = 16;
 
-size_t paged_rec_floats(int d) { return (size_t)2 * kPaMaxRows * (d + 2); }
-
-int paged_attn_ctas(int d) {
-  (void)d;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  return sm_count(dev) * kPaMaxPerSm;
+// Floats of all CTAs' records on a device with `sms` SMs: two CTAs an SM of these
+// kernels, or one of the many-row kernel.
+size_t paged_rec_floats(int d, int sms) {
+  const size_t few = (size_t)sms * kPaMaxPerSm * 2 * kPaMaxRows * (d + 2), many = (size_t)sms * paged_tc_rec_floats(d);
+  return few > many ? few : many;
 }
 
+int paged_attn_sms() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return sm_count(dev);
+}
+
+int paged_attn_ctas(int sms) { return sms * kPaMaxPerSm; }
+
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, const CUtensorMap& map, int d, int dtype, cudaStream_t st) {
+  // sequences of many rows on average: 256-row tiles on the tensor cores
+  if ((long long)a.r.n_rows * a.G >= (long long)kTcMinRows * a.r.batch)
+    return launch_paged_attention_tc(a, map, d, dtype, paged_attn_sms(), st);
   const bool half = dtype == FUTR_DTYPE_F16;
   if (d == 128) return half ? pa_launch_nt<128, true>(a, map, st) : pa_launch_nt<128, false>(a, map, st);
   return half ? pa_launch_nt<64, true>(a, map, st) : pa_launch_nt<64, false>(a, map, st);

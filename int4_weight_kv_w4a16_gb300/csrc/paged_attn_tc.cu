@@ -1,0 +1,694 @@
+// Attention over the paged 8-bit cache for many rows a sequence (chunks of a
+// prompt), on the 5th-generation tensor cores.  The mathematics, the roundings
+// and the cut of the work are those of paged_attn.cu; a row tile has 256 rows,
+// two halves of 128 = the lanes of tensor memory.
+//
+// One CTA an SM, 14 warps:
+//   warp 12      streams tiles of 128 positions (8-bit codes) into a ring;
+//   warps 8-11   widen a tile's codes to f16 (exact) into two operand buffers,
+//                keys and values: rows of 128 bytes (64 dims) with the 128-byte
+//                swizzle, which is a K-major operand for Q K^T and an MN-major one
+//                for P V; once for all 256 rows;
+//   warp 13      one thread issues the MMAs (kind::f16, M 128, fp32 accumulators):
+//                S_h = Q_h K^T (operands in shared memory) and O_h += P_h V (P in
+//                tensor memory), ordered P_0 V, S_0 of the next tile, P_1 V, S_1 of
+//                the next tile, so that the softmax of one half runs under the
+//                products of the other;
+//   warps 0-7    the softmax: a thread per row reads its 128 scores from tensor
+//                memory twice (maximum, then weights), and writes the weights as f16
+//                over the scores it has read, where they are P V's A operand.
+// Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (D columns each).
+//
+// The running reference M of a row follows its maximum only when that has grown
+// by more than 2^8: a weight up to 2^8 is a good f16, the normalizer is fp32, and
+// O, in tensor memory, is rescaled a few times an item instead of every tile.
+//
+// Bound by the tensor cores in principle (4 x 256 x 128 x D flops a tile take
+// 2048 cycles at D = 128), with 1024 to 2048 cycles of exponentials and some 600
+// of widening a scheduler beside them.
+#include "paged_dev.cuh"
+
+namespace futr {
+
+namespace {
+
+constexpr int kTcRows = 256, kTcHalf = 128;
+constexpr int kTcThreads = 14 * 32;
+constexpr int kTcSoft = 8 * 32;                 // softmax threads
+constexpr int kTcRing = 2;
+
+template <int D>
+struct TcLayout {
+  static constexpr int kBlk = D / 64;                            // 64-dim blocks of an operand row
+  static constexpr int kOp = kTcHalf * D * 2;                    // one f16 operand of 128 rows
+  static constexpr int kQ = 0;                                   // two halves
+  static constexpr int kK = kQ + 2 * kOp;
+  static constexpr int kV = kK + kOp;
+  static constexpr int kStage = kV + kOp;                        // ring of 8-bit tiles
+  static constexpr int kRaw = kStage + kTcRing * 2 * kPaTile * D;   // [ring][sub-tiles] float4
+  static constexpr int kScale = kRaw + kTcRing * kPaSub * 16;    // [2][sub-tiles] float4, by tile parity
+  static constexpr int kQs = kScale + 2 * kPaSub * 16;           // [256] score factors
+  static constexpr int kBar = kQs + kTcRows * 4;
+  static constexpr int kBytes = kBar + 24 * 8 + 64;
+};
+
+struct TcItem {
+  Walk w;
+  Cut cut;
+  int active;
+  int first, count, valid;       // tiles of this CTA's part, rows of the tile
+};
+
+__device__ __forceinline__ void tc_soft_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kTcSoft) : "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t u[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr)
+      : "memory");
+  tc_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+}
+
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+      "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+      "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Shared-memory operand descriptor with the 128-byte swizzle: rows of 128 bytes in
+// 8-row atoms of 1 KB (stride 1024); `lead`: bytes between 64-element blocks of an
+// MN-major operand (a K-major operand's block is one row wide: unused).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptors: D fp32, A and B f16, M = 128; N = 128 (scores), N = D
+// with B MN-major (bit 16: values as [position][dim]).
+constexpr uint32_t kIdescS = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+template <int D>
+constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
+
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+// Byte offset of dim i of row r in an f16 operand (blocks of 64 dims, swizzled rows).
+__device__ __forceinline__ int tc_at(int r, int i) {
+  return (i >> 6) * (kTcHalf * 128) + r * 128 + ((((i & 63) >> 3) ^ (r & 7)) << 4) + (i & 7) * 2;
+}
+
+// The rows of one half that belong to this softmax warp (32 of them), rotated,
+// divided by a power of two and stored as f16 (rows past `valid` as zeros); their
+// score factors to qs.
+template <int D, bool kHalf>
+__device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Walk& w, int valid, int half, uint8_t* q16,
+                                                float* qs) {
+  constexpr int J = D / 32, RW = 4;   // rows whose loads are in flight together
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+#pragma unroll 1
+  for (int r0 = 32 * warp; r0 < 32 * warp + 32; r0 += RW) {
+    uint16_t u[RW][J];
+    float2 cs[RW][J / 2];
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const int r = kTcHalf * half + r0 + k;
+      if (r < valid) {
+        const int row = w.rt * kTcRows + r, i = row / a.G, head = w.kvh * a.G + row - i * a.G;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (size_t)(w.row0 + i) * a.ld_q + (size_t)head * D;
+#pragma unroll
+        for (int j = 0; j < J; ++j) u[k][j] = q[lane + 32 * j];
+        if (a.c.rope) {
+#pragma unroll
+          for (int j = 0; j < J / 2; ++j) cs[k][j] = a.c.rope[(size_t)(w.p0 + i) * (D / 2) + lane + 32 * j];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const int r = kTcHalf * half + r0 + k;
+      float x[J], factor = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) x[j] = 0.f;
+      if (r < valid) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) x[j] = widen<kHalf>(u[k][j]);
+        if (a.c.rope) {
+#pragma unroll
+          for (int j = 0; j < J / 2; ++j) {
+            const float x1 = x[j], x2 = x[j + J / 2];
+            x[j] = x1 * cs[k][j].x - x2 * cs[k][j].y;
+            x[j + J / 2] = x2 * cs[k][j].x + x1 * cs[k][j].y;
+          }
+        }
+        float mx = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) mx = fmaxf(mx, fabsf(x[j]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int j = 0; j < J; ++j) x[j] *= inv;
+        factor = __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        *reinterpret_cast<__half*>(q16 + tc_at(r0 + k, lane + 32 * j)) = __float2half_rn(x[j]);
+      if (lane == 0) qs[kTcHalf * half + r0 + k] = factor;
+    }
+  }
+}
+
+// The bounds of the current part from its walk (one thread).
+__device__ __forceinline__ void tc_set(const PagedAttnArgs& a, TcItem& it) {
+  const Walk& c = it.w;
+  it.first = c.t.t0 + (int)(c.u - c.item0);
+  it.count = (int)(min(c.u1, c.item0 + (c.t.t1 - c.t.t0)) - c.u);
+  it.valid = min(kTcRows, c.n * a.G - c.rt * kTcRows);
+}
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    paged_attn_tc_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap map) {
+  using Lay = TcLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float4* s_raw = reinterpret_cast<float4*>(smem + Lay::kRaw);
+  float4* s_scale = reinterpret_cast<float4*>(smem + Lay::kScale);
+  float* s_qs = reinterpret_cast<float*>(smem + Lay::kQs);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::kBar);   // [2] a tile's codes have landed
+  uint64_t* empty = full + kTcRing;      // [2] they are widened
+  uint64_t* qready = empty + kTcRing;    // [2] the queries of a half are in place
+  uint64_t* kready = qready + 2;         // keys widened
+  uint64_t* kfree = kready + 1;          // both halves' scores are done
+  uint64_t* vready = kfree + 1;          // values widened
+  uint64_t* vfree = vready + 1;          // both halves' P V are done
+  uint64_t* sfull = vfree + 1;           // [2] scores of a half in tensor memory, scales in shared memory
+  uint64_t* pready = sfull + 2;          // [2] weights of a half in tensor memory
+  uint64_t* odone = pready + 2;          // [2] P V of a half is done
+  volatile int* s_dead = reinterpret_cast<volatile int*>(odone + 2);   // a wait ran out
+  volatile int* s_issued = s_dead + 1;
+  volatile int* s_last = s_dead + 2;
+  volatile int* s_snap = s_dead + 3;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(odone + 2) + 4;
+  __shared__ TcItem s_item;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kTcRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 4);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&qready[h], 4);
+      mbar_init(&sfull[h], 5);   // the MMAs and the four widening warps
+      mbar_init(&pready[h], 4);
+      mbar_init(&odone[h], 1);
+    }
+    mbar_init(kready, 4);
+    mbar_init(kfree, 1);
+    mbar_init(vready, 4);
+    mbar_init(vfree, 1);
+    fence_mbar_init();
+    *s_dead = 0;
+    *s_issued = 0;
+  }
+  if (warp == 13) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *s_tmem;
+  pdl_trigger();
+  pdl_wait();
+  const int cta = blockIdx.x, page = a.c.page, plog = a.c.page_log2;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {   // in dead mode: nothing to wait for
+    if (ok && !pa_wait(bar, parity, a.err)) {
+      ok = false;
+      record_timeout(a.err);
+      *s_dead = 1;
+    }
+    return ok;
+  };
+
+  if (warp == 12) {
+    // ---------------------------------------------------------- producer --
+    Walk w;
+    Cut cut;
+    if (find_share(a, kTcRows, cta, gridDim.x, w, cut, false)) {
+      int issued = 0;
+      if (!produce_tiles<D>(a, &map, kTcRows, w, smem + Lay::kStage, s_raw, full, empty, kTcRing, issued)) {
+        record_timeout(a.err);
+        *s_dead = 1;
+      }
+      if (lane == 0) *s_issued = issued;
+    }
+  } else if (warp == 13) {
+    // ------------------------------------------------------------ issuer --
+    Walk w;
+    Cut cut;
+    if (find_share(a, kTcRows, cta, gridDim.x, w, cut, false) && lane == 0) {
+      uint32_t t = 0, done[2] = {0, 0};   // tiles begun; P V issued by half
+      uint32_t part = 0, part1 = 0;       // parts, and parts with a second half
+      const uint32_t q16 = smem_u32(smem + Lay::kQ), k16 = smem_u32(smem + Lay::kK), v16 = smem_u32(smem + Lay::kV);
+      auto scores = [&](int h) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * (kTcHalf * 128) + (ks & 3) * 32;
+          tc_mma_ss(tm + 128 * h, tc_desc(q16 + h * Lay::kOp + off, 16), tc_desc(k16 + off, 16), kIdescS, ks > 0);
+        }
+        tc_commit(&sfull[h]);
+      };
+      auto values = [&](int h, bool first) {
+#pragma unroll
+        for (int ks = 0; ks < kPaTile / 16; ++ks)
+          tc_mma_ts(tm + 256 + D * h, tm + 128 * h + 8 * ks, tc_desc(v16 + ks * 2048, kTcHalf * 128), kIdescO<D>,
+                    !first || ks > 0);
+        tc_commit(&odone[h]);
+        ++done[h];
+      };
+      while (w.u < w.u1 && ok) {
+        const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);
+        const int nh = min(kTcRows, w.n * a.G - w.rt * kTcRows) > kTcHalf ? 2 : 1;
+        // the first tile's scores
+        if (!wait(kready, t & 1u)) break;
+        for (int h = 0; h < nh; ++h) {
+          if (!wait(&qready[h], (h == 0 ? part : part1) & 1u)) break;
+          tc_fence_after();
+          scores(h);
+        }
+        if (!ok) break;
+        tc_commit(kfree);
+        for (int i = 0; i < count && ok; ++i, ++t) {
+          const bool more = i + 1 < count;
+          if (!wait(vready, t & 1u)) break;
+          for (int h = 0; h < nh && ok; ++h) {
+            if (!wait(&pready[h], done[h] & 1u)) break;
+            tc_fence_after();
+            values(h, i == 0);
+            if (h + 1 == nh) tc_commit(vfree);
+            if (more) {
+              if (h == 0 && !wait(kready, (t + 1) & 1u)) break;
+              tc_fence_after();
+              scores(h);
+              if (h + 1 == nh) tc_commit(kfree);
+            }
+          }
+        }
+        w.u += count;
+        ++part;
+        part1 += nh - 1;
+        if (w.u < w.u1) w.next_item(a, kTcRows);
+      }
+    }
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------- widening --
+    Walk w;
+    Cut cut;
+    if (find_share(a, kTcRows, cta, gridDim.x, w, cut, false)) {
+      // A quarter-warp takes 4 chunks (of 16 codes) of rows r and r ^ 5: neither its
+      // reads of the 8-bit rows nor its writes of the f16 rows meet a bank twice.
+      constexpr int CH = D / 16, kQr = CH / 4;          // chunks of a row; column quarters
+      const int wg = warp - 8, qd = lane >> 3, l = lane & 7;
+      const int rl = (l >> 2) ? (qd ^ 5) : qd;          // row within 8
+      uint32_t t = 0, told[2] = {0, 0};   // tiles; arrivals at sfull by half
+      while (w.u < w.u1) {
+        const int first = w.t.t0 + (int)(w.u - w.item0);
+        const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);
+        const int nh = min(kTcRows, w.n * a.G - w.rt * kTcRows) > kTcHalf ? 2 : 1;
+        const int written = w.p0 + w.n;
+        for (int i = 0; i < count; ++i, ++t) {
+          const int slot = t % kTcRing;
+          wait(&full[slot], (t / kTcRing) & 1u);
+          const uint8_t* st = smem + Lay::kStage + slot * (2 * kPaTile * D);
+          const float4* raw = s_raw + slot * kPaSub;
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            // the operand buffer is free once the MMAs of the tile before have read it
+            if (t > 0) wait(kv ? vfree : kfree, (t - 1) & 1u);
+            uint8_t* dst = smem + (kv ? Lay::kV : Lay::kK);
+            if (ok) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const int r = 32 * wg + 8 * g + rl;     // position in the tile
+                // what was never written, or lies on a missing page, becomes zeros
+                const bool live = (first + i) * kPaTile + r < written && raw[r >> 4].y != -INFINITY;
+                const uint8_t* src = st + (r >> plog) * (2 * page * D) + ((r & (page - 1)) + kv * page) * D;
+                const int sr = D == 128 ? r & 7 : (r >> 1) & 3;
+#pragma unroll
+                for (int h = 0; h < kQr; ++h) {
+                  const int c = 4 * h + (l & 3);
+                  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                  if (live) v = *reinterpret_cast<const uint4*>(src + ((c ^ sr) << 4));
+                  uint4 o0, o1;
+                  cvt4(v.x, o0.x, o0.y);
+                  cvt4(v.y, o0.z, o0.w);
+                  cvt4(v.z, o1.x, o1.y);
+                  cvt4(v.w, o1.z, o1.w);
+                  *reinterpret_cast<uint4*>(dst + tc_at(r, 16 * c)) = o0;
+                  *reinterpret_cast<uint4*>(dst + tc_at(r, 16 * c + 8)) = o1;
+                }
+              }
+            }
+            if (kv == 0 && wg == 0 && lane < kPaSub) s_scale[(t & 1) * kPaSub + lane] = raw[lane];
+            tc_proxy_fence();
+            // (an arrival counts for this tile once the tile before is complete)
+            if (kv == 0)
+              for (int h = 0; h < nh; ++h)
+                if (told[h]++ > 0) wait(&sfull[h], told[h] & 1u);
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(kv ? vready : kready);
+              if (kv == 0)
+                for (int h = 0; h < nh; ++h) mbar_arrive(&sfull[h]);
+              else
+                mbar_arrive(&empty[slot]);
+            }
+          }
+        }
+        w.u += count;
+        if (w.u < w.u1) w.next_item(a, kTcRows);
+      }
+    }
+  } else {
+    // ----------------------------------------------------------- softmax --
+    const int half = warp >> 2, row = tid & (kTcHalf - 1);
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tm + lanes + 128 * half, to = tm + lanes + 256 + D * half;
+    TcItem& it = s_item;
+    if (warp == 0) {
+      Walk w;
+      Cut cut;
+      const bool active = find_share(a, kTcRows, cta, gridDim.x, w, cut, cta == 0);
+      if (lane == 0) {
+        it.w = w;
+        it.cut = cut;
+        it.active = active;
+      }
+    }
+    tc_soft_sync();
+    if (it.active) {
+      uint32_t t = 0, mine = 0;   // tiles of the CTA; tiles of this half
+      for (bool more = true; more;) {
+        if (tid == 0) tc_set(a, it);
+        tc_soft_sync();
+        const int count = it.count, valid = it.valid;
+        const bool here = kTcHalf * half < valid;
+        const int r = kTcHalf * half + row, myrow = it.w.rt * kTcRows + min(r, valid - 1);
+        float M = -INFINITY, L = 0.f;
+        if (here) {
+          tc_load_queries<D, kHalf>(a, it.w, valid, half, smem + Lay::kQ + half * Lay::kOp, s_qs);
+          tc_proxy_fence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&qready[half]);
+          const float qf = s_qs[r];   // this warp wrote it
+          const int p = it.w.p0 + myrow / a.G, back = a.window > 0 ? a.window - 1 : 0x3fffffff;
+          for (int i = 0; i < count; ++i, ++mine) {
+            const int pos0 = (it.first + i) * kPaTile;
+            wait(&sfull[half], mine & 1u);
+            tc_fence_after();
+            const float4* sc = s_scale + ((t + i) & 1) * kPaSub;
+            const int top = p - pos0, low = top - back;   // columns low .. top are visible
+            const bool cut = __any_sync(0xffffffffu, top < kPaTile - 1 || low > 0);
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float x[32];
+              tc_ld32(ts + 32 * c, x);
+              const float4 s0 = sc[2 * c], s1 = sc[2 * c + 1];
+              const float f0 = s0.x * qf, f1 = s1.x * qf;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                x[j] = fmaf(x[j], j < 16 ? f0 : f1, j < 16 ? s0.y : s1.y);
+                if (cut && (32 * c + j > top || 32 * c + j < low)) x[j] = -INFINITY;
+                mx = fmaxf(mx, x[j]);
+              }
+            }
+            // the reference moves when the maximum has outgrown it by 2^8 (or it has none yet)
+            const bool grow = mx > M + 8.f || (M == -INFINITY && mx > M);
+            if (__any_sync(0xffffffffu, grow)) {
+              const float now = grow ? mx : M;
+              const float corr = M == now ? 1.f : pa_ex2(M - now);
+              M = now;
+              L *= corr;
+              if (i > 0) {
+                wait(&odone[half], (mine - 1) & 1u);   // the sums so far are complete
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  float o[32];
+                  tc_ld32(to + 32 * c, o);
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) o[j] *= corr;
+                  tc_st32(to + 32 * c, o);
+                }
+              }
+            }
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float x[32];
+              tc_ld32(ts + 32 * c, x);
+              const float4 s0 = sc[2 * c], s1 = sc[2 * c + 1];
+              const float f0 = s0.x * qf, f1 = s1.x * qf, b0 = s0.y - ref, b1 = s1.y - ref;
+              float sum0 = 0.f, sum1 = 0.f;
+              uint32_t h[16];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                float y = fmaf(x[j], j < 16 ? f0 : f1, j < 16 ? b0 : b1);
+                if (cut && (32 * c + j > top || 32 * c + j < low)) y = -INFINITY;
+                x[j] = pa_ex2(y);
+                if (j < 16)
+                  sum0 += x[j];
+                else
+                  sum1 += x[j];
+              }
+              L = fmaf(sum0, s0.z, fmaf(sum1, s1.z, L));
+#pragma unroll
+              for (int j = 0; j < 16; ++j) h[j] = pack_half2(x[2 * j], x[2 * j + 1]);
+              tc_st16(ts + 16 * c, h);   // over scores 16 c .. 16 c + 15, read above or before
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pready[half]);
+          }
+          wait(&odone[half], (mine - 1) & 1u);
+          tc_fence_after();
+        }
+        t += count;
+        // ---- a whole item: its rows; a part of one: a record, and the CTA that
+        // arrives last adds the records in CTA order
+        const Walk& c = it.w;
+        const long long item1 = c.item0 + (c.t.t1 - c.t.t0);
+        const bool whole = c.u == c.item0 && c.u + count == item1;
+        if (tid == 0) *s_snap = *s_dead;
+        tc_soft_sync();
+        const bool live = *s_snap == 0;
+        bool write = whole && live;
+        constexpr size_t kRecRow = kTcRows, kRec = (size_t)kTcRows * (D + 2);
+        float* rec = a.rec + ((size_t)cta * 2 + (c.item0 < c.u ? 0 : 1)) * kRec;
+        const bool row_ok = r < valid;
+        const int i = myrow / a.G, head = c.kvh * a.G + myrow - i * a.G;
+        uint16_t* out = static_cast<uint16_t*>(a.out) + (size_t)(c.row0 + i) * a.ld_out + (size_t)head * D;
+        if (live && here) {
+          const float inv = L != 0.f ? __fdiv_rn(1.0f, L) : 0.f;   // a row that sees nothing: zeros
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            float o[32];
+            tc_ld32(to + 32 * k, o);
+            if (row_ok && whole) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint4 u;
+                u.x = narrow2<kHalf>(o[8 * j] * inv, o[8 * j + 1] * inv);
+                u.y = narrow2<kHalf>(o[8 * j + 2] * inv, o[8 * j + 3] * inv);
+                u.z = narrow2<kHalf>(o[8 * j + 4] * inv, o[8 * j + 5] * inv);
+                u.w = narrow2<kHalf>(o[8 * j + 6] * inv, o[8 * j + 7] * inv);
+                *reinterpret_cast<uint4*>(out + 32 * k + 8 * j) = u;
+              }
+            } else if (row_ok) {
+              // [dim quad][row] float4: neighbouring rows side by side
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                reinterpret_cast<float4*>(rec + 2 * kRecRow)[(8 * k + j) * kTcRows + r] =
+                    make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+          }
+          if (row_ok && !whole) {
+            rec[r] = M;
+            rec[kRecRow + r] = L;
+          }
+        }
+        if (!whole && live) {
+          tc_soft_sync();
+          const int c0 = it.cut.owner(c.item0), c1 = it.cut.owner(item1 - 1);
+          if (tid == 0) {
+            *s_last = atom_add_acq_rel_gpu(&a.cnt[c0], 1u) == (unsigned)(c1 - c0) ? 1 : 0;
+            if (*s_last) a.cnt[c0] = 0u;
+          }
+          tc_soft_sync();
+          write = *s_last != 0;
+          if (write && row_ok) {
+            // a thread per row: reference and normalizer of all parts, then its sums
+            const float* r0 = a.rec + ((size_t)c0 * 2 + 1) * kRec;      // CTA c0's second slot
+            const float* rn = a.rec + (size_t)(c0 + 1) * 2 * kRec;      // the others' first
+            const int nc = c1 - c0;
+            float top = __ldcg(r0 + r);
+#pragma unroll 1
+            for (int k = 0; k < nc; ++k) top = fmaxf(top, __ldcg(rn + (size_t)k * 2 * kRec + r));
+            const float ref = top == -INFINITY ? 0.f : top;
+            float sum = __ldcg(r0 + kRecRow + r) * pa_ex2(__ldcg(r0 + r) - ref);
+#pragma unroll 1
+            for (int k = 0; k < nc; ++k)
+              sum = fmaf(__ldcg(rn + (size_t)k * 2 * kRec + kRecRow + r),
+                         pa_ex2(__ldcg(rn + (size_t)k * 2 * kRec + r) - ref), sum);
+            const float inv = sum != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {   // 16 dims at a time
+              float4 acc[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+              for (int k = -1; k < nc; ++k) {
+                const float* src = k < 0 ? r0 : rn + (size_t)k * 2 * kRec;
+                const float wt = pa_ex2(__ldcg(src + r) - ref);
+                float4 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  v[j] = __ldcg(reinterpret_cast<const float4*>(src + 2 * kRecRow) + (4 * q + j) * kTcRows + r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  acc[j].x = fmaf(v[j].x, wt, acc[j].x);
+                  acc[j].y = fmaf(v[j].y, wt, acc[j].y);
+                  acc[j].z = fmaf(v[j].z, wt, acc[j].z);
+                  acc[j].w = fmaf(v[j].w, wt, acc[j].w);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                uint4 u;
+                u.x = narrow2<kHalf>(acc[2 * j].x * inv, acc[2 * j].y * inv);
+                u.y = narrow2<kHalf>(acc[2 * j].z * inv, acc[2 * j].w * inv);
+                u.z = narrow2<kHalf>(acc[2 * j + 1].x * inv, acc[2 * j + 1].y * inv);
+                u.w = narrow2<kHalf>(acc[2 * j + 1].z * inv, acc[2 * j + 1].w * inv);
+                *reinterpret_cast<uint4*>(out + 16 * q + 8 * j) = u;
+              }
+            }
+          }
+        }
+        more = c.u + count < c.u1;
+        if (more) {
+          tc_soft_sync();   // the item's bounds are read no more
+          if (tid == 0) {
+            it.w.u += count;
+            it.w.next_item(a, kTcRows);
+          }
+        }
+      }
+    }
+  }
+  // every MMA has been waited for (odone), or, after a time-out, gets its time here
+  __syncthreads();
+  if (*s_dead && tid == 0) drain_ring(full, kTcRing, *s_issued);
+  if (*s_dead && tid == 32) {
+    const unsigned long long dl = global_ns() + 1000000ull;   // 1 ms: far longer than what is in flight takes
+    while (global_ns() < dl) {
+    }
+  }
+  __syncthreads();
+  __syncwarp();
+  if (warp == 13)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
+}
+
+template <int D>
+size_t tc_smem() {
+  return (size_t)TcLayout<D>::kBytes + 1024;
+}
+
+template <int D, bool kHalf>
+cudaError_t tc_launch(const PagedAttnArgs& a, const CUtensorMap& map, int ctas, cudaStream_t st) {
+  static DeviceOnce configured;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!configured.done(dev)) {
+    e = cudaFuncSetAttribute(paged_attn_tc_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)tc_smem<D>());
+    if (e != cudaSuccess) return e;
+    configured.mark(dev);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = tc_smem<D>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<D, kHalf>, a, map);
+}
+
+}  // namespace
+
+size_t paged_tc_rec_floats(int d) { return (size_t)2 * kTcRows * (d + 2); }
+
+cudaError_t launch_paged_attention_tc(const PagedAttnArgs& a, const CUtensorMap& map, int d, int dtype, int ctas,
+                                      cudaStream_t st) {
+  const bool half = dtype == FUTR_DTYPE_F16;
+  if (d == 128) return half ? tc_launch<128, true>(a, map, ctas, st) : tc_launch<128, false>(a, map, ctas, st);
+  return half ? tc_launch<64, true>(a, map, ctas, st) : tc_launch<64, false>(a, map, ctas, st);
+}
+
+}  // namespace futr

@@ -176,6 +176,35 @@ ATTN = [
 ]
 
 
+# many rows a sequence: heads, kv-heads, d, page, dtype, fused, window, positions, rows
+CHUNKS = [
+    (4, 4, 128, 64, torch.bfloat16, False, 0, [0], [128]),
+    (4, 4, 128, 64, torch.bfloat16, False, 0, [1], [129]),
+    (8, 2, 128, 16, torch.bfloat16, True, 0, [0], [64]),
+    (32, 8, 128, 64, torch.bfloat16, True, 0, [700, 0, 130], [130, 65, 1]),
+    (8, 2, 128, 128, torch.float16, False, 0, [250], [257]),
+    (16, 2, 128, 32, torch.bfloat16, False, 200, [1000, 0], [90, 300]),
+    (16, 1, 128, 32, torch.bfloat16, False, 0, [77], [100]),
+    (10, 2, 64, 16, torch.float16, True, 0, [33, 500, 4], [60, 200, 0]),
+    (8, 8, 64, 128, torch.bfloat16, False, 50, [0, 10], [256, 255]),
+    (28, 4, 128, 64, torch.float16, False, 0, [2000, 1], [3, 150]),
+    (4, 1, 64, 64, torch.bfloat16, False, 0, [3000], [500]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CHUNKS)))
+def test_attention_chunks(case):
+    heads, hkv, d, page, dtype, fused, window, pos, counts = CHUNKS[case]
+    width = -(-max(p + n for p, n in zip(pos, counts)) // page) + 1
+    c = Paged(heads, hkv, d, page, len(pos), width)
+    c.fill(case)
+    q = rows(sum(counts), heads, d, dtype, case + 70, fused)
+    got = run_attention(c, q, pos, counts, window)
+    check_attention(c, q, got, pos, counts, window)
+    for _ in range(3):
+        assert torch.equal(run_attention(c, q, pos, counts, window), got)   # no sum depends on timing
+
+
 def run_attention(c, q, pos, counts, window=0, start=True, scale=0.0, layer=0):
     out = torch.full((q.shape[0] + 2, c.heads, c.d), 7.0, dtype=q.dtype, device="cuda")
     futr.futr_paged_attention(c.cache, layer, len(pos), ints(pos), starts(counts) if start else None, c.table, q,
@@ -209,6 +238,21 @@ def test_attention(case):
     assert torch.equal(again, got)   # no sum depends on timing
     if all(n == 1 for n in counts):
         assert torch.equal(run_attention(c, q, pos, counts, window, start=False, layer=1), got)
+
+
+def test_pages_before_the_window_are_not_read():
+    """A program may give pages back that no row can see any more."""
+    c = Paged(8, 2, 128, 16, 2, 40)
+    c.fill(2)
+    for counts in ([1, 1], [100, 90]):
+        pos, window = [400, 371], 60
+        q = rows(sum(counts), 8, 128, torch.bfloat16, 8)
+        got = run_attention(c, q, pos, counts, window)
+        table = c.table.clone()
+        for b in range(2):
+            c.table[b, :(pos[b] - window + 1) // 16] = -1
+        assert torch.equal(run_attention(c, q, pos, counts, window), got)
+        c.table = table
 
 
 def test_attention_scale_and_large_scores():
