@@ -39,7 +39,6 @@ constexpr int kTcRing = 2;
 
 template <int D>
 struct TcLayout {
-  static constexpr int kBlk = D / 64;                            // 64-dim blocks of an operand row
   static constexpr int kOp = kTcHalf * D * 2;                    // one f16 operand of 128 rows
   static constexpr int kQ = 0;                                   // two halves
   static constexpr int kK = kQ + 2 * kOp;
@@ -144,64 +143,114 @@ __device__ __forceinline__ int tc_at(int r, int i) {
 
 // The rows of one half that belong to this softmax warp (32 of them), rotated,
 // divided by a power of two and stored as f16 (rows past `valid` as zeros); their
-// score factors to qs.
+// score factors to qs.  A lane holds the rotation pairs 2 lane, 2 lane + 1 (D = 64:
+// pair `lane`) of a row; the loads of eight rows are in flight together.
 template <int D, bool kHalf>
 __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Walk& w, int valid, int half, uint8_t* q16,
                                                 float* qs) {
-  constexpr int J = D / 32, RW = 4;   // rows whose loads are in flight together
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  constexpr int P = D / 64, RW = 8;   // pairs of a lane, rows at a time
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, at = P * lane;
 #pragma unroll 1
   for (int r0 = 32 * warp; r0 < 32 * warp + 32; r0 += RW) {
-    uint16_t u[RW][J];
-    float2 cs[RW][J / 2];
+    uint32_t lo[RW], hi[RW];
+    float2 cs[RW][P];
+    int row = w.rt * kTcRows + kTcHalf * half + r0, i = row / a.G, g = row - i * a.G;
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
-      const int r = kTcHalf * half + r0 + k;
-      if (r < valid) {
-        const int row = w.rt * kTcRows + r, i = row / a.G, head = w.kvh * a.G + row - i * a.G;
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (size_t)(w.row0 + i) * a.ld_q + (size_t)head * D;
+      lo[k] = hi[k] = 0u;
 #pragma unroll
-        for (int j = 0; j < J; ++j) u[k][j] = q[lane + 32 * j];
-        if (a.c.rope) {
-#pragma unroll
-          for (int j = 0; j < J / 2; ++j) cs[k][j] = a.c.rope[(size_t)(w.p0 + i) * (D / 2) + lane + 32 * j];
+      for (int j = 0; j < P; ++j) cs[k][j] = make_float2(1.f, 0.f);
+      if (kTcHalf * half + r0 + k < valid) {
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (size_t)(w.row0 + i) * a.ld_q +
+                            (size_t)(w.kvh * a.G + g) * D + at;
+        if (P == 2) {
+          lo[k] = *reinterpret_cast<const uint32_t*>(q);
+          hi[k] = *reinterpret_cast<const uint32_t*>(q + D / 2);
+        } else {
+          lo[k] = *q;
+          hi[k] = q[D / 2];
         }
+        if (a.c.rope) {
+          const float2* c = a.c.rope + (size_t)(w.p0 + i) * (D / 2) + at;
+#pragma unroll
+          for (int j = 0; j < P; ++j) cs[k][j] = c[j];
+        }
+      }
+      if (++g == a.G) {
+        g = 0;
+        ++i;
       }
     }
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
-      const int r = kTcHalf * half + r0 + k;
-      float x[J], factor = 0.f;
+      float x[2][P], mx = 0.f;
 #pragma unroll
-      for (int j = 0; j < J; ++j) x[j] = 0.f;
-      if (r < valid) {
-#pragma unroll
-        for (int j = 0; j < J; ++j) x[j] = widen<kHalf>(u[k][j]);
-        if (a.c.rope) {
-#pragma unroll
-          for (int j = 0; j < J / 2; ++j) {
-            const float x1 = x[j], x2 = x[j + J / 2];
-            x[j] = x1 * cs[k][j].x - x2 * cs[k][j].y;
-            x[j + J / 2] = x2 * cs[k][j].x + x1 * cs[k][j].y;
-          }
-        }
-        float mx = 0.f;
-#pragma unroll
-        for (int j = 0; j < J; ++j) mx = fmaxf(mx, fabsf(x[j]));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int j = 0; j < J; ++j) x[j] *= inv;
-        factor = __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+      for (int j = 0; j < P; ++j) {
+        const float x1 = widen<kHalf>((uint16_t)(lo[k] >> (16 * j))), x2 = widen<kHalf>((uint16_t)(hi[k] >> (16 * j)));
+        x[0][j] = x1 * cs[k][j].x - x2 * cs[k][j].y;
+        x[1][j] = x2 * cs[k][j].x + x1 * cs[k][j].y;
+        mx = fmaxf(mx, fmaxf(fabsf(x[0][j]), fabsf(x[1][j])));
       }
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        *reinterpret_cast<__half*>(q16 + tc_at(r0 + k, lane + 32 * j)) = __float2half_rn(x[j]);
-      if (lane == 0) qs[kTcHalf * half + r0 + k] = factor;
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint8_t* dst = q16 + tc_at(r0 + k, at + h * (D / 2));
+        if (P == 2)
+          *reinterpret_cast<uint32_t*>(dst) = pack_half2(x[h][0] * inv, x[h][P - 1] * inv);
+        else
+          *reinterpret_cast<__half*>(dst) = __float2half_rn(x[h][0] * inv);
+      }
+      if (lane == 0)
+        qs[kTcHalf * half + r0 + k] =
+            kTcHalf * half + r0 + k < valid ? __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2 : 0.f;
     }
   }
+}
+
+// The largest x = s f + b of a row over the 32 columns from c (s in tensor memory,
+// 16 columns to a factor and a term; f >= 0), those outside low .. top left out.
+template <bool kCut>
+__device__ __forceinline__ float tc_max32(uint32_t ts, int c, float f0, float f1, float b0, float b1, int low, int top) {
+  float x[32];
+  tc_ld32(ts + 32 * c, x);
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (kCut && (32 * c + j > top || 32 * c + j < low)) x[j] = -INFINITY;
+    if (j < 16)
+      m0 = fmaxf(m0, x[j]);
+    else
+      m1 = fmaxf(m1, x[j]);
+  }
+  // (-inf marks an empty set: it must not meet a factor of 0)
+  m0 = m0 == -INFINITY ? m0 : fmaf(m0, f0, b0);
+  m1 = m1 == -INFINITY ? m1 : fmaf(m1, f1, b1);
+  return fmaxf(m0, m1);
+}
+
+// Their weights 2^(s f + b), as f16 over scores 16 c .. 16 c + 15 (which have been
+// read), and the sums of each 16.
+template <bool kCut>
+__device__ __forceinline__ void tc_weights32(uint32_t ts, int c, float f0, float f1, float b0, float b1, int low, int top,
+                                             float& sum0, float& sum1) {
+  float x[32];
+  uint32_t h[16];
+  tc_ld32(ts + 32 * c, x);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    x[j] = fmaf(x[j], j < 16 ? f0 : f1, j < 16 ? b0 : b1);
+    if (kCut && (32 * c + j > top || 32 * c + j < low)) x[j] = -INFINITY;
+    x[j] = pa_ex2(x[j]);
+    s[(j >> 4) * 2 + (j & 1)] += x[j];
+    if (j & 1) h[j >> 1] = pack_half2(x[j - 1], x[j]);
+  }
+  sum0 = s[0] + s[1];
+  sum1 = s[2] + s[3];
+  tc_st16(ts + 16 * c, h);
 }
 
 // The bounds of the current part from its walk (one thread).
@@ -461,16 +510,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float mx = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              float x[32];
-              tc_ld32(ts + 32 * c, x);
               const float4 s0 = sc[2 * c], s1 = sc[2 * c + 1];
               const float f0 = s0.x * qf, f1 = s1.x * qf;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                x[j] = fmaf(x[j], j < 16 ? f0 : f1, j < 16 ? s0.y : s1.y);
-                if (cut && (32 * c + j > top || 32 * c + j < low)) x[j] = -INFINITY;
-                mx = fmaxf(mx, x[j]);
-              }
+              mx = fmaxf(mx, cut ? tc_max32<true>(ts, c, f0, f1, s0.y, s1.y, low, top)
+                                 : tc_max32<false>(ts, c, f0, f1, s0.y, s1.y, low, top));
             }
             // the reference moves when the maximum has outgrown it by 2^8 (or it has none yet)
             const bool grow = mx > M + 8.f || (M == -INFINITY && mx > M);
@@ -495,26 +538,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              float x[32];
-              tc_ld32(ts + 32 * c, x);
               const float4 s0 = sc[2 * c], s1 = sc[2 * c + 1];
-              const float f0 = s0.x * qf, f1 = s1.x * qf, b0 = s0.y - ref, b1 = s1.y - ref;
-              float sum0 = 0.f, sum1 = 0.f;
-              uint32_t h[16];
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                float y = fmaf(x[j], j < 16 ? f0 : f1, j < 16 ? b0 : b1);
-                if (cut && (32 * c + j > top || 32 * c + j < low)) y = -INFINITY;
-                x[j] = pa_ex2(y);
-                if (j < 16)
-                  sum0 += x[j];
-                else
-                  sum1 += x[j];
-              }
+              const float f0 = s0.x * qf, f1 = s1.x * qf;
+              float sum0, sum1;
+              if (cut)
+                tc_weights32<true>(ts, c, f0, f1, s0.y - ref, s1.y - ref, low, top, sum0, sum1);
+              else
+                tc_weights32<false>(ts, c, f0, f1, s0.y - ref, s1.y - ref, low, top, sum0, sum1);
               L = fmaf(sum0, s0.z, fmaf(sum1, s1.z, L));
-#pragma unroll
-              for (int j = 0; j < 16; ++j) h[j] = pack_half2(x[2 * j], x[2 * j + 1]);
-              tc_st16(ts + 16 * c, h);   // over scores 16 c .. 16 c + 15, read above or before
             }
             tc_wait_st();
             tc_fence_before();
@@ -593,20 +624,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                          pa_ex2(__ldcg(rn + (size_t)k * 2 * kRec + r) - ref), sum);
             const float inv = sum != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
 #pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {   // 16 dims at a time
-              float4 acc[4];
+            for (int q = 0; q < D / 32; ++q) {   // 32 dims at a time
+              float4 acc[8];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+              for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
               for (int k = -1; k < nc; ++k) {
                 const float* src = k < 0 ? r0 : rn + (size_t)k * 2 * kRec;
                 const float wt = pa_ex2(__ldcg(src + r) - ref);
-                float4 v[4];
+                float4 v[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  v[j] = __ldcg(reinterpret_cast<const float4*>(src + 2 * kRecRow) + (4 * q + j) * kTcRows + r);
+                for (int j = 0; j < 8; ++j)
+                  v[j] = __ldcg(reinterpret_cast<const float4*>(src + 2 * kRecRow) + (8 * q + j) * kTcRows + r);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 8; ++j) {
                   acc[j].x = fmaf(v[j].x, wt, acc[j].x);
                   acc[j].y = fmaf(v[j].y, wt, acc[j].y);
                   acc[j].z = fmaf(v[j].z, wt, acc[j].z);
@@ -614,13 +645,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
               }
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
+              for (int j = 0; j < 4; ++j) {
                 uint4 u;
                 u.x = narrow2<kHalf>(acc[2 * j].x * inv, acc[2 * j].y * inv);
                 u.y = narrow2<kHalf>(acc[2 * j].z * inv, acc[2 * j].w * inv);
                 u.z = narrow2<kHalf>(acc[2 * j + 1].x * inv, acc[2 * j + 1].y * inv);
                 u.w = narrow2<kHalf>(acc[2 * j + 1].z * inv, acc[2 * j + 1].w * inv);
-                *reinterpret_cast<uint4*>(out + 16 * q + 8 * j) = u;
+                *reinterpret_cast<uint4*>(out + 32 * q + 8 * j) = u;
               }
             }
           }
