@@ -36,6 +36,7 @@ constexpr int kTcRows = 256, kTcHalf = 128;
 constexpr int kTcThreads = 14 * 32;
 constexpr int kTcSoft = 8 * 32;                 // softmax threads
 constexpr int kTcRing = 2;
+constexpr float kTiny = 1.17549435e-38f;
 
 template <int D>
 struct TcLayout {
@@ -62,23 +63,30 @@ __device__ __forceinline__ void tc_soft_sync() { asm volatile("bar.sync 1, %0;" 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 columns of this thread's lane; the values are there after tc_wait_ld.
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t u[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
       "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
-        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
-        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr)
       : "memory");
-  tc_wait_ld();
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+}
+
+// The wait for loads, tied to the values it makes valid.
+__device__ __forceinline__ void tc_wait_ld32(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
 }
 
 __device__ __forceinline__ void tc_st32(uint32_t taddr, const float (&v)[32]) {
@@ -150,11 +158,11 @@ __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Wa
                                                 float* qs) {
   constexpr int P = D / 64, RW = 8;   // pairs of a lane, rows at a time
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, at = P * lane;
-#pragma unroll 1
-  for (int r0 = 32 * warp; r0 < 32 * warp + 32; r0 += RW) {
-    uint32_t lo[RW], hi[RW];
-    float2 cs[RW][P];
-    int row = w.rt * kTcRows + kTcHalf * half + r0, i = row / a.G, g = row - i * a.G;
+  uint32_t lo[RW], hi[RW];
+  float2 cs[RW][P];
+  auto load = [&](int r0) {
+    const int row = w.rt * kTcRows + kTcHalf * half + r0;
+    int i = row / a.G, g = row - i * a.G;
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
       lo[k] = hi[k] = 0u;
@@ -172,8 +180,13 @@ __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Wa
         }
         if (a.c.rope) {
           const float2* c = a.c.rope + (size_t)(w.p0 + i) * (D / 2) + at;
-#pragma unroll
-          for (int j = 0; j < P; ++j) cs[k][j] = c[j];
+          if (P == 2) {
+            const float4 c2 = *reinterpret_cast<const float4*>(c);
+            cs[k][0] = make_float2(c2.x, c2.y);
+            cs[k][P - 1] = make_float2(c2.z, c2.w);
+          } else {
+            cs[k][0] = *c;
+          }
         }
       }
       if (++g == a.G) {
@@ -181,6 +194,10 @@ __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Wa
         ++i;
       }
     }
+  };
+#pragma unroll 1
+  for (int r0 = 32 * warp; r0 < 32 * warp + 32; r0 += RW) {
+    load(r0);
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
       float x[2][P], mx = 0.f;
@@ -191,8 +208,8 @@ __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Wa
         x[1][j] = x2 * cs[k][j].x + x1 * cs[k][j].y;
         mx = fmaxf(mx, fmaxf(fabsf(x[0][j]), fabsf(x[1][j])));
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // the largest magnitude: magnitudes order like their bits
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
       const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
       const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
@@ -210,47 +227,99 @@ __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Wa
   }
 }
 
-// The largest x = s f + b of a row over the 32 columns from c (s in tensor memory,
-// 16 columns to a factor and a term; f >= 0), those outside low .. top left out.
-template <bool kCut>
-__device__ __forceinline__ float tc_max32(uint32_t ts, int c, float f0, float f1, float b0, float b1, int low, int top) {
-  float x[32];
-  tc_ld32(ts + 32 * c, x);
-  float m0 = -INFINITY, m1 = -INFINITY;
+// The 16-column factors and terms of 32 columns: x = s f + b.
+struct TcScale {
+  float f0, f1, b0, b1;
+};
+
+// Columns of the chunk of 32 at column c that a row does not see (outside low ..
+// top) to -inf.
+__device__ __forceinline__ void tc_mask(float (&x)[32], int c, int low, int top) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    if (kCut && (32 * c + j > top || 32 * c + j < low)) x[j] = -INFINITY;
-    if (j < 16)
-      m0 = fmaxf(m0, x[j]);
-    else
-      m1 = fmaxf(m1, x[j]);
-  }
-  // (-inf marks an empty set: it must not meet a factor of 0)
-  m0 = m0 == -INFINITY ? m0 : fmaf(m0, f0, b0);
-  m1 = m1 == -INFINITY ? m1 : fmaf(m1, f1, b1);
-  return fmaxf(m0, m1);
+  for (int j = 0; j < 32; ++j)
+    if (c + j > top || c + j < low) x[j] = -INFINITY;
 }
 
-// Their weights 2^(s f + b), as f16 over scores 16 c .. 16 c + 15 (which have been
-// read), and the sums of each 16.
-template <bool kCut>
-__device__ __forceinline__ void tc_weights32(uint32_t ts, int c, float f0, float f1, float b0, float b1, int low, int top,
-                                             float& sum0, float& sum1) {
-  float x[32];
-  uint32_t h[16];
-  tc_ld32(ts + 32 * c, x);
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+// The largest s f + b of 32 columns (f > 0; -inf where nothing is seen).
+__device__ __forceinline__ float tc_max(const float (&s)[32], const TcScale& t) {
+  float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    x[j] = fmaf(x[j], j < 16 ? f0 : f1, j < 16 ? b0 : b1);
-    if (kCut && (32 * c + j > top || 32 * c + j < low)) x[j] = -INFINITY;
-    x[j] = pa_ex2(x[j]);
-    s[(j >> 4) * 2 + (j & 1)] += x[j];
-    if (j & 1) h[j >> 1] = pack_half2(x[j - 1], x[j]);
+  for (int j = 0; j < 16; ++j) {
+    m0 = fmaxf(m0, s[j]);
+    m1 = fmaxf(m1, s[16 + j]);
   }
-  sum0 = s[0] + s[1];
-  sum1 = s[2] + s[3];
-  tc_st16(ts + 16 * c, h);
+  return fmaxf(fmaf(m0, t.f0, t.b0), fmaf(m1, t.f1, t.b1));
+}
+
+// Their weights 2^(s f + b - ref) as f16, and the sums of each 16.  (A masked score
+// of -inf has weight 0: f > 0 wherever a position is seen; a row whose factor is 0
+// has weights that nothing reads.)
+__device__ __forceinline__ void tc_weights(const float (&s)[32], const TcScale& t, float ref, uint32_t (&h)[16],
+                                           float& sum0, float& sum1) {
+  const float b0 = t.b0 - ref, b1 = t.b1 - ref;
+  float q[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    float w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i] = pa_ex2(fmaf(s[j + i], j < 16 ? t.f0 : t.f1, j < 16 ? b0 : b1));
+      q[(j >> 4) * 2 + i] += w[i];
+    }
+    h[j >> 1] = pack_half2(w[0], w[1]);
+  }
+  sum0 = q[0] + q[1];
+  sum1 = q[2] + q[3];
+}
+
+__device__ __forceinline__ TcScale tc_scale_of(const float4* sc, int c, float qf) {
+  const float4 s0 = sc[2 * c], s1 = sc[2 * c + 1];
+  // (a factor of 0 must not meet a masked score of -inf)
+  return TcScale{fmaxf(s0.x * qf, kTiny), fmaxf(s1.x * qf, kTiny), s0.y, s1.y};
+}
+
+// A row's maximum over the tile, chunks of 32 columns, the next one's load under
+// way.  With and without a mask apart: the comparisons would cost every tile half
+// as much again; loops of two chunks: unrolled further, the roles' code no longer
+// fits the instruction cache (132 us for a call that takes MEASURED us like this).
+// A row's maximum over the tile, chunks of 32 columns.  With and without a mask
+// apart: the comparisons would cost every tile half as much again.  Rolled loops:
+// unrolled, with the next chunk's load under way, the roles' code no longer fits the
+// instruction cache (a call that takes 110 us like this took 132 us).
+template <bool kCut>
+__device__ __forceinline__ float tc_row_max(uint32_t ts, const float4* sc, float qf, int low, int top) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    float x[32];
+    tc_ld32(ts + 32 * c, x);
+    const TcScale t = tc_scale_of(sc, c, qf);
+    tc_wait_ld32(x);
+    if (kCut) tc_mask(x, 32 * c, low, top);
+    mx = fmaxf(mx, tc_max(x, t));
+  }
+  return mx;
+}
+
+// Its weights, over scores that have been read (chunk c's to columns 16 c .. 16 c +
+// 15); returns their sum with each 16 columns times their inverse value scale.
+template <bool kCut>
+__device__ __forceinline__ float tc_row_weights(uint32_t ts, const float4* sc, float qf, float ref, int low, int top) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    float x[32];
+    tc_ld32(ts + 32 * c, x);
+    const TcScale t = tc_scale_of(sc, c, qf);
+    tc_wait_ld32(x);
+    if (kCut) tc_mask(x, 32 * c, low, top);
+    uint32_t h[16];
+    float sum0, sum1;
+    tc_weights(x, t, ref, h, sum0, sum1);
+    sum = fmaf(sum0, sc[2 * c].z, fmaf(sum1, sc[2 * c + 1].z, sum));
+    tc_st16(ts + 16 * c, h);
+  }
+  return sum;
 }
 
 // The bounds of the current part from its walk (one thread).
@@ -318,6 +387,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_trigger();
   pdl_wait();
   const int cta = blockIdx.x, page = a.c.page, plog = a.c.page_log2;
+  TcItem& it = s_item;
+  if (warp == 0) {
+    Walk w;
+    Cut cut;
+    const bool active = find_share(a, kTcRows, cta, gridDim.x, w, cut, cta == 0);
+    if (lane == 0) {
+      it.w = w;
+      it.cut = cut;
+      it.active = active;
+    }
+  }
+  __syncthreads();
+  // each role steps its own copy
+  const bool active = it.active;
+  Walk w = it.w;
+  __syncthreads();
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {   // in dead mode: nothing to wait for
     if (ok && !pa_wait(bar, parity, a.err)) {
@@ -330,9 +415,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == 12) {
     // ---------------------------------------------------------- producer --
-    Walk w;
-    Cut cut;
-    if (find_share(a, kTcRows, cta, gridDim.x, w, cut, false)) {
+    if (active) {
       int issued = 0;
       if (!produce_tiles<D>(a, &map, kTcRows, w, smem + Lay::kStage, s_raw, full, empty, kTcRing, issued)) {
         record_timeout(a.err);
@@ -342,9 +425,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 13) {
     // ------------------------------------------------------------ issuer --
-    Walk w;
-    Cut cut;
-    if (find_share(a, kTcRows, cta, gridDim.x, w, cut, false) && lane == 0) {
+    if (active && lane == 0) {
       uint32_t t = 0, done[2] = {0, 0};   // tiles begun; P V issued by half
       uint32_t part = 0, part1 = 0;       // parts, and parts with a second half
       const uint32_t q16 = smem_u32(smem + Lay::kQ), k16 = smem_u32(smem + Lay::kK), v16 = smem_u32(smem + Lay::kV);
@@ -400,54 +481,63 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------- widening --
-    Walk w;
-    Cut cut;
-    if (find_share(a, kTcRows, cta, gridDim.x, w, cut, false)) {
-      // A quarter-warp takes 4 chunks (of 16 codes) of rows r and r ^ 5: neither its
-      // reads of the 8-bit rows nor its writes of the f16 rows meet a bank twice.
-      constexpr int CH = D / 16, kQr = CH / 4;          // chunks of a row; column quarters
-      const int wg = warp - 8, qd = lane >> 3, l = lane & 7;
+    // A quarter-warp takes 4 chunks (of 16 codes) of rows r and r ^ 5: neither its
+    // reads of the 8-bit rows nor its writes of the f16 rows meet a bank twice.
+    if (active) {
+      constexpr int kQr = D / 64;                       // column quarters of 64 codes
+      const int wg = warp - 8, l = lane & 7, qd = lane >> 3;
       const int rl = (l >> 2) ? (qd ^ 5) : qd;          // row within 8
+      // offsets of this lane's chunk: in the f16 operand, and of its four rows in a tile
+      const int r0 = 32 * wg + rl;
+      const int d0 = r0 * 128 + (((2 * (l & 3)) ^ rl) << 4), d1 = r0 * 128 + (((2 * (l & 3) + 1) ^ rl) << 4);
+      const int sr = D == 128 ? rl : (rl >> 1) & 3;
+      int src[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int r = r0 + 8 * g;
+        src[g] = (r >> plog) * (2 * page * D) + (r & (page - 1)) * D;
+      }
       uint32_t t = 0, told[2] = {0, 0};   // tiles; arrivals at sfull by half
       while (w.u < w.u1) {
         const int first = w.t.t0 + (int)(w.u - w.item0);
         const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);
         const int nh = min(kTcRows, w.n * a.G - w.rt * kTcRows) > kTcHalf ? 2 : 1;
-        const int written = w.p0 + w.n;
         for (int i = 0; i < count; ++i, ++t) {
           const int slot = t % kTcRing;
           wait(&full[slot], (t / kTcRing) & 1u);
           const uint8_t* st = smem + Lay::kStage + slot * (2 * kPaTile * D);
-          const float4* raw = s_raw + slot * kPaSub;
+          const float4 raw = s_raw[slot * kPaSub + (lane & (kPaSub - 1))];
+          // what was never written, or lies on a missing page, becomes zeros
+          const int left = w.p0 + w.n - (first + i) * kPaTile;   // written positions from the tile's first
+          const unsigned gone = __ballot_sync(0xffffffffu, lane < kPaSub && raw.y == -INFINITY);
+          const bool plain = left >= kPaTile && gone == 0u;
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             // the operand buffer is free once the MMAs of the tile before have read it
             if (t > 0) wait(kv ? vfree : kfree, (t - 1) & 1u);
             uint8_t* dst = smem + (kv ? Lay::kV : Lay::kK);
+            const uint8_t* from = st + kv * page * D;
             if (ok) {
-#pragma unroll
+#pragma unroll 2
               for (int g = 0; g < 4; ++g) {
-                const int r = 32 * wg + 8 * g + rl;     // position in the tile
-                // what was never written, or lies on a missing page, becomes zeros
-                const bool live = (first + i) * kPaTile + r < written && raw[r >> 4].y != -INFINITY;
-                const uint8_t* src = st + (r >> plog) * (2 * page * D) + ((r & (page - 1)) + kv * page) * D;
-                const int sr = D == 128 ? r & 7 : (r >> 1) & 3;
 #pragma unroll
                 for (int h = 0; h < kQr; ++h) {
-                  const int c = 4 * h + (l & 3);
-                  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                  if (live) v = *reinterpret_cast<const uint4*>(src + ((c ^ sr) << 4));
+                  uint4 v = *reinterpret_cast<const uint4*>(from + src[g] + (((4 * h + (l & 3)) ^ sr) << 4));
+                  if (!plain) {
+                    const int r = r0 + 8 * g;
+                    if (r >= left || ((gone >> (r >> 4)) & 1u)) v = make_uint4(0u, 0u, 0u, 0u);
+                  }
                   uint4 o0, o1;
                   cvt4(v.x, o0.x, o0.y);
                   cvt4(v.y, o0.z, o0.w);
                   cvt4(v.z, o1.x, o1.y);
                   cvt4(v.w, o1.z, o1.w);
-                  *reinterpret_cast<uint4*>(dst + tc_at(r, 16 * c)) = o0;
-                  *reinterpret_cast<uint4*>(dst + tc_at(r, 16 * c + 8)) = o1;
+                  *reinterpret_cast<uint4*>(dst + d0 + g * 1024 + h * (kTcHalf * 128)) = o0;
+                  *reinterpret_cast<uint4*>(dst + d1 + g * 1024 + h * (kTcHalf * 128)) = o1;
                 }
               }
             }
-            if (kv == 0 && wg == 0 && lane < kPaSub) s_scale[(t & 1) * kPaSub + lane] = raw[lane];
+            if (kv == 0 && wg == 0 && lane < kPaSub) s_scale[(t & 1) * kPaSub + lane] = raw;
             tc_proxy_fence();
             // (an arrival counts for this tile once the tile before is complete)
             if (kv == 0)
@@ -472,19 +562,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int half = warp >> 2, row = tid & (kTcHalf - 1);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tm + lanes + 128 * half, to = tm + lanes + 256 + D * half;
-    TcItem& it = s_item;
-    if (warp == 0) {
-      Walk w;
-      Cut cut;
-      const bool active = find_share(a, kTcRows, cta, gridDim.x, w, cut, cta == 0);
-      if (lane == 0) {
-        it.w = w;
-        it.cut = cut;
-        it.active = active;
-      }
-    }
-    tc_soft_sync();
-    if (it.active) {
+    if (active) {
       uint32_t t = 0, mine = 0;   // tiles of the CTA; tiles of this half
       for (bool more = true; more;) {
         if (tid == 0) tc_set(a, it);
@@ -507,14 +585,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const float4* sc = s_scale + ((t + i) & 1) * kPaSub;
             const int top = p - pos0, low = top - back;   // columns low .. top are visible
             const bool cut = __any_sync(0xffffffffu, top < kPaTile - 1 || low > 0);
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const float4 s0 = sc[2 * c], s1 = sc[2 * c + 1];
-              const float f0 = s0.x * qf, f1 = s1.x * qf;
-              mx = fmaxf(mx, cut ? tc_max32<true>(ts, c, f0, f1, s0.y, s1.y, low, top)
-                                 : tc_max32<false>(ts, c, f0, f1, s0.y, s1.y, low, top));
-            }
+            const float mx = cut ? tc_row_max<true>(ts, sc, qf, low, top) : tc_row_max<false>(ts, sc, qf, low, top);
             // the reference moves when the maximum has outgrown it by 2^8 (or it has none yet)
             const bool grow = mx > M + 8.f || (M == -INFINITY && mx > M);
             if (__any_sync(0xffffffffu, grow)) {
@@ -529,6 +600,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int c = 0; c < D / 32; ++c) {
                   float o[32];
                   tc_ld32(to + 32 * c, o);
+                  tc_wait_ld32(o);
 #pragma unroll
                   for (int j = 0; j < 32; ++j) o[j] *= corr;
                   tc_st32(to + 32 * c, o);
@@ -536,17 +608,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
             const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const float4 s0 = sc[2 * c], s1 = sc[2 * c + 1];
-              const float f0 = s0.x * qf, f1 = s1.x * qf;
-              float sum0, sum1;
-              if (cut)
-                tc_weights32<true>(ts, c, f0, f1, s0.y - ref, s1.y - ref, low, top, sum0, sum1);
-              else
-                tc_weights32<false>(ts, c, f0, f1, s0.y - ref, s1.y - ref, low, top, sum0, sum1);
-              L = fmaf(sum0, s0.z, fmaf(sum1, s1.z, L));
-            }
+            L += cut ? tc_row_weights<true>(ts, sc, qf, ref, low, top) : tc_row_weights<false>(ts, sc, qf, ref, low, top);
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -576,6 +638,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int k = 0; k < D / 32; ++k) {
             float o[32];
             tc_ld32(to + 32 * k, o);
+            tc_wait_ld32(o);
             if (row_ok && whole) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {

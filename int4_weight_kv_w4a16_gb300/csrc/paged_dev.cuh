@@ -53,6 +53,18 @@ __device__ __forceinline__ uint32_t narrow2(float a, float b) {
 
 // ------------------------------------------------------------------ shares --
 
+// a / b for a >= 0, b > 0, on the path to the first copy: unit counts are small
+// numbers in all but the longest calls, and there one fp32 division, off by one
+// at most, with its remainder checked costs a fraction of an integer division.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  if (((a | b) >> 21) != 0) return a / b;
+  int q = (int)__fdividef((float)(int)a, (float)(int)b);
+  const int r = (int)a - q * (int)b;
+  if (r < 0) --q;
+  if (r >= (int)b) ++q;
+  return q;
+}
+
 // Row tile rt of a sequence (n rows from position p0, G query heads a kv-head,
 // R rows a tile): its tiles [t0, t1).
 struct TileRange {
@@ -78,18 +90,6 @@ __device__ __forceinline__ long long seq_tiles(int n, int p0, int G, int R, int 
     w += t.t1 - t.t0;
   }
   return w;
-}
-
-// a / b for a >= 0, b > 0, on the path to the first copy: unit counts are small
-// numbers in all but the longest calls, and there one fp32 division, off by one
-// at most, with its remainder checked costs a fraction of an integer division.
-__device__ __forceinline__ long long quot(long long a, long long b) {
-  if (((a | b) >> 21) != 0) return a / b;
-  int q = (int)__fdividef((float)(int)a, (float)(int)b);
-  const int r = (int)a - q * (int)b;
-  if (r < 0) --q;
-  if (r >= (int)b) ++q;
-  return q;
 }
 
 // `total` units cut into `use` shares: the first `rem` of per + 1, the others of per.
