@@ -8,12 +8,17 @@
 //
 // One CTA per (touched page, kv-head, K or V): it alone writes that page's
 // codes and scale, so there are no atomics and the result does not depend on
-// any order.  A group of d/8 lanes takes one row, 8 elements a lane (one 16-byte
-// load, one 8-byte store; the rotation partner is d/16 lanes away).
+// any order.  A group of d/8 lanes takes one row, a lane the elements 4 i .. 4 i + 3
+// and their rotation partners d/2 further on, so that a table entry is read once and
+// nothing is exchanged.  A thread holds up to four rows from the maximum to the
+// codes: page / 4 rows at a time, whatever the page.
 //
-// Bound by memory for prompts (2 bytes read and 1 written per element) and by
-// latency for single tokens, whose chain is: row bounds -> table entry -> old
-// scale, and beside it row -> rotation -> maximum.
+// Bound by memory for prompts (2 bytes read and 1 written per element): 64 MB take
+// 18.3 us (3.5 TB/s; 9.5 us at the copy rate; half of it is the start of a CTA,
+// five waves of them).  Two rows a thread take 21.2 us, eight 18.4, and reading the
+// rows a second time instead of keeping them 36.  Bound by latency for single
+// tokens, whose chain is: row bounds -> table entry -> old scale, and beside it row
+// -> rotation -> maximum: 2.3 us for one, 3.9 us for 32 sequences.
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
@@ -22,7 +27,8 @@ namespace futr {
 
 namespace {
 
-constexpr int kAppThreads = 128;
+constexpr int kAppRounds = 4;                                 // rows a thread holds
+constexpr int kAppMaxThreads = 128 * (128 / 8) / kAppRounds;   // page 128, head dim 128
 
 // e4m3 of x in [-448, 448] (saturating), as bits; and back.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -48,8 +54,8 @@ __device__ __forceinline__ int scale_exp(float amax) {
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 template <bool kHalf>
-__device__ __forceinline__ void widen8(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void widen8(const uint2& lo, const uint2& hi, float (&x)[8]) {
+  const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (kHalf) {
@@ -71,45 +77,17 @@ struct AppendArgs {
   int* err;
 };
 
-// One row's 8 elements of this lane, rotated (keys) and with non-finite values
-// replaced by 0 (bad set).
 template <int D, bool kHalf>
-__device__ __forceinline__ void load_row(const AppendArgs& a, const uint16_t* row, int p, int lg, bool rotate,
-                                         float (&x)[8], bool& bad) {
-  constexpr int L = D / 8;   // lanes of a row
-  widen8<kHalf>(*reinterpret_cast<const uint4*>(row + 8 * lg), x);
-  if (rotate) {
-    const bool upper = lg >= L / 2;
-    const float4* t = reinterpret_cast<const float4*>(a.c.rope + (size_t)p * (D / 2) + 8 * (upper ? lg - L / 2 : lg));
-    float4 cs[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = t[i];
-    const float* f = reinterpret_cast<const float*>(cs);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_xor_sync(0xffffffffu, x[i], L / 2);
-      const float xc = __fmul_rn(x[i], f[2 * i]), os = __fmul_rn(o, f[2 * i + 1]);
-      x[i] = upper ? __fadd_rn(xc, os) : __fsub_rn(xc, os);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (!(fabsf(x[i]) <= 3.4028234e38f)) {
-      x[i] = 0.f;
-      bad = true;
-    }
-}
-
-template <int D, bool kHalf>
-__global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendArgs a) {
-  constexpr int L = D / 8, kRows = kAppThreads / L;   // lanes of a row, rows at a time
-  __shared__ float s_max[kAppThreads / 32];
+__global__ void __launch_bounds__(kAppMaxThreads) paged_append_kernel(const AppendArgs a) {
+  constexpr int L = D / 8;                            // lanes of a row
+  __shared__ float s_max[kAppMaxThreads / 32];
+  const int threads = blockDim.x, rows = threads / L;   // rows at a time
   const int tid = threadIdx.x, lane = tid & 31, lg = tid % L, rg = tid / L;
   const int kvh = blockIdx.y, which = blockIdx.z;
   pdl_trigger();
   pdl_wait();
   // one warp of the grid looks every sequence over (the search below stops early)
-  if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0 && tid >= kAppThreads - 32)
+  if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0 && tid >= threads - 32)
     for (int s = lane; s < a.r.batch; s += 32) {
       int r0, nn, pp;
       if (!paged_seq(a.r, a.c, s, r0, nn, pp)) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
@@ -144,32 +122,69 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendA
   if (b < 0) return;   // the grid is an upper bound
   const int page = a.c.page, pi = (p0 >> a.c.page_log2) + item;
   const int id = a.r.table[(size_t)b * a.r.table_ld + pi];
+  const int base = pi << a.c.page_log2;
+  const int lo = max(base, p0) - base, hi = min(base + page, p0 + n) - base;   // slots [lo, hi) are new
+  const uint16_t* src = (which ? a.src[1] : a.src[0]) + (size_t)kvh * D + 4 * lg;
+  const long long ld = which ? a.ld[1] : a.ld[0];
+  const bool rotate = which == 0 && a.c.rope != nullptr;
+
+  // The rows, all of them on their way before the page number is looked at.
+  float x[kAppRounds][8];
+  {
+    uint2 raw[kAppRounds][2];
+    float4 cs[kAppRounds][2];
+#pragma unroll
+    for (int i = 0; i < kAppRounds; ++i) {
+      const int slot = lo + i * rows + rg;
+      raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+      if (slot < hi) {
+        const uint16_t* row = src + (size_t)(row0 + base + slot - p0) * ld;
+        raw[i][0] = *reinterpret_cast<const uint2*>(row);
+        raw[i][1] = *reinterpret_cast<const uint2*>(row + D / 2);
+        if (rotate) {
+          const float4* t = reinterpret_cast<const float4*>(a.c.rope + (size_t)(base + slot) * (D / 2) + 4 * lg);
+          cs[i][0] = t[0];
+          cs[i][1] = t[1];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAppRounds; ++i) {
+      widen8<kHalf>(raw[i][0], raw[i][1], x[i]);
+      if (rotate && lo + i * rows + rg < hi) {
+        const float c[4] = {cs[i][0].x, cs[i][0].z, cs[i][1].x, cs[i][1].z};
+        const float n[4] = {cs[i][0].y, cs[i][0].w, cs[i][1].y, cs[i][1].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float l = x[i][j], u = x[i][4 + j];
+          x[i][j] = __fsub_rn(__fmul_rn(l, c[j]), __fmul_rn(u, n[j]));
+          x[i][4 + j] = __fadd_rn(__fmul_rn(u, c[j]), __fmul_rn(l, n[j]));
+        }
+      }
+    }
+  }
   if (id < 0 || id >= a.c.n_pages) {
     if (tid == 0) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
     return;
   }
-  const int base = pi << a.c.page_log2;
-  const int lo = max(base, p0) - base, hi = min(base + page, p0 + n) - base;   // slots [lo, hi) are new
   const size_t blk = ((size_t)id * a.c.n_kv + kvh) * 2 + which;
   uint8_t* codes = a.c.codes + blk * page * D;
   float* scale = a.c.scales + blk;
-  const uint16_t* src = a.src[which] + (size_t)kvh * D;
-  const bool rotate = which == 0 && a.c.rope != nullptr;
   // a page whose slot 0 is written starts over
   const float s_old = lo == 0 ? 0.f : *scale;
 
-  // largest magnitude; the first row of each lane group stays in registers
-  float x[8], first[8], m = 0.f;
+  // largest magnitude; what is not finite is stored as 0 and reported
+  float m = 0.f;
   bool bad = false;
-  const int rounds = (hi - lo + kRows - 1) / kRows;
-  for (int i = 0; i < rounds; ++i) {
-    const int slot = lo + i * kRows + rg;
-    const int use = slot < hi ? slot : lo;   // idle groups repeat a row: every lane takes part in the shuffles
-    load_row<D, kHalf>(a, src + (size_t)(row0 + base + use - p0) * a.ld[which], base + use, lg, rotate, x, bad);
+#pragma unroll
+  for (int i = 0; i < kAppRounds; ++i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      m = fmaxf(m, fabsf(x[j]));
-      if (i == 0) first[j] = x[j];
+      if (!(fabsf(x[i][j]) <= 3.4028234e38f)) {
+        x[i][j] = 0.f;
+        bad = true;
+      }
+      m = fmaxf(m, fabsf(x[i][j]));
     }
   }
   if (bad) set_err(a.err, FUTR_ERR_NOT_FINITE);
@@ -177,14 +192,14 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendA
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) s_max[tid >> 5] = m;
   __syncthreads();   // every thread has read the old scale by now, too
-#pragma unroll
-  for (int w = 0; w < kAppThreads / 32; ++w) m = fmaxf(m, s_max[w]);
+  for (int w = 0; w < threads / 32; ++w) m = fmaxf(m, s_max[w]);
   const float s_new = fmaxf(s_old, pow2(scale_exp(m)));
+  const float inv = __uint_as_float((254u << 23) - __float_as_uint(s_new));   // of a power of two: exact
   if (tid == 0 && s_new != s_old) *scale = s_new;
   if (s_old > 0.f && s_new > s_old) {
     // the page's other slots at the new scale, 8 codes a thread
-    const float ratio = __fdiv_rn(s_old, s_new);
-    for (int i = tid; i < page * L; i += kAppThreads) {
+    const float ratio = s_old * inv;
+    for (int i = tid; i < page * L; i += threads) {
       const int slot = i / L;
       if (slot >= lo && slot < hi) continue;
       uint2* at = reinterpret_cast<uint2*>(codes) + i;
@@ -198,22 +213,15 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendA
       *at = make_uint2(w[0], w[1]);
     }
   }
-  const float inv = __fdiv_rn(1.0f, s_new);   // exact: a power of two
-  for (int i = 0; i < rounds; ++i) {
-    const int slot = lo + i * kRows + rg;
-    const int use = slot < hi ? slot : lo;
-    if (i == 0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = first[j];
-    } else {
-      load_row<D, kHalf>(a, src + (size_t)(row0 + base + use - p0) * a.ld[which], base + use, lg, rotate, x, bad);
-    }
+  for (int i = 0; i < kAppRounds; ++i) {
+    const int slot = lo + i * rows + rg;
     if (slot < hi) {
-      uint32_t w[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        w[j] = e4m3x2(x[4 * j] * inv, x[4 * j + 1] * inv) | (e4m3x2(x[4 * j + 2] * inv, x[4 * j + 3] * inv) << 16);
-      *(reinterpret_cast<uint2*>(codes) + (size_t)slot * L + lg) = make_uint2(w[0], w[1]);
+      for (int h = 0; h < 2; ++h)
+        *(reinterpret_cast<uint32_t*>(codes + (size_t)slot * D + h * (D / 2)) + lg) =
+            e4m3x2(x[i][4 * h] * inv, x[i][4 * h + 1] * inv) |
+            (e4m3x2(x[i][4 * h + 2] * inv, x[i][4 * h + 3] * inv) << 16);
     }
   }
 }
@@ -229,7 +237,9 @@ cudaError_t launch_paged_append(const PagedView& c, const PagedRows& r, int d, i
   const long long items = bound < rows ? bound : rows;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)items, (unsigned)c.n_kv, 2);
-  cfg.blockDim = dim3(kAppThreads);
+  // a page's rows in four rounds; a single row's CTA has a row's lanes and some more,
+  // for the page's other codes when the scale grows
+  cfg.blockDim = dim3(r.start ? (unsigned)(c.page * (d / 8) / kAppRounds) : 64u);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
