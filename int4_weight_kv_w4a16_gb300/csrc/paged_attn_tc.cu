@@ -5,11 +5,12 @@
 //
 // One CTA an SM, 14 warps:
 //   warp 12      streams tiles of 128 positions (8-bit codes) into a ring;
-//   warps 8-11   widen a tile's codes to f16 (exact) into two operand buffers,
-//                keys and values: rows of 128 bytes (64 dims) with the 128-byte
+//   warps 8-11   widen a tile's codes to f16 (exact) into operand buffers, keys (one)
+//                and values (two, so that the next tile's are ready when this one's
+//                products end): rows of 128 bytes (64 dims) with the 128-byte
 //                swizzle, which is a K-major operand for Q K^T and an MN-major one
 //                for P V; once for all 256 rows;
-//   warp 13      one thread issues the MMAs (kind::f16, M 128, fp32 accumulators):
+//   warp 13      issues the MMAs (kind::f16, M 128, fp32 accumulators):
 //                S_h = Q_h K^T (operands in shared memory) and O_h += P_h V (P in
 //                tensor memory), ordered P_0 V, S_0 of the next tile, P_1 V, S_1 of
 //                the next tile, so that the softmax of one half runs under the
@@ -23,9 +24,14 @@
 // by more than 2^8: a weight up to 2^8 is a good f16, the normalizer is fp32, and
 // O, in tensor memory, is rescaled a few times an item instead of every tile.
 //
-// Bound by the tensor cores in principle (4 x 256 x 128 x D flops a tile take
-// 2048 cycles at D = 128), with 1024 to 2048 cycles of exponentials and some 600
-// of widening a scheduler beside them.
+// Bound by the tensor cores in principle (4 x 256 x 128 x D flops a tile take 2048
+// cycles at D = 128).  Measured on four prompts' chunks of 512 rows after contexts to
+// 8K, 32 heads over 8, D = 128: 93 us, 0.51 PFLOP/s of the seen positions.  A CTA's
+// 20 tiles take some 5200 cycles each (a half's softmax, 3300 while it shares the
+// schedulers with the other half's and the widening, and its products, 1024, follow
+// one another); the start, the queries of two parts and the joining of split items
+// take a third of the time.  Steps of 64 positions, whose products could run under
+// the softmax, took 104 us: twice the reads of the queries from shared memory.
 #include "paged_dev.cuh"
 
 namespace futr {
@@ -44,7 +50,7 @@ struct TcLayout {
   static constexpr int kQ = 0;                                   // two halves
   static constexpr int kK = kQ + 2 * kOp;
   static constexpr int kV = kK + kOp;
-  static constexpr int kStage = kV + kOp;                        // ring of 8-bit tiles
+  static constexpr int kStage = kV + 2 * kOp;                    // two of the values; ring of 8-bit tiles
   static constexpr int kRaw = kStage + kTcRing * 2 * kPaTile * D;   // [ring][sub-tiles] float4
   static constexpr int kScale = kRaw + kTcRing * kPaSub * 16;    // [2][sub-tiles] float4, by tile parity
   static constexpr int kQs = kScale + 2 * kPaSub * 16;           // [256] score factors
@@ -112,10 +118,8 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16])
 // Shared-memory operand descriptor with the 128-byte swizzle: rows of 128 bytes in
 // 8-row atoms of 1 KB (stride 1024); `lead`: bytes between 64-element blocks of an
 // MN-major operand (a K-major operand's block is one row wide: unused).
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
-}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t tc_desc_lo(uint32_t addr, uint32_t lead) { return (addr >> 4) | ((lead >> 4) << 16); }
 
 // Instruction descriptors: D fp32, A and B f16, M = 128; N = 128 (scores), N = D
 // with B MN-major (bit 16: values as [position][dim]).
@@ -123,25 +127,32 @@ constexpr uint32_t kIdescS = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 2
 template <int D>
 constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
 
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// The issuer's instructions: the whole warp comes here and one elected lane issues, so
+// that the operands stay in uniform registers.  Descriptors as their low words (the
+// high word is the same for all).
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(alo), "r"(blo), "r"(idesc), "r"(acc), "n"(kDescHi)
       : "memory");
 }
 
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(blo), "r"(idesc), "r"(acc), "n"(kDescHi)
       : "memory");
 }
 
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 // Byte offset of dim i of row r in an f16 operand (blocks of 64 dims, swizzled rows).
@@ -278,14 +289,11 @@ __device__ __forceinline__ TcScale tc_scale_of(const float4* sc, int c, float qf
   return TcScale{fmaxf(s0.x * qf, kTiny), fmaxf(s1.x * qf, kTiny), s0.y, s1.y};
 }
 
-// A row's maximum over the tile, chunks of 32 columns, the next one's load under
-// way.  With and without a mask apart: the comparisons would cost every tile half
-// as much again; loops of two chunks: unrolled further, the roles' code no longer
-// fits the instruction cache (132 us for a call that takes MEASURED us like this).
 // A row's maximum over the tile, chunks of 32 columns.  With and without a mask
-// apart: the comparisons would cost every tile half as much again.  Rolled loops:
-// unrolled, with the next chunk's load under way, the roles' code no longer fits the
-// instruction cache (a call that takes 110 us like this took 132 us).
+// apart: the comparisons would cost every tile half as much again.  Rolled loops over
+// 32 columns: with 64 a turn a call of 93 us took 101, unrolled 132 (the roles' code
+// no longer fits the instruction cache); a row's 128 scores held in registers, by a
+// split of the CTA's registers between the roles, 104 where this took 100.
 template <bool kCut>
 __device__ __forceinline__ float tc_row_max(uint32_t ts, const float4* sc, float qf, int low, int top) {
   float mx = -INFINITY;
@@ -344,9 +352,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* qready = empty + kTcRing;    // [2] the queries of a half are in place
   uint64_t* kready = qready + 2;         // keys widened
   uint64_t* kfree = kready + 1;          // both halves' scores are done
-  uint64_t* vready = kfree + 1;          // values widened
-  uint64_t* vfree = vready + 1;          // both halves' P V are done
-  uint64_t* sfull = vfree + 1;           // [2] scores of a half in tensor memory, scales in shared memory
+  uint64_t* vready = kfree + 1;          // [2] values widened, by the tile's parity
+  uint64_t* vfree = vready + 2;          // [2] both halves' P V are done
+  uint64_t* sfull = vfree + 2;           // [2] scores of a half in tensor memory, scales in shared memory
   uint64_t* pready = sfull + 2;          // [2] weights of a half in tensor memory
   uint64_t* odone = pready + 2;          // [2] P V of a half is done
   volatile int* s_dead = reinterpret_cast<volatile int*>(odone + 2);   // a wait ran out
@@ -362,6 +370,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&empty[i], 4);
     }
     for (int h = 0; h < 2; ++h) {
+      mbar_init(&vready[h], 4);
+      mbar_init(&vfree[h], 1);
       mbar_init(&qready[h], 4);
       mbar_init(&sfull[h], 5);   // the MMAs and the four widening warps
       mbar_init(&pready[h], 4);
@@ -369,8 +379,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     mbar_init(kready, 4);
     mbar_init(kfree, 1);
-    mbar_init(vready, 4);
-    mbar_init(vfree, 1);
     fence_mbar_init();
     *s_dead = 0;
     *s_issued = 0;
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = *s_tmem;
+  const uint32_t tm = __shfl_sync(0xffffffffu, *s_tmem, 0);
   pdl_trigger();
   pdl_wait();
   const int cta = blockIdx.x, page = a.c.page, plog = a.c.page_log2;
@@ -425,22 +433,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 13) {
     // ------------------------------------------------------------ issuer --
-    if (active && lane == 0) {
+    if (active) {
       uint32_t t = 0, done[2] = {0, 0};   // tiles begun; P V issued by half
       uint32_t part = 0, part1 = 0;       // parts, and parts with a second half
-      const uint32_t q16 = smem_u32(smem + Lay::kQ), k16 = smem_u32(smem + Lay::kK), v16 = smem_u32(smem + Lay::kV);
+      const uint32_t q16 = tc_desc_lo(smem_u32(smem + Lay::kQ), 16), k16 = tc_desc_lo(smem_u32(smem + Lay::kK), 16);
+      const uint32_t v16 = tc_desc_lo(smem_u32(smem + Lay::kV), kTcHalf * 128);
       auto scores = [&](int h) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * (kTcHalf * 128) + (ks & 3) * 32;
-          tc_mma_ss(tm + 128 * h, tc_desc(q16 + h * Lay::kOp + off, 16), tc_desc(k16 + off, 16), kIdescS, ks > 0);
+          const uint32_t off = ((ks >> 2) * (kTcHalf * 128) + (ks & 3) * 32) >> 4;
+          tc_mma_ss(tm + 128 * h, q16 + h * (Lay::kOp >> 4) + off, k16 + off, kIdescS, ks > 0);
         }
         tc_commit(&sfull[h]);
       };
       auto values = [&](int h, bool first) {
 #pragma unroll
         for (int ks = 0; ks < kPaTile / 16; ++ks)
-          tc_mma_ts(tm + 256 + D * h, tm + 128 * h + 8 * ks, tc_desc(v16 + ks * 2048, kTcHalf * 128), kIdescO<D>,
+          tc_mma_ts(tm + 256 + D * h, tm + 128 * h + 8 * ks, v16 + (t & 1) * (Lay::kOp >> 4) + ks * (2048 >> 4), kIdescO<D>,
                     !first || ks > 0);
         tc_commit(&odone[h]);
         ++done[h];
@@ -459,12 +468,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_commit(kfree);
         for (int i = 0; i < count && ok; ++i, ++t) {
           const bool more = i + 1 < count;
-          if (!wait(vready, t & 1u)) break;
+          if (!wait(&vready[t & 1], (t >> 1) & 1u)) break;
           for (int h = 0; h < nh && ok; ++h) {
             if (!wait(&pready[h], done[h] & 1u)) break;
             tc_fence_after();
             values(h, i == 0);
-            if (h + 1 == nh) tc_commit(vfree);
+            if (h + 1 == nh) tc_commit(&vfree[t & 1]);
             if (more) {
               if (h == 0 && !wait(kready, (t + 1) & 1u)) break;
               tc_fence_after();
@@ -513,9 +522,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool plain = left >= kPaTile && gone == 0u;
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
-            // the operand buffer is free once the MMAs of the tile before have read it
-            if (t > 0) wait(kv ? vfree : kfree, (t - 1) & 1u);
-            uint8_t* dst = smem + (kv ? Lay::kV : Lay::kK);
+            // the operand buffer is free once the MMAs of the tile before (values: of
+            // the one before that) have read it
+            if (kv ? t > 1 : t > 0) wait(kv ? &vfree[t & 1] : kfree, kv ? ((t >> 1) - 1) & 1u : (t - 1) & 1u);
+            uint8_t* dst = smem + (kv ? Lay::kV + (t & 1) * Lay::kOp : Lay::kK);
             const uint8_t* from = st + kv * page * D;
             if (ok) {
 #pragma unroll 2
@@ -545,7 +555,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (told[h]++ > 0) wait(&sfull[h], told[h] & 1u);
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(kv ? vready : kready);
+              mbar_arrive(kv ? &vready[t & 1] : kready);
               if (kv == 0)
                 for (int h = 0; h < nh; ++h) mbar_arrive(&sfull[h]);
               else
