@@ -4,8 +4,8 @@
 //   x_j = scale * q'.k_j  (k_j = code * key scale),  visible max(0, p - window + 1) <= j <= p
 //   o   = sum_j 2^(x_j log2 e) v_j / sum_j 2^(x_j log2 e)
 //
-// A row tile is up to R = 8 NT rows of one sequence that share a kv-head (row =
-// new token x query head of the group).  Its work is a run of 128-position
+// A row tile is up to 8 rows of one sequence that share a kv-head (row = new token
+// x query head of the group).  Its work is a run of 128-position
 // tiles; all runs of the call, one after the other, are cut into equal
 // contiguous shares, one per CTA of a grid that fills the GPU once.  The cut is
 // made on the device from the sequences' lengths, so ragged batches balance
@@ -27,8 +27,8 @@
 // element (put back in the score's factor): 11 significant bits, an order
 // below the cache's own 4; so do the weights.  All sums are fp32.
 //
-// Bound by memory while R <= 16 (the codes are read once, 2 d bytes a position
-// and kv-head), by the tensor pipe for long row runs.
+// Bound by memory while a sequence has one row tile (the codes are read once, 2 d
+// bytes a position and kv-head); further tiles of a sequence read them from L2.
 #include "paged_dev.cuh"
 
 namespace futr {
@@ -37,9 +37,15 @@ namespace {
 
 constexpr int kPaCW = 4;                        // consumer warps
 constexpr int kPaThreads = (kPaCW + 1) * 32;
-template <int D, int NT>
+// Blocks of 8 rows (MMA columns) in a row tile.  Two cost registers that one CTA in
+// two then lacks: 8 sequences of 16 rows over 4000 positions take 50 us with two and
+// 25 us with one (D = 128), 20 and 18 us (D = 64).
+constexpr int NT = 1;
+constexpr int kPaRows = 8 * NT;
+
+template <int D>
 struct PaLayout {
-  static constexpr int R = 8 * NT;
+  static constexpr int R = kPaRows;
   static constexpr int kRing = D == 128 ? 2 : 4;                // 64 KB of tiles: two CTAs share an SM's memory
   static constexpr int kStage = 2 * kPaTile * D;                // K and V codes
   static constexpr int kScale = kRing * kStage;                 // [ring][sub-tiles] float4 (ks, lv, 1/vs, -)
@@ -68,10 +74,10 @@ struct PaItem {
   int hi_min, lo_max;            // positions [lo_max, hi_min] are visible to every row
   int hi_max, lo_min;            // positions that some row sees
   int back;                      // a row at p sees positions >= p - back
-  int hi[16];                    // each row's position
+  int hi[kPaRows];                  // each row's position
 };
 
-template <int D, int NT>
+template <int D>
 struct PaWarp {
   float m[NT][2], l[NT][2], o[D / 16][NT][4];
   float qs[NT][2];
@@ -242,7 +248,7 @@ struct PaWarp {
 // Rows warp, warp + 4, ... of the tile: rotated, divided by a power of two and
 // stored as f16 into their places in the B fragments; their score factors to
 // qs.  The loads of all of a warp's rows are in flight together.
-template <int D, int NT, bool kHalf>
+template <int D, bool kHalf>
 __device__ __forceinline__ void load_queries(const PagedAttnArgs& a, const Walk& w, int valid, __half* qf, float* qs) {
   constexpr int J = D / 32, CH = D / 64, RW = 8 * NT / kPaCW;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -348,10 +354,10 @@ __device__ __forceinline__ void sum_records(const float* r0, const float* rn, in
   }
 }
 
-template <int D, int NT, bool kHalf>
+template <int D, bool kHalf>
 __global__ void __launch_bounds__(kPaThreads, 2)
     paged_attn_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap map) {
-  using Lay = PaLayout<D, NT>;
+  using Lay = PaLayout<D>;
   constexpr int R = Lay::R, kPaRing = Lay::kRing;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
       koff[h] = (p >> plog) * (2 * page * D) + (p & (page - 1)) * D;
     }
     const int voff = page * D;
-    PaWarp<D, NT> aw;
+    PaWarp<D> aw;
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -441,7 +447,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
       pa_sync();
       const int valid = it.valid, count = it.count;
       if (tid < R) it.hi[tid] = it.w.p0 + (it.w.rt * R + min(tid, valid - 1)) / a.G;
-      load_queries<D, NT, kHalf>(a, it.w, valid, reinterpret_cast<__half*>(qf), s_qs);
+      load_queries<D, kHalf>(a, it.w, valid, reinterpret_cast<__half*>(qf), s_qs);
       pa_sync();
       aw.init();
 #pragma unroll
@@ -578,19 +584,19 @@ __global__ void __launch_bounds__(kPaThreads, 2)
   if (*s_dead && tid == 0) drain_ring(full, kPaRing, *s_issued);
 }
 
-template <int D, int NT, bool kHalf>
+template <int D, bool kHalf>
 size_t pa_smem() {
-  return (size_t)PaLayout<D, NT>::kBytes + 1024;
+  return (size_t)PaLayout<D>::kBytes + 1024;
 }
 
-template <int D, int NT, bool kHalf>
+template <int D, bool kHalf>
 cudaError_t pa_configure(int dev) {
   static DeviceOnce configured;
   if (configured.done(dev)) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, NT, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)pa_smem<D, NT, kHalf>());
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)pa_smem<D, kHalf>());
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(paged_attn_kernel<D, NT, kHalf>, cudaFuncAttributePreferredSharedMemoryCarveout,
+  e = cudaFuncSetAttribute(paged_attn_kernel<D, kHalf>, cudaFuncAttributePreferredSharedMemoryCarveout,
                            cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   configured.mark(dev);
@@ -599,12 +605,12 @@ cudaError_t pa_configure(int dev) {
 
 constexpr int kPaMaxPerSm = 2;   // CTAs an SM that any variant is launched with at most
 
-template <int D, int NT, bool kHalf>
+template <int D, bool kHalf>
 int pa_per_sm(int dev) {
-  return remembered(occ_key(dev, D, NT * 2 + kHalf, 0), [&]() {
+  return remembered(occ_key(dev, D, kHalf, 0), [&]() {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attn_kernel<D, NT, kHalf>, kPaThreads,
-                                                      pa_smem<D, NT, kHalf>()) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attn_kernel<D, kHalf>, kPaThreads,
+                                                      pa_smem<D, kHalf>()) != cudaSuccess ||
         n < 1) {
       cudaGetLastError();
       return 1;
@@ -621,44 +627,39 @@ int sm_count(int dev) {
   });
 }
 
-template <int D, int NT, bool kHalf>
+template <int D, bool kHalf>
 cudaError_t pa_launch(const PagedAttnArgs& a, const CUtensorMap& map, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = pa_configure<D, NT, kHalf>(dev);
+  e = pa_configure<D, kHalf>(dev);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(sm_count(dev) * pa_per_sm<D, NT, kHalf>(dev)));
+  cfg.gridDim = dim3((unsigned)(sm_count(dev) * pa_per_sm<D, kHalf>(dev)));
   cfg.blockDim = dim3(kPaThreads);
-  cfg.dynamicSmemBytes = pa_smem<D, NT, kHalf>();
+  cfg.dynamicSmemBytes = pa_smem<D, kHalf>();
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, NT, kHalf>, a, map);
+  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, kHalf>, a, map);
 }
 
-constexpr int kTcMinRows = 64;   // rows (tokens x query heads of a kv-head) a sequence, on average
-
-template <int D, bool kHalf>
-cudaError_t pa_launch_nt(const PagedAttnArgs& a, const CUtensorMap& map, cudaStream_t st) {
-  // rows of a tile: those that a sequence has on average (the counts are on the device)
-  const int rows = (a.r.n_rows + a.r.batch - 1) / a.r.batch * a.G;
-  if (rows <= 8) return pa_launch<D, 1, kHalf>(a, map, st);
-  return pa_launch<D, 2, kHalf>(a, map, st);
-}
+// Rows (tokens x query heads of a kv-head) a sequence, on average, from which on the
+// many-row kernel is faster.  It costs the same for any number up to 128, these tiles
+// of 8 rows their number.  In us, these / that: 8 sequences over 4000 positions,
+// D = 128, 48 rows 43 / 50, 64 rows 50 / 50, 96 rows 73 / 51; D = 64, 64 rows 36 / 41,
+// 96 rows 52 / 42; one over 8000, D = 128, 64 rows 28 / 36, 96 rows 37 / 36.
+constexpr int kTcMinRows = 80;
 
 }  // namespace
-
-constexpr int kPaMaxRows = 16;
 
 // Floats of all CTAs' records on a device with `sms` SMs: two CTAs an SM of these
 // kernels, or one of the many-row kernel.
 size_t paged_rec_floats(int d, int sms) {
-  const size_t few = (size_t)sms * kPaMaxPerSm * 2 * kPaMaxRows * (d + 2), many = (size_t)sms * paged_tc_rec_floats(d);
+  const size_t few = (size_t)sms * kPaMaxPerSm * 2 * kPaRows * (d + 2), many = (size_t)sms * paged_tc_rec_floats(d);
   return few > many ? few : many;
 }
 
@@ -675,8 +676,8 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, const CUtensorMap& ma
   if ((long long)a.r.n_rows * a.G >= (long long)kTcMinRows * a.r.batch)
     return launch_paged_attention_tc(a, map, d, dtype, paged_attn_sms(), st);
   const bool half = dtype == FUTR_DTYPE_F16;
-  if (d == 128) return half ? pa_launch_nt<128, true>(a, map, st) : pa_launch_nt<128, false>(a, map, st);
-  return half ? pa_launch_nt<64, true>(a, map, st) : pa_launch_nt<64, false>(a, map, st);
+  if (d == 128) return half ? pa_launch<128, true>(a, map, st) : pa_launch<128, false>(a, map, st);
+  return half ? pa_launch<64, true>(a, map, st) : pa_launch<64, false>(a, map, st);
 }
 
 // Codes as [blocks][2 page][d] bytes, a block per (page, kv-head), copied whole;
