@@ -26,10 +26,10 @@
 //
 // Bound by the tensor cores in principle (4 x 256 x 128 x D flops a tile take 2048
 // cycles at D = 128).  Measured on four prompts' chunks of 512 rows after contexts to
-// 8K, 32 heads over 8, D = 128: 93 us, 0.51 PFLOP/s of the seen positions.  A CTA's
+// 8K, 32 heads over 8, D = 128: 96 us, 0.50 PFLOP/s of the seen positions.  A CTA's
 // 20 tiles take some 5200 cycles each (a half's softmax, 3300 while it shares the
 // schedulers with the other half's and the widening, and its products, 1024, follow
-// one another); the start, the queries of two parts and the joining of split items
+// one another); the start, the queries of two parts and the records of split items
 // take a third of the time.  Steps of 64 positions, whose products could run under
 // the softmax, took 104 us: twice the reads of the queries from shared memory.
 #include "paged_dev.cuh"
@@ -291,7 +291,7 @@ __device__ __forceinline__ TcScale tc_scale_of(const float4* sc, int c, float qf
 
 // A row's maximum over the tile, chunks of 32 columns.  With and without a mask
 // apart: the comparisons would cost every tile half as much again.  Rolled loops over
-// 32 columns: with 64 a turn a call of 93 us took 101, unrolled 132 (the roles' code
+// 32 columns: with 64 a turn those chunks took 101 us where this took 93, unrolled 132 (the roles' code
 // no longer fits the instruction cache); a row's 128 scores held in registers, by a
 // split of the CTA's registers between the roles, 104 where this took 100.
 template <bool kCut>
@@ -330,6 +330,12 @@ __device__ __forceinline__ float tc_row_weights(uint32_t ts, const float4* sc, f
   return sum;
 }
 
+// An item that spans CTAs: how many follow its first CTA (0: nothing to join), and
+// its rows.
+struct TcJoin {
+  int others, row0, kvh, rt, valid;
+};
+
 // The bounds of the current part from its walk (one thread).
 __device__ __forceinline__ void tc_set(const PagedAttnArgs& a, TcItem& it) {
   const Walk& c = it.w;
@@ -359,8 +365,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* odone = pready + 2;          // [2] P V of a half is done
   volatile int* s_dead = reinterpret_cast<volatile int*>(odone + 2);   // a wait ran out
   volatile int* s_issued = s_dead + 1;
-  volatile int* s_last = s_dead + 2;
-  volatile int* s_snap = s_dead + 3;
+  volatile int* s_snap = s_dead + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(odone + 2) + 4;
   __shared__ TcItem s_item;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -569,6 +574,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else {
     // ----------------------------------------------------------- softmax --
+    TcJoin join{};
     const int half = warp >> 2, row = tid & (kTcHalf - 1);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tm + lanes + 128 * half, to = tm + lanes + 256 + D * half;
@@ -628,15 +634,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_fence_after();
         }
         t += count;
-        // ---- a whole item: its rows; a part of one: a record, and the CTA that
-        // arrives last adds the records in CTA order
+        // ---- a whole item: its rows; a part of one: a record, which the joining kernel
+        // adds to the others
         const Walk& c = it.w;
         const long long item1 = c.item0 + (c.t.t1 - c.t.t0);
         const bool whole = c.u == c.item0 && c.u + count == item1;
         if (tid == 0) *s_snap = *s_dead;
         tc_soft_sync();
         const bool live = *s_snap == 0;
-        bool write = whole && live;
         constexpr size_t kRecRow = kTcRows, kRec = (size_t)kTcRows * (D + 2);
         float* rec = a.rec + ((size_t)cta * 2 + (c.item0 < c.u ? 0 : 1)) * kRec;
         const bool row_ok = r < valid;
@@ -672,63 +677,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             rec[kRecRow + r] = L;
           }
         }
-        if (!whole && live) {
-          tc_soft_sync();
-          const int c0 = it.cut.owner(c.item0), c1 = it.cut.owner(item1 - 1);
-          if (tid == 0) {
-            *s_last = atom_add_acq_rel_gpu(&a.cnt[c0], 1u) == (unsigned)(c1 - c0) ? 1 : 0;
-            if (*s_last) a.cnt[c0] = 0u;
-          }
-          tc_soft_sync();
-          write = *s_last != 0;
-          if (write && row_ok) {
-            // a thread per row: reference and normalizer of all parts, then its sums
-            const float* r0 = a.rec + ((size_t)c0 * 2 + 1) * kRec;      // CTA c0's second slot
-            const float* rn = a.rec + (size_t)(c0 + 1) * 2 * kRec;      // the others' first
-            const int nc = c1 - c0;
-            float top = __ldcg(r0 + r);
-#pragma unroll 1
-            for (int k = 0; k < nc; ++k) top = fmaxf(top, __ldcg(rn + (size_t)k * 2 * kRec + r));
-            const float ref = top == -INFINITY ? 0.f : top;
-            float sum = __ldcg(r0 + kRecRow + r) * pa_ex2(__ldcg(r0 + r) - ref);
-#pragma unroll 1
-            for (int k = 0; k < nc; ++k)
-              sum = fmaf(__ldcg(rn + (size_t)k * 2 * kRec + kRecRow + r),
-                         pa_ex2(__ldcg(rn + (size_t)k * 2 * kRec + r) - ref), sum);
-            const float inv = sum != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {   // 32 dims at a time
-              float4 acc[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-              for (int k = -1; k < nc; ++k) {
-                const float* src = k < 0 ? r0 : rn + (size_t)k * 2 * kRec;
-                const float wt = pa_ex2(__ldcg(src + r) - ref);
-                float4 v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  v[j] = __ldcg(reinterpret_cast<const float4*>(src + 2 * kRecRow) + (8 * q + j) * kTcRows + r);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  acc[j].x = fmaf(v[j].x, wt, acc[j].x);
-                  acc[j].y = fmaf(v[j].y, wt, acc[j].y);
-                  acc[j].z = fmaf(v[j].z, wt, acc[j].z);
-                  acc[j].w = fmaf(v[j].w, wt, acc[j].w);
-                }
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint4 u;
-                u.x = narrow2<kHalf>(acc[2 * j].x * inv, acc[2 * j].y * inv);
-                u.y = narrow2<kHalf>(acc[2 * j].z * inv, acc[2 * j].w * inv);
-                u.z = narrow2<kHalf>(acc[2 * j + 1].x * inv, acc[2 * j + 1].y * inv);
-                u.w = narrow2<kHalf>(acc[2 * j + 1].z * inv, acc[2 * j + 1].w * inv);
-                *reinterpret_cast<uint4*>(out + 32 * q + 8 * j) = u;
-              }
-            }
-          }
-        }
+        // the CTA with an item's beginning describes the join
+        if (!whole && live && c.item0 == c.u && tid == 0)
+          join = TcJoin{it.cut.owner(item1 - 1) - cta, c.row0, c.kvh, c.rt, valid};
         more = c.u + count < c.u1;
         if (more) {
           tc_soft_sync();   // the item's bounds are read no more
@@ -739,6 +690,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
+    if (tid == 0) reinterpret_cast<TcJoin*>(a.rec + (size_t)gridDim.x * 2 * kTcRows * (D + 2))[cta] = join;
   }
   // every MMA has been waited for (odone), or, after a time-out, gets its time here
   __syncthreads();
@@ -752,6 +704,62 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncwarp();
   if (warp == 13)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
+}
+
+// Joins the records of split items, in CTA order: block (c, y) rows 32 y .. 32 y + 31
+// of the item that begins in CTA c, a lane per row, a warp per eighth of its dims.
+// A kernel of its own, so that every SM takes part: the CTA that arrived last would
+// read 133 KB a part by itself, 19 of them for one sequence of 256 rows over 8000
+// positions, a call of 73 us that takes 46 us like this.  Where items have few parts
+// it costs a launch: 96 us for the chunks above, 93 without it.
+constexpr int kTcJoinRows = 32;
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnArgs a, int ctas) {
+  constexpr size_t kRecRow = kTcRows, kRec = (size_t)kTcRows * (D + 2);
+  constexpr int Q = D / 32;   // dim quads of a thread
+  const int cta = blockIdx.x, r = kTcJoinRows * blockIdx.y + (threadIdx.x & 31), q0 = Q * (threadIdx.x >> 5);
+  pdl_trigger();
+  pdl_wait();
+  const TcJoin join = reinterpret_cast<const TcJoin*>(a.rec + (size_t)ctas * 2 * kRec)[cta];
+  if (join.others == 0 || r >= join.valid || a.err[1] != 0) return;   // (after a time-out parts may be missing)
+  const float* r0 = a.rec + ((size_t)cta * 2 + 1) * kRec + r;         // its CTA's second slot
+  const float* rn = a.rec + (size_t)(cta + 1) * 2 * kRec + r;         // the others' first
+  const int nc = join.others;
+  float top = *r0;
+#pragma unroll 4
+  for (int k = 0; k < nc; ++k) top = fmaxf(top, rn[(size_t)k * 2 * kRec]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  float4 acc[Q];
+#pragma unroll
+  for (int j = 0; j < Q; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = -1; k < nc; ++k) {
+    const float* src = k < 0 ? r0 : rn + (size_t)k * 2 * kRec;
+    const float wt = pa_ex2(src[0] - ref);
+    sum = fmaf(src[kRecRow], wt, sum);
+#pragma unroll
+    for (int j = 0; j < Q; ++j) {
+      const float4 v = reinterpret_cast<const float4*>(src - r + 2 * kRecRow)[(q0 + j) * kTcRows + r];
+      acc[j].x = fmaf(v.x, wt, acc[j].x);
+      acc[j].y = fmaf(v.y, wt, acc[j].y);
+      acc[j].z = fmaf(v.z, wt, acc[j].z);
+      acc[j].w = fmaf(v.w, wt, acc[j].w);
+    }
+  }
+  const float inv = sum != 0.f ? __fdiv_rn(1.0f, sum) : 0.f;
+  const int row = join.rt * kTcRows + r, i = row / a.G, head = join.kvh * a.G + row - i * a.G;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + (size_t)(join.row0 + i) * a.ld_out + (size_t)head * D + 4 * q0;
+#pragma unroll
+  for (int j = 0; j < Q; j += 2) {
+    uint4 u;
+    u.x = narrow2<kHalf>(acc[j].x * inv, acc[j].y * inv);
+    u.y = narrow2<kHalf>(acc[j].z * inv, acc[j].w * inv);
+    u.z = narrow2<kHalf>(acc[j + 1].x * inv, acc[j + 1].y * inv);
+    u.w = narrow2<kHalf>(acc[j + 1].z * inv, acc[j + 1].w * inv);
+    *reinterpret_cast<uint4*>(out + 4 * j) = u;
+  }
 }
 
 template <int D>
@@ -781,12 +789,19 @@ cudaError_t tc_launch(const PagedAttnArgs& a, const CUtensorMap& map, int ctas, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<D, kHalf>, a, map);
+  e = cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<D, kHalf>, a, map);
+  if (e != cudaSuccess) return e;
+  // rows of a tile: no sequence has more than all of them
+  const long long rows = (long long)a.r.n_rows * a.G;
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)((rows < kTcRows ? rows : kTcRows) + kTcJoinRows - 1) / kTcJoinRows);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kHalf>, a, ctas);
 }
 
 }  // namespace
 
-size_t paged_tc_rec_floats(int d) { return (size_t)2 * kTcRows * (d + 2); }
+size_t paged_tc_rec_floats(int d) { return (size_t)2 * kTcRows * (d + 2) + sizeof(TcJoin) / 4; }
 
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs& a, const CUtensorMap& map, int d, int dtype, int ctas,
                                       cudaStream_t st) {
