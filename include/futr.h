@@ -382,7 +382,8 @@ futr_status futr_check(const futr_ws* ws, const futr_kv* kv, void* stream);
  * Row tensors are 16-bit (FUTR_DTYPE_*), heads and dims contiguous, tokens ld_*
  * elements apart (a multiple of 8, so a slice of a fused QKV row will do),
  * 16-byte aligned.  Only the shape's head counts, head_dim and rope_theta are
- * used.  The calls launch one kernel with programmatic dependent launch, read
+ * used.  The calls launch one kernel (attention for many rows a sequence: two)
+ * with programmatic dependent launch, read
  * pos, start and table on the device, and can be captured in a CUDA graph; a
  * captured call follows lengths that change. */
 #define FUTR_DTYPE_BF16 0
@@ -451,7 +452,7 @@ futr_status futr_paged_workspace_init(const futr_shape* shape, void* mem, size_t
  * The rotated query and the softmax weights enter the products as fp16 (the
  * query divided by a power of two near its largest element), sums and softmax
  * statistics are fp32.  A row that sees no position (missing pages) gets zeros.
- * out may not be q.
+ * out may not overlap q.
  */
 futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t batch, const int32_t* pos,
                                  const int32_t* start, int32_t n_rows, const int32_t* table, int32_t table_ld,
@@ -488,8 +489,9 @@ futr_status futr_moe_weights_size(const futr_moe_shape* shape, size_t* bytes);
 
 /* Pack one expert (fp32 wgate, wup [I, H], wdown [H, I], nn.Linear layout) into
  * the layer's blob (256-byte aligned): the codes, scales and units of
- * futr_pack_weights, with the nibbles of a word in an order of their own.  gain: the RMSNorm gain [H] folded into gate and up, or
- * NULL.  Experts may be packed in any order; all of them before the first use. */
+ * futr_pack_weights, with the nibbles of a word in an order of their own.  gain:
+ * the RMSNorm gain [H] folded into gate and up, or NULL.  Experts may be packed in
+ * any order; all of them before the first use. */
 futr_status futr_moe_pack(const futr_moe_shape* shape, int32_t expert, const float* wgate, const float* wup,
                           const float* wdown, const float* gain, void* blob, size_t blob_bytes, void* stream);
 
@@ -512,13 +514,13 @@ futr_status futr_moe_workspace_init(const futr_moe_shape* shape, int32_t max_bat
  *   softmax probabilities w over all E experts, divided by their sum if renorm
  *   y = bf16(resid + sum_j w_j Wdown_j (silu(r W'gate_j x) * (r W'up_j x)))
  * x, y, resid: bf16 [batch][H], 16-byte aligned (y may be x or resid; resid may
- * be NULL).  The inputs of both products are sums of e4m3 terms times a power of
- * two for each 128 (gate/up: x to 8 bits, its own; w * silu * up for each 64, 12
- * bits); all sums are fp32. ids (int32) and weights (fp32)
- * [batch][K], either may be NULL: the choice of each token, largest first.  A
- * token whose logits hold a NaN gets NaN weights.  A blob of another shape sets
- * FUTR_ERR_BAD_BLOB (see futr_moe_check).  Three kernels with programmatic
- * dependent launch; capturable in a CUDA graph.
+ * be NULL).  The inputs of both products enter as fp16 (x divided by a power of
+ * two near its RMS; w * silu * up by one near the largest of each 64); all sums
+ * are fp32.  ids (int32) and weights (fp32) [batch][K], either may be NULL: the
+ * choice of each token, largest first.  A token whose logits hold a NaN gets NaN
+ * weights.  A blob of another shape sets FUTR_ERR_BAD_BLOB (see futr_moe_check).
+ * Three kernels (four above 8 tokens) with programmatic dependent launch;
+ * capturable in a CUDA graph.
  */
 futr_status futr_moe_layer(const uint16_t* x, const float* gain, const uint16_t* router, const void* blob,
                            int32_t batch, const uint16_t* resid, uint16_t* y, int32_t* ids, float* weights,

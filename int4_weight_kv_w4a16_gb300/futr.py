@@ -335,6 +335,11 @@ def _bad_tensor(t, name, want, device):
     raise ValueError(f"{name} must be {want}{where}, not {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
+def _on_device(descriptor, name, device):
+    if descriptor._mem.get_device() != device:
+        raise ValueError(f"{name} is on {descriptor._mem.device}, not on CUDA device {device}, the current one")
+
+
 def _row_dtype(T, a, b, names) -> int:
     dtype = a.dtype
     if b.dtype is not dtype or dtype not in T.rows:
@@ -399,6 +404,7 @@ def futr_paged_append(cache, layer, batch, pos, start, table, k, v, stream=None)
     shape = cache.shape
     n, heads, d = k.shape[0], shape.n_kv_heads, shape.head_dim
     dtype = _row_dtype(T, k, v, "k and v")
+    _on_device(cache, "the cache", device)
     ld_k, ld_v = _row_stride(k, "k", device, n, heads, d), _row_stride(v, "v", device, n, heads, d)
     p, s, n, t, ld = _paged_rows(T, batch, pos, start, table, n, device)
     _ok(lib().futr_paged_append(C.addressof(cache), layer, batch, p, s, n, t, ld, k.data_ptr(), ld_k, v.data_ptr(),
@@ -428,6 +434,8 @@ def futr_paged_attention(cache, layer, batch, pos, start, table, q, out, ws, sca
     shape = cache.shape
     n, heads, d = q.shape[0], shape.n_q_heads, shape.head_dim
     dtype = _row_dtype(T, q, out, "q and out")
+    _on_device(cache, "the cache", device)
+    _on_device(ws, "the workspace", device)
     ld_q, ld_out = _row_stride(q, "q", device, n, heads, d), _row_stride(out, "out", device, n, heads, d)
     p, s, n, t, ld = _paged_rows(T, batch, pos, start, table, n, device)
     _ok(lib().futr_paged_attention(C.addressof(cache), layer, batch, p, s, n, t, ld, q.data_ptr(), ld_q,
@@ -462,10 +470,18 @@ def _dense(t, name: str, dtype, shape, device: int) -> Optional[int]:
     return t.data_ptr()
 
 
+def _moe_blob(blob, nbytes, device):
+    if blob.nbytes < nbytes or not blob.is_contiguous() or blob.get_device() != device:
+        raise ValueError(f"blob must hold the layer's packed experts, {nbytes} contiguous bytes on CUDA device "
+                         f"{device}, the current one")
+    return blob.data_ptr()
+
+
 def futr_moe_pack(shape, expert, wgate, wup, wdown, gain, blob, stream=None):
     T = _T or _torch()
     device = T.device()
     H, I, f32 = shape.hidden, shape.inter, T.float32
+    _moe_blob(blob, futr_moe_weights_size(shape), device)
     _ok(lib().futr_moe_pack(C.byref(shape), expert, _dense(wgate, "wgate", f32, (I, H), device),
                             _dense(wup, "wup", f32, (I, H), device), _dense(wdown, "wdown", f32, (H, I), device),
                             _dense(gain, "gain", f32, (H,), device), _ptr(blob), blob.numel() * blob.element_size(),
@@ -473,7 +489,12 @@ def futr_moe_pack(shape, expert, wgate, wup, wdown, gain, blob, stream=None):
 
 
 def futr_moe_unpack(shape, blob, expert, which, codes, scales, stream=None):
-    _ok(lib().futr_moe_unpack(C.byref(shape), _ptr(blob), expert, which, _ptr(codes), _ptr(scales), _stream(stream)),
+    import torch
+    device = torch.cuda.current_device() if _T is None else _T.device()
+    r, c = (shape.hidden, shape.inter) if which == FUTR_PROJ_DOWN else (shape.inter, shape.hidden)
+    _ok(lib().futr_moe_unpack(C.byref(shape), _moe_blob(blob, futr_moe_weights_size(shape), device), expert, which,
+                              _dense(codes, "codes", torch.int8, (r, c), device),
+                              _dense(scales, "scales", torch.float16, (r, c // 128), device), _stream(stream)),
         "futr_moe_unpack")
 
 
@@ -498,9 +519,8 @@ def futr_moe_layer(x, gain, router, blob, resid, y, ws, ids=None, weights=None, 
     s = ws.shape
     H, K, bf, n = s.hidden, s.top_k, T.bfloat16, x.shape[0]
     rows = (n, H)
-    if blob.nbytes < ws.blob_bytes or not blob.is_contiguous() or blob.get_device() != device:
-        raise ValueError(f"blob must hold the layer's packed experts, {ws.blob_bytes} contiguous bytes on CUDA device "
-                         f"{device}, the current one")
+    _moe_blob(blob, ws.blob_bytes, device)
+    _on_device(ws, "the workspace", device)
     _ok(lib().futr_moe_layer(_dense(x, "x", bf, rows, device), _dense(gain, "gain", T.float32, (H,), device),
                              _dense(router, "router", bf, (s.n_experts, H), device), blob.data_ptr(), n,
                              _dense(resid, "resid", bf, rows, device), _dense(y, "y", bf, rows, device),
