@@ -24,8 +24,12 @@
 //   O^T += V^T w: A = value codes, converted the same way; the score fragment
 //     becomes the B operand by an 8x8 register transpose.
 // The query enters as f16, each row divided by a power of two near its largest
-// element (put back in the score's factor): 11 significant bits, an order
-// below the cache's own 4; so do the weights.  All sums are fp32.
+// element (put back in the score's factor): 11 significant bits, below what bf16
+// rows resolve; f16 rows, which resolve more, in two parts (22 bits; an output's
+// error is then its own rounding, 2.0e-4, instead of 4.3e-4).  The second MMAs cost
+// drafted tokens nothing (13.1 us), 32 ragged sequences of D = 128 39.0 us instead of
+// 36.7.  The weights enter as f16: 11 bits, next to the 4 of the values they multiply.
+// All sums are fp32.
 //
 // Bound by memory while a sequence has one row tile (the codes are read once, 2 d
 // bytes a position and kv-head); further tiles of a sequence read them from L2.
@@ -49,8 +53,8 @@ struct PaLayout {
   static constexpr int kRing = D == 128 ? 2 : 4;                // 64 KB of tiles: two CTAs share an SM's memory
   static constexpr int kStage = 2 * kPaTile * D;                // K and V codes
   static constexpr int kScale = kRing * kStage;                 // [ring][sub-tiles] float4 (ks, lv, 1/vs, -)
-  static constexpr int kQ = kScale + kRing * kPaSub * 16;       // query fragments [D/16][NT][32] uint2
-  static constexpr int kQs = kQ + (D / 16) * NT * 32 * 8;       // [R] score factors
+  static constexpr int kQ = kScale + kRing * kPaSub * 16;       // query fragments [D/16][NT][32][parts] uint2
+  static constexpr int kQs = kQ + (D / 16) * NT * 32 * 16;      // [R] score factors
   static constexpr int kOLd = D + 4;
   static constexpr int kO = kQs + R * 4;                        // [4 warps][R][kOLd] fp32
   static constexpr int kM = kO + kPaCW * R * kOLd * 4;          // [4 warps][R]
@@ -62,6 +66,10 @@ struct PaLayout {
 __device__ __forceinline__ void pa_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kPaCW * 32) : "memory"); }
 
 // ---------------------------------------------------------------- consumer --
+
+// f16 parts of a query element, by the rows' type
+template <bool kHalf>
+constexpr int kQueryParts = kHalf ? 2 : 1;
 
 // The consumers' current item, in shared memory: its bounds are read where they
 // are needed instead of being held in registers through the tile loop.
@@ -77,7 +85,7 @@ struct PaItem {
   int hi[kPaRows];                  // each row's position
 };
 
-template <int D>
+template <int D, int kParts>
 struct PaWarp {
   float m[NT][2], l[NT][2], o[D / 16][NT][4];
   float qs[NT][2];
@@ -104,7 +112,7 @@ struct PaWarp {
   // below it.written exist.  Two halves at a time: their products are
   // independent chains, and they share one maximum.
   __device__ __forceinline__ void tile32(const uint8_t* const (&ks)[2], const uint8_t* const (&vs)[2],
-                                         const float4 (&sc)[2], const uint2* qf, const PaItem& it, int pos0) {
+                                         const float4 (&sc)[2], const __half* qf, const PaItem& it, int pos0) {
     constexpr int CH = D / 64;   // 16-byte chunks of a lane's key dims
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int swz = D == 128 ? g : (g >> 1) & 3;   // rows g and g + 8 share it
@@ -136,9 +144,15 @@ struct PaWarp {
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint2 q = qf[((4 * j + i) * NT + nt) * 32 + lane];
+          const uint2* q = reinterpret_cast<const uint2*>(qf + (((4 * j + i) * NT + nt) * 32 + lane) * 4 * kParts);
+          const uint2 q0 = q[0];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) mma_f16_16816(s[h][nt], af[h], q.x, q.y);
+          for (int h = 0; h < 2; ++h) mma_f16_16816(s[h][nt], af[h], q0.x, q0.y);
+          if (kParts == 2) {
+            const uint2 q1 = q[1];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mma_f16_16816(s[h][nt], af[h], q1.x, q1.y);
+          }
         }
       }
     }
@@ -300,7 +314,10 @@ __device__ __forceinline__ void load_queries(const PagedAttnArgs& a, const Walk&
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int i = lane + 32 * j, t = i / (16 * CH), rem = i % (16 * CH), ks = (rem / 16) * 4 + (rem % 16) / 4;
-      qf[((ks * NT + (r >> 3)) * 32 + (r & 7) * 4 + t) * 4 + (i & 3)] = __float2half_rn(x[j]);
+      const __half hi = __float2half_rn(x[j]);
+      __half* at = qf + ((ks * NT + (r >> 3)) * 32 + (r & 7) * 4 + t) * 4 * kQueryParts<kHalf> + (i & 3);
+      at[0] = hi;
+      if (kHalf) at[4] = __float2half_rn(x[j] - __half2float(hi));
     }
     if (lane == 0) qs[r] = factor;
   }
@@ -362,7 +379,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float4* s_scale = reinterpret_cast<float4*>(smem + Lay::kScale);
-  uint2* qf = reinterpret_cast<uint2*>(smem + Lay::kQ);
+  __half* qf = reinterpret_cast<__half*>(smem + Lay::kQ);
   float* s_qs = reinterpret_cast<float*>(smem + Lay::kQs);
   float* s_o = reinterpret_cast<float*>(smem + Lay::kO);
   float* s_m = reinterpret_cast<float*>(smem + Lay::kM);
@@ -414,7 +431,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
       koff[h] = (p >> plog) * (2 * page * D) + (p & (page - 1)) * D;
     }
     const int voff = page * D;
-    PaWarp<D> aw;
+    PaWarp<D, kQueryParts<kHalf>> aw;
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -447,7 +464,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
       pa_sync();
       const int valid = it.valid, count = it.count;
       if (tid < R) it.hi[tid] = it.w.p0 + (it.w.rt * R + min(tid, valid - 1)) / a.G;
-      load_queries<D, kHalf>(a, it.w, valid, reinterpret_cast<__half*>(qf), s_qs);
+      load_queries<D, kHalf>(a, it.w, valid, qf, s_qs);
       pa_sync();
       aw.init();
 #pragma unroll

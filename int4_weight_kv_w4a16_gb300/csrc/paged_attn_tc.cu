@@ -20,6 +20,9 @@
 //                over the scores it has read, where they are P V's A operand.
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (D columns each).
 //
+// The query of f16 rows has one f16 part here, too: a second does not fit into shared
+// memory beside two value buffers (an output's error is 4e-4 instead of 2e-4).
+//
 // The running reference M of a row follows its maximum only when that has grown
 // by more than 2^8: a weight up to 2^8 is a good f16, the normalizer is fp32, and
 // O, in tensor memory, is rescaled a few times an item instead of every tile.
