@@ -14,11 +14,11 @@
 // codes: page / 4 rows at a time, whatever the page.
 //
 // Bound by memory for prompts (2 bytes read and 1 written per element): 64 MB take
-// 18.3 us (3.5 TB/s; 9.5 us at the copy rate; half of it is the start of a CTA,
-// five waves of them).  Two rows a thread take 21.2 us, eight 18.4, and reading the
-// rows a second time instead of keeping them 36.  Bound by latency for single
-// tokens, whose chain is: row bounds -> table entry -> old scale, and beside it row
-// -> rotation -> maximum: 2.3 us for one, 3.9 us for 32 sequences.
+// 16.3 us (3.9 TB/s; 9.5 us at the copy rate; the rest is the start of a CTA, four
+// waves of them).  Two rows a thread took 21 us where four and eight took 18.4, and
+// reading the rows a second time instead of keeping them 36.  Bound by latency for
+// single tokens, whose chain is: row bounds -> table entry -> old scale, and beside
+// it row -> rotation -> maximum: 2.3 us for one, 3.1 us for 32 sequences.
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
@@ -81,6 +81,7 @@ template <int D, bool kHalf>
 __global__ void __launch_bounds__(kAppMaxThreads) paged_append_kernel(const AppendArgs a) {
   constexpr int L = D / 8;                            // lanes of a row
   __shared__ float s_max[kAppMaxThreads / 32];
+  __shared__ int s_found[5];
   const int threads = blockDim.x, rows = threads / L;   // rows at a time
   const int tid = threadIdx.x, lane = tid & 31, lg = tid % L, rg = tid / L;
   const int kvh = blockIdx.y, which = blockIdx.z;
@@ -93,9 +94,10 @@ __global__ void __launch_bounds__(kAppMaxThreads) paged_append_kernel(const Appe
       if (!paged_seq(a.r, a.c, s, r0, nn, pp)) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
     }
   // the touched page of this CTA: sequences in order, each with the pages that
-  // its new rows meet
+  // its new rows meet; one warp looks for all (every warp by itself: 18.4 us for the
+  // prompts that take 16.3)
   int item = blockIdx.x, row0 = 0, n = 0, p0 = 0, b = -1;
-  for (int b0 = 0; b0 < a.r.batch; b0 += 32) {
+  for (int b0 = 0; b0 < a.r.batch && tid < 32; b0 += 32) {
     int rr = 0, nn = 0, pp = 0, pages = 0;
     if (b0 + lane < a.r.batch) {
       paged_seq(a.r, a.c, b0 + lane, rr, nn, pp);
@@ -119,6 +121,15 @@ __global__ void __launch_bounds__(kAppMaxThreads) paged_append_kernel(const Appe
     }
     item -= __shfl_sync(0xffffffffu, incl, 31);
   }
+  if (tid == 0) {
+    s_found[0] = b;
+    s_found[1] = item;
+    s_found[2] = row0;
+    s_found[3] = n;
+    s_found[4] = p0;
+  }
+  __syncthreads();
+  b = s_found[0], item = s_found[1], row0 = s_found[2], n = s_found[3], p0 = s_found[4];
   if (b < 0) return;   // the grid is an upper bound
   const int page = a.c.page, pi = (p0 >> a.c.page_log2) + item;
   const int id = a.r.table[(size_t)b * a.r.table_ld + pi];
@@ -174,20 +185,25 @@ __global__ void __launch_bounds__(kAppMaxThreads) paged_append_kernel(const Appe
   const float s_old = lo == 0 ? 0.f : *scale;
 
   // largest magnitude; what is not finite is stored as 0 and reported
-  float m = 0.f;
-  bool bad = false;
+  float m = 0.f, none = 0.f;   // none: 0 times every element, 0 unless one is not finite
 #pragma unroll
-  for (int i = 0; i < kAppRounds; ++i) {
+  for (int i = 0; i < kAppRounds; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (!(fabsf(x[i][j]) <= 3.4028234e38f)) {
-        x[i][j] = 0.f;
-        bad = true;
-      }
       m = fmaxf(m, fabsf(x[i][j]));
+      none = fmaf(x[i][j], 0.f, none);
     }
+  if (none != 0.f) {
+    set_err(a.err, FUTR_ERR_NOT_FINITE);
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < kAppRounds; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!(fabsf(x[i][j]) <= 3.4028234e38f)) x[i][j] = 0.f;
+        m = fmaxf(m, fabsf(x[i][j]));
+      }
   }
-  if (bad) set_err(a.err, FUTR_ERR_NOT_FINITE);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) s_max[tid >> 5] = m;
