@@ -32,7 +32,10 @@
 // All sums are fp32.
 //
 // Bound by memory while a sequence has one row tile (the codes are read once, 2 d
-// bytes a position and kv-head); further tiles of a sequence read them from L2.
+// bytes a position and kv-head); further tiles of a sequence read them from L2.  32
+// ragged sequences of 512 to 4096 positions (148 MB): 36.4 us, 4.1 TB/s; four of 20K
+// to 50K (269 MB): 53.8 us, 5.0 TB/s; the copies alone 30 and 48.5 us.  One sequence
+// of 1024 positions: 7.9 us, the latency of share -> page id -> tile -> join.
 #include "paged_dev.cuh"
 
 namespace futr {
