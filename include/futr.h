@@ -367,7 +367,7 @@ futr_status futr_check(const futr_ws* ws, const futr_kv* kv, void* stream);
  * the caller's page table (device int32 [batch][table_ld]); entries past a
  * sequence's last page, and those of pages before every row's window, are not
  * read.  Several sequences may read one page; in
- * one append, a page may belong to one sequence only.
+ * one append, a page may belong to one sequence only, and stand in its row once.
  *
  * Ragged rows: rows start[b] .. start[b+1]-1 of a call's row tensors are the
  * new tokens of sequence b, at positions pos[b], pos[b]+1, ...  start is device

@@ -208,7 +208,7 @@ futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t
     const futr_status st = check_rows(cache, layer, batch, pos, start, n_rows, table, table_ld, dtype);
     if (st != FUTR_OK) return st;
     if (!ws_ok(ws) || ws->head_dim != cache->shape.head_dim || window < 0) return FUTR_ERR_INVALID_ARG;
-    if (!(std::isfinite(scale) && scale >= 0.f)) return FUTR_ERR_INVALID_ARG;
+    if (!(scale >= 0.f && std::isfinite(scale * 1.5f))) return FUTR_ERR_INVALID_ARG;   // times log2(e) below
     if (n_rows == 0) return FUTR_OK;
     const futr_shape& s = cache->shape;
     const int width = s.n_q_heads * s.head_dim;
@@ -224,7 +224,7 @@ futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t
     a.ld_out = ld_out;
     a.Hkv = s.n_kv_heads;
     a.G = s.n_q_heads / s.n_kv_heads;
-    a.window = window;
+    a.window = window < cache->max_pos ? window : 0;   // a window of every position is none
     a.block0 = (long long)layer * cache->n_pages * s.n_kv_heads;
     const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)s.head_dim);
     a.scale_log2 = (float)(sc * 1.4426950408889634);

@@ -404,3 +404,30 @@ def test_shared_pages_and_prompts_in_pieces():
     c.table = table[1:].contiguous()
     check_attention(c, q[96:], part, [96], [m])
     assert futr.futr_paged_check(c.cache, c.ws) == futr.FUTR_OK
+
+
+@pytest.mark.parametrize("n", [1, 150], ids=["token", "chunk"])
+def test_window_of_everything_is_none(n):
+    """Windows up to the largest int32 give what no window gives."""
+    c = Paged(4, 2, 128, 64, 1, 6)
+    c.fill(8)
+    q = rows(n, 4, 128, torch.bfloat16, 12)
+    want = run_attention(c, q, [130], [n], 0)
+    for window in (130 + n, c.max_pos - 1, c.max_pos, 2 ** 31 - 1):
+        assert torch.equal(run_attention(c, q, [130], [n], window), want)
+
+
+def test_query_that_is_not_finite_stays_its_own():
+    """An infinity or NaN in one row's query leaves the other rows as they were."""
+    for counts in ([3], [100]):
+        c = Paged(4, 2, 128, 64, 1, 6)
+        c.fill(9)
+        q = rows(counts[0], 4, 128, torch.bfloat16, 13)
+        want = run_attention(c, q, [200], counts)
+        bad = q.clone()
+        bad[1, 2, 5], bad[2, 0, 100] = float("nan"), float("inf")
+        got = run_attention(c, bad, [200], counts)
+        keep = torch.ones(q.shape[:2], dtype=torch.bool, device="cuda")
+        keep[1, 2] = keep[2, 0] = False
+        assert torch.equal(got[keep], want[keep])
+        assert bool(torch.isnan(got[1, 2]).all())

@@ -134,7 +134,7 @@ def test_append_refuses_row_tensors(L, kw):
 
 @pytest.mark.parametrize("kw", [{"q": None}, {"out": None}, {"q": MEM + 2}, {"out": MEM + 8}, {"ld_q": 248},
                                 {"ld_out": 260}, {"ld_q": -256}, {"out": MEM}, {"window": -1}, {"scale": -1.0},
-                                {"scale": float("nan")}, {"scale": float("inf")}])
+                                {"scale": float("nan")}, {"scale": float("inf")}, {"scale": 3e38}])
 def test_attention_refuses_row_tensors_and_scalars(L, kw):
     assert call_attention(L, a_cache(), a_paged_ws(), **kw) == ARG
 
