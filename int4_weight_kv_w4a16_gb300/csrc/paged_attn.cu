@@ -33,9 +33,10 @@
 //
 // Bound by memory while a sequence has one row tile (the codes are read once, 2 d
 // bytes a position and kv-head); further tiles of a sequence read them from L2.  32
-// ragged sequences of 512 to 4096 positions (148 MB): 36.4 us, 4.1 TB/s; four of 20K
-// to 50K (269 MB): 53.8 us, 5.0 TB/s; the copies alone 30 and 48.5 us.  One sequence
-// of 1024 positions: 7.9 us, the latency of share -> page id -> tile -> join.
+// ragged sequences of 512 to 4096 positions (148 MB): 33.0 us, 4.5 TB/s; four of 20K
+// to 50K (269 MB): 51.3 us, 5.2 TB/s; the copies alone, in equal shares of tiles, 30
+// and 48.5 us.  One sequence of 1024 positions: 7.9 us, the latency of share -> page
+// id -> tile -> join.
 #include "paged_dev.cuh"
 
 namespace futr {
@@ -49,6 +50,10 @@ constexpr int kPaThreads = (kPaCW + 1) * 32;
 // 25 us with one (D = 128), 20 and 18 us (D = 64).
 constexpr int NT = 1;
 constexpr int kPaRows = 8 * NT;
+// An item's start and join count as three tiles in the cut.  With 0, 2, 3, 4 and 6: 32
+// ragged sequences 36.6, 33.0, 33.1, 33.5, 35.1 us; four long ones 53.9, 52.4, 51.3, 51.1,
+// 51.3; drafted tokens (D = 64) 13.1, 11.4, 10.3, 10.4, 11.0.
+constexpr Rows kPaWork{kPaRows, 3};
 
 template <int D>
 struct PaLayout {
@@ -415,9 +420,9 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     // ---------------------------------------------------------- producer --
     Walk w;
     Cut cut;
-    if (!find_share(a, R, cta, gridDim.x, w, cut, false)) return;
+    if (!find_share(a, kPaWork, cta, gridDim.x, w, cut, false)) return;
     int issued = 0;
-    const bool ok = produce_tiles<D>(a, &map, R, w, smem, s_scale, full, empty, kPaRing, issued);
+    const bool ok = produce_tiles<D>(a, &map, kPaWork, w, smem, s_scale, full, empty, kPaRing, issued);
     if (!ok) {
       record_timeout(a.err);
       *s_dead = 1;
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     if (warp == 0) {
       Walk w;
       Cut cut;
-      const bool active = find_share(a, R, cta, gridDim.x, w, cut, cta == 0);
+      const bool active = find_share(a, kPaWork, cta, gridDim.x, w, cut, cta == 0);
       if (lane == 0) {
         it.w = w;
         it.cut = cut;
@@ -590,12 +595,12 @@ __global__ void __launch_bounds__(kPaThreads, 2)
                                     8 * q) = u;
         }
       }
-      more = c.u + count < c.u1;
+      more = c.u + count + kPaWork.pad < c.u1;
       if (more) {
         pa_sync();   // the sums, the query fragments and the item are free again
         if (tid == 0) {
           it.w.u += count;
-          it.w.next_item(a, R);
+          it.w.next_item(a, kPaWork);
         }
       }
     }
@@ -670,8 +675,8 @@ cudaError_t pa_launch(const PagedAttnArgs& a, const CUtensorMap& map, cudaStream
 // Rows (tokens x query heads of a kv-head) a sequence, on average, from which on the
 // many-row kernel is faster.  It costs the same for any number up to 128, these tiles
 // of 8 rows their number.  In us, these / that: 8 sequences over 4000 positions,
-// D = 128, 48 rows 43 / 50, 64 rows 50 / 50, 96 rows 73 / 51; D = 64, 64 rows 36 / 41,
-// 96 rows 52 / 42; one over 8000, D = 128, 64 rows 28 / 36, 96 rows 37 / 36.
+// D = 128, 48 rows 43 / 45, 64 rows 50 / 46, 96 rows 72 / 46; D = 64, 64 rows 36 / 38,
+// 96 rows 51 / 39; one over 8000, D = 128, 64 rows 26 / 30, 96 rows 35 / 31.
 constexpr int kTcMinRows = 80;
 
 }  // namespace

@@ -29,12 +29,13 @@
 //
 // Bound by the tensor cores in principle (4 x 256 x 128 x D flops a tile take 2048
 // cycles at D = 128).  Measured on four prompts' chunks of 512 rows after contexts to
-// 8K, 32 heads over 8, D = 128: 96 us, 0.50 PFLOP/s of the seen positions.  A CTA's
+// 8K, 32 heads over 8, D = 128: 84 us, 0.57 PFLOP/s of the seen positions.  A CTA's
 // 20 tiles take some 5200 cycles each (a half's softmax, 3300 while it shares the
 // schedulers with the other half's and the widening, and its products, 1024, follow
 // one another); the start, the queries of two parts and the records of split items
 // take a third of the time.  Steps of 64 positions, whose products could run under
-// the softmax, took 104 us: twice the reads of the queries from shared memory.
+// the softmax, took 104 us where this took 98: twice the reads of the queries from
+// shared memory.
 #include "paged_dev.cuh"
 
 namespace futr {
@@ -42,6 +43,10 @@ namespace futr {
 namespace {
 
 constexpr int kTcRows = 256, kTcHalf = 128;
+// An item's start (queries) and end (records) count as four tiles in the cut: CTAs with
+// three items ended last.  With 0, 3, 4, 5, 6 and 8 the chunks below take 96.0, 85.8,
+// 84.3, 85.1, 86.7 and 89.3 us.
+constexpr Rows kTcWork{kTcRows, 4};
 constexpr int kTcThreads = 14 * 32;
 constexpr int kTcSoft = 8 * 32;                 // softmax threads
 constexpr int kTcRing = 2;
@@ -157,6 +162,8 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
+
+__device__ __forceinline__ void tc_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Byte offset of dim i of row r in an f16 operand (blocks of 64 dims, swizzled rows).
 __device__ __forceinline__ int tc_at(int r, int i) {
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 0) {
     Walk w;
     Cut cut;
-    const bool active = find_share(a, kTcRows, cta, gridDim.x, w, cut, cta == 0);
+    const bool active = find_share(a, kTcWork, cta, gridDim.x, w, cut, cta == 0);
     if (lane == 0) {
       it.w = w;
       it.cut = cut;
@@ -433,7 +440,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---------------------------------------------------------- producer --
     if (active) {
       int issued = 0;
-      if (!produce_tiles<D>(a, &map, kTcRows, w, smem + Lay::kStage, s_raw, full, empty, kTcRing, issued)) {
+      if (!produce_tiles<D>(a, &map, kTcWork, w, smem + Lay::kStage, s_raw, full, empty, kTcRing, issued)) {
         record_timeout(a.err);
         *s_dead = 1;
       }
@@ -493,7 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         w.u += count;
         ++part;
         part1 += nh - 1;
-        if (w.u < w.u1) w.next_item(a, kTcRows);
+        if (w.u < w.u1) w.next_item(a, kTcWork);
       }
     }
   } else if (warp >= 8) {
@@ -572,7 +579,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         w.u += count;
-        if (w.u < w.u1) w.next_item(a, kTcRows);
+        if (w.u < w.u1) w.next_item(a, kTcWork);
       }
     }
   } else {
@@ -589,6 +596,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int count = it.count, valid = it.valid;
         const bool here = kTcHalf * half < valid;
         const int r = kTcHalf * half + row, myrow = it.w.rt * kTcRows + min(r, valid - 1);
+        if (r < valid) {   // all rows on their way at once: the loads below take eight at a time
+          const int i = myrow / a.G;
+          const uint16_t* q = static_cast<const uint16_t*>(a.q) + (size_t)(it.w.row0 + i) * a.ld_q +
+                              (size_t)(it.w.kvh * a.G + myrow - i * a.G) * D;
+          for (int l = 0; l < D / 64; ++l) tc_prefetch(q + 64 * l);
+          if (a.c.rope)
+            for (int l = myrow - i * a.G; l < D / 32; l += a.G)
+              tc_prefetch(a.c.rope + (size_t)(it.w.p0 + i) * (D / 2) + 16 * l);
+        }
         float M = -INFINITY, L = 0.f;
         if (here) {
           tc_load_queries<D, kHalf>(a, it.w, valid, half, smem + Lay::kQ + half * Lay::kOp, s_qs);
@@ -683,12 +699,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the CTA with an item's beginning describes the join
         if (!whole && live && c.item0 == c.u && tid == 0)
           join = TcJoin{it.cut.owner(item1 - 1) - cta, c.row0, c.kvh, c.rt, valid};
-        more = c.u + count < c.u1;
+        more = c.u + count + kTcWork.pad < c.u1;
         if (more) {
           tc_soft_sync();   // the item's bounds are read no more
           if (tid == 0) {
             it.w.u += count;
-            it.w.next_item(a, kTcRows);
+            it.w.next_item(a, kTcWork);
           }
         }
       }
@@ -714,7 +730,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // A kernel of its own, so that every SM takes part: the CTA that arrived last would
 // read 133 KB a part by itself, 19 of them for one sequence of 256 rows over 8000
 // positions, a call of 73 us that takes 46 us like this.  Where items have few parts
-// it costs a launch: 96 us for the chunks above, 93 without it.
+// it costs a launch: 96 us for the chunks above, 93 without it (in equal shares of
+// tiles).
 constexpr int kTcJoinRows = 32;
 
 template <int D, bool kHalf>

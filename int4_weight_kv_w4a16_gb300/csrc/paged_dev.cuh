@@ -65,6 +65,13 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
   return q;
 }
 
+// What a kernel makes of rows: R rows a row tile, whose start (queries, the join of
+// its parts) counts as much as `pad` tiles of positions.  The units of an item are
+// `pad` that hold nothing, then its tiles.
+struct Rows {
+  int R, pad;
+};
+
 // Row tile rt of a sequence (n rows from position p0, G query heads a kv-head,
 // R rows a tile): its tiles [t0, t1).
 struct TileRange {
@@ -81,13 +88,14 @@ __device__ __forceinline__ TileRange row_tile(int n, int p0, int G, int R, int w
   return {lo / kPaTile, last / kPaTile + 1};
 }
 
-__device__ __forceinline__ long long seq_tiles(int n, int p0, int G, int R, int window) {
+// The units of a sequence and kv-head.
+__device__ __forceinline__ long long seq_units(int n, int p0, int G, Rows s, int window) {
   long long w = 0;
-  const int nrt = (n * G + R - 1) / R;
+  const int nrt = (n * G + s.R - 1) / s.R;
 #pragma unroll 1
   for (int rt = 0; rt < nrt; ++rt) {
-    const TileRange t = row_tile(n, p0, G, R, window, rt);
-    w += t.t1 - t.t0;
+    const TileRange t = row_tile(n, p0, G, s.R, window, rt);
+    w += s.pad + t.t1 - t.t0;
   }
   return w;
 }
@@ -113,31 +121,34 @@ struct Cut {
 // the next tile.  The producer warp keeps one copy, the consumers another.
 struct Walk {
   int b, kvh, rt, row0, n, p0;
-  long long per_head;      // tiles of one kv-head of sequence b
+  long long per_head;      // units of one kv-head of sequence b
   long long u, u1;         // this CTA's share [u, u1), u advancing
   long long item0;         // unit index of the current item's first tile
   TileRange t;
 
   // Enter sequence b (rows known); the item that holds unit `at` of its units.
-  __device__ __forceinline__ void enter(const PagedAttnArgs& a, int R, long long at, long long base) {
+  __device__ __forceinline__ void enter(const PagedAttnArgs& a, Rows s, long long at, long long base) {
     kvh = (int)quot(at, per_head);
     long long rem = at - (long long)kvh * per_head;
     rt = 0;
-    t = row_tile(n, p0, a.G, R, a.window, 0);
+    t = row_tile(n, p0, a.G, s.R, a.window, 0);
 #pragma unroll 1
-    while (rem >= t.t1 - t.t0) {
-      rem -= t.t1 - t.t0;
+    while (rem >= s.pad + t.t1 - t.t0) {
+      rem -= s.pad + t.t1 - t.t0;
       ++rt;
-      t = row_tile(n, p0, a.G, R, a.window, rt);
+      t = row_tile(n, p0, a.G, s.R, a.window, rt);
     }
-    item0 = base + at - rem;
+    item0 = base + at - rem + s.pad;
+    u = max(u, item0);
   }
 
-  // Step to the item after the current one (its units start at item0 + tiles).
-  __device__ __forceinline__ void next_item(const PagedAttnArgs& a, int R) {
-    item0 += t.t1 - t.t0;
+  // Step to the first tile of the item after the current one, which is done (it may
+  // lie behind this share).
+  __device__ __forceinline__ void next_item(const PagedAttnArgs& a, Rows s) {
+    item0 += t.t1 - t.t0 + s.pad;
+    u = item0;
     ++rt;
-    if (rt * R >= n * a.G) {
+    if (rt * s.R >= n * a.G) {
       rt = 0;
       if (++kvh == a.Hkv) {
         kvh = 0;
@@ -145,26 +156,26 @@ struct Walk {
           ++b;
           paged_seq(a.r, a.c, b, row0, n, p0);
         } while (n == 0);   // u < u1: a later sequence has rows
-        per_head = seq_tiles(n, p0, a.G, R, a.window);
+        per_head = seq_units(n, p0, a.G, s, a.window);
       }
     }
-    t = row_tile(n, p0, a.G, R, a.window, rt);
+    t = row_tile(n, p0, a.G, s.R, a.window, rt);
   }
 };
 
 // The call's units, their cut, and the share of CTA `cta` (a full warp).  False:
-// it has none.
-__device__ __forceinline__ bool find_share(const PagedAttnArgs& a, int R, int cta, int ctas, Walk& w, Cut& cut,
+// it has no tile.
+__device__ __forceinline__ bool find_share(const PagedAttnArgs& a, Rows s, int cta, int ctas, Walk& w, Cut& cut,
                                            bool report) {
   const int lane = threadIdx.x & 31;
   int row0 = 0, n = 0, p0 = 0;   // of sequence b0 + lane
-  long long per = 0, incl = 0;   // its tiles per kv-head; all tiles of this round's sequences up to it
+  long long per = 0, incl = 0;   // its units per kv-head; all units of this round's sequences up to it
   auto look = [&](int b0) {
     n = 0;
     per = 0;
     if (b0 + lane < a.r.batch) {
       if (!paged_seq(a.r, a.c, b0 + lane, row0, n, p0) && report) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
-      per = seq_tiles(n, p0, a.G, R, a.window);
+      per = seq_units(n, p0, a.G, s, a.window);
     }
     incl = per * a.Hkv;
 #pragma unroll 1
@@ -197,8 +208,8 @@ __device__ __forceinline__ bool find_share(const PagedAttnArgs& a, int R, int ct
       w.p0 = __shfl_sync(0xffffffffu, p0, src);
       w.per_head = __shfl_sync(0xffffffffu, per, src);
       const long long base = before + __shfl_sync(0xffffffffu, incl - per * a.Hkv, src);
-      w.enter(a, R, w.u - base, base);
-      return true;
+      w.enter(a, s, w.u - base, base);
+      return w.u < w.u1;
     }
     before += __shfl_sync(0xffffffffu, incl, top);
   }
@@ -212,7 +223,7 @@ __device__ __forceinline__ bool find_share(const PagedAttnArgs& a, int R, int ct
 // sub-tiles, (key scale, log2 and inverse of the value scale, 0).  False: a wait
 // ran out (`issued` stages are under way or done).
 template <int D>
-__device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUtensorMap* map, int R, Walk& w,
+__device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUtensorMap* map, Rows s, Walk& w,
                                               uint8_t* stages, float4* s_scale, uint64_t* full, uint64_t* empty,
                                               int ring, int& issued) {
   const int lane = threadIdx.x & 31, page = a.c.page, plog = a.c.page_log2;
@@ -229,16 +240,16 @@ __device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUte
     const int pg0 = (first * kPaTile) >> plog, pg1 = (end - 1) >> plog;
     // (pages before the first row's window are not looked at: a program may have
     // given them back)
-    const int seen = a.window > 0 ? max(0, w.p0 + w.rt * R / a.G - a.window + 1) >> plog : 0;
+    const int seen = a.window > 0 ? max(0, w.p0 + w.rt * s.R / a.G - a.window + 1) >> plog : 0;
     const int* tab = a.r.table + (size_t)w.b * a.r.table_ld;
-    auto fetch = [&](int pg, int& id, float2& s) {
+    auto fetch = [&](int pg, int& id, float2& sc) {
       id = pg >= seen && pg <= pg1 ? tab[pg] : -1;
       if (id < 0 || id >= a.c.n_pages) {
         if (pg >= seen && pg <= pg1) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
         id = -1;
       }
-      s = make_float2(0.f, 0.f);
-      if (id >= 0) s = reinterpret_cast<const float2*>(a.c.scales)[(size_t)id * a.Hkv + w.kvh];
+      sc = make_float2(0.f, 0.f);
+      if (id >= 0) sc = reinterpret_cast<const float2*>(a.c.scales)[(size_t)id * a.Hkv + w.kvh];
     };
     int id, id_next = 0, base = pg0;
     float2 sc, sc_next = make_float2(0.f, 0.f);
@@ -289,7 +300,7 @@ __device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUte
       }
     }
     w.u += count;
-    if (w.u < w.u1) w.next_item(a, R);
+    if (w.u < w.u1) w.next_item(a, s);
   }
   return ok;
 }
