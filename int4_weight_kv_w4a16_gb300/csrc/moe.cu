@@ -17,8 +17,8 @@
 // Above 8 tokens a fourth adds down's parts.
 //
 // The expert kernels are bound by the weight stream: 17 tokens through 8 of 128
-// experts (4096 x 1536, 830 MB) take 162 us, 5.1 TB/s; 32 through 2 of 8 (4096 x
-// 14336, 726 MB) 189 us, 3.8 TB/s, where the unpacking and the products of up to 16
+// experts (4096 x 1536, 830 MB) take 160 us, 5.2 TB/s; 32 through 2 of 8 (4096 x
+// 14336, 726 MB) 184 us, 4.0 TB/s, where the unpacking and the products of up to 16
 // columns take as long as the stream; one token through 2 of 8 (181 MB) 47 us, some
 // 15 of them the router, the starts and the ends of three kernels.  All units of the
 // chosen experts form one run, cut into equal contiguous shares, one per CTA of a
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
     bool waited = !kDown;
     int rows_due = 0;   // down: stages whose activations wait for gate/up
     const __half* due[kMoeRing];
-    int due_n[kMoeRing];
+    int due_bytes[kMoeRing];
     for (int u = u0; u < u1 && ok;) {
       int rb, ai, g, end;
       run.at(u, rb, ai, g, end);
@@ -666,9 +666,13 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
       const int e = rt->expert[ai], off = rt->off[ai], n = rt->off[ai + 1] - off;
       const uint8_t* w = a.blob + kHeaderBytes + (size_t)e * a.expert_bytes + (kDown ? a.gu_bytes : 0) +
                          ((size_t)rb * run.ng + g) * kUnitBytes;
-      // this lane's token's records (columns n..31 have none)
-      const __half* row = kDown ? a.act : a.xh;
-      if (lane < n) row += ((size_t)(kDown ? off + lane : rt->token[off + lane]) * run.ng + g) * kRecHalves;
+      // Gate/up: this lane's token's records (lanes n..31 have none).  Down: the
+      // expert's records of a group lie side by side, one copy (a copy each: 189 us for
+      // the 32 tokens that take 184).
+      const int lanes = kDown ? 1 : n, rec_bytes = kDown ? n * kRecBytes : kRecBytes;
+      const size_t step = kDown ? (size_t)a.T * a.K * kRecHalves : kRecHalves;
+      const __half* row = kDown ? a.act + g * step + (size_t)off * kRecHalves : a.xh + g * step;
+      if (!kDown && lane < n) row += (size_t)rt->token[off + lane] * run.ng * kRecHalves;
       for (; u < end; ++u) {
         if (issued >= kMoeRing) {
           if (!moe_wait(&empty[slot], phase ^ 1u, a.err)) {
@@ -682,14 +686,14 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
           bulk_g2s(st, w, kUnitBytes, &full[slot]);
         }
         if (waited) {
-          if (lane < n) bulk_g2s(st + kUnitBytes + lane * kRecBytes, row, kRecBytes, &full[slot]);
+          if (lane < lanes) bulk_g2s(st + kUnitBytes + lane * kRecBytes, row, rec_bytes, &full[slot]);
         } else {
           // the ring's first stages: weights now, activations after the wait
 #pragma unroll
           for (int i = 0; i < kMoeRing; ++i)
             if (i == rows_due) {
               due[i] = row;
-              due_n[i] = n;
+              due_bytes[i] = rec_bytes;
             }
           ++rows_due;
           if (rows_due == kMoeRing || u + 1 == u1) {
@@ -697,12 +701,12 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
             waited = true;
 #pragma unroll
             for (int i = 0; i < kMoeRing; ++i)
-              if (i < rows_due && lane < due_n[i])
-                bulk_g2s(smem + i * Lay::kStage + kUnitBytes + lane * kRecBytes, due[i], kRecBytes, &full[i]);
+              if (i < rows_due && lane == 0)   // (down only)
+                bulk_g2s(smem + i * Lay::kStage + kUnitBytes, due[i], due_bytes[i], &full[i]);
           }
         }
         w += kUnitBytes;
-        row += kRecHalves;
+        row += step;
         ++issued;
         if (++slot == kMoeRing) {
           slot = 0;
@@ -796,7 +800,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
             const __half2 hv = __floats2half2_rn(v[0] * inv, v[1] * inv);
             const float2 hf = __half22float2(hv);
             const float sum = warp_sum(hf.x + hf.y);
-            __half* rec = a.act + ((size_t)(off + c) * (a.I / kGroup) + (rb >> 1)) * kRecHalves;
+            __half* rec = a.act + ((size_t)(rb >> 1) * (a.T * a.K) + off + c) * kRecHalves;
             reinterpret_cast<__half2*>(rec + 64 * (rb & 1))[lane] = hv;
             if (lane == 0) {
               MoeTail* tail = reinterpret_cast<MoeTail*>(rec + kGroup);

@@ -69,7 +69,7 @@ struct MoeArgs {
   float* logits;                       // [T][E]
   float* rms;                          // [T] RMSNorm factor times the factor of the token's f16 records
   __half* xh;                          // [T][H / 128][136]: the tokens as f16 records
-  __half* act;                         // [pairs][I / 128][136]: the down product's inputs
+  __half* act;                         // [I / 128][pairs][136]: the down product's inputs, pairs by expert
   float* rec;                          // split records, two per CTA
   int* choice;                         // [T][K] the router's choices
   float* share;                        // [T][K] and their weights
