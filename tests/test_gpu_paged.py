@@ -431,3 +431,22 @@ def test_query_that_is_not_finite_stays_its_own():
         keep[1, 2] = keep[2, 0] = False
         assert torch.equal(got[keep], want[keep])
         assert bool(torch.isnan(got[1, 2]).all())
+
+
+@pytest.mark.parametrize("counts", [[2, 0, 1], [70, 0, 41]], ids=["few", "many"])
+def test_rows_behind_the_last_sequence_stay(counts):
+    """Row tensors longer than start says: the rows behind are not read (NaN), nor written."""
+    c = Paged(8, 2, 64, 32, 3, 6)
+    c.fill(3)
+    n, pos = sum(counts), [33, 7, 64]
+    q, k, v = (rows(n + 5, h, 64, torch.bfloat16, 40 + h) for h in (8, 2, 2))
+    for t in (q, k, v):
+        t[n:] = float("nan")
+    before = c.codes[0].clone(), c.scales[0].clone()
+    futr.futr_paged_append(c.cache, 0, 3, ints(pos), starts(counts), c.table, k, v)
+    out = torch.full_like(q, 7.0)
+    futr.futr_paged_attention(c.cache, 0, 3, ints(pos), starts(counts), c.table, q, out, c.ws)
+    assert futr.futr_paged_check(c.cache, c.ws) == futr.FUTR_OK
+    check_append(c, before, k[:n], v[:n], pos, counts)
+    check_attention(c, q[:n], out[:n], pos, counts)
+    assert bool((out[n:] == 7).all())
