@@ -318,7 +318,8 @@ class _Torch:
         import torch
         self.int32, self.float32, self.bfloat16 = torch.int32, torch.float32, torch.bfloat16
         self.rows = {torch.bfloat16: FUTR_DTYPE_BF16, torch.float16: FUTR_DTYPE_F16}
-        self.device = torch.cuda.current_device
+        # (torch.cuda's own functions ask first whether CUDA is set up: tensors on it are at hand here)
+        self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
 
@@ -335,9 +336,8 @@ def _bad_tensor(t, name, want, device):
     raise ValueError(f"{name} must be {want}{where}, not {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _on_device(descriptor, name, device):
-    if descriptor._mem.get_device() != device:
-        raise ValueError(f"{name} is on {descriptor._mem.device}, not on CUDA device {device}, the current one")
+def _elsewhere(descriptor, name, device):
+    raise ValueError(f"{name} is on {descriptor._mem.device}, not on CUDA device {device}, the current one")
 
 
 def _row_dtype(T, a, b, names) -> int:
@@ -347,11 +347,12 @@ def _row_dtype(T, a, b, names) -> int:
     return T.rows[dtype]
 
 
-def _row_stride(t, name, device, n, heads, d) -> int:
-    """Elements from one row to the next of a row tensor [n, heads, d]."""
+def _row_stride(t, name, device, shape) -> int:
+    """Elements from one row to the next of a row tensor (rows, heads, head_dim)."""
     ld, sh, sd = t.stride()
-    if t.shape != (n, heads, d) or sd != 1 or (sh != d and heads != 1) or t.get_device() != device:
-        _bad_tensor(t, name, f"rows ({n}, {heads}, {d}), the heads of a row contiguous,", device)
+    n, heads, d = shape
+    if t.shape != shape or sd != 1 or (sh != d and heads != 1) or t.get_device() != device:
+        _bad_tensor(t, name, f"rows {shape}, the heads of a row contiguous,", device)
     return ld if n > 1 else -(-heads * d // 8) * 8
 
 
@@ -401,11 +402,12 @@ def futr_paged_append(cache, layer, batch, pos, start, table, k, v, stream=None)
     """Append the rows k, v [n_rows, kv-heads, head_dim]; start None: one row per sequence."""
     T = _T or _torch()
     device = T.device()
-    shape = cache.shape
-    n, heads, d = k.shape[0], shape.n_kv_heads, shape.head_dim
+    n = k.shape[0]
+    rows = (n, cache.shape.n_kv_heads, cache.shape.head_dim)
     dtype = _row_dtype(T, k, v, "k and v")
-    _on_device(cache, "the cache", device)
-    ld_k, ld_v = _row_stride(k, "k", device, n, heads, d), _row_stride(v, "v", device, n, heads, d)
+    if cache._mem.get_device() != device:
+        _elsewhere(cache, "the cache", device)
+    ld_k, ld_v = _row_stride(k, "k", device, rows), _row_stride(v, "v", device, rows)
     p, s, n, t, ld = _paged_rows(T, batch, pos, start, table, n, device)
     _ok(lib().futr_paged_append(C.addressof(cache), layer, batch, p, s, n, t, ld, k.data_ptr(), ld_k, v.data_ptr(),
                                 ld_v, dtype, T.stream(device) if stream is None else _stream(stream)),
@@ -431,12 +433,14 @@ def futr_paged_attention(cache, layer, batch, pos, start, table, q, out, ws, sca
     (same shape and type); scale 0 is 1/sqrt(head_dim), window 0 is none."""
     T = _T or _torch()
     device = T.device()
-    shape = cache.shape
-    n, heads, d = q.shape[0], shape.n_q_heads, shape.head_dim
+    n = q.shape[0]
+    rows = (n, cache.shape.n_q_heads, cache.shape.head_dim)
     dtype = _row_dtype(T, q, out, "q and out")
-    _on_device(cache, "the cache", device)
-    _on_device(ws, "the workspace", device)
-    ld_q, ld_out = _row_stride(q, "q", device, n, heads, d), _row_stride(out, "out", device, n, heads, d)
+    if cache._mem.get_device() != device:
+        _elsewhere(cache, "the cache", device)
+    if ws._mem.get_device() != device:
+        _elsewhere(ws, "the workspace", device)
+    ld_q, ld_out = _row_stride(q, "q", device, rows), _row_stride(out, "out", device, rows)
     p, s, n, t, ld = _paged_rows(T, batch, pos, start, table, n, device)
     _ok(lib().futr_paged_attention(C.addressof(cache), layer, batch, p, s, n, t, ld, q.data_ptr(), ld_q,
                                    out.data_ptr(), ld_out, dtype, scale, window, C.addressof(ws),
@@ -520,7 +524,8 @@ def futr_moe_layer(x, gain, router, blob, resid, y, ws, ids=None, weights=None, 
     H, K, bf, n = s.hidden, s.top_k, T.bfloat16, x.shape[0]
     rows = (n, H)
     _moe_blob(blob, ws.blob_bytes, device)
-    _on_device(ws, "the workspace", device)
+    if ws._mem.get_device() != device:
+        _elsewhere(ws, "the workspace", device)
     _ok(lib().futr_moe_layer(_dense(x, "x", bf, rows, device), _dense(gain, "gain", T.float32, (H,), device),
                              _dense(router, "router", bf, (s.n_experts, H), device), blob.data_ptr(), n,
                              _dense(resid, "resid", bf, rows, device), _dense(y, "y", bf, rows, device),
