@@ -728,6 +728,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
   } else {
     // ---------------------------------------------------------- consumers --
     if (kDown) pdl_wait();   // records and counters are gate/up's until it has ended
+    if (kDown && cta == 0 && tid == 0) *a.active = rt->n_active;
     MoeRing ring{0, 0u, true};
     for (int u = u0; u < u1;) {
       // one item's part in this share
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
       moe_sync();
       bool write = !*s_snap;
       const bool apart = kDown && sums_apart(a.T);
-      if (write && (apart || seg0 != i0 || seg1 != i1)) {
+      if (write && (seg0 != i0 || seg1 != i1)) {
         // a part: this CTA's record, then the last arrival adds them in CTA order
         float* rec = a.rec + ((size_t)cta * 2 + (i0 < seg0 ? 0 : 1)) * kMoeRecFloats;
         for (int i = tid; i < cols * 32; i += kMoeCW * 32) {
@@ -766,9 +767,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
         }
         moe_sync();
         const int c0 = cut.owner(i0), c1 = cut.owner(i1 - 1);
-        if (apart) {
-          if (cta == 0 && tid == 0) *a.active = rt->n_active;
-        } else if (tid == 0) {
+        if (!apart && tid == 0) {
           *s_last = atom_add_acq_rel_gpu(&a.cnt[kRouterTiles + c0], 1u) == (unsigned)(c1 - c0) ? 1 : 0;
           if (*s_last) a.cnt[kRouterTiles + c0] = 0u;
         }
@@ -833,6 +832,7 @@ __global__ void __launch_bounds__(256) moe_sum_kernel(const MoeArgs a) {
   const int rb = blockIdx.x, t = 8 * blockIdx.y + (threadIdx.x >> 5), q = threadIdx.x & 31;
   if (t >= a.T) return;
   const int i0 = rb * run.item_len, c0 = cut.owner(i0), c1 = cut.owner(i0 + run.item_len - 1);
+  if (c0 == c1) return;   // one CTA had the whole row block, and wrote it
   const float4* r0 = reinterpret_cast<const float4*>(a.rec + ((size_t)c0 * 2 + 1) * kMoeRecFloats);
   const float4* rn = reinterpret_cast<const float4*>(a.rec + (size_t)(c0 + 1) * 2 * kMoeRecFloats);
   const size_t o = (size_t)t * a.H + (size_t)rb * kRowsPerBlock + 4 * q;

@@ -139,6 +139,14 @@ def test_larger_layer_with_split_rows():
     m.check(rows(m, 20), None)
 
 
+@pytest.mark.parametrize("I", [128, 1280])
+def test_more_row_blocks_than_ctas(I):
+    """A wide layer: CTAs of the down product own several row blocks, whole ones beside parts."""
+    m = Moe(65536, I, 1, 1, eps=0.0, seed=11)
+    for T in (1, 8, 9, 20):
+        m.check(rows(m, T, T), rows(m, T, 30 + T))
+
+
 def test_every_token_with_one_expert_and_equal_logits():
     """All tokens at the same experts (full columns), and ties: the lowest experts first."""
     m = Moe(256, 256, 8, 3, seed=5)
