@@ -189,6 +189,8 @@ CHUNKS = [
     (8, 8, 64, 128, torch.bfloat16, False, 50, [0, 10], [256, 255]),
     (28, 4, 128, 64, torch.float16, False, 0, [2000, 1], [3, 150]),
     (4, 1, 64, 64, torch.bfloat16, False, 0, [3000], [500]),
+    (16, 1, 64, 32, torch.bfloat16, False, 0, [i * 53 % 300 for i in range(40)], [5 + i % 7 for i in range(40)]),
+    (16, 2, 128, 16, torch.bfloat16, True, 40, [2 * i for i in range(35)], [20 * (i % 3) for i in range(35)]),
 ]
 
 
