@@ -20,8 +20,9 @@
 //                over the scores it has read, where they are P V's A operand.
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (D columns each).
 //
-// The query of f16 rows has one f16 part here, too: a second does not fit into shared
-// memory beside two value buffers (an output's error is 4e-4 instead of 2e-4).
+// The query of f16 rows has two f16 parts only at D = 64: at D = 128 a second does not
+// fit into shared memory beside two value buffers (an output's error is then 4e-4
+// instead of 2e-4).
 //
 // The running reference M of a row follows its maximum only when that has grown
 // by more than 2^8: a weight up to 2^8 is a good f16, the normalizer is fp32, and
@@ -52,11 +53,18 @@ constexpr int kTcSoft = 8 * 32;                 // softmax threads
 constexpr int kTcRing = 2;
 constexpr float kTiny = 1.17549435e-38f;
 
-template <int D>
+// f16 parts of a query element: two for f16 rows where shared memory has the room (four
+// chunks of 256 rows after 4000 positions, D = 64: an error of 2.4e-4 in 61.7 us, with
+// one part 5.3e-4 in 58.3).
+template <int D, bool kHalf>
+constexpr int kTcParts = kHalf && D == 64 ? 2 : 1;
+
+template <int D, bool kHalf>
 struct TcLayout {
+  static constexpr int kParts = kTcParts<D, kHalf>;
   static constexpr int kOp = kTcHalf * D * 2;                    // one f16 operand of 128 rows
-  static constexpr int kQ = 0;                                   // two halves
-  static constexpr int kK = kQ + 2 * kOp;
+  static constexpr int kQ = 0;                                   // [half][part]
+  static constexpr int kK = kQ + 2 * kParts * kOp;
   static constexpr int kV = kK + kOp;
   static constexpr int kStage = kV + 2 * kOp;                    // two of the values; ring of 8-bit tiles
   static constexpr int kRaw = kStage + kTcRing * 2 * kPaTile * D;   // [ring][sub-tiles] float4
@@ -240,6 +248,10 @@ __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Wa
           *reinterpret_cast<uint32_t*>(dst) = pack_half2(x[h][0] * inv, x[h][P - 1] * inv);
         else
           *reinterpret_cast<__half*>(dst) = __float2half_rn(x[h][0] * inv);
+        if (kTcParts<D, kHalf> == 2) {
+          const float v = x[h][0] * inv;
+          *reinterpret_cast<__half*>(dst + kTcHalf * D * 2) = __float2half_rn(v - __half2float(__float2half_rn(v)));
+        }
       }
       if (lane == 0)
         qs[kTcHalf * half + r0 + k] =
@@ -357,7 +369,7 @@ __device__ __forceinline__ void tc_set(const PagedAttnArgs& a, TcItem& it) {
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged_attn_tc_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap map) {
-  using Lay = TcLayout<D>;
+  using Lay = TcLayout<D, kHalf>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float4* s_raw = reinterpret_cast<float4*>(smem + Lay::kRaw);
@@ -455,10 +467,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t v16 = tc_desc_lo(smem_u32(smem + Lay::kV), kTcHalf * 128);
       auto scores = [&](int h) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = ((ks >> 2) * (kTcHalf * 128) + (ks & 3) * 32) >> 4;
-          tc_mma_ss(tm + 128 * h, q16 + h * (Lay::kOp >> 4) + off, k16 + off, kIdescS, ks > 0);
-        }
+        for (int part = 0; part < Lay::kParts; ++part)
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * (kTcHalf * 128) + (ks & 3) * 32) >> 4;
+            tc_mma_ss(tm + 128 * h, q16 + (h * Lay::kParts + part) * (Lay::kOp >> 4) + off, k16 + off, kIdescS,
+                      part + ks > 0);
+          }
         tc_commit(&sfull[h]);
       };
       auto values = [&](int h, bool first) {
@@ -607,7 +622,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         float M = -INFINITY, L = 0.f;
         if (here) {
-          tc_load_queries<D, kHalf>(a, it.w, valid, half, smem + Lay::kQ + half * Lay::kOp, s_qs);
+          tc_load_queries<D, kHalf>(a, it.w, valid, half, smem + Lay::kQ + half * Lay::kParts * Lay::kOp, s_qs);
           tc_proxy_fence();
           __syncwarp();
           if (lane == 0) mbar_arrive(&qready[half]);
@@ -782,9 +797,9 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnArgs a, 
   }
 }
 
-template <int D>
+template <int D, bool kHalf>
 size_t tc_smem() {
-  return (size_t)TcLayout<D>::kBytes + 1024;
+  return (size_t)TcLayout<D, kHalf>::kBytes + 1024;
 }
 
 template <int D, bool kHalf>
@@ -795,14 +810,14 @@ cudaError_t tc_launch(const PagedAttnArgs& a, const CUtensorMap& map, int ctas, 
   if (e != cudaSuccess) return e;
   if (!configured.done(dev)) {
     e = cudaFuncSetAttribute(paged_attn_tc_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)tc_smem<D>());
+                             (int)tc_smem<D, kHalf>());
     if (e != cudaSuccess) return e;
     configured.mark(dev);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = tc_smem<D>();
+  cfg.dynamicSmemBytes = tc_smem<D, kHalf>();
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
