@@ -382,10 +382,9 @@ futr_status futr_check(const futr_ws* ws, const futr_kv* kv, void* stream);
  * Row tensors are 16-bit (FUTR_DTYPE_*), heads and dims contiguous, tokens ld_*
  * elements apart (a multiple of 8, so a slice of a fused QKV row will do),
  * 16-byte aligned.  Only the shape's head counts, head_dim and rope_theta are
- * used.  The calls launch one kernel (attention for many rows a sequence: two)
- * with programmatic dependent launch, read
- * pos, start and table on the device, and can be captured in a CUDA graph; a
- * captured call follows lengths that change. */
+ * used.  The calls launch one kernel (attention with many rows: up to three) with
+ * programmatic dependent launch, read pos, start and table on the device, and can
+ * be captured in a CUDA graph; a captured call follows lengths that change. */
 #define FUTR_DTYPE_BF16 0
 #define FUTR_DTYPE_F16  1
 
@@ -451,8 +450,8 @@ futr_status futr_paged_workspace_init(const futr_shape* shape, void* mem, size_t
  *   out = sum_j softmax_j(scale * q'.k_j) v_j      (scale 0: 1/sqrt(d))
  * The rotated query and the softmax weights enter the products as fp16 (the
  * query divided by a power of two near its largest element; of fp16 rows in two
- * parts, unless head_dim is 128 and a sequence has 80 or more rows x query heads of
- * a kv-head on average); sums and softmax statistics are fp32.  A row that sees no position (missing pages) gets zeros.
+ * parts, unless head_dim is 128 and the kernel for sequences of many rows, 80 or
+ * more times the query heads of a kv-head, takes them); sums and softmax statistics are fp32.  A row that sees no position (missing pages) gets zeros.
  * out may not overlap q.
  */
 futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t batch, const int32_t* pos,

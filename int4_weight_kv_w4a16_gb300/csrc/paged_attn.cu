@@ -37,6 +37,8 @@
 // to 50K (269 MB): 51.3 us, 5.2 TB/s; the copies alone, in equal shares of tiles, 30
 // and 48.5 us.  One sequence of 1024 positions: 7.9 us, the latency of share -> page
 // id -> tile -> join.
+#include <climits>
+
 #include "paged_dev.cuh"
 
 namespace futr {
@@ -678,6 +680,14 @@ cudaError_t pa_launch(const PagedAttnArgs& a, const CUtensorMap& map, cudaStream
 // D = 128, 48 rows 43 / 45, 64 rows 50 / 46, 96 rows 72 / 46; D = 64, 64 rows 36 / 38,
 // 96 rows 51 / 39; one over 8000, D = 128, 64 rows 26 / 30, 96 rows 35 / 31.
 constexpr int kTcMinRows = 80;
+// Where sequences may differ much (their rows are on the device), both kernels, each
+// for its sequences: from 1024 rows on in all, where a chunk among single tokens costs
+// the tiles of 8 rows more than two launches, and below 256 a sequence on average,
+// where the single tokens are worth one.  31 single tokens and a chunk of 512 tokens
+// after 2000 positions (G = 4): 85 us, by the tiles of 8 rows alone 250; with a chunk
+// of 256 72 and 134; 64 sequences of 5 drafted tokens, where the many-row kernel finds
+// nothing, 144 and 137.
+constexpr int kBothMinRows = 1024, kBothMaxRows = 256;
 
 }  // namespace
 
@@ -696,10 +706,20 @@ int paged_attn_sms() {
 
 int paged_attn_ctas(int sms) { return sms * kPaMaxPerSm; }
 
-cudaError_t launch_paged_attention(const PagedAttnArgs& a, const CUtensorMap& map, int d, int dtype, cudaStream_t st) {
-  // sequences of many rows on average: 256-row tiles on the tensor cores
-  if ((long long)a.r.n_rows * a.G >= (long long)kTcMinRows * a.r.batch)
-    return launch_paged_attention_tc(a, map, d, dtype, paged_attn_sms(), st);
+cudaError_t launch_paged_attention(const PagedAttnArgs& args, const CUtensorMap& map, int d, int dtype, cudaStream_t st) {
+  PagedAttnArgs a = args;
+  a.rows_lo = 0;
+  a.rows_hi = INT_MAX;
+  const long long rows = (long long)a.r.n_rows * a.G, batch = a.r.batch;
+  const bool many = rows >= kTcMinRows * batch;
+  const bool both = a.r.start && batch > 1 && rows >= kBothMinRows && rows < kBothMaxRows * batch;
+  if (many || both) {
+    if (both) a.rows_lo = kTcMinRows;
+    const cudaError_t e = launch_paged_attention_tc(a, map, d, dtype, paged_attn_sms(), st);
+    if (e != cudaSuccess || !both) return e;
+    a.rows_lo = 0;
+    a.rows_hi = kTcMinRows;
+  }
   const bool half = dtype == FUTR_DTYPE_F16;
   if (d == 128) return half ? pa_launch<128, true>(a, map, st) : pa_launch<128, false>(a, map, st);
   return half ? pa_launch<64, true>(a, map, st) : pa_launch<64, false>(a, map, st);

@@ -65,6 +65,13 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
   return q;
 }
 
+// Sequence b of the call: no rows where they are another launch's.
+__device__ __forceinline__ bool my_seq(const PagedAttnArgs& a, int b, int& row0, int& n, int& p0) {
+  const bool ok = paged_seq(a.r, a.c, b, row0, n, p0);
+  if (n * a.G < a.rows_lo || n * a.G >= a.rows_hi) n = 0;
+  return ok;
+}
+
 // What a kernel makes of rows: R rows a row tile, whose start (queries, the join of
 // its parts) counts as much as `pad` tiles of positions.  The units of an item are
 // `pad` that hold nothing, then its tiles.
@@ -154,7 +161,7 @@ struct Walk {
         kvh = 0;
         do {
           ++b;
-          paged_seq(a.r, a.c, b, row0, n, p0);
+          my_seq(a, b, row0, n, p0);
         } while (n == 0);   // u < u1: a later sequence has rows
         per_head = seq_units(n, p0, a.G, s, a.window);
       }
@@ -174,7 +181,7 @@ __device__ __forceinline__ bool find_share(const PagedAttnArgs& a, Rows s, int c
     n = 0;
     per = 0;
     if (b0 + lane < a.r.batch) {
-      if (!paged_seq(a.r, a.c, b0 + lane, row0, n, p0) && report) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
+      if (!my_seq(a, b0 + lane, row0, n, p0) && report) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
       per = seq_units(n, p0, a.G, s, a.window);
     }
     incl = per * a.Hkv;

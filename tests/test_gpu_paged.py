@@ -452,3 +452,16 @@ def test_rows_behind_the_last_sequence_stay(counts):
     check_append(c, before, k[:n], v[:n], pos, counts)
     check_attention(c, q[:n], out[:n], pos, counts)
     assert bool((out[n:] == 7).all())
+
+
+@pytest.mark.parametrize("heads,hkv,d,dtype,window", [(32, 8, 128, torch.bfloat16, 0), (8, 2, 64, torch.float16, 150)])
+def test_chunks_among_single_tokens(heads, hkv, d, dtype, window):
+    """Batches whose sequences differ much: single tokens, drafts, chunks and idle ones in one call."""
+    counts = [1, 300, 1, 0, 5, 19, 20, 21, 1, 1, 90, 0] + [1] * 25
+    pos = [(i * 97) % 500 for i in range(len(counts))]
+    c = Paged(heads, hkv, d, 32, len(counts), 26)
+    c.fill(2)
+    q = rows(sum(counts), heads, d, dtype, 21)
+    got = run_attention(c, q, pos, counts, window)
+    check_attention(c, q, got, pos, counts, window)
+    assert torch.equal(run_attention(c, q, pos, counts, window), got)
