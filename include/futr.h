@@ -450,8 +450,9 @@ futr_status futr_paged_workspace_init(const futr_shape* shape, void* mem, size_t
  *   out = sum_j softmax_j(scale * q'.k_j) v_j      (scale 0: 1/sqrt(d))
  * The rotated query and the softmax weights enter the products as fp16 (the
  * query divided by a power of two near its largest element; of fp16 rows in two
- * parts, unless head_dim is 128 and the kernel for sequences of many rows, 80 or
- * more times the query heads of a kv-head, takes them); sums and softmax statistics are fp32.  A row that sees no position (missing pages) gets zeros.
+ * parts, unless head_dim is 128 and the kernel for sequences of many rows takes
+ * them, from 80 tokens x query heads of a kv-head on); sums and softmax statistics
+ * are fp32.  A row that sees no position (missing pages) gets zeros.
  * out may not overlap q.
  */
 futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t batch, const int32_t* pos,
@@ -517,8 +518,8 @@ futr_status futr_moe_workspace_init(const futr_moe_shape* shape, int32_t max_bat
  * be NULL).  The inputs of both products enter as fp16 (x divided by a power of
  * two near its RMS; w * silu * up by one near the largest of each 64); all sums
  * are fp32.  ids (int32) and weights (fp32) [batch][K], either may be NULL: the
- * choice of each token, largest first.  A token whose logits hold a NaN (or +inf) gets NaN
- * weights.  A blob of another shape sets FUTR_ERR_BAD_BLOB (see futr_moe_check).
+ * choice of each token, largest first.  A token whose logits hold a NaN (or +inf)
+ * gets NaN weights.  A blob of another shape sets FUTR_ERR_BAD_BLOB (see futr_moe_check).
  * Three kernels (four above 8 tokens) with programmatic dependent launch;
  * capturable in a CUDA graph.
  */
