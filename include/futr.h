@@ -399,12 +399,13 @@ typedef struct futr_paged {
   uint64_t magic;
 } futr_paged;
 
-/* Workspace of futr_paged_attention: arrival counters and split records. */
+/* Workspace of futr_paged_attention: arrival counters, error words and split
+ * records. */
 typedef struct futr_paged_ws {
   int32_t head_dim, ctas;
   void* base;
   uint64_t bytes;
-  uint64_t rec_offset;
+  uint64_t err_offset, rec_offset;
   uint64_t magic;
 } futr_paged_ws;
 
@@ -461,7 +462,10 @@ futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t
                                  float scale, int32_t window, const futr_paged_ws* ws, void* stream);
 
 /* Compare the guards of `cache` and `ws` (may be NULL), synchronize `stream` and
- * return (and clear) the cache's first device error. */
+ * return (and clear) the first device error of the cache, else of the workspace.
+ * A wait of futr_paged_attention that runs out marks its workspace, too: the other
+ * workspaces of the cache are not affected, and that one is out of use (its calls
+ * give up) until a check with it has returned the error and set it up anew. */
 futr_status futr_paged_check(const futr_paged* cache, const futr_paged_ws* ws, void* stream);
 
 /* ------------------------------------------------------ mixture of experts -- */

@@ -65,7 +65,8 @@ struct PagedAttnArgs {
   float scale_log2;         // softmax scale * log2(e)
   float* rec;               // split records
   unsigned* cnt;            // arrival counters, one per CTA
-  int* err;
+  int* err;                 // the cache's error word: rows and pages out of range
+  int* stop;                // the workspace's error and abort words: a wait ran out
 };
 
 int paged_attn_sms();                        // of the current device

@@ -70,6 +70,18 @@ void cache_guards(const futr_paged& c, uint64_t* g) {
 bool cache_ok(const futr_paged* c) { return c && c->magic == kPagedMagic && c->base; }
 bool ws_ok(const futr_paged_ws* w) { return w && w->magic == kPagedWsMagic && w->base; }
 
+struct WsLayout {
+  uint64_t err, rec, total;   // counters at 0
+};
+
+WsLayout ws_layout(int head_dim, int sms) {
+  WsLayout L;
+  L.err = host::region_after(0, (uint64_t)paged_attn_ctas(sms) * 4);
+  L.rec = host::region_after(L.err, 16);
+  L.total = host::region_after(L.rec, (uint64_t)paged_rec_floats(head_dim, sms) * 4);
+  return L;
+}
+
 PagedView view(const futr_paged& c, int layer) {
   PagedView v{};
   const uint64_t per_layer = (uint64_t)c.n_pages * c.shape.n_kv_heads;
@@ -170,8 +182,7 @@ futr_status futr_paged_workspace_size(const futr_shape* shape, size_t* bytes) {
     if (!host::shape_valid(shape)) return FUTR_ERR_UNSUPPORTED;
     const int sms = paged_attn_sms();
     if (sms <= 0) return FUTR_ERR_CUDA;
-    const uint64_t rec = host::region_after(0, (uint64_t)paged_attn_ctas(sms) * 4);
-    *bytes = (size_t)host::region_after(rec, (uint64_t)paged_rec_floats(shape->head_dim, sms) * 4);
+    *bytes = (size_t)ws_layout(shape->head_dim, sms).total;
     return FUTR_OK;
   });
 }
@@ -186,15 +197,19 @@ futr_status futr_paged_workspace_init(const futr_shape* shape, void* mem, size_t
     if (!aligned(mem, 256) || mem_bytes < need) return FUTR_ERR_INVALID_ARG;
     futr_paged_ws w{};
     w.head_dim = shape->head_dim;
-    w.ctas = paged_attn_ctas(paged_attn_sms());
+    const int sms = paged_attn_sms();
+    const WsLayout L = ws_layout(shape->head_dim, sms);
+    w.ctas = paged_attn_ctas(sms);
     w.base = mem;
     w.bytes = need;
-    w.rec_offset = host::region_after(0, (uint64_t)w.ctas * 4);
+    w.err_offset = L.err;
+    w.rec_offset = L.rec;
     w.magic = kPagedWsMagic;
     const cudaStream_t s = as_stream(stream);
+    // counters and error words start at zero
     if (cudaMemsetAsync(mem, 0, w.rec_offset, s) != cudaSuccess) return FUTR_ERR_CUDA;
-    const uint64_t g[2] = {w.rec_offset, w.bytes};
-    if (host::fill_guards_before(mem, g, 2, s) != cudaSuccess) return FUTR_ERR_CUDA;
+    const uint64_t g[3] = {w.err_offset, w.rec_offset, w.bytes};
+    if (host::fill_guards_before(mem, g, 3, s) != cudaSuccess) return FUTR_ERR_CUDA;
     *ws = w;
     return FUTR_OK;
   });
@@ -231,6 +246,7 @@ futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t
     a.rec = at<float>(ws->base, ws->rec_offset);
     a.cnt = at<unsigned>(ws->base, 0);
     a.err = at<int>(cache->base, cache->err_offset);
+    a.stop = at<int>(ws->base, ws->err_offset);
     CUtensorMap map;
     std::memcpy(&map, cache->copy_map, sizeof(map));
     return launch_paged_attention(a, map, s.head_dim, dtype, as_stream(stream)) == cudaSuccess ? FUTR_OK
@@ -246,19 +262,22 @@ futr_status futr_paged_check(const futr_paged* cache, const futr_paged_ws* ws, v
     uint64_t g[4];
     cache_guards(*cache, g);
     if (host::check_guards_before(cache->base, g, 4, err, s) != cudaSuccess) return FUTR_ERR_CUDA;
+    int* stop = ws ? at<int>(ws->base, ws->err_offset) : nullptr;
     if (ws) {
-      const uint64_t gw[2] = {ws->rec_offset, ws->bytes};
-      if (host::check_guards_before(ws->base, gw, 2, err, s) != cudaSuccess) return FUTR_ERR_CUDA;
+      const uint64_t gw[3] = {ws->err_offset, ws->rec_offset, ws->bytes};
+      if (host::check_guards_before(ws->base, gw, 3, stop, s) != cudaSuccess) return FUTR_ERR_CUDA;
     }
-    int v[2] = {0, 0};
-    if (cudaMemcpyAsync(v, err, sizeof(v), cudaMemcpyDeviceToHost, s) != cudaSuccess) return FUTR_ERR_CUDA;
+    int v = 0, w[2] = {0, 0};
+    if (cudaMemcpyAsync(&v, err, sizeof(v), cudaMemcpyDeviceToHost, s) != cudaSuccess) return FUTR_ERR_CUDA;
+    if (ws && cudaMemcpyAsync(w, stop, sizeof(w), cudaMemcpyDeviceToHost, s) != cudaSuccess) return FUTR_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return FUTR_ERR_CUDA;
-    if (v[0] == 0 && v[1] == 0) return FUTR_OK;
-    if (cudaMemsetAsync(err, 0, 16, s) != cudaSuccess) return FUTR_ERR_CUDA;
+    if (v == 0 && w[0] == 0 && w[1] == 0) return FUTR_OK;
+    if (v != 0 && cudaMemsetAsync(err, 0, 16, s) != cudaSuccess) return FUTR_ERR_CUDA;
+    if ((w[0] != 0 || w[1] != 0) && cudaMemsetAsync(stop, 0, 16, s) != cudaSuccess) return FUTR_ERR_CUDA;
     // a launch that gave up left its arrival counters mid-count
-    if (ws && v[1] != 0 && cudaMemsetAsync(ws->base, 0, (size_t)ws->ctas * 4, s) != cudaSuccess) return FUTR_ERR_CUDA;
+    if (w[1] != 0 && cudaMemsetAsync(ws->base, 0, (size_t)ws->ctas * 4, s) != cudaSuccess) return FUTR_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return FUTR_ERR_CUDA;
-    return v[0] != 0 ? v[0] : FUTR_ERR_TIMEOUT;
+    return v != 0 ? v : w[0] != 0 ? w[0] : FUTR_ERR_TIMEOUT;
   });
 }
 

@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     int issued = 0;
     const bool ok = produce_tiles<D>(a, &map, kPaWork, w, smem, s_scale, full, empty, kPaRing, issued);
     if (!ok) {
-      record_timeout(a.err);
+      pa_timeout(a);
       *s_dead = 1;
     }
     if (lane == 0) *s_issued = issued;
@@ -483,9 +483,9 @@ __global__ void __launch_bounds__(kPaThreads, 2)
         for (int e = 0; e < 2; ++e) aw.qs[nt][e] = s_qs[8 * nt + 2 * t + e];
       int pos0 = it.first * kPaTile + 32 * warp;
       for (int i = 0; i < count; ++i) {
-        if (ok && !pa_wait(&full[slot], phase, a.err)) {
+        if (ok && !pa_wait(&full[slot], phase, a)) {
           ok = false;
-          record_timeout(a.err);
+          pa_timeout(a);
           *s_dead = 1;
         }
         if (ok && pos0 <= it.hi_max && pos0 + 31 >= it.lo_min) {

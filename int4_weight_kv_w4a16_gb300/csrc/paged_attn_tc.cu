@@ -440,9 +440,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {   // in dead mode: nothing to wait for
-    if (ok && !pa_wait(bar, parity, a.err)) {
+    if (ok && !pa_wait(bar, parity, a)) {
       ok = false;
-      record_timeout(a.err);
+      pa_timeout(a);
       *s_dead = 1;
     }
     return ok;
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (active) {
       int issued = 0;
       if (!produce_tiles<D>(a, &map, kTcWork, w, smem + Lay::kStage, s_raw, full, empty, kTcRing, issued)) {
-        record_timeout(a.err);
+        pa_timeout(a);
         *s_dead = 1;
       }
       if (lane == 0) *s_issued = issued;
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnArgs a, 
   pdl_trigger();
   pdl_wait();
   const TcJoin join = reinterpret_cast<const TcJoin*>(a.rec + (size_t)ctas * 2 * kRec)[cta];
-  if (join.others == 0 || r >= join.valid || a.err[1] != 0) return;   // (after a time-out parts may be missing)
+  if (join.others == 0 || r >= join.valid || a.stop[1] != 0) return;   // (after a time-out parts may be missing)
   const float* r0 = a.rec + ((size_t)cta * 2 + 1) * kRec + r;         // its CTA's second slot
   const float* rn = a.rec + (size_t)(cta + 1) * 2 * kRec + r;         // the others' first
   const int nc = join.others;

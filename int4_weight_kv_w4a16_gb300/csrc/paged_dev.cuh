@@ -12,10 +12,17 @@ constexpr int kPaTile = 128;                    // positions of a tile: 32 a war
 constexpr int kPaSub = kPaTile / 16;            // 16-position sub-tiles: what one page is a multiple of
 constexpr unsigned long long kPaWaitNs = 1000000000ull;
 
-__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, const int* err) {
+__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, const PagedAttnArgs& a) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long dl = global_ns() + kPaWaitNs;
-  return mbar_wait_until(bar, parity, dl, err);
+  return mbar_wait_until(bar, parity, dl, a.stop);
+}
+
+// A wait ran out: the workspace is out of use until a check with it; the cache
+// reports it, too, for a check without.
+__device__ __forceinline__ void pa_timeout(const PagedAttnArgs& a) {
+  record_timeout(a.stop);
+  set_err(a.err, FUTR_ERR_TIMEOUT);
 }
 
 __device__ __forceinline__ float pa_ex2(float x) {
@@ -270,7 +277,7 @@ __device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUte
         sc = sc_next;
         if (base + 32 <= pg1) fetch(base + 32 + lane, id_next, sc_next);
       }
-      if (issued >= ring && !pa_wait(&empty[slot], phase ^ 1u, a.err)) {
+      if (issued >= ring && !pa_wait(&empty[slot], phase ^ 1u, a)) {
         ok = false;
         break;
       }

@@ -65,7 +65,7 @@ class futr_paged(C.Structure):
 
 class futr_paged_ws(C.Structure):
     _fields_ = [("head_dim", C.c_int32), ("ctas", C.c_int32), ("base", C.c_void_p), ("bytes", C.c_uint64),
-                ("rec_offset", C.c_uint64), ("magic", C.c_uint64)]
+                ("err_offset", C.c_uint64), ("rec_offset", C.c_uint64), ("magic", C.c_uint64)]
 
 
 class futr_moe_shape(C.Structure):

@@ -465,3 +465,27 @@ def test_chunks_among_single_tokens(heads, hkv, d, dtype, window):
     got = run_attention(c, q, pos, counts, window)
     check_attention(c, q, got, pos, counts, window)
     assert torch.equal(run_attention(c, q, pos, counts, window), got)
+
+
+@pytest.mark.parametrize("n", [1, 90], ids=["few", "many"])
+def test_a_timeout_stays_with_its_workspace(n):
+    """What a call that gave up leaves in its workspace (error and abort words, counters mid-count)
+    reaches no other workspace of the cache, and stays until a check with that workspace."""
+    c = Paged(8, 2, 128, 32, 2, 100)
+    c.fill(6)
+    pos, counts = [3000, 2000], [n, n]
+    q = rows(2 * n, 8, 128, torch.bfloat16, 31)
+    good = run_attention(c, q, pos, counts)
+    mine = c.ws
+    other = futr.futr_paged_workspace_init(c.cs, futr.alloc_bytes(futr.futr_paged_workspace_size(c.cs)))
+    words = mine._mem[mine.err_offset:mine.err_offset + 8].view(torch.int32)
+    words[0], words[1] = futr.FUTR_ERR_TIMEOUT, 1
+    mine._mem[:4 * mine.ctas].view(torch.int32).fill_(1)
+    c.ws = other
+    assert torch.equal(run_attention(c, q, pos, counts), good)
+    assert futr.futr_paged_check(c.cache) == futr.FUTR_OK
+    assert words.tolist() == [futr.FUTR_ERR_TIMEOUT, 1]
+    c.ws = mine
+    assert futr.futr_paged_check(c.cache, mine) == futr.FUTR_ERR_TIMEOUT
+    assert futr.futr_paged_check(c.cache, mine) == futr.FUTR_OK
+    assert torch.equal(run_attention(c, q, pos, counts), good)
