@@ -523,7 +523,8 @@ futr_status futr_moe_workspace_init(const futr_moe_shape* shape, int32_t max_bat
  * two near its RMS; w * silu * up by one near the largest of each 64); all sums
  * are fp32.  ids (int32) and weights (fp32) [batch][K], either may be NULL: the
  * choice of each token, largest first.  A token whose logits hold a NaN (or +inf)
- * gets NaN weights.  A blob of another shape sets FUTR_ERR_BAD_BLOB (see futr_moe_check).
+ * gets NaN weights.  A blob whose header names another shape sets FUTR_ERR_BAD_BLOB
+ * (see futr_moe_check): nothing behind the header is read, and y stays as it was.
  * Three kernels (four above 8 tokens) with programmatic dependent launch;
  * capturable in a CUDA graph.
  */

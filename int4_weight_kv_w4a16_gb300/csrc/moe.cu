@@ -82,6 +82,13 @@ __device__ __forceinline__ float pow2_at(float v) {
 }
 __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
+// Whether the blob holds this layer's experts.  Where it does not, nothing behind its
+// header is read: its units may end before the layer's would.
+__device__ __forceinline__ bool own_blob(const MoeArgs& a) {
+  const MoeHeader* h = reinterpret_cast<const MoeHeader*>(a.blob);
+  return (h->magic == kMoeMagic) & (h->hidden == a.H) & (h->inter == a.I) & (h->n_experts == a.E);   // loads side by side
+}
+
 // ------------------------------------------------------------------ router --
 
 // Floats in ascending order as unsigned integers in ascending order above 0 (NaN: below -inf).
@@ -160,11 +167,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
   pdl_trigger();
   pdl_wait();
   const int et = blockIdx.x, t0 = blockIdx.y * kRouterT, nt = min(kRouterT, a.T - t0);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
-    const MoeHeader* h = reinterpret_cast<const MoeHeader*>(a.blob);
-    if (h->magic != kMoeMagic || h->hidden != a.H || h->inter != a.I || h->n_experts != a.E)
-      set_err(a.err, FUTR_ERR_BAD_BLOB);
-  }
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && !own_blob(a)) set_err(a.err, FUTR_ERR_BAD_BLOB);
   // warp = (expert, slice): every kRouterSlices-th chunk of 256 inputs
   {
     const int el = warp / kRouterSlices, sl = warp % kRouterSlices, e = et * kRouterE + el;
@@ -646,6 +649,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
   } else {
     pdl_trigger();
   }
+  const bool own = own_blob(a);   // the same for all CTAs; looked at below, when the choices are there, too
   __shared__ MoeRoute s_route;
   make_route<8 * NT>(a, s_route);
   const MoeRoute* rt = &s_route;
@@ -654,6 +658,10 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
   const MoeCut cut(total, run.item_len, (int)gridDim.x, run.least());
   const int cta = blockIdx.x;
   if (cta >= cut.use) return;
+  if (!own) {
+    if (kDown) pdl_wait();   // down's end is the call's
+    return;
+  }
   const int u0 = cut.begin(cta), u1 = cut.begin(cta + 1);
 
   if (warp == kMoeCW) {
@@ -827,6 +835,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
 __global__ void __launch_bounds__(256) moe_sum_kernel(const MoeArgs a) {
   pdl_trigger();
   pdl_wait();
+  if (!own_blob(a)) return;
   const MoeRun<true> run(a, *a.active);
   const MoeCut cut(run.total(), run.item_len, a.down_ctas, run.least());
   const int rb = blockIdx.x, t = 8 * blockIdx.y + (threadIdx.x >> 5), q = threadIdx.x & 31;

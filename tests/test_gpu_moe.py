@@ -220,3 +220,20 @@ def test_graph_replay_with_other_tokens():
         assert futr.futr_moe_check(m.ws) == futr.FUTR_OK
         ry, _, bound = m.reference(x, ids, res)
         assert bool(((y.to(F64) - ry).abs() <= 2.0 ** -8 * ry.abs() + bound + 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("T", [1, 9, 32])
+@pytest.mark.parametrize("word,value", [(0, 0), (3, 128), (4, 128), (5, 3)], ids=["magic", "hidden", "inter", "experts"])
+def test_foreign_blob_is_not_read(word, value, T):
+    """A header of another layer: the status, and an output that stays as it was."""
+    m = Moe(256, 256, 4, 2, seed=9)
+    x = rows(m, T)
+    header = m.blob[:24].view(torch.int32)
+    keep = header.clone()
+    header[word] = value
+    y = torch.full_like(x, 7.0)
+    futr.futr_moe_layer(x, m.gain, m.router, m.blob, None, y, m.ws)
+    assert futr.futr_moe_check(m.ws) == futr.FUTR_ERR_BAD_BLOB
+    assert bool((y == 7).all())
+    header.copy_(keep)
+    m.check(x)
