@@ -362,7 +362,8 @@ futr_status futr_check(const futr_ws* ws, const futr_kv* kv, void* stream);
  *   codes  [n_layers][n_pages][Hkv][2: keys, values][page][d]  e4m3, one byte each
  *   scales [n_layers][n_pages][Hkv][2]                          fp32
  *   the RoPE cos/sin table [max_pos][d/2] and the error word.
- * A value is code * scale.  Scales written here are powers of two.  Which page
+ * A value is code * scale.  Scales written here are powers of two; a program that
+ * fills pages itself may use any from 2^-90 to 2^120.  Which page
  * holds positions page*i .. page*i + page - 1 of sequence b is entry [b][i] of
  * the caller's page table (device int32 [batch][table_ld]); entries past a
  * sequence's last page, and those of pages before every row's window, are not
@@ -427,7 +428,8 @@ futr_status futr_paged_init(const futr_shape* shape, int32_t n_layers, int32_t n
  * new rows' largest magnitude is at most 448 * 2^e, and e >= -60; codes are
  * e4m3(x / s), rounded to nearest even.  When s > s_old the page's other codes
  * c become e4m3(c * s_old / s).  A call that writes slot 0 of a page starts the
- * page over (s_old = 0): what its other slots held is void.  An infinity or NaN
+ * page over (s_old = 0): what its other slots held is void.  (Quotients are fp32;
+ * of a power of two they are exact.)  An infinity or NaN
  * (after the rotation) is stored as 0 and sets FUTR_ERR_NOT_FINITE.
  */
 futr_status futr_paged_append(const futr_paged* cache, int32_t layer, int32_t batch, const int32_t* pos,

@@ -210,7 +210,16 @@ __global__ void __launch_bounds__(kAppMaxThreads) paged_append_kernel(const Appe
   __syncthreads();   // every thread has read the old scale by now, too
   for (int w = 0; w < threads / 32; ++w) m = fmaxf(m, s_max[w]);
   const float s_new = fmaxf(s_old, pow2(scale_exp(m)));
-  const float inv = __uint_as_float((254u << 23) - __float_as_uint(s_new));   // of a power of two: exact
+  // of a power of two as the append makes them, up to 2^120, exact
+  float inv = __uint_as_float((254u << 23) - __float_as_uint(s_new));
+  if ((__float_as_uint(s_new) & 0x7FFFFFu) != 0u || s_new > 0x1p120f) {
+    // an old scale that is a program's own: the rows are divided by it
+#pragma unroll
+    for (int i = 0; i < kAppRounds; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = __fdiv_rn(x[i][j], s_new);
+    inv = 1.f;
+  }
   if (tid == 0 && s_new != s_old) *scale = s_new;
   if (s_old > 0.f && s_new > s_old) {
     // the page's other slots at the new scale, 8 codes a thread

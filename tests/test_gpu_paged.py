@@ -489,3 +489,35 @@ def test_a_timeout_stays_with_its_workspace(n):
     assert futr.futr_paged_check(c.cache, mine) == futr.FUTR_ERR_TIMEOUT
     assert futr.futr_paged_check(c.cache, mine) == futr.FUTR_OK
     assert torch.equal(run_attention(c, q, pos, counts), good)
+
+
+@pytest.mark.parametrize("gain", [2.0 ** -5, 64.0], ids=["kept", "grown"])
+@pytest.mark.parametrize("n", [1, 9])
+def test_append_onto_scales_between_powers_of_two(n, gain):
+    """A page whose scale a program wrote by its own rule: new codes are e4m3(x / s), x / s in fp32, and
+    where s grows old ones e4m3(c * (s_old / s))."""
+    c = Paged(4, 2, 128, 16, 3, 2, rope=False)
+    c.fill(6, gain=1.0)
+    factor = torch.tensor([1.0, 1.5, 1.3, 1.9990234375], device="cuda")
+    c.scales[0] *= factor[torch.arange(c.scales[0].numel(), device="cuda") % 4].view_as(c.scales[0])
+    old_codes, old_scales = c.codes[0].clone(), c.scales[0].clone()
+    pos = [3, 5, 6]
+    k, v = (rows(3 * n, 2, 128, torch.bfloat16, s) * gain for s in (4, 5))
+    futr.futr_paged_append(c.cache, 0, 3, ints(pos), starts([n] * 3), c.table, k, v)
+    assert futr.futr_paged_check(c.cache) == futr.FUTR_OK
+    grown = 0
+    for b in range(3):
+        page = int(c.table[b, 0])
+        for h in range(2):
+            for w, t in enumerate((k, v)):
+                x = t[b * n:(b + 1) * n, h].float()
+                s_old = old_scales[page, h, w]
+                s = torch.clamp(s_old, min=page_scale(float(x.abs().max())))
+                assert torch.equal(c.scales[0, page, h, w], s), (b, h, w)
+                want = old_codes[page, h, w].clone()
+                if s > s_old:
+                    grown += 1
+                    want = (want.float() * (s_old / s)).to(torch.float8_e4m3fn)
+                want[pos[b]:pos[b] + n] = (x / s).to(torch.float8_e4m3fn)
+                assert torch.equal(c.codes[0, page, h, w].view(torch.uint8), want.view(torch.uint8)), (b, h, w)
+    assert grown == (0 if gain < 1 else 12)
