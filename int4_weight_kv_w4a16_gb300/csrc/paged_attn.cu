@@ -18,9 +18,11 @@
 // take 32 positions of each tile:
 //   S^T = K q'^T: mma.m16n8k16 f16, A = 16 positions of key codes converted in
 //     registers (exact: e4m3 is a subset of f16), B = the rows as columns;
-//   w = 2^(x + log2(value scale) - M), M the running maximum of that exponent:
-//     the value scale rides in the exponent, so w <= 1 is a safe f16 whatever
-//     the scales are, and the normalizer adds w / value scale in fp32;
+//   w = 2^(x + log2(value scale) - M + 14), M the running maximum of that exponent:
+//     the value scale rides in the exponent, so w <= 2^14 is a safe f16 whatever
+//     the scales are, and the normalizer adds w / value scale in fp32 (2^14 is in
+//     both and cancels; with w <= 1 a weight below 2^-24 of the largest became 0 or
+//     2^-24 in the products but not in the normalizer);
 //   O^T += V^T w: A = value codes, converted the same way; the score fragment
 //     becomes the B operand by an 8x8 register transpose.
 // The query enters as f16, each row divided by a power of two near its largest
@@ -28,7 +30,8 @@
 // rows resolve; f16 rows, which resolve more, in two parts (22 bits; an output's
 // error is then its own rounding, 2.0e-4, instead of 4.3e-4).  The second MMAs cost
 // drafted tokens nothing (13.1 us), 32 ragged sequences of D = 128 39.0 us instead of
-// 36.7.  The weights enter as f16: 11 bits, next to the 4 of the values they multiply.
+// 36.7.  The weights enter as f16: 11 bits down to 2^-28 of the largest, next to the 4 of
+// the values they multiply.
 // All sums are fp32.
 //
 // Bound by memory while a sequence has one row tile (the codes are read once, 2 d
@@ -51,6 +54,7 @@ constexpr int kPaThreads = (kPaCW + 1) * 32;
 // two then lacks: 8 sequences of 16 rows over 4000 positions take 50 us with two and
 // 25 us with one (D = 128), 20 and 18 us (D = 64).
 constexpr int NT = 1;
+constexpr float kTopWeight = 14.f;   // log2 of the largest weight
 constexpr int kPaRows = 8 * NT;
 // An item's start and join count as three tiles in the cut.  With 0, 2, 3, 4 and 6: 32
 // ragged sequences 36.6, 33.0, 33.1, 33.5, 35.1 us; four long ones 53.9, 52.4, 51.3, 51.1,
@@ -196,8 +200,9 @@ struct PaWarp {
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
         const float mn = fmaxf(m[nt][e], mx);
-        const float ref = mn == -INFINITY ? 0.f : mn;   // nothing visible yet: 2^(-inf - 0) = 0
-        corr[nt][e] = pa_ex2(m[nt][e] - ref);
+        // (nothing visible yet: 2^(-inf - 0) = 0)
+        corr[nt][e] = pa_ex2(m[nt][e] - (mn == -INFINITY ? 0.f : mn));
+        const float ref = mn == -INFINITY ? 0.f : mn - kTopWeight;
         moved |= m[nt][e] != mn;
         m[nt][e] = mn;
         float sum = l[nt][e] * corr[nt][e];

@@ -25,8 +25,10 @@
 // instead of 2e-4).
 //
 // The running reference M of a row follows its maximum only when that has grown
-// by more than 2^8: a weight up to 2^8 is a good f16, the normalizer is fp32, and
-// O, in tensor memory, is rescaled a few times an item instead of every tile.
+// by more than 2^4: weights, 2^11 at the reference, stay below f16's 2^16, the
+// normalizer is fp32, and O, in tensor memory, is rescaled a few times an item instead
+// of every tile.  A weight has 11 bits down to 2^-25 of the largest, and is nothing
+// below 2^-36 of it.
 //
 // Bound by the tensor cores in principle (4 x 256 x 128 x D flops a tile take 2048
 // cycles at D = 128).  Measured on four prompts' chunks of 512 rows after contexts to
@@ -52,6 +54,7 @@ constexpr int kTcThreads = 14 * 32;
 constexpr int kTcSoft = 8 * 32;                 // softmax threads
 constexpr int kTcRing = 2;
 constexpr float kTiny = 1.17549435e-38f;
+constexpr float kRefWeight = 11.f, kRefLag = 4.f;   // log2 of the weight at a row's reference, and of what the maximum may exceed it by
 
 // f16 parts of a query element: two for f16 rows where shared memory has the room (four
 // chunks of 256 rows after 4000 positions, D = 64: an error of 2.4e-4 in 61.7 us, with
@@ -636,8 +639,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int top = p - pos0, low = top - back;   // columns low .. top are visible
             const bool cut = __any_sync(0xffffffffu, top < kPaTile - 1 || low > 0);
             const float mx = cut ? tc_row_max<true>(ts, sc, qf, low, top) : tc_row_max<false>(ts, sc, qf, low, top);
-            // the reference moves when the maximum has outgrown it by 2^8 (or it has none yet)
-            const bool grow = mx > M + 8.f || (M == -INFINITY && mx > M);
+            // the reference moves when the maximum has outgrown it (or it has none yet)
+            const bool grow = mx > M + kRefLag || (M == -INFINITY && mx > M);
             if (__any_sync(0xffffffffu, grow)) {
               const float now = grow ? mx : M;
               const float corr = M == now ? 1.f : pa_ex2(M - now);
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
               }
             }
-            const float ref = M == -INFINITY ? 0.f : M;
+            const float ref = M == -INFINITY ? 0.f : M - kRefWeight;
             L += cut ? tc_row_weights<true>(ts, sc, qf, ref, low, top) : tc_row_weights<false>(ts, sc, qf, ref, low, top);
             tc_wait_st();
             tc_fence_before();

@@ -521,3 +521,28 @@ def test_append_onto_scales_between_powers_of_two(n, gain):
                 want[pos[b]:pos[b] + n] = (x / s).to(torch.float8_e4m3fn)
                 assert torch.equal(c.codes[0, page, h, w].view(torch.uint8), want.view(torch.uint8)), (b, h, w)
     assert grown == (0 if gain < 1 else 12)
+
+
+@pytest.mark.parametrize("nats", [17.0, 17.5, 18.0])
+@pytest.mark.parametrize("n,batch", [(1, 304), (32, 160)], ids=["few", "many"])
+def test_faint_keys_behind_one_that_carries_nothing(n, batch, nats):
+    """One key takes nearly all of the weight and has the value 0: the output is what 2^11 others carry, of
+    2^-24.5, 2^-25.2 or 2^-26 of its weight each, below fp16's smallest number next to 1.  As many sequences
+    as there are CTAs, so that one has a sequence to itself."""
+    N = 1 << 11
+    c = Paged(4, 1, 64, 128, 1, N // 128, rope=False)
+    c.codes[0, :, :, 0] = torch.tensor(-1.0, device="cuda").to(torch.float8_e4m3fn)
+    c.codes[0, :, :, 1] = torch.tensor(1.0, device="cuda").to(torch.float8_e4m3fn)
+    c.scales.fill_(1.0)
+    first = int(c.table[0, 0])
+    c.codes[0, first, :, 0, 5] = torch.tensor(1.0, device="cuda").to(torch.float8_e4m3fn)
+    c.codes[0, first, :, 1, 5] = torch.tensor(0.0, device="cuda").to(torch.float8_e4m3fn)
+    c.table = c.table.expand(batch, -1).contiguous()     # all read the same pages
+    q = torch.full((n * batch, 4, 64), nats / 16, device="cuda").to(torch.bfloat16)    # q.k / 8 = +- nats / 2
+    assert float(q[0, 0, 0]) * 16 == nats
+    got = run_attention(c, q, [N - n] * batch, [n] * batch).to(F64)
+    others = torch.arange(N - n, N, dtype=F64, device="cuda").repeat(batch)[:, None, None] * math.exp(-nats)
+    want = (others / (1 + others)).expand_as(got)
+    # the query, the keys and the values are exact: the output's half step, a weight's in fp16 (2^-25 at the
+    # most where the largest is 2^11, 2^-10 of these), and fp32 sums of 2^11 terms, 2^-24 each
+    assert float((got / want - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -12
