@@ -320,7 +320,7 @@ __device__ __forceinline__ void load_queries(const PagedAttnArgs& a, const Walk&
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       // exponent of the largest element, kept where 2^e and 2^-e are normal
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
       const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
       for (int j = 0; j < J; ++j) x[j] *= inv;

@@ -242,7 +242,7 @@ __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Wa
       }
       // the largest magnitude: magnitudes order like their bits
       mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);   // (2^-e is normal, too)
       const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

@@ -546,3 +546,22 @@ def test_faint_keys_behind_one_that_carries_nothing(n, batch, nats):
     # the query, the keys and the values are exact: the output's half step, a weight's in fp16 (2^-25 at the
     # most where the largest is 2^11, 2^-10 of these), and fp32 sums of 2^11 terms, 2^-24 each
     assert float((got / want - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -12
+
+
+@pytest.mark.parametrize("power", [118, -118])
+@pytest.mark.parametrize("n,rope", [(1, False), (1, True), (40, False), (40, True)])
+def test_queries_of_any_size(n, rope, power):
+    """Queries near either end of bf16's range, with a scale that brings the scores back.  Without a
+    rotation (whose small products may be subnormal) a power of two changes no bit."""
+    c = Paged(8, 2, 128, 32, 1, 8, rope=rope)
+    c.fill(3)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = (1 + torch.rand((n, 8, 128), generator=g, device="cuda")).to(torch.bfloat16)
+    q = torch.where(torch.rand(q.shape, generator=g, device="cuda") < 0.5, -q, q)
+    scale = 2.0 ** -5
+    want = run_attention(c, q, [100], [n], scale=scale)
+    check_attention(c, q, want, [100], [n], scale=scale)
+    q, scale = q * 2.0 ** power, scale * 2.0 ** -power
+    got = run_attention(c, q, [100], [n], scale=scale)
+    check_attention(c, q, got, [100], [n], scale=scale)
+    assert rope or torch.equal(got, want)
