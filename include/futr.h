@@ -452,10 +452,8 @@ futr_status futr_paged_workspace_init(const futr_shape* shape, void* mem, size_t
  * .. p (window 0: 0 .. p); query head h reads kv-head h / (Hq/Hkv).
  *   out = sum_j softmax_j(scale * q'.k_j) v_j      (scale 0: 1/sqrt(d))
  * The rotated query and the softmax weights enter the products as fp16 (the
- * query divided by a power of two near its largest element; of fp16 rows in two
- * parts, unless head_dim is 128 and the kernel for sequences of many rows takes
- * them, from 80 tokens x query heads of a kv-head on); sums and softmax statistics
- * are fp32.  A row that sees no position (missing pages) gets zeros.
+ * query divided by a power of two near its largest element, of fp16 rows in two
+ * parts); sums and softmax statistics are fp32.  A row that sees no position (missing pages) gets zeros.
  * out may not overlap q.
  */
 futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t batch, const int32_t* pos,

@@ -20,9 +20,9 @@
 //                over the scores it has read, where they are P V's A operand.
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (D columns each).
 //
-// The query of f16 rows has two f16 parts only at D = 64: at D = 128 a second does not
-// fit into shared memory beside two value buffers (an output's error is then 4e-4
-// instead of 2e-4).
+// The query of f16 rows has two f16 parts, as in paged_attn.cu.  At D = 128 the second
+// takes the shared memory of a value buffer and of a stage of the ring, so that the
+// next tile's copy and values wait for this one's products.
 //
 // The running reference M of a row follows its maximum only when that has grown
 // by more than 2^4: weights, 2^11 at the reference, stay below f16's 2^16, the
@@ -52,26 +52,29 @@ constexpr int kTcRows = 256, kTcHalf = 128;
 constexpr Rows kTcWork{kTcRows, 4};
 constexpr int kTcThreads = 14 * 32;
 constexpr int kTcSoft = 8 * 32;                 // softmax threads
-constexpr int kTcRing = 2;
 constexpr float kTiny = 1.17549435e-38f;
 constexpr float kRefWeight = 11.f, kRefLag = 4.f;   // log2 of the weight at a row's reference, and of what the maximum may exceed it by
 
-// f16 parts of a query element: two for f16 rows where shared memory has the room (four
-// chunks of 256 rows after 4000 positions, D = 64: an error of 2.4e-4 in 61.7 us, with
-// one part 5.3e-4 in 58.3).
-template <int D, bool kHalf>
-constexpr int kTcParts = kHalf && D == 64 ? 2 : 1;
+// f16 parts of a query element: two for f16 rows, as few rows have them, so that a
+// row's error does not depend on the kernel its batch takes.  The chunks of the head
+// comment with f16 rows: an error of 2.1e-4 in 104 us, with one part 4.3e-4 in 84 (the
+// products of the scores lie between a half's softmaxes).
+template <bool kHalf>
+constexpr int kTcParts = kHalf ? 2 : 1;
 
 template <int D, bool kHalf>
 struct TcLayout {
-  static constexpr int kParts = kTcParts<D, kHalf>;
+  static constexpr int kParts = kTcParts<kHalf>;
+  static constexpr bool kTight = D == 128 && kParts == 2;        // 227 KB hold one of each
+  static constexpr int kValues = kTight ? 1 : 2;                 // value buffers
+  static constexpr int kRing = kTight ? 1 : 2;                   // stages of 8-bit tiles
   static constexpr int kOp = kTcHalf * D * 2;                    // one f16 operand of 128 rows
   static constexpr int kQ = 0;                                   // [half][part]
   static constexpr int kK = kQ + 2 * kParts * kOp;
   static constexpr int kV = kK + kOp;
-  static constexpr int kStage = kV + 2 * kOp;                    // two of the values; ring of 8-bit tiles
-  static constexpr int kRaw = kStage + kTcRing * 2 * kPaTile * D;   // [ring][sub-tiles] float4
-  static constexpr int kScale = kRaw + kTcRing * kPaSub * 16;    // [2][sub-tiles] float4, by tile parity
+  static constexpr int kStage = kV + kValues * kOp;              // ring of 8-bit tiles
+  static constexpr int kRaw = kStage + kRing * 2 * kPaTile * D;  // [ring][sub-tiles] float4
+  static constexpr int kScale = kRaw + kRing * kPaSub * 16;      // [2][sub-tiles] float4, by tile parity
   static constexpr int kQs = kScale + 2 * kPaSub * 16;           // [256] score factors
   static constexpr int kBar = kQs + kTcRows * 4;
   static constexpr int kBytes = kBar + 24 * 8 + 64;
@@ -247,13 +250,17 @@ __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Wa
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint8_t* dst = q16 + tc_at(r0 + k, at + h * (D / 2));
-        if (P == 2)
-          *reinterpret_cast<uint32_t*>(dst) = pack_half2(x[h][0] * inv, x[h][P - 1] * inv);
-        else
-          *reinterpret_cast<__half*>(dst) = __float2half_rn(x[h][0] * inv);
-        if (kTcParts<D, kHalf> == 2) {
-          const float v = x[h][0] * inv;
-          *reinterpret_cast<__half*>(dst + kTcHalf * D * 2) = __float2half_rn(v - __half2float(__float2half_rn(v)));
+        float v[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) v[j] = x[h][j] * inv;
+#pragma unroll
+        for (int part = 0; part < kTcParts<kHalf>; ++part) {
+          if (P == 2)
+            *reinterpret_cast<uint32_t*>(dst + part * (kTcHalf * D * 2)) = pack_half2(v[0], v[P - 1]);
+          else
+            *reinterpret_cast<__half*>(dst + part * (kTcHalf * D * 2)) = __float2half_rn(v[0]);
+#pragma unroll
+          for (int j = 0; j < P; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
         }
       }
       if (lane == 0)
@@ -378,9 +385,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   float4* s_raw = reinterpret_cast<float4*>(smem + Lay::kRaw);
   float4* s_scale = reinterpret_cast<float4*>(smem + Lay::kScale);
   float* s_qs = reinterpret_cast<float*>(smem + Lay::kQs);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::kBar);   // [2] a tile's codes have landed
-  uint64_t* empty = full + kTcRing;      // [2] they are widened
-  uint64_t* qready = empty + kTcRing;    // [2] the queries of a half are in place
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::kBar);   // [ring] a tile's codes have landed
+  uint64_t* empty = full + 2;            // [ring] they are widened
+  uint64_t* qready = empty + 2;          // [2] the queries of a half are in place
   uint64_t* kready = qready + 2;         // keys widened
   uint64_t* kfree = kready + 1;          // both halves' scores are done
   uint64_t* vready = kfree + 1;          // [2] values widened, by the tile's parity
@@ -395,7 +402,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ TcItem s_item;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < kTcRing; ++i) {
+    for (int i = 0; i < Lay::kRing; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 4);
     }
@@ -451,11 +458,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return ok;
   };
 
+  auto vbuf = [](uint32_t t) { return Lay::kValues == 2 ? t & 1u : 0u; };   // tile t's value buffer
+
   if (warp == 12) {
     // ---------------------------------------------------------- producer --
     if (active) {
       int issued = 0;
-      if (!produce_tiles<D>(a, &map, kTcWork, w, smem + Lay::kStage, s_raw, full, empty, kTcRing, issued)) {
+      if (!produce_tiles<D>(a, &map, kTcWork, w, smem + Lay::kStage, s_raw, full, empty, Lay::kRing, issued)) {
         pa_timeout(a);
         *s_dead = 1;
       }
@@ -482,8 +491,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       auto values = [&](int h, bool first) {
 #pragma unroll
         for (int ks = 0; ks < kPaTile / 16; ++ks)
-          tc_mma_ts(tm + 256 + D * h, tm + 128 * h + 8 * ks, v16 + (t & 1) * (Lay::kOp >> 4) + ks * (2048 >> 4), kIdescO<D>,
-                    !first || ks > 0);
+          tc_mma_ts(tm + 256 + D * h, tm + 128 * h + 8 * ks, v16 + vbuf(t) * (Lay::kOp >> 4) + ks * (2048 >> 4),
+                    kIdescO<D>, !first || ks > 0);
         tc_commit(&odone[h]);
         ++done[h];
       };
@@ -545,8 +554,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);
         const int nh = min(kTcRows, w.n * a.G - w.rt * kTcRows) > kTcHalf ? 2 : 1;
         for (int i = 0; i < count; ++i, ++t) {
-          const int slot = t % kTcRing;
-          wait(&full[slot], (t / kTcRing) & 1u);
+          const int slot = t % Lay::kRing;
+          wait(&full[slot], (t / Lay::kRing) & 1u);
           const uint8_t* st = smem + Lay::kStage + slot * (2 * kPaTile * D);
           const float4 raw = s_raw[slot * kPaSub + (lane & (kPaSub - 1))];
           // what was never written, or lies on a missing page, becomes zeros
@@ -555,10 +564,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool plain = left >= kPaTile && gone == 0u;
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
-            // the operand buffer is free once the MMAs of the tile before (values: of
-            // the one before that) have read it
-            if (kv ? t > 1 : t > 0) wait(kv ? &vfree[t & 1] : kfree, kv ? ((t >> 1) - 1) & 1u : (t - 1) & 1u);
-            uint8_t* dst = smem + (kv ? Lay::kV + (t & 1) * Lay::kOp : Lay::kK);
+            // the operand buffer is free once the MMAs of the tile before (values in two
+            // buffers: of the one before that) have read it
+            const uint32_t prev = t - (kv ? Lay::kValues : 1);
+            if (t >= (kv ? Lay::kValues : 1)) wait(kv ? &vfree[prev & 1] : kfree, kv ? (prev >> 1) & 1u : prev & 1u);
+            uint8_t* dst = smem + (kv ? Lay::kV + vbuf(t) * Lay::kOp : Lay::kK);
             const uint8_t* from = st + kv * page * D;
             if (ok) {
 #pragma unroll 2
@@ -731,7 +741,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   // every MMA has been waited for (odone), or, after a time-out, gets its time here
   __syncthreads();
-  if (*s_dead && tid == 0) drain_ring(full, kTcRing, *s_issued);
+  if (*s_dead && tid == 0) drain_ring(full, Lay::kRing, *s_issued);
   if (*s_dead && tid == 32) {
     const unsigned long long dl = global_ns() + 1000000ull;   // 1 ms: far longer than what is in flight takes
     while (global_ns() < dl) {

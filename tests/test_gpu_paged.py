@@ -565,3 +565,20 @@ def test_queries_of_any_size(n, rope, power):
     got = run_attention(c, q, [100], [n], scale=scale)
     check_attention(c, q, got, [100], [n], scale=scale)
     assert rope or torch.equal(got, want)
+
+
+@pytest.mark.parametrize("heads,kv_heads,d,counts", [
+    (8, 2, 64, [1] * 40), (8, 2, 128, [1] * 40), (8, 2, 64, [100, 70]), (8, 2, 128, [100, 70]), (8, 8, 128, [300]),
+], ids=["tokens64", "tokens128", "chunks64", "chunks128", "prompt128"])
+def test_fp16_rows_keep_their_bits(heads, kv_heads, d, counts):
+    """fp16 rows whatever the kernel: the output's rounding and the weights'.  Over values spread evenly
+    in their logarithm a rounding to 11 bits is 2^-11 / sqrt(3) / 1.47 = 1.92e-4 of the norm; both
+    together sqrt(2) times that, 2.7e-4.  A query of 11 bits would add 2^-12 of each score."""
+    pos = [700 + 13 * i for i in range(len(counts))]
+    c = Paged(heads, kv_heads, d, 32, len(counts), 60)
+    c.fill(5)
+    q = rows(sum(counts), heads, d, torch.float16, 17)
+    got = run_attention(c, q, pos, counts).to(F64)
+    want, _ = c.attention(q, pos, counts)
+    e = float((got - want).norm() / want.norm())
+    assert e <= 3e-4
