@@ -529,6 +529,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         part1 += nh - 1;
         if (w.u < w.u1) w.next_item(a, kTcWork);
       }
+      // the buffers' last releases, which no other tile waits for, have to arrive while
+      // this CTA's shared memory is its own
+      if (t > 0) wait(kfree, (t - 1) & 1u);
+      for (uint32_t i = t > 2 ? t - 2 : 0; i < t; ++i) wait(&vfree[i & 1], (i >> 1) & 1u);
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------- widening --
@@ -637,6 +641,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (here) {
           tc_load_queries<D, kHalf>(a, it.w, valid, half, smem + Lay::kQ + half * Lay::kParts * Lay::kOp, s_qs);
           tc_proxy_fence();
+          tc_fence_before();   // (the item's products follow the reads of the last one's sums)
           __syncwarp();
           if (lane == 0) mbar_arrive(&qready[half]);
           const float qf = s_qs[r];   // this warp wrote it
@@ -739,8 +744,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (tid == 0) reinterpret_cast<TcJoin*>(a.rec + (size_t)gridDim.x * 2 * kTcRows * (D + 2))[cta] = join;
   }
-  // every MMA has been waited for (odone), or, after a time-out, gets its time here
+  // every MMA has been waited for (odone, vfree), or, after a time-out, gets its time here
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   if (*s_dead && tid == 0) drain_ring(full, Lay::kRing, *s_issued);
   if (*s_dead && tid == 32) {
     const unsigned long long dl = global_ns() + 1000000ull;   // 1 ms: far longer than what is in flight takes
