@@ -24,7 +24,7 @@
 // chosen experts form one run, cut into equal contiguous shares, one per CTA of a
 // grid that fills the GPU; the cut is made on the device from the routing.  A
 // unit (128 rows x 128 inputs) comes by one bulk copy, the record of each of the
-// expert's tokens (128 inputs and their sum) by one more; four warps unpack the
+// expert's tokens (128 inputs) by one more; four warps unpack the
 // nibbles straight into f16 A fragments and the tokens are the N side, so an
 // expert costs its own tokens' columns only.  A row block that spans CTAs leaves
 // one record per CTA, added in CTA order by the one that arrives last.  Down
@@ -32,16 +32,12 @@
 // row block meet in one fp32 tile per token in shared memory, so y needs no
 // second pass.
 //
-// The products.  A nibble u = code + 8 enters as v = 1 + u/16 (rows g of an MMA
-// tile) or 1 + u/256 (rows g + 8), so
-//   sum code x = 16 (sum v x - 1.5 sum x)   or   256 (sum v x - 1.03125 sum x):
-// the accumulators start at -1.5 (-1.03125) times the inputs' sum, and 16 (256)
-// is multiplied in once at the end.  That takes 5 operations a word instead of the
-// 9 of an exact conversion, which is what the kernels were short of.  It costs
-// accuracy where sums cancel: the fp32 accumulator holds up to 1.03 |sum x| next
-// to terms u x / 256, so a group's product is good to about 2^-24 * 264 |sum x|
-// against |code| |x|, some 2^-14 of it for 128 inputs of random sign, far below
-// the bf16 output's 2^-9.
+// The products.  A nibble u = code + 8 is masked into the f16 1 + u/16 (rows g of an
+// MMA tile) or 1 + u/256 (rows g + 8); one addition makes it code/16 or code/256, both
+// exact, and 16 (256) is multiplied in once at the end.  With the nibbles as masked, and
+// accumulators that start at -1.5 (-1.03125) times the inputs' sum, the additions are
+// saved (listed calls 2 to 8 % faster), but what the accumulators hold is then up to 264
+// times what the codes leave: inputs of one sign, 16384 of them, cost an output 3.1e-4.
 //
 // Rounding: inputs are f16 (x divided by a power of two near its RMS, so bf16
 // values keep all their bits down to 2^-14 of it; w * silu * up, the routing
@@ -257,12 +253,9 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
     const float f = s_factor[t];
     const __half2 h0 = __floats2half2_rn(__uint_as_float(v.x << 16) * f, __uint_as_float(v.x & 0xffff0000u) * f);
     const __half2 h1 = __floats2half2_rn(__uint_as_float(v.y << 16) * f, __uint_as_float(v.y & 0xffff0000u) * f);
-    const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-    const float sum = warp_sum((f0.x + f0.y) + (f1.x + f1.y));
     __half* rec = a.xh + ((size_t)(t0 + t) * ng + g) * kRecHalves;
     reinterpret_cast<uint2*>(rec)[lane] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-    if (lane == 0) *reinterpret_cast<float4*>(rec + kGroup) = make_float4(sum, 0.f, 1.f, 1.f);
   }
   // the last CTA of these tokens picks their experts
   __syncthreads();
@@ -362,21 +355,23 @@ struct MoeLayout {
   static constexpr int kBytes = kBar + 2 * kRing * 8 + 16;
 };
 
-// The four f16x2 registers of a word (see moe.cuh): rows g 1 + u/16, rows g + 8
-// 1 + u/256.
-__device__ __forceinline__ void place4(uint32_t w, uint32_t (&r)[4]) {
-  // "(a & b) | c" in one operation each; written out, because the compiler's own
-  // lowering of the expression takes two
-  asm("{\n\t.reg .b32 s;\n\t"
+// The four f16x2 registers of a word (see moe.cuh): the placed nibbles read 1 + u/16
+// (rows g) and 1 + u/256 (rows g + 8); less 1.5 and 1.03125 they are code/16 and
+// code/256, exact.
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b32 s, a, b, c, d;\n\t"
       "prmt.b32 s, %4, %4, 0x2301;\n\t"
-      "lop3.b32 %0, %4, 0x03C003C0, %5, 0xEA;\n\t"
-      "lop3.b32 %1, %4, 0x003C003C, %5, 0xEA;\n\t"
-      "lop3.b32 %2, s, 0x03C003C0, %5, 0xEA;\n\t"
-      "lop3.b32 %3, s, 0x003C003C, %5, 0xEA;\n\t}"
+      "lop3.b32 a, %4, 0x03C003C0, %5, 0xEA;\n\t"
+      "lop3.b32 b, %4, 0x003C003C, %5, 0xEA;\n\t"
+      "lop3.b32 c, s, 0x03C003C0, %5, 0xEA;\n\t"
+      "lop3.b32 d, s, 0x003C003C, %5, 0xEA;\n\t"
+      "add.rn.f16x2 %0, a, %6;\n\t"
+      "add.rn.f16x2 %1, b, %7;\n\t"
+      "add.rn.f16x2 %2, c, %6;\n\t"
+      "add.rn.f16x2 %3, d, %7;\n\t}"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(w), "r"(0x3C003C00u));
+      : "r"(w), "r"(0x3C003C00u), "r"(0xBE00BE00u), "r"(0xBC20BC20u));
 }
-constexpr float kBiasA = -1.5f, kBiasB = -1.03125f;   // -(16 + 8) / 16, -(256 + 8) / 256
 constexpr float kUnitA = 16.f, kUnitB = 256.f;
 
 // One unit times NT tiles of 8 columns for this warp's 32 rows, the group's
@@ -400,20 +395,15 @@ __device__ __forceinline__ void moe_unit(const uint8_t* st, const int (&xrow)[NT
     s_lo[m] = __half2float(sc[r0]);
     s_hi[m] = __half2float(sc[r0 + 8]);
   }
-  // sums (and factors) of this lane's two columns of each tile
-  MoeTail tail[NT][2];
+  // factors of this lane's two columns of each tile
+  float2 tail[NT][2];
+  if (kDown) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float* p = reinterpret_cast<const float*>(tile + (col[nt] + i) * kRecHalves + kGroup);
-      if (kDown) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        tail[nt][i] = MoeTail{{v.x, v.y}, {v.z, v.w}};
-      } else {
-        tail[nt][i].sum[0] = *p;
-      }
-    }
+      for (int i = 0; i < 2; ++i)
+        tail[nt][i] = *reinterpret_cast<const float2*>(tile + (col[nt] + i) * kRecHalves + kGroup);
+  }
   float d[2][NT][4], part[2][NT][4];
 #pragma unroll
   for (int kp = 0; kp < 4; ++kp) {
@@ -424,13 +414,10 @@ __device__ __forceinline__ void moe_unit(const uint8_t* st, const int (&xrow)[NT
         for (int nt = 0; nt < NT; ++nt) {
           if (kp == 2) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[m][nt][i] = d[m][nt][i] * tail[nt][i & 1].factor[0];
+            for (int i = 0; i < 4; ++i) part[m][nt][i] = d[m][nt][i] * tail[nt][i & 1].x;
           }
-          const float s0 = tail[nt][0].sum[kp >> 1], s1 = tail[nt][1].sum[kp >> 1];
-          d[m][nt][0] = kBiasA * s0;
-          d[m][nt][1] = kBiasA * s1;
-          d[m][nt][2] = kBiasB * s0;
-          d[m][nt][3] = kBiasB * s1;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[m][nt][i] = 0.f;
         }
     }
     uint32_t b[NT][4];
@@ -441,7 +428,7 @@ __device__ __forceinline__ void moe_unit(const uint8_t* st, const int (&xrow)[NT
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         uint32_t af[4];
-        place4(words[m][2 * kp + h], af);
+        codes4(words[m][2 * kp + h], af);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_f16_16816(d[m][nt], af, b[nt][2 * h], b[nt][2 * h + 1]);
       }
@@ -452,7 +439,7 @@ __device__ __forceinline__ void moe_unit(const uint8_t* st, const int (&xrow)[NT
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float v = kDown ? fmaf(d[m][nt][i], tail[nt][i & 1].factor[1], part[m][nt][i]) : d[m][nt][i];
+        const float v = kDown ? fmaf(d[m][nt][i], tail[nt][i & 1].y, part[m][nt][i]) : d[m][nt][i];
         acc[m][nt][i] = fmaf(i < 2 ? s_lo[m] : s_hi[m], v, acc[m][nt][i]);
       }
 }
@@ -811,15 +798,9 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const float f = pow2_at(mx), inv = pow2_inverse(f);
             const __half2 hv = __floats2half2_rn(v[0] * inv, v[1] * inv);
-            const float2 hf = __half22float2(hv);
-            const float sum = warp_sum(hf.x + hf.y);
             __half* rec = a.act + ((size_t)(rb >> 1) * (a.T * a.K) + off + c) * kRecHalves;
             reinterpret_cast<__half2*>(rec + 64 * (rb & 1))[lane] = hv;
-            if (lane == 0) {
-              MoeTail* tail = reinterpret_cast<MoeTail*>(rec + kGroup);
-              tail->sum[rb & 1] = sum;
-              tail->factor[rb & 1] = f;
-            }
+            if (lane == 0) reinterpret_cast<float*>(rec + kGroup)[rb & 1] = f;
           }
         }
       }

@@ -12,12 +12,10 @@
 // swapped masked again, all of them land in an f16's mantissa without a shift:
 // a word takes one byte permutation and four logic operations.  Or-ed with 1.0,
 // slots 0 and 2 (rows g of the A fragment) read 1 + u / 16 and slots 1 and 3
-// (rows g + 8) 1 + u / 256.
+// (rows g + 8) 1 + u / 256, one f16 addition away from code/16 and code/256.
 //
 // Activations are f16 rows, cut into records of 128 inputs (a unit's) and 16
-// bytes: what a product with 1 + u/16 and 1 + u/256 owes to the constant part
-// is a multiple of the inputs' sum, so each record carries that sum (of the
-// rounded values, fp32).
+// bytes (which also keep the rows of a tile on different banks).
 #pragma once
 
 #include "futr_internal.cuh"
@@ -31,15 +29,12 @@ constexpr int kMoeMaxExperts = 256;
 constexpr int kMoeMaxTopK = 16;
 constexpr int kMoeMaxPairs = kMaxBatch * kMoeMaxTopK;
 
-// One record of an activation row: 128 f16 values; then two sums and two factors
-// (inputs 0..63 and 64..127).  Gate/up inputs: sum[0] is the sum of all 128, the
-// factor is the token's (MoeArgs::rms).  Down inputs: each half is divided by
-// the power of two at its largest value, factor[h], and has its own sum.
+// One record of an activation row: 128 f16 values, then room for four floats.  Down
+// inputs: each half (inputs 0..63 and 64..127) is divided by the power of two at its
+// largest value; the first two floats are these factors.  Gate/up inputs have one a
+// token (MoeArgs::rms).
 constexpr int kRecHalves = 136;
 constexpr int kRecBytes = 2 * kRecHalves;
-struct MoeTail {
-  float sum[2], factor[2];
-};
 
 struct MoeHeader {
   uint64_t magic;

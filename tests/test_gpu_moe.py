@@ -237,3 +237,48 @@ def test_foreign_blob_is_not_read(word, value, T):
     assert bool((y == 7).all())
     header.copy_(keep)
     m.check(x)
+
+
+def moe_error(m, x):
+    """The layer's error next to its own size: the residual takes the expected output away, so that
+    the bf16 rounding of what is left says nothing."""
+    ids = m.run(x)[1]
+    ry, _, _ = m.reference(x, ids)
+    resid = (-ry).to(torch.bfloat16)
+    y, again, _ = m.run(x, resid)
+    assert torch.equal(again, ids)
+    return float((y.to(F64) - (resid.to(F64) + ry)).norm() / ry.norm())
+
+
+# activations w * silu * up are rounded to 11 bits: 2^-11 / sqrt(3) of each at the most, in the mean square
+# and of both signs; inputs of the first product that are exact, or rounded the same way, add less;
+# the sums are fp32
+MOE_ERROR = 3e-4
+
+
+@pytest.mark.parametrize("T", [1, 8, 20, 32])
+@pytest.mark.parametrize("H,I", [(16384, 128), (128, 16384), (4096, 512)])
+def test_inputs_of_one_sign(H, I, T):
+    """Positive inputs: codes of both signs cancel, the sums of what carries them do not."""
+    m = Moe(H, I, 1, 1, eps=0.0, seed=12)
+    wg, _, wd = m.w[0]
+    futr.futr_moe_pack(m.ms, 0, wg, wg, wd, None, m.blob)       # silu(g) g: (nearly) one sign, too
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = (0.5 + torch.rand((T, H), generator=g, device="cuda")).to(torch.bfloat16)
+    assert moe_error(m, x) <= MOE_ERROR
+
+
+@pytest.mark.parametrize("T", [1, 9, 32])
+def test_activations_keep_eleven_bits(T):
+    m = Moe(1024, 640, 4, 2, seed=13)
+    assert moe_error(m, rows(m, T)) <= MOE_ERROR
+
+
+@pytest.mark.parametrize("T", [1, 9, 32])
+def test_activations_far_apart(T):
+    """Groups whose activations are 2^16 apart and count the same: each has a factor of its own."""
+    m = Moe(512, 640, 1, 1, eps=0.0, seed=14)
+    wg, wu, wd = m.w[0]
+    f = 2.0 ** (8 - 4 * torch.arange(5, device="cuda").repeat_interleave(128).float())
+    futr.futr_moe_pack(m.ms, 0, wg, wu * f[:, None], wd / f, None, m.blob)
+    assert moe_error(m, rows(m, T)) <= MOE_ERROR
