@@ -830,6 +830,10 @@ int sm_count() { return current_sm_count(); }
 
 bool shape_valid(const futr_shape* s) { return shape_ok(s); }
 
+// FUTR_TEST_WITHHOLD_COPY=1, as in a block's step: one CTA of the paged attention (with
+// the last share) or of the experts' gate/up issues no copy.
+bool withhold_copy() { return env_int("FUTR_TEST_WITHHOLD_COPY") == 1; }
+
 uint64_t region_after(uint64_t off, uint64_t size) { return after(off, size); }
 
 // A region that starts at `start` is preceded by its predecessor's guard.

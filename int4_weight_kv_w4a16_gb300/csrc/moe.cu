@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
     int rows_due = 0;   // down: stages whose activations wait for gate/up
     const __half* due[kMoeRing];
     int due_bytes[kMoeRing];
-    for (int u = u0; u < u1 && ok;) {
+    for (int u = !kDown && a.withhold && cta == 0 ? u1 : u0; u < u1 && ok;) {
       int rb, ai, g, end;
       run.at(u, rb, ai, g, end);
       end = min(end, u1);

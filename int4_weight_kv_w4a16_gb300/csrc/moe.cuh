@@ -50,6 +50,7 @@ inline uint64_t moe_down_bytes(const futr_moe_shape& s) {
 
 struct MoeArgs {
   int H, I, E, K, T, renorm;
+  bool withhold;                       // tests of the failure path: gate/up's CTA 0 issues no copy
   float eps;                           // 0: no normalization
   const __nv_bfloat16* x;              // [T][H]
   const float* gain;                   // [H] or nullptr

@@ -7,6 +7,7 @@
 
 namespace futr {
 namespace host {
+bool withhold_copy();
 uint64_t region_after(uint64_t off, uint64_t size);
 cudaError_t fill_guards_before(void* base, const uint64_t* starts, int n, cudaStream_t st);
 cudaError_t check_guards_before(void* base, const uint64_t* starts, int n, int* err, cudaStream_t st);
@@ -192,6 +193,7 @@ futr_status futr_moe_layer(const uint16_t* x, const float* gain, const uint16_t*
     a.ids = ids;
     a.weights = weights;
     a.err = at<int>(ws->base, 0);
+    a.withhold = host::withhold_copy();
     a.cnt = at<unsigned>(ws->base, ws->off_cnt);
     a.rms = at<float>(ws->base, ws->off_rms);
     a.share = a.rms + ws->max_batch;

@@ -67,6 +67,7 @@ struct PagedAttnArgs {
   unsigned* cnt;            // arrival counters, one per CTA
   int* err;                 // the cache's error word: rows and pages out of range
   int* stop;                // the workspace's error and abort words: a wait ran out
+  bool withhold;            // tests of the failure path: the last share's copies are not issued
 };
 
 int paged_attn_sms();                        // of the current device

@@ -8,6 +8,7 @@
 namespace futr {
 namespace host {
 bool shape_valid(const futr_shape* s);
+bool withhold_copy();
 uint64_t region_after(uint64_t off, uint64_t size);
 cudaError_t fill_guards_before(void* base, const uint64_t* starts, int n, cudaStream_t st);
 cudaError_t check_guards_before(void* base, const uint64_t* starts, int n, int* err, cudaStream_t st);
@@ -247,6 +248,7 @@ futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t
     a.cnt = at<unsigned>(ws->base, 0);
     a.err = at<int>(cache->base, cache->err_offset);
     a.stop = at<int>(ws->base, ws->err_offset);
+    a.withhold = host::withhold_copy();
     CUtensorMap map;
     std::memcpy(&map, cache->copy_map, sizeof(map));
     return launch_paged_attention(a, map, s.head_dim, dtype, as_stream(stream)) == cudaSuccess ? FUTR_OK

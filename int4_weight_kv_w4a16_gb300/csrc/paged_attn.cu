@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     Cut cut;
     if (!find_share(a, kPaWork, cta, gridDim.x, w, cut, false)) return;
     int issued = 0;
-    const bool ok = produce_tiles<D>(a, &map, kPaWork, w, smem, s_scale, full, empty, kPaRing, issued);
+    const bool ok = produce_tiles<D>(a, &map, kPaWork, w, smem, s_scale, full, empty, kPaRing, cut.total, issued);
     if (!ok) {
       pa_timeout(a);
       *s_dead = 1;

@@ -464,7 +464,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---------------------------------------------------------- producer --
     if (active) {
       int issued = 0;
-      if (!produce_tiles<D>(a, &map, kTcWork, w, smem + Lay::kStage, s_raw, full, empty, Lay::kRing, issued)) {
+      if (!produce_tiles<D>(a, &map, kTcWork, w, smem + Lay::kStage, s_raw, full, empty, Lay::kRing,
+                            it.cut.total, issued)) {
         pa_timeout(a);
         *s_dead = 1;
       }

@@ -235,17 +235,18 @@ __device__ __forceinline__ bool find_share(const PagedAttnArgs& a, Rows s, int c
 // The tiles of a CTA's share into a ring of stages (a full warp): a tile's pages as
 // whole (page, kv-head) blocks, keys then values, and the scales of its 16-position
 // sub-tiles, (key scale, log2 and inverse of the value scale, 0).  False: a wait
-// ran out (`issued` stages are under way or done).
+// ran out (`issued` stages are under way or done).  total: the call's units.
 template <int D>
 __device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUtensorMap* map, Rows s, Walk& w,
                                               uint8_t* stages, float4* s_scale, uint64_t* full, uint64_t* empty,
-                                              int ring, int& issued) {
+                                              int ring, long long total, int& issued) {
   const int lane = threadIdx.x & 31, page = a.c.page, plog = a.c.page_log2;
   const int ppt = kPaTile >> plog;   // pages of a tile
   const uint32_t bytes = (uint32_t)(2 * page * D);
   int slot = 0;
   uint32_t phase = 0;
   bool ok = true;
+  if (a.withhold && w.u1 == total) return ok;
   while (w.u < w.u1 && ok) {
     const int first = w.t.t0 + (int)(w.u - w.item0);
     const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);

@@ -282,3 +282,17 @@ def test_activations_far_apart(T):
     f = 2.0 ** (8 - 4 * torch.arange(5, device="cuda").repeat_interleave(128).float())
     futr.futr_moe_pack(m.ms, 0, wg, wu * f[:, None], wd / f, None, m.blob)
     assert moe_error(m, rows(m, T)) <= MOE_ERROR
+
+
+@pytest.mark.parametrize("T", [1, 20])
+def test_a_copy_that_never_comes(monkeypatch, T):
+    """The first CTA's waits run out (test hook): the call ends with a status, and the next is exact again."""
+    m = Moe(512, 640, 8, 2, seed=15)
+    x = rows(m, T)
+    good = m.check(x)
+    for _ in range(2):
+        monkeypatch.setenv("FUTR_TEST_WITHHOLD_COPY", "1")
+        futr.futr_moe_layer(x, m.gain, m.router, m.blob, None, torch.empty_like(x), m.ws)
+        monkeypatch.delenv("FUTR_TEST_WITHHOLD_COPY")
+        assert futr.futr_moe_check(m.ws) == futr.FUTR_ERR_TIMEOUT
+        assert torch.equal(m.run(x)[0], good)

@@ -582,3 +582,26 @@ def test_fp16_rows_keep_their_bits(heads, kv_heads, d, counts):
     want, _ = c.attention(q, pos, counts)
     e = float((got - want).norm() / want.norm())
     assert e <= 3e-4
+
+
+@pytest.mark.parametrize("n", [1, 90], ids=["few", "many"])
+def test_a_copy_that_never_comes(monkeypatch, n):
+    """The last CTA's waits run out (test hook): the call ends, the cache and the workspace report it,
+    another workspace is not affected, and after a check with its own the call is exact again."""
+    c = Paged(8, 2, 128, 32, 2, 100)
+    c.fill(6)
+    pos, counts = [3000, 2000], [n, n]
+    q = rows(2 * n, 8, 128, torch.bfloat16, 31)
+    good = run_attention(c, q, pos, counts)
+    mine = c.ws
+    other = futr.futr_paged_workspace_init(c.cs, futr.alloc_bytes(futr.futr_paged_workspace_size(c.cs)))
+    for _ in range(2):
+        monkeypatch.setenv("FUTR_TEST_WITHHOLD_COPY", "1")
+        futr.futr_paged_attention(c.cache, 0, 2, ints(pos), starts(counts), c.table, q, torch.empty_like(q), mine)
+        monkeypatch.delenv("FUTR_TEST_WITHHOLD_COPY")
+        assert futr.futr_paged_check(c.cache) == futr.FUTR_ERR_TIMEOUT
+        c.ws = other
+        assert torch.equal(run_attention(c, q, pos, counts), good)
+        c.ws = mine
+        assert futr.futr_paged_check(c.cache, mine) == futr.FUTR_ERR_TIMEOUT
+        assert torch.equal(run_attention(c, q, pos, counts), good)
