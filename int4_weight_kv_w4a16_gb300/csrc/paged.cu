@@ -210,17 +210,28 @@ __global__ void __launch_bounds__(kAppMaxThreads) paged_append_kernel(const Appe
   __syncthreads();   // every thread has read the old scale by now, too
   for (int w = 0; w < threads / 32; ++w) m = fmaxf(m, s_max[w]);
   const float s_new = fmaxf(s_old, pow2(scale_exp(m)));
-  // of a power of two as the append makes them, up to 2^120, exact
-  float inv = __uint_as_float((254u << 23) - __float_as_uint(s_new));
-  if ((__float_as_uint(s_new) & 0x7FFFFFu) != 0u || s_new > 0x1p120f) {
-    // an old scale that is a program's own: the rows are divided by it
-#pragma unroll
-    for (int i = 0; i < kAppRounds; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = __fdiv_rn(x[i][j], s_new);
-    inv = 1.f;
-  }
+  const float inv = __uint_as_float((254u << 23) - __float_as_uint(s_new));   // of a power of two: exact
   if (tid == 0 && s_new != s_old) *scale = s_new;
+  if ((__float_as_uint(s_new) & 0x7FFFFFu) != 0u || s_new > 0x1p120f) {
+    // an old scale that is no power of two as they are made here, but a program's own:
+    // the rows are divided by it, x[0] a turn
+#pragma unroll 1
+    for (int slot = lo + rg; slot < hi; slot += rows) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = __fdiv_rn(x[0][4 * h + j], s_new);
+        *(reinterpret_cast<uint32_t*>(codes + (size_t)slot * D + h * (D / 2)) + lg) =
+            e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16);
+      }
+#pragma unroll
+      for (int i = 0; i + 1 < kAppRounds; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = x[i + 1][j];
+    }
+    return;
+  }
   if (s_old > 0.f && s_new > s_old) {
     // the page's other slots at the new scale, 8 codes a thread
     const float ratio = s_old * inv;
