@@ -681,18 +681,28 @@ cudaError_t pa_launch(const PagedAttnArgs& a, const CUtensorMap& map, cudaStream
 
 // Rows (tokens x query heads of a kv-head) a sequence, on average, from which on the
 // many-row kernel is faster.  It costs the same for any number up to 128, these tiles
-// of 8 rows their number.  In us, these / that: 8 sequences over 4000 positions,
-// D = 128, 48 rows 43 / 45, 64 rows 50 / 46, 96 rows 72 / 46; D = 64, 64 rows 36 / 38,
-// 96 rows 51 / 39; one over 8000, D = 128, 64 rows 26 / 30, 96 rows 35 / 31.
-constexpr int kTcMinRows = 80;
+// of 8 rows their number; but it has an SM for a CTA, which few (sequence, kv-head)
+// pairs do not fill.  In us, these / that, after 4000 positions: 64 pairs, D = 128, 32
+// rows 44 / 43, 48 rows 62 / 43, 64 rows 80 / 44; D = 64, 40 rows 38 / 38, 64 rows
+// 56 / 38; 32 pairs, D = 128, 48 rows 36 / 29; D = 64, 48 rows 27 / 26; 16 pairs, D = 128,
+// 48 rows 23 / 24; D = 64, 64 rows 22 / 22; 8 pairs after 8000, D = 128, 64 rows
+// 27 / 30, 96 rows 35 / 31.  Where contexts are short or kv-heads few the two meet later:
+// 64 pairs after 500, D = 64, 64 rows 20 / 20; 32 sequences of 2 kv-heads after 1000,
+// D = 64, 64 rows 25 / 25.
+constexpr int kTcPairs = 32;
+int tc_min_rows(const PagedAttnArgs& a, int d) {
+  return (long long)a.r.batch * a.Hkv < kTcPairs ? 80 : d == 128 ? 48 : 64;
+}
 // Where sequences may differ much (their rows are on the device), both kernels, each
 // for its sequences: from 1024 rows on in all, where a chunk among single tokens costs
 // the tiles of 8 rows more than two launches, and below 256 a sequence on average,
 // where the single tokens are worth one.  31 single tokens and a chunk of 512 tokens
-// after 2000 positions (G = 4): 85 us, by the tiles of 8 rows alone 250; with a chunk
-// of 256 72 and 134; 64 sequences of 5 drafted tokens, where the many-row kernel finds
-// nothing, 144 and 137.
-constexpr int kBothMinRows = 1024, kBothMaxRows = 256;
+// after 2000 positions (G = 4): 85 us, by the tiles of 8 rows alone 253; with a chunk
+// of 256 73 and 136; 64 sequences of 5 drafted tokens, where the many-row kernel finds
+// nothing, 145 and 139.  Single tokens alone have no chunk (64 of G = 16 after 1000
+// positions 36 with both, 32 with one): the rows beyond one token a sequence have to be
+// worth one.
+constexpr int kBothMinRows = 1024, kBothMaxRows = 256, kBothMinChunk = 512;
 
 }  // namespace
 
@@ -716,14 +726,16 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& args, const CUtensorMap&
   a.rows_lo = 0;
   a.rows_hi = INT_MAX;
   const long long rows = (long long)a.r.n_rows * a.G, batch = a.r.batch;
-  const bool many = rows >= kTcMinRows * batch;
-  const bool both = a.r.start && batch > 1 && rows >= kBothMinRows && rows < kBothMaxRows * batch;
+  const int least = tc_min_rows(a, d);
+  const bool many = rows >= least * batch;
+  const bool both = a.r.start && batch > 1 && rows >= kBothMinRows && rows < kBothMaxRows * batch &&
+                    rows - batch * a.G >= kBothMinChunk;
   if (many || both) {
-    if (both) a.rows_lo = kTcMinRows;
+    if (both) a.rows_lo = least;
     const cudaError_t e = launch_paged_attention_tc(a, map, d, dtype, paged_attn_sms(), st);
     if (e != cudaSuccess || !both) return e;
     a.rows_lo = 0;
-    a.rows_hi = kTcMinRows;
+    a.rows_hi = least;
   }
   const bool half = dtype == FUTR_DTYPE_F16;
   if (d == 128) return half ? pa_launch<128, true>(a, map, st) : pa_launch<128, false>(a, map, st);
