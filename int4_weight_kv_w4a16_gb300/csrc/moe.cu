@@ -17,9 +17,9 @@
 // Above 8 tokens a fourth adds down's parts.
 //
 // The expert kernels are bound by the weight stream: 17 tokens through 8 of 128
-// experts (4096 x 1536, 830 MB) take 160 us, 5.2 TB/s; 32 through 2 of 8 (4096 x
-// 14336, 726 MB) 184 us, 4.0 TB/s, where the unpacking and the products of up to 16
-// columns take as long as the stream; one token through 2 of 8 (181 MB) 47 us, some
+// experts (4096 x 1536, 830 MB) take 172 us, 4.8 TB/s; 32 through 2 of 8 (4096 x
+// 14336, 726 MB) 193 us, 3.8 TB/s, where the unpacking and the products of up to 16
+// columns take as long as the stream; one token through 2 of 8 (181 MB) 49 us, some
 // 15 of them the router, the starts and the ends of three kernels.  All units of the
 // chosen experts form one run, cut into equal contiguous shares, one per CTA of a
 // grid that fills the GPU; the cut is made on the device from the routing.  A
@@ -458,8 +458,8 @@ struct MoeRun {
   // The least units of a share.  Down: a row block's parts are added one after the
   // other, a part in about a third of a unit's time: with few units, parts and units a
   // part balance near the root of the item.  Without / with it, 8 tokens through 4 of
-  // 128 experts of 640 x 512 34 / 23 us, 1 through 2 of 8 of 1024 x 3584 20 / 17.6, 20
-  // through the same 32.6 / 34.2; layers from 2048 x 1408 on the same within 2 %.
+  // 128 experts of 640 x 512 35 / 24 us, 1 through 2 of 8 of 1024 x 3584 20 / 18, 20
+  // through the same 32.9 / 34.5; larger layers the same within 2 %.
   __device__ __forceinline__ int least() const { return kDown ? max(1, (int)sqrtf((float)item_len * (1.f / 3.f))) : 1; }
   __device__ __forceinline__ int total() const { return kDown ? n_rb * item_len : n_rb * item_len * active; }
   // row block and active-expert index of unit u; the units of that (row
@@ -504,7 +504,7 @@ struct MoeCut {
 // More than 8 tokens: the records of a down row block (14 of 16 KB at 32 tokens on
 // 152 SMs) are added by a kernel of their own, by 8 tokens; the one CTA that arrives
 // last would read them alone, for longer than a launch takes (32 tokens through 2 of
-// 8 experts 194 us so, 189 with the kernel).  With up to 8 tokens the launch costs
+// 8 experts 199 us so, 193 with the kernel; through 8 of 128 of 2048 x 768 96 and 79).  With up to 8 tokens the launch costs
 // what it saves (1 to 8 tokens through five layers: within 1 us either way).
 __host__ __device__ inline bool sums_apart(int T) { return T > 8; }
 
@@ -668,8 +668,8 @@ __global__ void __launch_bounds__(kMoeThreads, NT == 4 ? 2 : 3) moe_expert_kerne
       const uint8_t* w = a.blob + kHeaderBytes + (size_t)e * a.expert_bytes + (kDown ? a.gu_bytes : 0) +
                          ((size_t)rb * run.ng + g) * kUnitBytes;
       // Gate/up: this lane's token's records (lanes n..31 have none).  Down: the
-      // expert's records of a group lie side by side, one copy (a copy each: 189 us for
-      // the 32 tokens that take 184).
+      // expert's records of a group lie side by side, one copy (with a copy each the
+      // 32 tokens took 189 us, with one 184).
       const int lanes = kDown ? 1 : n, rec_bytes = kDown ? n * kRecBytes : kRecBytes;
       const size_t step = kDown ? (size_t)a.T * a.K * kRecHalves : kRecHalves;
       const __half* row = kDown ? a.act + g * step + (size_t)off * kRecHalves : a.xh + g * step;
@@ -964,8 +964,9 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t st) {
   // Columns of a pass: an expert has at most T tokens.  Above 16, passes of 16 (three
   // CTAs an SM) unless experts have more than 8 tokens on average, where many would
   // have to be streamed twice.  In passes of 16 / of 32: 32 tokens through 2 of 8
-  // experts of 4096 x 14336 189 / 220 us, through 8 of 128 of 2048 x 768 77 / 85 us;
-  // of 8 small experts (4096 x 2048) 59 / 55 us.
+  // experts of 4096 x 14336 193 / 212 us, through 8 of 128 of 2048 x 768 79 / 88 us; the
+  // other way where the layer is small: 2 of 8 experts of 4096 x 2048 60 / 55 us, which
+  // the rule, that knows the tokens an expert only, gives to the passes of 16.
   if (a.T <= 8) return launch_experts<1>(a, dev, st);
   if (a.T <= 16 || a.T * a.K <= 8 * a.E) return launch_experts<2>(a, dev, st);
   return launch_experts<4>(a, dev, st);

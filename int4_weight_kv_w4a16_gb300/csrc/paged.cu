@@ -14,11 +14,11 @@
 // codes: page / 4 rows at a time, whatever the page.
 //
 // Bound by memory for prompts (2 bytes read and 1 written per element): 64 MB take
-// 16.3 us (3.9 TB/s; 9.5 us at the copy rate; the rest is the start of a CTA, four
+// 16.4 us (3.9 TB/s; 9.5 us at the copy rate; the rest is the start of a CTA, four
 // waves of them).  Two rows a thread took 21 us where four and eight took 18.4, and
 // reading the rows a second time instead of keeping them 36.  Bound by latency for
 // single tokens, whose chain is: row bounds -> table entry -> old scale, and beside
-// it row -> rotation -> maximum: 2.3 us for one, 3.1 us for 32 sequences.
+// it row -> rotation -> maximum: 2.3 us for one, 3.2 us for 32 sequences.
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kAppMaxThreads) paged_append_kernel(const Appe
     }
   // the touched page of this CTA: sequences in order, each with the pages that
   // its new rows meet; one warp looks for all (every warp by itself: 18.4 us for the
-  // prompts that take 16.3)
+  // prompts that take 16.4)
   int item = blockIdx.x, row0 = 0, n = 0, p0 = 0, b = -1;
   for (int b0 = 0; b0 < a.r.batch && tid < 32; b0 += 32) {
     int rr = 0, nn = 0, pp = 0, pages = 0;

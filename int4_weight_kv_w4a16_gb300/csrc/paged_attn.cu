@@ -29,16 +29,16 @@
 // element (put back in the score's factor): 11 significant bits, below what bf16
 // rows resolve; f16 rows, which resolve more, in two parts (22 bits; an output's
 // error is then its own rounding, 2.0e-4, instead of 4.3e-4).  The second MMAs cost
-// drafted tokens nothing (13.1 us), 32 ragged sequences of D = 128 39.0 us instead of
-// 36.7.  The weights enter as f16: 11 bits down to 2^-28 of the largest, next to the 4 of
+// drafted tokens nothing (10.3 us), 32 ragged sequences of D = 128 34.6 us instead of
+// 33.3.  The weights enter as f16: 11 bits down to 2^-28 of the largest, next to the 4 of
 // the values they multiply.
 // All sums are fp32.
 //
 // Bound by memory while a sequence has one row tile (the codes are read once, 2 d
 // bytes a position and kv-head); further tiles of a sequence read them from L2.  32
-// ragged sequences of 512 to 4096 positions (148 MB): 33.0 us, 4.5 TB/s; four of 20K
+// ragged sequences of 512 to 4096 positions (148 MB): 33.3 us, 4.4 TB/s; four of 20K
 // to 50K (269 MB): 51.3 us, 5.2 TB/s; the copies alone, in equal shares of tiles, 30
-// and 48.5 us.  One sequence of 1024 positions: 7.9 us, the latency of share -> page
+// and 48.5 us.  One sequence of 1024 positions: 8.0 us, the latency of share -> page
 // id -> tile -> join.
 #include <climits>
 
@@ -57,8 +57,8 @@ constexpr int NT = 1;
 constexpr float kTopWeight = 14.f;   // log2 of the largest weight
 constexpr int kPaRows = 8 * NT;
 // An item's start and join count as three tiles in the cut.  With 0, 2, 3, 4 and 6: 32
-// ragged sequences 36.6, 33.0, 33.1, 33.5, 35.1 us; four long ones 53.9, 52.4, 51.3, 51.1,
-// 51.3; drafted tokens (D = 64) 13.1, 11.4, 10.3, 10.4, 11.0.
+// ragged sequences 36.8, 33.3, 33.3, 33.8, 35.3 us; four long ones 53.8, 52.0, 51.2, 51.2,
+// 51.5; drafted tokens (D = 64) 13.2, 11.5, 10.4, 10.5, 11.0.
 constexpr Rows kPaWork{kPaRows, 3};
 
 template <int D>

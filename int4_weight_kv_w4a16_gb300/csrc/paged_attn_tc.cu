@@ -32,7 +32,8 @@
 //
 // Bound by the tensor cores in principle (4 x 256 x 128 x D flops a tile take 2048
 // cycles at D = 128).  Measured on four prompts' chunks of 512 rows after contexts to
-// 8K, 32 heads over 8, D = 128: 84 us, 0.57 PFLOP/s of the seen positions.  A CTA's
+// 8K, 32 heads over 8, D = 128: 86 us, 0.56 PFLOP/s of the seen positions (84.5 with a
+// reference that lags by 2^8).  A CTA's
 // 20 tiles take some 5200 cycles each (a half's softmax, 3300 while it shares the
 // schedulers with the other half's and the widening, and its products, 1024, follow
 // one another); the start, the queries of two parts and the records of split items
@@ -47,8 +48,8 @@ namespace {
 
 constexpr int kTcRows = 256, kTcHalf = 128;
 // An item's start (queries) and end (records) count as four tiles in the cut: CTAs with
-// three items ended last.  With 0, 3, 4, 5, 6 and 8 the chunks below take 96.0, 85.8,
-// 84.3, 85.1, 86.7 and 89.3 us.
+// three items ended last.  With 0, 3, 4, 5, 6 and 8 the chunks above take 98.1, 87.6,
+// 86.0, 86.6, 88.0 and 90.8 us.
 constexpr Rows kTcWork{kTcRows, 4};
 constexpr int kTcThreads = 14 * 32;
 constexpr int kTcSoft = 8 * 32;                 // softmax threads
@@ -58,7 +59,8 @@ constexpr float kRefWeight = 11.f, kRefLag = 4.f;   // log2 of the weight at a r
 // f16 parts of a query element: two for f16 rows, as few rows have them, so that a
 // row's error does not depend on the kernel its batch takes.  The chunks of the head
 // comment with f16 rows: an error of 2.1e-4 in 104 us, with one part 4.3e-4 in 84 (the
-// products of the scores lie between a half's softmaxes).
+// products of the scores lie between a half's softmaxes); four chunks of up to 256 rows
+// after 4000 positions, D = 64: 40.5 and 37.8.
 template <bool kHalf>
 constexpr int kTcParts = kHalf ? 2 : 1;
 
@@ -765,8 +767,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // of the item that begins in CTA c, a lane per row, a warp per eighth of its dims.
 // A kernel of its own, so that every SM takes part: the CTA that arrived last would
 // read 133 KB a part by itself, 19 of them for one sequence of 256 rows over 8000
-// positions, a call of 73 us that takes 46 us like this.  Where items have few parts
-// it costs a launch: 96 us for the chunks above, 93 without it (in equal shares of
+// positions: a call of 73 us became one of 46 (36.5 by now).  Where items have few parts
+// it costs a launch: 96 us for the chunks above, 93 without it (both in equal shares of
 // tiles).
 constexpr int kTcJoinRows = 32;
 
