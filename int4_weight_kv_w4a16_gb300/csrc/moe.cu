@@ -963,10 +963,12 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // Columns of a pass: an expert has at most T tokens.  Above 16, passes of 16 (three
   // CTAs an SM) unless experts have more than 8 tokens on average, where many would
-  // have to be streamed twice.  In passes of 16 / of 32: 32 tokens through 2 of 8
-  // experts of 4096 x 14336 193 / 212 us, through 8 of 128 of 2048 x 768 79 / 88 us; the
-  // other way where the layer is small: 2 of 8 experts of 4096 x 2048 60 / 55 us, which
-  // the rule, that knows the tokens an expert only, gives to the passes of 16.
+  // have to be streamed twice.  In passes of 16 / of 32, at two tokens an expert: 32
+  // through 8 of 128 of 2048 x 768 79 / 88 us, through 4 of 60 of 2048 x 1408 72 / 74; at
+  // six: 24 through 2 of 8 of 4096 x 14336 182 / 197; at 16: 32 through 2 of 4 of 4096 x
+  // 14336 163 / 161, 4 of 8 of 4096 x 4096 112 / 110.  At eight, where the rule changes
+  // sides, the layer's size decides, which it does not know: 2 of 8 of 4096 x 14336
+  // 193 / 212, x 8192 139 / 137, x 4096 87 / 84, x 2048 60 / 55.
   if (a.T <= 8) return launch_experts<1>(a, dev, st);
   if (a.T <= 16 || a.T * a.K <= 8 * a.E) return launch_experts<2>(a, dev, st);
   return launch_experts<4>(a, dev, st);
