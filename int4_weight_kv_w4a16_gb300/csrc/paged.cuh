@@ -3,7 +3,7 @@
 //
 // A page holds `page` consecutive positions of one sequence, for every kv-head
 //   codes  [layer][page id][kv-head][K, V][slot][d]   e4m3, one byte each
-//   scales [layer][page id][kv-head][K, V]            fp32, powers of two
+//   scales [layer][page id][kv-head][K, V]            fp32, powers of two where the append wrote them
 // value = code * scale.  Powers of two make the scale exact in every use: codes
 // are x / s rounded once, a page whose scale grows by 2^n keeps its codes
 // exactly (except those that reach e4m3's subnormals, which lose their low
