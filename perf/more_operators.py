@@ -135,6 +135,8 @@ def draw(rng):
         layers = _log(rng, 1, max(1, min(32, (500 * 4 * 8 * 64 * 128) // (pages * kv_heads * page * d))))
         return _compact(None, batch, pages, rng.randint(0, pages // 4), layers, kv_heads, d, page)
     heads = kv_heads * rng.choice([1, 2, 4, 4, 5, 8, 16])
+    if heads * d % 128:                             # a model's width is a multiple of 128
+        kv_heads, heads = 2 * kv_heads, 2 * heads
     if rng.random() < 0.3:                          # chunks
         batch, new, hi = _log(rng, 1, 4), _log(rng, 9, 300), _log(rng, 100, 8000)
     else:                                           # decoding, drafted tokens
@@ -357,7 +359,7 @@ def prepare(case, seed):
             st["ws"] = futr.futr_beam_workspace_init(*n, futr.alloc_bytes(futr.futr_beam_workspace_size(*n)))
             return st
         kv_heads, d = case.get("kv_heads", 1), case.get("d", 128)
-        sh = futr.make_shape(inputs.BlockShape(hidden=128, n_q_heads=case.get("heads", kv_heads), n_kv_heads=kv_heads,
+        sh = futr.make_shape(inputs.BlockShape(hidden=128, n_q_heads=case.get("heads", 2 * kv_heads), n_kv_heads=kv_heads,
                                                head_dim=d, inter=128, had_block=d, rope_theta=THETA))
         if op == "reorder":
             size = (case["layers"], case["groups"] * case["beams"], case["capacity"])
