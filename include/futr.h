@@ -47,7 +47,9 @@ typedef int32_t futr_status;
 #define FUTR_ERR_NOT_PD        7  /* GPTQ: a dampened Hessian is not positive definite */
 #define FUTR_ERR_CORRUPT       8  /* device: guard words after a region overwritten    */
 #define FUTR_ERR_BOUNDS        9  /* device, debug build: an index failed its check    */
-#define FUTR_ERR_NOT_FINITE   10  /* device: infinity or NaN appended to a paged cache */
+#define FUTR_ERR_NOT_FINITE   10  /* device: infinity or NaN appended to a paged cache, NaN in logits */
+#define FUTR_ERR_NO_PAGES     11  /* device: fewer free pages than a call needs         */
+#define FUTR_ERR_NOT_HELD     12  /* device: a table names a page that its pool has free */
 
 /* Shape of one decoder block. */
 typedef struct futr_shape {
@@ -467,6 +469,163 @@ futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t
  * workspaces of the cache are not affected, and that one is out of use (its calls
  * give up) until a check with it has returned the error and set it up anew. */
 futr_status futr_paged_check(const futr_paged* cache, const futr_paged_ws* ws, void* stream);
+
+/* ------------------------------------------- first tokens that stay visible --
+ *
+ * futr_paged_attention with a window and the first `sinks` positions of each
+ * sequence, which every row sees: the row at position p sees the positions j <= p
+ * with j < sinks or j > p - window.  Positions are those of the append: the keys
+ * carry them, and the query its own.  Entries of the page table for pages that lie
+ * wholly between the sinks and every row's window are not read: those pages may
+ * have been given back (futr_pages_free).  window 0: every position is visible and
+ * sinks changes nothing; sinks 0: futr_paged_attention.  Everything else as there. */
+futr_status futr_paged_attention_sinks(const futr_paged* cache, int32_t layer, int32_t batch, const int32_t* pos,
+                                       const int32_t* start, int32_t n_rows, const int32_t* table, int32_t table_ld,
+                                       const void* q, int64_t ld_q, void* out, int64_t ld_out, int32_t dtype,
+                                       float scale, int32_t window, int32_t sinks, const futr_paged_ws* ws,
+                                       void* stream);
+
+/* ------------------------------------------------------------------- beams --
+ *
+ * Choice of the best continuations of each prompt's beams:
+ *   value(w, v) = score[w] + logits[w][v] - log sum_u exp(logits[w][u])
+ * and of a prompt's beams * vocab values the `keep` largest, equal ones by the
+ * lowest (w, v).  logits: [batch * beams][vocab], rows ld elements apart, of the
+ * type dtype (FUTR_DTYPE_F32, _BF16, _F16), aligned to an element; a beam's rows
+ * one after another: row b * beams + w.  scores: fp32 [batch][beams]; a beam whose
+ * score is -inf offers nothing and its logits are not read.  done (int32
+ * [batch][beams], or NULL): a beam with a nonzero entry has ended; it offers one
+ * candidate, the token `end` at its score, and its logits are not read.  A logit
+ * of -inf is no candidate.  A row that is read and holds a NaN or +inf, and a
+ * score that is NaN or +inf, set FUTR_ERR_NOT_FINITE (see futr_beam_check); that
+ * beam offers nothing.
+ *
+ * Outputs [batch][keep], best first: score_out fp32 (the value, rounded once),
+ * parent (the row b * beams + w), token, and done_out (may be NULL): 1 where the
+ * token is `end`.  Where there are fewer candidates than keep, the places left
+ * have score -inf, parent -1, the token `end` (0 if there is none) and done_out 0.
+ * end: -1 if no token ends a beam (done must be NULL then).  stay 1 (keep ==
+ * beams): a beam's best child takes the beam's own place, the others the places
+ * left, in order, so that the caches move as little as they have to.  Outputs
+ * must not overlap inputs, but score_out may be scores and done_out may be done.
+ *
+ * Sums of exponentials are fp32 within a thread's part of a row and fp64 between
+ * parts; logits of a row are compared exactly, values of beams in fp64.  beams
+ * 1..32, keep 1..64, vocab below 2^31.  Capturable in a CUDA graph. */
+#define FUTR_DTYPE_F32  2
+
+typedef struct futr_beam_ws {
+  int32_t rows, keep, ctas, _pad;
+  void* base;
+  uint64_t bytes;
+  uint64_t err_offset, row_offset, rec_offset;
+  uint64_t magic;
+} futr_beam_ws;
+
+/* Workspace of futr_beam_select for up to `rows` rows of logits and `keep`
+ * candidates on the current device (rows 1..65536).  Calls that overlap on the GPU
+ * need a workspace each. */
+futr_status futr_beam_workspace_size(int32_t rows, int32_t keep, size_t* bytes);
+futr_status futr_beam_workspace_init(int32_t rows, int32_t keep, void* mem, size_t mem_bytes, futr_beam_ws* ws,
+                                     void* stream);
+
+futr_status futr_beam_select(const void* logits, int64_t ld, int32_t dtype, int32_t batch, int32_t beams,
+                             int32_t vocab, const float* scores, const int32_t* done, int32_t end, int32_t keep,
+                             int32_t stay, float* score_out, int32_t* parent, int32_t* token, int32_t* done_out,
+                             const futr_beam_ws* ws, void* stream);
+
+/* Compare the guards of `ws`, synchronize `stream` and return (and clear) its
+ * first device error. */
+futr_status futr_beam_check(const futr_beam_ws* ws, void* stream);
+
+/*
+ * The slots of an INT4 cache follow the chosen beams, in place and in all layers:
+ * slot i (of 0 .. batch-1, batch 1..32) takes what slot parent[i] held before the
+ * call, its positions below pos[parent[i]] (whole tiles of 16 positions; what lies
+ * behind is left as it was).  parent: device int32 [batch], a slot below batch, or
+ * -1: the slot becomes empty.  pos (device int32 [batch]): tokens cached in each
+ * slot; it moves with the slots (empty: 0).  A parent outside [-1, batch) or a pos
+ * outside [0, capacity] sets FUTR_ERR_OUT_OF_RANGE in the cache's error word (see
+ * futr_check) and nothing is moved.  Capturable in a CUDA graph.
+ */
+futr_status futr_kv_reorder(const futr_kv* kv, int32_t batch, const int32_t* parent, int32_t* pos, void* stream);
+
+/* ------------------------------------------------------- pages of a cache --
+ *
+ * A pool says which pages of a paged cache are in use, on the device: how many
+ * places of the caller's page tables name each page.  The calls below read and
+ * change page tables (device int32 [batch][table_ld], -1 where a sequence has no
+ * page), so a captured step can take, share and give back pages.  A page that no
+ * place names is free; a call that takes pages takes the lowest free ones, in the
+ * order of sequences and positions, so results do not depend on timing.  page i of
+ * a row holds positions page*i .. page*i + page - 1.  One pool serves one cache,
+ * and its calls follow one another (one stream, or ordered streams).
+ *
+ * A call that finds too few free pages sets FUTR_ERR_NO_PAGES and changes nothing.
+ * A page id outside [0, n_pages) is treated as no page and sets
+ * FUTR_ERR_OUT_OF_RANGE; giving back a page that the pool has free sets
+ * FUTR_ERR_NOT_HELD.  futr_pages_check returns these.  Capturable in CUDA graphs. */
+typedef struct futr_pages {
+  int32_t n_pages, max_seqs;
+  void* base;
+  uint64_t bytes;
+  uint64_t refs_offset;    /* int32 [n_pages]: places that name each page  */
+  uint64_t free_offset;    /* bit p % 32 of word p / 32: page p is free    */
+  uint64_t plan_offset, err_offset;
+  uint64_t magic;
+} futr_pages;
+
+/* Bytes of a pool for n_pages pages and tables of up to max_seqs sequences
+ * (1..1024), and its set-up: every page free. */
+futr_status futr_pages_size(int32_t n_pages, int32_t max_seqs, size_t* bytes);
+futr_status futr_pages_init(int32_t n_pages, int32_t max_seqs, void* mem, size_t mem_bytes, futr_pages* pool,
+                            void* stream);
+
+/* Count the pages that a table made by hand names (for a table that is filled
+ * already; the calls below keep the counts themselves). */
+futr_status futr_pages_hold(const futr_paged* cache, const futr_pages* pool, int32_t batch, const int32_t* table,
+                            int32_t table_ld, void* stream);
+
+/* Take a page for every page without one that the new rows of a call meet: the
+ * positions pos[b] .. pos[b] + n - 1 of each sequence, n = start[b+1] - start[b]
+ * (start NULL: 1), as futr_paged_append will write them.  A sequence whose rows do
+ * not fit the table or the cache's max_pos sets FUTR_ERR_OUT_OF_RANGE and is
+ * skipped. */
+futr_status futr_pages_grow(const futr_paged* cache, const futr_pages* pool, int32_t batch, const int32_t* pos,
+                            const int32_t* start, int32_t* table, int32_t table_ld, void* stream);
+
+/* Give back the pages that no row at position pos[b] or later sees through `window`
+ * and `sinks` (as in futr_paged_attention_sinks; window 0: all positions), and those
+ * at and behind pos[b] that hold no position below it (after refused drafts; pos[b]
+ * 0: the sequence ended, all its pages).  Their places become -1.  (pos below 0 is
+ * taken as 0.) */
+futr_status futr_pages_free(const futr_paged* cache, const futr_pages* pool, int32_t batch, const int32_t* pos,
+                            int32_t* table, int32_t table_ld, int32_t window, int32_t sinks, void* stream);
+
+/*
+ * The sequences of a table follow the chosen beams, in place: row i continues row
+ * parent[i] (device int32 [batch], a row below batch, or -1: the row becomes empty)
+ * and pos[i] becomes pos[parent[i]] (empty: 0).  Pages are shared and counted.  The
+ * page that is partly written (the one of position pos, when pos is no multiple of
+ * the page) and pages taken ahead behind it stay with the parent's first child;
+ * every further child gets a page of its own with a copy of the written positions
+ * and the scales, in all layers.  Needs one free page a copy, beside those that the call itself gives
+ * back.  A parent outside [-1, batch) or a pos outside [0, min(max_pos, table_ld *
+ * page)] of a parent sets FUTR_ERR_OUT_OF_RANGE, and nothing is changed.
+ */
+futr_status futr_pages_fork(const futr_paged* cache, const futr_pages* pool, int32_t batch, const int32_t* parent,
+                            int32_t* pos, int32_t* table, int32_t table_ld, void* stream);
+
+/* Move the pages in use of [lo, hi) to the lowest free pages outside of it, in
+ * order, in all layers, and name them anew in the table, which has to hold every
+ * place that names them.  (lo = pages kept, hi = n_pages: the cache's end becomes
+ * free.)  Too few free pages outside: FUTR_ERR_NO_PAGES, nothing is moved. */
+futr_status futr_pages_compact(const futr_paged* cache, const futr_pages* pool, int32_t batch, int32_t* table,
+                               int32_t table_ld, int32_t lo, int32_t hi, void* stream);
+
+/* Compare the guards of `pool`, synchronize `stream` and return (and clear) its
+ * first device error; n_free (host, may be NULL): the number of free pages. */
+futr_status futr_pages_check(const futr_pages* pool, int32_t* n_free, void* stream);
 
 /* ------------------------------------------------------ mixture of experts -- */
 typedef struct futr_moe_shape {

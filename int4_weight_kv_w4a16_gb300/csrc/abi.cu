@@ -489,7 +489,9 @@ const char* futr_status_string(futr_status s) {
     case FUTR_ERR_NOT_PD: return "dampened Hessian not positive definite";
     case FUTR_ERR_CORRUPT: return "guard words after a workspace or cache region overwritten";
     case FUTR_ERR_BOUNDS: return "device bounds check failed (debug build)";
-    case FUTR_ERR_NOT_FINITE: return "infinity or NaN in a row appended to the paged cache";
+    case FUTR_ERR_NOT_FINITE: return "infinity or NaN in a row appended to the paged cache, or NaN in logits";
+    case FUTR_ERR_NO_PAGES: return "not enough free pages";
+    case FUTR_ERR_NOT_HELD: return "a page table names a page that its pool has free";
     default: return "unknown status";
   }
 }

@@ -60,6 +60,7 @@ struct PagedAttnArgs {
   void* out;
   long long ld_q, ld_out;
   int Hkv, G, window;
+  int sinks, sink_tiles, sink_pages;   // first positions that every row sees; tiles and pages that hold them
   int rows_lo, rows_hi;     // sequences of [rows_lo, rows_hi) rows x G are this launch's
   long long block0;         // (layer's first page) * Hkv: outermost coordinate of the tensor map
   float scale_log2;         // softmax scale * log2(e)

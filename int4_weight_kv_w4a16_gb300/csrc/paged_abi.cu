@@ -220,10 +220,19 @@ futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t
                                  const int32_t* start, int32_t n_rows, const int32_t* table, int32_t table_ld,
                                  const void* q, int64_t ld_q, void* out, int64_t ld_out, int32_t dtype, float scale,
                                  int32_t window, const futr_paged_ws* ws, void* stream) {
+  return futr_paged_attention_sinks(cache, layer, batch, pos, start, n_rows, table, table_ld, q, ld_q, out, ld_out, dtype,
+                                    scale, window, 0, ws, stream);
+}
+
+futr_status futr_paged_attention_sinks(const futr_paged* cache, int32_t layer, int32_t batch, const int32_t* pos,
+                                       const int32_t* start, int32_t n_rows, const int32_t* table, int32_t table_ld,
+                                       const void* q, int64_t ld_q, void* out, int64_t ld_out, int32_t dtype,
+                                       float scale, int32_t window, int32_t sinks, const futr_paged_ws* ws,
+                                       void* stream) {
   return guarded([&]() -> futr_status {
     const futr_status st = check_rows(cache, layer, batch, pos, start, n_rows, table, table_ld, dtype);
     if (st != FUTR_OK) return st;
-    if (!ws_ok(ws) || ws->head_dim != cache->shape.head_dim || window < 0) return FUTR_ERR_INVALID_ARG;
+    if (!ws_ok(ws) || ws->head_dim != cache->shape.head_dim || window < 0 || sinks < 0) return FUTR_ERR_INVALID_ARG;
     if (!(scale >= 0.f && std::isfinite(scale * 1.5f))) return FUTR_ERR_INVALID_ARG;   // times log2(e) below
     if (n_rows == 0) return FUTR_OK;
     const futr_shape& s = cache->shape;
@@ -241,6 +250,11 @@ futr_status futr_paged_attention(const futr_paged* cache, int32_t layer, int32_t
     a.Hkv = s.n_kv_heads;
     a.G = s.n_q_heads / s.n_kv_heads;
     a.window = window < cache->max_pos ? window : 0;   // a window of every position is none
+    if (a.window > 0) {
+      a.sinks = sinks < cache->max_pos ? sinks : cache->max_pos;
+      a.sink_tiles = (a.sinks + 127) / 128;
+      a.sink_pages = (a.sinks + cache->page - 1) / cache->page;
+    }
     a.block0 = (long long)layer * cache->n_pages * s.n_kv_heads;
     const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)s.head_dim);
     a.scale_log2 = (float)(sc * 1.4426950408889634);

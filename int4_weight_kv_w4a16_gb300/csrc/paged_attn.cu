@@ -91,7 +91,8 @@ struct PaItem {
   Walk w;
   Cut cut;
   int active;                    // this CTA has a share
-  int first, count, valid;       // tiles of this CTA's part, rows of the tile
+  int first, count, valid;       // tiles of this CTA's part (the first's number among the item's), rows of the tile
+  int sinks;                     // positions below it are visible to every row behind them
   int written;                   // positions below it exist
   int hi_min, lo_max;            // positions [lo_max, hi_min] are visible to every row
   int hi_max, lo_min;            // positions that some row sees
@@ -174,7 +175,7 @@ struct PaWarp {
     int end[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) end[h] = sc[h].y == -INFINITY ? 0 : it.written;
-    const bool all = pos0 >= it.lo_max && pos0 + 31 <= it.hi_min && end[0] > 0 && end[1] > 0;
+    const bool all = (pos0 >= it.lo_max || pos0 + 31 < it.sinks) && pos0 + 31 <= it.hi_min && end[0] > 0 && end[1] > 0;
     uint32_t bt[2][NT], bb[2][NT];
     bool moved = false;
     float corr[NT][2];
@@ -191,7 +192,7 @@ struct PaWarp {
             float x = fmaf(s[h][nt][2 * r + e], f, sc[h].y);
             if (!all) {
               const int p = pos0 + 16 * h + 8 * r + g, top = it.hi[8 * nt + 2 * t + e];
-              if (p > top || p < top - it.back || p >= end[h]) x = -INFINITY;
+              if (p > top || (p < top - it.back && p >= it.sinks) || p >= end[h]) x = -INFINITY;
             }
             s[h][nt][2 * r + e] = x;
             mx = fmaxf(mx, x);
@@ -466,7 +467,8 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     for (bool more = true; more;) {
       if (tid == 0) {
         const Walk& c = it.w;
-        it.first = c.t.t0 + (int)(c.u - c.item0);
+        it.first = (int)(c.u - c.item0);
+        it.sinks = a.sinks;
         it.count = (int)(min(c.u1, c.item0 + (c.t.t1 - c.t.t0)) - c.u);
         it.valid = min(R, c.n * a.G - c.rt * R);
         it.written = c.p0 + c.n;
@@ -486,21 +488,20 @@ __global__ void __launch_bounds__(kPaThreads, 2)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) aw.qs[nt][e] = s_qs[8 * nt + 2 * t + e];
-      int pos0 = it.first * kPaTile + 32 * warp;
       for (int i = 0; i < count; ++i) {
         if (ok && !pa_wait(&full[slot], phase, a)) {
           ok = false;
           pa_timeout(a);
           *s_dead = 1;
         }
-        if (ok && pos0 <= it.hi_max && pos0 + 31 >= it.lo_min) {
+        const int pos0 = tile_at(a, it.w.t, it.first + i) * kPaTile + 32 * warp;
+        if (ok && pos0 <= it.hi_max && (pos0 + 31 >= it.lo_min || pos0 < it.sinks)) {
           const uint8_t* st = smem + slot * Lay::kStage;
           const uint8_t* ks[2] = {st + koff[0], st + koff[1]};
           const uint8_t* vs[2] = {ks[0] + voff, ks[1] + voff};
           const float4 sc[2] = {s_scale[slot * kPaSub + 2 * warp], s_scale[slot * kPaSub + 2 * warp + 1]};
           aw.tile32(ks, vs, sc, qf, it, pos0);
         }
-        pos0 += kPaTile;
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
         if (++slot == kPaRing) {

@@ -86,7 +86,7 @@ struct TcItem {
   Walk w;
   Cut cut;
   int active;
-  int first, count, valid;       // tiles of this CTA's part, rows of the tile
+  int first, count, valid;       // tiles of this CTA's part (the first's number among the item's), rows of the tile
 };
 
 __device__ __forceinline__ void tc_soft_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kTcSoft) : "memory"); }
@@ -277,12 +277,18 @@ struct TcScale {
   float f0, f1, b0, b1;
 };
 
-// Columns of the chunk of 32 at column c that a row does not see (outside low ..
-// top) to -inf.
-__device__ __forceinline__ void tc_mask(float (&x)[32], int c, int low, int top) {
+// The columns of a tile that a row does not see: behind top, and `hole` columns from
+// `sink` on (between the sinks and its window).
+struct TcSight {
+  int top, sink;
+  uint32_t hole;
+};
+
+// Those of the chunk of 32 at column c to -inf.
+__device__ __forceinline__ void tc_mask(float (&x)[32], int c, const TcSight& v) {
 #pragma unroll
   for (int j = 0; j < 32; ++j)
-    if (c + j > top || c + j < low) x[j] = -INFINITY;
+    if (c + j > v.top || (uint32_t)(c + j - v.sink) < v.hole) x[j] = -INFINITY;
 }
 
 // The largest s f + b of 32 columns (f > 0; -inf where nothing is seen).
@@ -329,7 +335,7 @@ __device__ __forceinline__ TcScale tc_scale_of(const float4* sc, int c, float qf
 // no longer fits the instruction cache); a row's 128 scores held in registers, by a
 // split of the CTA's registers between the roles, 104 where this took 100.
 template <bool kCut>
-__device__ __forceinline__ float tc_row_max(uint32_t ts, const float4* sc, float qf, int low, int top) {
+__device__ __forceinline__ float tc_row_max(uint32_t ts, const float4* sc, float qf, const TcSight& v) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -337,7 +343,7 @@ __device__ __forceinline__ float tc_row_max(uint32_t ts, const float4* sc, float
     tc_ld32(ts + 32 * c, x);
     const TcScale t = tc_scale_of(sc, c, qf);
     tc_wait_ld32(x);
-    if (kCut) tc_mask(x, 32 * c, low, top);
+    if (kCut) tc_mask(x, 32 * c, v);
     mx = fmaxf(mx, tc_max(x, t));
   }
   return mx;
@@ -346,7 +352,8 @@ __device__ __forceinline__ float tc_row_max(uint32_t ts, const float4* sc, float
 // Its weights, over scores that have been read (chunk c's to columns 16 c .. 16 c +
 // 15); returns their sum with each 16 columns times their inverse value scale.
 template <bool kCut>
-__device__ __forceinline__ float tc_row_weights(uint32_t ts, const float4* sc, float qf, float ref, int low, int top) {
+__device__ __forceinline__ float tc_row_weights(uint32_t ts, const float4* sc, float qf, float ref,
+                                                const TcSight& v) {
   float sum = 0.f;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -354,7 +361,7 @@ __device__ __forceinline__ float tc_row_weights(uint32_t ts, const float4* sc, f
     tc_ld32(ts + 32 * c, x);
     const TcScale t = tc_scale_of(sc, c, qf);
     tc_wait_ld32(x);
-    if (kCut) tc_mask(x, 32 * c, low, top);
+    if (kCut) tc_mask(x, 32 * c, v);
     uint32_t h[16];
     float sum0, sum1;
     tc_weights(x, t, ref, h, sum0, sum1);
@@ -373,7 +380,7 @@ struct TcJoin {
 // The bounds of the current part from its walk (one thread).
 __device__ __forceinline__ void tc_set(const PagedAttnArgs& a, TcItem& it) {
   const Walk& c = it.w;
-  it.first = c.t.t0 + (int)(c.u - c.item0);
+  it.first = (int)(c.u - c.item0);
   it.count = (int)(min(c.u1, c.item0 + (c.t.t1 - c.t.t0)) - c.u);
   it.valid = min(kTcRows, c.n * a.G - c.rt * kTcRows);
 }
@@ -557,7 +564,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       uint32_t t = 0, told[2] = {0, 0};   // tiles; arrivals at sfull by half
       while (w.u < w.u1) {
-        const int first = w.t.t0 + (int)(w.u - w.item0);
+        const int first = (int)(w.u - w.item0);
         const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);
         const int nh = min(kTcRows, w.n * a.G - w.rt * kTcRows) > kTcHalf ? 2 : 1;
         for (int i = 0; i < count; ++i, ++t) {
@@ -566,7 +573,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint8_t* st = smem + Lay::kStage + slot * (2 * kPaTile * D);
           const float4 raw = s_raw[slot * kPaSub + (lane & (kPaSub - 1))];
           // what was never written, or lies on a missing page, becomes zeros
-          const int left = w.p0 + w.n - (first + i) * kPaTile;   // written positions from the tile's first
+          const int left = w.p0 + w.n - tile_at(a, w.t, first + i) * kPaTile;   // written positions from the tile's first
           const unsigned gone = __ballot_sync(0xffffffffu, lane < kPaSub && raw.y == -INFINITY);
           const bool plain = left >= kPaTile && gone == 0u;
 #pragma unroll 1
@@ -650,13 +657,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float qf = s_qs[r];   // this warp wrote it
           const int p = it.w.p0 + myrow / a.G, back = a.window > 0 ? a.window - 1 : 0x3fffffff;
           for (int i = 0; i < count; ++i, ++mine) {
-            const int pos0 = (it.first + i) * kPaTile;
+            const int pos0 = tile_at(a, it.w.t, it.first + i) * kPaTile;
             wait(&sfull[half], mine & 1u);
             tc_fence_after();
             const float4* sc = s_scale + ((t + i) & 1) * kPaSub;
-            const int top = p - pos0, low = top - back;   // columns low .. top are visible
+            // columns low .. top are visible, and those below `sink`
+            const int top = p - pos0, low = top - back, sink = max(0, a.sinks - pos0);
+            const TcSight v{top, sink, (uint32_t)max(0, low - sink)};
             const bool cut = __any_sync(0xffffffffu, top < kPaTile - 1 || low > 0);
-            const float mx = cut ? tc_row_max<true>(ts, sc, qf, low, top) : tc_row_max<false>(ts, sc, qf, low, top);
+            const float mx = cut ? tc_row_max<true>(ts, sc, qf, v) : tc_row_max<false>(ts, sc, qf, v);
             // the reference moves when the maximum has outgrown it (or it has none yet)
             const bool grow = mx > M + kRefLag || (M == -INFINITY && mx > M);
             if (__any_sync(0xffffffffu, grow)) {
@@ -679,7 +688,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
             const float ref = M == -INFINITY ? 0.f : M - kRefWeight;
-            L += cut ? tc_row_weights<true>(ts, sc, qf, ref, low, top) : tc_row_weights<false>(ts, sc, qf, ref, low, top);
+            L += cut ? tc_row_weights<true>(ts, sc, qf, ref, v) : tc_row_weights<false>(ts, sc, qf, ref, v);
             tc_wait_st();
             tc_fence_before();
             __syncwarp();

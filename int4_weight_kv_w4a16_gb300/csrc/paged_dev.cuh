@@ -86,29 +86,34 @@ struct Rows {
   int R, pad;
 };
 
-// Row tile rt of a sequence (n rows from position p0, G query heads a kv-head,
-// R rows a tile): its tiles [t0, t1).
+// Row tile rt of a sequence (n rows from position p0, R rows a tile): its tiles, those
+// of the sinks first, then those from the first that its window meets.  The i-th of them,
+// 0 <= i < t1 - t0, is tile i among the sinks', else t0 + i.
 struct TileRange {
   int t0, t1;
 };
-__device__ __forceinline__ TileRange row_tile(int n, int p0, int G, int R, int window, int rt) {
+__device__ __forceinline__ int tile_at(const PagedAttnArgs& a, const TileRange& t, int i) {
+  return i < a.sink_tiles ? i : t.t0 + i;
+}
+__device__ __forceinline__ TileRange row_tile(const PagedAttnArgs& a, int n, int p0, int R, int rt) {
   int first = p0, last = p0;
   if (n > 1) {
-    const int r0 = rt * R, r1 = min(n * G, r0 + R) - 1;
-    first = p0 + r0 / G;
-    last = p0 + r1 / G;
+    const int r0 = rt * R, r1 = min(n * a.G, r0 + R) - 1;
+    first = p0 + r0 / a.G;
+    last = p0 + r1 / a.G;
   }
-  const int lo = window > 0 ? max(0, first - window + 1) : 0;
-  return {lo / kPaTile, last / kPaTile + 1};
+  // (sinks that reach the window's tiles: one run from tile 0)
+  const int lo = a.window > 0 ? max(0, first - a.window + 1) / kPaTile : 0;
+  return {lo - min(lo, a.sink_tiles), last / kPaTile + 1};
 }
 
 // The units of a sequence and kv-head.
-__device__ __forceinline__ long long seq_units(int n, int p0, int G, Rows s, int window) {
+__device__ __forceinline__ long long seq_units(const PagedAttnArgs& a, int n, int p0, Rows s) {
   long long w = 0;
-  const int nrt = (n * G + s.R - 1) / s.R;
+  const int nrt = (n * a.G + s.R - 1) / s.R;
 #pragma unroll 1
   for (int rt = 0; rt < nrt; ++rt) {
-    const TileRange t = row_tile(n, p0, G, s.R, window, rt);
+    const TileRange t = row_tile(a, n, p0, s.R, rt);
     w += s.pad + t.t1 - t.t0;
   }
   return w;
@@ -145,12 +150,12 @@ struct Walk {
     kvh = (int)quot(at, per_head);
     long long rem = at - (long long)kvh * per_head;
     rt = 0;
-    t = row_tile(n, p0, a.G, s.R, a.window, 0);
+    t = row_tile(a, n, p0, s.R, 0);
 #pragma unroll 1
     while (rem >= s.pad + t.t1 - t.t0) {
       rem -= s.pad + t.t1 - t.t0;
       ++rt;
-      t = row_tile(n, p0, a.G, s.R, a.window, rt);
+      t = row_tile(a, n, p0, s.R, rt);
     }
     item0 = base + at - rem + s.pad;
     u = max(u, item0);
@@ -170,10 +175,10 @@ struct Walk {
           ++b;
           my_seq(a, b, row0, n, p0);
         } while (n == 0);   // u < u1: a later sequence has rows
-        per_head = seq_units(n, p0, a.G, s, a.window);
+        per_head = seq_units(a, n, p0, s);
       }
     }
-    t = row_tile(n, p0, a.G, s.R, a.window, rt);
+    t = row_tile(a, n, p0, s.R, rt);
   }
 };
 
@@ -189,7 +194,7 @@ __device__ __forceinline__ bool find_share(const PagedAttnArgs& a, Rows s, int c
     per = 0;
     if (b0 + lane < a.r.batch) {
       if (!my_seq(a, b0 + lane, row0, n, p0) && report) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
-      per = seq_units(n, p0, a.G, s, a.window);
+      per = seq_units(a, n, p0, s);
     }
     incl = per * a.Hkv;
 #pragma unroll 1
@@ -248,19 +253,24 @@ __device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUte
   bool ok = true;
   if (a.withhold && w.u1 == total) return ok;
   while (w.u < w.u1 && ok) {
-    const int first = w.t.t0 + (int)(w.u - w.item0);
+    const int first = (int)(w.u - w.item0);   // the first tile's number among the item's
     const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);
-    const int end = min(w.p0 + w.n, (first + count) * kPaTile);   // positions needed
-    // page ids and scales, 32 pages a round (one per lane), one round ahead
-    const int pg0 = (first * kPaTile) >> plog, pg1 = (end - 1) >> plog;
-    // (pages before the first row's window are not looked at: a program may have
-    // given them back)
+    const int last = tile_at(a, w.t, first + count - 1) * kPaTile;
+    const int end = min(w.p0 + w.n, last + kPaTile);   // positions needed
+    // page ids and scales, 32 pages a round (one per lane), one round ahead; pages are
+    // numbered through the item's tiles
+    const int tlog = 7 - plog;
+    const int pg0 = first << tlog, pg1 = ((first + count - 1) << tlog) + ((end - 1 - last) >> plog);
+    // (pages before the first row's window, behind the sinks, are not looked at: a program
+    // may have given them back)
     const int seen = a.window > 0 ? max(0, w.p0 + w.rt * s.R / a.G - a.window + 1) >> plog : 0;
     const int* tab = a.r.table + (size_t)w.b * a.r.table_ld;
     auto fetch = [&](int pg, int& id, float2& sc) {
-      id = pg >= seen && pg <= pg1 ? tab[pg] : -1;
+      const int at = (tile_at(a, w.t, pg >> tlog) << tlog) + (pg & (ppt - 1));   // its place in the table
+      const bool look = pg <= pg1 && (at >= seen || at < a.sink_pages);
+      id = look ? tab[at] : -1;
       if (id < 0 || id >= a.c.n_pages) {
-        if (pg >= seen && pg <= pg1) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
+        if (look) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
         id = -1;
       }
       sc = make_float2(0.f, 0.f);
@@ -271,7 +281,7 @@ __device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUte
     fetch(base + lane, id, sc);
     if (base + 32 <= pg1) fetch(base + 32 + lane, id_next, sc_next);
     for (int i = 0; i < count && ok; ++i) {
-      const int pos = (first + i) * kPaTile, pg = pos >> plog;
+      const int pg = (first + i) << tlog;
       if (pg >= base + 32) {   // 32 and pg0 are multiples of the pages of a tile: no tile straddles
         base += 32;
         id = id_next;
@@ -290,7 +300,7 @@ __device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUte
       const unsigned mask = __ballot_sync(0xffffffffu, have);
       if (have)
         tma_3d(smem_u32(st + lane * bytes), map, 0, (int)(a.block0 + (long long)zid * a.Hkv + w.kvh), &full[slot]);
-      const int from = (((pos + 16 * (lane & (kPaSub - 1))) >> plog) - base) & 31;   // the page of sub-tile `lane`
+      const int from = (pg + ((16 * (lane & (kPaSub - 1))) >> plog) - base) & 31;   // the page of sub-tile `lane`
       const float kscale = __shfl_sync(0xffffffffu, sc.x, from), vscale = __shfl_sync(0xffffffffu, sc.y, from);
       const int myid = __shfl_sync(0xffffffffu, id, from);
       if (lane < kPaSub) {

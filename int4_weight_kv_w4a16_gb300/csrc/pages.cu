@@ -1,0 +1,468 @@
+// Pages of a paged cache on the device: counts of the places that name each page,
+// a bit per free page, and the calls that take, share, move and give back pages.
+//
+// Whatever threads add to or take from a count commutes, and so does setting and
+// clearing bits of pages that are not the same; a call that takes pages hands out
+// the lowest free ones by rank.  So nothing depends on the order in which threads
+// arrive, and no list of free pages has to be kept in order.
+//
+// grow, fork and compact decide in one CTA (ranks over the free bits: a word a
+// thread, 32768 pages a round) and leave a plan; fork and compact then change the
+// table and copy pages with the whole GPU in a second kernel.
+#include "pages.cuh"
+
+namespace futr {
+
+namespace {
+
+constexpr int kPgThreads = 256;
+constexpr int kPgPlan = 1024, kPgWarps = kPgPlan / 32;   // threads of a deciding CTA
+constexpr int kPgTile = 16384;                           // table entries of a CTA in fork
+
+__device__ __forceinline__ int* plan_from(const PoolView& p) { return p.plan + kPlanHeader; }
+__device__ __forceinline__ int* plan_to(const PoolView& p) { return plan_from(p) + p.n_pages; }
+__device__ __forceinline__ int* plan_slots(const PoolView& p) { return plan_to(p) + p.n_pages; }
+__device__ __forceinline__ int4* plan_seqs(const PoolView& p) {
+  return reinterpret_cast<int4*>(p.plan + kPlanHeader + ((3 * (size_t)p.n_pages + 3) & ~size_t(3)));
+}
+
+// `n` places fewer (n > 0) name page id; the last one frees it.
+__device__ __forceinline__ void release(const PoolView& p, int id, int n) {
+  const int old = atomicSub(&p.refs[id], n);
+  if (old < n) {   // not held that often: as it was
+    atomicAdd(&p.refs[id], n);
+    set_err(p.err, FUTR_ERR_NOT_HELD);
+  } else if (old == n) {
+    atomicOr(&p.free[id >> 5], 1u << (id & 31));
+    atomicAdd(&p.err[2], 1);
+  }
+}
+
+// `n` places more name page id, which some place does already.
+__device__ __forceinline__ void hold(const PoolView& p, int id, int n) {
+  if (atomicAdd(&p.refs[id], n) > 0) return;
+  atomicSub(&p.refs[id], n);
+  set_err(p.err, FUTR_ERR_NOT_HELD);
+}
+
+// An entry of a table as a page id, -1 if there is none (an id out of range counts as none).
+__device__ __forceinline__ int page_of(const PoolView& p, int id) {
+  if (id < 0) return -1;
+  if (id < p.n_pages) return id;
+  set_err(p.err, FUTR_ERR_OUT_OF_RANGE);
+  return -1;
+}
+
+__global__ void pages_init_kernel(const PoolView p) {
+  const int i = blockIdx.x * kPgThreads + threadIdx.x;
+  if (i < p.n_pages) p.refs[i] = 0;
+  if (i < p.words) p.free[i] = i * 32 + 32 <= p.n_pages ? ~0u : (1u << (p.n_pages - i * 32)) - 1;
+  if (i == 0) p.err[2] = p.n_pages;
+}
+
+__global__ void __launch_bounds__(kPgThreads) pages_hold_kernel(const PagesArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const long long n = (long long)a.batch * a.table_ld, step = (long long)gridDim.x * kPgThreads;
+  for (long long i = (long long)blockIdx.x * kPgThreads + threadIdx.x; i < n; i += step) {
+    const int id = page_of(a.p, a.table[i]);
+    if (id >= 0 && atomicAdd(&a.p.refs[id], 1) == 0) {
+      atomicAnd(&a.p.free[id >> 5], ~(1u << (id & 31)));
+      atomicSub(&a.p.err[2], 1);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPgThreads) pages_free_kernel(const PagesArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.y, plog = a.c.page_log2;
+  const int pos = max(0, a.pos[b]);
+  const int end = (int)(((long long)pos + a.c.page - 1) >> plog);   // pages below it hold positions below pos
+  // pages that only a window can hide: behind the sinks, before the first visible position
+  const int s1 = a.window > 0 ? (int)(((long long)a.sinks + a.c.page - 1) >> plog) : 0;
+  const int w0 = a.window > 0 ? max(0, pos - a.window + 1) >> plog : 0;
+  int* row = a.table + (size_t)b * a.table_ld;
+  for (int i = blockIdx.x * kPgThreads + threadIdx.x; i < a.table_ld; i += gridDim.x * kPgThreads) {
+    const int e = row[i];
+    if (e < 0 || (i < end && (i >= w0 || i < s1))) continue;
+    row[i] = -1;
+    const int id = page_of(a.p, e);
+    if (id >= 0) release(a.p, id, 1);
+  }
+}
+
+// ------------------------------------------------------- the deciding CTA --
+
+// Exclusive sum over the CTA's threads, and the total (shared: kPgWarps words).
+__device__ __forceinline__ int scan(int v, int* words, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  __syncthreads();   // the words of the call before have been read
+  if (lane == 31) words[warp] = incl;
+  __syncthreads();
+  const int w = words[lane];
+  int ws = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, ws, o);
+    if (lane >= o) ws += t;
+  }
+  total = __shfl_sync(0xffffffffu, ws, 31);
+  return incl - v + __shfl_sync(0xffffffffu, ws - w, warp);
+}
+
+// The first `want` set bits of words[0 .. n) as numbers into list, in order (mask: bits
+// of a word that count).  Returns how many there were (at most want).
+template <class F>
+__device__ __forceinline__ int list_bits(const F& word, int n, int want, int* list, int* words) {
+  int done = 0;
+  for (int base = 0; base < n && done < want; base += kPgPlan) {
+    const int i = base + threadIdx.x;
+    unsigned w = i < n ? word(i) : 0u;
+    int total;
+    int r = done + scan(__popc(w), words, total);
+    for (; w && r < want; ++r, w &= w - 1) list[r] = i * 32 + __ffs(w) - 1;
+    done += total;
+  }
+  return min(done, want);
+}
+
+// The first `want` free pages into list, with the count `refs`; there are that many.
+__device__ __forceinline__ void take(const PoolView& p, int want, int* list, int* words) {
+  list_bits([&](int i) { return p.free[i]; }, p.words, want, list, words);
+  __syncthreads();
+  for (int k = threadIdx.x; k < want; k += kPgPlan) {
+    const int id = list[k];
+    p.refs[id] = 1;
+    atomicAnd(&p.free[id >> 5], ~(1u << (id & 31)));
+  }
+  if (threadIdx.x == 0) p.err[2] -= want;
+}
+
+// Rows of sequence b in `grow`: its pages [i0, i1) (none: i0 == i1).
+__device__ __forceinline__ void grow_pages(const PagesArgs& a, int b, int& i0, int& i1, bool report) {
+  const long long n = a.start ? (long long)a.start[b + 1] - a.start[b] : 1, p0 = a.pos[b], end = p0 + n;
+  i0 = i1 = 0;
+  if (n == 0) return;
+  if (n < 0 || p0 < 0 || end > a.c.max_pos || end > ((long long)a.table_ld << a.c.page_log2)) {
+    if (report) set_err(a.p.err, FUTR_ERR_OUT_OF_RANGE);
+    return;
+  }
+  i0 = (int)(p0 >> a.c.page_log2);
+  i1 = (int)((end - 1) >> a.c.page_log2) + 1;
+}
+
+__global__ void __launch_bounds__(kPgPlan) pages_grow_kernel(const PagesArgs a) {
+  __shared__ int words[kPgWarps];
+  __shared__ int need[kPagesMaxSeqs];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // what each sequence needs, a warp a sequence
+  for (int b = warp; b < a.batch; b += kPgWarps) {
+    int i0, i1, n = 0;
+    grow_pages(a, b, i0, i1, lane == 0);
+    const int* row = a.table + (size_t)b * a.table_ld;
+    for (int i = i0 + lane; i < i1; i += 32) n += row[i] < 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) need[b] = n;
+  }
+  __syncthreads();
+  int total;
+  const int mine = tid < a.batch ? need[tid] : 0;
+  const int before = scan(mine, words, total);
+  if (total == 0) return;
+  if (total > a.p.err[2]) {
+    if (tid == 0) set_err(a.p.err, FUTR_ERR_NO_PAGES);
+    return;
+  }
+  if (tid < a.batch) need[tid] = before;
+  int* list = plan_to(a.p);
+  __syncthreads();
+  take(a.p, total, list, words);
+  __syncthreads();
+  for (int b = warp; b < a.batch; b += kPgWarps) {
+    int i0, i1, k = need[b];
+    grow_pages(a, b, i0, i1, false);
+    int* row = a.table + (size_t)b * a.table_ld;
+    for (int base = i0; base < i1; base += 32) {
+      const int i = base + lane;
+      const bool none = i < i1 && row[i] < 0;
+      const unsigned votes = __ballot_sync(0xffffffffu, none);
+      if (none) row[i] = list[k + __popc(votes & ((1u << lane) - 1))];
+      k += __popc(votes);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPgPlan) fork_plan_kernel(const PagesArgs a) {
+  __shared__ int words[kPgWarps];
+  __shared__ int first[kPagesMaxSeqs];   // a row's first child
+  __shared__ int oldpos[kPagesMaxSeqs];
+  __shared__ int s_bad;
+  pdl_trigger();
+  pdl_wait();
+  const int i = threadIdx.x;
+  const int most = (int)min((long long)a.c.max_pos, (long long)a.table_ld << a.c.page_log2);
+  if (i == 0) s_bad = 0;
+  int parent = -1;
+  if (i < a.batch) {
+    parent = a.parent[i];
+    first[i] = a.batch;
+    oldpos[i] = a.pos[i];
+  }
+  __syncthreads();
+  int from = -1, at = 0;
+  if (parent >= 0 && parent < a.batch) {
+    atomicMin(&first[parent], i);
+    const int p = oldpos[parent];
+    if (p < 0 || p > most)
+      s_bad = 1;
+    else {
+      at = p >> a.c.page_log2;   // places below it are shared
+      if (p & (a.c.page - 1)) from = page_of(a.p, a.table[(size_t)parent * a.table_ld + at]);
+    }
+  } else if (i < a.batch && parent != -1) {
+    s_bad = 1;
+  }
+  __syncthreads();
+  const bool one = parent >= 0 && !s_bad && first[parent] == i;
+  const bool copy = parent >= 0 && !s_bad && !one && from >= 0;
+  int total;
+  const int k = scan(copy, words, total);
+  const bool ok = !s_bad && total <= a.p.err[2];
+  if (i == 0) {
+    a.p.plan[0] = ok ? total : 0;
+    a.p.plan[1] = ok;
+    if (!ok) set_err(a.p.err, s_bad ? FUTR_ERR_OUT_OF_RANGE : FUTR_ERR_NO_PAGES);
+  }
+  if (!ok) return;
+  int* list = plan_to(a.p);
+  __syncthreads();   // the count of free pages has been read
+  if (total > 0) take(a.p, total, list, words);
+  __syncthreads();
+  if (i < a.batch) {
+    if (copy) {
+      plan_from(a.p)[k] = from;
+      plan_slots(a.p)[k] = oldpos[parent] & (a.c.page - 1);
+    }
+    plan_seqs(a.p)[i] = make_int4(parent, at, copy ? list[k] : -1, one);
+    a.pos[i] = parent >= 0 ? oldpos[parent] : 0;
+  }
+}
+
+// ------------------------------------------------------------------ copies --
+
+// Slots 0 .. n-1 of the keys and values of a page and head, `bytes` each, to another page;
+// a warp.
+__device__ __forceinline__ void copy_rows(const uint8_t* src, uint8_t* dst, int bytes) {
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  uint4* t = reinterpret_cast<uint4*>(dst);
+  const int n = bytes >> 4, lane = threadIdx.x & 31;
+  int i = lane;
+  for (; i + 7 * 32 < n; i += 8 * 32) {
+    uint4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = s[i + 32 * j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[i + 32 * j] = v[j];
+  }
+  for (; i < n; i += 32) t[i] = s[i];
+}
+
+// The plan's copies, a (copy, layer, head, keys or values) a warp (warps `w` of `warps`).
+__device__ __forceinline__ void do_copies(const PagesArgs& a, int w, int warps, bool whole) {
+  const int blocks = 2 * a.c.n_kv;   // of a page in a layer
+  const long long per = (long long)blocks * a.n_layers, n = a.p.plan[0] * per;
+  const int *from = plan_from(a.p), *to = plan_to(a.p), *slots = plan_slots(a.p);
+  for (long long e = w; e < n; e += warps) {
+    const int k = (int)(e / per), r = (int)(e - k * per), layer = r / blocks, h = r - layer * blocks;
+    const size_t src = (size_t)from[k] * blocks + h, dst = (size_t)to[k] * blocks + h;
+    const int block = a.c.page * a.d;
+    uint8_t* codes = a.c.codes + (size_t)layer * a.layer_codes;
+    float* scales = a.c.scales + (size_t)layer * a.layer_scales;
+    copy_rows(codes + src * block, codes + dst * block, whole ? block : slots[k] * a.d);
+    if ((threadIdx.x & 31) == 0) scales[dst] = scales[src];
+  }
+}
+
+// The first blocks change the table, columns [cols * blockIdx.x, ..) of all rows each; the
+// others copy.
+__global__ void __launch_bounds__(kPgThreads) fork_apply_kernel(const PagesArgs a, int cols, int table_ctas) {
+  extern __shared__ int old[];   // [batch][cols]
+  pdl_trigger();
+  pdl_wait();
+  if (!a.p.plan[1]) return;
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= table_ctas) {
+    const int w = ((int)blockIdx.x - table_ctas) * (kPgThreads / 32) + (tid >> 5);
+    do_copies(a, w, ((int)gridDim.x - table_ctas) * (kPgThreads / 32), false);
+    return;
+  }
+  __shared__ int kids[kPagesMaxSeqs], shared[kPagesMaxSeqs];   // a row's children; its first place that is not shared
+  const int c0 = blockIdx.x * cols, n = min(cols, a.table_ld - c0);
+  const int4* seqs = plan_seqs(a.p);
+  for (int i = tid; i < a.batch; i += kPgThreads) kids[i] = 0, shared[i] = 0;
+  for (int e = tid; e < a.batch * cols; e += kPgThreads) {
+    const int i = e / cols, j = e - i * cols;
+    if (j < n) old[e] = a.table[(size_t)i * a.table_ld + c0 + j];
+  }
+  __syncthreads();
+  for (int i = tid; i < a.batch; i += kPgThreads) {
+    const int4 s = seqs[i];
+    if (s.x >= 0) {
+      atomicAdd(&kids[s.x], 1);
+      shared[s.x] = s.y;   // the same for all children
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < a.batch * cols; e += kPgThreads) {
+    const int i = e / cols, j = e - i * cols, c = c0 + j;
+    if (j >= n) continue;
+    // row i's new entry
+    const int4 s = seqs[i];
+    int now = -1;
+    if (s.x >= 0) now = c < s.y || s.w ? old[s.x * cols + j] : c == s.y ? s.z : -1;
+    if (now != old[e]) a.table[(size_t)i * a.table_ld + c] = now;
+    // and what becomes of its old page
+    const int more = (c < shared[i] ? kids[i] : kids[i] > 0) - 1;
+    if (old[e] >= 0 && more != 0) {
+      const int id = page_of(a.p, old[e]);
+      if (id >= 0) {
+        if (more < 0)
+          release(a.p, id, 1);
+        else
+          hold(a.p, id, more);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPgPlan) compact_plan_kernel(const PagesArgs a) {
+  __shared__ int words[kPgWarps];
+  pdl_trigger();
+  pdl_wait();
+  const PoolView& p = a.p;
+  // pages of word i inside [lo, hi)
+  auto inside = [&](int i) {
+    unsigned m = 0;
+    const int b = i * 32;
+    if (a.hi > b && a.lo < b + 32) {
+      m = ~0u;
+      if (a.lo > b) m &= ~0u << (a.lo - b);
+      if (a.hi < b + 32) m &= ~(~0u << (a.hi - b));
+    }
+    return m;
+  };
+  auto valid = [&](int i) { return i * 32 + 32 <= p.n_pages ? ~0u : (1u << (p.n_pages - i * 32)) - 1; };
+  int *from = plan_from(p), *to = plan_to(p), *where = plan_slots(p);
+  const int moves = list_bits([&](int i) { return ~p.free[i] & inside(i) & valid(i); }, p.words, p.n_pages, from, words);
+  const int room = list_bits([&](int i) { return p.free[i] & ~inside(i); }, p.words, moves, to, words);
+  const bool ok = room == moves;
+  if (threadIdx.x == 0) {
+    p.plan[0] = ok ? moves : 0;
+    p.plan[1] = ok;
+    if (!ok) set_err(p.err, FUTR_ERR_NO_PAGES);
+  }
+  if (!ok) return;
+  for (int i = a.lo + threadIdx.x; i < a.hi; i += kPgPlan) where[i] = i;
+  __syncthreads();
+  for (int k = threadIdx.x; k < moves; k += kPgPlan) {
+    const int s = from[k], t = to[k];
+    where[s] = t;
+    p.refs[t] = p.refs[s];
+    p.refs[s] = 0;
+    atomicOr(&p.free[s >> 5], 1u << (s & 31));
+    atomicAnd(&p.free[t >> 5], ~(1u << (t & 31)));
+  }
+}
+
+__global__ void __launch_bounds__(kPgThreads) compact_apply_kernel(const PagesArgs a, int table_ctas) {
+  pdl_trigger();
+  pdl_wait();
+  if (!a.p.plan[1]) return;
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= table_ctas) {
+    const int w = ((int)blockIdx.x - table_ctas) * (kPgThreads / 32) + (tid >> 5);
+    do_copies(a, w, ((int)gridDim.x - table_ctas) * (kPgThreads / 32), true);
+    return;
+  }
+  const int* where = plan_slots(a.p);
+  const long long n = (long long)a.batch * a.table_ld, step = (long long)table_ctas * kPgThreads;
+  for (long long i = (long long)blockIdx.x * kPgThreads + tid; i < n; i += step) {
+    const int id = page_of(a.p, a.table[i]);
+    if (id >= a.lo && id < a.hi && where[id] != id) a.table[i] = where[id];
+  }
+}
+
+template <class F, class... Args>
+cudaError_t pg_launch(F* f, dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, args...);
+}
+
+unsigned blocks_for(long long n, long long most) {
+  const long long b = (n + kPgThreads - 1) / kPgThreads;
+  return (unsigned)(b < most ? b : most);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_init(const PoolView& p, cudaStream_t st) {
+  pages_init_kernel<<<(unsigned)((p.n_pages + kPgThreads - 1) / kPgThreads), kPgThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_hold(const PagesArgs& a, cudaStream_t st) {
+  return pg_launch(pages_hold_kernel, dim3(blocks_for((long long)a.batch * a.table_ld, 1024)), kPgThreads, 0, st, a);
+}
+
+cudaError_t launch_pages_grow(const PagesArgs& a, cudaStream_t st) {
+  return pg_launch(pages_grow_kernel, dim3(1), kPgPlan, 0, st, a);
+}
+
+cudaError_t launch_pages_free(const PagesArgs& a, cudaStream_t st) {
+  return pg_launch(pages_free_kernel, dim3(blocks_for(a.table_ld, 64), (unsigned)a.batch), kPgThreads, 0, st, a);
+}
+
+cudaError_t launch_pages_fork(const PagesArgs& a, int sms, cudaStream_t st) {
+  cudaError_t e = pg_launch(fork_plan_kernel, dim3(1), kPgPlan, 0, st, a);
+  if (e != cudaSuccess) return e;
+  const int most = kPgTile / a.batch, cols = a.table_ld < most ? a.table_ld : most;
+  const int table_ctas = (a.table_ld + cols - 1) / cols;
+  static DeviceOnce configured;
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!configured.done(dev)) {
+    e = cudaFuncSetAttribute(fork_apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgTile * 4);
+    if (e != cudaSuccess) return e;
+    configured.mark(dev);
+  }
+  return pg_launch(fork_apply_kernel, dim3((unsigned)(table_ctas + 4 * sms)), kPgThreads, (size_t)a.batch * cols * 4, st,
+                   a, cols, table_ctas);
+}
+
+cudaError_t launch_pages_compact(const PagesArgs& a, int sms, cudaStream_t st) {
+  const cudaError_t e = pg_launch(compact_plan_kernel, dim3(1), kPgPlan, 0, st, a);
+  if (e != cudaSuccess) return e;
+  const int table_ctas = (int)blocks_for((long long)a.batch * a.table_ld, 64);
+  return pg_launch(compact_apply_kernel, dim3((unsigned)(table_ctas + 4 * sms)), kPgThreads, 0, st, a, table_ctas);
+}
+
+}  // namespace futr

@@ -28,7 +28,10 @@ FUTR_ERR_CORRUPT = 8
 FUTR_ERR_BOUNDS = 9
 FUTR_ERR_NOT_FINITE = 10
 
-FUTR_DTYPE_BF16, FUTR_DTYPE_F16 = range(2)
+FUTR_ERR_NO_PAGES = 11
+FUTR_ERR_NOT_HELD = 12
+
+FUTR_DTYPE_BF16, FUTR_DTYPE_F16, FUTR_DTYPE_F32 = range(3)
 
 FUTR_PROJ_QKV, FUTR_PROJ_O, FUTR_PROJ_GATE, FUTR_PROJ_UP, FUTR_PROJ_DOWN = range(5)
 
@@ -80,6 +83,18 @@ class futr_moe_ws(C.Structure):
                 ("magic", C.c_uint64)]
 
 
+class futr_beam_ws(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("keep", C.c_int32), ("ctas", C.c_int32), ("_pad", C.c_int32),
+                ("base", C.c_void_p), ("bytes", C.c_uint64), ("err_offset", C.c_uint64), ("row_offset", C.c_uint64),
+                ("rec_offset", C.c_uint64), ("magic", C.c_uint64)]
+
+
+class futr_pages(C.Structure):
+    _fields_ = [("n_pages", C.c_int32), ("max_seqs", C.c_int32), ("base", C.c_void_p), ("bytes", C.c_uint64),
+                ("refs_offset", C.c_uint64), ("free_offset", C.c_uint64), ("plan_offset", C.c_uint64),
+                ("err_offset", C.c_uint64), ("magic", C.c_uint64)]
+
+
 class FutrError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -118,7 +133,22 @@ _SIGS = {
     "futr_paged_workspace_init": (I32, [C.POINTER(futr_shape), P, C.c_size_t, C.POINTER(futr_paged_ws), P]),
     "futr_paged_attention": (I32, [P, I32, I32, P, P, I32, P, I32, P, C.c_int64, P, C.c_int64, I32, C.c_float, I32,
                                    P, P]),
+    "futr_paged_attention_sinks": (I32, [P, I32, I32, P, P, I32, P, I32, P, C.c_int64, P, C.c_int64, I32, C.c_float,
+                                         I32, I32, P, P]),
     "futr_paged_check": (I32, [P, P, P]),
+    "futr_beam_workspace_size": (I32, [I32, I32, C.POINTER(C.c_size_t)]),
+    "futr_beam_workspace_init": (I32, [I32, I32, P, C.c_size_t, C.POINTER(futr_beam_ws), P]),
+    "futr_beam_select": (I32, [P, C.c_int64, I32, I32, I32, I32, P, P, I32, I32, I32, P, P, P, P, P, P]),
+    "futr_beam_check": (I32, [P, P]),
+    "futr_kv_reorder": (I32, [P, I32, P, P, P]),
+    "futr_pages_size": (I32, [I32, I32, C.POINTER(C.c_size_t)]),
+    "futr_pages_init": (I32, [I32, I32, P, C.c_size_t, C.POINTER(futr_pages), P]),
+    "futr_pages_hold": (I32, [P, P, I32, P, I32, P]),
+    "futr_pages_grow": (I32, [P, P, I32, P, P, P, I32, P]),
+    "futr_pages_free": (I32, [P, P, I32, P, P, I32, I32, I32, P]),
+    "futr_pages_fork": (I32, [P, P, I32, P, P, P, I32, P]),
+    "futr_pages_compact": (I32, [P, P, I32, P, I32, I32, I32, P]),
+    "futr_pages_check": (I32, [P, C.POINTER(I32), P]),
     "futr_moe_weights_size": (I32, [C.POINTER(futr_moe_shape), C.POINTER(C.c_size_t)]),
     "futr_moe_pack": (I32, [C.POINTER(futr_moe_shape), I32, P, P, P, P, P, C.c_size_t, P]),
     "futr_moe_unpack": (I32, [C.POINTER(futr_moe_shape), P, I32, I32, P, P, P]),
@@ -318,6 +348,7 @@ class _Torch:
         import torch
         self.int32, self.float32, self.bfloat16 = torch.int32, torch.float32, torch.bfloat16
         self.rows = {torch.bfloat16: FUTR_DTYPE_BF16, torch.float16: FUTR_DTYPE_F16}
+        self.logits = dict(self.rows) | {torch.float32: FUTR_DTYPE_F32}
         # (torch.cuda's own functions ask first whether CUDA is set up: tensors on it are at hand here)
         self.device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -428,9 +459,10 @@ def futr_paged_workspace_init(shape, mem, stream=None) -> futr_paged_ws:
     return ws
 
 
-def futr_paged_attention(cache, layer, batch, pos, start, table, q, out, ws, scale=0.0, window=0, stream=None):
+def futr_paged_attention(cache, layer, batch, pos, start, table, q, out, ws, scale=0.0, window=0, stream=None, sinks=0):
     """Attention of the rows q [n_rows, heads, head_dim] over the cache into out
-    (same shape and type); scale 0 is 1/sqrt(head_dim), window 0 is none."""
+    (same shape and type); scale 0 is 1/sqrt(head_dim), window 0 is none, the first
+    `sinks` positions of a sequence are visible through any window."""
     T = _T or _torch()
     device = T.device()
     n = q.shape[0]
@@ -442,9 +474,10 @@ def futr_paged_attention(cache, layer, batch, pos, start, table, q, out, ws, sca
         _elsewhere(ws, "the workspace", device)
     ld_q, ld_out = _row_stride(q, "q", device, rows), _row_stride(out, "out", device, rows)
     p, s, n, t, ld = _paged_rows(T, batch, pos, start, table, n, device)
-    _ok(lib().futr_paged_attention(C.addressof(cache), layer, batch, p, s, n, t, ld, q.data_ptr(), ld_q,
-                                   out.data_ptr(), ld_out, dtype, scale, window, C.addressof(ws),
-                                   T.stream(device) if stream is None else _stream(stream)), "futr_paged_attention")
+    _ok(lib().futr_paged_attention_sinks(C.addressof(cache), layer, batch, p, s, n, t, ld, q.data_ptr(), ld_q,
+                                         out.data_ptr(), ld_out, dtype, scale, window, sinks, C.addressof(ws),
+                                         T.stream(device) if stream is None else _stream(stream)),
+        "futr_paged_attention")
 
 
 def futr_paged_check(cache, ws=None, stream=None) -> int:
@@ -537,6 +570,165 @@ def futr_moe_layer(x, gain, router, blob, resid, y, ws, ids=None, weights=None, 
 def futr_moe_check(ws, stream=None) -> int:
     """Synchronize and return the device status (0 = ok); does not raise."""
     return lib().futr_moe_check(C.byref(ws), _stream(stream))
+
+
+# ----------------------------------------------------------------------------
+# beams
+# ----------------------------------------------------------------------------
+
+def futr_beam_workspace_size(rows, keep) -> int:
+    n = C.c_size_t()
+    _ok(lib().futr_beam_workspace_size(rows, keep, C.byref(n)), "futr_beam_workspace_size")
+    return n.value
+
+
+def futr_beam_workspace_init(rows, keep, mem, stream=None) -> futr_beam_ws:
+    ws = futr_beam_ws()
+    _ok(lib().futr_beam_workspace_init(rows, keep, _ptr(mem), mem.numel() * mem.element_size(), C.byref(ws),
+                                       _stream(stream)), "futr_beam_workspace_init")
+    ws._mem = mem
+    return ws
+
+
+def futr_beam_select(logits, scores, score_out, parent, token, ws, done=None, done_out=None, end=-1, stay=False,
+                     stream=None):
+    """The best continuations of the beams scores [batch, beams] by the logits
+    [batch * beams, vocab] into score_out, parent, token and done_out [batch, keep]."""
+    T = _T or _torch()
+    device = T.device()
+    f32, i32 = T.float32, T.int32
+    shape, kept = scores.shape, score_out.shape
+    if len(shape) != 2 or len(kept) != 2 or kept[0] != shape[0]:
+        raise ValueError(f"scores and score_out must be [batch, beams] and [batch, keep], not {tuple(shape)} and "
+                         f"{tuple(kept)}")
+    batch, beams = shape
+    n = batch * beams
+    dtype = T.logits.get(logits.dtype)
+    if dtype is None:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, not {logits.dtype}")
+    if (logits.dim() != 2 or logits.shape[0] != n or (logits.stride(1) != 1 and logits.shape[1] > 1) or
+            logits.get_device() != device):
+        _bad_tensor(logits, "logits", f"rows ({n}, vocab), a row contiguous,", device)
+    vocab = logits.shape[1]
+    ld = logits.stride(0) if n > 1 else vocab
+    if ws._mem.get_device() != device:
+        _elsewhere(ws, "the workspace", device)
+    _ok(lib().futr_beam_select(logits.data_ptr(), ld, dtype, batch, beams, vocab,
+                               _dense(scores, "scores", f32, shape, device), _dense(done, "done", i32, shape, device),
+                               end, kept[1], int(stay), _dense(score_out, "score_out", f32, kept, device),
+                               _dense(parent, "parent", i32, kept, device), _dense(token, "token", i32, kept, device),
+                               _dense(done_out, "done_out", i32, kept, device), C.addressof(ws),
+                               T.stream(device) if stream is None else _stream(stream)), "futr_beam_select")
+
+
+def futr_beam_check(ws, stream=None) -> int:
+    """Synchronize and return the device status (0 = ok); does not raise."""
+    return lib().futr_beam_check(C.byref(ws), _stream(stream))
+
+
+def futr_kv_reorder(kv, parent, pos, stream=None):
+    """Slot i of the INT4 cache continues slot parent[i] (int32 [batch]); pos [batch] follows."""
+    T = _T or _torch()
+    device = T.device()
+    shape = (parent.shape[0],) if parent.dim() == 1 else (parent.numel(),)
+    if kv._mem.get_device() != device:
+        _elsewhere(kv, "the cache", device)
+    _ok(lib().futr_kv_reorder(C.addressof(kv), shape[0], _dense(parent, "parent", T.int32, shape, device),
+                              _dense(pos, "pos", T.int32, shape, device),
+                              T.stream(device) if stream is None else _stream(stream)), "futr_kv_reorder")
+
+
+# ----------------------------------------------------------------------------
+# pages of a paged cache.  Tables are contiguous int32 tensors [batch, pages] and
+# are changed in place.
+# ----------------------------------------------------------------------------
+
+def futr_pages_size(n_pages, max_seqs) -> int:
+    n = C.c_size_t()
+    _ok(lib().futr_pages_size(n_pages, max_seqs, C.byref(n)), "futr_pages_size")
+    return n.value
+
+
+def futr_pages_init(n_pages, max_seqs, mem, stream=None) -> futr_pages:
+    pool = futr_pages()
+    _ok(lib().futr_pages_init(n_pages, max_seqs, _ptr(mem), mem.numel() * mem.element_size(), C.byref(pool),
+                              _stream(stream)), "futr_pages_init")
+    pool._mem = mem
+    return pool
+
+
+def pages_refs(pool):
+    """How many places of the page tables name each page (int32 [n_pages], a view of the pool)."""
+    import torch
+    return pool._mem[pool.refs_offset:pool.refs_offset + 4 * pool.n_pages].view(torch.int32)
+
+
+def _pages(T, cache, pool, table, device):
+    """The table's rows and places, after the checks that every call on a table shares."""
+    if table.dtype is not T.int32 or table.dim() != 2 or not table.is_contiguous() or table.get_device() != device:
+        _bad_tensor(table, "table", "a contiguous int32 tensor (batch, pages)", device)
+    if cache._mem.get_device() != device:
+        _elsewhere(cache, "the cache", device)
+    if pool._mem.get_device() != device:
+        _elsewhere(pool, "the pool", device)
+    return table.shape
+
+
+def futr_pages_hold(cache, pool, table, stream=None):
+    """Count the pages that a table made by hand names."""
+    T = _T or _torch()
+    device = T.device()
+    batch, ld = _pages(T, cache, pool, table, device)
+    _ok(lib().futr_pages_hold(C.addressof(cache), C.addressof(pool), batch, table.data_ptr(), ld,
+                              T.stream(device) if stream is None else _stream(stream)), "futr_pages_hold")
+
+
+def futr_pages_grow(cache, pool, pos, start, table, stream=None):
+    """Take pages for the new rows of a call (start None: one row per sequence)."""
+    T = _T or _torch()
+    device = T.device()
+    batch, ld = _pages(T, cache, pool, table, device)
+    _ok(lib().futr_pages_grow(C.addressof(cache), C.addressof(pool), batch,
+                              _dense(pos, "pos", T.int32, (batch,), device),
+                              _dense(start, "start", T.int32, (batch + 1,), device), table.data_ptr(), ld,
+                              T.stream(device) if stream is None else _stream(stream)), "futr_pages_grow")
+
+
+def futr_pages_free(cache, pool, pos, table, window=0, sinks=0, stream=None):
+    """Give back the pages that no row at pos or later sees, and those behind pos."""
+    T = _T or _torch()
+    device = T.device()
+    batch, ld = _pages(T, cache, pool, table, device)
+    _ok(lib().futr_pages_free(C.addressof(cache), C.addressof(pool), batch,
+                              _dense(pos, "pos", T.int32, (batch,), device), table.data_ptr(), ld, window, sinks,
+                              T.stream(device) if stream is None else _stream(stream)), "futr_pages_free")
+
+
+def futr_pages_fork(cache, pool, parent, pos, table, stream=None):
+    """Row i of the table continues row parent[i] (-1: empty); pos follows."""
+    T = _T or _torch()
+    device = T.device()
+    batch, ld = _pages(T, cache, pool, table, device)
+    _ok(lib().futr_pages_fork(C.addressof(cache), C.addressof(pool), batch,
+                              _dense(parent, "parent", T.int32, (batch,), device),
+                              _dense(pos, "pos", T.int32, (batch,), device), table.data_ptr(), ld,
+                              T.stream(device) if stream is None else _stream(stream)), "futr_pages_fork")
+
+
+def futr_pages_compact(cache, pool, table, lo, hi=None, stream=None):
+    """Move the pages in use of [lo, hi) (hi None: the end) to the lowest free pages outside of it."""
+    T = _T or _torch()
+    device = T.device()
+    batch, ld = _pages(T, cache, pool, table, device)
+    _ok(lib().futr_pages_compact(C.addressof(cache), C.addressof(pool), batch, table.data_ptr(), ld, lo,
+                                 pool.n_pages if hi is None else hi,
+                                 T.stream(device) if stream is None else _stream(stream)), "futr_pages_compact")
+
+
+def futr_pages_check(pool, stream=None):
+    """Synchronize and return (device status, number of free pages); does not raise."""
+    n = I32()
+    return lib().futr_pages_check(C.byref(pool), C.byref(n), _stream(stream)), n.value
 
 
 # ----------------------------------------------------------------------------
