@@ -518,7 +518,7 @@ typedef struct futr_beam_ws {
   int32_t rows, keep, ctas, _pad;
   void* base;
   uint64_t bytes;
-  uint64_t err_offset, row_offset, rec_offset;
+  uint64_t err_offset, cnt_offset, row_offset, rec_offset;
   uint64_t magic;
 } futr_beam_ws;
 

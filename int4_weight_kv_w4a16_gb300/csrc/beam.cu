@@ -4,23 +4,25 @@
 //
 // L_w is the same for a whole row, so a row's candidates are its `keep` largest
 // logits (equal ones by the lowest token), compared as they are; only those meet the
-// other beams' in fp64.  One pass over the logits:
-//   parts  a CTA takes a part of a row in tiles of 4096, a thread 16 logits of a tile in
-//          registers: running maximum and sum of exponentials per thread, and every logit
-//          that reaches a threshold goes to a list in shared memory.  The threshold starts
-//          at (about) the keep-th largest of the 256 threads' maxima of the first tile: so
-//          many logits reach it at least, and few more.  A list that fills up is cut down
-//          to its keep largest, and the threshold follows.
-//   rows   the parts' sums and lists of a row become one.
-//   beams  the rows' candidates of a prompt, by value.
+// other beams', as sums in two fp32 parts.  One pass over the logits, one kernel:
+//   part   a CTA takes a part of a row in tiles, a thread 64 bytes of a tile in registers
+//          (the next tile's are on their way): running maximum and sum of exponentials per
+//          thread, and every logit that reaches a threshold goes to a list in shared memory.
+//          The threshold starts at (about) the keep-th largest of the threads' maxima of the
+//          first tile: so many logits reach it at least, and few more.  A list that grows is cut
+//          down to its keep largest, and the threshold follows.
+//   row    the CTA that ends a row's last part makes one list and sum of all (where a
+//          prompt's parts are too many for the next step by themselves).
+//   pick   the CTA that ends a prompt's last row: log-sums, then the candidates by value.
 // A list's entries are keys (logit in an order-preserving 32-bit form, then the inverted
-// token), all different, so the order in which threads add to it has no effect.
+// token), all different, so the order in which threads add to it has no effect; sums are
+// added in the order of threads and parts.
 //
-// Selecting the k largest of a list: bisection of the key's value, one count over the
-// CTA a step, until k keys are at or above it.
+// Short lists are put in order by counting, for each entry, those before it; of long ones
+// the k largest are found by bisection, a count over the CTA a step.
 #include <cfloat>
 #include <climits>
-#include <cstring>
+#include <type_traits>
 
 #include "beam.cuh"
 
@@ -29,9 +31,15 @@ namespace futr {
 namespace {
 
 constexpr int kBmThreads = 256, kBmWarps = kBmThreads / 32;
-constexpr int kBmPer = 16;                        // logits of a thread in a tile
-constexpr int kBmTile = kBmThreads * kBmPer;
+constexpr int kBmVecs = 4;                        // 16-byte vectors of a thread in a tile
 constexpr int kBmList = 1024;                     // entries of a part's list
+constexpr int kBmCut = 64;                        // entries of a list that is cut, at least
+constexpr int kBmShort = kBmThreads;              // entries that are put in order by counting
+constexpr int kBmOne = 2048;                      // most candidates of a prompt that are picked from at once
+constexpr int kBmMaxParts = 64;                   // parts of a row
+constexpr int kBmPerSm = 4;                       // CTAs an SM
+constexpr int kBmMaxWaves = 4;                    // parts of all rows, in CTAs that run at once
+constexpr double kBmStart = 1.0;                  // what a part costs beside its tiles, in tiles
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float bm_ex2(float x) {
@@ -50,9 +58,33 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 }
 constexpr uint32_t kLowest = 0x00800000u;   // ordered(-FLT_MAX)
 
-__device__ __forceinline__ unsigned long long ordered64(double x) {
-  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
-  return u ^ ((unsigned long long)((long long)u >> 63) | 0x8000000000000000ull);
+// A sum in two fp32 parts, hi the sum rounded: some 2^-46 of its size (fp64 adds take 16
+// times an fp32 one's time here, and exp and log some 30 of them: 5 of 20 us for one prompt).
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two add(Two x, float y) {
+  const float s = x.hi + y, t = s - x.hi;
+  const float e = (x.hi - (s - t)) + (y - t) + x.lo;   // (the first two terms: what s lost, exactly)
+  const float hi = s + e;
+  return {hi, e - (hi - s)};
+}
+__device__ __forceinline__ Two add(Two x, Two y) { return add(add(x, y.hi), y.lo); }
+
+// Order-preserving form of a value in two parts, and its rounded part.
+__device__ __forceinline__ unsigned long long ordered64(Two x) {
+  return ((unsigned long long)ordered(x.hi) << 32) | ordered(x.lo);
+}
+
+// log x of x.hi >= 2^-100: x.hi = 2^e f with f near 1, whose logarithm is small enough for
+// fp32 (an error of 2^-26 at most, where log x itself, rounded, has 2^-21).
+__device__ __forceinline__ Two log_of(Two x) {
+  constexpr double ln2 = 0.69314718055994530942;
+  constexpr float ln2_hi = (float)ln2, ln2_lo = (float)(ln2 - (double)(float)ln2);
+  const int u = __float_as_int(x.hi), e = (u - __float_as_int(0.75f)) >> 23;
+  const float f = __int_as_float(u - e * (1 << 23)), p = (float)e * ln2_hi;
+  const float rest = fmaf((float)e, ln2_hi, -p) + (float)e * ln2_lo;
+  return add(add(add(Two{p, 0.f}, logf(f)), rest), __fdiv_rn(x.lo, x.hi));
 }
 
 __device__ __forceinline__ unsigned long long make_key(float x, int v) {
@@ -73,92 +105,146 @@ __device__ __forceinline__ int cta_sum(int v, int* words, int turn) {
   return t;
 }
 
-// The value T that exactly k of the CTA's keys reach (at most N a thread, 0 = none), all
-// different; at most k keys: 1 (every key reaches it).  `turn` counts the sums made.
+// The largest and the smallest nonzero of the CTA's values (0 and ~0: there are none).
 template <int N>
-__device__ __forceinline__ unsigned long long select_key(const unsigned long long (&key)[N], int k, int* words,
-                                                         int& turn) {
+__device__ __forceinline__ void cta_range(const unsigned long long (&v)[N], unsigned long long* words,
+                                          unsigned long long& lo, unsigned long long& hi) {
+  lo = ~0ull, hi = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    hi = v[i] > hi ? v[i] : hi;
+    lo = v[i] != 0 && v[i] < lo ? v[i] : lo;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
+    hi = h > hi ? h : hi;
+    lo = l < lo ? l : lo;
+  }
+  __syncthreads();   // the words of the call before have been read
+  if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = hi, words[kBmWarps + (threadIdx.x >> 5)] = lo;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kBmWarps; ++i) {
+    hi = words[i] > hi ? words[i] : hi;
+    lo = words[kBmWarps + i] < lo ? words[kBmWarps + i] : lo;
+  }
+}
+
+// How many of the CTA's values reach t.
+template <int N>
+__device__ __forceinline__ int cta_reach(const unsigned long long (&v)[N], unsigned long long t, int* words, int& turn) {
   int n = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) n += key[i] != 0;
-  if (cta_sum(n, words, turn++) <= k) return 1;
-  // invariant: more than k keys reach lo, fewer than k reach hi
-  unsigned long long lo = 1, hi = ~0ull;
+  for (int i = 0; i < N; ++i) n += v[i] >= t;
+  return cta_sum(n, words, turn++);
+}
+
+// The value that exactly k of the CTA's keys reach, all different (0: none); 1, which all
+// reach, where there are at most k.  `range`: words for cta_range; `turn` counts the sums.
+template <int N>
+__device__ __forceinline__ unsigned long long select_key(const unsigned long long (&v)[N], int k, int* words,
+                                                         unsigned long long* range, int& turn) {
+  unsigned long long lo, hi;
+  cta_range(v, range, lo, hi);
+  if (hi == 0 || cta_reach(v, lo, words, turn) <= k) return 1;
+  ++hi;   // invariant: more than k reach lo, fewer than k reach hi
   while (hi - lo > 1) {
     const unsigned long long mid = lo + ((hi - lo) >> 1);
-    n = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) n += key[i] >= mid;
-    n = cta_sum(n, words, turn++);
+    const int n = cta_reach(v, mid, words, turn);
     if (n == k) return mid;
     if (n > k)
       lo = mid;
     else
       hi = mid;
   }
-  return hi;   // not reached: keys differ, so some value has exactly k above it
+  return hi;
+}
+
+// A value that at least k of the CTA's threads' values reach, and few more (0 where fewer
+// than k are not 0): the k-th largest of the ceil(k / 4) largest of each of the 8 warps.
+// (Counting for each of the 256 values those above took 2.4 us, 3.5 with four CTAs an SM.)
+__device__ __forceinline__ uint32_t reached(uint32_t v, int k, uint32_t* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = (k + 3) >> 2;   // 1 .. 16
+  uint32_t mine = 0;
+  for (int i = 0; i < each; ++i) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, v);
+    if (lane == i) mine = top;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, v == top)) - 1) v = 0;   // of equal values one goes
+  }
+  const int n = each * kBmWarps;
+  if (lane < each) all[warp * each + lane] = mine;
+  __syncthreads();
+  uint32_t low = ~0u;
+  for (int c = lane; c < n; c += 32) {   // every warp by itself
+    const uint32_t t = all[c];
+    int above = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; i += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(all + i);
+      above += (o.x > t) + (o.y > t) + (o.z > t) + (o.w > t);
+    }
+    if (above < k) low = min(low, t);    // the least of those that fewer than k exceed
+  }
+  return __reduce_min_sync(0xffffffffu, low);
 }
 
 template <int kType>
-struct Vec;
-template <>
-struct Vec<FUTR_DTYPE_F32> {
-  using T = float;
-};
-template <>
-struct Vec<FUTR_DTYPE_BF16> {
-  using T = uint16_t;
-};
-template <>
-struct Vec<FUTR_DTYPE_F16> {
-  using T = uint16_t;
-};
+using Logit = std::conditional_t<kType == FUTR_DTYPE_F32, float, uint16_t>;
 
+// Logit i of 16 bytes.
 template <int kType>
-__device__ __forceinline__ float logit_of(typename Vec<kType>::T u) {
+__device__ __forceinline__ float logit_of(const uint32_t (&u)[4], int i) {
   if constexpr (kType == FUTR_DTYPE_F32)
-    return u;
+    return __uint_as_float(u[i]);
   else if constexpr (kType == FUTR_DTYPE_BF16)
-    return __uint_as_float((uint32_t)u << 16);
+    return __uint_as_float(i & 1 ? u[i >> 1] & 0xffff0000u : u[i >> 1] << 16);
   else
-    return __half2float(__ushort_as_half(u));
+    return __half2float(__ushort_as_half((uint16_t)(i & 1 ? u[i >> 1] >> 16 : u[i >> 1] & 0xffffu)));
 }
 
-// The W logits from token W * vec on (vec < v1; -inf behind the row's end): one 16-byte load,
-// or two that a row off such a boundary lies across; single ones at its ends.
+// The logits from token W * vec on (vec < v1; -inf behind the row's end) as they are: one
+// 16-byte load, or two that a row off such a boundary lies across; single ones at its ends.
+// Wherever a row lies, a thread gets the same tokens: equal rows have equal sums.
 template <int kType>
-__device__ __forceinline__ void load_vec(const typename Vec<kType>::T* x, int vec, int v1, int vocab, float* v) {
-  using T = typename Vec<kType>::T;
+__device__ __forceinline__ void load_vec(const Logit<kType>* x, int vec, int v1, int vocab, uint32_t (&u)[4]) {
+  using T = Logit<kType>;
   constexpr int W = 16 / sizeof(T);
+  constexpr uint32_t none = kType == FUTR_DTYPE_F32 ? 0xff800000u : kType == FUTR_DTYPE_BF16 ? 0xff80u : 0xfc00u;
   const long long e = (long long)vec * W;
   const int shift = (int)(reinterpret_cast<uintptr_t>(x) & 15), off = shift / (int)sizeof(T);
-  uint32_t u[9] = {};
   if (vec < v1 && shift == 0 && e + W <= vocab) {
     const uint4 p = __ldcs(reinterpret_cast<const uint4*>(x + e));
     u[0] = p.x, u[1] = p.y, u[2] = p.z, u[3] = p.w;
   } else if (vec < v1 && shift != 0 && e >= off && e - off + 2 * W <= vocab) {
     const uint4* a = reinterpret_cast<const uint4*>(x + e - off);
     const uint4 p = a[0], q = a[1];
-    u[0] = p.x, u[1] = p.y, u[2] = p.z, u[3] = p.w, u[4] = q.x, u[5] = q.y, u[6] = q.z, u[7] = q.w;
+    uint32_t w[9] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w, 0};
     if (shift & 8) {
 #pragma unroll
-      for (int i = 0; i < 6; ++i) u[i] = u[i + 2];
+      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
     }
     if (shift & 4) {
 #pragma unroll
-      for (int i = 0; i < 5; ++i) u[i] = u[i + 1];
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(u[i], u[i + 1], (shift & 3) * 8);
+    for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(w[i], w[i + 1], (shift & 3) * 8);
   } else {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = vec < v1 && e + i < vocab ? logit_of<kType>(x[e + i]) : -INFINITY;
-    return;
-  }
-  T t[W];
-  memcpy(t, u, 16);
+    for (int i = 0; i < 4; ++i) u[i] = 0;
 #pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = logit_of<kType>(t[i]);
+    for (int i = 0; i < W; ++i) {
+      uint32_t t = none;
+      if (vec < v1 && e + i < vocab) {
+        if constexpr (sizeof(T) == 4)
+          t = __float_as_uint(x[e + i]);
+        else
+          t = x[e + i];
+      }
+      u[i * (int)sizeof(T) / 4] |= t << (8 * (i * (int)sizeof(T) % 4));
+    }
+  }
 }
 
 // Rows that are not read: without a finite score, or ended.
@@ -167,378 +253,454 @@ __device__ __forceinline__ bool row_read(const BeamArgs& a, int row) {
   return s >= -FLT_MAX && s <= FLT_MAX && !(a.done && a.done[row] != 0);
 }
 
+// Shared memory of a CTA.
+struct BmShared {
+  union {
+    unsigned long long list[kBmList + 2];   // a part's list
+    ulonglong2 cand[kBmOne];                // pick: candidates, ordered value and place (w, v)
+  };
+  uint4 all[kBeamMaxKeep / 2];   // the warps' largest values: 2 keep, rounded up
+  unsigned long long range[2 * kBmWarps];
+  int words[2 * kBmWarps];
+  int n[3];                   // entries that a tile adds, three tiles in turn
+  int out;
+  unsigned last;
+  Two sum[kBmWarps];
+  float top[kBmWarps];
+  Two lse[kBeamMaxBeams];
+  // the chosen, best first: value, row, token; their places
+  float f[kBeamMaxKeep];
+  int beam[kBeamMaxKeep], token[kBeamMaxKeep], slot[kBeamMaxKeep];
+};
+
+__device__ __forceinline__ unsigned long long* keys_of(uint8_t* rec) {
+  return reinterpret_cast<unsigned long long*>(rec + 16);
+}
+
+__device__ __forceinline__ void put_stats(uint8_t* rec, float M, Two S) {
+  *reinterpret_cast<float4*>(rec) = make_float4(M, S.hi, S.lo, 0.f);
+}
+
+__device__ __forceinline__ Two warp_sum(Two s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    s = add(s, Two{__shfl_down_sync(0xffffffffu, s.hi, o), __shfl_down_sync(0xffffffffu, s.lo, o)});
+  return Two{__shfl_sync(0xffffffffu, s.hi, 0), __shfl_sync(0xffffffffu, s.lo, 0)};
+}
+
+// The entries of the list that reach thr, to the front of it or to a record.
+template <int N>
+__device__ __forceinline__ void put_keys(BmShared& sh, const unsigned long long (&key)[N], unsigned long long thr,
+                                         unsigned long long* to) {
+  __syncthreads();   // the list has been read
+  if (threadIdx.x == 0) sh.out = 0;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < N; ++q)
+    if (key[q] >= thr) to[atomicAdd(&sh.out, 1)] = key[q];
+  __syncthreads();
+}
+
+__device__ __forceinline__ void read_list(const BmShared& sh, int n, unsigned long long (&key)[kBmList / kBmThreads]) {
+#pragma unroll
+  for (int q = 0; q < kBmList / kBmThreads; ++q) {
+    const int p = threadIdx.x + q * kBmThreads;
+    key[q] = p < n ? sh.list[p] : 0;
+  }
+}
+
+// The list's n <= kBmShort entries in order, the K largest of them at `to` (n > K, or all).
+__device__ __forceinline__ void sort_list(BmShared& sh, int n, int K, unsigned long long* to) {
+  const int tid = threadIdx.x;
+  if (tid == 0) sh.list[n] = 0;   // (the count goes by twos)
+  __syncthreads();
+  const unsigned long long key = tid < n ? sh.list[tid] : 0;
+  int rank = 0;
+  if ((tid & ~31) < n) {
+    for (int i = 0; i < n; i += 2) {
+      const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&sh.list[i]);
+      rank += (k2.x > key) + (k2.y > key);
+    }
+  }
+  __syncthreads();   // the list has been read
+  if (tid < n && rank < K) to[rank] = key;
+  __syncthreads();
+}
+
+// A part of a row: its record.
 template <int kType>
-__global__ void __launch_bounds__(kBmThreads) beam_parts_kernel(const BeamArgs a) {
-  using T = typename Vec<kType>::T;
-  constexpr int W = 16 / sizeof(T);       // logits of a 16-byte vector
-  constexpr int NV = kBmPer / W;          // vectors of a thread in a tile
-  __shared__ unsigned long long list[kBmList];
-  __shared__ int words[2 * kBmWarps];
-  __shared__ int s_n[3];                  // entries that a tile adds, three tiles in turn
-  __shared__ float s_m[kBmWarps];
-  __shared__ double s_s[kBmWarps];
-  __shared__ int s_out;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x / a.splits, part = blockIdx.x % a.splits, K = a.keep;
-  pdl_trigger();
-  pdl_wait();
-  if (!row_read(a, row)) return;
-  uint8_t* rec = a.parts + ((size_t)row * a.splits + part) * beam_record(K);
-  // the row in vectors of W logits from its first on, wherever it lies: equal rows have
-  // equal sums
+__device__ __forceinline__ void do_part(const BeamArgs& a, BmShared& sh, int row, int part, uint8_t* rec) {
+  using T = Logit<kType>;
+  constexpr int W = 16 / sizeof(T);            // logits of a vector
+  constexpr int P = kBmVecs * W;               // of a thread in a tile
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.keep;
   const T* x = static_cast<const T*>(a.logits) + (size_t)row * a.ld;
   const int nv = (a.vocab - 1) / W + 1;
   const int v0 = (int)((long long)nv * part / a.splits), v1 = (int)((long long)nv * (part + 1) / a.splits);
-  if (tid < 3) s_n[tid] = 0;
-  if (tid == 0) s_out = 0;
-  __syncthreads();
-  int turn = 0, n = 0, tile = 0;          // sums made, entries of the list, tiles
+  constexpr int kStep = kBmThreads * kBmVecs;
+  const bool aligned = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
+  int turn = 0, n = 0, tile = 0;               // sums made, entries of the list, tiles
+  const int kCut = max(2 * K, kBmCut);         // entries above which the list is cut
   float m = -INFINITY, s = 0.f;
   unsigned long long thr = 1;
-  float thr_x = -FLT_MAX;                 // a logit below it does not reach thr
-  for (int at = v0; at < v1; at += kBmThreads * NV, ++tile) {
-    float v[kBmPer];
+  float thr_x = -FLT_MAX;                      // a logit below it does not reach thr
+  uint32_t u[kBmVecs][4], next[kBmVecs][4];
+  // a tile's logits; one that lies in the row as a whole, on 16-byte boundaries, without checks
+  auto load = [&](int at, uint32_t (&to)[kBmVecs][4]) {
+    if (aligned && at + kStep <= v1 && (long long)(at + kStep) * W <= a.vocab) {
+      const uint4* p = reinterpret_cast<const uint4*>(x) + at + tid;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_vec<kType>(x, at + tid + kBmThreads * j, v1, a.vocab, v + j * W);
-    float top = v[0];
+      for (int j = 0; j < kBmVecs; ++j) {
+        const uint4 q = __ldcs(p + kBmThreads * j);
+        to[j][0] = q.x, to[j][1] = q.y, to[j][2] = q.z, to[j][3] = q.w;
+      }
+    } else {
 #pragma unroll
-    for (int i = 1; i < kBmPer; ++i) top = fmaxf(top, v[i]);
+      for (int j = 0; j < kBmVecs; ++j) load_vec<kType>(x, at + tid + kBmThreads * j, v1, a.vocab, to[j]);
+    }
+  };
+  load(v0, next);
+  if (tid < 3) sh.n[tid] = 0;
+  __syncthreads();
+  for (int at = v0; at < v1; at += kStep, ++tile) {
+#pragma unroll
+    for (int j = 0; j < kBmVecs; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[j][i] = next[j][i];
+    if (at + kStep < v1) load(at + kStep, next);
+    auto logit = [&](int i) { return logit_of<kType>(u[i / W], i % W); };
+    auto token = [&](int i) { return (at + tid + kBmThreads * (i / W)) * W + i % W; };
+    float tops[kBmVecs];
+#pragma unroll
+    for (int j = 0; j < kBmVecs; ++j) {
+      tops[j] = logit(j * W);
+#pragma unroll
+      for (int i = 1; i < W; ++i) tops[j] = fmaxf(tops[j], logit(j * W + i));
+    }
+    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     if (top > m) {
-      s *= bm_ex2((m - top) * kLog2e);    // (the first time 2^-inf = 0)
+      s *= bm_ex2((m - top) * kLog2e);         // (the first time 2^-inf = 0)
       m = top;
     }
     const float ref = m == -INFINITY ? 0.f : m;
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int i = 0; i < kBmPer; i += 2) {
-      s0 += bm_ex2((v[i] - ref) * kLog2e);
-      s1 += bm_ex2((v[i + 1] - ref) * kLog2e);
+    for (int i = 0; i < P; i += 2) {
+      s0 += bm_ex2((logit(i) - ref) * kLog2e);
+      s1 += bm_ex2((logit(i + 1) - ref) * kLog2e);
     }
-    s += s0 + s1;                         // a NaN or +inf in the row makes it a NaN
+    s += s0 + s1;                              // a NaN or +inf in the row makes it a NaN
     if (tile == 0) {
-      // the threshold: K or a few more of the threads' maxima reach it
-      const uint32_t o = ordered(top);
-      uint32_t lo = kLowest, hi = 0xFF7FFFFFu;   // ordered(FLT_MAX)
-      if (cta_sum(o >= lo, words, turn++) > K) {
-        while (lo < hi) {
-          const uint32_t mid = lo + ((hi - lo + 1) >> 1);
-          const int c = cta_sum(o >= mid, words, turn++);
-          if (c >= K) lo = mid; else hi = mid - 1;
-          if (c >= K && c <= K + K / 4) break;
-        }
+      const uint32_t lo = reached(top > -INFINITY ? ordered(top) : 0u, K, reinterpret_cast<uint32_t*>(sh.all));
+      if (lo >= kLowest) {
         thr = (unsigned long long)lo << 32;
         thr_x = unordered(lo);
       }
     }
-    auto token = [&](int i) { return (at + tid + kBmThreads * (i / W)) * W + i % W; };
-    unsigned reach = 0;
+    int* counter = &sh.n[tile % 3];
     if (top >= thr_x) {
 #pragma unroll
-      for (int i = 0; i < kBmPer; ++i) {
-        if (v[i] >= thr_x && make_key(v[i], token(i)) >= thr) reach |= 1u << i;
-      }
+      for (int j = 0; j < kBmVecs; ++j)
+        if (tops[j] >= thr_x) {
+#pragma unroll
+          for (int i = j * W; i < j * W + W; ++i)
+            if (logit(i) >= thr_x) {
+              const unsigned long long key = make_key(logit(i), token(i));
+              if (key >= thr) {
+                const int to = n + atomicAdd(counter, 1);
+                if (to < kBmList) sh.list[to] = key;
+              }
+            }
+        }
     }
-    const int c = __popc(reach);
-    int* counter = &s_n[tile % 3];
-    int to = 0;
-    if (c) to = atomicAdd(counter, c);
     __syncthreads();
     const int more = *counter;
-    if (tid == 0) s_n[(tile + 2) % 3] = 0;   // last read before this tile's barrier, next used two tiles on
+    if (tid == 0) sh.n[(tile + 2) % 3] = 0;    // last read before this tile's barrier, next used two tiles on
     if (n + more <= kBmList) {
-      to += n;
-#pragma unroll
-      for (int i = 0; i < kBmPer; ++i)
-        if (reach >> i & 1)
-          list[to++] = make_key(v[i], token(i));
       n += more;
-    } else {
-      // too many at once: one logit a thread at a time, the list cut down between
-#pragma unroll 1
-      for (int i = -1; i < kBmPer; ++i) {
-        if (i >= 0) {
-          float xi = v[0];
-#pragma unroll
-          for (int q = 1; q < kBmPer; ++q) xi = q == i ? v[q] : xi;
-          const unsigned long long key = (reach >> i & 1) ? make_key(xi, token(i)) : 0;
-          const bool in = key >= thr && key != 0;
-          const unsigned votes = __ballot_sync(0xffffffffu, in);
-          int* w = words + (turn++ & 1) * kBmWarps;
-          if (lane == 0) w[warp] = __popc(votes);
-          __syncthreads();
-          int before = 0, all = 0;
-#pragma unroll
-          for (int q = 0; q < kBmWarps; ++q) {
-            before += q < warp ? w[q] : 0;
-            all += w[q];
-          }
-          if (in) list[n + before + __popc(votes & ((1u << lane) - 1))] = key;
-          n += all;
-        }
-        if (n > kBmList - kBmThreads) {
-          __syncthreads();
+      if (more > 0 && n > kCut && at + kStep < v1) {
+        if (n <= kBmShort) {
+          sort_list(sh, n, K, sh.list);
+          thr = sh.list[K - 1];
+        } else {
           unsigned long long key[kBmList / kBmThreads];
-#pragma unroll
-          for (int q = 0; q < kBmList / kBmThreads; ++q) {
-            const int p = tid + q * kBmThreads;
-            key[q] = p < n ? list[p] : 0;
-          }
-          thr = select_key(key, K, words, turn);
-          thr_x = unordered((uint32_t)(thr >> 32) < kLowest ? kLowest : (uint32_t)(thr >> 32));
-          __syncthreads();   // every key has been read
-          if (tid == 0) s_out = 0;
           __syncthreads();
-#pragma unroll
-          for (int q = 0; q < kBmList / kBmThreads; ++q)
-            if (key[q] >= thr) list[atomicAdd(&s_out, 1)] = key[q];
-          __syncthreads();
-          n = s_out;
+          read_list(sh, n, key);
+          thr = select_key(key, K, sh.words, sh.range, turn);
+          put_keys(sh, key, thr, sh.list);
         }
+        thr_x = unordered((uint32_t)(thr >> 32));
+        n = K;
+      }
+      continue;
+    }
+    // too many at once: what the tile added is dropped, and added a logit a thread at a time,
+    // the list cut down between
+#pragma unroll 1
+    for (int i = -1; i < P; ++i) {
+      if (i >= 0) {
+        float xi = logit(0);
+#pragma unroll
+        for (int q = 1; q < P; ++q) xi = q == i ? logit(q) : xi;
+        const unsigned long long key = xi >= thr_x ? make_key(xi, token(i)) : 0;
+        const bool in = key >= thr;
+        const unsigned votes = __ballot_sync(0xffffffffu, in);
+        int* w = sh.words + (turn++ & 1) * kBmWarps;
+        if (lane == 0) w[warp] = __popc(votes);
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int q = 0; q < kBmWarps; ++q) {
+          before += q < warp ? w[q] : 0;
+          all += w[q];
+        }
+        if (in) sh.list[n + before + __popc(votes & ((1u << lane) - 1))] = key;
+        n += all;
+      }
+      if (n > kBmList - kBmThreads) {
+        __syncthreads();
+        unsigned long long key[kBmList / kBmThreads];
+        read_list(sh, n, key);
+        thr = select_key(key, K, sh.words, sh.range, turn);
+        thr_x = unordered((uint32_t)(thr >> 32) < kLowest ? kLowest : (uint32_t)(thr >> 32));
+        put_keys(sh, key, thr, sh.list);
+        n = sh.out;
       }
     }
   }
   // the part's K largest
   __syncthreads();
-  {
+  if (n <= K) {
+    for (int i = tid; i < K; i += kBmThreads) keys_of(rec)[i] = i < n ? sh.list[i] : 0;
+  } else if (n <= kBmShort) {
+    sort_list(sh, n, K, keys_of(rec));
+  } else {
     unsigned long long key[kBmList / kBmThreads];
-#pragma unroll
-    for (int q = 0; q < kBmList / kBmThreads; ++q) {
-      const int p = tid + q * kBmThreads;
-      key[q] = p < n ? list[p] : 0;
-    }
-    thr = select_key(key, K, words, turn);
-    if (tid == 0) s_out = 0;
-    __syncthreads();
-    unsigned long long* out = reinterpret_cast<unsigned long long*>(rec + 16);
-#pragma unroll
-    for (int q = 0; q < kBmList / kBmThreads; ++q)
-      if (key[q] >= thr) out[atomicAdd(&s_out, 1)] = key[q];
-    __syncthreads();
-    for (int i = s_out + tid; i < K; i += kBmThreads) out[i] = 0;
+    read_list(sh, n, key);
+    put_keys(sh, key, select_key(key, K, sh.words, sh.range, turn), keys_of(rec));
   }
   // its maximum and sum
   float M = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_m[warp] = M;
+  if (lane == 0) sh.top[warp] = M;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kBmWarps; ++i) M = fmaxf(M, s_m[i]);
+  for (int i = 0; i < kBmWarps; ++i) M = fmaxf(M, sh.top[i]);
   // (a thread without a logit has the sum 0, or a NaN)
-  double S = m == -INFINITY ? (double)s : (double)s * (double)bm_ex2((m - M) * kLog2e);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-  if (lane == 0) s_s[warp] = S;
+  Two S{m == -INFINITY ? s : s * bm_ex2((m - M) * kLog2e), 0.f};
+  S = warp_sum(S);
+  if (lane == 0) sh.sum[warp] = S;
   __syncthreads();
-  if (tid == 0) {
-    double sum = 0.0;
-    for (int i = 0; i < kBmWarps; ++i) sum += s_s[i];
-    *reinterpret_cast<float*>(rec) = M;
-    reinterpret_cast<double*>(rec)[1] = sum;
+  if (tid < 32) {
+    S = tid < kBmWarps ? sh.sum[tid] : Two{0.f, 0.f};
+#pragma unroll
+    for (int o = kBmWarps / 2; o > 0; o >>= 1)
+      S = add(S, Two{__shfl_down_sync(0xffffffffu, S.hi, o), __shfl_down_sync(0xffffffffu, S.lo, o)});
+    if (tid == 0) put_stats(rec, M, S);
   }
 }
 
-// A row's parts become one: log-sum, and the K largest keys.  A row with an infinity or
-// NaN has no keys.
-constexpr int kBmMaxKeys = 16;   // keys of a thread: up to 64 parts of 64 keys
+// The maximum and the sum of `n` records (a warp; n up to kBmMaxParts): in all lanes.
+__device__ __forceinline__ void join_sums(const uint8_t* recs, int n, size_t step, float& M, Two& S) {
+  const int lane = threadIdx.x & 31;
+  float m[kBmMaxParts / 32];
+  Two s[kBmMaxParts / 32];
+  M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kBmMaxParts / 32; ++i) {
+    const int p = lane + 32 * i;
+    m[i] = -INFINITY;
+    s[i] = Two{0.f, 0.f};
+    if (p < n) {
+      const float4 r = __ldcg(reinterpret_cast<const float4*>(recs + p * step));
+      m[i] = r.x;
+      s[i] = Two{r.y, r.z};
+    }
+    M = fmaxf(M, m[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  S = Two{0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kBmMaxParts / 32; ++i) {
+    const float w = m[i] == -INFINITY ? 1.f : bm_ex2((m[i] - M) * kLog2e);   // (no logit: 0, or a NaN)
+    S = add(S, Two{s[i].hi * w, fmaf(s[i].hi, w, -(s[i].hi * w)) + s[i].lo * w});
+  }
+  S = warp_sum(S);
+}
 
-__global__ void __launch_bounds__(kBmThreads) beam_rows_kernel(const BeamArgs a) {
-  __shared__ int words[2 * kBmWarps];
-  __shared__ int s_out;
-  __shared__ double s_lse;
-  const int tid = threadIdx.x, row = blockIdx.x, K = a.keep;
-  pdl_trigger();
-  pdl_wait();
-  uint8_t* rec = a.rows + (size_t)row * beam_record(K);
-  unsigned long long* out = reinterpret_cast<unsigned long long*>(rec + 16);
-  if (!row_read(a, row)) {
-    const float sc = a.scores[row];
-    const bool bad = !(sc <= FLT_MAX);   // NaN or +inf
-    const bool ended = !bad && sc >= -FLT_MAX;   // (a finite score that is not read: done)
-    for (int i = tid; i < K; i += kBmThreads) out[i] = i == 0 && ended ? make_key(0.f, a.end) : 0;
-    if (tid == 0) {
-      reinterpret_cast<double*>(rec)[1] = 0.0;
-      if (bad) set_err(a.err, FUTR_ERR_NOT_FINITE);
-    }
-    return;
-  }
-  const uint8_t* parts = a.parts + (size_t)row * a.splits * beam_record(K);
-  if (tid == 0) s_out = 0;
+// A row's parts become one record.
+__device__ __forceinline__ void do_row(const BeamArgs& a, BmShared& sh, int row) {
+  const int tid = threadIdx.x, K = a.keep;
+  const size_t step = beam_record(K);
+  const uint8_t* parts = a.parts + (size_t)row * a.splits * step;
+  uint8_t* rec = a.rows + (size_t)row * step;
   if (tid < 32) {
-    float M = -INFINITY;
-    for (int p = tid; p < a.splits; p += 32) M = fmaxf(M, *reinterpret_cast<const float*>(parts + p * beam_record(K)));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    double S = 0.0;
-    for (int p = tid; p < a.splits; p += 32) {
-      const float m = *reinterpret_cast<const float*>(parts + p * beam_record(K));
-      const double s = reinterpret_cast<const double*>(parts + p * beam_record(K))[1];
-      S += m == -INFINITY ? s : s * exp((double)m - (double)M);   // (no logit: 0, or a NaN)
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-    if (tid == 0) {
-      const bool bad = !(S <= DBL_MAX) || M == INFINITY;
-      if (bad) set_err(a.err, FUTR_ERR_NOT_FINITE);
-      s_lse = bad || M == -INFINITY ? (double)INFINITY : (double)M + log(S);
-    }
+    float M;
+    Two S;
+    join_sums(parts, a.splits, step, M, S);
+    if (tid == 0) put_stats(rec, M, S);
   }
-  __syncthreads();
-  const double lse = s_lse;
-  int turn = 0;
-  unsigned long long key[kBmMaxKeys];
+  constexpr int N = kBmMaxParts * kBeamMaxKeep / kBmThreads;
+  unsigned long long key[N];
 #pragma unroll
-  for (int q = 0; q < kBmMaxKeys; ++q) {
+  for (int q = 0; q < N; ++q) {
     const int i = tid + q * kBmThreads;
     key[q] = 0;
-    if (i < a.splits * K && lse < (double)INFINITY)
-      key[q] = reinterpret_cast<const unsigned long long*>(parts + (size_t)(i / K) * beam_record(K) + 16)[i % K];
+    if (i < a.splits * K)
+      key[q] = __ldcg(reinterpret_cast<const unsigned long long*>(parts + (size_t)(i / K) * step + 16) + i % K);
   }
-  const unsigned long long thr = select_key(key, K, words, turn);
-#pragma unroll
-  for (int q = 0; q < kBmMaxKeys; ++q)
-    if (key[q] >= thr) out[atomicAdd(&s_out, 1)] = key[q];
-  __syncthreads();
-  for (int i = s_out + tid; i < K; i += kBmThreads) out[i] = 0;
-  if (tid == 0) reinterpret_cast<double*>(rec)[1] = lse;
+  int turn = 0;
+  put_keys(sh, key, select_key(key, K, sh.words, sh.range, turn), keys_of(rec));
+  for (int i = sh.out + tid; i < K; i += kBmThreads) keys_of(rec)[i] = 0;
 }
 
-// A prompt's beams: the K best of their candidates, by value, equal ones by (w, v).
-constexpr int kBmCands = kBeamMaxBeams * kBeamMaxKeep / kBmThreads;   // of a thread
+// i / d for i d < 2^32, by ceil(2^32 / d) (0: d is 1).
+__device__ __forceinline__ int quotient(int i, uint32_t by) { return by ? (int)__umulhi((uint32_t)i, by) : i; }
+uint32_t quotient_by(int d) { return d == 1 ? 0 : (uint32_t)(((1ull << 32) + d - 1) / d); }
 
-__global__ void __launch_bounds__(kBmThreads) beam_pick_kernel(const BeamArgs a) {
-  __shared__ int words[2 * kBmWarps];
-  __shared__ int s_out;
-  __shared__ unsigned long long s_val[kBeamMaxKeep];      // the chosen: ordered value, place (w, v), value
-  __shared__ long long s_at[kBeamMaxKeep];
-  __shared__ float s_f[kBeamMaxKeep];
-  __shared__ int s_rank[kBeamMaxKeep];
-  const int tid = threadIdx.x, b = blockIdx.x, W = a.beams, K = a.keep;
-  pdl_trigger();
-  pdl_wait();
-  if (tid == 0) s_out = 0;
-  unsigned long long val[kBmCands];
-  long long at[kBmCands];
-  float f[kBmCands];
+// A prompt's beams: the K best of their candidates, `lists` records a beam.
+__device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, const uint8_t* recs, int lists) {
+  const int tid = threadIdx.x, warp = tid >> 5, W = a.beams, K = a.keep;
+  const size_t step = beam_record(K);
+  recs += (size_t)b * W * lists * step;
+  // the candidates' keys, on their way before the sums are looked at (those of beams that
+  // offer nothing, or have ended, are not used)
+  constexpr int N = kBmOne / kBmThreads;
+  unsigned long long val[N], at[N];
 #pragma unroll
-  for (int q = 0; q < kBmCands; ++q) {
-    const int i = tid + q * kBmThreads, w = i / K;
+  for (int q = 0; q < N; ++q) {
+    const int i = tid + q * kBmThreads, r = quotient(i, a.by_keep);
+    at[q] = 0;
+    if (i < W * lists * K) at[q] = __ldcg(reinterpret_cast<const unsigned long long*>(recs + (size_t)r * step + 16) + i - r * K);
+  }
+  for (int w = warp; w < W; w += kBmWarps) {
+    const int row = b * W + w;
+    const float score = a.scores[row];
+    Two lse{INFINITY, 0.f};      // the beam offers nothing
+    if (!(score <= FLT_MAX)) {   // NaN or +inf
+      if ((tid & 31) == 0) set_err(a.err, FUTR_ERR_NOT_FINITE);
+    } else if (row_read(a, row)) {
+      float M;
+      Two S;
+      join_sums(recs + (size_t)w * lists * step, lists, step, M, S);
+      const bool bad = !(S.hi <= FLT_MAX) || M == INFINITY;
+      if (bad && (tid & 31) == 0) set_err(a.err, FUTR_ERR_NOT_FINITE);
+      if (!bad && M > -INFINITY) lse = add(log_of(S), M);
+    } else if (score >= -FLT_MAX) {
+      lse.hi = -INFINITY;        // ended: one candidate
+    }
+    if ((tid & 31) == 0) sh.lse[w] = lse;
+  }
+  if (tid == 0) sh.out = 0;
+  __syncthreads();
+  // the candidates' ordered values; the first word decides that most are not chosen
+  uint32_t top = 0;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const int i = tid + q * kBmThreads;
     val[q] = 0;
-    if (i < W * K) {
-      const uint8_t* rec = a.rows + ((size_t)b * W + w) * beam_record(K);
-      const unsigned long long key = reinterpret_cast<const unsigned long long*>(rec + 16)[i % K];
-      if (key != 0) {
-        const double v = (double)a.scores[b * W + w] + ((double)key_logit(key) - reinterpret_cast<const double*>(rec)[1]);
-        val[q] = ordered64(v);
-        at[q] = ((long long)w << 32) | (uint32_t)key_token(key);
-        f[q] = (float)v;
+    if (i < W * lists * K) {
+      const int w = quotient(i, lists > 1 ? a.by_beam : a.by_keep);
+      const Two lse = sh.lse[w];
+      const unsigned long long key = at[q];
+      const Two score{a.scores[b * W + w], 0.f};
+      at[q] = (unsigned long long)w << 32;
+      if (lse.hi == -INFINITY) {
+        if (i == w * lists * K) val[q] = ordered64(score);
+        at[q] |= (uint32_t)a.end;
+      } else if (lse.hi < INFINITY && key != 0) {
+        val[q] = ordered64(add(add(add(score, key_logit(key)), -lse.hi), -lse.lo));
+        at[q] |= (uint32_t)key_token(key);
       }
+      top = max(top, (uint32_t)(val[q] >> 32));
     }
   }
-  // the largest value that at least K candidates reach
-  int turn = 0, n = 0;
+  const uint32_t low = reached(top, K, reinterpret_cast<uint32_t*>(sh.all));
 #pragma unroll
-  for (int q = 0; q < kBmCands; ++q) n += val[q] != 0;
-  unsigned long long lo = 1;
-  int left = 0;                 // of those at lo itself, how many are chosen
-  bool all = true;              // every candidate that reaches lo is chosen
-  if (cta_sum(n, words, turn++) > K) {
-    unsigned long long hi = ~0ull;   // fewer than K reach hi
-    int above = 0;                   // that reach hi
-    all = false;
-    while (hi - lo > 1) {
-      const unsigned long long mid = lo + ((hi - lo) >> 1);
-      n = 0;
-#pragma unroll
-      for (int q = 0; q < kBmCands; ++q) n += val[q] >= mid;
-      n = cta_sum(n, words, turn++);
-      if (n >= K) lo = mid; else hi = mid, above = n;
-      if (n == K) {
-        all = true;
-        break;
-      }
-    }
-    left = K - above;
-  }
+  for (int q = 0; q < N; ++q)
+    if (val[q] != 0 && (uint32_t)(val[q] >> 32) >= low) sh.cand[atomicAdd(&sh.out, 1)] = make_ulonglong2(val[q], at[q]);
   __syncthreads();
-  // equal values at the border: the lowest places
-  if (!all) {
-    for (int k = 0; k < left; ++k) {
-      long long best = LLONG_MAX;
-#pragma unroll
-      for (int q = 0; q < kBmCands; ++q)
-        if (val[q] == lo && at[q] < best) best = at[q];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const long long other = __shfl_xor_sync(0xffffffffu, best, o);
-        best = other < best ? other : best;
-      }
-      __shared__ long long s_best[kBmWarps];
-      if ((tid & 31) == 0) s_best[tid >> 5] = best;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kBmWarps; ++i) best = s_best[i] < best ? s_best[i] : best;
-#pragma unroll
-      for (int q = 0; q < kBmCands; ++q)
-        if (val[q] == lo && at[q] == best) {
-          const int to = atomicAdd(&s_out, 1);
-          s_val[to] = lo, s_at[to] = best, s_f[to] = f[q];
-          val[q] = 0;
-        }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int q = 0; q < kBmCands; ++q)
-      if (val[q] == lo) val[q] = 0;
-  }
-#pragma unroll
-  for (int q = 0; q < kBmCands; ++q)
-    if (val[q] >= lo) {
-      const int to = atomicAdd(&s_out, 1);
-      s_val[to] = val[q], s_at[to] = at[q], s_f[to] = f[q];
-    }
-  __syncthreads();
-  const int got = s_out;
-  // their order
-  if (tid < got) {
+  // their order: larger values, then lower places
+  const int n = sh.out, got = min(n, K);
+  for (int c = tid; c < n; c += kBmThreads) {
+    const ulonglong2 my = sh.cand[c];
     int r = 0;
-    for (int i = 0; i < got; ++i)
-      r += s_val[i] > s_val[tid] || (s_val[i] == s_val[tid] && s_at[i] < s_at[tid]);
-    s_rank[r] = tid;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const ulonglong2 t = sh.cand[i];
+      r += (t.x > my.x) | ((t.x == my.x) & (t.y < my.y));
+    }
+    if (r < K) {
+      sh.f[r] = unordered((uint32_t)(my.x >> 32));
+      sh.beam[r] = (int)(my.y >> 32);
+      sh.token[r] = (int)(uint32_t)my.y;
+    }
   }
   __syncthreads();
   // a beam's best child in its place, the others in the places left
-  __shared__ int s_slot[kBeamMaxKeep];
-  if (a.stay && tid == 0) {
-    unsigned taken = 0;
-    for (int i = 0; i < got; ++i) {
-      const unsigned w = 1u << (int)(s_at[s_rank[i]] >> 32);
-      s_slot[i] = taken & w ? -1 : (int)(s_at[s_rank[i]] >> 32);
-      taken |= w;
+  if (a.stay) {
+    if (tid == 0) {
+      unsigned taken = 0;
+      for (int i = 0; i < got; ++i) {
+        const int w = sh.beam[i];
+        sh.slot[i] = taken >> w & 1 ? -1 : w;
+        taken |= 1u << w;
+      }
+      int next = 0;
+      for (int i = 0; i < K; ++i) {
+        if (i < got && sh.slot[i] >= 0) continue;
+        while (taken >> next & 1) ++next;
+        sh.slot[i] = next;
+        taken |= 1u << next;
+      }
     }
-    int next = 0;
-    for (int i = 0; i < K; ++i) {
-      if (i < got && s_slot[i] >= 0) continue;
-      while (taken >> next & 1) ++next;
-      s_slot[i] = next;
-      taken |= 1u << next;
-    }
+    __syncthreads();
   }
-  __syncthreads();
   if (tid < K) {
-    const size_t o = (size_t)b * K + (a.stay ? s_slot[tid] : tid);
+    const size_t o = (size_t)b * K + (a.stay ? sh.slot[tid] : tid);
     if (tid < got) {
-      const int c = s_rank[tid], token = (int)(uint32_t)s_at[c];
-      a.score_out[o] = s_f[c];
-      a.parent[o] = b * W + (int)(s_at[c] >> 32);
-      a.token[o] = token;
-      if (a.done_out) a.done_out[o] = token == a.end;
+      a.score_out[o] = sh.f[tid];
+      a.parent[o] = b * W + sh.beam[tid];
+      a.token[o] = sh.token[tid];
+      if (a.done_out) a.done_out[o] = sh.token[tid] == a.end;
     } else {
       a.score_out[o] = -INFINITY;
       a.parent[o] = -1;
       a.token[o] = a.end < 0 ? 0 : a.end;
       if (a.done_out) a.done_out[o] = 0;
     }
+  }
+}
+
+// True in the CTA that arrives last of `n` at a counter, which starts over; what the
+// others wrote before is there.
+__device__ __forceinline__ bool arrive_last(BmShared& sh, unsigned* counter, unsigned n) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sh.last = atom_add_acq_rel_gpu(counter, 1u) == n - 1;
+    if (sh.last) *counter = 0u;
+  }
+  __syncthreads();
+  return sh.last != 0;
+}
+
+template <int kType>
+__global__ void __launch_bounds__(kBmThreads, 4) beam_kernel(const BeamArgs a) {
+  __shared__ BmShared sh;
+  pdl_trigger();
+  pdl_wait();
+  const int row = blockIdx.x / a.splits, part = blockIdx.x % a.splits, b = row / a.beams;
+  if (row_read(a, row)) do_part<kType>(a, sh, row, part, a.parts + (size_t)blockIdx.x * beam_record(a.keep));
+  if (a.by_row) {
+    if (!arrive_last(sh, a.cnt + a.batch + row, (unsigned)a.splits)) return;
+    if (row_read(a, row)) do_row(a, sh, row);
+    if (!arrive_last(sh, a.cnt + b, (unsigned)a.beams)) return;
+    do_pick(a, sh, b, a.rows, 1);
+  } else {
+    if (!arrive_last(sh, a.cnt + b, (unsigned)(a.beams * a.splits))) return;
+    do_pick(a, sh, b, a.parts, a.splits);
   }
 }
 
@@ -558,24 +720,29 @@ cudaError_t bm_launch(F* f, unsigned grid, const BeamArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-int beam_part_ctas(int sms) { return 4 * sms; }
+int beam_part_ctas(int sms) { return kBmPerSm * kBmMaxWaves * sms; }
 
 cudaError_t launch_beam_select(const BeamArgs& args, int dtype, int sms, cudaStream_t st) {
   BeamArgs a = args;
-  const int rows = a.batch * a.beams;
-  // parts: as many CTAs as run at once, no part below a tile, 64 at most (the rows kernel's keys)
-  int splits = beam_part_ctas(sms) / rows;
-  const int tiles = (a.vocab + kBmTile - 1) / kBmTile;
-  splits = splits < tiles ? splits : tiles;
-  a.splits = splits < 1 ? 1 : splits > 64 ? 64 : splits;
+  const long long rows = (long long)a.batch * a.beams, slots = (long long)kBmPerSm * sms;
+  // parts of a row: those that end soonest, in tiles; a part costs about kBmStart more
+  const int per = kBmThreads * kBmVecs * (dtype == FUTR_DTYPE_F32 ? 4 : 8), tiles = (a.vocab - 1) / per + 1;
+  double best = 1e30;
+  a.splits = 1;
+  for (int s = 1; s <= kBmMaxParts && s <= tiles && (s == 1 || rows * s <= beam_part_ctas(sms)); ++s) {
+    const double cost = (double)((rows * s + slots - 1) / slots) * ((double)tiles / s + kBmStart);
+    if (cost < best * 0.98) {
+      best = cost;
+      a.splits = s;
+    }
+  }
+  a.by_row = a.beams * a.splits * a.keep > kBmOne;
+  a.by_keep = quotient_by(a.keep);
+  a.by_beam = quotient_by(a.keep * a.splits);
   const unsigned grid = (unsigned)(rows * a.splits);
-  cudaError_t e = dtype == FUTR_DTYPE_F32    ? bm_launch(beam_parts_kernel<FUTR_DTYPE_F32>, grid, a, st)
-                  : dtype == FUTR_DTYPE_BF16 ? bm_launch(beam_parts_kernel<FUTR_DTYPE_BF16>, grid, a, st)
-                                             : bm_launch(beam_parts_kernel<FUTR_DTYPE_F16>, grid, a, st);
-  if (e != cudaSuccess) return e;
-  e = bm_launch(beam_rows_kernel, (unsigned)rows, a, st);
-  if (e != cudaSuccess) return e;
-  return bm_launch(beam_pick_kernel, (unsigned)a.batch, a, st);
+  return dtype == FUTR_DTYPE_F32    ? bm_launch(beam_kernel<FUTR_DTYPE_F32>, grid, a, st)
+         : dtype == FUTR_DTYPE_BF16 ? bm_launch(beam_kernel<FUTR_DTYPE_BF16>, grid, a, st)
+                                    : bm_launch(beam_kernel<FUTR_DTYPE_F16>, grid, a, st);
 }
 
 }  // namespace futr

@@ -20,12 +20,15 @@ struct BeamArgs {
   int* err;                  // the workspace's error words
   uint8_t* rows;             // [rows] row records
   uint8_t* parts;            // [rows][splits] part records
+  unsigned* cnt;             // arrival counters: [batch] prompts, [rows] rows
   int splits;                // parts of a row
+  uint32_t by_keep, by_beam; // for quotients by keep and by keep * splits
+  int by_row;                // a row's parts are made one before the prompt's beams meet
 };
 
-// A record: statistics (part: maximum in fp32, sum in fp64; row: log-sum in fp64 in the
-// sum's place), then `keep` keys.
-__host__ __device__ inline size_t beam_record(int keep) { return 16 + 8 * (size_t)keep; }
+// A record of a part or a row: maximum and sum (in two parts), 16 bytes; then `keep` keys.
+// (A multiple of 16: the statistics are one access.)
+__host__ __device__ inline size_t beam_record(int keep) { return 16 + 16 * (((size_t)keep + 1) / 2); }
 
 int beam_part_ctas(int sms);   // parts of all rows together, where there are fewer rows than that
 cudaError_t launch_beam_select(const BeamArgs& a, int dtype, int sms, cudaStream_t st);

@@ -55,14 +55,15 @@ futr_status read_errors(void* base, const uint64_t* starts, int guards, int* err
 // ------------------------------------------------------------------- beams --
 
 struct BeamLayout {
-  uint64_t err, rows, recs, total;
+  uint64_t err, cnt, rows, recs, total;
 };
 
 BeamLayout beam_layout(int rows, int keep, int ctas) {
   BeamLayout L{};
   const uint64_t parts = rows > ctas ? rows : ctas;
   L.err = 0;
-  L.rows = host::region_after(0, 16);
+  L.cnt = host::region_after(0, 16);
+  L.rows = host::region_after(L.cnt, 2 * (uint64_t)rows * 4);
   L.recs = host::region_after(L.rows, (uint64_t)rows * beam_record(keep));
   L.total = host::region_after(L.recs, parts * beam_record(keep));
   return L;
@@ -71,9 +72,10 @@ BeamLayout beam_layout(int rows, int keep, int ctas) {
 bool beam_ok(const futr_beam_ws* w) { return w && w->magic == kBeamWsMagic && w->base; }
 
 void beam_guards(const futr_beam_ws& w, uint64_t* g) {
-  g[0] = w.row_offset;
-  g[1] = w.rec_offset;
-  g[2] = w.bytes;
+  g[0] = w.cnt_offset;
+  g[1] = w.row_offset;
+  g[2] = w.rec_offset;
+  g[3] = w.bytes;
 }
 
 // ------------------------------------------------------------------- pages --
@@ -171,14 +173,16 @@ futr_status futr_beam_workspace_init(int32_t rows, int32_t keep, void* mem, size
     w.base = mem;
     w.bytes = L.total;
     w.err_offset = L.err;
+    w.cnt_offset = L.cnt;
     w.row_offset = L.rows;
     w.rec_offset = L.recs;
     w.magic = kBeamWsMagic;
     const cudaStream_t s = as_stream(stream);
-    if (cudaMemsetAsync(mem, 0, L.total, s) != cudaSuccess) return FUTR_ERR_CUDA;
-    uint64_t g[3];
+    // error word and counters start at zero
+    if (cudaMemsetAsync(mem, 0, L.rows, s) != cudaSuccess) return FUTR_ERR_CUDA;
+    uint64_t g[4];
     beam_guards(w, g);
-    if (host::fill_guards_before(mem, g, 3, s) != cudaSuccess) return FUTR_ERR_CUDA;
+    if (host::fill_guards_before(mem, g, 4, s) != cudaSuccess) return FUTR_ERR_CUDA;
     *ws = w;
     return FUTR_OK;
   });
@@ -218,6 +222,7 @@ futr_status futr_beam_select(const void* logits, int64_t ld, int32_t dtype, int3
     a.token = token;
     a.done_out = done_out;
     a.err = at<int>(ws->base, ws->err_offset);
+    a.cnt = at<unsigned>(ws->base, ws->cnt_offset);
     a.rows = at<uint8_t>(ws->base, ws->row_offset);
     a.parts = at<uint8_t>(ws->base, ws->rec_offset);
     return status_of(launch_beam_select(a, dtype, sms, as_stream(stream)));
@@ -227,10 +232,10 @@ futr_status futr_beam_select(const void* logits, int64_t ld, int32_t dtype, int3
 futr_status futr_beam_check(const futr_beam_ws* ws, void* stream) {
   return guarded([&]() -> futr_status {
     if (!beam_ok(ws)) return FUTR_ERR_INVALID_ARG;
-    uint64_t g[3];
+    uint64_t g[4];
     beam_guards(*ws, g);
     int word = 0;
-    return read_errors(ws->base, g, 3, at<int>(ws->base, ws->err_offset), &word, 1, as_stream(stream));
+    return read_errors(ws->base, g, 4, at<int>(ws->base, ws->err_offset), &word, 1, as_stream(stream));
   });
 }
 

@@ -59,7 +59,8 @@ constexpr int kPaRows = 8 * NT;
 // An item's start and join count as three tiles in the cut.  With 0, 2, 3, 4 and 6: 32
 // ragged sequences 36.8, 33.3, 33.3, 33.8, 35.3 us; four long ones 53.8, 52.0, 51.2, 51.2,
 // 51.5; drafted tokens (D = 64) 13.2, 11.5, 10.4, 10.5, 11.0.
-constexpr Rows kPaWork{kPaRows, 3};
+template <bool kSinks>
+constexpr Rows kPaWork{kPaRows, 3, kSinks};
 
 template <int D>
 struct PaLayout {
@@ -91,8 +92,7 @@ struct PaItem {
   Walk w;
   Cut cut;
   int active;                    // this CTA has a share
-  int first, count, valid;       // tiles of this CTA's part (the first's number among the item's), rows of the tile
-  int sinks;                     // positions below it are visible to every row behind them
+  int first, count, valid;       // tiles of this CTA's part (from number `first` on), rows of the tile
   int written;                   // positions below it exist
   int hi_min, lo_max;            // positions [lo_max, hi_min] are visible to every row
   int hi_max, lo_min;            // positions that some row sees
@@ -126,8 +126,9 @@ struct PaWarp {
   // log2 and inverse of the value scale); qf: the query fragments; positions
   // below it.written exist.  Two halves at a time: their products are
   // independent chains, and they share one maximum.
+  template <bool kSinks>
   __device__ __forceinline__ void tile32(const uint8_t* const (&ks)[2], const uint8_t* const (&vs)[2],
-                                         const float4 (&sc)[2], const __half* qf, const PaItem& it, int pos0) {
+                                         const float4 (&sc)[2], const __half* qf, const PaItem& it, int pos0, int sinks) {
     constexpr int CH = D / 64;   // 16-byte chunks of a lane's key dims
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int swz = D == 128 ? g : (g >> 1) & 3;   // rows g and g + 8 share it
@@ -175,7 +176,7 @@ struct PaWarp {
     int end[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) end[h] = sc[h].y == -INFINITY ? 0 : it.written;
-    const bool all = (pos0 >= it.lo_max || pos0 + 31 < it.sinks) && pos0 + 31 <= it.hi_min && end[0] > 0 && end[1] > 0;
+    const bool all = (pos0 >= it.lo_max || (kSinks && pos0 + 31 < sinks)) && pos0 + 31 <= it.hi_min && end[0] > 0 && end[1] > 0;
     uint32_t bt[2][NT], bb[2][NT];
     bool moved = false;
     float corr[NT][2];
@@ -192,7 +193,7 @@ struct PaWarp {
             float x = fmaf(s[h][nt][2 * r + e], f, sc[h].y);
             if (!all) {
               const int p = pos0 + 16 * h + 8 * r + g, top = it.hi[8 * nt + 2 * t + e];
-              if (p > top || (p < top - it.back && p >= it.sinks) || p >= end[h]) x = -INFINITY;
+              if (p > top || (p < top - it.back && !(kSinks && p < sinks)) || p >= end[h]) x = -INFINITY;
             }
             s[h][nt][2 * r + e] = x;
             mx = fmaxf(mx, x);
@@ -387,7 +388,7 @@ __device__ __forceinline__ void sum_records(const float* r0, const float* rn, in
   }
 }
 
-template <int D, bool kHalf>
+template <int D, bool kHalf, bool kSinks>
 __global__ void __launch_bounds__(kPaThreads, 2)
     paged_attn_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap map) {
   using Lay = PaLayout<D>;
@@ -428,9 +429,9 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     // ---------------------------------------------------------- producer --
     Walk w;
     Cut cut;
-    if (!find_share(a, kPaWork, cta, gridDim.x, w, cut, false)) return;
+    if (!find_share(a, kPaWork<kSinks>, cta, gridDim.x, w, cut, false)) return;
     int issued = 0;
-    const bool ok = produce_tiles<D>(a, &map, kPaWork, w, smem, s_scale, full, empty, kPaRing, cut.total, issued);
+    const bool ok = produce_tiles<D>(a, &map, kPaWork<kSinks>, w, smem, s_scale, full, empty, kPaRing, cut.total, issued);
     if (!ok) {
       pa_timeout(a);
       *s_dead = 1;
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     if (warp == 0) {
       Walk w;
       Cut cut;
-      const bool active = find_share(a, kPaWork, cta, gridDim.x, w, cut, cta == 0);
+      const bool active = find_share(a, kPaWork<kSinks>, cta, gridDim.x, w, cut, cta == 0);
       if (lane == 0) {
         it.w = w;
         it.cut = cut;
@@ -467,8 +468,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     for (bool more = true; more;) {
       if (tid == 0) {
         const Walk& c = it.w;
-        it.first = (int)(c.u - c.item0);
-        it.sinks = a.sinks;
+        it.first = first_number(kPaWork<kSinks>, c.t) + (int)(c.u - c.item0);
         it.count = (int)(min(c.u1, c.item0 + (c.t.t1 - c.t.t0)) - c.u);
         it.valid = min(R, c.n * a.G - c.rt * R);
         it.written = c.p0 + c.n;
@@ -488,19 +488,20 @@ __global__ void __launch_bounds__(kPaThreads, 2)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) aw.qs[nt][e] = s_qs[8 * nt + 2 * t + e];
-      for (int i = 0; i < count; ++i) {
+      int pos0 = it.first * kPaTile + 32 * warp;
+      for (int i = 0; i < count; ++i, pos0 += kPaTile) {
         if (ok && !pa_wait(&full[slot], phase, a)) {
           ok = false;
           pa_timeout(a);
           *s_dead = 1;
         }
-        const int pos0 = tile_at(a, it.w.t, it.first + i) * kPaTile + 32 * warp;
-        if (ok && pos0 <= it.hi_max && (pos0 + 31 >= it.lo_min || pos0 < it.sinks)) {
+        if (kSinks) pos0 = tile_of(a, kPaWork<kSinks>, it.w.t, it.first + i) * kPaTile + 32 * warp;
+        if (ok && pos0 <= it.hi_max && (pos0 + 31 >= it.lo_min || (kSinks && pos0 < a.sinks))) {
           const uint8_t* st = smem + slot * Lay::kStage;
           const uint8_t* ks[2] = {st + koff[0], st + koff[1]};
           const uint8_t* vs[2] = {ks[0] + voff, ks[1] + voff};
           const float4 sc[2] = {s_scale[slot * kPaSub + 2 * warp], s_scale[slot * kPaSub + 2 * warp + 1]};
-          aw.tile32(ks, vs, sc, qf, it, pos0);
+          aw.template tile32<kSinks>(ks, vs, sc, qf, it, pos0, a.sinks);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
@@ -603,12 +604,12 @@ __global__ void __launch_bounds__(kPaThreads, 2)
                                     8 * q) = u;
         }
       }
-      more = c.u + count + kPaWork.pad < c.u1;
+      more = c.u + count + kPaWork<kSinks>.pad < c.u1;
       if (more) {
         pa_sync();   // the sums, the query fragments and the item are free again
         if (tid == 0) {
           it.w.u += count;
-          it.w.next_item(a, kPaWork);
+          it.w.next_item(a, kPaWork<kSinks>);
         }
       }
     }
@@ -617,19 +618,19 @@ __global__ void __launch_bounds__(kPaThreads, 2)
   if (*s_dead && tid == 0) drain_ring(full, kPaRing, *s_issued);
 }
 
-template <int D, bool kHalf>
+template <int D>
 size_t pa_smem() {
   return (size_t)PaLayout<D>::kBytes + 1024;
 }
 
-template <int D, bool kHalf>
+template <int D, bool kHalf, bool kSinks>
 cudaError_t pa_configure(int dev) {
   static DeviceOnce configured;
   if (configured.done(dev)) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)pa_smem<D, kHalf>());
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, kHalf, kSinks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)pa_smem<D>());
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(paged_attn_kernel<D, kHalf>, cudaFuncAttributePreferredSharedMemoryCarveout,
+  e = cudaFuncSetAttribute(paged_attn_kernel<D, kHalf, kSinks>, cudaFuncAttributePreferredSharedMemoryCarveout,
                            cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   configured.mark(dev);
@@ -638,12 +639,12 @@ cudaError_t pa_configure(int dev) {
 
 constexpr int kPaMaxPerSm = 2;   // CTAs an SM that any variant is launched with at most
 
-template <int D, bool kHalf>
+template <int D, bool kHalf, bool kSinks>
 int pa_per_sm(int dev) {
-  return remembered(occ_key(dev, D, kHalf, 0), [&]() {
+  return remembered(occ_key(dev, D, kHalf + 2 * kSinks, 0), [&]() {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attn_kernel<D, kHalf>, kPaThreads,
-                                                      pa_smem<D, kHalf>()) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attn_kernel<D, kHalf, kSinks>, kPaThreads,
+                                                      pa_smem<D>()) != cudaSuccess ||
         n < 1) {
       cudaGetLastError();
       return 1;
@@ -660,24 +661,30 @@ int sm_count(int dev) {
   });
 }
 
-template <int D, bool kHalf>
+template <int D, bool kHalf, bool kSinks>
 cudaError_t pa_launch(const PagedAttnArgs& a, const CUtensorMap& map, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = pa_configure<D, kHalf>(dev);
+  e = pa_configure<D, kHalf, kSinks>(dev);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(sm_count(dev) * pa_per_sm<D, kHalf>(dev)));
+  cfg.gridDim = dim3((unsigned)(sm_count(dev) * pa_per_sm<D, kHalf, kSinks>(dev)));
   cfg.blockDim = dim3(kPaThreads);
-  cfg.dynamicSmemBytes = pa_smem<D, kHalf>();
+  cfg.dynamicSmemBytes = pa_smem<D>();
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, kHalf>, a, map);
+  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, kHalf, kSinks>, a, map);
+}
+
+template <bool kSinks>
+cudaError_t pa_launch_any(const PagedAttnArgs& a, const CUtensorMap& map, int d, bool half, cudaStream_t st) {
+  if (d == 128) return half ? pa_launch<128, true, kSinks>(a, map, st) : pa_launch<128, false, kSinks>(a, map, st);
+  return half ? pa_launch<64, true, kSinks>(a, map, st) : pa_launch<64, false, kSinks>(a, map, st);
 }
 
 // Rows (tokens x query heads of a kv-head) a sequence, on average, from which on the
@@ -739,8 +746,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& args, const CUtensorMap&
     a.rows_hi = least;
   }
   const bool half = dtype == FUTR_DTYPE_F16;
-  if (d == 128) return half ? pa_launch<128, true>(a, map, st) : pa_launch<128, false>(a, map, st);
-  return half ? pa_launch<64, true>(a, map, st) : pa_launch<64, false>(a, map, st);
+  return a.sinks > 0 ? pa_launch_any<true>(a, map, d, half, st) : pa_launch_any<false>(a, map, d, half, st);
 }
 
 // Codes as [blocks][2 page][d] bytes, a block per (page, kv-head), copied whole;

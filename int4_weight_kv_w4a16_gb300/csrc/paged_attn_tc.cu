@@ -50,7 +50,8 @@ constexpr int kTcRows = 256, kTcHalf = 128;
 // An item's start (queries) and end (records) count as four tiles in the cut: CTAs with
 // three items ended last.  With 0, 3, 4, 5, 6 and 8 the chunks above take 98.1, 87.6,
 // 86.0, 86.6, 88.0 and 90.8 us.
-constexpr Rows kTcWork{kTcRows, 4};
+template <bool kSinks>
+constexpr Rows kTcWork{kTcRows, 4, kSinks};
 constexpr int kTcThreads = 14 * 32;
 constexpr int kTcSoft = 8 * 32;                 // softmax threads
 constexpr float kTiny = 1.17549435e-38f;
@@ -86,7 +87,7 @@ struct TcItem {
   Walk w;
   Cut cut;
   int active;
-  int first, count, valid;       // tiles of this CTA's part (the first's number among the item's), rows of the tile
+  int first, count, valid;       // tiles of this CTA's part (from number `first` on), rows of the tile
 };
 
 __device__ __forceinline__ void tc_soft_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kTcSoft) : "memory"); }
@@ -277,18 +278,18 @@ struct TcScale {
   float f0, f1, b0, b1;
 };
 
-// The columns of a tile that a row does not see: behind top, and `hole` columns from
-// `sink` on (between the sinks and its window).
+// The columns of a tile that a row sees: low .. top, and those below `sink`.
 struct TcSight {
-  int top, sink;
-  uint32_t hole;
+  int low, top, sink;
 };
 
-// Those of the chunk of 32 at column c to -inf.
+// What it does not see of the chunk of 32 at column c to -inf.
+template <bool kSinks>
 __device__ __forceinline__ void tc_mask(float (&x)[32], int c, const TcSight& v) {
+  const uint32_t hole = (uint32_t)max(0, v.low - v.sink);   // columns from `sink` on, before `low`
 #pragma unroll
   for (int j = 0; j < 32; ++j)
-    if (c + j > v.top || (uint32_t)(c + j - v.sink) < v.hole) x[j] = -INFINITY;
+    if (c + j > v.top || (kSinks ? (uint32_t)(c + j - v.sink) < hole : c + j < v.low)) x[j] = -INFINITY;
 }
 
 // The largest s f + b of 32 columns (f > 0; -inf where nothing is seen).
@@ -334,7 +335,7 @@ __device__ __forceinline__ TcScale tc_scale_of(const float4* sc, int c, float qf
 // 32 columns: with 64 a turn those chunks took 101 us where this took 93, unrolled 132 (the roles' code
 // no longer fits the instruction cache); a row's 128 scores held in registers, by a
 // split of the CTA's registers between the roles, 104 where this took 100.
-template <bool kCut>
+template <bool kCut, bool kSinks>
 __device__ __forceinline__ float tc_row_max(uint32_t ts, const float4* sc, float qf, const TcSight& v) {
   float mx = -INFINITY;
 #pragma unroll 1
@@ -343,7 +344,7 @@ __device__ __forceinline__ float tc_row_max(uint32_t ts, const float4* sc, float
     tc_ld32(ts + 32 * c, x);
     const TcScale t = tc_scale_of(sc, c, qf);
     tc_wait_ld32(x);
-    if (kCut) tc_mask(x, 32 * c, v);
+    if (kCut) tc_mask<kSinks>(x, 32 * c, v);
     mx = fmaxf(mx, tc_max(x, t));
   }
   return mx;
@@ -351,7 +352,7 @@ __device__ __forceinline__ float tc_row_max(uint32_t ts, const float4* sc, float
 
 // Its weights, over scores that have been read (chunk c's to columns 16 c .. 16 c +
 // 15); returns their sum with each 16 columns times their inverse value scale.
-template <bool kCut>
+template <bool kCut, bool kSinks>
 __device__ __forceinline__ float tc_row_weights(uint32_t ts, const float4* sc, float qf, float ref,
                                                 const TcSight& v) {
   float sum = 0.f;
@@ -361,7 +362,7 @@ __device__ __forceinline__ float tc_row_weights(uint32_t ts, const float4* sc, f
     tc_ld32(ts + 32 * c, x);
     const TcScale t = tc_scale_of(sc, c, qf);
     tc_wait_ld32(x);
-    if (kCut) tc_mask(x, 32 * c, v);
+    if (kCut) tc_mask<kSinks>(x, 32 * c, v);
     uint32_t h[16];
     float sum0, sum1;
     tc_weights(x, t, ref, h, sum0, sum1);
@@ -378,14 +379,14 @@ struct TcJoin {
 };
 
 // The bounds of the current part from its walk (one thread).
-__device__ __forceinline__ void tc_set(const PagedAttnArgs& a, TcItem& it) {
+__device__ __forceinline__ void tc_set(const PagedAttnArgs& a, Rows s, TcItem& it) {
   const Walk& c = it.w;
-  it.first = (int)(c.u - c.item0);
+  it.first = first_number(s, c.t) + (int)(c.u - c.item0);
   it.count = (int)(min(c.u1, c.item0 + (c.t.t1 - c.t.t0)) - c.u);
   it.valid = min(kTcRows, c.n * a.G - c.rt * kTcRows);
 }
 
-template <int D, bool kHalf>
+template <int D, bool kHalf, bool kSinks>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged_attn_tc_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap map) {
   using Lay = TcLayout<D, kHalf>;
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 0) {
     Walk w;
     Cut cut;
-    const bool active = find_share(a, kTcWork, cta, gridDim.x, w, cut, cta == 0);
+    const bool active = find_share(a, kTcWork<kSinks>, cta, gridDim.x, w, cut, cta == 0);
     if (lane == 0) {
       it.w = w;
       it.cut = cut;
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---------------------------------------------------------- producer --
     if (active) {
       int issued = 0;
-      if (!produce_tiles<D>(a, &map, kTcWork, w, smem + Lay::kStage, s_raw, full, empty, Lay::kRing,
+      if (!produce_tiles<D>(a, &map, kTcWork<kSinks>, w, smem + Lay::kStage, s_raw, full, empty, Lay::kRing,
                             it.cut.total, issued)) {
         pa_timeout(a);
         *s_dead = 1;
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         w.u += count;
         ++part;
         part1 += nh - 1;
-        if (w.u < w.u1) w.next_item(a, kTcWork);
+        if (w.u < w.u1) w.next_item(a, kTcWork<kSinks>);
       }
       // the buffers' last releases, which no other tile waits for, have to arrive while
       // this CTA's shared memory is its own
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       uint32_t t = 0, told[2] = {0, 0};   // tiles; arrivals at sfull by half
       while (w.u < w.u1) {
-        const int first = (int)(w.u - w.item0);
+        const int first = first_number(kTcWork<kSinks>, w.t) + (int)(w.u - w.item0);
         const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);
         const int nh = min(kTcRows, w.n * a.G - w.rt * kTcRows) > kTcHalf ? 2 : 1;
         for (int i = 0; i < count; ++i, ++t) {
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint8_t* st = smem + Lay::kStage + slot * (2 * kPaTile * D);
           const float4 raw = s_raw[slot * kPaSub + (lane & (kPaSub - 1))];
           // what was never written, or lies on a missing page, becomes zeros
-          const int left = w.p0 + w.n - tile_at(a, w.t, first + i) * kPaTile;   // written positions from the tile's first
+          const int left = w.p0 + w.n - tile_of(a, kTcWork<kSinks>, w.t, first + i) * kPaTile;   // written positions from the tile's first
           const unsigned gone = __ballot_sync(0xffffffffu, lane < kPaSub && raw.y == -INFINITY);
           const bool plain = left >= kPaTile && gone == 0u;
 #pragma unroll 1
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         w.u += count;
-        if (w.u < w.u1) w.next_item(a, kTcWork);
+        if (w.u < w.u1) w.next_item(a, kTcWork<kSinks>);
       }
     }
   } else {
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (active) {
       uint32_t t = 0, mine = 0;   // tiles of the CTA; tiles of this half
       for (bool more = true; more;) {
-        if (tid == 0) tc_set(a, it);
+        if (tid == 0) tc_set(a, kTcWork<kSinks>, it);
         tc_soft_sync();
         const int count = it.count, valid = it.valid;
         const bool here = kTcHalf * half < valid;
@@ -657,15 +658,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float qf = s_qs[r];   // this warp wrote it
           const int p = it.w.p0 + myrow / a.G, back = a.window > 0 ? a.window - 1 : 0x3fffffff;
           for (int i = 0; i < count; ++i, ++mine) {
-            const int pos0 = tile_at(a, it.w.t, it.first + i) * kPaTile;
+            const int pos0 = tile_of(a, kTcWork<kSinks>, it.w.t, it.first + i) * kPaTile;
             wait(&sfull[half], mine & 1u);
             tc_fence_after();
             const float4* sc = s_scale + ((t + i) & 1) * kPaSub;
-            // columns low .. top are visible, and those below `sink`
-            const int top = p - pos0, low = top - back, sink = max(0, a.sinks - pos0);
-            const TcSight v{top, sink, (uint32_t)max(0, low - sink)};
+            const int top = p - pos0, low = top - back;   // columns low .. top are visible
+            const TcSight v{low, top, kSinks ? max(0, a.sinks - pos0) : 0};
             const bool cut = __any_sync(0xffffffffu, top < kPaTile - 1 || low > 0);
-            const float mx = cut ? tc_row_max<true>(ts, sc, qf, v) : tc_row_max<false>(ts, sc, qf, v);
+            const float mx = cut ? tc_row_max<true, kSinks>(ts, sc, qf, v)
+                                 : tc_row_max<false, kSinks>(ts, sc, qf, v);
             // the reference moves when the maximum has outgrown it (or it has none yet)
             const bool grow = mx > M + kRefLag || (M == -INFINITY && mx > M);
             if (__any_sync(0xffffffffu, grow)) {
@@ -688,7 +689,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
             const float ref = M == -INFINITY ? 0.f : M - kRefWeight;
-            L += cut ? tc_row_weights<true>(ts, sc, qf, ref, v) : tc_row_weights<false>(ts, sc, qf, ref, v);
+            L += cut ? tc_row_weights<true, kSinks>(ts, sc, qf, ref, v)
+                     : tc_row_weights<false, kSinks>(ts, sc, qf, ref, v);
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -744,12 +746,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the CTA with an item's beginning describes the join
         if (!whole && live && c.item0 == c.u && tid == 0)
           join = TcJoin{it.cut.owner(item1 - 1) - cta, c.row0, c.kvh, c.rt, valid};
-        more = c.u + count + kTcWork.pad < c.u1;
+        more = c.u + count + kTcWork<kSinks>.pad < c.u1;
         if (more) {
           tc_soft_sync();   // the item's bounds are read no more
           if (tid == 0) {
             it.w.u += count;
-            it.w.next_item(a, kTcWork);
+            it.w.next_item(a, kTcWork<kSinks>);
           }
         }
       }
@@ -834,14 +836,14 @@ size_t tc_smem() {
   return (size_t)TcLayout<D, kHalf>::kBytes + 1024;
 }
 
-template <int D, bool kHalf>
+template <int D, bool kHalf, bool kSinks>
 cudaError_t tc_launch(const PagedAttnArgs& a, const CUtensorMap& map, int ctas, cudaStream_t st) {
   static DeviceOnce configured;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!configured.done(dev)) {
-    e = cudaFuncSetAttribute(paged_attn_tc_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(paged_attn_tc_kernel<D, kHalf, kSinks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)tc_smem<D, kHalf>());
     if (e != cudaSuccess) return e;
     configured.mark(dev);
@@ -856,7 +858,7 @@ cudaError_t tc_launch(const PagedAttnArgs& a, const CUtensorMap& map, int ctas, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<D, kHalf>, a, map);
+  e = cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<D, kHalf, kSinks>, a, map);
   if (e != cudaSuccess) return e;
   // rows of a tile: no sequence has more than all of them
   const long long rows = (long long)a.r.n_rows * a.G;
@@ -866,6 +868,13 @@ cudaError_t tc_launch(const PagedAttnArgs& a, const CUtensorMap& map, int ctas, 
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kHalf>, a, ctas);
 }
 
+template <bool kSinks>
+cudaError_t tc_launch_any(const PagedAttnArgs& a, const CUtensorMap& map, int d, bool half, int ctas, cudaStream_t st) {
+  if (d == 128)
+    return half ? tc_launch<128, true, kSinks>(a, map, ctas, st) : tc_launch<128, false, kSinks>(a, map, ctas, st);
+  return half ? tc_launch<64, true, kSinks>(a, map, ctas, st) : tc_launch<64, false, kSinks>(a, map, ctas, st);
+}
+
 }  // namespace
 
 size_t paged_tc_rec_floats(int d) { return (size_t)2 * kTcRows * (d + 2) + sizeof(TcJoin) / 4; }
@@ -873,8 +882,7 @@ size_t paged_tc_rec_floats(int d) { return (size_t)2 * kTcRows * (d + 2) + sizeo
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs& a, const CUtensorMap& map, int d, int dtype, int ctas,
                                       cudaStream_t st) {
   const bool half = dtype == FUTR_DTYPE_F16;
-  if (d == 128) return half ? tc_launch<128, true>(a, map, ctas, st) : tc_launch<128, false>(a, map, ctas, st);
-  return half ? tc_launch<64, true>(a, map, ctas, st) : tc_launch<64, false>(a, map, ctas, st);
+  return a.sinks > 0 ? tc_launch_any<true>(a, map, d, half, ctas, st) : tc_launch_any<false>(a, map, d, half, ctas, st);
 }
 
 }  // namespace futr

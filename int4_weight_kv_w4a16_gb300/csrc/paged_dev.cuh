@@ -81,30 +81,35 @@ __device__ __forceinline__ bool my_seq(const PagedAttnArgs& a, int b, int& row0,
 
 // What a kernel makes of rows: R rows a row tile, whose start (queries, the join of
 // its parts) counts as much as `pad` tiles of positions.  The units of an item are
-// `pad` that hold nothing, then its tiles.
+// `pad` that hold nothing, then its tiles.  sinks: the call has some (a constant: the
+// kernels without them would be 1 to 3 % slower, 10.8 us for the drafted tokens that take
+// 10.4).
 struct Rows {
   int R, pad;
+  bool sinks;
 };
 
 // Row tile rt of a sequence (n rows from position p0, R rows a tile): its tiles, those
-// of the sinks first, then those from the first that its window meets.  The i-th of them,
-// 0 <= i < t1 - t0, is tile i among the sinks', else t0 + i.
+// of the sinks first, then those from the first that its window meets.  They have
+// consecutive numbers: without sinks the tiles' own, t0 .. t1 - 1; with sinks 0 .. t1 - t0
+// - 1, the sinks' tiles their own, the others' t0 less.
 struct TileRange {
   int t0, t1;
 };
-__device__ __forceinline__ int tile_at(const PagedAttnArgs& a, const TileRange& t, int i) {
-  return i < a.sink_tiles ? i : t.t0 + i;
+__device__ __forceinline__ int first_number(Rows s, const TileRange& t) { return s.sinks ? 0 : t.t0; }
+__device__ __forceinline__ int tile_of(const PagedAttnArgs& a, Rows s, const TileRange& t, int number) {
+  return s.sinks && number >= a.sink_tiles ? t.t0 + number : number;
 }
-__device__ __forceinline__ TileRange row_tile(const PagedAttnArgs& a, int n, int p0, int R, int rt) {
+__device__ __forceinline__ TileRange row_tile(const PagedAttnArgs& a, Rows s, int n, int p0, int rt) {
   int first = p0, last = p0;
   if (n > 1) {
-    const int r0 = rt * R, r1 = min(n * a.G, r0 + R) - 1;
+    const int r0 = rt * s.R, r1 = min(n * a.G, r0 + s.R) - 1;
     first = p0 + r0 / a.G;
     last = p0 + r1 / a.G;
   }
   // (sinks that reach the window's tiles: one run from tile 0)
   const int lo = a.window > 0 ? max(0, first - a.window + 1) / kPaTile : 0;
-  return {lo - min(lo, a.sink_tiles), last / kPaTile + 1};
+  return {s.sinks ? lo - min(lo, a.sink_tiles) : lo, last / kPaTile + 1};
 }
 
 // The units of a sequence and kv-head.
@@ -113,7 +118,7 @@ __device__ __forceinline__ long long seq_units(const PagedAttnArgs& a, int n, in
   const int nrt = (n * a.G + s.R - 1) / s.R;
 #pragma unroll 1
   for (int rt = 0; rt < nrt; ++rt) {
-    const TileRange t = row_tile(a, n, p0, s.R, rt);
+    const TileRange t = row_tile(a, s, n, p0, rt);
     w += s.pad + t.t1 - t.t0;
   }
   return w;
@@ -150,12 +155,12 @@ struct Walk {
     kvh = (int)quot(at, per_head);
     long long rem = at - (long long)kvh * per_head;
     rt = 0;
-    t = row_tile(a, n, p0, s.R, 0);
+    t = row_tile(a, s, n, p0, 0);
 #pragma unroll 1
     while (rem >= s.pad + t.t1 - t.t0) {
       rem -= s.pad + t.t1 - t.t0;
       ++rt;
-      t = row_tile(a, n, p0, s.R, rt);
+      t = row_tile(a, s, n, p0, rt);
     }
     item0 = base + at - rem + s.pad;
     u = max(u, item0);
@@ -178,7 +183,7 @@ struct Walk {
         per_head = seq_units(a, n, p0, s);
       }
     }
-    t = row_tile(a, n, p0, s.R, rt);
+    t = row_tile(a, s, n, p0, rt);
   }
 };
 
@@ -253,21 +258,23 @@ __device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUte
   bool ok = true;
   if (a.withhold && w.u1 == total) return ok;
   while (w.u < w.u1 && ok) {
-    const int first = (int)(w.u - w.item0);   // the first tile's number among the item's
+    const int first = first_number(s, w.t) + (int)(w.u - w.item0);
     const int count = (int)(min(w.u1, w.item0 + (w.t.t1 - w.t.t0)) - w.u);
-    const int last = tile_at(a, w.t, first + count - 1) * kPaTile;
+    const int last = tile_of(a, s, w.t, first + count - 1) * kPaTile;
     const int end = min(w.p0 + w.n, last + kPaTile);   // positions needed
     // page ids and scales, 32 pages a round (one per lane), one round ahead; pages are
-    // numbered through the item's tiles
+    // numbered as their tiles are
     const int tlog = 7 - plog;
-    const int pg0 = first << tlog, pg1 = ((first + count - 1) << tlog) + ((end - 1 - last) >> plog);
+    const int pg0 = first << tlog;
+    const int pg1 = s.sinks ? ((first + count - 1) << tlog) + ((end - 1 - last) >> plog) : (end - 1) >> plog;
     // (pages before the first row's window, behind the sinks, are not looked at: a program
     // may have given them back)
     const int seen = a.window > 0 ? max(0, w.p0 + w.rt * s.R / a.G - a.window + 1) >> plog : 0;
     const int* tab = a.r.table + (size_t)w.b * a.r.table_ld;
     auto fetch = [&](int pg, int& id, float2& sc) {
-      const int at = (tile_at(a, w.t, pg >> tlog) << tlog) + (pg & (ppt - 1));   // its place in the table
-      const bool look = pg <= pg1 && (at >= seen || at < a.sink_pages);
+      // its place in the table
+      const int at = s.sinks ? (tile_of(a, s, w.t, pg >> tlog) << tlog) + (pg & (ppt - 1)) : pg;
+      const bool look = pg <= pg1 && (at >= seen || (s.sinks && at < a.sink_pages));
       id = look ? tab[at] : -1;
       if (id < 0 || id >= a.c.n_pages) {
         if (look) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
@@ -281,7 +288,7 @@ __device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUte
     fetch(base + lane, id, sc);
     if (base + 32 <= pg1) fetch(base + 32 + lane, id_next, sc_next);
     for (int i = 0; i < count && ok; ++i) {
-      const int pg = (first + i) << tlog;
+      const int pos = (first + i) * kPaTile, pg = pos >> plog;
       if (pg >= base + 32) {   // 32 and pg0 are multiples of the pages of a tile: no tile straddles
         base += 32;
         id = id_next;
@@ -300,7 +307,7 @@ __device__ __forceinline__ bool produce_tiles(const PagedAttnArgs& a, const CUte
       const unsigned mask = __ballot_sync(0xffffffffu, have);
       if (have)
         tma_3d(smem_u32(st + lane * bytes), map, 0, (int)(a.block0 + (long long)zid * a.Hkv + w.kvh), &full[slot]);
-      const int from = (pg + ((16 * (lane & (kPaSub - 1))) >> plog) - base) & 31;   // the page of sub-tile `lane`
+      const int from = (((pos + 16 * (lane & (kPaSub - 1))) >> plog) - base) & 31;   // the page of sub-tile `lane`
       const float kscale = __shfl_sync(0xffffffffu, sc.x, from), vscale = __shfl_sync(0xffffffffu, sc.y, from);
       const int myid = __shfl_sync(0xffffffffu, id, from);
       if (lane < kPaSub) {

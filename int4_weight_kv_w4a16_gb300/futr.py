@@ -85,8 +85,8 @@ class futr_moe_ws(C.Structure):
 
 class futr_beam_ws(C.Structure):
     _fields_ = [("rows", C.c_int32), ("keep", C.c_int32), ("ctas", C.c_int32), ("_pad", C.c_int32),
-                ("base", C.c_void_p), ("bytes", C.c_uint64), ("err_offset", C.c_uint64), ("row_offset", C.c_uint64),
-                ("rec_offset", C.c_uint64), ("magic", C.c_uint64)]
+                ("base", C.c_void_p), ("bytes", C.c_uint64), ("err_offset", C.c_uint64), ("cnt_offset", C.c_uint64),
+                ("row_offset", C.c_uint64), ("rec_offset", C.c_uint64), ("magic", C.c_uint64)]
 
 
 class futr_pages(C.Structure):
