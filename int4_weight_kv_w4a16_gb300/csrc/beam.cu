@@ -5,9 +5,9 @@
 // L_w is the same for a whole row, so a row's candidates are its `keep` largest
 // logits (equal ones by the lowest token), compared as they are; only those meet the
 // other beams', as sums in two fp32 parts.  One pass over the logits, one kernel:
-//   part   a CTA takes a part of a row in tiles, a thread 64 bytes of a tile in registers
-//          (the next tile's are on their way): running maximum and sum of exponentials per
-//          thread, and every logit that reaches a threshold goes to a list in shared memory.
+//   part   a CTA takes a part of a row in tiles, a thread 32 logits of a tile in registers:
+//          running maximum and sum of exponentials per thread, and every logit that reaches
+//          a threshold goes to a list in shared memory.
 //          The threshold starts at (about) the keep-th largest of the threads' maxima of the
 //          first tile: so many logits reach it at least, and few more.  A list that grows is cut
 //          down to its keep largest, and the threshold follows.
@@ -31,7 +31,7 @@ namespace futr {
 namespace {
 
 constexpr int kBmThreads = 256, kBmWarps = kBmThreads / 32;
-constexpr int kBmVecs = 4;                        // 16-byte vectors of a thread in a tile
+constexpr int kBmLogits = 32;                     // logits of a thread in a tile
 constexpr int kBmList = 1024;                     // entries of a part's list
 constexpr int kBmCut = 64;                        // entries of a list that is cut, at least
 constexpr int kBmShort = kBmThreads;              // entries that are put in order by counting
@@ -39,8 +39,25 @@ constexpr int kBmOne = 2048;                      // most candidates of a prompt
 constexpr int kBmMaxParts = 64;                   // parts of a row
 constexpr int kBmPerSm = 4;                       // CTAs an SM
 constexpr int kBmMaxWaves = 4;                    // parts of all rows, in CTAs that run at once
-constexpr double kBmStart = 1.0;                  // what a part costs beside its tiles, in tiles
+constexpr double kBmStart = 4.0;                  // what a part costs beside its logits, in halves of tiles
 constexpr float kLog2e = 1.4426950408889634f;
+
+// Two fp32 numbers side by side, as one instruction takes them.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+  return (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float pair_lo(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float pair_hi(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
 
 __device__ __forceinline__ float bm_ex2(float x) {
   float y;
@@ -85,6 +102,13 @@ __device__ __forceinline__ Two log_of(Two x) {
   const float f = __int_as_float(u - e * (1 << 23)), p = (float)e * ln2_hi;
   const float rest = fmaf((float)e, ln2_hi, -p) + (float)e * ln2_lo;
   return add(add(add(Two{p, 0.f}, logf(f)), rest), __fdiv_rn(x.lo, x.hi));
+}
+
+// log sum e^x of S = sum of 2^((x - M) c), c the fp32 constant for log2 e: M + log S / (c ln 2).
+__device__ __forceinline__ Two log_sum(float M, Two S) {
+  constexpr float tiny = (float)(1.0 / ((double)kLog2e * 0.69314718055994530942) - 1.0);
+  const Two l = log_of(S);
+  return add(add(l, l.hi * tiny), M);
 }
 
 __device__ __forceinline__ unsigned long long make_key(float x, int v) {
@@ -332,64 +356,76 @@ template <int kType>
 __device__ __forceinline__ void do_part(const BeamArgs& a, BmShared& sh, int row, int part, uint8_t* rec) {
   using T = Logit<kType>;
   constexpr int W = 16 / sizeof(T);            // logits of a vector
-  constexpr int P = kBmVecs * W;               // of a thread in a tile
+  constexpr int P = kBmLogits, V = P / W;      // logits and vectors of a thread in a tile
+  constexpr int kStep = kBmThreads * V;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.keep;
   const T* x = static_cast<const T*>(a.logits) + (size_t)row * a.ld;
   const int nv = (a.vocab - 1) / W + 1;
   const int v0 = (int)((long long)nv * part / a.splits), v1 = (int)((long long)nv * (part + 1) / a.splits);
-  constexpr int kStep = kBmThreads * kBmVecs;
   const bool aligned = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
   int turn = 0, n = 0, tile = 0;               // sums made, entries of the list, tiles
   const int kCut = max(2 * K, kBmCut);         // entries above which the list is cut
-  float m = -INFINITY, s = 0.f;
+  float m = -INFINITY, s = 0.f;                // maximum, sum of 2^((x - m) log2 e)
   unsigned long long thr = 1;
   float thr_x = -FLT_MAX;                      // a logit below it does not reach thr
-  uint32_t u[kBmVecs][4], next[kBmVecs][4];
-  // a tile's logits; one that lies in the row as a whole, on 16-byte boundaries, without checks
-  auto load = [&](int at, uint32_t (&to)[kBmVecs][4]) {
-    if (aligned && at + kStep <= v1 && (long long)(at + kStep) * W <= a.vocab) {
-      const uint4* p = reinterpret_cast<const uint4*>(x) + at + tid;
-#pragma unroll
-      for (int j = 0; j < kBmVecs; ++j) {
-        const uint4 q = __ldcs(p + kBmThreads * j);
-        to[j][0] = q.x, to[j][1] = q.y, to[j][2] = q.z, to[j][3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kBmVecs; ++j) load_vec<kType>(x, at + tid + kBmThreads * j, v1, a.vocab, to[j]);
-    }
-  };
-  load(v0, next);
   if (tid < 3) sh.n[tid] = 0;
   __syncthreads();
   for (int at = v0; at < v1; at += kStep, ++tile) {
+    uint32_t u[V][4];
+    // a tile that lies in the part and the row as a whole, on 16-byte boundaries, without checks
+    if (aligned && at + kStep <= v1 && (long long)(at + kStep) * W <= a.vocab) {
+      const uint4* p = reinterpret_cast<const uint4*>(x) + at + tid;
 #pragma unroll
-    for (int j = 0; j < kBmVecs; ++j)
+      for (int j = 0; j < V; ++j) {
+        const uint4 q = __ldcs(p + kBmThreads * j);
+        u[j][0] = q.x, u[j][1] = q.y, u[j][2] = q.z, u[j][3] = q.w;
+      }
+    } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[j][i] = next[j][i];
-    if (at + kStep < v1) load(at + kStep, next);
+      for (int j = 0; j < V; ++j) load_vec<kType>(x, at + tid + kBmThreads * j, v1, a.vocab, u[j]);
+    }
     auto logit = [&](int i) { return logit_of<kType>(u[i / W], i % W); };
     auto token = [&](int i) { return (at + tid + kBmThreads * (i / W)) * W + i % W; };
-    float tops[kBmVecs];
+    // maxima of 8 logits, and of all
+    float tops[P / 8], top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kBmVecs; ++j) {
-      tops[j] = logit(j * W);
+    for (int j = 0; j < P / 8; ++j) {
+      tops[j] = logit(8 * j);
 #pragma unroll
-      for (int i = 1; i < W; ++i) tops[j] = fmaxf(tops[j], logit(j * W + i));
+      for (int i = 1; i < 8; ++i) tops[j] = fmaxf(tops[j], logit(8 * j + i));
+      top = fmaxf(top, tops[j]);
     }
-    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     if (top > m) {
       s *= bm_ex2((m - top) * kLog2e);         // (the first time 2^-inf = 0)
       m = top;
     }
-    const float ref = m == -INFINITY ? 0.f : m;
-    float s0 = 0.f, s1 = 0.f;
+    const float at_m = m == -INFINITY ? 0.f : m;
+    if (fabsf(at_m) <= 0x1p20f) {
+      // 2^(x log2 e - ref), two logits an instruction where there is one; ref is m log2 e
+      // rounded, what that lost is put back
+      const float ref = __fmul_rn(at_m, kLog2e), lost = fmaf(at_m, kLog2e, -ref);
+      const uint64_t c2 = pair_of(kLog2e, kLog2e), r2 = pair_of(-ref, -ref);
+      uint64_t sum = 0;
 #pragma unroll
-    for (int i = 0; i < P; i += 2) {
-      s0 += bm_ex2((logit(i) - ref) * kLog2e);
-      s1 += bm_ex2((logit(i + 1) - ref) * kLog2e);
+      for (int i = 0; i < P; i += 2) {
+        const uint64_t e = pair_fma(pair_of(logit(i), logit(i + 1)), c2, r2);
+        sum = pair_add(sum, pair_of(bm_ex2(pair_lo(e)), bm_ex2(pair_hi(e))));
+      }
+      s = fmaf(pair_lo(sum) + pair_hi(sum), bm_ex2(-lost), s);   // a NaN or +inf in the row makes it one
+    } else {   // a row that masks have left nothing but their own large values, or so
+#pragma unroll 1
+      for (int j = 0; j < V; ++j) {
+        uint32_t t[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = u[0][i];
+#pragma unroll
+        for (int q = 1; q < V; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = q == j ? u[q][i] : t[i];
+#pragma unroll
+        for (int i = 0; i < W; ++i) s += bm_ex2((logit_of<kType>(t, i) - at_m) * kLog2e);
+      }
     }
-    s += s0 + s1;                              // a NaN or +inf in the row makes it a NaN
     if (tile == 0) {
       const uint32_t lo = reached(top > -INFINITY ? ordered(top) : 0u, K, reinterpret_cast<uint32_t*>(sh.all));
       if (lo >= kLowest) {
@@ -400,10 +436,10 @@ __device__ __forceinline__ void do_part(const BeamArgs& a, BmShared& sh, int row
     int* counter = &sh.n[tile % 3];
     if (top >= thr_x) {
 #pragma unroll
-      for (int j = 0; j < kBmVecs; ++j)
+      for (int j = 0; j < P / 8; ++j)
         if (tops[j] >= thr_x) {
 #pragma unroll
-          for (int i = j * W; i < j * W + W; ++i)
+          for (int i = 8 * j; i < 8 * j + 8; ++i)
             if (logit(i) >= thr_x) {
               const unsigned long long key = make_key(logit(i), token(i));
               if (key >= thr) {
@@ -524,7 +560,8 @@ __device__ __forceinline__ void join_sums(const uint8_t* recs, int n, size_t ste
   S = Two{0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kBmMaxParts / 32; ++i) {
-    const float w = m[i] == -INFINITY ? 1.f : bm_ex2((m[i] - M) * kLog2e);   // (no logit: 0, or a NaN)
+    // (no logit: 0, or a NaN)
+    const float w = m[i] == -INFINITY ? 1.f : bm_ex2((m[i] - M) * kLog2e);
     S = add(S, Two{s[i].hi * w, fmaf(s[i].hi, w, -(s[i].hi * w)) + s[i].lo * w});
   }
   S = warp_sum(S);
@@ -587,7 +624,7 @@ __device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, 
       join_sums(recs + (size_t)w * lists * step, lists, step, M, S);
       const bool bad = !(S.hi <= FLT_MAX) || M == INFINITY;
       if (bad && (tid & 31) == 0) set_err(a.err, FUTR_ERR_NOT_FINITE);
-      if (!bad && M > -INFINITY) lse = add(log_of(S), M);
+      if (!bad && M > -INFINITY) lse = log_sum(M, S);
     } else if (score >= -FLT_MAX) {
       lse.hi = -INFINITY;        // ended: one candidate
     }
@@ -725,8 +762,10 @@ int beam_part_ctas(int sms) { return kBmPerSm * kBmMaxWaves * sms; }
 cudaError_t launch_beam_select(const BeamArgs& args, int dtype, int sms, cudaStream_t st) {
   BeamArgs a = args;
   const long long rows = (long long)a.batch * a.beams, slots = (long long)kBmPerSm * sms;
-  // parts of a row: those that end soonest, in tiles; a part costs about kBmStart more
-  const int per = kBmThreads * kBmVecs * (dtype == FUTR_DTYPE_F32 ? 4 : 8), tiles = (a.vocab - 1) / per + 1;
+  // parts of a row: those that end soonest, by waves of CTAs, in halves of tiles (4096
+  // logits); a part costs about kBmStart more.  256 rows of 128256 logits in 1, 2, 3, 4 and 7
+  // parts: 47, 33.5, 43, 39 and 44 us; 4 rows in 8, 16, 32 and 64: 9.7, 9.0, 9.0 and 11.
+  const int tiles = (a.vocab - 1) / (kBmThreads * kBmLogits / 2) + 1;
   double best = 1e30;
   a.splits = 1;
   for (int s = 1; s <= kBmMaxParts && s <= tiles && (s == 1 || rows * s <= beam_part_ctas(sms)); ++s) {

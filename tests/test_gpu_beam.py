@@ -195,6 +195,35 @@ def test_masked_logits():
     assert parent[0].tolist() == [0, 1, -1, -1]
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_rows_of_masks_alone(dtype):
+    """Rows in which every token has the mask's large value: each has -log(their number).  Beside it, larger ones of
+    whole steps of the type take all of the weight, in ranges where fp64 has the differences."""
+    low = torch.finfo(dtype).min
+    for mask in (low, -1e4, -1e9 if dtype != torch.float16 else -3e4, -2.0 ** 15,
+                 -2.0 ** 20 if dtype != torch.float16 else -9.0, -1.1e6 if dtype != torch.float16 else -5e4, -low):
+        for V in (10, 5000, 40000):
+            x = torch.full((2, V), mask, device="cuda").to(dtype)
+            x[1, V // 2:] = -math.inf
+            score, parent, token, _ = select(x, torch.tensor([[-1.0, -3.0]], device="cuda"), 12)
+            n = min(V, 12)
+            assert parent[0, :min(n, 5)].tolist() == [0] * min(n, 5)
+            for p, t, v in zip(parent[0].tolist(), token[0].tolist(), score[0].tolist()):
+                if p >= 0:
+                    want = -1.0 - math.log(V) if p == 0 else -3.0 - math.log(V // 2)
+                    assert abs(v - want) <= beam_tolerance(V) + 2.0 ** -23 * abs(want)
+    if dtype == torch.float32:
+        x = torch.full((1, 20000), -1e9, device="cuda")
+        x[0, 77] += 64                        # fp32's step there
+        score, _, token, _ = select(x, torch.zeros((1, 1), device="cuda"), 2)
+        assert token[0].tolist() == [77, 0] and float(score[0, 1]) == -64.0
+        assert abs(float(score[0, 0])) <= 2 * 19999 * math.exp(-64)          # -log(1 + 19999 e^-64)
+        x = torch.linspace(-2.0 ** 20 - 4, -2.0 ** 20 + 4, 30000, device="cuda")[None].repeat(3, 1)    # either side of a branch
+        x[1] -= 8
+        x[2] += 8
+        check(x, scores_of(1, 3, 5), 20)
+
+
 @pytest.mark.parametrize("value", [math.nan, math.inf])
 @pytest.mark.parametrize("at", [0, 4095, 4999])
 def test_rows_that_are_not_finite_are_reported(value, at):
@@ -290,6 +319,23 @@ def test_workspace_of_more_rows_and_two_at_once():
         assert futr.futr_beam_check(ws[i], streams[i]) == futr.FUTR_OK
         want = select(*data[i], 8)
         assert all(torch.equal(a, b) for a, b in zip(outs[i], want))
+
+
+def test_candidates_of_nearly_one_value():
+    """Hundreds of candidates that agree in the first 24 bits of their values, and more than the pick's list holds:
+    the order of the rest, then of the places."""
+    V = 40000
+    x = torch.full((8, V), -30.0, device="cuda")
+    x[:, 7:207:2] = 0.0                       # a hundred tokens of each beam, equal
+    s = torch.full((1, 8), -16384.0, device="cuda")
+    s[0, 5] = -16384.0 + 2.0 ** -9
+    for keep in (64, 16, 1):
+        _, parent, token, _ = select(x, s, keep)
+        assert parent[0].tolist() == [5] * keep and token[0].tolist() == [7 + 2 * i for i in range(keep)]
+    s[0, 5] = -16384.0
+    x[3, 8000] = 2.0 ** -9                    # 2^-9 - log(100 + e^(2^-9)) < -log 100: not among the best
+    _, parent, token, _ = select(x, s, 64)
+    assert parent[0].tolist() == [0] * 64 and token[0].tolist() == [7 + 2 * i for i in range(64)]
 
 
 # ----------------------------------------------------------------- reorder --
