@@ -244,7 +244,10 @@ futr_status futr_kv_reorder(const futr_kv* kv, int32_t batch, const int32_t* par
     if (!kv || kv->magic != kKvMagic || !kv->base || !parent || !pos || parent == pos) return FUTR_ERR_INVALID_ARG;
     if (batch < 1 || batch > kv->max_batch) return FUTR_ERR_INVALID_ARG;
     if (batch > kMaxBatch) return FUTR_ERR_UNSUPPORTED;
-    return status_of(launch_kv_reorder(*kv, batch, parent, pos, at<int>(kv->base, kv->err_offset), as_stream(stream)));
+    const int sms = host::sm_count();
+    if (sms <= 0) return FUTR_ERR_CUDA;
+    return status_of(
+        launch_kv_reorder(*kv, batch, parent, pos, at<int>(kv->base, kv->err_offset), sms, as_stream(stream)));
   });
 }
 

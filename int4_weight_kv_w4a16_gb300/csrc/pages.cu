@@ -158,46 +158,59 @@ __device__ __forceinline__ void grow_pages(const PagesArgs& a, int b, int& i0, i
   i1 = (int)((end - 1) >> a.c.page_log2) + 1;
 }
 
+// The places that a call's rows meet, of all sequences one after another: place f is entry
+// [b][i] of the table.
 __global__ void __launch_bounds__(kPgPlan) pages_grow_kernel(const PagesArgs a) {
   __shared__ int words[kPgWarps];
-  __shared__ int need[kPagesMaxSeqs];
+  __shared__ int first[kPagesMaxSeqs], place[kPagesMaxSeqs];   // a sequence's first page, and its place
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // what each sequence needs, a warp a sequence
-  for (int b = warp; b < a.batch; b += kPgWarps) {
-    int i0, i1, n = 0;
-    grow_pages(a, b, i0, i1, lane == 0);
-    const int* row = a.table + (size_t)b * a.table_ld;
-    for (int i = i0 + lane; i < i1; i += 32) n += row[i] < 0;
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) need[b] = n;
-  }
+  const int tid = threadIdx.x;
+  int i0 = 0, i1 = 0, places;
+  if (tid < a.batch) grow_pages(a, tid, i0, i1, true);
+  const int before = scan(i1 - i0, words, places);
+  first[tid] = i0;
+  place[tid] = before;
   __syncthreads();
-  int total;
-  const int mine = tid < a.batch ? need[tid] : 0;
-  const int before = scan(mine, words, total);
-  if (total == 0) return;
-  if (total > a.p.err[2]) {
+  // the last sequence that begins at or before place f (of those that begin together the last
+  // is the one with pages)
+  auto entry = [&](int f) {
+    int lo = 0;
+    for (int step = kPagesMaxSeqs / 2; step > 0; step >>= 1)
+      if (lo + step < a.batch && place[lo + step] <= f) lo += step;
+    return a.table + (size_t)lo * a.table_ld + first[lo] + (f - place[lo]);
+  };
+  // those without a page: the round's, kept, and of all rounds before it
+  int* list = plan_to(a.p);
+  int need = 0, mine = 0, at = 0;
+  int* e = nullptr;
+  for (int f0 = 0; f0 < places; f0 += kPgPlan) {
+    e = f0 + tid < places ? entry(f0 + tid) : nullptr;
+    mine = e && *e < 0;
+    int total;
+    at = need + scan(mine, words, total);
+    need += total;
+  }
+  if (need == 0) return;
+  if (need > a.p.err[2]) {
     if (tid == 0) set_err(a.p.err, FUTR_ERR_NO_PAGES);
     return;
   }
-  if (tid < a.batch) need[tid] = before;
-  int* list = plan_to(a.p);
+  __syncthreads();   // the count of free pages has been read
+  take(a.p, need, list, words);
   __syncthreads();
-  take(a.p, total, list, words);
-  __syncthreads();
-  for (int b = warp; b < a.batch; b += kPgWarps) {
-    int i0, i1, k = need[b];
-    grow_pages(a, b, i0, i1, false);
-    int* row = a.table + (size_t)b * a.table_ld;
-    for (int base = i0; base < i1; base += 32) {
-      const int i = base + lane;
-      const bool none = i < i1 && row[i] < 0;
-      const unsigned votes = __ballot_sync(0xffffffffu, none);
-      if (none) row[i] = list[k + __popc(votes & ((1u << lane) - 1))];
-      k += __popc(votes);
-    }
+  if (places <= kPgPlan) {
+    if (mine) *e = list[at];
+    return;
+  }
+  need = 0;
+  for (int f0 = 0; f0 < places; f0 += kPgPlan) {
+    e = f0 + tid < places ? entry(f0 + tid) : nullptr;
+    mine = e && *e < 0;
+    int total;
+    at = need + scan(mine, words, total);
+    need += total;
+    if (mine) *e = list[at];
   }
 }
 
@@ -259,36 +272,47 @@ __global__ void __launch_bounds__(kPgPlan) fork_plan_kernel(const PagesArgs a) {
 
 // ------------------------------------------------------------------ copies --
 
-// Slots 0 .. n-1 of the keys and values of a page and head, `bytes` each, to another page;
-// a warp.
-__device__ __forceinline__ void copy_rows(const uint8_t* src, uint8_t* dst, int bytes) {
+// Up to kPgPiece bytes (a multiple of 16), a warp: all loads are under way before the first
+// store.
+constexpr int kPgPiece = 4096;
+__device__ __forceinline__ void copy_piece(const uint8_t* src, uint8_t* dst, int bytes) {
   const uint4* s = reinterpret_cast<const uint4*>(src);
   uint4* t = reinterpret_cast<uint4*>(dst);
   const int n = bytes >> 4, lane = threadIdx.x & 31;
-  int i = lane;
-  for (; i + 7 * 32 < n; i += 8 * 32) {
-    uint4 v[8];
+  uint4 v[kPgPiece / 512];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = s[i + 32 * j];
+  for (int j = 0; j < kPgPiece / 512; ++j)
+    if (lane + 32 * j < n) v[j] = s[lane + 32 * j];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t[i + 32 * j] = v[j];
-  }
-  for (; i < n; i += 32) t[i] = s[i];
+  for (int j = 0; j < kPgPiece / 512; ++j)
+    if (lane + 32 * j < n) t[lane + 32 * j] = v[j];
 }
 
-// The plan's copies, a (copy, layer, head, keys or values) a warp (warps `w` of `warps`).
+// The plan's copies, a piece of up to kPgPiece bytes of a (copy, layer, head, keys or
+// values) a warp at a time (warps `w` of `warps`): small pieces, so that the warps end
+// together.  262 MB moved twice, with 2, 4, 6 and 8 CTAs an SM: 195, 180, 172 and 171 us.
+constexpr int kPgCopyCtas = 8;
 __device__ __forceinline__ void do_copies(const PagesArgs& a, int w, int warps, bool whole) {
-  const int blocks = 2 * a.c.n_kv;   // of a page in a layer
-  const long long per = (long long)blocks * a.n_layers, n = a.p.plan[0] * per;
+  const int block = a.c.page * a.d, pieces = (block + kPgPiece - 1) / kPgPiece;
+  const int blocks = 2 * a.c.n_kv, per = blocks * a.n_layers * pieces;   // of a page in a layer; pieces of a copy
+  const int n = a.p.plan[0];
   const int *from = plan_from(a.p), *to = plan_to(a.p), *slots = plan_slots(a.p);
-  for (long long e = w; e < n; e += warps) {
-    const int k = (int)(e / per), r = (int)(e - k * per), layer = r / blocks, h = r - layer * blocks;
+  const int dk = warps / per, dr = warps - dk * per;
+  int k = w / per, r = w - k * per;
+  while (k < n) {
+    const int piece = r % pieces, q = r / pieces, layer = q / blocks, h = q - layer * blocks;
     const size_t src = (size_t)from[k] * blocks + h, dst = (size_t)to[k] * blocks + h;
-    const int block = a.c.page * a.d;
     uint8_t* codes = a.c.codes + (size_t)layer * a.layer_codes;
     float* scales = a.c.scales + (size_t)layer * a.layer_scales;
-    copy_rows(codes + src * block, codes + dst * block, whole ? block : slots[k] * a.d);
-    if ((threadIdx.x & 31) == 0) scales[dst] = scales[src];
+    const int at = piece * kPgPiece, bytes = min(whole ? block : slots[k] * a.d, at + kPgPiece) - at;
+    if (bytes > 0) copy_piece(codes + src * block + at, codes + dst * block + at, bytes);
+    if (piece == 0 && (threadIdx.x & 31) == 0) scales[dst] = scales[src];
+    k += dk;
+    r += dr;
+    if (r >= per) {
+      r -= per;
+      ++k;
+    }
   }
 }
 
@@ -454,7 +478,7 @@ cudaError_t launch_pages_fork(const PagesArgs& a, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     configured.mark(dev);
   }
-  return pg_launch(fork_apply_kernel, dim3((unsigned)(table_ctas + 4 * sms)), kPgThreads, (size_t)a.batch * cols * 4, st,
+  return pg_launch(fork_apply_kernel, dim3((unsigned)(table_ctas + kPgCopyCtas * sms)), kPgThreads, (size_t)a.batch * cols * 4, st,
                    a, cols, table_ctas);
 }
 
@@ -462,7 +486,7 @@ cudaError_t launch_pages_compact(const PagesArgs& a, int sms, cudaStream_t st) {
   const cudaError_t e = pg_launch(compact_plan_kernel, dim3(1), kPgPlan, 0, st, a);
   if (e != cudaSuccess) return e;
   const int table_ctas = (int)blocks_for((long long)a.batch * a.table_ld, 64);
-  return pg_launch(compact_apply_kernel, dim3((unsigned)(table_ctas + 4 * sms)), kPgThreads, 0, st, a, table_ctas);
+  return pg_launch(compact_apply_kernel, dim3((unsigned)(table_ctas + kPgCopyCtas * sms)), kPgThreads, 0, st, a, table_ctas);
 }
 
 }  // namespace futr

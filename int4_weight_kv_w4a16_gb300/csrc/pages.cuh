@@ -50,6 +50,7 @@ cudaError_t launch_pages_free(const PagesArgs& a, cudaStream_t st);
 cudaError_t launch_pages_fork(const PagesArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_pages_compact(const PagesArgs& a, int sms, cudaStream_t st);
 
-cudaError_t launch_kv_reorder(const futr_kv& kv, int batch, const int* parent, int* pos, int* err, cudaStream_t st);
+cudaError_t launch_kv_reorder(const futr_kv& kv, int batch, const int* parent, int* pos, int* err, int sms,
+                              cudaStream_t st);
 
 }  // namespace futr
