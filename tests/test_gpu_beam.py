@@ -6,9 +6,11 @@ import pytest
 import torch
 
 from int4_weight_kv_w4a16_gb300 import futr
+from int4_weight_kv_w4a16_gb300.inputs import TOY
 from tests._gen_ref import beam_best, beam_tolerance, beam_values
 from tests._gpu_helpers import ensure_lib
 from tests._paged_ref import ints, shape_of
+from tests.test_gpu_step import Model
 
 pytestmark = pytest.mark.gpu
 I32 = torch.int32
@@ -443,3 +445,44 @@ def test_reorder_in_a_graph_and_on_another_stream():
         graph.replay()
         assert futr.futr_check(kv=s.kv) == futr.FUTR_OK
         assert torch.equal(s.streams, want) and pos.tolist() == [at[q] if q >= 0 else 0 for q in par]
+
+
+@pytest.mark.parametrize("stay", [False, True])
+def test_a_search_with_the_decode_step(stay):
+    """Beams over the INT4 cache: the complete step, the choice and the slots' new order, again and again; a beam's
+    logits are those of its tokens decoded one after another by themselves."""
+    W, groups, V = 3, 2, 512
+    n = W * groups
+    m, alone = (Model(TOY, 2, V, max_batch=n, capacity=40, seed=5, host_weights=False) for _ in range(2))
+    m.lm_head.mul_(8)
+    alone.lm_head.mul_(8)
+    ws = workspace(n, W)
+    token = torch.arange(n, dtype=I32, device="cuda").view(groups, W)
+    scores = torch.full((groups, W), -math.inf, device="cuda")
+    scores[:, 0] = 0
+    parent, pos = torch.empty((groups, W), dtype=I32, device="cuda"), ints([0] * n)
+    fed = [[t] for t in range(n)]
+    moved = 0
+    for i in range(30):
+        logits = m.step(token.view(-1).cpu().numpy(), [i] * n)
+        if i in (0, 9, 29):
+            for j in range(i + 1):
+                want = alone.step([f[j] for f in fed], [j] * n)
+            assert torch.equal(logits, want)
+        before = scores.clone()
+        futr.futr_beam_select(logits, scores, scores, parent, token, ws, stay=stay)
+        check(logits, before, W, got=ranked(scores, parent, token))
+        pos.fill_(i + 1)
+        futr.futr_kv_reorder(m.kv, parent.view(-1), pos)
+        assert pos.tolist() == [i + 1] * n
+        p = parent.view(-1).tolist()
+        moved += sum(a != b for a, b in enumerate(p))
+        fed = [fed[a] + [t] for a, t in zip(p, token.view(-1).tolist())]
+    assert futr.futr_check(m.ws, m.kv) == futr.FUTR_OK and futr.futr_beam_check(ws) == futr.FUTR_OK
+    assert moved > 30
+
+
+def ranked(score, parent, token):
+    """Outputs best first, as check() takes them (no beam ends)."""
+    order = torch.sort(score, dim=1, descending=True, stable=True).indices
+    return [t.gather(1, order) for t in (score, parent, token)] + [torch.zeros_like(token)]
