@@ -50,6 +50,7 @@ typedef int32_t futr_status;
 #define FUTR_ERR_NOT_FINITE   10  /* device: infinity or NaN appended to a paged cache, NaN in logits */
 #define FUTR_ERR_NO_PAGES     11  /* device: fewer free pages than a call needs         */
 #define FUTR_ERR_NOT_HELD     12  /* device: a table names a page that its pool has free */
+#define FUTR_ERR_SHARED       13  /* device: rows of a page that other sequences hold, too */
 
 /* Shape of one decoder block. */
 typedef struct futr_shape {
@@ -590,7 +591,9 @@ futr_status futr_pages_hold(const futr_paged* cache, const futr_pages* pool, int
  * positions pos[b] .. pos[b] + n - 1 of each sequence, n = start[b+1] - start[b]
  * (start NULL: 1), as futr_paged_append will write them.  A sequence whose rows do
  * not fit the table or the cache's max_pos sets FUTR_ERR_OUT_OF_RANGE and is
- * skipped. */
+ * skipped.  A page that is there and that another place names, too, is not for new
+ * rows (after futr_pages_free had brought a sequence back into pages that it shares):
+ * FUTR_ERR_SHARED, and nothing is changed; futr_pages_fork makes a copy. */
 futr_status futr_pages_grow(const futr_paged* cache, const futr_pages* pool, int32_t batch, const int32_t* pos,
                             const int32_t* start, int32_t* table, int32_t table_ld, void* stream);
 
@@ -609,7 +612,7 @@ futr_status futr_pages_free(const futr_paged* cache, const futr_pages* pool, int
  * page that is partly written (the one of position pos, when pos is no multiple of
  * the page) and pages taken ahead behind it stay with the parent's first child;
  * every further child gets a page of its own with a copy of the written positions
- * and the scales, in all layers.  Needs one free page a copy, beside those that the call itself gives
+ * and the scales, in all layers (the first, too, if other places name the page).  Needs one free page a copy, beside those that the call itself gives
  * back.  A parent outside [-1, batch) or a pos outside [0, min(max_pos, table_ld *
  * page)] of a parent sets FUTR_ERR_OUT_OF_RANGE, and nothing is changed.
  */

@@ -492,6 +492,7 @@ const char* futr_status_string(futr_status s) {
     case FUTR_ERR_NOT_FINITE: return "infinity or NaN in a row appended to the paged cache, or NaN in logits";
     case FUTR_ERR_NO_PAGES: return "not enough free pages";
     case FUTR_ERR_NOT_HELD: return "a page table names a page that its pool has free";
+    case FUTR_ERR_SHARED: return "new rows of a page that other sequences hold";
     default: return "unknown status";
   }
 }

@@ -648,7 +648,8 @@ __device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, 
         if (i == w * lists * K) val[q] = ordered64(score);
         at[q] |= (uint32_t)a.end;
       } else if (lse.hi < INFINITY && key != 0) {
-        val[q] = ordered64(add(add(add(score, key_logit(key)), -lse.hi), -lse.lo));
+        const Two v = add(add(add(Two{key_logit(key), 0.f}, -lse.hi), -lse.lo), score);
+        if (v.hi >= -FLT_MAX) val[q] = ordered64(v);   // (below it: as little as a logit of -inf)
         at[q] |= (uint32_t)key_token(key);
       }
       top = max(top, (uint32_t)(val[q] >> 32));

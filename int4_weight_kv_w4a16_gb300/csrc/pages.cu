@@ -53,10 +53,15 @@ __device__ __forceinline__ int page_of(const PoolView& p, int id) {
   return -1;
 }
 
+// The bits of word i that are pages.
+__device__ __forceinline__ unsigned valid_bits(const PoolView& p, int i) {
+  return p.n_pages - 32 * i >= 32 ? ~0u : (1u << (p.n_pages - 32 * i)) - 1;
+}
+
 __global__ void pages_init_kernel(const PoolView p) {
   const int i = blockIdx.x * kPgThreads + threadIdx.x;
   if (i < p.n_pages) p.refs[i] = 0;
-  if (i < p.words) p.free[i] = i * 32 + 32 <= p.n_pages ? ~0u : (1u << (p.n_pages - i * 32)) - 1;
+  if (i < p.words) p.free[i] = valid_bits(p, i);
   if (i == 0) p.err[2] = p.n_pages;
 }
 
@@ -184,12 +189,19 @@ __global__ void __launch_bounds__(kPgPlan) pages_grow_kernel(const PagesArgs a) 
   int* list = plan_to(a.p);
   int need = 0, mine = 0, at = 0;
   int* e = nullptr;
+  bool shared = false;
   for (int f0 = 0; f0 < places; f0 += kPgPlan) {
     e = f0 + tid < places ? entry(f0 + tid) : nullptr;
-    mine = e && *e < 0;
+    const int id = e ? *e : -1;
+    mine = e && id < 0;
+    if (id >= 0 && page_of(a.p, id) >= 0) shared |= a.p.refs[id] > 1;   // rows go to a page of their own
     int total;
     at = need + scan(mine, words, total);
     need += total;
+  }
+  if (__syncthreads_or(shared)) {
+    if (tid == 0) set_err(a.p.err, FUTR_ERR_SHARED);
+    return;
   }
   if (need == 0) return;
   if (need > a.p.err[2]) {
@@ -232,6 +244,7 @@ __global__ void __launch_bounds__(kPgPlan) fork_plan_kernel(const PagesArgs a) {
   }
   __syncthreads();
   int from = -1, at = 0;
+  bool others = false;   // name the written page
   if (parent >= 0 && parent < a.batch) {
     atomicMin(&first[parent], i);
     const int p = oldpos[parent];
@@ -240,13 +253,14 @@ __global__ void __launch_bounds__(kPgPlan) fork_plan_kernel(const PagesArgs a) {
     else {
       at = p >> a.c.page_log2;   // places below it are shared
       if (p & (a.c.page - 1)) from = page_of(a.p, a.table[(size_t)parent * a.table_ld + at]);
+      if (from >= 0) others = a.p.refs[from] > 1;
     }
   } else if (i < a.batch && parent != -1) {
     s_bad = 1;
   }
   __syncthreads();
   const bool one = parent >= 0 && !s_bad && first[parent] == i;
-  const bool copy = parent >= 0 && !s_bad && !one && from >= 0;
+  const bool copy = parent >= 0 && !s_bad && (!one || others) && from >= 0;
   int total;
   const int k = scan(copy, words, total);
   const bool ok = !s_bad && total <= a.p.err[2];
@@ -329,10 +343,13 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply_kernel(const PagesArgs 
     do_copies(a, w, ((int)gridDim.x - table_ctas) * (kPgThreads / 32), false);
     return;
   }
-  __shared__ int kids[kPagesMaxSeqs], shared[kPagesMaxSeqs];   // a row's children; its first place that is not shared
+  // a row's children; its first place that is not shared; whether its first child has a copy
+  // of that place's page
+  __shared__ int kids[kPagesMaxSeqs], shared[kPagesMaxSeqs];
+  __shared__ uint8_t copied[kPagesMaxSeqs];
   const int c0 = blockIdx.x * cols, n = min(cols, a.table_ld - c0);
   const int4* seqs = plan_seqs(a.p);
-  for (int i = tid; i < a.batch; i += kPgThreads) kids[i] = 0, shared[i] = 0;
+  for (int i = tid; i < a.batch; i += kPgThreads) kids[i] = 0, shared[i] = 0, copied[i] = 0;
   for (int e = tid; e < a.batch * cols; e += kPgThreads) {
     const int i = e / cols, j = e - i * cols;
     if (j < n) old[e] = a.table[(size_t)i * a.table_ld + c0 + j];
@@ -343,6 +360,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply_kernel(const PagesArgs 
     if (s.x >= 0) {
       atomicAdd(&kids[s.x], 1);
       shared[s.x] = s.y;   // the same for all children
+      if (s.w) copied[s.x] = s.z >= 0;
     }
   }
   __syncthreads();
@@ -352,10 +370,10 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply_kernel(const PagesArgs 
     // row i's new entry
     const int4 s = seqs[i];
     int now = -1;
-    if (s.x >= 0) now = c < s.y || s.w ? old[s.x * cols + j] : c == s.y ? s.z : -1;
+    if (s.x >= 0) now = c == s.y && s.z >= 0 ? s.z : c < s.y || s.w ? old[s.x * cols + j] : -1;
     if (now != old[e]) a.table[(size_t)i * a.table_ld + c] = now;
     // and what becomes of its old page
-    const int more = (c < shared[i] ? kids[i] : kids[i] > 0) - 1;
+    const int more = (c < shared[i] ? kids[i] : kids[i] > 0 && !(copied[i] && c == shared[i])) - 1;
     if (old[e] >= 0 && more != 0) {
       const int id = page_of(a.p, old[e]);
       if (id >= 0) {
@@ -375,18 +393,14 @@ __global__ void __launch_bounds__(kPgPlan) compact_plan_kernel(const PagesArgs a
   const PoolView& p = a.p;
   // pages of word i inside [lo, hi)
   auto inside = [&](int i) {
-    unsigned m = 0;
-    const int b = i * 32;
-    if (a.hi > b && a.lo < b + 32) {
-      m = ~0u;
-      if (a.lo > b) m &= ~0u << (a.lo - b);
-      if (a.hi < b + 32) m &= ~(~0u << (a.hi - b));
-    }
+    const int lo = a.lo - i * 32, hi = a.hi - i * 32;
+    unsigned m = hi > 0 && lo < 32 ? ~0u : 0u;
+    if (lo > 0 && lo < 32) m &= ~0u << lo;
+    if (hi > 0 && hi < 32) m &= ~(~0u << hi);
     return m;
   };
-  auto valid = [&](int i) { return i * 32 + 32 <= p.n_pages ? ~0u : (1u << (p.n_pages - i * 32)) - 1; };
   int *from = plan_from(p), *to = plan_to(p), *where = plan_slots(p);
-  const int moves = list_bits([&](int i) { return ~p.free[i] & inside(i) & valid(i); }, p.words, p.n_pages, from, words);
+  const int moves = list_bits([&](int i) { return ~p.free[i] & inside(i) & valid_bits(p, i); }, p.words, p.n_pages, from, words);
   const int room = list_bits([&](int i) { return p.free[i] & ~inside(i); }, p.words, moves, to, words);
   const bool ok = room == moves;
   if (threadIdx.x == 0) {

@@ -23,7 +23,7 @@ struct PoolView {
 //   from, to [n_pages]   pages to copy (to: also the pages that a call takes)
 //   slots [n_pages]      slots of a page that are copied; compact: where page p goes
 //   seqs [max_seqs][4]   fork: parent's row or -1, first place behind the shared ones,
-//                        fresh page or -1, 1: keeps the parent's places behind the shared
+//                        fresh page for it or -1, 1: keeps the parent's places from there on
 constexpr int kPlanHeader = 64;
 inline size_t plan_ints(int n_pages, int max_seqs) {
   // (the sequences' rows are aligned to 16 bytes)

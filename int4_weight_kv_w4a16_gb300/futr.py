@@ -30,6 +30,7 @@ FUTR_ERR_NOT_FINITE = 10
 
 FUTR_ERR_NO_PAGES = 11
 FUTR_ERR_NOT_HELD = 12
+FUTR_ERR_SHARED = 13
 
 FUTR_DTYPE_BF16, FUTR_DTYPE_F16, FUTR_DTYPE_F32 = range(3)
 
@@ -478,6 +479,11 @@ def futr_paged_attention(cache, layer, batch, pos, start, table, q, out, ws, sca
                                          out.data_ptr(), ld_out, dtype, scale, window, sinks, C.addressof(ws),
                                          T.stream(device) if stream is None else _stream(stream)),
         "futr_paged_attention")
+
+
+def futr_paged_attention_sinks(cache, layer, batch, pos, start, table, q, out, ws, window, sinks, scale=0.0, stream=None):
+    """futr_paged_attention with a window and the first `sinks` positions, which every row sees."""
+    futr_paged_attention(cache, layer, batch, pos, start, table, q, out, ws, scale, window, stream, sinks)
 
 
 def futr_paged_check(cache, ws=None, stream=None) -> int:

@@ -67,11 +67,14 @@ class Pool:
         return [p for p, r in enumerate(self.refs()) if r == 0]
 
     def grow(self, pos, new):
-        """False: too few free pages."""
-        want = []
+        """False: too few free pages; None: rows would go to a page that another place names, too."""
+        want, refs = [], self.refs()
         for b, (p, n) in enumerate(zip(pos, new)):
             if n > 0 and p >= 0 and p + n <= min(self.max_pos, self.width * self.page):
-                want += [(b, i) for i in range(p // self.page, (p + n - 1) // self.page + 1) if self.table[b][i] < 0]
+                met = [(b, i) for i in range(p // self.page, (p + n - 1) // self.page + 1)]
+                if any(self.table[b][i] >= 0 and refs[self.table[b][i]] > 1 for b, i in met):
+                    return None
+                want += [(b, i) for b, i in met if self.table[b][i] < 0]
         free = self.free()
         if len(want) > len(free):
             return False
@@ -91,18 +94,16 @@ class Pool:
 
     def fork(self, parent, pos):
         """(source, target, slots) of the copies, and the new positions; None: too few free pages."""
-        free, copies, rows, seen = self.free(), [], [], set()
+        free, refs, copies, rows, seen = self.free(), self.refs(), [], [], set()
         for i, p in enumerate(parent):
             if p < 0:
                 rows.append([-1] * self.width)
                 continue
-            if p not in seen:
-                seen.add(p)
-                rows.append(list(self.table[p]))
-                continue
             at, part = divmod(pos[p], self.page)
-            row = self.table[p][:at] + [-1] * (self.width - at)
-            if part and self.table[p][at] >= 0:
+            first = p not in seen
+            seen.add(p)
+            row = list(self.table[p]) if first else self.table[p][:at] + [-1] * (self.width - at)
+            if part and self.table[p][at] >= 0 and (not first or refs[self.table[p][at]] > 1):
                 if len(copies) == len(free):
                     return None
                 row[at] = free[len(copies)]

@@ -128,6 +128,34 @@ def test_too_few_pages_change_nothing():
     b.same()
 
 
+def test_rows_are_not_for_pages_that_others_hold():
+    """Back to a position inside a page that a fork shared: refused, until a fork has made a copy."""
+    b = Both(40, 16, 3, 8)
+    assert b.grow([0, 0, 0], [70, 20, 0])
+    pos = b.fork([0, 1, 0], [70, 20, 0])            # rows 0 and 2 share four pages
+    b.same()
+    b.free([40, 20, 70])                            # row 0 goes back into the third
+    b.same()
+    assert b.grow([40, 20, 70], [1, 1, 1]) is None
+    b.same(futr.FUTR_ERR_SHARED)
+    assert b.grow([48, 20, 70], [1, 1, 1])          # behind it, in a page of its own
+    b.same()
+    b.free([40, 20, 71])
+    assert b.grow([64, 20, 70], [0, 13, 10]) is True
+    b.same()
+    # a fork of every row into itself copies the page, in the order of rows
+    b.free([40, 0, 71])
+    assert b.fork([0, 1, 2], [40, 0, 71]) == [40, 0, 71]
+    b.same()
+    assert b.grow([40, 0, 71], [30, 0, 1])
+    b.same()
+    # of two that share one, both copy, and the page is free; with further children
+    b.free([70, 0, 72])
+    b.free([35, 0, 36])
+    assert b.fork([2, 2, 0], [35, 0, 36]) == [36, 36, 35]
+    b.same()
+
+
 def test_free_by_window_sinks_and_position():
     b = Both(200, 16, 4, 40)
     assert b.grow([0] * 4, [640, 640, 640, 640])
@@ -239,10 +267,11 @@ def test_random_runs(seed):
         status = OK
         if op == "grow":
             new = [int(min(r.integers(0, 3 * page), width * page - p)) for p in pos]
-            if b.grow(pos, new):
+            done = b.grow(pos, new)
+            if done:
                 pos = [p + n for p, n in zip(pos, new)]
             else:
-                status = futr.FUTR_ERR_NO_PAGES
+                status = futr.FUTR_ERR_SHARED if done is None else futr.FUTR_ERR_NO_PAGES
         elif op == "free":
             pos = [max(0, p - int(r.integers(0, page))) if r.random() < 0.3 else p for p in pos]
             b.free(pos, *((int(r.integers(1, 6 * page)), int(r.integers(0, 2 * page))) if seed % 2 else ()))
