@@ -4,11 +4,10 @@
 // A thread takes 16 bytes at the same place of every slot's stream: it reads all that move
 // before it writes any, so slots may trade places and one slot may go to several.  All of
 // them are in registers at once, for as many moves as the call's batch can have: so many
-// loads are in flight together (one after another through shared memory: 559 us for 32 slots
-// of 16 layers, 1.1 GB read and written, that now take 169; 20.6 for one slot of 32
-// layers, 62 MB, that now take 10.3).  A stream has four runs (codes of keys and of
-// values, their scales) of which the first tiles move; threads count through those alone.
-// Bound by memory.
+// loads are in flight together (one after another through shared memory took 559 us for 32
+// slots of 16 layers, 1.1 GB read and written, that take 170 here).  A stream has four runs
+// (codes of keys and of values, their scales) of which the first tiles move; threads count
+// through those alone.  Bound by memory: 6.4 TB/s for those, 0.95 of the copy rate.
 #include "pages.cuh"
 
 namespace futr {
@@ -39,41 +38,22 @@ __device__ __forceinline__ bool read_slots(const ReorderArgs& a, int& parent, in
   return !__any_sync(0xffffffffu, bad);
 }
 
-// M: most moves; C: 16-byte columns of a thread at once.
+struct Moves {
+  uint64_t from[32], to[32];   // slots as offsets
+  int tiles[32];               // that move
+  int n, most;                 // moves, tiles of the longest
+};
+
+// The columns of all streams, C at a time in a thread, with n <= M moves.
 template <int M, int C>
-__global__ void __launch_bounds__(kKrThreads) kv_reorder_kernel(const ReorderArgs a) {
-  __shared__ uint64_t s_from[M], s_to[M];   // the moves' slots as offsets, and their tiles
-  __shared__ int s_tiles[M], s_n, s_most;
-  pdl_trigger();
-  pdl_wait();
-  const int tid = threadIdx.x;
-  if (tid < 32) {
-    int parent, tiles, pos;
-    const bool ok = read_slots(a, parent, tiles, pos);
-    if (!ok) tiles = 0;
-    const unsigned votes = __ballot_sync(0xffffffffu, tiles > 0);
-    const uint64_t slot = (uint64_t)a.n_kv * a.stream_bytes;
-    if (tiles > 0) {
-      const int i = __popc(votes & ((1u << tid) - 1));
-      s_from[i] = parent * slot;
-      s_to[i] = tid * slot;
-      s_tiles[i] = tiles;
-    }
-    const int most = __reduce_max_sync(0xffffffffu, tiles);
-    if (tid == 0) {
-      s_n = __popc(votes);
-      s_most = most;
-      if (!ok) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
-    }
-  }
-  __syncthreads();
-  const int n = s_n, most = s_most;
-  if (n == 0) return;
+__device__ __forceinline__ void move_columns(const ReorderArgs& a, const Moves& mv) {
+  const int tid = threadIdx.x, n = mv.n, most = mv.most;
   // columns of a stream: codes of keys, of values (d / 2 a tile each), then scales (2 each)
   const int half = a.d / 2, codes = most * half, cols = 2 * (codes + 2 * most);
   const int per = (cols + kKrThreads * C - 1) / (kKrThreads * C);
   const uint64_t code_bytes = (uint64_t)a.cap * a.d;
   const long long items = (long long)a.n_layers * a.n_kv * per;
+#pragma unroll 1
   for (long long e = blockIdx.x; e < items; e += gridDim.x) {
     const int stream = (int)(e / per), first = (int)(e - (long long)stream * per) * (kKrThreads * C) + tid;
     const int layer = stream / a.n_kv, head = stream - layer * a.n_kv;
@@ -88,7 +68,7 @@ __global__ void __launch_bounds__(kKrThreads) kv_reorder_kernel(const ReorderArg
       if (col < 2 * codes) {
         const bool v = col >= codes;
         if (v) col -= codes;
-        tile[c] = col / half;
+        tile[c] = a.d == 128 ? col >> 6 : col >> 5;
         off[c] = (v ? code_bytes / 2 : 0) + (uint64_t)col * 16;
       } else if (col < cols) {
         col -= 2 * codes;
@@ -103,13 +83,66 @@ __global__ void __launch_bounds__(kKrThreads) kv_reorder_kernel(const ReorderArg
     for (int i = 0; i < M; ++i)
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        if (i < n && tile[c] < s_tiles[i]) x[i][c] = *reinterpret_cast<const uint4*>(at + s_from[i] + off[c]);
+        if (i < n && tile[c] < mv.tiles[i]) x[i][c] = *reinterpret_cast<const uint4*>(at + mv.from[i] + off[c]);
 #pragma unroll
     for (int i = 0; i < M; ++i)
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        if (i < n && tile[c] < s_tiles[i]) *reinterpret_cast<uint4*>(at + s_to[i] + off[c]) = x[i][c];
+        if (i < n && tile[c] < mv.tiles[i]) *reinterpret_cast<uint4*>(at + mv.to[i] + off[c]) = x[i][c];
   }
+}
+
+// M: most moves of the batch.  Few take more columns at once, 8 loads a thread at least: one
+// slot of 32 layers at 900 positions, from memory, 13.6 us (two loads: 15.3).  Three CTAs an
+// SM (168 registers) for 32 moves: 170 us, two (189) 187.
+template <int M>
+__global__ void __launch_bounds__(kKrThreads, M > 16 ? 3 : 4) kv_reorder_kernel(const ReorderArgs a) {
+  __shared__ Moves mv;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  if (tid < 32) {
+    int parent, tiles, pos;
+    const bool ok = read_slots(a, parent, tiles, pos);
+    if (!ok) tiles = 0;
+    const unsigned votes = __ballot_sync(0xffffffffu, tiles > 0);
+    const uint64_t slot = (uint64_t)a.n_kv * a.stream_bytes;
+    if (tiles > 0) {
+      const int i = __popc(votes & ((1u << tid) - 1));
+      mv.from[i] = parent * slot;
+      mv.to[i] = tid * slot;
+      mv.tiles[i] = tiles;
+    }
+    const int most = __reduce_max_sync(0xffffffffu, tiles);
+    if (tid == 0) {
+      mv.n = __popc(votes);
+      mv.most = most;
+      if (!ok) set_err(a.err, FUTR_ERR_OUT_OF_RANGE);
+    }
+  }
+  __syncthreads();
+  const int n = mv.n;
+  if (n == 0) return;
+  if constexpr (M > 8) {
+    if (n > 8) {
+      move_columns<M, 1>(a, mv);
+      return;
+    }
+  } else {
+    if (n == 1) {
+      move_columns<1, 8>(a, mv);
+      return;
+    }
+    if (n == 2) {
+      move_columns<2, 4>(a, mv);
+      return;
+    }
+    if (n <= 4) {
+      move_columns<4, 2>(a, mv);
+      return;
+    }
+  }
+  if constexpr (M > 4) move_columns<8, 1>(a, mv);
 }
 
 // The positions follow, once no CTA above reads them.
@@ -136,11 +169,11 @@ cudaError_t kr_launch(F* f, int grid, int threads, const ReorderArgs& a, cudaStr
 }
 
 // CTAs that run at once.
-template <int M, int C>
+template <int M>
 int kr_ctas(int dev, int sms) {
-  return sms * remembered(occ_key(dev, M, C, 0), [&]() {
+  return sms * remembered(occ_key(dev, M, 0, 0), [&]() {
            int n = 0;
-           if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_reorder_kernel<M, C>, kKrThreads, 0) != cudaSuccess ||
+           if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_reorder_kernel<M>, kKrThreads, 0) != cudaSuccess ||
                n < 1) {
              cudaGetLastError();
              return 1;
@@ -149,9 +182,9 @@ int kr_ctas(int dev, int sms) {
          });
 }
 
-template <int M, int C>
+template <int M>
 cudaError_t kr_run(const ReorderArgs& a, int dev, int sms, cudaStream_t st) {
-  return kr_launch(kv_reorder_kernel<M, C>, kr_ctas<M, C>(dev, sms), kKrThreads, a, st);
+  return kr_launch(kv_reorder_kernel<M>, kr_ctas<M>(dev, sms), kKrThreads, a, st);
 }
 
 }  // namespace
@@ -173,10 +206,10 @@ cudaError_t launch_kv_reorder(const futr_kv& kv, int batch, const int* parent, i
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = batch <= 4    ? kr_run<4, 2>(a, dev, sms, st)
-      : batch <= 8  ? kr_run<8, 1>(a, dev, sms, st)
-      : batch <= 16 ? kr_run<16, 1>(a, dev, sms, st)
-                    : kr_run<32, 1>(a, dev, sms, st);
+  e = batch <= 4    ? kr_run<4>(a, dev, sms, st)
+      : batch <= 8  ? kr_run<8>(a, dev, sms, st)
+      : batch <= 16 ? kr_run<16>(a, dev, sms, st)
+                    : kr_run<32>(a, dev, sms, st);
   if (e != cudaSuccess) return e;
   return kr_launch(kv_reorder_pos_kernel, 1, 32, a, st);
 }
