@@ -510,9 +510,11 @@ futr_status futr_paged_attention_sinks(const futr_paged* cache, int32_t layer, i
  * left, in order, so that the caches move as little as they have to.  Outputs
  * must not overlap inputs, but score_out may be scores and done_out may be done.
  *
- * Sums of exponentials are fp32 within a thread's part of a row and fp64 between
- * parts; logits of a row are compared exactly, values of beams in fp64.  beams
- * 1..32, keep 1..64, vocab below 2^31.  Capturable in a CUDA graph. */
+ * Logits of a row are compared exactly, values of beams in two fp32 parts (some 46
+ * bits), as they are summed in.  A log-sum is fp32 within a thread's logits and two
+ * parts beyond (off by about 2^-23); equal rows have equal ones.  A value below fp32's
+ * range is no candidate.  beams 1..32, keep 1..64, vocab below 2^31.  One kernel;
+ * capturable in a CUDA graph. */
 #define FUTR_DTYPE_F32  2
 
 typedef struct futr_beam_ws {
@@ -593,7 +595,8 @@ futr_status futr_pages_hold(const futr_paged* cache, const futr_pages* pool, int
  * not fit the table or the cache's max_pos sets FUTR_ERR_OUT_OF_RANGE and is
  * skipped.  A page that is there and that another place names, too, is not for new
  * rows (after futr_pages_free had brought a sequence back into pages that it shares):
- * FUTR_ERR_SHARED, and nothing is changed; futr_pages_fork makes a copy. */
+ * FUTR_ERR_SHARED; futr_pages_fork makes a copy.  A page that is there and that the
+ * pool has free: FUTR_ERR_NOT_HELD (see futr_pages_hold).  Either changes nothing. */
 futr_status futr_pages_grow(const futr_paged* cache, const futr_pages* pool, int32_t batch, const int32_t* pos,
                             const int32_t* start, int32_t* table, int32_t table_ld, void* stream);
 

@@ -8,7 +8,7 @@ newer than every source and header.
 --debug``) makes the debug variant ``libfutr_debug.so`` from the same sources
 with ``-DFUTR_DEBUG``: device bounds checks in the decode step's kernels, before
 the global accesses of the split records, the projection outputs, the weight-unit and
-KV-tile copies (the paged cache's and the experts' kernels have none; a
+KV-tile copies (the kernels of the paged cache, the experts, beams and pages have none; a
 failed check reports FUTR_ERR_BOUNDS and skips the access).  ``futr.lib()``
 loads it when the environment has FUTR_DEBUG=1.
 """

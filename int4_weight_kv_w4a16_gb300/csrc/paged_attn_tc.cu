@@ -32,8 +32,8 @@
 //
 // Bound by the tensor cores in principle (4 x 256 x 128 x D flops a tile take 2048
 // cycles at D = 128).  Measured on four prompts' chunks of 512 rows after contexts to
-// 8K, 32 heads over 8, D = 128: 86 us, 0.56 PFLOP/s of the seen positions (84.5 with a
-// reference that lags by 2^8).  A CTA's
+// 8K, 32 heads over 8, D = 128: 84 us, 0.57 PFLOP/s of the seen positions (a reference that
+// lags by 2^8: 1.5 us less).  A CTA's
 // 20 tiles take some 5200 cycles each (a half's softmax, 3300 while it shares the
 // schedulers with the other half's and the widening, and its products, 1024, follow
 // one another); the start, the queries of two parts and the records of split items

@@ -252,6 +252,11 @@ def test_hold_counts_a_table_made_by_hand():
     b.table[2, 0], b.table[2, 1] = 7, -1
     futr.futr_pages_free(b.cache, b.pool, ints([48, 33, 0]), b.table)
     b.same(futr.FUTR_ERR_NOT_HELD)
+    # nor written
+    b.table[2, 0] = 8
+    futr.futr_pages_grow(b.cache, b.pool, ints([48, 64, 0]), starts([0, 0, 20]), b.table)
+    b.table[2, 0] = -1
+    b.same(futr.FUTR_ERR_NOT_HELD)
 
 
 @pytest.mark.parametrize("seed", range(6))
