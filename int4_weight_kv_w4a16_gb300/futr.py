@@ -603,28 +603,30 @@ def futr_beam_select(logits, scores, score_out, parent, token, ws, done=None, do
     T = _T or _torch()
     device = T.device()
     f32, i32 = T.float32, T.int32
-    shape, kept = scores.shape, score_out.shape
+    shape, kept, rows = scores.shape, score_out.shape, logits.shape
     if len(shape) != 2 or len(kept) != 2 or kept[0] != shape[0]:
         raise ValueError(f"scores and score_out must be [batch, beams] and [batch, keep], not {tuple(shape)} and "
                          f"{tuple(kept)}")
     batch, beams = shape
-    n = batch * beams
     dtype = T.logits.get(logits.dtype)
     if dtype is None:
         raise TypeError(f"logits must be float32, bfloat16 or float16, not {logits.dtype}")
-    if (logits.dim() != 2 or logits.shape[0] != n or (logits.stride(1) != 1 and logits.shape[1] > 1) or
-            logits.get_device() != device):
+    n = batch * beams
+    if len(rows) != 2 or rows[0] != n or logits.get_device() != device:
         _bad_tensor(logits, "logits", f"rows ({n}, vocab), a row contiguous,", device)
-    vocab = logits.shape[1]
-    ld = logits.stride(0) if n > 1 else vocab
+    vocab, (ld, step) = rows[1], logits.stride()
+    if step != 1 and vocab > 1:
+        _bad_tensor(logits, "logits", f"rows ({n}, vocab), a row contiguous,", device)
     if ws._mem.get_device() != device:
         _elsewhere(ws, "the workspace", device)
-    _ok(lib().futr_beam_select(logits.data_ptr(), ld, dtype, batch, beams, vocab,
-                               _dense(scores, "scores", f32, shape, device), _dense(done, "done", i32, shape, device),
-                               end, kept[1], int(stay), _dense(score_out, "score_out", f32, kept, device),
+    _ok(lib().futr_beam_select(logits.data_ptr(), ld if n > 1 else vocab, dtype, batch, beams, vocab,
+                               _dense(scores, "scores", f32, shape, device),
+                               None if done is None else _dense(done, "done", i32, shape, device), end, kept[1],
+                               1 if stay else 0, _dense(score_out, "score_out", f32, kept, device),
                                _dense(parent, "parent", i32, kept, device), _dense(token, "token", i32, kept, device),
-                               _dense(done_out, "done_out", i32, kept, device), C.addressof(ws),
-                               T.stream(device) if stream is None else _stream(stream)), "futr_beam_select")
+                               None if done_out is None else _dense(done_out, "done_out", i32, kept, device),
+                               C.addressof(ws), T.stream(device) if stream is None else _stream(stream)),
+        "futr_beam_select")
 
 
 def futr_beam_check(ws, stream=None) -> int:
