@@ -189,86 +189,94 @@ __device__ __forceinline__ int tc_at(int r, int i) {
 
 // The rows of one half that belong to this softmax warp (32 of them), rotated,
 // divided by a power of two and stored as f16 (rows past `valid` as zeros); their
-// score factors to qs.  A lane holds the rotation pairs 2 lane, 2 lane + 1 (D = 64:
-// pair `lane`) of a row; the loads of eight rows are in flight together.
+// score factors to qs.  16 lanes take a row, a lane D / 32 rotation pairs of it; the
+// loads of eight rows are in flight together.
 template <int D, bool kHalf>
 __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Walk& w, int valid, int half, uint8_t* q16,
                                                 float* qs) {
-  constexpr int P = D / 64, RW = 8;   // pairs of a lane, rows at a time
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, at = P * lane;
-  uint32_t lo[RW], hi[RW];
+  constexpr int P = D / 32, RW = 4;   // pairs of a lane, steps of two rows at a time
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, sub = lane >> 4, at = P * (lane & 15);
+  uint32_t lo[RW][P / 2], hi[RW][P / 2];
   float2 cs[RW][P];
   auto load = [&](int r0) {
-    const int row = w.rt * kTcRows + kTcHalf * half + r0;
+    const int row = w.rt * kTcRows + kTcHalf * half + r0 + sub;
     int i = row / a.G, g = row - i * a.G;
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
-      lo[k] = hi[k] = 0u;
+#pragma unroll
+      for (int j = 0; j < P / 2; ++j) lo[k][j] = hi[k][j] = 0u;
 #pragma unroll
       for (int j = 0; j < P; ++j) cs[k][j] = make_float2(1.f, 0.f);
-      if (kTcHalf * half + r0 + k < valid) {
+      if (kTcHalf * half + r0 + 2 * k + sub < valid) {
         const uint16_t* q = static_cast<const uint16_t*>(a.q) + (size_t)(w.row0 + i) * a.ld_q +
                             (size_t)(w.kvh * a.G + g) * D + at;
-        if (P == 2) {
-          lo[k] = *reinterpret_cast<const uint32_t*>(q);
-          hi[k] = *reinterpret_cast<const uint32_t*>(q + D / 2);
+        if (P == 4) {
+          const uint2 l = *reinterpret_cast<const uint2*>(q), h = *reinterpret_cast<const uint2*>(q + D / 2);
+          lo[k][0] = l.x, lo[k][P / 2 - 1] = l.y;
+          hi[k][0] = h.x, hi[k][P / 2 - 1] = h.y;
         } else {
-          lo[k] = *q;
-          hi[k] = q[D / 2];
+          lo[k][0] = *reinterpret_cast<const uint32_t*>(q);
+          hi[k][0] = *reinterpret_cast<const uint32_t*>(q + D / 2);
         }
         if (a.c.rope) {
-          const float2* c = a.c.rope + (size_t)(w.p0 + i) * (D / 2) + at;
-          if (P == 2) {
-            const float4 c2 = *reinterpret_cast<const float4*>(c);
-            cs[k][0] = make_float2(c2.x, c2.y);
-            cs[k][P - 1] = make_float2(c2.z, c2.w);
-          } else {
-            cs[k][0] = *c;
+          const float4* c = reinterpret_cast<const float4*>(a.c.rope + (size_t)(w.p0 + i) * (D / 2) + at);
+#pragma unroll
+          for (int j = 0; j < P / 2; ++j) {
+            const float4 c2 = c[j];
+            cs[k][2 * j] = make_float2(c2.x, c2.y);
+            cs[k][2 * j + 1] = make_float2(c2.z, c2.w);
           }
         }
       }
-      if (++g == a.G) {
-        g = 0;
-        ++i;
-      }
+      g += 2;   // two rows on
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (g >= a.G) {
+          g -= a.G;
+          ++i;
+        }
     }
   };
 #pragma unroll 1
-  for (int r0 = 32 * warp; r0 < 32 * warp + 32; r0 += RW) {
+  for (int r0 = 32 * warp; r0 < 32 * warp + 32; r0 += 2 * RW) {
     load(r0);
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
+      const int r = r0 + 2 * k + sub;
       float x[2][P], mx = 0.f;
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        const float x1 = widen<kHalf>((uint16_t)(lo[k] >> (16 * j))), x2 = widen<kHalf>((uint16_t)(hi[k] >> (16 * j)));
+        const float x1 = widen<kHalf>((uint16_t)(lo[k][j / 2] >> (16 * (j & 1)))),
+                    x2 = widen<kHalf>((uint16_t)(hi[k][j / 2] >> (16 * (j & 1))));
         x[0][j] = x1 * cs[k][j].x - x2 * cs[k][j].y;
         x[1][j] = x2 * cs[k][j].x + x1 * cs[k][j].y;
         mx = fmaxf(mx, fmaxf(fabsf(x[0][j]), fabsf(x[1][j])));
       }
-      // the largest magnitude: magnitudes order like their bits
-      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);   // (2^-e is normal, too)
+      // the largest magnitudes of both rows: magnitudes order like their bits
+      const uint32_t m0 = __reduce_max_sync(0xffffffffu, sub ? 0u : __float_as_uint(mx));
+      const uint32_t m1 = __reduce_max_sync(0xffffffffu, sub ? __float_as_uint(mx) : 0u);
+      const int e = min(max((int)((sub ? m1 : m0) >> 23) - 127, -126), 126);   // (2^-e is normal, too)
       const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint8_t* dst = q16 + tc_at(r0 + k, at + h * (D / 2));
+        uint8_t* dst = q16 + tc_at(r, at + h * (D / 2));
         float v[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) v[j] = x[h][j] * inv;
 #pragma unroll
         for (int part = 0; part < kTcParts<kHalf>; ++part) {
-          if (P == 2)
-            *reinterpret_cast<uint32_t*>(dst + part * (kTcHalf * D * 2)) = pack_half2(v[0], v[P - 1]);
+          if (P == 4)
+            *reinterpret_cast<uint2*>(dst + part * (kTcHalf * D * 2)) =
+                make_uint2(pack_half2(v[0], v[1]), pack_half2(v[P - 2], v[P - 1]));
           else
-            *reinterpret_cast<__half*>(dst + part * (kTcHalf * D * 2)) = __float2half_rn(v[0]);
+            *reinterpret_cast<uint32_t*>(dst + part * (kTcHalf * D * 2)) = pack_half2(v[0], v[1]);
 #pragma unroll
           for (int j = 0; j < P; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
         }
       }
-      if (lane == 0)
-        qs[kTcHalf * half + r0 + k] =
-            kTcHalf * half + r0 + k < valid ? __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2 : 0.f;
+      if ((lane & 15) == 0)
+        qs[kTcHalf * half + r] =
+            kTcHalf * half + r < valid ? __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2 : 0.f;
     }
   }
 }
