@@ -32,7 +32,7 @@
 //
 // Bound by the tensor cores in principle (4 x 256 x 128 x D flops a tile take 2048
 // cycles at D = 128).  Measured on four prompts' chunks of 512 rows after contexts to
-// 8K, 32 heads over 8, D = 128: 84 us, 0.57 PFLOP/s of the seen positions (a reference that
+// 8K, 32 heads over 8, D = 128: 82 us, 0.59 PFLOP/s of the seen positions (a reference that
 // lags by 2^8: 1.5 us less).  A CTA's
 // 20 tiles take some 5200 cycles each (a half's softmax, 3300 while it shares the
 // schedulers with the other half's and the widening, and its products, 1024, follow
@@ -190,7 +190,9 @@ __device__ __forceinline__ int tc_at(int r, int i) {
 // The rows of one half that belong to this softmax warp (32 of them), rotated,
 // divided by a power of two and stored as f16 (rows past `valid` as zeros); their
 // score factors to qs.  16 lanes take a row, a lane D / 32 rotation pairs of it; the
-// loads of eight rows are in flight together.
+// loads of eight rows are in flight together.  (A warp a row: 84.2 us for the chunks of the
+// head comment, 6.5 of them an item's first queries, that take 5.5 here.  Their way to L2
+// while the item before is still at work changed nothing.)
 template <int D, bool kHalf>
 __device__ __forceinline__ void tc_load_queries(const PagedAttnArgs& a, const Walk& w, int valid, int half, uint8_t* q16,
                                                 float* qs) {
@@ -342,7 +344,7 @@ __device__ __forceinline__ TcScale tc_scale_of(const float4* sc, int c, float qf
 // see some.  A warp's 32 rows are few tokens, so the borders of a tile that is cut (by a
 // row's own position, its window, the sinks) lie in one or two of its chunks.
 // (Comparisons for all four: 74 us for the fp16 chunks of a window of 1000 with 100 sinks
-// that take 69.5, 85.8 for the chunks of the head comment that take 84.2.)
+// that took 69.5 so, 85.8 for the chunks of the head comment that took 84.2.)
 enum TcChunk { kNone, kSome, kAll };
 template <bool kSinks>
 __device__ __forceinline__ TcChunk tc_chunk(int c, const TcSight& v) {

@@ -340,6 +340,24 @@ def test_candidates_of_nearly_one_value():
     assert parent[0].tolist() == [0] * 64 and token[0].tolist() == [7 + 2 * i for i in range(64)]
 
 
+def test_logits_beyond_32_bits():
+    """20000 rows, 2.6e9 logits: the last prompts by themselves give the same."""
+    batch, beams, V = 2500, 8, 128256
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty((batch * beams, V), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, batch * beams, 2000):
+        x[i:i + 2000] = torch.randn((2000, V), generator=g, device="cuda").to(torch.bfloat16) * 3
+    s = scores_of(batch, beams, 2)
+    score, parent, token, _ = select(x, s, beams)
+    for b in (0, 1200, 2096, 2499):
+        one = select(x[b * beams:(b + 1) * beams].clone(), s[b:b + 1].clone(), beams)
+        # (other parts: the sums differ by their roundings)
+        assert float((one[0] - score[b]).abs().max()) <= 2 * beam_tolerance(V) + 30 * 2.0 ** -23
+        assert torch.equal(one[1] + b * beams, parent[b:b + 1]) and torch.equal(one[2], token[b:b + 1])
+    check(x[-4 * beams:], s[-4:], beams, got=[score[-4:], parent[-4:] - (batch - 4) * beams, token[-4:],
+                                              torch.zeros_like(token[-4:])])
+
+
 # ----------------------------------------------------------------- reorder --
 
 class Slots:
@@ -392,6 +410,19 @@ def test_reorder(case):
         assert torch.equal(s.streams, want)
         pos = [pos[q] if q >= 0 else 0 for q in parent]
         assert p.tolist() == pos
+
+
+def test_reorder_beyond_32_bits():
+    """A cache of 8.9 GB: slots of the first and the last layer."""
+    s = Slots(32, 32, 8, 128, 8192, 3)
+    parent, pos = [(i * 7 + 3) % 32 for i in range(32)], [8192 - i for i in range(32)]
+    first, last = s.streams[0].clone(), s.streams[-1].clone()
+    futr.futr_kv_reorder(s.kv, ints(parent), ints(pos))
+    assert futr.futr_check(kv=s.kv) == futr.FUTR_OK
+    got = s.streams[0].clone(), s.streams[-1].clone()
+    for was, now in zip((first, last), got):
+        s.streams = was[None]
+        assert torch.equal(s.moved(parent, pos)[0], now)
 
 
 def test_reorder_moves_what_kv_read_gives():

@@ -294,6 +294,17 @@ def test_random_runs(seed):
         b.same(status)
 
 
+def test_pages_beyond_32_bits():
+    """A cache of 5.4 GB: copies of a fork and moves of its pages in the last layer."""
+    b = Both(300, 128, 4, 70, layers=70, hkv=8, d=128)
+    pos = [8000, 120, 0, 0]
+    assert b.grow([0] * 4, pos)
+    pos = b.fork([0, 1, 1, 0], pos)
+    b.same()
+    assert b.compact(0, 140)
+    b.same()
+
+
 def test_many_sequences_and_pages():
     """The largest table: 1024 sequences, pages over several rounds of the search."""
     b = Both(70000, 16, 1024, 64, layers=1, hkv=1)
