@@ -5,9 +5,9 @@
 // before it writes any, so slots may trade places and one slot may go to several.  All of
 // them are in registers at once, for as many moves as the call's batch can have: so many
 // loads are in flight together (one after another through shared memory took 559 us for 32
-// slots of 16 layers, 1.1 GB read and written, that take 170 here).  A stream has four runs
+// slots of 16 layers, 1.0 GB read and written, that take 160 here).  A stream has four runs
 // (codes of keys and of values, their scales) of which the first tiles move; threads count
-// through those alone.  Bound by memory: 6.4 TB/s for those, 0.95 of the copy rate.
+// through those alone.  Bound by memory: 6.3 TB/s for those, 0.93 of the copy rate.
 #include "pages.cuh"
 
 namespace futr {
@@ -93,10 +93,11 @@ __device__ __forceinline__ void move_columns(const ReorderArgs& a, const Moves& 
 }
 
 // M: most moves of the batch.  Few take more columns at once, 8 loads a thread at least: one
-// slot of 32 layers at 900 positions, from memory, 13.6 us (two loads: 15.3).  Three CTAs an
-// SM (168 registers) for 32 moves: 170 us, two (189) 187.
+// slot of 32 layers at 900 positions, from memory, 13.1 us (two loads: 15.3).  Three CTAs an
+// SM (168 registers) for 32 moves: 170 us, two (189) 187; for 16 (147 us) four would not hold
+// the data (223).
 template <int M>
-__global__ void __launch_bounds__(kKrThreads, M > 16 ? 3 : 4) kv_reorder_kernel(const ReorderArgs a) {
+__global__ void __launch_bounds__(kKrThreads, M > 16 ? 3 : 2) kv_reorder_kernel(const ReorderArgs a) {
   __shared__ Moves mv;
   pdl_trigger();
   pdl_wait();
@@ -168,10 +169,15 @@ cudaError_t kr_launch(F* f, int grid, int threads, const ReorderArgs& a, cudaStr
   return cudaLaunchKernelEx(&cfg, f, a);
 }
 
-// CTAs that run at once.
+// CTAs: those that run at once, several times, so that late ones find what is left.  Times 1,
+// 2, 4 and 6: one slot 13.8, 13.1, 13.6, 14.1 us; 16 147.7, 147.2, 145.0, 148.6; 32 174, 172,
+// 165, 159.
+template <int M>
+constexpr int kKrWaves = M > 16 ? 6 : M > 8 ? 4 : 2;
+
 template <int M>
 int kr_ctas(int dev, int sms) {
-  return sms * remembered(occ_key(dev, M, 0, 0), [&]() {
+  return kKrWaves<M> * sms * remembered(occ_key(dev, M, 0, 0), [&]() {
            int n = 0;
            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_reorder_kernel<M>, kKrThreads, 0) != cudaSuccess ||
                n < 1) {
@@ -184,7 +190,9 @@ int kr_ctas(int dev, int sms) {
 
 template <int M>
 cudaError_t kr_run(const ReorderArgs& a, int dev, int sms, cudaStream_t st) {
-  return kr_launch(kv_reorder_kernel<M>, kr_ctas<M>(dev, sms), kKrThreads, a, st);
+  const long long most = (long long)a.n_layers * a.n_kv * (long long)((a.stream_bytes / 16 + kKrThreads - 1) / kKrThreads);
+  const int ctas = kr_ctas<M>(dev, sms);
+  return kr_launch(kv_reorder_kernel<M>, most < ctas ? (int)most : ctas, kKrThreads, a, st);
 }
 
 }  // namespace
