@@ -41,6 +41,7 @@ __device__ __forceinline__ void release(const PoolView& p, int id, int n) {
   } else if (old == n) {
     atomicOr(&p.free[id >> 5], 1u << (id & 31));
     atomicAdd(&p.err[2], 1);
+    if ((id >> 5) < *static_cast<volatile int*>(&p.err[3])) atomicMin(&p.err[3], id >> 5);
   }
 }
 
@@ -68,7 +69,7 @@ __global__ void pages_init_kernel(const PoolView p) {
   const int i = blockIdx.x * kPgThreads + threadIdx.x;
   if (i < p.n_pages) p.refs[i] = 0;
   if (i < p.words) p.free[i] = valid_bits(p, i);
-  if (i == 0) p.err[2] = p.n_pages;
+  if (i == 0) p.err[2] = p.n_pages, p.err[3] = 0;
 }
 
 __global__ void __launch_bounds__(kPgThreads) pages_hold_kernel(const PagesArgs a) {
@@ -128,13 +129,13 @@ __device__ __forceinline__ int scan(int v, int* words, int& total) {
   return incl - v + __shfl_sync(0xffffffffu, ws - w, warp);
 }
 
-// The first `want` set bits of words[0 .. n) as numbers into list, in order (mask: bits
-// of a word that count).  Returns how many there were (at most want).
+// The first `want` set bits of words [first, n) as numbers into list, in order.  Returns how
+// many there were (at most want).
 template <class F>
-__device__ __forceinline__ int list_bits(const F& word, int n, int want, int* list, int* words) {
+__device__ __forceinline__ int list_bits(const F& word, int first, int n, int want, int* list, int* words) {
   int done = 0;
-  for (int base = 0; base < n && done < want; base += kPgPlan) {
-    const int i = base + threadIdx.x;
+  for (long long base = first; base < n && done < want; base += kPgPlan) {
+    const int i = (int)min(base + threadIdx.x, (long long)n);
     unsigned w = i < n ? word(i) : 0u;
     int total;
     int r = done + scan(__popc(w), words, total);
@@ -144,16 +145,20 @@ __device__ __forceinline__ int list_bits(const F& word, int n, int want, int* li
   return min(done, want);
 }
 
-// The first `want` free pages into list, with the count `refs`; there are that many.
-__device__ __forceinline__ void take(const PoolView& p, int want, int* list, int* words) {
-  list_bits([&](int i) { return p.free[i]; }, p.words, want, list, words);
+// The first `want` > 0 free pages into list, held once; there are that many, none before word
+// `first`.
+__device__ __forceinline__ void take(const PoolView& p, int first, int want, int* list, int* words) {
+  list_bits([&](int i) { return p.free[i]; }, first, p.words, want, list, words);
   __syncthreads();
   for (int k = threadIdx.x; k < want; k += kPgPlan) {
     const int id = list[k];
     p.refs[id] = 1;
     atomicAnd(&p.free[id >> 5], ~(1u << (id & 31)));
   }
-  if (threadIdx.x == 0) p.err[2] -= want;
+  if (threadIdx.x == 0) {
+    p.err[2] -= want;
+    p.err[3] = list[want - 1] >> 5;   // the lowest are gone
+  }
 }
 
 // Rows of sequence b in `grow`: its pages [i0, i1) (none: i0 == i1).
@@ -177,6 +182,7 @@ __global__ void __launch_bounds__(kPgPlan) pages_grow_kernel(const PagesArgs a) 
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
+  const int n_free = a.p.err[2], word = a.p.err[3];
   int i0 = 0, i1 = 0, places;
   if (tid < a.batch) grow_pages(a, tid, i0, i1, true);
   const int before = scan(i1 - i0, words, places);
@@ -210,12 +216,11 @@ __global__ void __launch_bounds__(kPgPlan) pages_grow_kernel(const PagesArgs a) 
     return;
   }
   if (need == 0) return;
-  if (need > a.p.err[2]) {
+  if (need > n_free) {
     if (tid == 0) set_err(a.p.err, FUTR_ERR_NO_PAGES);
     return;
   }
-  __syncthreads();   // the count of free pages has been read
-  take(a.p, need, list, words);
+  take(a.p, word, need, list, words);
   __syncthreads();
   if (places <= kPgPlan) {
     if (mine) *e = list[at];
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(kPgPlan) fork_plan_kernel(const PagesArgs a) {
   __shared__ int s_bad;
   pdl_trigger();
   pdl_wait();
-  const int i = threadIdx.x;
+  const int i = threadIdx.x, n_free = a.p.err[2], word = a.p.err[3];
   const int most = (int)min((long long)a.c.max_pos, (long long)a.table_ld << a.c.page_log2);
   if (i == 0) s_bad = 0;
   int parent = -1;
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(kPgPlan) fork_plan_kernel(const PagesArgs a) {
   const bool copy = parent >= 0 && !s_bad && (!one || others) && from >= 0;
   int total;
   const int k = scan(copy, words, total);
-  const bool ok = !s_bad && total <= a.p.err[2];
+  const bool ok = !s_bad && total <= n_free;
   if (i == 0) {
     a.p.plan[0] = ok ? total : 0;
     a.p.plan[1] = ok;
@@ -277,8 +282,7 @@ __global__ void __launch_bounds__(kPgPlan) fork_plan_kernel(const PagesArgs a) {
   }
   if (!ok) return;
   int* list = plan_to(a.p);
-  __syncthreads();   // the count of free pages has been read
-  if (total > 0) take(a.p, total, list, words);
+  if (total > 0) take(a.p, word, total, list, words);
   __syncthreads();
   if (i < a.batch) {
     if (copy) {
@@ -397,6 +401,7 @@ __global__ void __launch_bounds__(kPgPlan) compact_plan_kernel(const PagesArgs a
   pdl_trigger();
   pdl_wait();
   const PoolView& p = a.p;
+  const int word = p.err[3];
   // pages of word i inside [lo, hi)
   auto inside = [&](int i) {
     const int lo = a.lo - i * 32, hi = a.hi - i * 32;
@@ -406,8 +411,9 @@ __global__ void __launch_bounds__(kPgPlan) compact_plan_kernel(const PagesArgs a
     return m;
   };
   int *from = plan_from(p), *to = plan_to(p), *where = plan_slots(p);
-  const int moves = list_bits([&](int i) { return ~p.free[i] & inside(i) & valid_bits(p, i); }, p.words, p.n_pages, from, words);
-  const int room = list_bits([&](int i) { return p.free[i] & ~inside(i); }, p.words, moves, to, words);
+  const int moves = list_bits([&](int i) { return ~p.free[i] & inside(i) & valid_bits(p, i); }, a.lo >> 5,
+                              (int)((a.hi + 31ll) >> 5), p.n_pages, from, words);
+  const int room = list_bits([&](int i) { return p.free[i] & ~inside(i); }, word, p.words, moves, to, words);
   const bool ok = room == moves;
   if (threadIdx.x == 0) {
     p.plan[0] = ok ? moves : 0;
@@ -415,6 +421,8 @@ __global__ void __launch_bounds__(kPgPlan) compact_plan_kernel(const PagesArgs a
     if (!ok) set_err(p.err, FUTR_ERR_NO_PAGES);
   }
   if (!ok) return;
+  __syncthreads();
+  if (threadIdx.x == 0 && moves > 0) p.err[3] = min(word, from[0] >> 5);
   for (int i = a.lo + threadIdx.x; i < a.hi; i += kPgPlan) where[i] = i;
   __syncthreads();
   for (int k = threadIdx.x; k < moves; k += kPgPlan) {

@@ -14,7 +14,7 @@ struct PoolView {
   int* refs;            // [n_pages] places that name a page
   unsigned* free;       // [words] bit p % 32 of word p / 32: page p is free
   int* plan;            // what a call decided: see below
-  int* err;             // error word; word 2: the number of free pages
+  int* err;             // error word; word 2: the number of free pages; word 3: no word of `free` before it has one
   int n_pages, words;
 };
 

@@ -319,6 +319,14 @@ def test_many_sequences_and_pages():
     b.same()
     assert b.compact(20000, 70000) and b.compact(0, 40000)
     b.same()
+    new = [int(n) for n in r.integers(0, 40, 1024)]
+    assert b.grow(pos, new)
+    b.same()
+    b.free([p if i % 3 else 0 for i, p in enumerate(pos)])
+    b.same()
+    pos = [p if i % 3 else 0 for i, p in enumerate(pos)]
+    assert b.grow(pos, [33] * 1024)
+    b.same()
 
 
 def test_a_search_in_a_graph():
