@@ -320,13 +320,14 @@ def test_many_sequences_and_pages():
     assert b.compact(20000, 70000) and b.compact(0, 40000)
     b.same()
     new = [int(n) for n in r.integers(0, 40, 1024)]
+    fits = lambda new: OK if all(p + n <= 1024 for p, n in zip(pos, new)) else futr.FUTR_ERR_OUT_OF_RANGE
     assert b.grow(pos, new)
-    b.same()
-    b.free([p if i % 3 else 0 for i, p in enumerate(pos)])
-    b.same()
+    b.same(fits(new))
     pos = [p if i % 3 else 0 for i, p in enumerate(pos)]
-    assert b.grow(pos, [33] * 1024)
+    b.free(pos)
     b.same()
+    assert b.grow(pos, [33] * 1024)
+    b.same(fits([33] * 1024))
 
 
 def test_a_search_in_a_graph():
