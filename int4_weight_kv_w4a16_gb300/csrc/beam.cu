@@ -45,6 +45,7 @@ constexpr int kBmMaxParts = 64;                   // parts of a row
 constexpr int kBmPerSm = 4;                       // CTAs an SM
 constexpr int kBmMaxWaves = 4;                    // parts of all rows, in CTAs that run at once
 constexpr double kBmStart = 4.0;                  // what a part costs beside its logits, in halves of tiles
+constexpr double kBmByRow = 6.0;                  // and the row's step
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Two fp32 numbers side by side, as one instruction takes them.
@@ -572,6 +573,10 @@ __device__ __forceinline__ void join_sums(const uint8_t* recs, int n, size_t ste
   S = warp_sum(S);
 }
 
+// i / d for i d < 2^32, by ceil(2^32 / d) (0: d is 1).
+__device__ __forceinline__ int quotient(int i, uint32_t by) { return by ? (int)__umulhi((uint32_t)i, by) : i; }
+uint32_t quotient_by(int d) { return d == 1 ? 0 : (uint32_t)(((1ull << 32) + d - 1) / d); }
+
 // A row's parts become one record.
 __device__ __forceinline__ void do_row(const BeamArgs& a, BmShared& sh, int row) {
   const int tid = threadIdx.x, K = a.keep;
@@ -584,23 +589,36 @@ __device__ __forceinline__ void do_row(const BeamArgs& a, BmShared& sh, int row)
     join_sums(parts, a.splits, step, M, S);
     if (tid == 0) put_stats(rec, M, S);
   }
+  if (tid == 0) sh.out = 0;
   constexpr int N = kBmMaxParts * kBeamMaxKeep / kBmThreads;
   unsigned long long key[N];
+  uint32_t top = 0;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
-    const int i = tid + q * kBmThreads;
+    const int i = tid + q * kBmThreads, r = quotient(i, a.by_keep);
     key[q] = 0;
     if (i < a.splits * K)
-      key[q] = __ldcg(reinterpret_cast<const unsigned long long*>(parts + (size_t)(i / K) * step + 16) + i % K);
+      key[q] = __ldcg(reinterpret_cast<const unsigned long long*>(parts + (size_t)r * step + 16) + i - r * K);
+    top = max(top, (uint32_t)(key[q] >> 32));
   }
-  int turn = 0;
-  put_keys(sh, key, select_key(key, K, sh.words, sh.range, turn), keys_of(rec));
-  for (int i = sh.out + tid; i < K; i += kBmThreads) keys_of(rec)[i] = 0;
+  const uint32_t low = reached(top, K, reinterpret_cast<uint32_t*>(sh.all));
+#pragma unroll
+  for (int q = 0; q < N; ++q)
+    if (key[q] != 0 && (uint32_t)(key[q] >> 32) >= low) {
+      const int to = atomicAdd(&sh.out, 1);
+      if (to < kBmShort) sh.list[to] = key[q];
+    }
+  __syncthreads();
+  const int n = sh.out;
+  if (n <= K) {
+    for (int i = tid; i < K; i += kBmThreads) keys_of(rec)[i] = i < n ? sh.list[i] : 0;
+  } else if (n <= kBmShort) {
+    sort_list(sh, n, K, keys_of(rec));
+  } else {
+    int turn = 0;
+    put_keys(sh, key, select_key(key, K, sh.words, sh.range, turn), keys_of(rec));
+  }
 }
-
-// i / d for i d < 2^32, by ceil(2^32 / d) (0: d is 1).
-__device__ __forceinline__ int quotient(int i, uint32_t by) { return by ? (int)__umulhi((uint32_t)i, by) : i; }
-uint32_t quotient_by(int d) { return d == 1 ? 0 : (uint32_t)(((1ull << 32) + d - 1) / d); }
 
 // A prompt's beams: the K best of their candidates, `lists` records a beam.
 __device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, const uint8_t* recs, int lists) {
@@ -775,7 +793,8 @@ cudaError_t launch_beam_select(const BeamArgs& args, int dtype, int sms, cudaStr
   double best = 1e30;
   a.splits = 1;
   for (int s = 1; s <= kBmMaxParts && s <= tiles && (s == 1 || rows * s <= beam_part_ctas(sms)); ++s) {
-    const double cost = (double)((rows * s + slots - 1) / slots) * ((double)tiles / s + kBmStart);
+    const double cost = (double)((rows * s + slots - 1) / slots) * ((double)tiles / s + kBmStart) +
+                        (a.beams * s * a.keep > kBmOne ? kBmByRow : 0.0);
     if (cost < best * 0.98) {
       best = cost;
       a.splits = s;
