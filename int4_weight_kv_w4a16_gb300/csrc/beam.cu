@@ -193,30 +193,34 @@ __device__ __forceinline__ unsigned long long select_key(const unsigned long lon
 
 // A value that at least k of the CTA's threads' values reach, and few more (0 where fewer
 // than k are not 0): the k-th largest of the ceil(k / 4) largest of each of the 8 warps.
-// (Counting for each of the 256 values those above took 2.4 us, 3.5 with four CTAs an SM.)
-__device__ __forceinline__ uint32_t reached(uint32_t v, int k, uint32_t* all) {
+// Each warp counts for its own of these those above, a half of the lanes over a half of them.
+// (Counting for each of the 256 values took 2.4 us, 3.5 with four CTAs an SM; every warp for
+// all of k = 64's 128 values 6 and 13.)
+__device__ __forceinline__ uint32_t reached(uint32_t v, int k, uint32_t* all, int* words) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = (k + 3) >> 2;   // 1 .. 16
   uint32_t mine = 0;
   for (int i = 0; i < each; ++i) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, v);
-    if (lane == i) mine = top;
+    if ((lane & 15) == i) mine = top;
     if (lane == __ffs(__ballot_sync(0xffffffffu, v == top)) - 1) v = 0;   // of equal values one goes
   }
   const int n = each * kBmWarps;
   if (lane < each) all[warp * each + lane] = mine;
   __syncthreads();
-  uint32_t low = ~0u;
-  for (int c = lane; c < n; c += 32) {   // every warp by itself
-    const uint32_t t = all[c];
-    int above = 0;
+  int above = 0;
 #pragma unroll 4
-    for (int i = 0; i < n; i += 4) {
-      const uint4 o = *reinterpret_cast<const uint4*>(all + i);
-      above += (o.x > t) + (o.y > t) + (o.z > t) + (o.w > t);
-    }
-    if (above < k) low = min(low, t);    // the least of those that fewer than k exceed
+  for (int i = lane & 16 ? n / 2 : 0; i < (lane & 16 ? n : n / 2); i += 4) {
+    const uint4 o = *reinterpret_cast<const uint4*>(all + i);
+    above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
   }
-  return __reduce_min_sync(0xffffffffu, low);
+  above += __shfl_xor_sync(0xffffffffu, above, 16);
+  // the least of those that fewer than k exceed
+  uint32_t low = __reduce_min_sync(0xffffffffu, (lane & 15) < each && above < k ? mine : ~0u);
+  if (lane == 0) words[warp] = (int)low;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kBmWarps; ++i) low = min(low, (uint32_t)words[i]);
+  return low;
 }
 
 template <int kType>
@@ -291,7 +295,7 @@ struct BmShared {
   };
   uint4 all[kBeamMaxKeep / 2];   // the warps' largest values: 2 keep, rounded up
   unsigned long long range[2 * kBmWarps];
-  int words[2 * kBmWarps];
+  int words[2 * kBmWarps], warps[kBmWarps];
   int n[3];                   // entries that a tile adds, three tiles in turn
   int out;
   unsigned last;
@@ -433,7 +437,7 @@ __device__ __forceinline__ void do_part(const BeamArgs& a, BmShared& sh, int row
       }
     }
     if (tile == 0) {
-      const uint32_t lo = reached(top > -INFINITY ? ordered(top) : 0u, K, reinterpret_cast<uint32_t*>(sh.all));
+      const uint32_t lo = reached(top > -INFINITY ? ordered(top) : 0u, K, reinterpret_cast<uint32_t*>(sh.all), sh.warps);
       if (lo >= kLowest) {
         thr = (unsigned long long)lo << 32;
         thr_x = unordered(lo);
@@ -577,6 +581,14 @@ __device__ __forceinline__ void join_sums(const uint8_t* recs, int n, size_t ste
 __device__ __forceinline__ int quotient(int i, uint32_t by) { return by ? (int)__umulhi((uint32_t)i, by) : i; }
 uint32_t quotient_by(int d) { return d == 1 ? 0 : (uint32_t)(((1ull << 32) + d - 1) / d); }
 
+// Which entry of record r index i takes: the records' entries one after another, each turned
+// by 5 against the one before, so that a thread (every 256th index) does not get the best of
+// all of them.
+__device__ __forceinline__ int entry_of(const BeamArgs& a, int i, int r) {
+  const int t = i - r * a.keep + 5 * r;
+  return t - quotient(t, a.by_keep) * a.keep;
+}
+
 // A row's parts become one record.
 __device__ __forceinline__ void do_row(const BeamArgs& a, BmShared& sh, int row) {
   const int tid = threadIdx.x, K = a.keep;
@@ -598,10 +610,10 @@ __device__ __forceinline__ void do_row(const BeamArgs& a, BmShared& sh, int row)
     const int i = tid + q * kBmThreads, r = quotient(i, a.by_keep);
     key[q] = 0;
     if (i < a.splits * K)
-      key[q] = __ldcg(reinterpret_cast<const unsigned long long*>(parts + (size_t)r * step + 16) + i - r * K);
+      key[q] = __ldcg(reinterpret_cast<const unsigned long long*>(parts + (size_t)r * step + 16) + entry_of(a, i, r));
     top = max(top, (uint32_t)(key[q] >> 32));
   }
-  const uint32_t low = reached(top, K, reinterpret_cast<uint32_t*>(sh.all));
+  const uint32_t low = reached(top, K, reinterpret_cast<uint32_t*>(sh.all), sh.warps);
 #pragma unroll
   for (int q = 0; q < N; ++q)
     if (key[q] != 0 && (uint32_t)(key[q] >> 32) >= low) {
@@ -633,7 +645,8 @@ __device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, 
   for (int q = 0; q < N; ++q) {
     const int i = tid + q * kBmThreads, r = quotient(i, a.by_keep);
     at[q] = 0;
-    if (i < W * lists * K) at[q] = __ldcg(reinterpret_cast<const unsigned long long*>(recs + (size_t)r * step + 16) + i - r * K);
+    if (i < W * lists * K)
+      at[q] = __ldcg(reinterpret_cast<const unsigned long long*>(recs + (size_t)r * step + 16) + entry_of(a, i, r));
   }
   for (int w = warp; w < W; w += kBmWarps) {
     const int row = b * W + w;
@@ -678,7 +691,7 @@ __device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, 
       top = max(top, (uint32_t)(val[q] >> 32));
     }
   }
-  const uint32_t low = reached(top, K, reinterpret_cast<uint32_t*>(sh.all));
+  const uint32_t low = reached(top, K, reinterpret_cast<uint32_t*>(sh.all), sh.warps);
 #pragma unroll
   for (int q = 0; q < N; ++q)
     if (val[q] != 0 && (uint32_t)(val[q] >> 32) >= low) sh.cand[atomicAdd(&sh.out, 1)] = make_ulonglong2(val[q], at[q]);
