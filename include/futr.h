@@ -615,8 +615,8 @@ futr_status futr_pages_free(const futr_paged* cache, const futr_pages* pool, int
  * page that is partly written (the one of position pos, when pos is no multiple of
  * the page) and pages taken ahead behind it stay with the parent's first child;
  * every further child gets a page of its own with a copy of the written positions
- * and the scales, in all layers (the first, too, if other places name the page).  Needs one free page a copy, beside those that the call itself gives
- * back.  A parent outside [-1, batch) or a pos outside [0, min(max_pos, table_ld *
+ * and the scales, in all layers (the first, too, if other places name the page).
+ * Needs one free page a copy, beside those that the call itself gives back.  A parent outside [-1, batch) or a pos outside [0, min(max_pos, table_ld *
  * page)] of a parent sets FUTR_ERR_OUT_OF_RANGE, and nothing is changed.
  */
 futr_status futr_pages_fork(const futr_paged* cache, const futr_pages* pool, int32_t batch, const int32_t* parent,
