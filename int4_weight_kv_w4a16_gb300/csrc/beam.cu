@@ -365,6 +365,49 @@ __device__ __forceinline__ void sort_list(BmShared& sh, int n, int K, unsigned l
   __syncthreads();
 }
 
+// The list's K largest of n > K to the front of it or to a record; the least of them, or a
+// value between it and the next.  (Out of line, as what follows: rare, and the way past it is
+// fetched in each call.)
+__device__ __noinline__ unsigned long long cut_list(BmShared& sh, int n, int K, unsigned long long* to) {
+  unsigned long long key[kBmList / kBmThreads];
+  int turn = 0;
+  __syncthreads();
+  read_list(sh, n, key);
+  const unsigned long long thr = select_key(key, K, sh.words, sh.range, turn);
+  put_keys(sh, key, thr, to);
+  return thr;
+}
+
+// A tile's logits x (kBmLogits a thread, W in a row, from vector `at` on) that reach thr to the
+// list of n entries, one a thread at a time, the list cut down between; its entries.
+template <int W>
+__device__ __noinline__ int crowded_tile(BmShared& sh, const float* x, int at, int K, int n, unsigned long long& thr) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll 1
+  for (int i = 0; i < kBmLogits; ++i) {
+    if (n > kBmList - kBmThreads) {
+      thr = cut_list(sh, n, K, sh.list);
+      n = K;
+    }
+    const int token = (at + tid + kBmThreads * (i / W)) * W + i % W;
+    const unsigned long long key = x[i] >= -FLT_MAX ? make_key(x[i], token) : 0;
+    const bool in = key != 0 && key >= thr;
+    const unsigned votes = __ballot_sync(0xffffffffu, in);
+    __syncthreads();   // the words have been read
+    if (lane == 0) sh.words[warp] = __popc(votes);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int q = 0; q < kBmWarps; ++q) {
+      before += q < warp ? sh.words[q] : 0;
+      all += sh.words[q];
+    }
+    if (in) sh.list[n + before + __popc(votes & ((1u << lane) - 1))] = key;
+    n += all;
+  }
+  return n;
+}
+
 // A part of a row: its record.
 template <int kType>
 __device__ __forceinline__ void do_part(const BeamArgs& a, BmShared& sh, int row, int part, uint8_t* rec) {
@@ -377,7 +420,7 @@ __device__ __forceinline__ void do_part(const BeamArgs& a, BmShared& sh, int row
   const int nv = (a.vocab - 1) / W + 1;
   const int v0 = (int)((long long)nv * part / a.splits), v1 = (int)((long long)nv * (part + 1) / a.splits);
   const int shift = (int)(reinterpret_cast<uintptr_t>(x) & 15);
-  int turn = 0, n = 0, tile = 0;               // sums made, entries of the list, tiles
+  int n = 0, tile = 0;                         // entries of the list, tiles
   const int kCut = max(2 * K, kBmCut);         // entries above which the list is cut
   float m = -INFINITY, s = 0.f;                // maximum, sum of 2^((x - m) log2 e)
   unsigned long long thr = 1;
@@ -480,11 +523,7 @@ __device__ __forceinline__ void do_part(const BeamArgs& a, BmShared& sh, int row
           sort_list(sh, n, K, sh.list);
           thr = sh.list[K - 1];
         } else {
-          unsigned long long key[kBmList / kBmThreads];
-          __syncthreads();
-          read_list(sh, n, key);
-          thr = select_key(key, K, sh.words, sh.range, turn);
-          put_keys(sh, key, thr, sh.list);
+          thr = cut_list(sh, n, K, sh.list);
         }
         thr_x = unordered((uint32_t)(thr >> 32));
         n = K;
@@ -493,37 +532,11 @@ __device__ __forceinline__ void do_part(const BeamArgs& a, BmShared& sh, int row
     }
     // too many at once: what the tile added is dropped, and added a logit a thread at a time,
     // the list cut down between
-#pragma unroll 1
-    for (int i = -1; i < P; ++i) {
-      if (i >= 0) {
-        float xi = logit(0);
+    float all[P];
 #pragma unroll
-        for (int q = 1; q < P; ++q) xi = q == i ? logit(q) : xi;
-        const unsigned long long key = xi >= thr_x ? make_key(xi, token(i)) : 0;
-        const bool in = key >= thr;
-        const unsigned votes = __ballot_sync(0xffffffffu, in);
-        int* w = sh.words + (turn++ & 1) * kBmWarps;
-        if (lane == 0) w[warp] = __popc(votes);
-        __syncthreads();
-        int before = 0, all = 0;
-#pragma unroll
-        for (int q = 0; q < kBmWarps; ++q) {
-          before += q < warp ? w[q] : 0;
-          all += w[q];
-        }
-        if (in) sh.list[n + before + __popc(votes & ((1u << lane) - 1))] = key;
-        n += all;
-      }
-      if (n > kBmList - kBmThreads) {
-        __syncthreads();
-        unsigned long long key[kBmList / kBmThreads];
-        read_list(sh, n, key);
-        thr = select_key(key, K, sh.words, sh.range, turn);
-        thr_x = unordered((uint32_t)(thr >> 32) < kLowest ? kLowest : (uint32_t)(thr >> 32));
-        put_keys(sh, key, thr, sh.list);
-        n = sh.out;
-      }
-    }
+    for (int i = 0; i < P; ++i) all[i] = logit(i);
+    n = crowded_tile<W>(sh, all, at, K, n, thr);
+    thr_x = unordered(max((uint32_t)(thr >> 32), kLowest));
   }
   // the part's K largest
   __syncthreads();
@@ -532,9 +545,7 @@ __device__ __forceinline__ void do_part(const BeamArgs& a, BmShared& sh, int row
   } else if (n <= kBmShort) {
     sort_list(sh, n, K, keys_of(rec));
   } else {
-    unsigned long long key[kBmList / kBmThreads];
-    read_list(sh, n, key);
-    put_keys(sh, key, select_key(key, K, sh.words, sh.range, turn), keys_of(rec));
+    cut_list(sh, n, K, keys_of(rec));
   }
   // its maximum and sum
   float M = m;
@@ -601,7 +612,7 @@ __device__ __forceinline__ int entry_of(const BeamArgs& a, int i, int r) {
 }
 
 // A row's parts become one record.
-__device__ __forceinline__ void do_row(const BeamArgs& a, BmShared& sh, int row) {
+__device__ __noinline__ void do_row(const BeamArgs& a, BmShared& sh, int row) {
   const int tid = threadIdx.x, K = a.keep;
   const size_t step = beam_record(K);
   const uint8_t* parts = a.parts + (size_t)row * a.splits * step;
