@@ -21,9 +21,10 @@
 // Short lists are put in order by counting, for each entry, those before it; of long ones
 // the k largest are found by bisection, a count over the CTA a step.
 //
-// 256 rows of 128256 fp32 logits (131 MB) take 33.4 us, of which the tiles 17 (at the rate of
-// memory), the way to the first threshold 5 and the steps behind the last tile 6; 4 rows 8.7
-// us, the same steps.  Not faster: a ring of bulk copies in place of the loads (39 us), and a
+// 256 rows of 128256 fp32 logits (131 MB) take 31.2 us, of which the tiles some 17 (at the
+// rate of memory), the way to the first threshold 4 and the steps behind the last tile 6; 4
+// rows 8.7 us, the same steps.  Fetching instructions is the largest of their waits, so the
+// rare steps are out of line (34.1 and 9.1 us with them in line).  Not faster: a ring of bulk copies in place of the loads (39 us), and a
 // persistent kernel whose ring runs on through its parts (42).
 #include <cfloat>
 #include <climits>
@@ -430,8 +431,8 @@ __device__ __forceinline__ void do_part(const BeamArgs& a, BmShared& sh, int row
   for (int at = v0; at < v1; at += kStep, ++tile) {
     uint32_t u[V][4];
     // a tile that lies in the part and the row as a whole, on 16-byte boundaries or off them,
-    // without checks (of 50257 logits, which are, 256 rows take 26.7 us with them for every
-    // vector)
+    // without checks (256 rows of 50257 logits, most of them off: 26.7 us with checks for every
+    // vector, 24.0 without)
     const bool whole = at + kStep <= v1 && (long long)(at + kStep + (shift != 0)) * W <= a.vocab;
     if (whole && shift == 0) {
       const uint4* p = reinterpret_cast<const uint4*>(x) + at + tid;
