@@ -508,7 +508,8 @@ futr_status futr_paged_attention_sinks(const futr_paged* cache, int32_t layer, i
  * end: -1 if no token ends a beam (done must be NULL then).  stay 1 (keep ==
  * beams): a beam's best child takes the beam's own place, the others the places
  * left, in order, so that the caches move as little as they have to.  Outputs
- * must not overlap inputs, but score_out may be scores and done_out may be done.
+ * must not overlap inputs, but where keep == beams score_out may be scores and
+ * done_out may be done.
  *
  * Logits of a row are compared exactly, values of beams in two fp32 parts (some 46
  * bits), as they are summed in.  A log-sum is fp32 within a thread's logits and two
@@ -616,8 +617,9 @@ futr_status futr_pages_free(const futr_paged* cache, const futr_pages* pool, int
  * the page) and pages taken ahead behind it stay with the parent's first child;
  * every further child gets a page of its own with a copy of the written positions
  * and the scales, in all layers (the first, too, if other places name the page).
- * Needs one free page a copy, beside those that the call itself gives back.  A parent outside [-1, batch) or a pos outside [0, min(max_pos, table_ld *
- * page)] of a parent sets FUTR_ERR_OUT_OF_RANGE, and nothing is changed.
+ * Needs one free page a copy, beside those that the call itself gives back.  A
+ * parent outside [-1, batch) or a pos outside [0, min(max_pos, table_ld * page)] of a
+ * parent sets FUTR_ERR_OUT_OF_RANGE, and nothing is changed.
  */
 futr_status futr_pages_fork(const futr_paged* cache, const futr_pages* pool, int32_t batch, const int32_t* parent,
                             int32_t* pos, int32_t* table, int32_t table_ld, void* stream);
