@@ -1,8 +1,8 @@
 // Pages of a paged cache on the device: counts of the places that name each page,
 // a bit per free page, and the calls that take, share, move and give back pages.
 //
-// Whatever threads add to or take from a count commutes, and so does setting and
-// clearing bits of pages that are not the same; a call that takes pages hands out
+// Whatever threads add to or take from a count commutes, and so does turning the bits of
+// pages over whose count becomes zero or leaves it; a call that takes pages hands out
 // the lowest free ones by rank.  So nothing depends on the order in which threads
 // arrive, and no list of free pages has to be kept in order.
 //
@@ -32,24 +32,31 @@ __device__ __forceinline__ int4* plan_seqs(const PoolView& p) {
   return reinterpret_cast<int4*>(p.plan + kPlanHeader + ((3 * (size_t)p.n_pages + 3) & ~size_t(3)));
 }
 
-// `n` places fewer (n > 0) name page id; the last one frees it.
-__device__ __forceinline__ void release(const PoolView& p, int id, int n) {
-  const int old = atomicSub(&p.refs[id], n);
-  if (old < n) {   // not held that often: as it was
-    atomicAdd(&p.refs[id], n);
-    set_err(p.err, FUTR_ERR_NOT_HELD);
-  } else if (old == n) {
-    atomicOr(&p.free[id >> 5], 1u << (id & 31));
-    atomicAdd(&p.err[2], 1);
-    if ((id >> 5) < *static_cast<volatile int*>(&p.err[3])) atomicMin(&p.err[3], id >> 5);
+// `n` more places name page id (n < 0: fewer); returns how many did before.  A page that no
+// place names is free: whoever takes its count across that border turns its bit over and
+// counts it among the free pages, or no longer.  Such crossings alternate, and turning over and
+// adding commute, so the bits and their number follow the counts in whatever order threads
+// arrive, whatever a table names.
+__device__ __forceinline__ int add_places(const PoolView& p, int id, int n) {
+  const int old = atomicAdd(&p.refs[id], n);
+  if ((old > 0) != (old + n > 0)) {
+    atomicXor(&p.free[id >> 5], 1u << (id & 31));
+    atomicAdd(&p.err[2], old > 0 ? 1 : -1);
+    if (old > 0 && (id >> 5) < *static_cast<volatile int*>(&p.err[3])) atomicMin(&p.err[3], id >> 5);
   }
+  return old;
+}
+
+// One place fewer names page id.
+__device__ __forceinline__ void release(const PoolView& p, int id) {
+  if (add_places(p, id, -1) > 0) return;
+  add_places(p, id, 1);   // not held: as it was
+  set_err(p.err, FUTR_ERR_NOT_HELD);
 }
 
 // `n` places more name page id, which some place does already.
 __device__ __forceinline__ void hold(const PoolView& p, int id, int n) {
-  if (atomicAdd(&p.refs[id], n) > 0) return;
-  atomicSub(&p.refs[id], n);
-  set_err(p.err, FUTR_ERR_NOT_HELD);
+  if (add_places(p, id, n) < 1) set_err(p.err, FUTR_ERR_NOT_HELD);
 }
 
 // An entry of a table as a page id, -1 if there is none (an id out of range counts as none).
@@ -78,10 +85,7 @@ __global__ void __launch_bounds__(kPgThreads) pages_hold_kernel(const PagesArgs 
   const long long n = (long long)a.batch * a.table_ld, step = (long long)gridDim.x * kPgThreads;
   for (long long i = (long long)blockIdx.x * kPgThreads + threadIdx.x; i < n; i += step) {
     const int id = page_of(a.p, a.table[i]);
-    if (id >= 0 && atomicAdd(&a.p.refs[id], 1) == 0) {
-      atomicAnd(&a.p.free[id >> 5], ~(1u << (id & 31)));
-      atomicSub(&a.p.err[2], 1);
-    }
+    if (id >= 0) add_places(a.p, id, 1);
   }
 }
 
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(kPgThreads) pages_free_kernel(const PagesArgs 
     if (e < 0 || (i < end && (i >= w0 || i < s1))) continue;
     row[i] = -1;
     const int id = page_of(a.p, e);
-    if (id >= 0) release(a.p, id, 1);
+    if (id >= 0) release(a.p, id);
   }
 }
 
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply_kernel(const PagesArgs 
       const int id = page_of(a.p, old[e]);
       if (id >= 0) {
         if (more < 0)
-          release(a.p, id, 1);
+          release(a.p, id);
         else
           hold(a.p, id, more);
       }

@@ -402,3 +402,47 @@ def test_a_search_in_a_graph():
         own.codes[:, at] = own.codes[:, at[p]].clone()
         own.scales[:, at] = own.scales[:, at[p]].clone()
     assert len(b.ref.free()) > rows * width // 3        # pages are shared
+
+
+def counts_agree(b):
+    """The free bits, their number and the counts say the same; returns the counts."""
+    n_free = futr.futr_pages_check(b.pool)[1]
+    refs = futr.pages_refs(b.pool).tolist()
+    at = b.pool.free_offset
+    words = b.pool._mem[at:at + 4 * (-(-b.ref.n // 32))].cpu().numpy().view(np.uint32)
+    free = [p for p in range(b.ref.n) if words[p // 32] >> (p % 32) & 1]
+    assert free == [p for p, r in enumerate(refs) if r == 0] and n_free == len(free)
+    assert min(refs) >= 0
+    return refs
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_tables_that_were_not_counted_in_full(seed):
+    """Tables of which only some rows were counted, shared pages among them: places are given back that the pool knows
+    nothing of, and others go on.  Whatever comes of the calls, the free bits follow the counts, and a page that is
+    taken was free."""
+    r = np.random.default_rng(seed)
+    page, rows, width = 16, int(r.choice([2, 5, 32])), int(r.integers(3, 12))
+    n = rows * width
+    b = Both(n, page, rows, width, layers=1, hkv=1, seed=seed)
+    for _ in range(12):
+        hand = r.integers(-1, max(2, n // int(r.integers(2, 20))), (rows, width)).astype(np.int32)
+        b.table.copy_(torch.from_numpy(hand))
+        some = [i for i in range(rows) if r.random() < 0.5] or [0]
+        futr.futr_pages_hold(b.cache, b.pool, b.table[some].contiguous())
+        pos = ints(r.integers(0, width * page + 1, rows).tolist())
+        counts_agree(b)
+        for _ in range(3):
+            parent = ints(r.integers(-1, rows, rows).tolist())
+            futr.futr_pages_fork(b.cache, b.pool, parent, pos, b.table)
+            counts_agree(b)
+        futr.futr_pages_free(b.cache, b.pool, pos, b.table, window=40, sinks=5)
+        was, before = counts_agree(b), b.table.clone()
+        futr.futr_pages_grow(b.cache, b.pool, pos, starts(r.integers(0, 20, rows).tolist()), b.table)
+        now = counts_agree(b)
+        new = b.table[b.table != before].tolist()
+        assert all(was[p] == 0 and now[p] == 1 for p in new) and len(set(new)) == len(new)
+        assert sum(now) == sum(was) + len(new)
+        futr.futr_pages_free(b.cache, b.pool, ints([0] * rows), b.table)
+        counts_agree(b)
+        futr.futr_pages_init(b.ref.n, rows, b.pool._mem)
