@@ -568,7 +568,11 @@ futr_status futr_kv_reorder(const futr_kv* kv, int32_t batch, const int32_t* par
  * A call that finds too few free pages sets FUTR_ERR_NO_PAGES and changes nothing.
  * A page id outside [0, n_pages) is treated as no page and sets
  * FUTR_ERR_OUT_OF_RANGE; giving back a page that the pool has free sets
- * FUTR_ERR_NOT_HELD.  futr_pages_check returns these.  Capturable in CUDA graphs. */
+ * FUTR_ERR_NOT_HELD.  Every page that a table names has to be held (futr_pages_hold):
+ * fork and compact look at all of the table first, and where it names a page that the
+ * pool has free they set FUTR_ERR_NOT_HELD and change nothing; grow looks at the pages
+ * that its rows meet, and may hand out a page that is named elsewhere and not held.
+ * futr_pages_check returns these.  Capturable in CUDA graphs. */
 typedef struct futr_pages {
   int32_t n_pages, max_seqs;
   void* base;

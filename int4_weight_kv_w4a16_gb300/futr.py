@@ -713,7 +713,7 @@ def futr_pages_free(cache, pool, pos, table, window=0, sinks=0, stream=None):
 
 
 def futr_pages_fork(cache, pool, parent, pos, table, stream=None):
-    """Row i of the table continues row parent[i] (-1: empty); pos follows."""
+    """Row i of the table continues row parent[i] (-1: empty); pos follows.  Every page that the table names is held."""
     T = _T or _torch()
     device = T.device()
     batch, ld = _pages(T, cache, pool, table, device)
@@ -724,7 +724,8 @@ def futr_pages_fork(cache, pool, parent, pos, table, stream=None):
 
 
 def futr_pages_compact(cache, pool, table, lo, hi=None, stream=None):
-    """Move the pages in use of [lo, hi) (hi None: the end) to the lowest free pages outside of it."""
+    """Move the pages in use of [lo, hi) (hi None: the end) to the lowest free pages outside of it.  Every page that
+    the table names is held."""
     T = _T or _torch()
     device = T.device()
     batch, ld = _pages(T, cache, pool, table, device)

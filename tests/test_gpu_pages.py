@@ -446,3 +446,68 @@ def test_tables_that_were_not_counted_in_full(seed):
         futr.futr_pages_free(b.cache, b.pool, ints([0] * rows), b.table)
         counts_agree(b)
         futr.futr_pages_init(b.ref.n, rows, b.pool._mem)
+
+
+NOT_HELD = [
+    # row and place of a table that is held but for one page there; its parents
+    (0, 0, [0, 0, -1]),       # shared with every child
+    (0, 1, [0, 0, -1]),       # the page that is partly written
+    (0, 3, [0, 0, -1]),       # taken ahead
+    (2, 1, [0, 0, -1]),       # of a sequence that ends
+    (1, 2, [0, 1, 2]),        # nothing to copy
+]
+
+
+@pytest.mark.parametrize("case", range(len(NOT_HELD)))
+@pytest.mark.parametrize("width", [4, 30000])        # a CTA looks at the table, and several
+def test_pages_that_are_not_held_are_not_written_over(case, width):
+    """A table made by hand of which a page was not counted: fork and compact would take that page for a copy. They change
+    nothing; once it is counted they do as ever."""
+    row, place, parent = NOT_HELD[case]
+    b = Both(40, 16, 3, width, seed=case, max_pos=1 << 16)
+    hand, pos = [[5, 6, 0, 8], [9, 10, 11, 12], [13, 14, 15, 16]], [20, 40, 33]
+    for i, r in enumerate(hand):
+        b.ref.table[i][:4] = r
+    b.ref.table[row][place] = 1 if (row, place) != (0, 2) else 0
+    missing = ints([[b.ref.table[row][place]]])
+    b.table.copy_(ints(b.ref.table))
+    part = b.table.clone()
+    part[row, place] = -1
+    futr.futr_pages_hold(b.cache, b.pool, part)
+    was = b.bits.clone(), b.scales.clone(), b.table.clone(), futr.pages_refs(b.pool).clone()
+
+    def unchanged():
+        now = b.bits, b.scales, b.table, futr.pages_refs(b.pool)
+        assert all(torch.equal(x, y) for x, y in zip(was, now))
+        assert futr.futr_pages_check(b.pool)[0] == OK
+        assert sum(counts_agree(b)) == 11
+
+    p = ints(pos)
+    for lo, hi in ((0, 20), (20, 40), (0, 0)):
+        for _ in range(2):
+            futr.futr_pages_fork(b.cache, b.pool, ints(parent), p, b.table)
+            assert futr.futr_pages_check(b.pool)[0] == futr.FUTR_ERR_NOT_HELD
+            assert p.tolist() == pos
+            unchanged()
+        futr.futr_pages_compact(b.cache, b.pool, b.table, lo, hi)
+        assert futr.futr_pages_check(b.pool)[0] == futr.FUTR_ERR_NOT_HELD
+        unchanged()
+    futr.futr_pages_hold(b.cache, b.pool, missing)
+    b.same()
+    pos = b.fork(parent, pos)
+    b.same()
+    assert b.compact(0, 20)
+    b.same()
+
+
+def test_a_table_that_is_not_counted_at_all():
+    """Two rows of pages 0 and 1, none counted: the partly written page is not copied over the first."""
+    b = Both(8, 16, 2, 4)
+    b.table[0, :2] = ints([0, 1])
+    was, p = b.bits.clone(), ints([20, 0])
+    futr.futr_pages_fork(b.cache, b.pool, ints([0, 0]), p, b.table)
+    assert futr.futr_pages_check(b.pool) == (futr.FUTR_ERR_NOT_HELD, 8)
+    assert torch.equal(b.bits, was) and p.tolist() == [20, 0] and b.table.tolist() == [[0, 1, -1, -1], [-1] * 4]
+    futr.futr_pages_compact(b.cache, b.pool, b.table, 0, 8)
+    assert futr.futr_pages_check(b.pool) == (futr.FUTR_ERR_NOT_HELD, 8)
+    assert torch.equal(b.bits, was) and b.table.tolist() == [[0, 1, -1, -1], [-1] * 4]
