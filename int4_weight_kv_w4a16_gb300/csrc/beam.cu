@@ -111,13 +111,6 @@ __device__ __forceinline__ Two log_of(Two x) {
   return add(add(add(Two{p, 0.f}, logf(f)), rest), __fdiv_rn(x.lo, x.hi));
 }
 
-// log sum e^x of S = sum of 2^((x - M) c), c the fp32 constant for log2 e: M + log S / (c ln 2).
-__device__ __forceinline__ Two log_sum(float M, Two S) {
-  constexpr float tiny = (float)(1.0 / ((double)kLog2e * 0.69314718055994530942) - 1.0);
-  const Two l = log_of(S);
-  return add(add(l, l.hi * tiny), M);
-}
-
 __device__ __forceinline__ unsigned long long make_key(float x, int v) {
   return ((unsigned long long)ordered(x) << 32) | (0xFFFFFFFFu - (uint32_t)v);
 }
@@ -683,7 +676,7 @@ __device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, 
       join_sums(recs + (size_t)w * lists * step, lists, step, M, S);
       const bool bad = !(S.hi <= FLT_MAX) || M == INFINITY;
       if (bad && (tid & 31) == 0) set_err(a.err, FUTR_ERR_NOT_FINITE);
-      if (!bad && M > -INFINITY) lse = log_sum(M, S);
+      if (!bad && M > -INFINITY) lse = add(log_of(S), M);
     } else if (score >= -FLT_MAX) {
       lse.hi = -INFINITY;        // ended: one candidate
     }

@@ -517,3 +517,22 @@ def ranked(score, parent, token):
     """Outputs best first, as check() takes them (no beam ends)."""
     order = torch.sort(score, dim=1, descending=True, stable=True).indices
     return [t.gather(1, order) for t in (score, parent, token)] + [torch.zeros_like(token)]
+
+
+# ------------------------------------------------- values of rows, to the bit --
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("V", [2, 1000, 8192, 50257, 128256, 1000003])
+def test_the_log_sum_of_equal_logits(V, dtype):
+    """n equal logits (the others -inf) have the log-sum M + log n.  Where M is 0 or a power of two, each exponent is
+    0, and n ones add up as they are: only the logarithm's own error (2^-26), sums in two parts (2^-46 of 32768) and the
+    value's rounding are left.  The score log n leaves a value near 0, which a rounding hides least."""
+    for M in (0.0, 1.0, -0.5, -4.0, 64.0, -32768.0):
+        for rows in (1, 40):
+            for n in {V, V // 2 + 1}:
+                x = torch.full((rows, V), -math.inf, dtype=dtype, device="cuda")
+                x[:, torch.randperm(V, device="cuda")[:n]] = M
+                s = torch.full((rows, 1), math.log(n), device="cuda")
+                score, _, _, _ = select(x, s, 1)
+                want = float(s[0, 0]) - math.log(n)
+                assert float((score.double() - want).abs().max()) <= 2.0 ** -25 + 2.0 ** -24 * abs(want), (M, rows, n)
