@@ -676,7 +676,11 @@ __device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, 
       join_sums(recs + (size_t)w * lists * step, lists, step, M, S);
       const bool bad = !(S.hi <= FLT_MAX) || M == INFINITY;
       if (bad && (tid & 31) == 0) set_err(a.err, FUTR_ERR_NOT_FINITE);
-      if (!bad && M > -INFINITY) lse = add(log_of(S), M);
+      if (!bad && M > -INFINITY) {
+        Two l = log_of(S);
+        if (!(l.hi > 0.f)) l = Two{0.f, 0.f};   // S holds e^0: less than 1 it is by roundings alone
+        lse = add(l, M);
+      }
     } else if (score >= -FLT_MAX) {
       lse.hi = -INFINITY;        // ended: one candidate
     }

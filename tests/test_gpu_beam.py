@@ -536,3 +536,51 @@ def test_the_log_sum_of_equal_logits(V, dtype):
                 score, _, _, _ = select(x, s, 1)
                 want = float(s[0, 0]) - math.log(n)
                 assert float((score.double() - want).abs().max()) <= 2.0 ** -25 + 2.0 ** -24 * abs(want), (M, rows, n)
+
+
+def log_sum_bound(x):
+    """What a row's log-sum may be off by at most, in units of u = 2^-24: the exponentials and the first factor of a tile
+    4 each (ex2.approx: 2^-22), 16 + 1 + 1 additions of a tile, 1 and 1/4 for the logarithm, two rescalings of 5 when a
+    part's and a row's threads meet, and for every tile (of 8192 logits) that a part has, one addition and a rescaling of 5;
+    the exponents' own roundings, and the constant's, 2.25 of the mean of max - x under the softmax."""
+    m = x.double().amax(-1, keepdim=True)
+    p = torch.softmax(x.double(), -1)
+    mean = torch.where(p > 0, p * (m - x.double()), 0.0).sum(-1)
+    return 2.0 ** -24 * (39 + 6 * -(-x.shape[-1] // 8192) + 2.25 * mean)
+
+
+@pytest.mark.parametrize("kind", ["normal", "wide", "far", "rising", "falling", "large", "two", "halves"])
+@pytest.mark.parametrize("V,rows", [(700, 5), (32000, 3), (128256, 1), (128256, 64), (128256, 700), (400000, 600)])
+def test_values_of_rows(kind, V, rows):
+    """The best token's value with a score that leaves it near 0, rows of one part and of many."""
+    g = torch.Generator(device="cuda").manual_seed(V + rows)
+    z = torch.randn((rows, V), generator=g, device="cuda")
+    up = torch.linspace(0, 9, V, device="cuda")
+    x = {"normal": z, "wide": 8 * z, "far": 2 * z - 3000, "rising": z * 0.1 + up, "falling": z * 0.1 + up.flip(0),
+         "large": z * 300 + 2.0 ** 20, "two": torch.where(z > 2, 1.5, -7.7), "halves": 7.3 - (z > 0).float() * 0.1}[kind]
+    m = x.double().amax(-1)
+    lse = m + torch.log(torch.exp(x.double() - m[:, None]).sum(-1))
+    s = (lse - m).float()[:, None].contiguous()
+    score, _, token, _ = select(x, s, 1)
+    want = x.double().gather(1, token.long())[:, 0] - lse + s[:, 0].double()
+    assert torch.equal(x.double().gather(1, token.long())[:, 0], m)
+    assert bool(((score[:, 0].double() - want).abs() <= log_sum_bound(x) + 2.0 ** -24 * want.abs()).all())
+
+
+def test_no_value_is_above_its_score():
+    """A token's probability is 1 at most, however near: one logit far above the others, at magnitudes whose exponents
+    are rounded, in one part and in many."""
+    for V, rows in ((50, 300), (20000, 300), (128256, 40), (128256, 700)):
+        g = torch.Generator(device="cuda").manual_seed(V + rows)
+        x = torch.randn((rows, V), generator=g, device="cuda")
+        at = torch.randint(0, V, (rows, 1), generator=g, device="cuda")
+        top = 200.0 + 900.0 * torch.rand((rows, 1), generator=g, device="cuda")
+        x.scatter_(1, at, top)
+        s = torch.where(torch.arange(rows, device="cuda") % 2 == 0, 0.0, -0.37)[:, None].contiguous()
+        score, _, token, _ = select(x, s, 1)
+        assert torch.equal(token, at.to(I32))
+        assert torch.equal(score, s)       # the others weigh less than e^-150
+        s = torch.zeros((rows, 1), device="cuda")
+        x = torch.where(x < 100, x + top - 18.0 - math.log(V), x)     # and some 2^-26 of it
+        score, _, token, _ = select(x, s, 1)
+        assert bool((score <= 0).all())
