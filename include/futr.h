@@ -511,13 +511,13 @@ futr_status futr_paged_attention_sinks(const futr_paged* cache, int32_t layer, i
  * must not overlap inputs, but where keep == beams score_out may be scores and
  * done_out may be done.
  *
- * Logits of a row are compared exactly, values of beams in two fp32 parts (some 46
- * bits), as they are summed in.  A log-sum is fp32 within a thread's logits and two
- * parts beyond: off by at most 2^-17 and 2^-21 for every 8192 logits of a row (2^-22
- * measured on normal logits), and never less than the row's largest logit, so that no
- * value is above its beam's score; equal rows have equal ones.  A value below fp32's
- * range is no candidate.  beams 1..32, keep 1..64, vocab below 2^31.  One kernel;
- * capturable in a CUDA graph. */
+ * Logits of a row are compared exactly: a beam's tokens go by their logits, whatever its
+ * score leaves of their differences.  Values of beams are compared in some 46 bits.  A
+ * log-sum is fp32 within a thread's logits and two parts beyond: off by at most 2^-17 and
+ * 2^-21 for every 8192 logits of a row (2^-22 measured on normal logits), and never less
+ * than the row's largest logit, so that no value is above its beam's score; equal rows
+ * have equal ones.  A value below fp32's range is no candidate.  beams 1..32, keep 1..64,
+ * vocab below 2^31.  One kernel; capturable in a CUDA graph. */
 #define FUTR_DTYPE_F32  2
 
 typedef struct futr_beam_ws {

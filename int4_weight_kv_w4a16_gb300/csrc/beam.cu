@@ -4,7 +4,7 @@
 //
 // L_w is the same for a whole row, so a row's candidates are its `keep` largest
 // logits (equal ones by the lowest token), compared as they are; only those meet the
-// other beams', as sums in two fp32 parts.  One pass over the logits, one kernel:
+// other beams', as sums in fp64.  One pass over the logits, one kernel:
 //   part   a CTA takes a part of a row in tiles, a thread 32 logits of a tile in registers:
 //          running maximum and sum of exponentials per thread, and every logit that reaches
 //          a threshold goes to a list in shared memory.
@@ -95,9 +95,19 @@ __device__ __forceinline__ Two add(Two x, float y) {
 }
 __device__ __forceinline__ Two add(Two x, Two y) { return add(add(x, y.hi), y.lo); }
 
-// Order-preserving form of a value in two parts, and its rounded part.
-__device__ __forceinline__ unsigned long long ordered64(Two x) {
-  return ((unsigned long long)ordered(x.hi) << 32) | ordered(x.lo);
+// A candidate's place in the order of a prompt, in two words: larger values first (an
+// order-preserving form of the fp64, its last five bits cut off), then lower beams; the second
+// word, the key turned over, larger logits and then lower tokens.  A beam's values grow with
+// its logits or stay equal (each step of x - M + C rounds to the nearest), so its candidates are in
+// the order of their logits.
+constexpr unsigned long long kBeamBits = 31;
+__device__ __forceinline__ unsigned long long place_of(double v, int beam) {
+  const long long u = __double_as_longlong(v + 0.0);   // (-0 counts as +0)
+  return ((unsigned long long)(u ^ (u >> 63 | (long long)(1ull << 63))) & ~kBeamBits) | (kBeamBits - beam);
+}
+__device__ __forceinline__ double value_at(unsigned long long place) {
+  const long long u = (long long)(place & ~kBeamBits);
+  return __longlong_as_double(u ^ (~(u >> 63) | (long long)(1ull << 63)));
 }
 
 // log x of x.hi >= 2^-100: x.hi = 2^e f with f near 1, whose logarithm is small enough for
@@ -115,7 +125,6 @@ __device__ __forceinline__ unsigned long long make_key(float x, int v) {
   return ((unsigned long long)ordered(x) << 32) | (0xFFFFFFFFu - (uint32_t)v);
 }
 __device__ __forceinline__ float key_logit(unsigned long long k) { return unordered((uint32_t)(k >> 32)); }
-__device__ __forceinline__ int key_token(unsigned long long k) { return (int)(0xFFFFFFFFu - (uint32_t)k); }
 
 // Sum over the CTA; `turn` alternates between calls (two sets of words).
 __device__ __forceinline__ int cta_sum(int v, int* words, int turn) {
@@ -289,7 +298,7 @@ __device__ __forceinline__ bool row_read(const BeamArgs& a, int row) {
 struct BmShared {
   union {
     unsigned long long list[kBmList + 2];   // a part's list
-    ulonglong2 cand[kBmOne];                // pick: candidates, ordered value and place (w, v)
+    ulonglong2 cand[kBmOne];                // pick: candidates, as place_of has it
   };
   uint4 all[kBeamMaxKeep / 2];   // the warps' largest values: 2 keep, rounded up
   unsigned long long range[2 * kBmWarps];
@@ -299,7 +308,9 @@ struct BmShared {
   unsigned last;
   Two sum[kBmWarps];
   float top[kBmWarps];
-  Two lse[kBeamMaxBeams];
+  // a beam's value: logit - most + base; base -inf: it offers nothing, most inf: it has ended
+  float most[kBeamMaxBeams];
+  Two base[kBeamMaxBeams];
   // the chosen, best first: value, row, token; their places
   float f[kBeamMaxKeep];
   int beam[kBeamMaxKeep], token[kBeamMaxKeep], slot[kBeamMaxKeep];
@@ -656,18 +667,19 @@ __device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, 
   // the candidates' keys, on their way before the sums are looked at (those of beams that
   // offer nothing, or have ended, are not used)
   constexpr int N = kBmOne / kBmThreads;
-  unsigned long long val[N], at[N];
+  unsigned long long key[N];
 #pragma unroll
   for (int q = 0; q < N; ++q) {
     const int i = tid + q * kBmThreads, r = quotient(i, a.by_keep);
-    at[q] = 0;
+    key[q] = 0;
     if (i < W * lists * K)
-      at[q] = __ldcg(reinterpret_cast<const unsigned long long*>(recs + (size_t)r * step + 16) + entry_of(a, i, r));
+      key[q] = __ldcg(reinterpret_cast<const unsigned long long*>(recs + (size_t)r * step + 16) + entry_of(a, i, r));
   }
   for (int w = warp; w < W; w += kBmWarps) {
     const int row = b * W + w;
     const float score = a.scores[row];
-    Two lse{INFINITY, 0.f};      // the beam offers nothing
+    float most = 0.f;
+    Two base{-INFINITY, 0.f};
     if (!(score <= FLT_MAX)) {   // NaN or +inf
       if ((tid & 31) == 0) set_err(a.err, FUTR_ERR_NOT_FINITE);
     } else if (row_read(a, row)) {
@@ -677,47 +689,66 @@ __device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, 
       const bool bad = !(S.hi <= FLT_MAX) || M == INFINITY;
       if (bad && (tid & 31) == 0) set_err(a.err, FUTR_ERR_NOT_FINITE);
       if (!bad && M > -INFINITY) {
-        Two l = log_of(S);
-        if (!(l.hi > 0.f)) l = Two{0.f, 0.f};   // S holds e^0: less than 1 it is by roundings alone
-        lse = add(l, M);
+        const Two l = log_of(S);
+        most = M;
+        base = Two{score, 0.f};
+        if (l.hi > 0.f) base = add(add(base, -l.hi), -l.lo);   // S holds e^0: less than 1 it is by roundings alone
       }
     } else if (score >= -FLT_MAX) {
-      lse.hi = -INFINITY;        // ended: one candidate
+      most = INFINITY;
+      base = Two{score, 0.f};
     }
-    if ((tid & 31) == 0) sh.lse[w] = lse;
+    if ((tid & 31) == 0) sh.most[w] = most, sh.base[w] = base;
   }
   if (tid == 0) sh.out = 0;
   __syncthreads();
-  // the candidates' ordered values; the first word decides that most are not chosen
-  uint32_t top = 0;
+  // the candidates' values in fp32 decide that most are not chosen: they are off by 4 u A at
+  // most, u = 2^-24 and A the largest of the best beam's base (no value of its beam is above it)
+  // and of the bound by which `keep` of them lie, so those within 2^-20 A of it (16 u) may be
+  uint32_t near[N], top = 0;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
     const int i = tid + q * kBmThreads;
-    val[q] = 0;
+    near[q] = 0;
     if (i < W * lists * K) {
       const int w = quotient(i, lists > 1 ? a.by_beam : a.by_keep);
-      const Two lse = sh.lse[w];
-      const unsigned long long key = at[q];
-      const Two score{a.scores[b * W + w], 0.f};
-      at[q] = (unsigned long long)w << 32;
-      if (lse.hi == -INFINITY) {
-        if (i == w * lists * K) val[q] = ordered64(score);
-        at[q] |= (uint32_t)a.end;
-      } else if (lse.hi < INFINITY && key != 0) {
-        const Two v = add(add(add(Two{key_logit(key), 0.f}, -lse.hi), -lse.lo), score);
-        if (v.hi >= -FLT_MAX) val[q] = ordered64(v);   // (below it: as little as a logit of -inf)
-        at[q] |= (uint32_t)key_token(key);
+      const float most = sh.most[w], base = sh.base[w].hi;
+      float v = -INFINITY;
+      if (most == INFINITY) {
+        if (i == w * lists * K) v = base;
+        key[q] = ~(unsigned long long)(uint32_t)a.end;
+      } else if (key[q] != 0) {
+        v = (key_logit(key[q]) - most) + base;
       }
-      top = max(top, (uint32_t)(val[q] >> 32));
+      if (v >= -FLT_MAX) near[q] = ordered(v);   // (below it: as little as a logit of -inf)
+      top = max(top, near[q]);
     }
   }
-  const uint32_t low = reached(top, K, reinterpret_cast<uint32_t*>(sh.all), sh.warps);
+  const float best = unordered(__reduce_max_sync(0xffffffffu, ordered((tid & 31) < W ? sh.base[tid & 31].hi : -INFINITY)));
+  uint32_t low = reached(top, K, reinterpret_cast<uint32_t*>(sh.all), sh.warps);
+  if (low != 0) {
+    const float bound = unordered(low);
+    low = max(1u, ordered(fmaf(fmaxf(fabsf(bound), fabsf(best)), -0x1p-20f, bound)));
+  }
 #pragma unroll
   for (int q = 0; q < N; ++q)
-    if (val[q] != 0 && (uint32_t)(val[q] >> 32) >= low) sh.cand[atomicAdd(&sh.out, 1)] = make_ulonglong2(val[q], at[q]);
+    if (near[q] != 0 && near[q] >= low) {
+      const int i = tid + q * kBmThreads, w = quotient(i, lists > 1 ? a.by_beam : a.by_keep);
+      sh.cand[atomicAdd(&sh.out, 1)] = make_ulonglong2((unsigned)w, ~key[q]);
+    }
   __syncthreads();
-  // their order: larger values, then lower places
   const int n = sh.out, got = min(n, K);
+  // their places, by fp64 (0.3 us; of all candidates 0.5 to 3)
+#pragma unroll 1
+  for (int c = tid; c < n; c += kBmThreads) {
+    const int w = (int)sh.cand[c].x;
+    const float most = sh.most[w];
+    const double base = (double)sh.base[w].hi + sh.base[w].lo;
+    sh.cand[c].x = place_of(most == INFINITY ? base : ((double)key_logit(~sh.cand[c].y) - most) + base, w);
+  }
+  __syncthreads();
+  // their order
+#pragma unroll 1
   for (int c = tid; c < n; c += kBmThreads) {
     const ulonglong2 my = sh.cand[c];
     int r = 0;
@@ -727,8 +758,8 @@ __device__ __forceinline__ void do_pick(const BeamArgs& a, BmShared& sh, int b, 
       r += (t.x > my.x) | ((t.x == my.x) & (t.y < my.y));
     }
     if (r < K) {
-      sh.f[r] = unordered((uint32_t)(my.x >> 32));
-      sh.beam[r] = (int)(my.y >> 32);
+      sh.f[r] = fmaxf((float)value_at(my.x), -FLT_MAX);
+      sh.beam[r] = (int)(kBeamBits - (my.x & kBeamBits));
       sh.token[r] = (int)(uint32_t)my.y;
     }
   }

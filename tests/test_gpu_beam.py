@@ -584,3 +584,40 @@ def test_no_value_is_above_its_score():
         x = torch.where(x < 100, x + top - 18.0 - math.log(V), x)     # and some 2^-26 of it
         score, _, token, _ = select(x, s, 1)
         assert bool((score <= 0).all())
+
+
+@pytest.mark.parametrize("base", [-1e9, -3e7, 4096.0, -1e30, 1e30, 0.0])
+@pytest.mark.parametrize("V", [500, 60000])
+def test_a_beams_tokens_are_in_the_order_of_their_logits(base, V):
+    """Scores that leave nothing of small differences between a beam's values: its tokens go by their logits all the
+    same, equal logits by the lowest token, and none is left out for a lower token."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    near = 1.0 + torch.randint(0, 40, (6, V), generator=g, device="cuda") * 2.0 ** -23       # steps of fp32, ties among them
+    spread = torch.randn((6, V), generator=g, device="cuda") * 20                            # about the sums' own steps
+    tiny = torch.randint(-30, 30, (6, V), generator=g, device="cuda").float() * 1e-30
+    for x in (near, spread, tiny):
+        for dtype in (torch.float32, torch.bfloat16):
+            y = x.to(dtype)
+            order = torch.sort(y, dim=1, descending=True, stable=True).indices
+            for step in (0.0, abs(base) * 2.0 ** -20):
+                s = (base - step * torch.tensor([[0.0, 1, 2], [2, 0, 1]], device="cuda")).contiguous()
+                for keep in (1, 3, 7, 64):
+                    _, parent, token, _ = select(y, s, keep)
+                    for w in range(6):
+                        mine = token[w // 3][parent[w // 3] == w]
+                        assert torch.equal(mine, order[w, :mine.numel()].to(I32)), (base, keep, w)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("V", [3, 128256])
+def test_the_log_sum_of_equal_large_logits(V, dtype):
+    """As above, where M is so large that M + log n has little of log n left.  Beyond 2^20 exponents are differences, and
+    0 again; fp16's largest stay below it, where M log2 e is rounded unless M is a power of two: the exponentials of what it
+    lost, 2^-22 off each, and additions of such numbers are those of log_sum_bound."""
+    for M in (torch.finfo(dtype).min, torch.finfo(dtype).max, 3.0 * 2.0 ** (13 if dtype == torch.float16 else 21)):
+        x = torch.full((4, V), M, device="cuda").to(dtype)
+        s = torch.full((2, 2), math.log(V), device="cuda")
+        score, _, _, _ = select(x, s, 3)
+        want = float(s[0, 0]) - math.log(V)
+        own = 2.0 ** -25 if abs(M) > 2.0 ** 20 else float(log_sum_bound(x).max())
+        assert float((score.double() - want).abs().max()) <= own + 2.0 ** -24 * abs(want), M
