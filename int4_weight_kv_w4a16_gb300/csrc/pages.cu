@@ -266,9 +266,9 @@ __global__ void __launch_bounds__(kPgPlan) pages_grow_kernel(const PagesArgs a) 
   int* e = nullptr;
   for (int f0 = 0; f0 < places; f0 += kPgPlan) {
     e = f0 + tid < places ? entry(f0 + tid) : nullptr;
-    const int id = e ? *e : -1;
+    const int id = e ? page_of(a.p, *e) : -1;
     mine = e && id < 0;
-    const int held = id >= 0 && page_of(a.p, id) >= 0 ? a.p.refs[id] : 1;   // rows go to a page of their own
+    const int held = id >= 0 ? a.p.refs[id] : 1;   // rows go to a page of their own
     if (held != 1) bad = held > 1 ? FUTR_ERR_SHARED : FUTR_ERR_NOT_HELD;
     int total;
     at = need + scan(mine, words, total);
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kPgPlan) pages_grow_kernel(const PagesArgs a) 
   need = 0;
   for (int f0 = 0; f0 < places; f0 += kPgPlan) {
     e = f0 + tid < places ? entry(f0 + tid) : nullptr;
-    mine = e && *e < 0;
+    mine = e && (unsigned)*e >= (unsigned)a.p.n_pages;
     int total;
     at = need + scan(mine, words, total);
     need += total;

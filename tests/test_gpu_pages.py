@@ -511,3 +511,17 @@ def test_a_table_that_is_not_counted_at_all():
     futr.futr_pages_compact(b.cache, b.pool, b.table, 0, 8)
     assert futr.futr_pages_check(b.pool) == (futr.FUTR_ERR_NOT_HELD, 8)
     assert torch.equal(b.bits, was) and b.table.tolist() == [[0, 1, -1, -1], [-1] * 4]
+
+
+@pytest.mark.parametrize("rows,new", [(2, 40), (40, 500)])      # places of one round, and of several
+def test_new_rows_take_pages_for_ids_out_of_range(rows, new):
+    """An id that is no page's is reported and counts as no page: rows that meet it get one."""
+    width = -(-new // 16) + 2
+    b = Both(rows * width, 16, rows, width, layers=1, hkv=1)
+    b.table[:, 1], b.table[0, 0], b.table[1, 2] = rows * width, 2 ** 31 - 1, -5
+    b.table[:, width - 1] = rows * width + 3                    # not met
+    futr.futr_pages_grow(b.cache, b.pool, ints([0] * rows), starts([new] * rows), b.table)
+    assert b.ref.grow([0] * rows, [new] * rows)
+    assert b.table[:, width - 1].tolist() == [rows * width + 3] * rows
+    b.table[:, width - 1] = -1
+    b.same(futr.FUTR_ERR_OUT_OF_RANGE)
