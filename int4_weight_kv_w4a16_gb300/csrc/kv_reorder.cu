@@ -92,8 +92,9 @@ __device__ __forceinline__ void move_columns(const ReorderArgs& a, const Moves& 
   }
 }
 
-// M: most moves of the batch.  Few take more columns at once, 8 loads a thread at least: one
-// slot of 32 layers at 900 positions, from memory, 13.1 us (two loads: 15.3).  Three CTAs an
+// M: most moves of the batch.  Few moves of up to 8 slots take more columns at once, 8 loads a
+// thread at least: one slot of 32 layers at 900 positions, from memory, 13.1 us (two loads: 15.3);
+// of 9 to 32 slots up to 8 moves take a column a thread.  Three CTAs an
 // SM (168 registers) for 32 moves: 170 us, two (189) 187; for 16 (147 us) four would not hold
 // the data (223).
 template <int M>

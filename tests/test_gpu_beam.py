@@ -621,3 +621,54 @@ def test_the_log_sum_of_equal_large_logits(V, dtype):
         want = float(s[0, 0]) - math.log(V)
         own = 2.0 ** -25 if abs(M) > 2.0 ** 20 else float(log_sum_bound(x).max())
         assert float((score.double() - want).abs().max()) <= own + 2.0 ** -24 * abs(want), M
+
+
+def some_moves(batch, n, seed):
+    """Parents of `batch` slots of which n take another's tokens, some slots are emptied, and the rest stay."""
+    r = np.random.default_rng(seed)
+    parent = list(range(batch))
+    moved = r.permutation(batch)[:n].tolist()
+    for i in moved:
+        parent[i] = int((i + r.integers(1, batch)) % batch)
+    for i in r.permutation(batch)[:batch // 5].tolist():
+        if i not in moved:
+            parent[i] = -1
+    return parent
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch,moves", [(b, m) for b in (7, 8, 9, 12, 16, 17, 24, 32) for m in (0, 1, 2, 4, 5, 8, 9, 16, 17, 32)
+                                         if m <= b] + [(9, 3), (16, 7), (16, 15), (32, 31)])
+def test_reorder_of_every_number_of_moves(batch, moves, d):
+    """Every kernel for a batch, each number of slots that move in it: few of many, and all."""
+    r = np.random.default_rng(100 * batch + moves)
+    s = Slots(2, batch + moves % 3, 3, d, 150, batch + moves)
+    pos = r.integers(1, 151, batch).tolist()
+    for i in range(2):
+        parent = some_moves(batch, moves, 7 * batch + moves + i)
+        if i == 1 and moves == batch:
+            parent = [(j + 1) % batch for j in range(batch)]        # all change places
+        assert sum(p >= 0 and p != j for j, p in enumerate(parent)) == moves
+        want, p = s.moved(parent, pos), ints(pos)
+        futr.futr_kv_reorder(s.kv, ints(parent), p)
+        assert futr.futr_check(kv=s.kv) == futr.FUTR_OK
+        assert torch.equal(s.streams, want)
+        pos = [pos[q] if q >= 0 else 0 for q in parent]
+        assert p.tolist() == pos
+
+
+def test_the_largest_vocabulary():
+    """A row of 2^31 - 1 logits, the best of them at its ends."""
+    V = 2 ** 31 - 1
+    x = torch.zeros((1, V), dtype=torch.bfloat16, device="cuda")
+    best = [V - 1, 0, 7, V - 2, 2 ** 30, V - 9]
+    x[0, best[0]], x[0, best[1]], x[0, best[2]] = 3.0, 3.0, 2.0
+    x[0, best[3]], x[0, best[4]], x[0, best[5]] = 1.0, 0.5, 0.25
+    score, parent, token, ended = select(x, torch.zeros((1, 1), device="cuda"), 8, end=V - 1)
+    assert token[0].tolist() == [0, V - 1, 7, V - 2, 2 ** 30, V - 9, 1, 2]
+    assert parent[0].tolist() == [0] * 8 and ended[0].tolist() == [0, 1] + [0] * 6
+    x[0, best] = 0
+    score, _, token, _ = select(x, torch.full((1, 1), math.log(V), device="cuda"), 2)
+    # (a thread has 2^17 zeros at most, whose e^0 add up as they are)
+    want = float(torch.tensor(math.log(V))) - math.log(V)
+    assert token[0].tolist() == [0, 1] and float((score.double() - want).abs().max()) <= 2.0 ** -25 + 2.0 ** -24 * abs(want)

@@ -1,4 +1,5 @@
 """Attention over the paged cache with a window and first tokens that stay visible, against 64 bits."""
+import ctypes as C
 import math
 
 import pytest
@@ -205,3 +206,32 @@ def test_a_long_answer_in_few_pages():
         futr.futr_paged_attention(c.cache, 0, B, p, None, c.table, q, want, c.ws, window=window, sinks=sinks)
         assert torch.equal(out, want), i
     assert futr.futr_pages_check(pool)[0] == futr.FUTR_OK and futr.futr_paged_check(cache, ws) == futr.FUTR_OK
+
+
+@pytest.mark.parametrize("n", [1, 3, 150], ids=["token", "draft", "chunk"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_the_entry_point_without_sinks(n, dtype):
+    """futr_paged_attention by its own name, with windows and scales: what the one with sinks gives for none, bit for
+    bit, and right."""
+    c = Paged(8, 2, 64, 32, 2, 30)
+    c.fill(4)
+    pos, counts = [700, 64], [n, n]
+    q = rows(2 * n, 8, 64, dtype, 30 + n)
+    p, s, stream = ints(pos), starts(counts), torch.cuda.current_stream().cuda_stream
+    kind = futr.FUTR_DTYPE_F16 if dtype == torch.float16 else futr.FUTR_DTYPE_BF16
+    for window in (0, 1, 40, 300, 2 ** 31 - 1):
+        for scale in (0.0, 0.05, 0.5):
+            args = [C.addressof(c.cache), 0, 2, p.data_ptr(), s.data_ptr(), 2 * n, c.table.data_ptr(), c.table.shape[1],
+                    q.data_ptr(), q.stride(0)]
+            outs = [torch.full_like(q, 7.0) for _ in range(2)]
+            assert futr.lib().futr_paged_attention(*args, outs[0].data_ptr(), q.stride(0), kind, scale, window,
+                                                   C.addressof(c.ws), stream) == futr.FUTR_OK
+            assert futr.lib().futr_paged_attention_sinks(*args, outs[1].data_ptr(), q.stride(0), kind, scale, window, 0,
+                                                         C.addressof(c.ws), stream) == futr.FUTR_OK
+            assert futr.futr_paged_check(c.cache, c.ws) == futr.FUTR_OK
+            assert torch.equal(outs[0], outs[1])
+            if scale == 0.0:
+                check(c, q, outs[0], pos, counts, window, 0)
+                default = outs[0]
+            else:
+                assert not torch.equal(outs[0], default) or window == 1
