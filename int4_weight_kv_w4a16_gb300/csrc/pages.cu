@@ -7,9 +7,8 @@
 // arrive, and no list of free pages has to be kept in order.
 //
 // grow, fork and compact decide in one CTA (ranks over the free bits: a word a
-// thread, 32768 pages a round) and leave a plan; fork and compact, which look at the whole
-// table first (large ones by more CTAs), then change it and copy pages with the whole GPU in
-// a second kernel.
+// thread, 32768 pages a round).  fork and compact leave a plan, and a second kernel changes
+// counts and tables and copies pages with the whole GPU.
 //
 // The deciding CTA is a chain of loads and sums over the CTA, 3 to 4 us: to fork one of four
 // sequences takes 6.0 us in all, to give back and take a token's pages for 8 sequences 5.4,
@@ -24,7 +23,7 @@ namespace {
 
 constexpr int kPgThreads = 256;
 constexpr int kPgPlan = 1024, kPgWarps = kPgPlan / 32;   // threads of a deciding CTA
-constexpr int kPgLook = 8, kPgMaxLook = 128;             // table entries of a thread at a time, and CTAs, that are looked at
+constexpr int kPgLook = 1024, kPgMaxLook = 256;          // table entries of a CTA that looks at them, most such CTAs
 constexpr int kPgTile = 16384;                           // table entries of a CTA in fork
 
 __device__ __forceinline__ int* plan_from(const PoolView& p) { return p.plan + kPlanHeader; }
@@ -78,7 +77,7 @@ __global__ void pages_init_kernel(const PoolView p) {
   const int i = blockIdx.x * kPgThreads + threadIdx.x;
   if (i < p.n_pages) p.refs[i] = 0;
   if (i < p.words) p.free[i] = valid_bits(p, i);
-  if (i == 0) p.err[2] = p.n_pages, p.err[3] = 0, p.plan[kPlanMet] = p.plan[kPlanMet + 1] = 0;
+  if (i == 0) p.err[2] = p.n_pages, p.err[3] = 0, p.plan[kPlanMet] = p.plan[kPlanBad] = 0;
 }
 
 __global__ void __launch_bounds__(kPgThreads) pages_hold_kernel(const PagesArgs a) {
@@ -136,61 +135,34 @@ __device__ __forceinline__ int scan(int v, int* words, int& total) {
 }
 
 // Whether the pages that the call's table names are held: a page that is named and free would
-// be taken for a copy and written over.  Every CTA looks at its part of the table, and the last
-// to arrive goes on with the call.  The look's loads are under way between the decision's own:
-// to fork 128 sequences takes 29.6 us as without a look (31.1 with the look ahead of the
-// decision), to move 500 pages twice 174.5 (177.5; 173.7 without).
-struct Look {
-  int of[kPgLook];   // of the thread's places: page ids, then their counts
-  bool bad;          // some page is not held
+// be taken for a copy and written over.  All CTAs of a deciding kernel but the first look, while
+// that one decides; whatever the call changes the second kernel changes, which knows what they
+// found.  (In front of the decision the look cost 1 to 3 us: 128 sequences of 75 pages, forked in
+// 29.9 us, took 31.2.)
+__device__ __forceinline__ void look(const PagesArgs& a) {
+  const long long n = (long long)a.batch * a.table_ld, step = (long long)(gridDim.x - 1) * kPgPlan;
+  bool bad = false;
+#pragma unroll 4
+  for (long long i = (long long)(blockIdx.x - 1) * kPgPlan + threadIdx.x; i < n; i += step) {
+    const int id = a.table[i];
+    if ((unsigned)id < (unsigned)a.p.n_pages) bad |= a.p.refs[id] < 1;
+  }
+  if (__syncthreads_or(bad) && threadIdx.x == 0) a.p.plan[kPlanBad] = 1;
+}
 
-  // The thread's places of the CTA's `part` of the table.
-  __device__ __forceinline__ void ids(const PagesArgs& a, long long part) {
-    constexpr int kPart = kPgPlan * kPgLook;
-    const long long n = (long long)a.batch * a.table_ld - part * kPart;
-    const int left = (int)min(n, (long long)kPart) - (int)threadIdx.x;
-    const int* at = a.table + part * kPart + threadIdx.x;
-#pragma unroll
-    for (int j = 0; j < kPgLook; ++j) of[j] = j * kPgPlan < left ? at[j * kPgPlan] : -1;
+// In the second kernel: whether the call goes ahead.  (Of the CTAs that have read that it does
+// not for the look's sake, the last takes that back.)
+__device__ __forceinline__ bool goes_ahead(const PagesArgs& a) {
+  const int ok = a.p.plan[1], bad = a.p.plan[kPlanBad];
+  if (!bad) return ok;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    set_err(a.p.err, FUTR_ERR_NOT_HELD);
+    unsigned* met = reinterpret_cast<unsigned*>(a.p.plan + kPlanMet);
+    if (atom_add_acq_rel_gpu(met, 1u) == gridDim.x - 1) a.p.plan[kPlanBad] = 0, *met = 0;
   }
-  __device__ __forceinline__ void start(const PagesArgs& a) {
-    bad = false;
-    ids(a, blockIdx.x);
-    const long long n = (long long)a.batch * a.table_ld;
-#pragma unroll 1
-    for (long long part = (long long)blockIdx.x + gridDim.x; part * (kPgPlan * kPgLook) < n; part += gridDim.x) {
-      counts(a);   // (a table of more parts than kPgMaxLook)
-      judge();
-      ids(a, part);
-    }
-  }
-  __device__ __forceinline__ void counts(const PagesArgs& a) {
-#pragma unroll
-    for (int j = 0; j < kPgLook; ++j) of[j] = (unsigned)of[j] < (unsigned)a.p.n_pages ? a.p.refs[of[j]] : 1;
-  }
-  __device__ __forceinline__ void judge() {
-#pragma unroll
-    for (int j = 0; j < kPgLook; ++j) bad |= of[j] < 1;
-  }
-  // The last CTA of a grid of several; it knows what the others have found.
-  __device__ __forceinline__ bool last(const PagesArgs& a) {
-    __shared__ int s_last;
-    judge();
-    const bool any = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-      int* met = a.p.plan + kPlanMet;
-      if (any) atomicExch(met + 1, 1);
-      s_last = atom_add_acq_rel_gpu(reinterpret_cast<unsigned*>(met), 1u) == gridDim.x - 1;
-      if (s_last) {
-        if (atomicExch(met + 1, 0)) s_last = 2;
-        *met = 0;
-      }
-    }
-    __syncthreads();
-    bad = s_last == 2;
-    return s_last != 0;
-  }
-};
+  return false;
+}
 
 // The first `want` set bits of words [first, n) as numbers into list, in order.  Returns how
 // many there were (at most want).
@@ -208,20 +180,15 @@ __device__ __forceinline__ int list_bits(const F& word, int first, int n, int wa
   return min(done, want);
 }
 
-// The first `want` > 0 free pages into list, held once; there are that many, none before word
-// `first`.
-__device__ __forceinline__ void take(const PoolView& p, int first, int want, int* list, int* words) {
+// The first `want` > 0 free pages into list; there are that many, none before word `first`.
+__device__ __forceinline__ void list_free(const PoolView& p, int first, int want, int* list, int* words) {
   list_bits([&](int i) { return p.free[i]; }, first, p.words, want, list, words);
-  __syncthreads();
-  for (int k = threadIdx.x; k < want; k += kPgPlan) {
-    const int id = list[k];
-    p.refs[id] = 1;
-    atomicAnd(&p.free[id >> 5], ~(1u << (id & 31)));
-  }
-  if (threadIdx.x == 0) {
-    p.err[2] -= want;
-    p.err[3] = list[want - 1] >> 5;   // the lowest are gone
-  }
+}
+
+// A free page is named by one place.
+__device__ __forceinline__ void take(const PoolView& p, int id) {
+  p.refs[id] = 1;
+  atomicAnd(&p.free[id >> 5], ~(1u << (id & 31)));
 }
 
 // Rows of sequence b in `grow`: its pages [i0, i1) (none: i0 == i1).
@@ -283,8 +250,13 @@ __global__ void __launch_bounds__(kPgPlan) pages_grow_kernel(const PagesArgs a) 
     if (tid == 0) set_err(a.p.err, FUTR_ERR_NO_PAGES);
     return;
   }
-  take(a.p, word, need, list, words);
+  list_free(a.p, word, need, list, words);
   __syncthreads();
+  for (int k = tid; k < need; k += kPgPlan) take(a.p, list[k]);
+  if (tid == 0) {
+    a.p.err[2] -= need;
+    a.p.err[3] = list[need - 1] >> 5;   // the lowest are gone
+  }
   if (places <= kPgPlan) {
     if (mine) *e = list[at];
     return;
@@ -307,6 +279,7 @@ __global__ void __launch_bounds__(kPgPlan) fork_plan_kernel(const PagesArgs a) {
   __shared__ int s_bad;
   pdl_trigger();
   pdl_wait();
+  if (blockIdx.x > 0) return look(a);
   const int i = threadIdx.x, n_free = a.p.err[2], word = a.p.err[3];
   const int most = (int)min((long long)a.c.max_pos, (long long)a.table_ld << a.c.page_log2);
   if (i == 0) s_bad = 0;
@@ -316,8 +289,6 @@ __global__ void __launch_bounds__(kPgPlan) fork_plan_kernel(const PagesArgs a) {
     first[i] = a.batch;
     oldpos[i] = a.pos[i];
   }
-  Look look;
-  look.start(a);
   __syncthreads();
   int from = -1, at = 0;
   bool others = false;   // name the written page
@@ -329,36 +300,33 @@ __global__ void __launch_bounds__(kPgPlan) fork_plan_kernel(const PagesArgs a) {
     else {
       at = p >> a.c.page_log2;   // places below it are shared
       if (p & (a.c.page - 1)) from = page_of(a.p, a.table[(size_t)parent * a.table_ld + at]);
+      if (from >= 0) others = a.p.refs[from] > 1;
     }
   } else if (i < a.batch && parent != -1) {
     s_bad = 1;
   }
-  look.counts(a);
-  if (from >= 0) others = a.p.refs[from] > 1;
-  if (gridDim.x > 1 && !look.last(a)) return;
-  look.judge();
-  const bool held = !__syncthreads_or(look.bad);   // (and s_bad and `first` are there)
+  __syncthreads();
   const bool one = parent >= 0 && !s_bad && first[parent] == i;
   const bool copy = parent >= 0 && !s_bad && (!one || others) && from >= 0;
   int total;
   const int k = scan(copy, words, total);
-  const bool ok = !s_bad && held && total <= n_free;
+  const bool ok = !s_bad && total <= n_free;
   if (i == 0) {
     a.p.plan[0] = ok ? total : 0;
     a.p.plan[1] = ok;
-    if (!ok) set_err(a.p.err, s_bad ? FUTR_ERR_OUT_OF_RANGE : held ? FUTR_ERR_NO_PAGES : FUTR_ERR_NOT_HELD);
+    if (!ok) set_err(a.p.err, s_bad ? FUTR_ERR_OUT_OF_RANGE : FUTR_ERR_NO_PAGES);
   }
   if (!ok) return;
   int* list = plan_to(a.p);
-  if (total > 0) take(a.p, word, total, list, words);
+  if (total > 0) list_free(a.p, word, total, list, words);
   __syncthreads();
+  if (i == 0 && total > 0) a.p.err[3] = list[0] >> 5;
   if (i < a.batch) {
     if (copy) {
       plan_from(a.p)[k] = from;
       plan_slots(a.p)[k] = oldpos[parent] & (a.c.page - 1);
     }
-    plan_seqs(a.p)[i] = make_int4(parent, at, copy ? list[k] : -1, one);
-    a.pos[i] = parent >= 0 ? oldpos[parent] : 0;
+    plan_seqs(a.p)[i] = make_int4(parent, parent >= 0 ? oldpos[parent] : 0, copy ? list[k] : -1, one);
   }
 }
 
@@ -409,16 +377,24 @@ __device__ __forceinline__ void do_copies(const PagesArgs& a, int w, int warps, 
 }
 
 // The first blocks change the table, columns [cols * blockIdx.x, ..) of all rows each; the
-// others copy.
+// next takes the copies' pages and moves the positions, the others copy.
 __global__ void __launch_bounds__(kPgThreads) fork_apply_kernel(const PagesArgs a, int cols, int table_ctas) {
   extern __shared__ int old[];   // [batch][cols]
   pdl_trigger();
   pdl_wait();
-  if (!a.p.plan[1]) return;
-  const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= table_ctas) {
-    const int w = ((int)blockIdx.x - table_ctas) * (kPgThreads / 32) + (tid >> 5);
-    do_copies(a, w, ((int)gridDim.x - table_ctas) * (kPgThreads / 32), false);
+  if (!goes_ahead(a)) return;
+  const int tid = threadIdx.x, plog = a.c.page_log2;
+  const int4* seqs = plan_seqs(a.p);
+  if ((int)blockIdx.x == table_ctas) {
+    const int copies = a.p.plan[0];
+    for (int k = tid; k < copies; k += kPgThreads) take(a.p, plan_to(a.p)[k]);
+    for (int i = tid; i < a.batch; i += kPgThreads) a.pos[i] = seqs[i].y;
+    if (tid == 0 && copies > 0) atomicSub(&a.p.err[2], copies);
+    return;
+  }
+  if ((int)blockIdx.x > table_ctas) {
+    const int w = ((int)blockIdx.x - table_ctas - 1) * (kPgThreads / 32) + (tid >> 5);
+    do_copies(a, w, ((int)gridDim.x - table_ctas - 1) * (kPgThreads / 32), false);
     return;
   }
   // a row's children; its first place that is not shared; whether its first child has a copy
@@ -426,7 +402,6 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply_kernel(const PagesArgs 
   __shared__ int kids[kPagesMaxSeqs], shared[kPagesMaxSeqs];
   __shared__ uint8_t copied[kPagesMaxSeqs];
   const int c0 = blockIdx.x * cols, n = min(cols, a.table_ld - c0);
-  const int4* seqs = plan_seqs(a.p);
   for (int i = tid; i < a.batch; i += kPgThreads) kids[i] = 0, shared[i] = 0, copied[i] = 0;
   for (int e = tid; e < a.batch * cols; e += kPgThreads) {
     const int i = e / cols, j = e - i * cols;
@@ -437,7 +412,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply_kernel(const PagesArgs 
     const int4 s = seqs[i];
     if (s.x >= 0) {
       atomicAdd(&kids[s.x], 1);
-      shared[s.x] = s.y;   // the same for all children
+      shared[s.x] = s.y >> plog;   // the same for all children
       if (s.w) copied[s.x] = s.z >= 0;
     }
   }
@@ -448,7 +423,8 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply_kernel(const PagesArgs 
     // row i's new entry
     const int4 s = seqs[i];
     int now = -1;
-    if (s.x >= 0) now = c == s.y && s.z >= 0 ? s.z : c < s.y || s.w ? old[s.x * cols + j] : -1;
+    const int at = s.y >> plog;
+    if (s.x >= 0) now = c == at && s.z >= 0 ? s.z : c < at || s.w ? old[s.x * cols + j] : -1;
     if (now != old[e]) a.table[(size_t)i * a.table_ld + c] = now;
     // and what becomes of its old page
     const int more = (c < shared[i] ? kids[i] : kids[i] > 0 && !(copied[i] && c == shared[i])) - 1;
@@ -468,14 +444,9 @@ __global__ void __launch_bounds__(kPgPlan) compact_plan_kernel(const PagesArgs a
   __shared__ int words[kPgWarps];
   pdl_trigger();
   pdl_wait();
+  if (blockIdx.x > 0) return look(a);
   const PoolView& p = a.p;
   const int word = p.err[3];
-  Look look;
-  look.start(a);
-  if (gridDim.x > 1) {
-    look.counts(a);
-    if (!look.last(a)) return;
-  }
   // pages of word i inside [lo, hi)
   auto inside = [&](int i) {
     const int lo = a.lo - i * 32, hi = a.hi - i * 32;
@@ -487,43 +458,42 @@ __global__ void __launch_bounds__(kPgPlan) compact_plan_kernel(const PagesArgs a
   int *from = plan_from(p), *to = plan_to(p), *where = plan_slots(p);
   const int moves = list_bits([&](int i) { return ~p.free[i] & inside(i) & valid_bits(p, i); }, a.lo >> 5,
                               (int)((a.hi + 31ll) >> 5), p.n_pages, from, words);
-  if (gridDim.x == 1) look.counts(a);
   const int room = list_bits([&](int i) { return p.free[i] & ~inside(i); }, word, p.words, moves, to, words);
-  look.judge();
-  const bool held = !__syncthreads_or(look.bad), ok = held && room == moves;
+  const bool ok = room == moves;
   if (threadIdx.x == 0) {
     p.plan[0] = ok ? moves : 0;
     p.plan[1] = ok;
-    if (!ok) set_err(p.err, held ? FUTR_ERR_NO_PAGES : FUTR_ERR_NOT_HELD);
+    if (!ok) set_err(p.err, FUTR_ERR_NO_PAGES);
   }
   if (!ok) return;
-  __syncthreads();
-  if (threadIdx.x == 0 && moves > 0) p.err[3] = min(word, from[0] >> 5);
   for (int i = a.lo + threadIdx.x; i < a.hi; i += kPgPlan) where[i] = i;
   __syncthreads();
-  for (int k = threadIdx.x; k < moves; k += kPgPlan) {
-    const int s = from[k], t = to[k];
-    where[s] = t;
-    p.refs[t] = p.refs[s];
-    p.refs[s] = 0;
-    atomicOr(&p.free[s >> 5], 1u << (s & 31));
-    atomicAnd(&p.free[t >> 5], ~(1u << (t & 31)));
-  }
+  for (int k = threadIdx.x; k < moves; k += kPgPlan) where[from[k]] = to[k];
 }
 
 __global__ void __launch_bounds__(kPgThreads) compact_apply_kernel(const PagesArgs a, int table_ctas) {
   pdl_trigger();
   pdl_wait();
-  if (!a.p.plan[1]) return;
+  if (!goes_ahead(a)) return;
   const int tid = threadIdx.x;
   if ((int)blockIdx.x >= table_ctas) {
     const int w = ((int)blockIdx.x - table_ctas) * (kPgThreads / 32) + (tid >> 5);
     do_copies(a, w, ((int)gridDim.x - table_ctas) * (kPgThreads / 32), true);
     return;
   }
-  const int* where = plan_slots(a.p);
-  const long long n = (long long)a.batch * a.table_ld, step = (long long)table_ctas * kPgThreads;
-  for (long long i = (long long)blockIdx.x * kPgThreads + tid; i < n; i += step) {
+  const PoolView& p = a.p;
+  const int *where = plan_slots(p), *from = plan_from(p), *to = plan_to(p), moves = p.plan[0];
+  const int first = blockIdx.x * kPgThreads + tid, step = table_ctas * kPgThreads;
+  if (first == 0 && moves > 0) atomicMin(&p.err[3], from[0] >> 5);
+  for (int k = first; k < moves; k += step) {
+    const int s = from[k], t = to[k];
+    p.refs[t] = p.refs[s];
+    p.refs[s] = 0;
+    atomicOr(&p.free[s >> 5], 1u << (s & 31));
+    atomicAnd(&p.free[t >> 5], ~(1u << (t & 31)));
+  }
+  const long long n = (long long)a.batch * a.table_ld;
+  for (long long i = first; i < n; i += step) {
     const int id = page_of(a.p, a.table[i]);
     if (id >= a.lo && id < a.hi && where[id] != id) a.table[i] = where[id];
   }
@@ -560,10 +530,10 @@ cudaError_t launch_pages_hold(const PagesArgs& a, cudaStream_t st) {
   return pg_launch(pages_hold_kernel, dim3(blocks_for((long long)a.batch * a.table_ld, 1024)), kPgThreads, 0, st, a);
 }
 
-// CTAs of a deciding kernel.
+// CTAs of a deciding kernel: one, and those that look at the table.
 unsigned looking(const PagesArgs& a) {
-  const long long n = ((long long)a.batch * a.table_ld + kPgPlan * kPgLook - 1) / (kPgPlan * kPgLook);
-  return (unsigned)(n < kPgMaxLook ? n : kPgMaxLook);
+  const long long n = ((long long)a.batch * a.table_ld + kPgLook - 1) / kPgLook;
+  return 1 + (unsigned)(n < kPgMaxLook ? n : kPgMaxLook);
 }
 
 cudaError_t launch_pages_grow(const PagesArgs& a, cudaStream_t st) {
@@ -588,7 +558,7 @@ cudaError_t launch_pages_fork(const PagesArgs& a, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     configured.mark(dev);
   }
-  return pg_launch(fork_apply_kernel, dim3((unsigned)(table_ctas + kPgCopyCtas * sms)), kPgThreads, (size_t)a.batch * cols * 4, st,
+  return pg_launch(fork_apply_kernel, dim3((unsigned)(table_ctas + kPgCopyCtas * sms + 1)), kPgThreads, (size_t)a.batch * cols * 4, st,
                    a, cols, table_ctas);
 }
 

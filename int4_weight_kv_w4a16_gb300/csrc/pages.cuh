@@ -19,13 +19,13 @@ struct PoolView {
 };
 
 // The plan: a header, then lists of n_pages each and one row of four per sequence.
-//   header [0] copies, [1] 1: the call goes ahead; [kPlanMet] CTAs that have looked at the table,
-//   [kPlanMet + 1] 1: they met a page that is not held (both 0 between calls)
+//   header [0] copies, [1] 1: the call goes ahead; [kPlanBad] 1: but the table names a page that
+//   is not held, [kPlanMet] CTAs that have read this (both 0 between calls)
 //   from, to [n_pages]   pages to copy (to: also the pages that a call takes)
 //   slots [n_pages]      slots of a page that are copied; compact: where page p goes
-//   seqs [max_seqs][4]   fork: parent's row or -1, first place behind the shared ones,
-//                        fresh page for it or -1, 1: keeps the parent's places from there on
-constexpr int kPlanHeader = 64, kPlanMet = 32;
+//   seqs [max_seqs][4]   fork: parent's row or -1, its position (0), fresh page for the place of
+//                        that position or -1, 1: keeps the parent's places from there on
+constexpr int kPlanHeader = 64, kPlanBad = 32, kPlanMet = 33;
 inline size_t plan_ints(int n_pages, int max_seqs) {
   // (the sequences' rows are aligned to 16 bytes)
   return kPlanHeader + ((3 * (size_t)n_pages + 3) & ~size_t(3)) + 4 * (size_t)max_seqs; }
