@@ -21,11 +21,12 @@
 // Short lists are put in order by counting, for each entry, those before it; of long ones
 // the k largest are found by bisection, a count over the CTA a step.
 //
-// 256 rows of 128256 fp32 logits (131 MB) take 31.2 us, of which the tiles some 17 (at the
+// 256 rows of 128256 fp32 logits (131 MB) take 31.5 us, of which the tiles some 16 (at the
 // rate of memory), the way to the first threshold 4 and the steps behind the last tile 6; 4
-// rows 8.7 us, the same steps.  Fetching instructions is the largest of their waits, so the
-// rare steps are out of line (34.1 and 9.1 us with them in line).  Not faster: a ring of bulk copies in place of the loads (39 us), and a
-// persistent kernel whose ring runs on through its parts (42).
+// rows 9.0 us, the same steps; 256 rows of bf16 27.5 us.  Waits for instructions are among the
+// largest of a few rows, so the rare steps are out of line (34.1 and 9.1 us with them in line,
+// where the rest took 31.2 and 8.7).  Not faster: a ring of bulk copies in place of the loads
+// (39 us), and a persistent kernel whose ring runs on through its parts (42).
 #include <cfloat>
 #include <climits>
 #include <type_traits>

@@ -12,9 +12,9 @@
 //
 // The deciding CTA is a chain of loads and sums over the CTA, 3 to 4 us: to fork one of four
 // sequences takes 6.0 us in all, to give back and take a token's pages for 8 sequences 5.4,
-// for 256 with a window and 32 prompts among them 8.2 (a warp a sequence, one after another,
-// took 14.6).  Copies are bound by memory: 500 pages of 4 layers (262 MB) moved in 85 us, 0.91
-// of the copy rate; 64 half pages of 8 layers (67 MB) in 26.7 us with the decision.
+// for 256 with a window and 32 prompts among them 7.4 (a warp a sequence, one after another,
+// took 14.6).  Copies are bound by memory: 500 pages of 4 layers (262 MB) moved in 86 us, 0.91
+// of the copy rate; 64 half pages of 8 layers (67 MB) in 26.4 us with the decision.
 #include "pages.cuh"
 
 namespace futr {
